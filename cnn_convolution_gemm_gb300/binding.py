@@ -21,7 +21,12 @@ LIB_PATH = os.path.join(PKG, "libgbconv.so")
 
 CONV_BF16, CONV_F32, CONV_INT8 = 0, 1, 2
 CONV_NHWC, CONV_NCHW, CONV_NC32HW32 = 0, 1, 2
-CONV_ACT_NONE, CONV_ACT_RELU, CONV_ACT_RELU6 = 0, 1, 2
+CONV_ACT_NONE, CONV_ACT_RELU, CONV_ACT_RELU6, CONV_ACT_GELU, CONV_ACT_SILU = 0, 1, 2, 3, 4
+CONV_FP4_MX, CONV_FP4_NV = 0, 1
+CONV_FP4_IO_BF16, CONV_FP4_IO_F32, CONV_FP4_IO_CODES = 0, 1, 2
+CONV_NORM_NONE, CONV_NORM_RMS, CONV_NORM_LAYER = 0, 1, 2
+CONV_GATE_NONE, CONV_GATE_LINEAR, CONV_GATE_SIGMOID = 0, 1, 2
+CONV_NORM_OUT_FLOAT, CONV_NORM_OUT_FP4_MX, CONV_NORM_OUT_FP4_NV = 0, 1, 2
 
 CONV_ALGO_AUTO = -1
 CONV_ALGO_DIRECT = 0
@@ -51,6 +56,7 @@ STATUS_NAMES = {
 
 # Every symbol include/gbconv.h declares, with (restype, argtypes).
 _i, _sz, _p, _f = ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_float
+_ll = ctypes.c_longlong
 _cp = ctypes.c_char_p
 SIGNATURES = {
     "conv_desc_create": (_i, [ctypes.POINTER(_p)] + [_i] * 12),
@@ -84,6 +90,25 @@ SIGNATURES = {
     "conv_nhwc_bf16_to_nchw_f32": (_i, [_p, _p, _i, _i, _i, _i, _i, _p]),
     "conv_maxpool2d_nhwc_bf16": (_i, [_p, _p, _i, _i, _i, _i, _i, _i, _i, _p]),
     "conv_global_avgpool_nhwc_bf16": (_i, [_p, _p, _i, _i, _i, _i, _p]),
+    "conv_fp4_size": (_i, [_i, _i, _i, ctypes.POINTER(_sz), ctypes.POINTER(_sz)]),
+    "conv_fp4_quantize": (_i, [_i, _i, _i, _i, _p, _ll, _f, _p, _p, _p]),
+    "conv_fp4_dequantize": (_i, [_i, _i, _i, _i, _p, _p, _f, _p, _ll, _p]),
+    "conv_fp4_pack_scales": (_i, [_i, _i, _i, _p, _p, _p]),
+    "conv_fp4_create": (_i, [ctypes.POINTER(_p), _i, _i, _i, _i, _i]),
+    "conv_fp4_destroy": (_i, [_p]),
+    "conv_fp4_set_epilogue": (_i, [_p, _i, _i]),
+    "conv_fp4_set_tensor_scales": (_i, [_p, _f, _f, _f]),
+    "conv_fp4_set_strides": (_i, [_p, _ll, _ll, _ll]),
+    "conv_fp4_workspace_size": (_i, [_p, _i, ctypes.POINTER(_sz)]),
+    "conv_fp4_fwd": (_i, [_p, _i, _p, _p, _p, _p, _p, _p, _p, _p, _p, _sz, _p]),
+    "conv_norm_create": (_i, [ctypes.POINTER(_p), _i, _i, _i]),
+    "conv_norm_destroy": (_i, [_p]),
+    "conv_norm_set_post": (_i, [_p, _i, _f, _p, _p]),
+    "conv_norm_set_pre": (_i, [_p, _i, _f, _p, _p]),
+    "conv_norm_set_gate": (_i, [_p, _i, _i, _f]),
+    "conv_norm_set_output": (_i, [_p, _i, _f]),
+    "conv_norm_set_strides": (_i, [_p, _ll, _ll, _ll, _ll, _ll]),
+    "conv_norm_fwd": (_i, [_p, _i, _p, _p, _p, _p, _p, _p, _p]),
     "conv_sync_status": (_i, [_p]),
     "conv_selftest_wait_timeout": (_i, [ctypes.c_uint, _p]),
     "conv_status_string": (_cp, [_i]),
@@ -320,6 +345,109 @@ def conv_global_avgpool_nhwc_bf16(x_ptr, y_ptr, N, C, H, W, stream=None):
     _check(load_library().conv_global_avgpool_nhwc_bf16(_ptr(x_ptr), _ptr(y_ptr), N, C, H, W,
                                                         _stream(stream)),
            "conv_global_avgpool_nhwc_bf16")
+
+
+def conv_fp4_size(fmt, rows, cols):
+    """(code bytes, scale bytes) of a [rows][cols] 4-bit matrix."""
+    c, s = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(load_library().conv_fp4_size(fmt, rows, cols, ctypes.byref(c), ctypes.byref(s)),
+           "conv_fp4_size")
+    return c.value, s.value
+
+
+def conv_fp4_quantize(fmt, dtype, rows, cols, x_ptr, ldx, tensor_scale, codes_ptr, scales_ptr,
+                      stream=None):
+    _check(load_library().conv_fp4_quantize(fmt, dtype, rows, cols, x_ptr, ldx, tensor_scale,
+                                            codes_ptr, scales_ptr, stream), "conv_fp4_quantize")
+
+
+def conv_fp4_dequantize(fmt, dtype, rows, cols, codes_ptr, scales_ptr, tensor_scale, y_ptr, ldy,
+                        stream=None):
+    _check(load_library().conv_fp4_dequantize(fmt, dtype, rows, cols, codes_ptr, scales_ptr,
+                                              tensor_scale, y_ptr, ldy, stream),
+           "conv_fp4_dequantize")
+
+
+def conv_fp4_pack_scales(fmt, rows, cols, src_ptr, scales_ptr, stream=None):
+    _check(load_library().conv_fp4_pack_scales(fmt, rows, cols, src_ptr, scales_ptr, stream),
+           "conv_fp4_pack_scales")
+
+
+def conv_fp4_create(fmt, C, K, x_io=CONV_FP4_IO_BF16, y_io=CONV_FP4_IO_BF16):
+    d = ctypes.c_void_p()
+    _check(load_library().conv_fp4_create(ctypes.byref(d), fmt, C, K, x_io, y_io),
+           "conv_fp4_create")
+    return d
+
+
+def conv_fp4_destroy(desc):
+    _check(load_library().conv_fp4_destroy(desc), "conv_fp4_destroy")
+
+
+def conv_fp4_set_epilogue(desc, act, has_residual):
+    _check(load_library().conv_fp4_set_epilogue(desc, act, 1 if has_residual else 0),
+           "conv_fp4_set_epilogue")
+
+
+def conv_fp4_set_tensor_scales(desc, x=1.0, w=1.0, y=1.0):
+    _check(load_library().conv_fp4_set_tensor_scales(desc, x, w, y), "conv_fp4_set_tensor_scales")
+
+
+def conv_fp4_set_strides(desc, ldx=0, ldr=0, ldy=0):
+    _check(load_library().conv_fp4_set_strides(desc, ldx, ldr, ldy), "conv_fp4_set_strides")
+
+
+def conv_fp4_workspace_size(desc, M):
+    n = ctypes.c_size_t()
+    _check(load_library().conv_fp4_workspace_size(desc, M, ctypes.byref(n)),
+           "conv_fp4_workspace_size")
+    return n.value
+
+
+def conv_fp4_fwd(desc, M, x_ptr, x_scales_ptr, w_codes_ptr, w_scales_ptr, bias_ptr, residual_ptr,
+                 y_ptr, y_scales_ptr, ws_ptr=None, ws_bytes=0, stream=None):
+    _check(load_library().conv_fp4_fwd(desc, M, x_ptr, x_scales_ptr, w_codes_ptr, w_scales_ptr,
+                                       bias_ptr, residual_ptr, y_ptr, y_scales_ptr, ws_ptr,
+                                       ws_bytes, stream), "conv_fp4_fwd")
+
+
+def conv_norm_create(C, x_dtype=CONV_BF16, z_dtype=CONV_BF16):
+    d = ctypes.c_void_p()
+    _check(load_library().conv_norm_create(ctypes.byref(d), C, x_dtype, z_dtype),
+           "conv_norm_create")
+    return d
+
+
+def conv_norm_destroy(desc):
+    _check(load_library().conv_norm_destroy(desc), "conv_norm_destroy")
+
+
+def conv_norm_set_post(desc, kind, eps=1e-6, w_ptr=None, b_ptr=None):
+    _check(load_library().conv_norm_set_post(desc, kind, eps, w_ptr, b_ptr), "conv_norm_set_post")
+
+
+def conv_norm_set_pre(desc, kind, eps=1e-6, w_ptr=None, b_ptr=None):
+    _check(load_library().conv_norm_set_pre(desc, kind, eps, w_ptr, b_ptr), "conv_norm_set_pre")
+
+
+def conv_norm_set_gate(desc, gate, gate_rows=1, residual_scale=1.0):
+    _check(load_library().conv_norm_set_gate(desc, gate, gate_rows, residual_scale),
+           "conv_norm_set_gate")
+
+
+def conv_norm_set_output(desc, out, tensor_scale=1.0):
+    _check(load_library().conv_norm_set_output(desc, out, tensor_scale), "conv_norm_set_output")
+
+
+def conv_norm_set_strides(desc, ldx=0, ldz=0, ldg=0, ldxo=0, ldh=0):
+    _check(load_library().conv_norm_set_strides(desc, ldx, ldz, ldg, ldxo, ldh),
+           "conv_norm_set_strides")
+
+
+def conv_norm_fwd(desc, rows, x_ptr, z_ptr, gate_ptr, x_out_ptr, h_ptr, h_scales_ptr=None,
+                  stream=None):
+    _check(load_library().conv_norm_fwd(desc, rows, x_ptr, z_ptr, gate_ptr, x_out_ptr, h_ptr,
+                                        h_scales_ptr, stream), "conv_norm_fwd")
 
 
 def conv_sync_status(stream=None):

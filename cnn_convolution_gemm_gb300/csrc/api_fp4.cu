@@ -1,0 +1,389 @@
+// C-ABI entry points of the microscaled 4-bit matrices, their product and the norms
+// around a residual block: argument checks, workspace layout, dispatch.
+#include <cmath>
+#include <cstring>
+#include <new>
+
+#include "fp4.cuh"
+#include "internal.h"
+
+namespace {
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+size_t elem_bytes(int dtype) { return dtype == CONV_BF16 ? 2 : 4; }
+bool is_float(int dtype) { return dtype == CONV_BF16 || dtype == CONV_F32; }
+bool is_format(int fmt) { return fmt == CONV_FP4_MX || fmt == CONV_FP4_NV; }
+
+conv_status_t cuda_status(cudaError_t e, const char* what) {
+  return e == cudaSuccess ? gb_ok()
+                          : gb_fail(CONV_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+
+// CONV_OK or the failure for a tensor scale
+conv_status_t check_scale(int fmt, float s, const char* what) {
+  if (fmt == CONV_FP4_MX)
+    return s == 1.0f ? CONV_OK
+                     : gb_fail(CONV_ERR_BAD_PARAM, "%s must be 1 for CONV_FP4_MX", what);
+  return s >= 1e-30f && s <= 1e30f
+             ? CONV_OK
+             : gb_fail(CONV_ERR_BAD_PARAM, "%s must lie in [1e-30, 1e30]", what);
+}
+
+size_t code_bytes(int rows, int cols) { return (size_t)rows * gb::fp4::code_pitch(cols); }
+size_t scale_bytes(int fmt, int rows, int cols) {
+  return ((size_t)rows + 127) / 128 * gb::fp4::tiles_per_row(fmt, cols) * 512;
+}
+
+// the checks that the matrix calls share
+conv_status_t check_matrix(int fmt, int dtype, int rows, int cols, const void* t, long long* ld,
+                           const char* tname, const void* codes, const void* scales) {
+  if (!is_format(fmt)) return gb_fail(CONV_ERR_BAD_PARAM, "unknown 4-bit format %d", fmt);
+  if (!is_float(dtype)) return gb_fail(CONV_ERR_BAD_PARAM, "%s must be bf16 or fp32", tname);
+  if (rows < 0 || cols <= 0)
+    return gb_fail(CONV_ERR_BAD_PARAM, "rows must be >= 0 and cols > 0");
+  if (*ld == 0) *ld = cols;
+  if (*ld < cols) return gb_fail(CONV_ERR_BAD_PARAM, "row stride of %s below its row", tname);
+  if (rows == 0) return CONV_OK;
+  if (!t || !codes || !scales) return gb_fail(CONV_ERR_BAD_PARAM, "NULL tensor");
+  if (!aligned(t, elem_bytes(dtype)))
+    return gb_fail(CONV_ERR_ALIGNMENT, "%s must be aligned to its element", tname);
+  if (!aligned(codes, 16) || !aligned(scales, 16))
+    return gb_fail(CONV_ERR_ALIGNMENT, "codes and scales must be 16-byte aligned");
+  return CONV_OK;
+}
+
+}  // namespace
+
+extern "C" conv_status_t conv_fp4_size(conv_fp4_format_t fmt, int rows, int cols, size_t* cb,
+                                       size_t* sb) {
+  if (!cb || !sb) return gb_fail(CONV_ERR_BAD_PARAM, "NULL argument");
+  if (!is_format(fmt)) return gb_fail(CONV_ERR_BAD_PARAM, "unknown 4-bit format %d", (int)fmt);
+  if (rows < 0 || cols <= 0)
+    return gb_fail(CONV_ERR_BAD_PARAM, "rows must be >= 0 and cols > 0");
+  *cb = code_bytes(rows, cols);
+  *sb = scale_bytes(fmt, rows, cols);
+  return gb_ok();
+}
+
+extern "C" conv_status_t conv_fp4_quantize(conv_fp4_format_t fmt, conv_dtype_t dtype, int rows,
+                                           int cols, const void* x, long long ldx,
+                                           float tensor_scale, void* codes, void* scales,
+                                           void* stream) {
+  conv_status_t st = check_matrix(fmt, dtype, rows, cols, x, &ldx, "x", codes, scales);
+  if (st != CONV_OK) return st;
+  if ((st = check_scale(fmt, tensor_scale, "tensor_scale")) != CONV_OK) return st;
+  if (rows == 0) return gb_ok();
+  return cuda_status(launch_fp4_quantize(fmt, dtype, rows, cols, x, ldx, tensor_scale, codes,
+                                         scales, static_cast<cudaStream_t>(stream)),
+                     "4-bit quantisation");
+}
+
+extern "C" conv_status_t conv_fp4_dequantize(conv_fp4_format_t fmt, conv_dtype_t dtype, int rows,
+                                             int cols, const void* codes, const void* scales,
+                                             float tensor_scale, void* y, long long ldy,
+                                             void* stream) {
+  conv_status_t st = check_matrix(fmt, dtype, rows, cols, y, &ldy, "y", codes, scales);
+  if (st != CONV_OK) return st;
+  if ((st = check_scale(fmt, tensor_scale, "tensor_scale")) != CONV_OK) return st;
+  if (rows == 0) return gb_ok();
+  return cuda_status(launch_fp4_dequantize(fmt, dtype, rows, cols, codes, scales, tensor_scale, y,
+                                           ldy, static_cast<cudaStream_t>(stream)),
+                     "4-bit dequantisation");
+}
+
+extern "C" conv_status_t conv_fp4_pack_scales(conv_fp4_format_t fmt, int rows, int cols,
+                                              const void* src, void* scales, void* stream) {
+  if (!is_format(fmt)) return gb_fail(CONV_ERR_BAD_PARAM, "unknown 4-bit format %d", (int)fmt);
+  if (rows < 0 || cols <= 0)
+    return gb_fail(CONV_ERR_BAD_PARAM, "rows must be >= 0 and cols > 0");
+  if (rows == 0) return gb_ok();
+  if (!src || !scales) return gb_fail(CONV_ERR_BAD_PARAM, "NULL tensor");
+  if (!aligned(scales, 16)) return gb_fail(CONV_ERR_ALIGNMENT, "scales must be 16-byte aligned");
+  return cuda_status(launch_fp4_pack_scales(fmt, rows, cols, src, scales,
+                                            static_cast<cudaStream_t>(stream)),
+                     "scale packing");
+}
+
+// ---------------------------------------------------------------------------
+// the product
+
+extern "C" conv_status_t conv_fp4_create(conv_fp4_t* out, conv_fp4_format_t fmt, int C, int K,
+                                         int x_io, int y_io) {
+  if (!out) return gb_fail(CONV_ERR_BAD_PARAM, "out is NULL");
+  *out = nullptr;
+  if (!is_format(fmt)) return gb_fail(CONV_ERR_BAD_PARAM, "unknown 4-bit format %d", (int)fmt);
+  if (C <= 0 || K <= 0) return gb_fail(CONV_ERR_BAD_PARAM, "sizes must be positive");
+  if (x_io < CONV_FP4_IO_BF16 || x_io > CONV_FP4_IO_CODES || y_io < CONV_FP4_IO_BF16 ||
+      y_io > CONV_FP4_IO_CODES)
+    return gb_fail(CONV_ERR_BAD_PARAM, "x_io and y_io must be 0, 1 or 2");
+  gbconv_fp4_s* d = new (std::nothrow) gbconv_fp4_s{};
+  if (!d) return gb_fail(CONV_ERR_BAD_PARAM, "out of host memory");
+  d->fmt = fmt;
+  d->C = C;
+  d->K = K;
+  d->x_io = x_io;
+  d->y_io = y_io;
+  d->x_scale = d->w_scale = d->y_scale = 1.0f;
+  d->ldx = C;
+  d->ldr = d->ldy = K;
+  *out = d;
+  return gb_ok();
+}
+
+extern "C" conv_status_t conv_fp4_destroy(conv_fp4_t d) {
+  delete d;
+  return gb_ok();
+}
+
+extern "C" conv_status_t conv_fp4_set_epilogue(conv_fp4_t d, int act, int has_residual) {
+  if (!d) return gb_fail(CONV_ERR_BAD_PARAM, "desc is NULL");
+  if (act < CONV_ACT_NONE || act > CONV_ACT_SILU)
+    return gb_fail(CONV_ERR_BAD_PARAM, "act must be 0 .. 4");
+  if (has_residual && d->y_io == CONV_FP4_IO_CODES)
+    return gb_fail(CONV_ERR_UNSUPPORTED, "no residual with a 4-bit output");
+  d->act = act;
+  d->has_residual = has_residual ? 1 : 0;
+  return gb_ok();
+}
+
+extern "C" conv_status_t conv_fp4_set_tensor_scales(conv_fp4_t d, float x, float w, float y) {
+  if (!d) return gb_fail(CONV_ERR_BAD_PARAM, "desc is NULL");
+  conv_status_t st;
+  if ((st = check_scale(d->fmt, x, "the tensor scale of x")) != CONV_OK) return st;
+  if ((st = check_scale(d->fmt, w, "the tensor scale of w")) != CONV_OK) return st;
+  if ((st = check_scale(d->fmt, y, "the tensor scale of y")) != CONV_OK) return st;
+  if (!(x * w >= 1e-37f && x * w <= 1e38f))
+    return gb_fail(CONV_ERR_BAD_PARAM, "product of the tensor scales outside fp32");
+  d->x_scale = x;
+  d->w_scale = w;
+  d->y_scale = y;
+  return gb_ok();
+}
+
+extern "C" conv_status_t conv_fp4_set_strides(conv_fp4_t d, long long ldx, long long ldr,
+                                              long long ldy) {
+  if (!d) return gb_fail(CONV_ERR_BAD_PARAM, "desc is NULL");
+  if (ldx && d->x_io == CONV_FP4_IO_CODES && ldx != d->C)
+    return gb_fail(CONV_ERR_UNSUPPORTED, "4-bit x is contiguous");
+  if (ldy && d->y_io == CONV_FP4_IO_CODES && ldy != d->K)
+    return gb_fail(CONV_ERR_UNSUPPORTED, "4-bit y is contiguous");
+  if ((ldx && ldx < d->C) || (ldr && ldr < d->K) || (ldy && ldy < d->K))
+    return gb_fail(CONV_ERR_BAD_PARAM, "row stride below the row");
+  d->ldx = ldx ? ldx : d->C;
+  d->ldr = ldr ? ldr : d->K;
+  d->ldy = ldy ? ldy : d->K;
+  return gb_ok();
+}
+
+// workspace: codes of a float x, then its scales
+static size_t fp4_workspace(const gbconv_fp4_s& d, int M) {
+  return d.x_io == CONV_FP4_IO_CODES ? 0 : code_bytes(M, d.C) + scale_bytes(d.fmt, M, d.C);
+}
+
+extern "C" conv_status_t conv_fp4_workspace_size(conv_fp4_t d, int M, size_t* bytes) {
+  if (!d || !bytes) return gb_fail(CONV_ERR_BAD_PARAM, "NULL argument");
+  if (M < 0) return gb_fail(CONV_ERR_BAD_PARAM, "M must be >= 0");
+  *bytes = fp4_workspace(*d, M);
+  return gb_ok();
+}
+
+extern "C" conv_status_t conv_fp4_fwd(conv_fp4_t d, int M, const void* x, const void* x_scales,
+                                      const void* w_codes, const void* w_scales, const float* bias,
+                                      const void* residual, void* y, void* y_scales, void* ws,
+                                      size_t ws_bytes, void* stream) {
+  if (!d) return gb_fail(CONV_ERR_BAD_PARAM, "desc is NULL");
+  if (M < 0) return gb_fail(CONV_ERR_BAD_PARAM, "M must be >= 0");
+  if (M == 0) return gb_ok();
+  const bool xc = d->x_io == CONV_FP4_IO_CODES, yc = d->y_io == CONV_FP4_IO_CODES;
+  if (!x || !w_codes || !w_scales || !y) return gb_fail(CONV_ERR_BAD_PARAM, "NULL tensor");
+  if (xc != (x_scales != nullptr) || yc != (y_scales != nullptr))
+    return gb_fail(CONV_ERR_BAD_PARAM,
+                   "x_scales / y_scales must be given exactly for a 4-bit x / y");
+  if ((residual != nullptr) != (d->has_residual != 0))
+    return gb_fail(CONV_ERR_BAD_PARAM,
+                   "residual must be given exactly when the descriptor has one");
+  const size_t xa = xc ? 16 : elem_bytes(d->x_io), ya = yc ? 16 : elem_bytes(d->y_io);
+  if (!aligned(x, xa) || !aligned(y, ya) || !aligned(residual, ya) || !aligned(bias, 4))
+    return gb_fail(CONV_ERR_ALIGNMENT, "a tensor is not aligned to its element (codes: 16 bytes)");
+  if (!aligned(x_scales, 16) || !aligned(y_scales, 16) || !aligned(w_codes, 16) ||
+      !aligned(w_scales, 16))
+    return gb_fail(CONV_ERR_ALIGNMENT, "codes and scales must be 16-byte aligned");
+  const size_t need = fp4_workspace(*d, M);
+  if (need && (!ws || ws_bytes < need))
+    return gb_fail(CONV_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need,
+                   ws ? ws_bytes : (size_t)0);
+  if (!aligned(ws, 16)) return gb_fail(CONV_ERR_ALIGNMENT, "workspace must be 16-byte aligned");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  Fp4Gemm g{};
+  g.fmt = d->fmt;
+  g.M = M;
+  g.C = d->C;
+  g.K = d->K;
+  g.act = d->act;
+  g.y_io = d->y_io;
+  g.alpha = d->x_scale * d->w_scale;
+  g.y_scale = d->y_scale;
+  g.w = static_cast<const uint8_t*>(w_codes);
+  g.ws = static_cast<const uint8_t*>(w_scales);
+  g.bias = bias;
+  g.res = residual;
+  g.ldr = d->ldr;
+  g.ldy = d->ldy;
+  g.y = y;
+  g.ys = static_cast<uint8_t*>(y_scales);
+  if (xc) {
+    g.x = static_cast<const uint8_t*>(x);
+    g.xs = static_cast<const uint8_t*>(x_scales);
+  } else {
+    uint8_t* codes = static_cast<uint8_t*>(ws);
+    uint8_t* scales = codes + code_bytes(M, d->C);
+    const cudaError_t e = launch_fp4_quantize(d->fmt, d->x_io, M, d->C, x, d->ldx, d->x_scale,
+                                              codes, scales, st);
+    if (e != cudaSuccess) return cuda_status(e, "4-bit quantisation");
+    g.x = codes;
+    g.xs = scales;
+  }
+  return cuda_status(launch_fp4_gemm(g, st), "4-bit product");
+}
+
+// ---------------------------------------------------------------------------
+// norms around a residual block
+
+struct gbconv_norm_s {
+  NormArgs a;  // everything but rows and tensors; strides resolved
+};
+
+extern "C" conv_status_t conv_norm_create(conv_norm_t* out, int C, conv_dtype_t x_dtype,
+                                          conv_dtype_t z_dtype) {
+  if (!out) return gb_fail(CONV_ERR_BAD_PARAM, "out is NULL");
+  *out = nullptr;
+  if (C <= 0) return gb_fail(CONV_ERR_BAD_PARAM, "C must be positive");
+  if (C > 32768) return gb_fail(CONV_ERR_UNSUPPORTED, "C above 32768");
+  if (!is_float(x_dtype) || !is_float(z_dtype))
+    return gb_fail(CONV_ERR_BAD_PARAM, "x_dtype and z_dtype must be bf16 or fp32");
+  gbconv_norm_s* d = new (std::nothrow) gbconv_norm_s{};
+  if (!d) return gb_fail(CONV_ERR_BAD_PARAM, "out of host memory");
+  NormArgs& a = d->a;
+  a.C = C;
+  a.x_dtype = x_dtype;
+  a.z_dtype = z_dtype;
+  a.gate_rows = 1;
+  a.rs = a.h_scale = 1.0f;
+  a.ldx = a.ldz = a.ldg = a.ldxo = a.ldh = C;
+  *out = d;
+  return gb_ok();
+}
+
+extern "C" conv_status_t conv_norm_destroy(conv_norm_t d) {
+  delete d;
+  return gb_ok();
+}
+
+static conv_status_t check_norm(conv_norm_t d, int kind, float eps, const float* w,
+                                const float* b) {
+  if (!d) return gb_fail(CONV_ERR_BAD_PARAM, "desc is NULL");
+  if (kind < CONV_NORM_NONE || kind > CONV_NORM_LAYER)
+    return gb_fail(CONV_ERR_BAD_PARAM, "unknown norm %d", kind);
+  if (!(eps >= 0.0f && eps < INFINITY)) return gb_fail(CONV_ERR_BAD_PARAM, "eps must be >= 0");
+  if (kind == CONV_NORM_NONE && (w || b))
+    return gb_fail(CONV_ERR_BAD_PARAM, "w and b belong to a norm");
+  if (b && kind != CONV_NORM_LAYER)
+    return gb_fail(CONV_ERR_UNSUPPORTED, "b belongs to a layer norm");
+  if (!aligned(w, 4) || !aligned(b, 4))
+    return gb_fail(CONV_ERR_ALIGNMENT, "w and b must be aligned to their elements");
+  return CONV_OK;
+}
+
+extern "C" conv_status_t conv_norm_set_post(conv_norm_t d, int kind, float eps, const float* w,
+                                            const float* b) {
+  const conv_status_t st = check_norm(d, kind, eps, w, b);
+  if (st != CONV_OK) return st;
+  d->a.post = kind;
+  d->a.eps_post = eps;
+  d->a.w_post = w;
+  d->a.b_post = b;
+  return gb_ok();
+}
+
+extern "C" conv_status_t conv_norm_set_pre(conv_norm_t d, int kind, float eps, const float* w,
+                                           const float* b) {
+  const conv_status_t st = check_norm(d, kind, eps, w, b);
+  if (st != CONV_OK) return st;
+  d->a.pre = kind;
+  d->a.eps_pre = eps;
+  d->a.w_pre = w;
+  d->a.b_pre = b;
+  return gb_ok();
+}
+
+extern "C" conv_status_t conv_norm_set_gate(conv_norm_t d, int gate, int gate_rows,
+                                            float residual_scale) {
+  if (!d) return gb_fail(CONV_ERR_BAD_PARAM, "desc is NULL");
+  if (gate < CONV_GATE_NONE || gate > CONV_GATE_SIGMOID)
+    return gb_fail(CONV_ERR_BAD_PARAM, "unknown gate %d", gate);
+  if (gate_rows <= 0) return gb_fail(CONV_ERR_BAD_PARAM, "gate_rows must be positive");
+  if (!std::isfinite(residual_scale))
+    return gb_fail(CONV_ERR_BAD_PARAM, "residual_scale must be finite");
+  d->a.gate_kind = gate;
+  d->a.gate_rows = gate_rows;
+  d->a.rs = residual_scale;
+  return gb_ok();
+}
+
+extern "C" conv_status_t conv_norm_set_output(conv_norm_t d, int out, float tensor_scale) {
+  if (!d) return gb_fail(CONV_ERR_BAD_PARAM, "desc is NULL");
+  if (out < CONV_NORM_OUT_FLOAT || out > CONV_NORM_OUT_FP4_NV)
+    return gb_fail(CONV_ERR_BAD_PARAM, "unknown output %d", out);
+  const conv_status_t st =
+      check_scale(out == CONV_NORM_OUT_FP4_NV ? CONV_FP4_NV : CONV_FP4_MX, tensor_scale,
+                  "tensor_scale");
+  if (st != CONV_OK) return st;
+  d->a.out = out;
+  d->a.h_scale = tensor_scale;
+  return gb_ok();
+}
+
+extern "C" conv_status_t conv_norm_set_strides(conv_norm_t d, long long ldx, long long ldz,
+                                               long long ldg, long long ldxo, long long ldh) {
+  if (!d) return gb_fail(CONV_ERR_BAD_PARAM, "desc is NULL");
+  const long long ld[5] = {ldx, ldz, ldg, ldxo, ldh};
+  for (long long v : ld)
+    if (v && v < d->a.C) return gb_fail(CONV_ERR_BAD_PARAM, "row stride below the row");
+  long long* const to[5] = {&d->a.ldx, &d->a.ldz, &d->a.ldg, &d->a.ldxo, &d->a.ldh};
+  for (int i = 0; i < 5; ++i) *to[i] = ld[i] ? ld[i] : d->a.C;
+  return gb_ok();
+}
+
+extern "C" conv_status_t conv_norm_fwd(conv_norm_t d, int rows, const void* x, const void* z,
+                                       const void* gate, void* x_out, void* h, void* h_scales,
+                                       void* stream) {
+  if (!d) return gb_fail(CONV_ERR_BAD_PARAM, "desc is NULL");
+  if (rows < 0) return gb_fail(CONV_ERR_BAD_PARAM, "rows must be >= 0");
+  if (rows == 0) return gb_ok();
+  NormArgs a = d->a;
+  if (!x) return gb_fail(CONV_ERR_BAD_PARAM, "x is NULL");
+  if (!x_out && !h) return gb_fail(CONV_ERR_BAD_PARAM, "no output");
+  if ((h != nullptr) != (a.pre != CONV_NORM_NONE))
+    return gb_fail(CONV_ERR_BAD_PARAM, "h must be given exactly when there is a norm before");
+  const bool codes = a.out != CONV_NORM_OUT_FLOAT;
+  if ((h_scales != nullptr) != (h != nullptr && codes))
+    return gb_fail(CONV_ERR_BAD_PARAM, "h_scales must be given exactly for a 4-bit h");
+  if ((gate != nullptr) != (z != nullptr && a.gate_kind != CONV_GATE_NONE))
+    return gb_fail(CONV_ERR_BAD_PARAM,
+                   "gate must be given exactly when the descriptor has one and z is given");
+  if (codes && a.ldh != a.C) return gb_fail(CONV_ERR_UNSUPPORTED, "4-bit h is contiguous");
+  const size_t xb = elem_bytes(a.x_dtype), zb = elem_bytes(a.z_dtype);
+  if (!aligned(x, xb) || !aligned(x_out, xb) || !aligned(z, zb) || !aligned(gate, zb) ||
+      !aligned(h, codes ? 16 : zb) || !aligned(h_scales, 16))
+    return gb_fail(CONV_ERR_ALIGNMENT, "a tensor is not aligned to its element (codes: 16 bytes)");
+  if (x_out == x && a.ldxo != a.ldx)
+    return gb_fail(CONV_ERR_BAD_PARAM, "x_out may be x only with x's row stride");
+  a.rows = rows;
+  a.x = x;
+  a.z = z;
+  a.gate = gate;
+  a.x_out = x_out;
+  a.h = h;
+  a.hs = static_cast<uint8_t*>(h_scales);
+  return cuda_status(launch_norm(a, static_cast<cudaStream_t>(stream)), "norm");
+}

@@ -255,3 +255,48 @@ cudaError_t launch_pack_int8_wino(const gbconv_desc_s& d, const void* w, void* w
 cudaError_t launch_int8_wino(const gbconv_desc_s& d, const void* x, const void* wpack,
                              const int32_t* bias, void* y, void* ws, int* err,
                              unsigned long long wait_ns, cudaStream_t st);
+
+// ---- microscaled 4-bit matrices (formats and layouts: gbconv.h) ---------------
+
+struct gbconv_fp4_s {
+  conv_fp4_format_t fmt;
+  int C, K, x_io, y_io, act, has_residual;
+  float x_scale, w_scale, y_scale;
+  long long ldx, ldr, ldy;  // resolved: never 0
+};
+
+cudaError_t launch_fp4_quantize(int fmt, int dtype, int rows, int cols, const void* x,
+                                long long ldx, float ts, void* codes, void* scales,
+                                cudaStream_t st);
+cudaError_t launch_fp4_dequantize(int fmt, int dtype, int rows, int cols, const void* codes,
+                                  const void* scales, float ts, void* y, long long ldy,
+                                  cudaStream_t st);
+cudaError_t launch_fp4_pack_scales(int fmt, int rows, int cols, const void* src, void* scales,
+                                   cudaStream_t st);
+
+// y[m][k] = act(alpha * sum_c x[m][c] w[k][c] + bias[k] + res[m][k]), 4-bit x and w.
+struct Fp4Gemm {
+  int fmt, M, C, K, act, y_io;
+  const uint8_t *x, *xs, *w, *ws;  // codes and tiled scales
+  float alpha, y_scale;
+  const float* bias;
+  const void* res;  // of y's type
+  long long ldr, ldy;
+  void* y;
+  uint8_t* ys;
+};
+cudaError_t launch_fp4_gemm(const Fp4Gemm& g, cudaStream_t st);
+
+// ---- norms around a residual block ----------------------------------------------
+
+struct NormArgs {
+  int C, rows, x_dtype, z_dtype;
+  int post, pre, gate_kind, gate_rows, out;
+  float eps_post, eps_pre, rs, h_scale;
+  const float *w_post, *b_post, *w_pre, *b_pre;
+  const void *x, *z, *gate;
+  void *x_out, *h;
+  uint8_t* hs;
+  long long ldx, ldz, ldg, ldxo, ldh;
+};
+cudaError_t launch_norm(const NormArgs& a, cudaStream_t st);

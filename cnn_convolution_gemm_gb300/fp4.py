@@ -1,0 +1,211 @@
+"""Microscaled 4-bit matrices and the fully connected layer over them, as torch tensors.
+
+Every computation is a call into libgbconv.so through ``binding`` (the formats and
+their layout in memory: include/gbconv.h); memory and streams come from PyTorch.
+"""
+from __future__ import annotations
+
+import contextlib
+
+import torch
+
+from . import binding as B
+
+CONV_DTYPE = {torch.bfloat16: B.CONV_BF16, torch.float32: B.CONV_F32}
+BLOCK = {B.CONV_FP4_MX: 32, B.CONV_FP4_NV: 16}
+
+
+def stream_handle(stream) -> int:
+    return torch.cuda.current_stream().cuda_stream if stream is None else stream
+
+
+def allocating_on(stream):
+    """Context in which torch allocates for the stream handle (None: the current stream),
+    so that memory freed by another stream's work is not handed out too early."""
+    if stream is None or stream == torch.cuda.current_stream().cuda_stream:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream))
+
+
+def rows_of(t: torch.Tensor, cols: int, what: str):
+    """(rows, elements between rows) of a tensor [..., cols] whose rows are evenly spaced."""
+    if t.shape[-1] != cols:
+        raise ValueError(f"{what}: last dimension {t.shape[-1]}, expected {cols}")
+    if t.dim() == 2:
+        rows, ld = t.shape[0], t.stride(0)
+        if t.stride(1) != 1 and cols > 1 and rows:
+            raise ValueError(f"{what}: the elements of a row must be contiguous")
+        return rows, ld if rows > 1 else cols
+    if not t.is_contiguous():
+        raise ValueError(f"{what}: must be contiguous (or 2-D with contiguous rows)")
+    return t.numel() // cols, cols
+
+
+class Fp4Tensor:
+    """A 4-bit matrix [rows][cols]: codes, scales (tiled, as conv_fp4_size says), tensor scale."""
+
+    __slots__ = ("rows", "cols", "fmt", "tensor_scale", "codes", "scales")
+
+    def __init__(self, rows, cols, fmt, tensor_scale, codes, scales):
+        self.rows, self.cols, self.fmt, self.tensor_scale = rows, cols, fmt, tensor_scale
+        self.codes, self.scales = codes, scales
+
+
+def empty(rows, cols, fmt, device, tensor_scale=1.0, stream=None) -> Fp4Tensor:
+    """An uninitialised 4-bit matrix."""
+    cb, sb = B.conv_fp4_size(fmt, rows, cols)
+    with allocating_on(stream):
+        return Fp4Tensor(rows, cols, fmt, tensor_scale,
+                         torch.empty(cb, dtype=torch.uint8, device=device),
+                         torch.empty(sb, dtype=torch.uint8, device=device))
+
+
+def quantize(x: torch.Tensor, fmt, tensor_scale=1.0, out: Fp4Tensor | None = None,
+             stream=None) -> Fp4Tensor:
+    """x [..., cols] (bf16 or fp32) in 4 bits."""
+    cols = x.shape[-1]
+    rows, ld = rows_of(x, cols, "x")
+    if out is None:
+        out = empty(rows, cols, fmt, x.device, tensor_scale, stream)
+    elif (out.rows, out.cols, out.fmt) != (rows, cols, fmt):
+        raise ValueError("out: a 4-bit matrix of another shape or format")
+    B.conv_fp4_quantize(fmt, CONV_DTYPE[x.dtype], rows, cols, x.data_ptr(), ld, tensor_scale,
+                        out.codes.data_ptr(), out.scales.data_ptr(), stream_handle(stream))
+    out.tensor_scale = tensor_scale
+    return out
+
+
+def dequantize(t: Fp4Tensor, dtype=torch.bfloat16, out: torch.Tensor | None = None,
+               stream=None) -> torch.Tensor:
+    """The values that t stands for, [rows][cols] in dtype (or out's)."""
+    if out is None:
+        with allocating_on(stream):
+            out = torch.empty(t.rows, t.cols, dtype=dtype, device=t.codes.device)
+    rows, ld = rows_of(out, t.cols, "out")
+    if rows != t.rows:
+        raise ValueError(f"out: {rows} rows, expected {t.rows}")
+    B.conv_fp4_dequantize(t.fmt, CONV_DTYPE[out.dtype], rows, t.cols, t.codes.data_ptr(),
+                          t.scales.data_ptr(), t.tensor_scale, out.data_ptr(), ld,
+                          stream_handle(stream))
+    return out
+
+
+class Fp4Linear:
+    """y = act(x W^T + bias (+ residual)) with 4-bit x and W [K][C]; equally a 1x1
+    convolution over NHWC pixels (x [..., C]).
+
+    x_dtype: torch.bfloat16 or torch.float32 (quantised on the way in with tensor scale
+    x_scale), or None for an ``Fp4Tensor``.  y_dtype: likewise, None gives an ``Fp4Tensor``
+    with tensor scale y_scale.  Row strides of the tensors are followed."""
+
+    def __init__(self, C, K, fmt=B.CONV_FP4_MX, x_dtype=torch.bfloat16, y_dtype=torch.bfloat16,
+                 act=B.CONV_ACT_NONE, has_residual=False, x_scale=1.0, y_scale=1.0):
+        self.C, self.K, self.fmt = C, K, fmt
+        self.x_dtype, self.y_dtype = x_dtype, y_dtype
+        self.x_scale, self.y_scale = x_scale, y_scale
+        io = {torch.bfloat16: B.CONV_FP4_IO_BF16, torch.float32: B.CONV_FP4_IO_F32,
+              None: B.CONV_FP4_IO_CODES}
+        self.desc = B.conv_fp4_create(fmt, C, K, io[x_dtype], io[y_dtype])
+        B.conv_fp4_set_epilogue(self.desc, act, has_residual)
+        self.w = None
+        self._strides = (C, K, K)
+        self._sizes = {}  # rows -> workspace bytes
+        self._ws = {}     # stream handle -> workspace (calls on one stream follow each other)
+
+    def __del__(self):
+        d = getattr(self, "desc", None)
+        if d is not None:
+            try:
+                B.conv_fp4_destroy(d)
+            except Exception:
+                pass
+
+    def prepack(self, w: torch.Tensor, w_scale=1.0, stream=None):
+        """Quantise the weights [K][C] (bf16 or fp32) once."""
+        if tuple(w.shape) != (self.K, self.C):
+            raise ValueError(f"w: {tuple(w.shape)}, expected {(self.K, self.C)}")
+        self._set(quantize(w, self.fmt, w_scale, stream=stream))
+
+    def load(self, codes: torch.Tensor, scales: torch.Tensor, w_scale=1.0, stream=None):
+        """Weights held in 4 bits: codes uint8 [K][16 * ceil(C / 32)], scales uint8
+        [K][ceil(C / block)] row by row (a checkpoint's order; tiled here once)."""
+        blocks = -(-self.C // BLOCK[self.fmt])
+        if (tuple(codes.shape) != (self.K, 16 * -(-self.C // 32)) or codes.dtype != torch.uint8
+                or not codes.is_contiguous()):
+            raise ValueError("codes: expected contiguous uint8 [K][16 * ceil(C / 32)]")
+        if (tuple(scales.shape) != (self.K, blocks) or scales.dtype != torch.uint8
+                or not scales.is_contiguous()):
+            raise ValueError("scales: expected contiguous uint8 [K][ceil(C / block)]")
+        _, sb = B.conv_fp4_size(self.fmt, self.K, self.C)
+        with allocating_on(stream):
+            tiled = torch.empty(sb, dtype=torch.uint8, device=codes.device)
+        B.conv_fp4_pack_scales(self.fmt, self.K, self.C, scales.data_ptr(), tiled.data_ptr(),
+                               stream_handle(stream))
+        self._set(Fp4Tensor(self.K, self.C, self.fmt, w_scale, codes, tiled))
+
+    def _set(self, w: Fp4Tensor):
+        B.conv_fp4_set_tensor_scales(self.desc, self.x_scale, w.tensor_scale, self.y_scale)
+        self.w = w
+
+    def _workspace(self, rows, stream, handle):
+        need = self._sizes.get(rows)
+        if need is None:
+            need = self._sizes[rows] = B.conv_fp4_workspace_size(self.desc, rows)
+        ws = self._ws.get(handle)
+        if need and (ws is None or ws.numel() < need):
+            with allocating_on(stream):
+                ws = torch.empty(need, dtype=torch.uint8, device=self.w.codes.device)
+            self._ws[handle] = ws
+        return ws
+
+    def forward(self, x, bias=None, residual=None, out=None, stream=None):
+        if self.w is None:
+            raise RuntimeError("prepack() or load() the weights first")
+        handle = stream_handle(stream)
+        if self.x_dtype is None:
+            if (x.cols, x.fmt, x.tensor_scale) != (self.C, self.fmt, self.x_scale):
+                raise ValueError("x: a 4-bit matrix of another width, format or tensor scale")
+            rows, ldx, lead = x.rows, self.C, (x.rows,)
+            xp, xsp = x.codes.data_ptr(), x.scales.data_ptr()
+        else:
+            if x.dtype != self.x_dtype:
+                raise ValueError(f"x: {x.dtype}, expected {self.x_dtype}")
+            (rows, ldx), lead = rows_of(x, self.C, "x"), x.shape[:-1]
+            xp, xsp = x.data_ptr(), None
+        if bias is not None and (bias.dtype != torch.float32 or bias.numel() != self.K
+                                 or not bias.is_contiguous()):
+            raise ValueError("bias: expected contiguous fp32 [K]")
+        ldr = ldy = self.K
+        ysp = None
+        if self.y_dtype is None:
+            if out is None:
+                out = empty(rows, self.K, self.fmt, self.w.codes.device, self.y_scale, stream)
+            elif (out.rows, out.cols, out.fmt) != (rows, self.K, self.fmt):
+                raise ValueError("out: a 4-bit matrix of another shape or format")
+            out.tensor_scale = self.y_scale
+            yp, ysp = out.codes.data_ptr(), out.scales.data_ptr()
+        else:
+            if out is None:
+                with allocating_on(stream):
+                    out = torch.empty(*lead, self.K, dtype=self.y_dtype,
+                                      device=self.w.codes.device)
+            got, ldy = rows_of(out, self.K, "out")
+            if got != rows or out.dtype != self.y_dtype:
+                raise ValueError("out: another number of rows or type")
+            yp = out.data_ptr()
+        if residual is not None:
+            got, ldr = rows_of(residual, self.K, "residual")
+            if got != rows or residual.dtype != self.y_dtype:
+                raise ValueError("residual: another number of rows or type than y")
+        if (ldx, ldr, ldy) != self._strides:
+            B.conv_fp4_set_strides(self.desc, ldx, ldr, ldy)
+            self._strides = (ldx, ldr, ldy)
+        ws = self._workspace(rows, stream, handle)
+        B.conv_fp4_fwd(self.desc, rows, xp, xsp, self.w.codes.data_ptr(),
+                       self.w.scales.data_ptr(), None if bias is None else bias.data_ptr(),
+                       None if residual is None else residual.data_ptr(), yp, ysp,
+                       None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
+                       handle)
+        return out
+
+    __call__ = forward

@@ -1,0 +1,96 @@
+"""The pass between two residual blocks as a torch-facing layer (conv_norm_* of gbconv.h)."""
+from __future__ import annotations
+
+import torch
+
+from . import binding as B
+from . import fp4
+from .fp4 import CONV_DTYPE, allocating_on, rows_of, stream_handle
+
+
+class ResidualNorm:
+    """u = norm_post(z);  x' = x + residual_scale * g(gate) * u;  h = norm_pre(x').
+
+    post, pre: binding.CONV_NORM_*; w_*, b_*: fp32 [C] or None.  gate: binding.CONV_GATE_*,
+    one row of gates for gate_rows consecutive rows.  dtype: of x and x'; z_dtype: of z,
+    gate and h (dtype if None).  h_fmt: binding.CONV_FP4_* gives h as an ``Fp4Tensor`` with
+    tensor scale h_scale.  Row strides of 2-D tensors are followed."""
+
+    def __init__(self, C, dtype=torch.bfloat16, z_dtype=None, eps=1e-6, post=B.CONV_NORM_NONE,
+                 w_post=None, b_post=None, pre=B.CONV_NORM_NONE, w_pre=None, b_pre=None,
+                 gate=B.CONV_GATE_NONE, gate_rows=1, residual_scale=1.0, h_fmt=None, h_scale=1.0):
+        self.C, self.dtype, self.z_dtype = C, dtype, dtype if z_dtype is None else z_dtype
+        self.post, self.pre, self.gate, self.gate_rows = post, pre, gate, gate_rows
+        self.h_fmt, self.h_scale = h_fmt, h_scale
+        self._params = (w_post, b_post, w_pre, b_pre)  # the descriptor holds their addresses
+        for p in self._params:
+            if p is not None and (p.dtype != torch.float32 or p.numel() != C
+                                  or not p.is_contiguous()):
+                raise ValueError("weights and biases: expected contiguous fp32 [C]")
+        wp, bp, wq, bq = (None if p is None else p.data_ptr() for p in self._params)
+        self.desc = B.conv_norm_create(C, CONV_DTYPE[dtype], CONV_DTYPE[self.z_dtype])
+        B.conv_norm_set_post(self.desc, post, eps, wp, bp)
+        B.conv_norm_set_pre(self.desc, pre, eps, wq, bq)
+        B.conv_norm_set_gate(self.desc, gate, gate_rows, residual_scale)
+        if h_fmt is not None:
+            B.conv_norm_set_output(self.desc, B.CONV_NORM_OUT_FP4_MX if h_fmt == B.CONV_FP4_MX
+                                   else B.CONV_NORM_OUT_FP4_NV, h_scale)
+        self._strides = (C,) * 5
+
+    def __del__(self):
+        d = getattr(self, "desc", None)
+        if d is not None:
+            try:
+                B.conv_norm_destroy(d)
+            except Exception:
+                pass
+
+    def _tensor(self, t, dtype, rows, what):
+        got, ld = rows_of(t, self.C, what)
+        if t.dtype != dtype or got != rows:
+            raise ValueError(f"{what}: {got} rows of {t.dtype}, expected {rows} of {dtype}")
+        return t.data_ptr(), ld
+
+    def forward(self, x, z=None, gate=None, x_out=None, h_out=None, want_x=True, stream=None):
+        """Returns (x', h).  x' is None when want_x is false, h when there is no norm_pre.
+        x_out may be x itself."""
+        C = self.C
+        rows, ldx = rows_of(x, C, "x")
+        if x.dtype != self.dtype:
+            raise ValueError(f"x: {x.dtype}, expected {self.dtype}")
+        zp = gp = xop = hp = hsp = None
+        ldz = ldg = ldxo = ldh = C
+        if z is not None:
+            zp, ldz = self._tensor(z, self.z_dtype, rows, "z")
+        if gate is not None:
+            gp, ldg = self._tensor(gate, self.z_dtype, -(-rows // self.gate_rows), "gate")
+        if want_x:
+            if x_out is None:
+                with allocating_on(stream):
+                    x_out = torch.empty(x.shape, dtype=self.dtype, device=x.device)
+            xop, ldxo = self._tensor(x_out, self.dtype, rows, "x_out")
+        else:
+            x_out = None
+        if self.pre == B.CONV_NORM_NONE:
+            h_out = None
+        elif self.h_fmt is not None:
+            if h_out is None:
+                h_out = fp4.empty(rows, C, self.h_fmt, x.device, self.h_scale, stream)
+            elif (h_out.rows, h_out.cols, h_out.fmt) != (rows, C, self.h_fmt):
+                raise ValueError("h_out: a 4-bit matrix of another shape or format")
+            h_out.tensor_scale = self.h_scale
+            hp, hsp = h_out.codes.data_ptr(), h_out.scales.data_ptr()
+        else:
+            if h_out is None:
+                with allocating_on(stream):
+                    h_out = torch.empty(x.shape, dtype=self.z_dtype, device=x.device)
+            hp, ldh = self._tensor(h_out, self.z_dtype, rows, "h_out")
+        strides = (ldx, ldz, ldg, ldxo, ldh)
+        if strides != self._strides:
+            B.conv_norm_set_strides(self.desc, *strides)
+            self._strides = strides
+        B.conv_norm_fwd(self.desc, rows, x.data_ptr(), zp, gp, xop, hp, hsp,
+                        stream_handle(stream))
+        return x_out, h_out
+
+    __call__ = forward

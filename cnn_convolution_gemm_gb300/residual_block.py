@@ -1,0 +1,79 @@
+"""A residual block in 4 bits: two fully connected layers (1x1 convolutions over NHWC
+pixels) between the norms around them.
+
+  h  = norm_pre(x), 4 bits             one pass over x
+  t  = gelu(h W1^T + b1), 4 bits       quantised in the product's epilogue
+  z  = t W2^T + b2
+  x' = x + residual_scale * g(gate) * norm_post(z);  h' = norm_next(x')    one pass
+
+h' is what the next block starts from: blocks chained with ``chain=True`` hand it on in
+4 bits, so the stream x is read and written once per block.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import binding as B
+from . import fp4
+from .fp4 import Fp4Linear
+from .norm import ResidualNorm
+
+
+class Fp4ResidualBlock:
+    """RMS norms throughout; gate, gate_rows, residual_scale as in ``ResidualNorm``.
+    w_next: weight of the norm behind the block (the next block's, or the final one);
+    chain: give h' in 4 bits with tensor scale next_scale instead of dtype.
+    h_scale, t_scale: tensor scales of h and t (CONV_FP4_NV)."""
+
+    def __init__(self, C, hidden, fmt=B.CONV_FP4_MX, dtype=torch.bfloat16, eps=1e-6,
+                 residual_scale=1.0, gate=B.CONV_GATE_NONE, gate_rows=1, w_pre=None, w_post=None,
+                 w_next=None, b1=None, b2=None, h_scale=1.0, t_scale=1.0, chain=False,
+                 next_scale=1.0):
+        self.C, self.hidden, self.fmt, self.dtype = C, hidden, fmt, dtype
+        self.h_scale, self.t_scale = h_scale, t_scale
+        self.b1, self.b2 = b1, b2
+        self.norm_in = ResidualNorm(C, dtype, torch.bfloat16, eps=eps, pre=B.CONV_NORM_RMS,
+                                    w_pre=w_pre, h_fmt=fmt, h_scale=h_scale)
+        self.fc1 = Fp4Linear(C, hidden, fmt, x_dtype=None, y_dtype=None, act=B.CONV_ACT_GELU,
+                             x_scale=h_scale, y_scale=t_scale)
+        self.fc2 = Fp4Linear(hidden, C, fmt, x_dtype=None, y_dtype=torch.bfloat16,
+                             x_scale=t_scale)
+        self.norm_out = ResidualNorm(C, dtype, torch.bfloat16, eps=eps, post=B.CONV_NORM_RMS,
+                                     w_post=w_post, pre=B.CONV_NORM_RMS, w_pre=w_next, gate=gate,
+                                     gate_rows=gate_rows, residual_scale=residual_scale,
+                                     h_fmt=fmt if chain else None, h_scale=next_scale)
+        self._bufs = {}  # stream handle -> (rows, h, t, z)
+
+    def prepack(self, w1, w2, w1_scale=1.0, w2_scale=1.0, stream=None):
+        """Quantise the weights w1 [hidden][C], w2 [C][hidden] once."""
+        self.fc1.prepack(w1, w1_scale, stream)
+        self.fc2.prepack(w2, w2_scale, stream)
+
+    def load(self, w1, s1, g1, w2, s2, g2, stream=None):
+        """Weights held in 4 bits (codes, row-by-row scales, tensor scale of each)."""
+        self.fc1.load(w1, s1, g1, stream)
+        self.fc2.load(w2, s2, g2, stream)
+
+    def _buffers(self, rows, device, stream, handle):
+        got = self._bufs.get(handle)
+        if got is None or got[0] != rows:
+            with fp4.allocating_on(stream):
+                got = (rows, fp4.empty(rows, self.C, self.fmt, device, self.h_scale),
+                       fp4.empty(rows, self.hidden, self.fmt, device, self.t_scale),
+                       torch.empty(rows, self.C, dtype=torch.bfloat16, device=device))
+            self._bufs[handle] = got
+        return got[1:]
+
+    def forward(self, x, gate=None, h=None, x_out=None, h_out=None, stream=None):
+        """x [..., C] -> (x', h').  h: norm_pre(x) in 4 bits when the block before handed
+        it on, else None."""
+        rows, _ = fp4.rows_of(x, self.C, "x")
+        handle = fp4.stream_handle(stream)
+        hb, t, z = self._buffers(rows, x.device, stream, handle)
+        if h is None:
+            _, h = self.norm_in(x, h_out=hb, want_x=False, stream=stream)
+        self.fc1(h, bias=self.b1, out=t, stream=stream)
+        self.fc2(t, bias=self.b2, out=z, stream=stream)
+        return self.norm_out(x, z, gate=gate, x_out=x_out, h_out=h_out, stream=stream)
+
+    __call__ = forward

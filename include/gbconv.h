@@ -63,7 +63,14 @@ typedef enum { CONV_BF16 = 0, CONV_F32 = 1, CONV_INT8 = 2 } conv_dtype_t;
  * multiples of 32; weights stay [K][R][S][C]. */
 typedef enum { CONV_NHWC = 0, CONV_NCHW = 1, CONV_NC32HW32 = 2 } conv_layout_t;
 
-typedef enum { CONV_ACT_NONE = 0, CONV_ACT_RELU = 1, CONV_ACT_RELU6 = 2 } conv_act_t;
+/* GELU (x Phi(x), through erf) and SILU (x / (1 + exp(-x))): conv_fp4_* only. */
+typedef enum {
+  CONV_ACT_NONE = 0,
+  CONV_ACT_RELU = 1,
+  CONV_ACT_RELU6 = 2,
+  CONV_ACT_GELU = 3,
+  CONV_ACT_SILU = 4
+} conv_act_t;
 
 /* Algorithm ids ([MegEngine] "Fast-Run": Im2col, Direct and Winograd are the
  * candidate implementations).  Ids are stable. */
@@ -337,6 +344,140 @@ conv_status_t conv_maxpool2d_nhwc_bf16(const void* x, void* y, int N, int C, int
 /* Global average pooling, NHWC bf16 [N][H][W][C] -> bf16 [N][C]. */
 conv_status_t conv_global_avgpool_nhwc_bf16(const void* x, void* y, int N, int C, int H, int W,
                                             void* stream);
+
+/* ---- microscaled 4-bit floating point --------------------------------------- */
+
+/* A matrix [rows][cols] whose rows are cut into blocks of consecutive elements;
+ * each element is an E2M1 code (sign, 2 exponent bits, 1 mantissa bit: 0, 0.5, 1,
+ * 1.5, 2, 3, 4, 6 and their negatives), each block has one scale:
+ *   CONV_FP4_MX  blocks of 32, scale 2^e (E8M0: the byte e + 127);
+ *                e = max(floor(log2(max |x|)) - 2, -127), -127 for a block of zeros;
+ *   CONV_FP4_NV  blocks of 16, scale s * tensor_scale, s in E4M3 (a byte);
+ *                s = the E4M3 value nearest to min(max |x| / (6 tensor_scale), 448).
+ * An element is the E2M1 value nearest to x / scale (ties to the even code,
+ * magnitudes above 6 become 6; 0 where the scale is 0).  A block that holds an
+ * infinity or a NaN gets the scale NaN (byte 0xFF; 0x7F for NV) and codes 0: its
+ * values are NaN, so the fault stays visible in every product it enters.
+ * tensor_scale: 1e-30 .. 1e30; it must be 1 for CONV_FP4_MX.
+ *
+ * In memory:
+ *   codes   [rows][P] bytes, P = 16 * ceil(cols / 32); element c of a row is the
+ *           low (c even) or high (c odd) half of byte c / 2; padding codes are 0.
+ *   scales  tiles of 128 rows x 4 blocks, 512 bytes each, in the order the tensor
+ *           core takes them: with TJ = ceil(cols / (4 * block)), the scale of row r,
+ *           block b is at ((r / 128) * TJ + b / 4) * 512 + (r % 32) * 16 +
+ *           (r / 32 % 4) * 4 + b % 4.  Blocks past the last of a row are written
+ *           as byte 0; rows past the last are not written. */
+typedef enum { CONV_FP4_MX = 0, CONV_FP4_NV = 1 } conv_fp4_format_t;
+
+/* Bytes of the codes and of the scales of a [rows][cols] matrix. */
+conv_status_t conv_fp4_size(conv_fp4_format_t fmt, int rows, int cols, size_t* code_bytes,
+                            size_t* scale_bytes);
+/* Quantise x: device, dtype CONV_BF16 or CONV_F32, row r at x + r * ldx elements
+ * (ldx >= cols, or 0 for contiguous rows), aligned to its element.  codes, scales: device,
+ * 16-byte aligned.  The quotients are rounded to fp32 before they are rounded to
+ * E2M1 (and max / (6 tensor_scale) before E4M3).  rows may be 0.  Stream-ordered. */
+conv_status_t conv_fp4_quantize(conv_fp4_format_t fmt, conv_dtype_t dtype, int rows, int cols,
+                                const void* x, long long ldx, float tensor_scale, void* codes,
+                                void* scales, void* stream);
+/* The values that codes and scales stand for: y = code * (s * tensor_scale) in
+ * fp32, rounded to dtype (CONV_BF16 or CONV_F32); ldy as ldx above.  Stream-ordered. */
+conv_status_t conv_fp4_dequantize(conv_fp4_format_t fmt, conv_dtype_t dtype, int rows, int cols,
+                                  const void* codes, const void* scales, float tensor_scale,
+                                  void* y, long long ldy, void* stream);
+/* Scale bytes held row by row ([rows][ceil(cols / block)], as checkpoints hold
+ * them; any alignment) into the tiled order above.  Stream-ordered. */
+conv_status_t conv_fp4_pack_scales(conv_fp4_format_t fmt, int rows, int cols, const void* src,
+                                   void* scales, void* stream);
+
+/* The fully connected layer (equally the 1x1 convolution over NHWC pixels) with
+ * both operands in 4 bits:
+ *   y[m][k] = act(alpha * sum_c X[m][c] W[k][c] + bias[k] (+ residual[m][k]))
+ * with W [K][C] and X [M][C] the values of 4-bit matrices of one format, alpha the
+ * product of their tensor scales, fp32 accumulation.  x_io / y_io: */
+typedef enum {
+  CONV_FP4_IO_BF16 = 0,  /* a bf16 tensor; x is quantised on the way in              */
+  CONV_FP4_IO_F32 = 1,   /* an fp32 tensor; x is quantised on the way in             */
+  CONV_FP4_IO_CODES = 2  /* codes and scales as above; y is quantised from its fp32
+                            values, so that it can be the next layer's x             */
+} conv_fp4_io_t;
+typedef struct gbconv_fp4_s* conv_fp4_t;
+
+/* C inputs, K outputs (both > 0).  Defaults: no activation, no residual, tensor
+ * scales 1, contiguous rows.  The descriptor is owned by the caller. */
+conv_status_t conv_fp4_create(conv_fp4_t* out, conv_fp4_format_t fmt, int C, int K, int x_io,
+                              int y_io);
+conv_status_t conv_fp4_destroy(conv_fp4_t desc);
+/* act: conv_act_t; has_residual: conv_fp4_fwd reads a residual of y's type and adds
+ * it before the activation (not with y_io CONV_FP4_IO_CODES). */
+conv_status_t conv_fp4_set_epilogue(conv_fp4_t desc, int act, int has_residual);
+/* Tensor scales of x, of the weights and (y_io CONV_FP4_IO_CODES) of y. */
+conv_status_t conv_fp4_set_tensor_scales(conv_fp4_t desc, float x, float w, float y);
+/* Elements between rows of x, residual and y (0: contiguous; codes are always
+ * contiguous).  At least the row's length. */
+conv_status_t conv_fp4_set_strides(conv_fp4_t desc, long long ldx, long long ldr, long long ldy);
+/* Bytes of device workspace conv_fp4_fwd needs for M rows on the current device. */
+conv_status_t conv_fp4_workspace_size(conv_fp4_t desc, int M, size_t* bytes);
+/* x: device, per x_io and strides, aligned to its element (codes: 16 bytes);
+ * x_scales: the tiled scales of codes, else NULL.  w_codes, w_scales: the weights as
+ * [K][C] 4-bit matrix (conv_fp4_quantize, or conv_fp4_pack_scales), 16-byte aligned.
+ * bias: device fp32 [K] or NULL.  residual: NULL unless the descriptor has one.
+ * y, y_scales: as x, x_scales, not overlapping any input (y may equal residual when
+ * their row strides are equal).  ws: 16-byte aligned, conv_fp4_workspace_size(M) bytes;
+ * calls that can overlap on the GPU need their own.  M may be 0.  Stream-ordered. */
+conv_status_t conv_fp4_fwd(conv_fp4_t desc, int M, const void* x, const void* x_scales,
+                           const void* w_codes, const void* w_scales, const float* bias,
+                           const void* residual, void* y, void* y_scales, void* ws,
+                           size_t ws_bytes, void* stream);
+
+/* ---- norms around a residual block ------------------------------------------- */
+
+/* One pass over the rows of a residual stream, between one block and the next:
+ *   u  = norm_post(z)                                     z: the block's output
+ *   x' = x + residual_scale * g(gate[row / gate_rows]) * u
+ *   h  = norm_pre(x')                                     the next block's input
+ * norm: none; RMS, v / sqrt(mean(v^2) + eps) * w; layer, (v - mean) / sqrt(var + eps)
+ * * w + b.  g: no gate, the gate itself, or its sigmoid.  Everything between the
+ * loads and the stores is fp32; h is made from x' before x' is rounded. */
+typedef enum { CONV_NORM_NONE = 0, CONV_NORM_RMS = 1, CONV_NORM_LAYER = 2 } conv_norm_kind_t;
+typedef enum { CONV_GATE_NONE = 0, CONV_GATE_LINEAR = 1, CONV_GATE_SIGMOID = 2 } conv_gate_t;
+typedef enum {
+  CONV_NORM_OUT_FLOAT = 0,   /* h in z_dtype                                        */
+  CONV_NORM_OUT_FP4_MX = 1,  /* h as 4-bit codes and scales (conv_fp4_size)         */
+  CONV_NORM_OUT_FP4_NV = 2
+} conv_norm_out_t;
+typedef struct gbconv_norm_s* conv_norm_t;
+
+/* C channels (1 .. 32768).  x_dtype: type of x and x'; z_dtype: type of z, gate and
+ * h (each CONV_BF16 or CONV_F32).  Defaults: both norms none, no gate,
+ * residual_scale 1, h in z_dtype, contiguous rows. */
+conv_status_t conv_norm_create(conv_norm_t* out, int C, conv_dtype_t x_dtype,
+                               conv_dtype_t z_dtype);
+conv_status_t conv_norm_destroy(conv_norm_t desc);
+/* The norm of z / of x': kind, eps (>= 0), w and b device fp32 [C] that must stay
+ * valid while the descriptor is used (NULL: ones / zeros; b: layer norms only). */
+conv_status_t conv_norm_set_post(conv_norm_t desc, int kind, float eps, const float* w,
+                                 const float* b);
+conv_status_t conv_norm_set_pre(conv_norm_t desc, int kind, float eps, const float* w,
+                                const float* b);
+/* gate: conv_gate_t; one row of gates serves gate_rows (> 0) consecutive rows: 1 for a
+ * gate per token, H * W for one per image, the row count or more for one per call. */
+conv_status_t conv_norm_set_gate(conv_norm_t desc, int gate, int gate_rows,
+                                 float residual_scale);
+/* out: conv_norm_out_t; tensor_scale: of the 4-bit h (1 unless CONV_NORM_OUT_FP4_NV). */
+conv_status_t conv_norm_set_output(conv_norm_t desc, int out, float tensor_scale);
+/* Elements between rows of x, z, gate, x' and h (0: contiguous). */
+conv_status_t conv_norm_set_strides(conv_norm_t desc, long long ldx, long long ldz, long long ldg,
+                                    long long ldxo, long long ldh);
+/* rows may be 0.  z NULL: x' = x (no block before: the first norm of a network).
+ * gate: given exactly when the descriptor has a gate and z is given.  x_out: x' or
+ * NULL when it is not wanted; it may be x itself.  h: NULL exactly when norm_pre is
+ * none; h_scales: the scales of a 4-bit h, else NULL.  Tensors are device memory
+ * aligned to their element (4-bit h: 16 bytes) and, but for x_out == x, do not
+ * overlap outputs.  Stream-ordered. */
+conv_status_t conv_norm_fwd(conv_norm_t desc, int rows, const void* x, const void* z,
+                            const void* gate, void* x_out, void* h, void* h_scales,
+                            void* stream);
 
 /* ---- status ------------------------------------------------------------- */
 

@@ -1,0 +1,185 @@
+"""Refusals and sizes of the 4-bit and norm entry points (no GPU: everything here returns
+before anything is launched), and the reference of their GPU tests against itself."""
+import numpy as np
+import pytest
+
+from tests import fp4_ref as R
+
+
+@pytest.fixture(scope="module")
+def B():
+    from cnn_convolution_gemm_gb300 import build
+    build.build()
+    from cnn_convolution_gemm_gb300 import binding
+    binding.load_library()
+    return binding
+
+
+def refused(B, status, fn, *args, **kw):
+    with pytest.raises(B.GbconvError) as e:
+        fn(*args, **kw)
+    assert e.value.status_name == status, (e.value.status_name, e.value.detail)
+    assert e.value.detail
+
+
+BAD, UNSUP, ALIGN, WS = ("CONV_ERR_BAD_PARAM", "CONV_ERR_UNSUPPORTED", "CONV_ERR_ALIGNMENT",
+                         "CONV_ERR_WORKSPACE")
+P = 0x10000  # a 16-byte aligned address that nothing dereferences
+
+
+def test_sizes(B):
+    assert B.conv_fp4_size(B.CONV_FP4_MX, 1, 1) == (16, 512)
+    assert B.conv_fp4_size(B.CONV_FP4_MX, 129, 128) == (129 * 64, 2 * 512)
+    assert B.conv_fp4_size(B.CONV_FP4_NV, 129, 129) == (129 * 80, 2 * 3 * 512)
+    assert B.conv_fp4_size(B.CONV_FP4_NV, 0, 64) == (0, 0)
+    # past 32 bits
+    assert B.conv_fp4_size(B.CONV_FP4_MX, 1 << 20, 1 << 14) == (1 << 33, 1 << 29)
+    refused(B, BAD, B.conv_fp4_size, 2, 4, 4)
+    refused(B, BAD, B.conv_fp4_size, B.CONV_FP4_MX, -1, 4)
+    refused(B, BAD, B.conv_fp4_size, B.CONV_FP4_MX, 4, 0)
+
+
+def test_quantize_refusals(B):
+    q, dq = B.conv_fp4_quantize, B.conv_fp4_dequantize
+    MX, NV, BF = B.CONV_FP4_MX, B.CONV_FP4_NV, B.CONV_BF16
+    refused(B, BAD, q, 5, BF, 4, 64, P, 64, 1.0, P, P)
+    refused(B, BAD, q, MX, B.CONV_INT8, 4, 64, P, 64, 1.0, P, P)
+    refused(B, BAD, q, MX, BF, 4, 64, P, 63, 1.0, P, P)
+    refused(B, BAD, q, MX, BF, -4, 64, P, 64, 1.0, P, P)
+    refused(B, BAD, q, MX, BF, 4, 64, 0, 64, 1.0, P, P)
+    refused(B, BAD, q, MX, BF, 4, 64, P, 64, 0.5, P, P)   # MX has no tensor scale
+    for g in (0.0, -1.0, float("nan"), float("inf"), 1e-31, 1e31):
+        refused(B, BAD, q, NV, BF, 4, 64, P, 64, g, P, P)
+        refused(B, BAD, dq, NV, BF, 4, 64, P, P, g, P, 64)
+    refused(B, ALIGN, q, MX, BF, 4, 64, P + 1, 64, 1.0, P, P)
+    refused(B, ALIGN, q, MX, B.CONV_F32, 4, 64, P + 2, 64, 1.0, P, P)
+    refused(B, ALIGN, q, MX, BF, 4, 64, P, 64, 1.0, P + 8, P)
+    refused(B, ALIGN, dq, MX, BF, 4, 64, P, P + 8, 1.0, P, 64)
+    refused(B, BAD, B.conv_fp4_pack_scales, MX, 4, 0, P, P)
+    refused(B, BAD, B.conv_fp4_pack_scales, MX, 4, 64, 0, P)
+    refused(B, ALIGN, B.conv_fp4_pack_scales, MX, 4, 64, P + 1, P + 1)
+    # nothing to do: no tensor is looked at
+    q(MX, BF, 0, 64, 0, 64, 1.0, 0, 0)
+    dq(NV, BF, 0, 64, 0, 0, 0.5, 0, 64)
+    B.conv_fp4_pack_scales(MX, 0, 64, 0, 0)
+
+
+def test_product_refusals(B):
+    MX, NV = B.CONV_FP4_MX, B.CONV_FP4_NV
+    refused(B, BAD, B.conv_fp4_create, 7, 64, 64)
+    refused(B, BAD, B.conv_fp4_create, MX, 0, 64)
+    refused(B, BAD, B.conv_fp4_create, MX, 64, -1)
+    refused(B, BAD, B.conv_fp4_create, MX, 64, 64, 3)
+    d = B.conv_fp4_create(NV, 96, 48)
+    refused(B, BAD, B.conv_fp4_set_epilogue, d, 5, False)
+    refused(B, BAD, B.conv_fp4_set_tensor_scales, d, 0.0, 1.0, 1.0)
+    refused(B, BAD, B.conv_fp4_set_tensor_scales, d, 1e30, 1e30, 1.0)
+    refused(B, BAD, B.conv_fp4_set_strides, d, 95, 0, 0)
+    refused(B, BAD, B.conv_fp4_set_strides, d, 0, 47, 0)
+    refused(B, BAD, B.conv_fp4_set_strides, d, 0, 0, 47)
+    refused(B, BAD, B.conv_fp4_workspace_size, d, -1)
+    need = B.conv_fp4_workspace_size(d, 200)
+    assert need >= sum(B.conv_fp4_size(NV, 200, 96))
+    f = B.conv_fp4_fwd
+    refused(B, BAD, f, d, -1, P, None, P, P, None, None, P, None, P, need)
+    refused(B, BAD, f, d, 200, None, None, P, P, None, None, P, None, P, need)
+    refused(B, BAD, f, d, 200, P, P, P, P, None, None, P, None, P, need)      # scales of a float x
+    refused(B, BAD, f, d, 200, P, None, P, P, None, None, P, P, P, need)      # scales of a float y
+    refused(B, BAD, f, d, 200, P, None, P, P, None, P, P, None, P, need)      # residual not declared
+    refused(B, WS, f, d, 200, P, None, P, P, None, None, P, None, None, 0)
+    refused(B, WS, f, d, 200, P, None, P, P, None, None, P, None, P, need - 1)
+    refused(B, ALIGN, f, d, 200, P + 1, None, P, P, None, None, P, None, P, need)
+    refused(B, ALIGN, f, d, 200, P, None, P + 8, P, None, None, P, None, P, need)
+    refused(B, ALIGN, f, d, 200, P, None, P, P, P + 2, None, P, None, P, need)
+    refused(B, ALIGN, f, d, 200, P, None, P, P, None, None, P, None, P + 4, need)
+    f(d, 0, None, None, None, None, None, None, None, None)  # no rows
+    B.conv_fp4_destroy(d)
+    c = B.conv_fp4_create(MX, 96, 48, B.CONV_FP4_IO_CODES, B.CONV_FP4_IO_CODES)
+    refused(B, UNSUP, B.conv_fp4_set_epilogue, c, 0, True)
+    refused(B, UNSUP, B.conv_fp4_set_strides, c, 100, 0, 0)
+    refused(B, UNSUP, B.conv_fp4_set_strides, c, 0, 0, 100)
+    refused(B, BAD, B.conv_fp4_set_tensor_scales, c, 2.0, 1.0, 1.0)
+    refused(B, BAD, f, c, 8, P, None, P, P, None, None, P, P, P, 1 << 20)     # codes without scales
+    refused(B, ALIGN, f, c, 8, P + 2, P, P, P, None, None, P, P, P, 1 << 20)
+    B.conv_fp4_destroy(c)
+    # the activations of the 4-bit product stay refused where convolutions do not have them
+    conv = B.conv_desc_create(1, 8, 8, 8, 8, 3, 3, 1, 1)
+    refused(B, BAD, B.conv_desc_set_epilogue, conv, B.CONV_ACT_GELU, False)
+    B.conv_desc_destroy(conv)
+
+
+def test_norm_refusals(B):
+    refused(B, BAD, B.conv_norm_create, 0)
+    refused(B, UNSUP, B.conv_norm_create, 32769)
+    refused(B, BAD, B.conv_norm_create, 64, B.CONV_INT8)
+    d = B.conv_norm_create(64)
+    refused(B, BAD, B.conv_norm_set_post, d, 3)
+    refused(B, BAD, B.conv_norm_set_post, d, B.CONV_NORM_RMS, -1.0)
+    refused(B, BAD, B.conv_norm_set_pre, d, B.CONV_NORM_RMS, float("nan"))
+    refused(B, BAD, B.conv_norm_set_pre, d, B.CONV_NORM_NONE, 0.0, P)
+    refused(B, UNSUP, B.conv_norm_set_pre, d, B.CONV_NORM_RMS, 0.0, P, P)
+    refused(B, ALIGN, B.conv_norm_set_pre, d, B.CONV_NORM_RMS, 0.0, P + 2)
+    refused(B, BAD, B.conv_norm_set_gate, d, 3)
+    refused(B, BAD, B.conv_norm_set_gate, d, 1, 0)
+    refused(B, BAD, B.conv_norm_set_gate, d, 1, 1, float("inf"))
+    refused(B, BAD, B.conv_norm_set_output, d, 3)
+    refused(B, BAD, B.conv_norm_set_output, d, B.CONV_NORM_OUT_FP4_MX, 0.5)
+    refused(B, BAD, B.conv_norm_set_output, d, B.CONV_NORM_OUT_FP4_NV, 0.0)
+    refused(B, BAD, B.conv_norm_set_strides, d, 63)
+    f = B.conv_norm_fwd
+    refused(B, BAD, f, d, -1, P, P, None, P, None)
+    refused(B, BAD, f, d, 4, None, P, None, P, None)
+    refused(B, BAD, f, d, 4, P, P, None, None, None)      # nothing to write
+    refused(B, BAD, f, d, 4, P, P, None, P, P)            # h without a norm before
+    refused(B, BAD, f, d, 4, P, P, P, P, None)            # a gate that is not declared
+    refused(B, ALIGN, f, d, 4, P + 1, P, None, P, None)
+    B.conv_norm_set_pre(d, B.CONV_NORM_RMS)
+    B.conv_norm_set_gate(d, B.CONV_GATE_SIGMOID)
+    refused(B, BAD, f, d, 4, P, P, P, P, None)            # no h
+    refused(B, BAD, f, d, 4, P, P, None, P, P)            # no gate
+    refused(B, BAD, f, d, 4, P, P, P, P, P, P)            # scales of a float h
+    B.conv_norm_set_output(d, B.CONV_NORM_OUT_FP4_MX)
+    refused(B, BAD, f, d, 4, P, P, P, P, P)               # no scales of a 4-bit h
+    refused(B, ALIGN, f, d, 4, P, P, P, P, P + 2, P)
+    B.conv_norm_set_strides(d, 80, 0, 0, 72, 0)
+    refused(B, BAD, f, d, 4, P, P, P, P, P, P)            # in place with another stride
+    B.conv_norm_set_strides(d, 0, 0, 0, 0, 80)
+    refused(B, UNSUP, f, d, 4, P, P, P, P, P, P)          # 4-bit rows are contiguous
+    f(d, 0, None, None, None, None, None)
+    B.conv_norm_destroy(d)
+
+
+def test_reference_rounding():
+    """The tests' own reference: levels, ties and saturation of E2M1 and E4M3."""
+    v = np.array([0.25, 0.2501, 0.75, 0.7499, 1.25, 1.75, 2.5, 3.5, 5.0, 5.001, 7.0, -0.3, -9.0])
+    want = [0, 0.5, 1, 0.5, 1, 2, 2, 4, 4, 6, 6, -0.5, -6]
+    np.testing.assert_array_equal(R.e2m1_value(R.e2m1_code(v)), want)
+    np.testing.assert_array_equal(R.e2m1_code(R.e2m1_value(np.arange(8, dtype=np.uint8))), np.arange(8))
+    assert R.E4M3[-1] == 448 and R.E4M3[1] == 2.0 ** -9 and R.E4M3[8] == 2.0 ** -6
+    np.testing.assert_array_equal(R.e4m3_byte(R.E4M3), np.arange(127))
+    assert R.e4m3_value(R.e4m3_byte([17.0, 19.0, 2.0 ** -10, 3 * 2.0 ** -10])).tolist() == [16, 20, 0, 2.0 ** -8]
+    # every MX block's largest element keeps 4 <= |x| / scale < 8
+    x = np.abs(np.random.default_rng(0).standard_normal((50, 64))).astype(np.float32)
+    code, byte = R.quantize(x, R.MX)
+    s = R.scale_values(byte, R.MX)
+    ratio = x.reshape(50, 2, 32).max(2) / s
+    assert ((4 <= ratio) & (ratio < 8)).all()
+
+
+def test_torch_layers_check_their_tensors(B):
+    torch = pytest.importorskip("torch")
+    from cnn_convolution_gemm_gb300 import fp4
+    from cnn_convolution_gemm_gb300.norm import ResidualNorm
+    with pytest.raises(ValueError):
+        fp4.rows_of(torch.zeros(4, 6).t(), 4, "x")       # columns not contiguous
+    with pytest.raises(ValueError):
+        fp4.rows_of(torch.zeros(2, 3, 4)[:, :, :3], 3, "x")
+    assert fp4.rows_of(torch.zeros(5, 9)[:, 2:8], 6, "x") == (5, 9)
+    assert fp4.rows_of(torch.zeros(2, 3, 4), 4, "x") == (6, 4)
+    layer = fp4.Fp4Linear(64, 32)
+    with pytest.raises(RuntimeError):
+        layer(torch.zeros(1, 64, dtype=torch.bfloat16))
+    with pytest.raises(ValueError):
+        layer.load(torch.zeros(32, 33, dtype=torch.uint8), torch.zeros(32, 2, dtype=torch.uint8))
+    with pytest.raises(ValueError):
+        ResidualNorm(64, w_pre=torch.zeros(63), pre=B.CONV_NORM_RMS)

@@ -1,0 +1,332 @@
+"""Microscaled 4-bit quantisation (bit for bit against the definition) and the product
+of 4-bit matrices (against 64 bits) on the GPU."""
+import numpy as np
+import pytest
+
+from tests import fp4_ref as R
+from tests.gpu_util import need_gpu
+
+pytestmark = pytest.mark.gpu
+FMTS = [R.MX, R.NV]
+NAMES = {R.MX: "mx", R.NV: "nv"}
+
+
+def _fp4():
+    torch = need_gpu()
+    from cnn_convolution_gemm_gb300 import fp4
+    return torch, fp4
+
+
+def _sync(torch):
+    R.B.conv_sync_status(torch.cuda.current_stream().cuda_stream)
+
+
+def _activations(rng, rows, cols):
+    """Normal values of channel-wise different size, some exact ties and zeros among them."""
+    x = rng.standard_normal((rows, cols)) * np.exp(0.7 * rng.standard_normal(cols))
+    pick = rng.random((rows, cols))
+    x = np.where(pick < 0.1, rng.choice([0.0, 0.25, -0.75, 1.25, 1.75, 2.5, -3.5, 5.0], (rows, cols)), x)
+    x[rng.random(rows) < 0.1] = 0
+    return x.astype(np.float32)
+
+
+def _to(torch, a, dtype):
+    return torch.from_numpy(np.ascontiguousarray(a)).to(dtype).cuda()
+
+
+def _f32(t):
+    return t.float().cpu().numpy()
+
+
+@pytest.mark.parametrize("fmt", FMTS, ids=NAMES.get)
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("rows,cols", [(1, 1), (1, 4096), (3, 16), (5, 31), (2, 33), (130, 64),
+                                       (7, 100), (257, 272), (64, 1000), (33, 2080), (300, 129)])
+def test_quantize_is_the_definition(fmt, dtype, rows, cols):
+    torch, fp4 = _fp4()
+    rng = np.random.default_rng(rows * 10007 + cols)
+    x = _to(torch, _activations(rng, rows, cols), getattr(torch, dtype))
+    for g in ([1.0] if fmt == R.MX else [1.0, 0.01171875, 0.00873]):
+        t = fp4.quantize(x, fmt, g)
+        code, byte = R.quantize(_f32(x), fmt, g)
+        got_code, got_byte = R.unpack(t)
+        blocks = byte.shape[1]
+        np.testing.assert_array_equal(got_byte[:, :blocks], byte)
+        assert not got_byte[:, blocks:].any()
+        n = min(code.shape[1], got_code.shape[1])
+        # -0 and +0 stand for the same value
+        np.testing.assert_array_equal(R.e2m1_value(got_code[:, :n]), R.e2m1_value(code[:, :n]))
+        assert not got_code[:, cols:].any()
+        y = fp4.dequantize(t, x.dtype)
+        want = R.values(code, byte, fmt, cols, g)
+        bits = 8 if dtype == "bfloat16" else 23
+        np.testing.assert_allclose(y.double().cpu().numpy(), want, rtol=2.0 ** -bits, atol=0)
+
+
+@pytest.mark.parametrize("fmt", FMTS, ids=NAMES.get)
+def test_quantize_extremes(fmt):
+    """Infinities, NaNs, subnormals, the largest numbers: a NaN scale where a block is not
+    finite, the definition elsewhere."""
+    torch, fp4 = _fp4()
+    rng = np.random.default_rng(1)
+    x = rng.standard_normal((12, 96)).astype(np.float32)
+    x[0, 3], x[1, 40], x[2, 95] = np.inf, np.nan, -np.inf
+    x[3] *= np.float32(1e-38)
+    x[4] = np.float32(1e-45) * rng.integers(-9, 9, 96)
+    x[5] *= np.float32(3e37)
+    x[6] = 0
+    x[7] = np.where(rng.random(96) < 0.5, np.float32(3.3e38), np.float32(1.0))
+    x[8] = -x[7]
+    x[9] *= np.float32(1e-30)
+    x[10, 5], x[10, 6] = -np.nan, np.inf
+    for g in ([1.0] if fmt == R.MX else [1.0, 1e-30, 1e30, 3e-3]):
+        t = fp4.quantize(torch.from_numpy(x).cuda(), fmt, g)
+        code, byte = R.quantize(x, fmt, g)
+        got_code, got_byte = R.unpack(t)
+        np.testing.assert_array_equal(got_byte[:, : byte.shape[1]], byte)
+        np.testing.assert_array_equal(R.e2m1_value(got_code), R.e2m1_value(code))
+        y = fp4.dequantize(t, torch.float32).double().cpu().numpy()
+        want = R.values(code, byte, fmt, 96, g)
+        with np.errstate(over="ignore"):
+            want = want.astype(np.float32).astype(np.float64)
+        np.testing.assert_allclose(y, want, rtol=2.0 ** -23, atol=1e-45)
+
+
+@pytest.mark.parametrize("fmt", FMTS, ids=NAMES.get)
+def test_every_code_and_scale_dequantizes(fmt):
+    """All 16 codes under all scale bytes (but negative and NaN E4M3)."""
+    torch, fp4 = _fp4()
+    n_bytes = 255 if fmt == R.MX else 127
+    b = R.BLOCK[fmt]
+    code = np.tile(np.arange(16, dtype=np.uint8), (n_bytes, b // 16))
+    byte = np.arange(n_bytes, dtype=np.uint8)[:, None]
+    packed = R.pack_codes(code, b)
+    t = fp4.empty(n_bytes, b, fmt, "cuda", 1.0 if fmt == R.MX else 0.25)
+    t.codes.copy_(torch.from_numpy(packed).reshape(-1))
+    R.B.conv_fp4_pack_scales(fmt, n_bytes, b, torch.from_numpy(byte).cuda().data_ptr(),
+                             t.scales.data_ptr(), torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    y = fp4.dequantize(t, torch.float32).double().cpu().numpy()
+    with np.errstate(over="ignore"):
+        want = R.values(code, byte, fmt, b, t.tensor_scale).astype(np.float32)
+    np.testing.assert_array_equal(y, want.astype(np.float64))
+
+
+@pytest.mark.parametrize("fmt", FMTS, ids=NAMES.get)
+def test_quantize_strided_rows_and_offsets(fmt):
+    """Rows inside a wider matrix, at addresses that allow no vector loads."""
+    torch, fp4 = _fp4()
+    rng = np.random.default_rng(2)
+    wide = torch.from_numpy(_activations(rng, 37, 700)).cuda()
+    for dt in (torch.bfloat16, torch.float32):
+        w = wide.to(dt)
+        for off, cols in ((1, 96), (3, 333), (8, 512), (0, 700)):
+            x = w[:, off:off + cols]
+            t = fp4.quantize(x, fmt)
+            code, byte = R.quantize(_f32(x), fmt)
+            got_code, got_byte = R.unpack(t)
+            np.testing.assert_array_equal(got_byte[:, : byte.shape[1]], byte)
+            np.testing.assert_array_equal(R.e2m1_value(got_code[:, :cols]),
+                                          R.e2m1_value(code[:, :cols]))
+            out = torch.full((37, 720), 7.0, dtype=dt, device="cuda")
+            y = fp4.dequantize(t, out=out[:, 5:5 + cols])
+            assert torch.equal(y, fp4.dequantize(t, dt))
+            assert (out[:, :5] == 7).all() and (out[:, 5 + cols:] == 7).all()
+
+
+# ---- product -------------------------------------------------------------------
+
+
+def _product(fmt, M, C, K, x_dtype="bfloat16", y_dtype="bfloat16", act=0, bias=True, residual=False,
+             seed=0, strided=False):
+    torch, fp4 = _fp4()
+    rng = np.random.default_rng(seed + 7 * M + 131 * C + 1009 * K + fmt)
+    gx, gw, gy = (1.0, 1.0, 1.0) if fmt == R.MX else (0.0087, 0.0031 / np.sqrt(C), 0.0011)
+    gx, gw, gy = (float(np.float32(v)) for v in (gx, gw, gy))
+    xd = getattr(torch, x_dtype) if x_dtype else None
+    yd = getattr(torch, y_dtype) if y_dtype else None
+    x = _to(torch, _activations(rng, M, C), xd or torch.bfloat16)
+    w = _to(torch, rng.standard_normal((K, C)) / np.sqrt(C), torch.bfloat16)
+    b = _to(torch, 0.3 * rng.standard_normal(K), torch.float32) if bias else None
+    r = _to(torch, rng.standard_normal((M, K)), yd) if residual else None
+    out = None
+    if strided:  # rows inside wider matrices
+        x = torch.cat([x, x[:, :3]], 1)[:, :C]
+        big = torch.full((M, K + 13), 7.0, dtype=yd, device="cuda")
+        out = big[:, 5:5 + K]
+        if residual:
+            r = torch.cat([r, r[:, :1]], 1)[:, :K]
+    layer = fp4.Fp4Linear(C, K, fmt, xd, yd, act, residual, gx, gy)
+    layer.prepack(w, gw)
+    xin = fp4.quantize(x, fmt, gx) if xd is None else x
+    y = layer(xin, bias=b, residual=r, out=out)
+    _sync(torch)
+    xv = R.values(*R.quantize(_f32(x), fmt, gx), fmt, C, gx)
+    wv = R.values(*R.quantize(_f32(w), fmt, gw), fmt, C, gw)
+    pre = xv @ wv.T
+    extra = np.zeros_like(pre)
+    if bias:
+        bb = b.double().cpu().numpy()
+        pre, extra = pre + bb, extra + np.abs(bb)
+    if residual:
+        rr = r.double().cpu().numpy()
+        pre, extra = pre + rr, extra + np.abs(rr)
+    want = R.activate(pre, act)
+    if yd is None:
+        err = R.product_bound(xv, wv, want, extra, 24)
+        R.check_quantized(y, want, err, fmt, gy)
+        return y
+    err = R.product_bound(xv, wv, want, extra, 8 if y_dtype == "bfloat16" else 24)
+    got = y.double().cpu().numpy()
+    assert got.shape == want.shape
+    off = np.abs(got - want)
+    assert (off <= err).all(), (off / err).max()
+    if strided:
+        assert (big[:, :5] == 7).all() and (big[:, 5 + K:] == 7).all()
+    return y
+
+
+SHAPES = [(1, 1, 1), (1, 32, 8), (1, 4096, 512), (2, 16, 31), (3, 33, 40), (7, 1000, 300),
+          (8, 64, 32), (16, 2048, 1000), (17, 130, 129), (33, 256, 64), (64, 2048, 1000),
+          (65, 512, 100), (100, 96, 257), (128, 256, 128), (129, 272, 384), (200, 64, 640),
+          (255, 700, 255), (256, 1024, 256), (300, 1456, 1111), (515, 2080, 260), (777, 100, 520)]
+
+
+@pytest.mark.parametrize("fmt", FMTS, ids=NAMES.get)
+@pytest.mark.parametrize("M,C,K", SHAPES)
+def test_product(fmt, M, C, K):
+    _product(fmt, M, C, K)
+
+
+@pytest.mark.parametrize("fmt", FMTS, ids=NAMES.get)
+@pytest.mark.parametrize("M,C,K", [(1, 512, 256), (5, 100, 33), (64, 300, 1000), (300, 520, 400)])
+@pytest.mark.parametrize("x,y,act,bias,residual", [
+    ("float32", "float32", 0, False, False), ("bfloat16", "float32", 1, True, True),
+    ("float32", "bfloat16", 2, True, True), ("bfloat16", "bfloat16", 3, False, True),
+    (None, "float32", 4, True, False), (None, "bfloat16", 0, True, True),
+    ("bfloat16", None, 3, True, False), (None, None, 0, False, False)])
+def test_product_types_and_epilogues(fmt, M, C, K, x, y, act, bias, residual):
+    _product(fmt, M, C, K, x, y, act, bias, residual)
+
+
+@pytest.mark.parametrize("fmt", FMTS, ids=NAMES.get)
+@pytest.mark.parametrize("M,C,K", [(3, 90, 70), (64, 320, 96), (140, 259, 301)])
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+def test_product_strided_rows(fmt, M, C, K, dtype):
+    _product(fmt, M, C, K, dtype, dtype, 1, True, True, strided=True)
+
+
+@pytest.mark.parametrize("fmt", FMTS, ids=NAMES.get)
+@pytest.mark.parametrize("M,C,K", [(4, 256, 96), (150, 512, 300)])
+def test_product_infinities_stay_in_their_rows(fmt, M, C, K):
+    """A row of x that holds an Inf or a NaN gives a row of NaN; the other rows, and the
+    rows of zeros, are untouched.  The same for a row of the weights and its column."""
+    torch, fp4 = _fp4()
+    rng = np.random.default_rng(5)
+    x, w = rng.standard_normal((M, C)), rng.standard_normal((K, C))
+    x[1] = 0
+    clean = fp4.Fp4Linear(C, K, fmt)
+    clean.prepack(_to(torch, w, torch.bfloat16))
+    y0 = clean(_to(torch, x, torch.bfloat16))
+    x[2, C // 2], w[K - 1, 3] = np.inf, np.nan
+    layer = fp4.Fp4Linear(C, K, fmt)
+    layer.prepack(_to(torch, w, torch.bfloat16))
+    y = layer(_to(torch, x, torch.bfloat16))
+    _sync(torch)
+    assert torch.isnan(y[2]).all() and torch.isnan(y[:, K - 1]).all()
+    keep = [i for i in range(M) if i != 2]
+    assert torch.equal(y[keep][:, : K - 1], y0[keep][:, : K - 1])
+    assert (y0[1] == 0).all()
+
+
+@pytest.mark.parametrize("fmt", FMTS, ids=NAMES.get)
+def test_product_rows_do_not_depend_on_their_neighbours(fmt):
+    """A row's result is the same bits alone and in any batch that takes the same kernel, and
+    two runs give the same bits."""
+    torch, fp4 = _fp4()
+    rng = np.random.default_rng(6)
+    C, K = 1024, 520
+    x = _to(torch, _activations(rng, 600, C), torch.bfloat16)
+    layer = fp4.Fp4Linear(C, K, fmt, y_dtype=torch.float32)
+    layer.prepack(_to(torch, rng.standard_normal((K, C)), torch.bfloat16))
+    y = layer(x)
+    assert torch.equal(y, layer(x))
+    assert torch.equal(y[200:], layer(x[200:]))
+    small = layer(x[:9])
+    assert torch.equal(small, layer(x[:9]))
+    assert torch.equal(small[4:], layer(x[4:9]))
+
+
+@pytest.mark.parametrize("fmt", FMTS, ids=NAMES.get)
+@pytest.mark.parametrize("M", [2, 200])
+def test_product_into_its_residual(fmt, M):
+    torch, fp4 = _fp4()
+    rng = np.random.default_rng(8)
+    C, K = 192, 136
+    x, r = _to(torch, _activations(rng, M, C), torch.bfloat16), _to(
+        torch, rng.standard_normal((M, K)), torch.bfloat16)
+    layer = fp4.Fp4Linear(C, K, fmt, has_residual=True)
+    layer.prepack(_to(torch, rng.standard_normal((K, C)), torch.bfloat16))
+    want = layer(x, residual=r)
+    got = layer(x, residual=r, out=r)
+    assert torch.equal(want, got)
+
+
+def test_no_rows_and_other_streams():
+    """Zero rows launch nothing; a layer used on two streams at once keeps them apart; a
+    captured graph replays."""
+    torch, fp4 = _fp4()
+    B = R.B
+    rng = np.random.default_rng(9)
+    C, K = 256, 320
+    layer = fp4.Fp4Linear(C, K, R.NV, x_scale=0.01)
+    layer.prepack(_to(torch, rng.standard_normal((K, C)), torch.bfloat16), 0.001)
+    n = B.conv_launch_count()
+    assert layer(torch.empty(0, C, dtype=torch.bfloat16, device="cuda")).shape == (0, K)
+    t = fp4.quantize(torch.empty(0, C, device="cuda"), R.MX)
+    assert fp4.dequantize(t).shape == (0, C)
+    assert B.conv_launch_count() == n
+    xs = [_to(torch, _activations(rng, 150, C), torch.bfloat16) for _ in range(2)]
+    want = [layer(x) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    got = [[], []]
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            got[i].append(layer(xs[i], stream=s.cuda_stream))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(want[i], y) for y in got[i])
+    x = xs[0].clone()
+    y = torch.empty(150, K, dtype=torch.bfloat16, device="cuda")
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        layer(x, out=y)
+        side.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            layer(x, out=y)
+    x.copy_(xs[1])
+    torch.cuda.synchronize()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, want[1])
+
+
+def test_offsets_past_32_bits():
+    """Elements past 2^31 of x and y: the last rows of a tall matrix and of its product."""
+    torch, fp4 = _fp4()
+    M, C, K = 70000, 32768, 32
+    x = torch.zeros(M, C, dtype=torch.bfloat16, device="cuda")
+    rng = np.random.default_rng(10)
+    tail = _to(torch, _activations(rng, 5, C), torch.bfloat16)
+    x[-5:] = tail
+    layer = fp4.Fp4Linear(C, K, R.MX, y_dtype=torch.float32)
+    layer.prepack(_to(torch, rng.standard_normal((K, C)), torch.bfloat16))
+    y = layer(x)
+    xv = R.values(*R.quantize(_f32(tail), R.MX), R.MX, C)
+    wv = R.tensor_values(layer.w)
+    want = xv @ wv.T
+    err = R.product_bound(xv, wv, want, 0, 24)
+    assert (np.abs(y[-5:].double().cpu().numpy() - want) <= err).all()
+    assert not y[:-5].any()

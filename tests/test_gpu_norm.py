@@ -1,0 +1,221 @@
+"""The norms around a residual block against 64 bits, and the 4-bit residual block."""
+import numpy as np
+import pytest
+
+from tests import fp4_ref as R
+from tests.gpu_util import need_gpu
+
+pytestmark = pytest.mark.gpu
+B = R.B
+EPS = 1e-6
+
+
+def _norm():
+    torch = need_gpu()
+    from cnn_convolution_gemm_gb300.norm import ResidualNorm
+    return torch, ResidualNorm
+
+
+def _case(post, pre, rows, C, gate=0, gate_rows=1, dt="bfloat16", zdt=None, h_fmt=None, rs=0.5,
+          offset=0.0, weights=True, strided=False, with_z=True, in_place=False):
+    """Runs one case and compares it with 64 bits.  Tolerance: a row's sums are added in fp32
+    in at most C / 32 + 10 dependent steps (relative 2^-24 each, halved on average by nothing:
+    taken in full), the rest of a value is a dozen fp32 operations; layer norms subtract the
+    mean, so the error is relative to the largest magnitude before the subtraction."""
+    torch, ResidualNorm = _norm()
+    rng = np.random.default_rng(rows * 31 + C * 7 + post + 3 * pre + 11 * gate)
+    zdt = zdt or dt
+    xd, zd = getattr(torch, dt), getattr(torch, zdt)
+    up = lambda a, d: torch.from_numpy(np.ascontiguousarray(a)).to(d).cuda()  # noqa: E731
+    size = np.exp(0.5 * rng.standard_normal(C))
+    x = up(rng.standard_normal((rows, C)) * size * 4 + offset, xd)
+    z = up(rng.standard_normal((rows, C)) * size + offset, zd) if with_z else None
+    g = up(rng.standard_normal((-(-rows // gate_rows), C)), zd) if gate and with_z else None
+    if strided:
+        x = torch.cat([x, x[:, :1]], 1)[:, :C]
+        z = torch.cat([z, z[:, :1], z[:, :1]], 1)[:, :C]
+    vec = lambda s, o: up(o + s * rng.standard_normal(C), torch.float32)  # noqa: E731
+    p = {"w_post": vec(0.1, 1) if weights and post else None,
+         "b_post": vec(0.1, 0) if weights and post == B.CONV_NORM_LAYER else None,
+         "w_pre": vec(0.1, 1) if weights and pre else None,
+         "b_pre": vec(0.1, 0) if weights and pre == B.CONV_NORM_LAYER else None}
+    h_scale = 1.0 if h_fmt != R.NV else float(np.float32(0.0041))
+    layer = ResidualNorm(C, xd, zd, eps=EPS, post=post, pre=pre, gate=gate, gate_rows=gate_rows,
+                         residual_scale=rs, h_fmt=h_fmt, h_scale=h_scale, **p)
+    x64 = x.double().cpu().numpy()
+    x_out = x if in_place else None
+    if strided:
+        big = torch.full((rows, C + 9), 7.0, dtype=xd, device="cuda")
+        x_out = big[:, 4:4 + C]
+    xo, h = layer(x, z, gate=g, x_out=x_out)
+    B.conv_sync_status(torch.cuda.current_stream().cuda_stream)
+    n64 = {k: None if v is None else v.double().cpu().numpy() for k, v in p.items()}
+    steps = (C / 32 + 10 + 12) * 2.0 ** -24
+    want, bound = x64, 4 * 2.0 ** -24 * np.abs(x64)
+    if with_z:
+        z64 = z.double().cpu().numpy()
+        u = R.norm(z64, post, EPS, n64["w_post"], n64["b_post"])
+        gg = np.float64(rs)
+        if gate:
+            gv = g.double().cpu().numpy()
+            gv = 1 / (1 + np.exp(-gv)) if gate == B.CONV_GATE_SIGMOID else gv
+            gg = rs * gv[np.arange(rows) // gate_rows]
+        rstd = _rstd(z64, post)
+        amp = np.abs(z64) * rstd if post != B.CONV_NORM_LAYER else (
+            (np.abs(z64) + np.abs(z64).max(axis=1, keepdims=True)) * rstd)
+        w = 1 if n64["w_post"] is None else np.abs(n64["w_post"])
+        ub = steps * (amp * w + (0 if n64["b_post"] is None else np.abs(n64["b_post"])))
+        want = x64 + gg * u
+        bound = bound + np.abs(gg) * (ub + 8 * 2.0 ** -24 * np.abs(u)) + 4 * 2.0 ** -24 * np.abs(want)
+    ulp = {"bfloat16": 2.0 ** -8, "float32": 2.0 ** -24}
+    off = np.abs(xo.double().cpu().numpy() - want)
+    assert (off <= bound + ulp[dt] * np.abs(want) + 1e-37).all(), (off / (bound + ulp[dt] * np.abs(want))).max()
+    if strided:
+        assert (big[:, :4] == 7).all() and (big[:, 4 + C:] == 7).all()
+    if not pre:
+        assert h is None
+        return
+    wanth = R.norm(want, pre, EPS, n64["w_pre"], n64["b_pre"])
+    rstd = _rstd(want, pre)
+    amp = np.abs(want) + (np.abs(want).max(axis=1, keepdims=True) if pre == B.CONV_NORM_LAYER else 0)
+    w = 1 if n64["w_pre"] is None else np.abs(n64["w_pre"])
+    # the error of x' enters directly and through the row's statistics
+    through = bound + np.sqrt((bound ** 2).mean(axis=1, keepdims=True)) * (
+        1 + np.abs(want) * rstd * (2 if pre == B.CONV_NORM_LAYER else 1))
+    hb = (steps * amp + through) * rstd * w + steps * (0 if n64["b_pre"] is None else np.abs(n64["b_pre"]))
+    if h_fmt is not None:
+        R.check_quantized(h, wanth, hb, h_fmt, h_scale)
+        return
+    off = np.abs(h.double().cpu().numpy() - wanth)
+    assert (off <= hb + ulp[zdt] * np.abs(wanth) + 1e-37).all(), (off / (hb + ulp[zdt] * np.abs(wanth))).max()
+
+
+def _rstd(v, kind):
+    if kind == B.CONV_NORM_NONE:
+        return 1.0
+    m = v.mean(axis=1, keepdims=True) if kind == B.CONV_NORM_LAYER else 0.0
+    return 1 / np.sqrt(((v - m) ** 2).mean(axis=1, keepdims=True) + EPS)
+
+
+N, RMS, LN = B.CONV_NORM_NONE, B.CONV_NORM_RMS, B.CONV_NORM_LAYER
+
+
+@pytest.mark.parametrize("rows,C", [(1, 1), (1, 4096), (3, 7), (5, 32), (130, 64), (9, 100), (33, 257),
+                                    (17, 1000), (4, 1001), (300, 768), (7, 2048), (5, 4100), (3, 8192),
+                                    (2, 12345), (2, 16384), (2, 32768)])
+@pytest.mark.parametrize("dt", ["bfloat16", "float32"])
+def test_rms_both_sides(rows, C, dt):
+    _case(RMS, RMS, rows, C, dt=dt)
+
+
+@pytest.mark.parametrize("post,pre", [(N, RMS), (RMS, N), (N, LN), (LN, LN), (LN, RMS), (RMS, LN), (N, N)])
+@pytest.mark.parametrize("rows,C", [(5, 96), (33, 515), (6, 2304)])
+def test_norm_kinds(post, pre, rows, C):
+    _case(post, pre, rows, C)
+    _case(post, pre, rows, C, dt="float32", weights=False)
+
+
+@pytest.mark.parametrize("gate", [B.CONV_GATE_LINEAR, B.CONV_GATE_SIGMOID])
+@pytest.mark.parametrize("rows,C,gate_rows", [(6, 128, 1), (50, 200, 7), (49, 256, 49), (10, 96, 1000)])
+def test_gates(gate, rows, C, gate_rows):
+    _case(RMS, RMS, rows, C, gate, gate_rows)
+    _case(LN, LN, rows, C, gate, gate_rows, dt="float32", zdt="bfloat16")
+
+
+@pytest.mark.parametrize("h_fmt", [R.MX, R.NV])
+@pytest.mark.parametrize("rows,C", [(1, 2048), (3, 40), (130, 288), (7, 1000), (2, 4096), (140, 64)])
+def test_quantized_output(h_fmt, rows, C):
+    _case(RMS, RMS, rows, C, h_fmt=h_fmt)
+    _case(LN, LN, rows, C, dt="float32", zdt="bfloat16", h_fmt=h_fmt, gate=2)
+
+
+def test_mixed_types_strides_in_place_and_first_norm():
+    _case(RMS, LN, 20, 320, dt="float32", zdt="bfloat16")
+    _case(RMS, LN, 20, 320, dt="bfloat16", zdt="float32")
+    for C in (95, 256):
+        _case(RMS, RMS, 12, C, strided=True)
+        _case(LN, RMS, 12, C, strided=True, dt="float32")
+        _case(RMS, RMS, 40, C, in_place=True)
+        _case(N, RMS, 12, C, with_z=False)
+        _case(N, LN, 12, C, with_z=False, h_fmt=R.MX)
+
+
+def test_large_means_keep_their_digits():
+    """Layer norms of rows whose mean is a thousand times their deviation."""
+    _case(LN, LN, 9, 1024, dt="float32", offset=4000.0)
+    _case(LN, LN, 9, 300, dt="float32", offset=-4000.0)
+
+
+def test_zero_rows_and_rows_of_zeros():
+    torch, ResidualNorm = _norm()
+    layer = ResidualNorm(64, post=RMS, pre=RMS)
+    n = B.conv_launch_count()
+    x, h = layer(torch.empty(0, 64, dtype=torch.bfloat16, device="cuda"),
+                 torch.empty(0, 64, dtype=torch.bfloat16, device="cuda"))
+    assert x.shape == h.shape == (0, 64) and B.conv_launch_count() == n
+    z = torch.zeros(3, 64, dtype=torch.bfloat16, device="cuda")
+    x, h = layer(z, z)
+    assert not x.any() and not h.any()
+    # an infinity or a NaN stays in its row
+    z[1, 5] = float("inf")
+    x, h = layer(torch.ones_like(z), z)
+    assert torch.isnan(x[1, 5]) and torch.isnan(h[1]).all()
+    assert torch.isfinite(x[[0, 2]]).all() and torch.isfinite(h[[0, 2]]).all()
+
+
+def test_other_stream_and_determinism():
+    torch, ResidualNorm = _norm()
+    layer = ResidualNorm(1000, post=LN, pre=RMS)
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    x, z = (torch.randn(700, 1000, generator=gen, device="cuda").bfloat16() for _ in range(2))
+    want = layer(x, z)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for _ in range(5):
+        got = layer(x, z, stream=s.cuda_stream)
+        s.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("fmt", [R.MX, R.NV])
+@pytest.mark.parametrize("rows,C,hidden", [(1, 256, 512), (70, 96, 200), (300, 256, 640)])
+def test_residual_block(fmt, rows, C, hidden):
+    """Two chained blocks against 64 bits.  A 4-bit value within the fp32 error of a rounding
+    boundary may go either way, which moves a product by a few times 2^-5 of one term:
+    the comparison is over the norm of the difference."""
+    torch = need_gpu()
+    from cnn_convolution_gemm_gb300.residual_block import Fp4ResidualBlock
+    rng = np.random.default_rng(rows + C)
+    up = lambda a, d=torch.float32: torch.from_numpy(np.ascontiguousarray(a)).to(d).cuda()  # noqa: E731
+    g = 1.0 if fmt == R.MX else float(np.float32(0.0052))
+    gw = 1.0 if fmt == R.MX else float(np.float32(0.00037))
+    x = up(3 * rng.standard_normal((rows, C)), torch.bfloat16)
+    gate = up(rng.standard_normal((1, C)), torch.bfloat16)
+    norms = [1 + 0.1 * rng.standard_normal(C) for _ in range(5)]
+    nt = [up(n) for n in norms]
+    blocks, weights = [], []
+    for i in range(2):
+        w1, w2 = rng.standard_normal((hidden, C)) / np.sqrt(C), rng.standard_normal((C, hidden)) / np.sqrt(hidden)
+        b1, b2 = 0.1 * rng.standard_normal(hidden), 0.1 * rng.standard_normal(C)
+        blk = Fp4ResidualBlock(C, hidden, fmt, residual_scale=0.5, gate=B.CONV_GATE_LINEAR, gate_rows=rows,
+                               w_pre=nt[2 * i], w_post=nt[2 * i + 1], w_next=nt[2 * i + 2], b1=up(b1), b2=up(b2),
+                               h_scale=g, t_scale=g, chain=i == 0, next_scale=g)
+        blk.prepack(up(w1, torch.bfloat16), up(w2, torch.bfloat16), gw, gw)
+        blocks.append(blk)
+        weights.append((R.tensor_values(blk.fc1.w), R.tensor_values(blk.fc2.w),
+                        blk.b1.double().cpu().numpy(), blk.b2.double().cpu().numpy()))
+    xo, h = blocks[0](x, gate=gate)
+    assert h.rows == rows and h.fmt == fmt
+    xo, h = blocks[1](xo, gate=gate, h=h)
+    B.conv_sync_status(torch.cuda.current_stream().cuda_stream)
+    v = x.double().cpu().numpy()
+    n64 = [n.double().cpu().numpy() for n in nt]
+    q = lambda a: R.values(*R.quantize(a.astype(np.float32), fmt, g), fmt, a.shape[1], g)  # noqa: E731
+    for i, (w1, w2, b1, b2) in enumerate(weights):
+        t = R.activate(q(R.norm(v, RMS, EPS, n64[2 * i])) @ w1.T + b1, B.CONV_ACT_GELU)
+        zz = q(t) @ w2.T + b2
+        v = v + 0.5 * gate.double().cpu().numpy() * R.norm(zz, RMS, EPS, n64[2 * i + 1])
+        hh = R.norm(v, RMS, EPS, n64[2 * i + 2])
+    for got, want in ((xo, v), (h, hh)):
+        off = np.linalg.norm(got.double().cpu().numpy() - want) / np.linalg.norm(want)
+        assert off <= 0.01, off
