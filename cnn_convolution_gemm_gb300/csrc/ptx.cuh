@@ -390,4 +390,72 @@ __host__ __device__ constexpr uint32_t idesc_f16(int m, int n, int ab_type) {
          | ((uint32_t)(m >> 4) << 24);          // M / 16
 }
 
+// ---- block-scaled 4-bit MMAs ---------------------------------------------------
+
+// Instruction descriptor for kind::mxf4 / kind::mxf4nvf4: E2M1 operands, both
+// K-major, fp32 accumulate.  ue8m0: the scales' type (else UE4M3).  sf_id: which
+// byte of a scale word the MMA starts at (scale_vec::2X: 0 or 2; 4X: 0).
+__host__ __device__ constexpr uint32_t idesc_fp4(int m, int n, bool ue8m0, uint32_t sf_id) {
+  return (sf_id << 4)                           // scale id of B
+         | (1u << 7)                            // A format E2M1
+         | (1u << 10)                           // B format E2M1
+         | ((uint32_t)(n >> 3) << 17)           // N / 8
+         | ((ue8m0 ? 1u : 0u) << 23)            // scale format
+         | ((uint32_t)(m >> 4) << 24)           // M / 16
+         | (sf_id << 29);                       // scale id of A
+}
+
+// D[tmem] (+)= (A scaled) * (B scaled)^T over 64 elements of K.  MX: one scale per
+// 32 elements (two per MMA); else one per 16 (four).  PAIR: as tc_mma_f16_pair, the
+// scales of each CTA's TMEM: A's of its own rows, B's of all N rows.
+template <bool MX, bool PAIR>
+__device__ __forceinline__ void tc_mma_fp4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                           uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                           uint32_t accumulate) {
+#define GB_MMA_FP4(GROUP, KIND, VEC)                                                        \
+  asm volatile("{\n\t.reg .pred p;\n\t"                                                    \
+               "setp.ne.b32 p, %6, 0;\n\t"                                                  \
+               "tcgen05.mma.cta_group::" GROUP ".kind::" KIND ".block_scale.scale_vec::" VEC \
+               " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),                      \
+               "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)    \
+               : "memory")
+  if constexpr (MX && PAIR)
+    GB_MMA_FP4("2", "mxf4", "2X");
+  else if constexpr (MX)
+    GB_MMA_FP4("1", "mxf4", "2X");
+  else if constexpr (PAIR)
+    GB_MMA_FP4("2", "mxf4nvf4", "4X");
+  else
+    GB_MMA_FP4("1", "mxf4nvf4", "4X");
+#undef GB_MMA_FP4
+}
+
+// 32 rows of 16 bytes (512 consecutive bytes) from shared memory into 4 TMEM columns,
+// the same in each of the four 32-lane groups: a tile of block scales.  In order with
+// the MMAs that the same thread issues afterwards.  PAIR: in both CTAs, each from
+// its own shared memory.
+template <bool PAIR>
+__device__ __forceinline__ void tc_copy_scales(uint32_t taddr, uint64_t s_desc) {
+  if constexpr (PAIR)
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(s_desc)
+                 : "memory");
+  else
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(s_desc)
+                 : "memory");
+}
+
+// 32 lanes x 32 bit, 32 consecutive columns per thread.
+__device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+
 }  // namespace gb
