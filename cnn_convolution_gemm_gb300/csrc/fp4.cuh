@@ -63,12 +63,16 @@ __device__ __forceinline__ float from_e4m3(uint32_t b) {
   return (b & 0x80u) ? -a : a;
 }
 
-// The scale byte of a block from its largest magnitude, and the factor between an
-// element and its E2M1 value.
+// The scale byte of a block from its largest magnitude, and the quotients of its
+// elements.  NV divides by t = s * tensor_scale: with r = 1 / t rounded to nearest,
+// q0 = v r and the exact remainder v - q0 t (one fma) correct each other to the
+// rounded quotient (Markstein's correction), so that a quotient that lies on a
+// tie of E2M1 arrives there exactly; three operations an element where an IEEE
+// division takes about ten.
 template <int FMT>
 struct BlockScale {
   uint32_t byte;
-  float f;  // MX: what to multiply by (a power of two); NV: what to divide by
+  float t, r;  // MX: r alone, a power of two
 
   __device__ __forceinline__ BlockScale(float amax, float tensor_scale) {
     const uint32_t e = __float_as_uint(amax) >> 23;  // amax >= 0 (a NaN: its sign dropped)
@@ -76,18 +80,33 @@ struct BlockScale {
     if (FMT == CONV_FP4_MX) {
       // floor(log2 amax) = e - 127 for normal numbers; e <= 2 and subnormals: 2^-127
       byte = bad ? 255u : (e > 2u ? e - 2u : 0u);
-      f = bad ? 0.0f : __uint_as_float((254u - byte) << 23);  // 2^(127 - byte)
+      r = bad ? 0.0f : __uint_as_float((254u - byte) << 23);  // 2^(127 - byte)
+      t = r;
     } else {
       byte = bad ? 0x7Fu : to_e4m3(__fdiv_rn(amax, __fmul_rn(6.0f, tensor_scale)));
-      f = bad ? 0.0f : __fmul_rn(from_e4m3(byte), tensor_scale);
+      t = bad ? 0.0f : __fmul_rn(from_e4m3(byte), tensor_scale);
+      r = __frcp_rn(t);
     }
   }
   // codes of eight elements of the block
   __device__ __forceinline__ uint32_t codes(const float (&v)[8]) const {
     float q[8];
-    if (f == 0.0f) return 0u;
+    if (t == 0.0f) return 0u;
+    if (FMT == CONV_FP4_MX) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = FMT == CONV_FP4_MX ? v[i] * f : __fdiv_rn(v[i], f);
+      for (int i = 0; i < 8; ++i) q[i] = v[i] * r;
+    } else if (byte == 0x7Eu) {
+      // the largest scale: elements may lie far above 6 t, where the product with r
+      // could overflow
+#pragma unroll
+      for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(v[i], t);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float q0 = v[i] * r;
+        q[i] = __fmaf_rn(__fmaf_rn(-q0, t, v[i]), r, q0);
+      }
+    }
     return pack8_e2m1(q);
   }
 };
@@ -201,15 +220,35 @@ inline bool rows_vec(const void* p, long long ld) {
   return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (ld * (long long)sizeof(T)) % 16 == 0;
 }
 
-// The epilogue's activation.  GELU: x Phi(x); SiLU: x / (1 + exp(-x)) (exp overflows
-// to infinity for very negative x, the quotient is then -0).
-__device__ __forceinline__ float activate(float v, int act) {
-  switch (act) {
-    case CONV_ACT_RELU: return v < 0.0f ? 0.0f : v;  // keeps a NaN
-    case CONV_ACT_RELU6: return v < 0.0f ? 0.0f : (v > 6.0f ? 6.0f : v);
-    case CONV_ACT_GELU: return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
-    case CONV_ACT_SILU: return v / (1.0f + expf(-v));
-    default: return v;
+// GELU, x Phi(x).  Phi(-|x|) = 1/2 (a1 u + .. + a5 u^5) exp(-x^2 / 2) with
+// u = 1 / (1 + p |x| / sqrt 2): Abramowitz and Stegun 7.1.26, within 0.75e-7 of Phi
+// (the product's own rounding is larger), one reciprocal and one exponential.
+__device__ __forceinline__ float gelu(float x) {
+  const float u = __fdividef(1.0f, fmaf(0.3275911f * 0.70710678f, fabsf(x), 1.0f));
+  float q = fmaf(1.061405429f, u, -1.453152027f);
+  q = fmaf(q, u, 1.421413741f);
+  q = fmaf(q, u, -0.284496736f);
+  q = fmaf(q, u, 0.254829592f);
+  q = 0.5f * q * u * __expf(-0.5f * x * x);
+  return x * (x < 0.0f ? q : 1.0f - q);
+}
+
+// The epilogue's activation over N values.  SiLU: x / (1 + exp(-x)) (exp overflows to
+// infinity for very negative x, the quotient is then -0).  Comparisons keep a NaN.
+template <int N>
+__device__ __forceinline__ void activate(float (&v)[N], int act) {
+  if (act == CONV_ACT_RELU) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = v[i] < 0.0f ? 0.0f : v[i];
+  } else if (act == CONV_ACT_RELU6) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = v[i] < 0.0f ? 0.0f : (v[i] > 6.0f ? 6.0f : v[i]);
+  } else if (act == CONV_ACT_GELU) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = gelu(v[i]);
+  } else if (act == CONV_ACT_SILU) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = __fdividef(v[i], 1.0f + __expf(-v[i]));
   }
 }
 

@@ -2,13 +2,14 @@
 // on the block-scaled tcgen05 MMAs.
 //
 // GEMM names here: M rows of X, N rows of W (the layer's outputs), KR the reduction.
-// Persistent CTAs of 192 threads: warp 0 loads (TMA), one thread of warp 1 copies the
-// block scales to TMEM and issues the MMAs, warps 2..5 run the epilogue.  A k-step is
+// Persistent CTAs of three warpgroups: warp 0 loads (TMA), one thread of warp 1 copies
+// the block scales to TMEM and issues the MMAs, warps 4..11 run the epilogue.  A k-step is
 // 256 elements: 128-byte rows of codes (128-byte swizzle) and 512-byte scale tiles.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "fp4.cuh"
 #include "internal.h"
@@ -19,6 +20,7 @@ using namespace gb::fp4;
 
 constexpr int BM = 128;
 constexpr int BKB = 128;  // bytes of a row per k-step: 256 codes
+constexpr int THREADS = 384;
 
 template <int FMT, int BN, bool PAIR>
 struct Cfg {
@@ -35,7 +37,8 @@ struct Cfg {
   // scale columns of a stage, in a slot of its own per stage: a slot is written again
   // only after the MMAs that read it have committed the stage
   static constexpr int SF_COLS = ATOMS * 4 * (1 + PB);
-  static constexpr int EPI_BYTES = 4 * 32 * 33 * 4;
+  static constexpr int EPI_WARP = 4096 + 128;  // a warp's staging buffer and 32 biases
+  static constexpr int EPI_BYTES = 8 * EPI_WARP;
   static constexpr int SMEM = STAGES * STAGE_BYTES + EPI_BYTES + 256 + 1024;
   static_assert(NACC * BN + STAGES * SF_COLS <= 512, "TMEM");
   static_assert(SMEM <= 232448, "shared memory");
@@ -44,7 +47,7 @@ struct Cfg {
 struct GemmParams {
   int M, N, ksteps, kmmas_last;  // 64-element MMAs of the last k-step
   int m_tiles, n_tiles;          // PAIR: m_tiles counts 256-row units
-  int act, y_io, fmt;
+  int act, vec_y, vec_r;  // 16-byte accesses to rows of y / of the residual
   float alpha, y_scale;
   const float* bias;
   const void* res;
@@ -55,42 +58,129 @@ struct GemmParams {
   unsigned long long wait_ns;
 };
 
-// Epilogue of a 32 x 32 block whose accumulators lie in the warp's staging buffer
-// (row r, column c at stage[33 r + c]): a lane owns a column, rows go one by one, so
-// that every access to the residual and the output is one segment per row.
+// ---- epilogue of a 32 x 32 block: a lane holds a row's 32 fp32 accumulators --------
+//
+// Rows of the output (and of the residual) pass through a staging buffer of the warp,
+// so that global accesses are whole row segments: 32 rows of 32 elements, their
+// 16-byte pieces swizzled (a quarter-warp's accesses hit all banks once, by row and
+// by piece alike).
+
 template <typename T>
-__device__ __forceinline__ void epilogue_float(const GemmParams& p, const float* stage, int m0,
-                                               int n0) {
+struct Block {
+  static constexpr int ES = sizeof(T);
+  static constexpr int PIECES = 32 * ES / 16;  // 16-byte pieces of a row
+  static constexpr int RPI = 32 / PIECES;      // rows of one warp-wide access
+
+  static __device__ __forceinline__ uint8_t* at(uint8_t* buf, int row, int piece) {
+    if constexpr (ES == 2)
+      return buf + row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
+    else
+      return buf + row * 128 + ((piece ^ (row & 7)) << 4);
+  }
+  static __device__ __forceinline__ T* elem(uint8_t* buf, int row, int col) {
+    return reinterpret_cast<T*>(at(buf, row, col * ES / 16) + col * ES % 16);
+  }
+  // 16-byte pieces of a 32 x 32 block of global memory into registers; rows < rows
+  static __device__ __forceinline__ void fetch(uint4 (&r)[PIECES], const T* g, long long ld,
+                                               int rows) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+      const int row = i * RPI + lane / PIECES;
+      r[i] = make_uint4(0, 0, 0, 0);
+      if (row < rows)
+        r[i] = *reinterpret_cast<const uint4*>(g + row * ld + lane % PIECES * (16 / ES));
+    }
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ void unpack(float (&v)[32], const uint8_t* buf) {
+  using B = Block<T>;
   const int lane = threadIdx.x & 31;
-  const int n = n0 + lane;
-  const bool live = n < p.N;
-  const float b = p.bias && live ? p.bias[n] : 0.0f;
-  const int rows = min(32, p.M - m0);
-  const T* res = static_cast<const T*>(p.res);
-  for (int r = 0; r < rows; ++r) {
-    float v = stage[33 * r + lane] * p.alpha + b;
-    if (!live) continue;
-    if (res) v += load_f32(res + (long long)(m0 + r) * p.ldr + n);
-    store_f32(static_cast<T*>(p.y) + (long long)(m0 + r) * p.ldy + n, activate(v, p.act));
+#pragma unroll
+  for (int i = 0; i < B::PIECES; ++i) {
+    const uint4 u = *reinterpret_cast<const uint4*>(B::at(const_cast<uint8_t*>(buf), lane, i));
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if constexpr (B::ES == 2) {
+        v[i * 8 + 2 * k] += __uint_as_float(w[k] << 16);
+        v[i * 8 + 2 * k + 1] += __uint_as_float(w[k] & 0xFFFF0000u);
+      } else {
+        v[i * 4 + k] += __uint_as_float(w[k]);
+      }
+    }
   }
 }
 
-// The same block as 4-bit codes: a lane owns a row, whose 32 columns are one MX block
-// or two NV blocks.
-template <int FMT>
-__device__ __forceinline__ void epilogue_codes(const GemmParams& p, const float* stage, int m0,
-                                               int n0) {
+// v (acc * alpha + bias) of rows m0.. and columns n0..: residual, activation, store.
+// pre: the residual's pieces, fetched ahead (vec_r and a whole block of columns).
+template <typename T>
+__device__ __forceinline__ void finish_float(const GemmParams& p, float (&v)[32], uint8_t* buf,
+                                             int m0, int n0, uint4 (&pre)[Block<T>::PIECES]) {
+  using B = Block<T>;
   const int lane = threadIdx.x & 31;
-  const long long m = m0 + lane;
-  const long long pitch = code_pitch(p.N);
-  const int tiles = tiles_per_row(FMT, p.N);
-  if (m >= p.M || n0 >= p.N) return;
-  float v[32];
+  const int rows = min(32, p.M - m0), cols = min(32, p.N - n0);
+  if (p.res) {
+    if (p.vec_r && cols == 32) {
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    const int n = n0 + i;
-    const float b = p.bias && n < p.N ? p.bias[n] : 0.0f;
-    v[i] = n < p.N ? activate(stage[33 * lane + i] * p.alpha + b, p.act) : 0.0f;
+      for (int i = 0; i < B::PIECES; ++i)
+        *reinterpret_cast<uint4*>(B::at(buf, i * B::RPI + lane / B::PIECES, lane % B::PIECES)) =
+            pre[i];
+    } else if (lane < cols) {
+      const T* g = static_cast<const T*>(p.res) + (long long)m0 * p.ldr + n0 + lane;
+#pragma unroll 4
+      for (int r = 0; r < rows; ++r) *B::elem(buf, r, lane) = g[r * p.ldr];
+    }
+    __syncwarp();
+    unpack<T>(v, buf);
+    __syncwarp();
+  }
+  activate(v, p.act);
+#pragma unroll
+  for (int i = 0; i < B::PIECES; ++i) {
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if constexpr (B::ES == 2) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[i * 8 + 2 * k], v[i * 8 + 2 * k + 1]);
+        w[k] = *reinterpret_cast<const uint32_t*>(&h);
+      } else {
+        w[k] = __float_as_uint(v[i * 4 + k]);
+      }
+    }
+    *reinterpret_cast<uint4*>(B::at(buf, lane, i)) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __syncwarp();
+  T* y = static_cast<T*>(p.y) + (long long)m0 * p.ldy + n0;
+  if (p.vec_y && cols == 32) {
+#pragma unroll
+    for (int i = 0; i < B::PIECES; ++i) {
+      const int row = i * B::RPI + lane / B::PIECES;
+      if (row < rows)
+        *reinterpret_cast<uint4*>(y + row * p.ldy + lane % B::PIECES * (16 / B::ES)) =
+            *reinterpret_cast<const uint4*>(B::at(buf, row, lane % B::PIECES));
+    }
+  } else if (lane < cols) {
+#pragma unroll 4
+    for (int r = 0; r < rows; ++r) y[r * p.ldy + lane] = *B::elem(buf, r, lane);
+  }
+  __syncwarp();
+}
+
+// The same block as 4-bit codes: a row's 32 columns are one MX block or two NV blocks,
+// and lie in one lane.
+template <int FMT>
+__device__ __forceinline__ void finish_codes(const GemmParams& p, float (&v)[32], int m0, int n0) {
+  const long long m = m0 + (threadIdx.x & 31);
+  const int cols = min(32, p.N - n0);
+  activate(v, p.act);
+  if (m >= p.M) return;
+  if (cols < 32) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (i >= cols) v[i] = 0.0f;
   }
   constexpr int B = kBlock<FMT>;
   uint32_t bytes = 0, code[4];
@@ -109,6 +199,8 @@ __device__ __forceinline__ void epilogue_codes(const GemmParams& p, const float*
       code[k * (B / 8) + i] = s.codes(e);
     }
   }
+  const long long pitch = code_pitch(p.N);
+  const int tiles = tiles_per_row(FMT, p.N);
   *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.y) + m * pitch + n0 / 2) =
       make_uint4(code[0], code[1], code[2], code[3]);
   const int b0 = n0 / B;
@@ -123,8 +215,8 @@ __device__ __forceinline__ void epilogue_codes(const GemmParams& p, const float*
       p.ys[scale_word_offset(m, b >> 2, tiles) + (b & 3)] = 0;
 }
 
-template <int FMT, int BN, bool PAIR>
-__global__ void __launch_bounds__(192, 1)
+template <int FMT, int BN, bool PAIR, int YIO>
+__global__ void __launch_bounds__(THREADS, 1)
     fp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_xs,
                     const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_ws,
                     const GemmParams p) {
@@ -137,8 +229,8 @@ __global__ void __launch_bounds__(192, 1)
   uint8_t* sB = sA + C::STAGES * C::A_BYTES;
   uint8_t* sFA = sB + C::STAGES * C::B_BYTES;
   uint8_t* sFB = sFA + C::STAGES * C::SFA_BYTES;
-  float* sEpi = reinterpret_cast<float*>(sFB + C::STAGES * C::SFB_BYTES);
-  uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(sEpi) + C::EPI_BYTES);
+  uint8_t* sEpi = sFB + C::STAGES * C::SFB_BYTES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sEpi + C::EPI_BYTES);
   uint64_t* empty = full + C::STAGES;
   uint64_t* tfull = empty + C::STAGES;
   uint64_t* tempty = tfull + C::NACC;
@@ -158,7 +250,7 @@ __global__ void __launch_bounds__(192, 1)
     }
     for (int b = 0; b < C::NACC; ++b) {
       gb::mbar_init(&tfull[b], 1);
-      gb::mbar_init(&tempty[b], PAIR ? 8 : 4);  // one arrival per epilogue warp
+      gb::mbar_init(&tempty[b], PAIR ? 16 : 8);  // one arrival per epilogue warp
     }
     gb::mbar_init(mma_done, 1);
     gb::fence_barrier_init();
@@ -184,7 +276,10 @@ __global__ void __launch_bounds__(192, 1)
   gb::allow_dependents();
 
   const int units = p.m_tiles * p.n_tiles;
-
+  // The registers of the launch, 384 x 168, as 128 x 40 + 256 x 232: the epilogue holds
+  // half a row of the tile.
+  if (warp < 4) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
   if (warp == 0) {
     if (lane == 0) {
       // ---------------- TMA producer ----------------
@@ -309,38 +404,37 @@ __global__ void __launch_bounds__(192, 1)
         gb::tc_commit(mma_done);
       gb::mbar_wait_bounded(mma_done, 0, p.wait_ns, p.err);
     }
+  }
   } else {
-    // ---------------- epilogue (warps 2..5) ----------------
-    const int q = warp & 3;  // TMEM lane quarter this warp may access
-    float* stage = sEpi + q * 32 * 33;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+    // ---------------- epilogue (warps 4..11) ----------------
+    // A warp owns 32 rows (the TMEM lane quarter it may access) and half the tile's
+    // columns.  It takes all its accumulators into registers and frees the TMEM
+    // accumulator before it works on them: the next tile's MMAs wait for TMEM reads only.
+    using T = std::conditional_t<YIO == CONV_FP4_IO_BF16, __nv_bfloat16, float>;
+    constexpr int COLS = BN / 2, NCH = COLS / 32;
+    constexpr bool FLOAT = YIO != CONV_FP4_IO_CODES;
+    const int q = warp & 3, half = (warp - 4) >> 2;
+    uint8_t* const buf = sEpi + (warp - 4) * C::EPI_WARP;
+    float* const sbias = reinterpret_cast<float*>(buf + 4096);
     const uint32_t tempty_pair = PAIR ? gb::mapa_shared(gb::smem_u32(tempty), 0) : 0u;
     int acc = 0;
     uint32_t acc_phase = 0;
+    uint4 pre[Block<T>::PIECES] = {};
     asm volatile("griddepcontrol.wait;" ::: "memory");
     for (int u = unit0; u < units; u += ustep) {
       const int mt = (u / p.n_tiles) * (PAIR ? 2 : 1) + (int)rank, nt = u % p.n_tiles;
-      const int m0 = mt * BM + q * 32, n0 = nt * BN;
+      const int m0 = mt * BM + q * 32, nb = nt * BN + half * COLS;
+      const bool ahead = FLOAT && p.res && p.vec_r;
+      const T* res = static_cast<const T*>(p.res) + (long long)m0 * p.ldr + nb;
+      if (ahead && nb + 32 <= p.N) Block<T>::fetch(pre, res, p.ldr, p.M - m0);
       if (!gb::mbar_wait_bounded(&tfull[acc], acc_phase, p.wait_ns, p.err)) break;
       gb::tc_fence_after();
-      const uint32_t t = tmem + ((uint32_t)(q * 32) << 16) + acc * BN;
-#pragma unroll 1
-      for (int c = 0; c < BN; c += 32) {
-        uint32_t r[32];
-        gb::tmem_ld_x32(t + c, r);
-        gb::tmem_ld_wait();
-        __syncwarp();
+      const uint32_t t = tmem + ((uint32_t)(q * 32) << 16) + acc * BN + half * COLS;
+      uint32_t r[NCH][32];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) stage[33 * lane + i] = __uint_as_float(r[i]);
-        __syncwarp();
-        if (m0 < p.M && n0 + c < p.N) {
-          if (p.y_io == CONV_FP4_IO_BF16)
-            epilogue_float<__nv_bfloat16>(p, stage, m0, n0 + c);
-          else if (p.y_io == CONV_FP4_IO_F32)
-            epilogue_float<float>(p, stage, m0, n0 + c);
-          else
-            epilogue_codes<FMT>(p, stage, m0, n0 + c);
-        }
-      }
+      for (int c = 0; c < NCH; ++c) gb::tmem_ld_x32(t + 32 * c, r[c]);
+      gb::tmem_ld_wait();
       gb::tc_fence_before();
       __syncwarp();
       if (lane == 0) {
@@ -348,6 +442,42 @@ __global__ void __launch_bounds__(192, 1)
           gb::mbar_arrive_cluster(tempty_pair + acc * 8);
         else
           gb::mbar_arrive(&tempty[acc]);
+      }
+      if (m0 < p.M) {
+#pragma unroll 1
+        for (int c = 0; c < NCH; ++c) {
+          const int n0 = nb + 32 * c;
+          if (n0 >= p.N) break;
+          float v[32];
+          if (p.bias) {
+            sbias[lane] = n0 + lane < p.N ? p.bias[n0 + lane] : 0.0f;
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float4 b = reinterpret_cast<const float4*>(sbias)[i];
+              v[4 * i] = fmaf(__uint_as_float(r[0][4 * i]), p.alpha, b.x);
+              v[4 * i + 1] = fmaf(__uint_as_float(r[0][4 * i + 1]), p.alpha, b.y);
+              v[4 * i + 2] = fmaf(__uint_as_float(r[0][4 * i + 2]), p.alpha, b.z);
+              v[4 * i + 3] = fmaf(__uint_as_float(r[0][4 * i + 3]), p.alpha, b.w);
+            }
+            __syncwarp();
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[0][i]) * p.alpha;
+          }
+          // the next block of columns moves to the front: registers are not indexed
+#pragma unroll
+          for (int k = 0; k + 1 < NCH; ++k)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) r[k][i] = r[k + 1][i];
+          if constexpr (FLOAT) {
+            finish_float<T>(p, v, buf, m0, n0, pre);
+            if (ahead && c + 1 < NCH && n0 + 64 <= p.N)
+              Block<T>::fetch(pre, res + 32 * (c + 1), p.ldr, p.M - m0);
+          } else {
+            finish_codes<FMT>(p, v, m0, n0);
+          }
+        }
       }
       if (++acc == C::NACC) {
         acc = 0;
@@ -388,7 +518,7 @@ bool scales_map(CUtensorMap* map, const uint8_t* p, int fmt, int rows, int cols,
                          strides, box, estr, CU_TENSOR_MAP_SWIZZLE_NONE) == CUDA_SUCCESS;
 }
 
-template <int FMT, int BN, bool PAIR>
+template <int FMT, int BN, bool PAIR, int YIO>
 cudaError_t launch_tile(const Fp4Gemm& g, cudaStream_t st) {
   using C = Cfg<FMT, BN, PAIR>;
   CUtensorMap tx, txs, tw, tws;
@@ -404,7 +534,6 @@ cudaError_t launch_tile(const Fp4Gemm& g, cudaStream_t st) {
   p.m_tiles = (int)gb_ceil_div_ll(g.M, PAIR ? 2 * BM : BM);
   p.n_tiles = gb_ceil_div(g.K, BN);
   p.act = g.act;
-  p.y_io = g.y_io;
   p.alpha = g.alpha;
   p.y_scale = g.y_scale;
   p.bias = g.bias;
@@ -413,18 +542,31 @@ cudaError_t launch_tile(const Fp4Gemm& g, cudaStream_t st) {
   p.ys = g.ys;
   p.ldr = g.ldr;
   p.ldy = g.ldy;
+  if (YIO == CONV_FP4_IO_BF16) {
+    p.vec_y = rows_vec<__nv_bfloat16>(g.y, g.ldy);
+    p.vec_r = rows_vec<__nv_bfloat16>(g.res, g.ldr);
+  } else {
+    p.vec_y = rows_vec<float>(g.y, g.ldy);
+    p.vec_r = rows_vec<float>(g.res, g.ldr);
+  }
   p.err = gb_device_error_word();
   p.wait_ns = gb_wait_limit_ns();
-  auto* kern = fp4_gemm_kernel<FMT, BN, PAIR>;
+  auto* kern = fp4_gemm_kernel<FMT, BN, PAIR, YIO>;
   cudaError_t e = gb_set_smem_once(reinterpret_cast<const void*>(kern), C::SMEM);
   if (e != cudaSuccess) return e;
+  // the kernel's register split waits forever if it was launched with fewer
+  static const int regs = [&] {
+    cudaFuncAttributes fa = {};
+    return cudaFuncGetAttributes(&fa, kern) == cudaSuccess ? fa.numRegs : 0;
+  }();
+  if (regs * THREADS < 128 * 40 + 256 * 232) return cudaErrorLaunchOutOfResources;
   const long long units = (long long)p.m_tiles * p.n_tiles;
   if (units >= (1LL << 31)) return cudaErrorInvalidValue;
   const int slots = PAIR ? gb_num_sms() / 2 : gb_num_sms();
   const int grid = (int)std::min<long long>(units, slots) * (PAIR ? 2 : 1);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(192);
+  cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
@@ -441,10 +583,17 @@ cudaError_t launch_tile(const Fp4Gemm& g, cudaStream_t st) {
   return e;
 }
 
+template <int FMT, int YIO>
+cudaError_t launch_y(const Fp4Gemm& g, cudaStream_t st) {
+  if (g.M > 128 && g.K > 128) return launch_tile<FMT, 256, true, YIO>(g, st);
+  return launch_tile<FMT, 128, false, YIO>(g, st);
+}
+
 template <int FMT>
 cudaError_t launch_fmt(const Fp4Gemm& g, cudaStream_t st) {
-  if (g.M > 128 && g.K > 128) return launch_tile<FMT, 256, true>(g, st);
-  return launch_tile<FMT, 128, false>(g, st);
+  if (g.y_io == CONV_FP4_IO_BF16) return launch_y<FMT, CONV_FP4_IO_BF16>(g, st);
+  if (g.y_io == CONV_FP4_IO_F32) return launch_y<FMT, CONV_FP4_IO_F32>(g, st);
+  return launch_y<FMT, CONV_FP4_IO_CODES>(g, st);
 }
 
 }  // namespace
