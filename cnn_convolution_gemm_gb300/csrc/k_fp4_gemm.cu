@@ -2,8 +2,8 @@
 // on the block-scaled tcgen05 MMAs.
 //
 // GEMM names here: M rows of X, N rows of W (the layer's outputs), KR the reduction.
-// Persistent CTAs of three warpgroups: warp 0 loads (TMA), one thread of warp 1 copies
-// the block scales to TMEM and issues the MMAs, warps 4..11 run the epilogue.  A k-step is
+// Persistent CTAs of three warpgroups: warp 0 loads (TMA), warp 1 copies the block
+// scales to TMEM and issues the MMAs (one elected lane), warps 4..11 run the epilogue.  A k-step is
 // 256 elements: 128-byte rows of codes (128-byte swizzle) and 512-byte scale tiles.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t* mma_done = tempty + C::NACC;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
 
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0);  // uniform
   const int lane = threadIdx.x & 31;
   const uint32_t rank = PAIR ? gb::cluster_ctarank() : 0u;
   const int unit0 = PAIR ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   __syncthreads();
   if constexpr (PAIR) gb::cluster_sync();
   gb::tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
   gb::allow_dependents();
 
   const int units = p.m_tiles * p.n_tiles;
@@ -281,22 +281,23 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (warp < 4) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
   if (warp == 0) {
-    if (lane == 0) {
-      // ---------------- TMA producer ----------------
-      int stage = 0;
-      uint32_t phase = 0;
-      long long issued = 0;
-      bool ok = true;
-      const uint32_t full_pair = PAIR ? gb::mapa_shared(gb::smem_u32(full), 0) : 0u;
-      asm volatile("griddepcontrol.wait;" ::: "memory");
-      for (int u = unit0; u < units && ok; u += ustep) {
-        const int mt = (u / p.n_tiles) * (PAIR ? 2 : 1) + (int)rank, nt = u % p.n_tiles;
-        const int brow = nt * BN + (PAIR ? (int)rank * C::BROWS : 0);
-        for (int it = 0; it < p.ksteps; ++it) {
-          if (!gb::mbar_wait_bounded(&empty[stage], phase ^ 1, p.wait_ns, p.err)) {
-            ok = false;
-            break;
-          }
+    // ---------------- TMA producer ----------------
+    const bool one = gb::elect_one();
+    int stage = 0;
+    uint32_t phase = 0;
+    long long issued = 0;
+    bool ok = true;
+    const uint32_t full_pair = PAIR ? gb::mapa_shared(gb::smem_u32(full), 0) : 0u;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (int u = unit0; u < units && ok; u += ustep) {
+      const int mt = (u / p.n_tiles) * (PAIR ? 2 : 1) + (int)rank, nt = u % p.n_tiles;
+      const int brow = nt * BN + (PAIR ? (int)rank * C::BROWS : 0);
+      for (int it = 0; it < p.ksteps; ++it) {
+        if (!gb::mbar_wait_bounded_warp<PAIR>(&empty[stage], phase ^ 1, p.wait_ns, p.err)) {
+          ok = false;
+          break;
+        }
+        if (one) {
           uint8_t* const a = sA + stage * C::A_BYTES;
           uint8_t* const b = sB + stage * C::B_BYTES;
           uint8_t* const fa = sFA + stage * C::SFA_BYTES;
@@ -316,48 +317,50 @@ __global__ void __launch_bounds__(THREADS, 1)
             gb::tma_load_2d(fa, &tm_xs, &full[stage], sc, mt);
             gb::tma_load_2d(fb, &tm_ws, &full[stage], sc, nt * BN / 128);
           }
-          ++issued;
-          if (++stage == C::STAGES) {
-            stage = 0;
-            phase ^= 1;
-          }
         }
-      }
-      // no copy into shared memory may be in flight at exit (pair: the even CTA's
-      // barriers count both CTAs' bytes, so it drains for both)
-      long long pending = issued < C::STAGES ? issued : C::STAGES;
-      if (PAIR && rank != 0) pending = 0;
-      for (long long i = 0; i < pending; ++i) {
-        if (--stage < 0) {
-          stage = C::STAGES - 1;
+        __syncwarp();
+        ++issued;
+        if (++stage == C::STAGES) {
+          stage = 0;
           phase ^= 1;
         }
-        gb::mbar_wait_bounded(&full[stage], phase, p.wait_ns, p.err);
       }
     }
-  } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
-      // ---------------- scale copies and MMAs ----------------
-      constexpr int MM = PAIR ? 2 * BM : BM;
-      int stage = 0, acc = 0;
-      uint32_t phase = 0, acc_phase = 0;
-      bool ok = true;
-      for (int u = unit0; u < units && ok; u += ustep) {
-        if (!gb::mbar_wait_bounded(&tempty[acc], acc_phase ^ 1, p.wait_ns, p.err)) break;
+    // no copy into shared memory may be in flight at exit (pair: the even CTA's
+    // barriers count both CTAs' bytes, so it drains for both)
+    long long pending = issued < C::STAGES ? issued : C::STAGES;
+    if (PAIR && rank != 0) pending = 0;
+    for (long long i = 0; i < pending; ++i) {
+      if (--stage < 0) {
+        stage = C::STAGES - 1;
+        phase ^= 1;
+      }
+      gb::mbar_wait_bounded_warp<PAIR>(&full[stage], phase, p.wait_ns, p.err);
+    }
+  } else if (warp == 1 && rank == 0) {
+    // ---------------- scale copies and MMAs ----------------
+    const bool one = gb::elect_one();
+    constexpr int MM = PAIR ? 2 * BM : BM;
+    int stage = 0, acc = 0;
+    uint32_t phase = 0, acc_phase = 0;
+    bool ok = true;
+    for (int u = unit0; u < units && ok; u += ustep) {
+      if (!gb::mbar_wait_bounded_warp<PAIR>(&tempty[acc], acc_phase ^ 1, p.wait_ns, p.err)) break;
+      gb::tc_fence_after();
+      const uint32_t d = tmem + acc * BN;
+      for (int it = 0; it < p.ksteps; ++it) {
+        if (!gb::mbar_wait_bounded_warp<PAIR>(&full[stage], phase, p.wait_ns, p.err)) {
+          ok = false;
+          break;
+        }
         gb::tc_fence_after();
-        const uint32_t d = tmem + acc * BN;
-        for (int it = 0; it < p.ksteps; ++it) {
+        if (one) {
           const uint64_t ad = gb::sw128_kmajor_desc(gb::smem_u32(sA + stage * C::A_BYTES));
           const uint64_t bd = gb::sw128_kmajor_desc(gb::smem_u32(sB + stage * C::B_BYTES));
           const uint32_t fa = gb::smem_u32(sFA + stage * C::SFA_BYTES);
           const uint32_t fb = gb::smem_u32(sFB + stage * C::SFB_BYTES);
           const uint32_t sfa = tmem + C::NACC * BN + stage * C::SF_COLS;
           const uint32_t sfb = sfa + C::ATOMS * 4;
-          if (!gb::mbar_wait_bounded(&full[stage], phase, p.wait_ns, p.err)) {
-            ok = false;
-            break;
-          }
-          gb::tc_fence_after();
           // scale tiles (32 rows x 16 bytes): A's tile j at columns 4 j, B's panel q of
           // tile j at 4 (j PB + q), so that an MMA's B scales are consecutive
 #pragma unroll
@@ -383,27 +386,34 @@ __global__ void __launch_bounds__(THREADS, 1)
             gb::tc_commit_pair_multicast(&empty[stage], 0x3);
           else
             gb::tc_commit(&empty[stage]);
-          if (++stage == C::STAGES) {
-            stage = 0;
-            phase ^= 1;
-          }
         }
-        if (!ok) break;
+        __syncwarp();
+        if (++stage == C::STAGES) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+      if (!ok) break;
+      if (one) {
         if constexpr (PAIR)
           gb::tc_commit_pair_multicast(&tfull[acc], 0x3);
         else
           gb::tc_commit(&tfull[acc]);
-        if (++acc == C::NACC) {
-          acc = 0;
-          acc_phase ^= 1;
-        }
       }
+      __syncwarp();
+      if (++acc == C::NACC) {
+        acc = 0;
+        acc_phase ^= 1;
+      }
+    }
+    if (one) {
       if constexpr (PAIR)
         gb::tc_commit_pair_multicast(mma_done, 0x1);
       else
         gb::tc_commit(mma_done);
-      gb::mbar_wait_bounded(mma_done, 0, p.wait_ns, p.err);
     }
+    __syncwarp();
+    gb::mbar_wait_bounded_warp<PAIR>(mma_done, 0, p.wait_ns, p.err);
   }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");

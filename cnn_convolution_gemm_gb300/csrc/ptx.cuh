@@ -69,6 +69,19 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
+// mbar_try_wait for a barrier on which other CTAs of the cluster arrive too.
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // Wait for the phase with the given parity to complete, giving up after
 // limit_ns of wall time.  Returns false (and records DEV timeout in *err) if
 // the limit ran out.
@@ -83,6 +96,40 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity
       return false;
     }
   }
+}
+
+// The same, by a whole warp that goes on together.
+template <bool CLUSTER>
+__device__ __forceinline__ bool mbar_wait_bounded_warp(uint64_t* bar, uint32_t parity,
+                                                       unsigned long long limit_ns, int* err) {
+  bool ok = CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity);
+  if (!__all_sync(0xFFFFFFFFu, ok)) {
+    const uint64_t t0 = global_timer_ns();
+    bool late = false;
+    while (!ok && !late) {
+      ok = CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity);
+      late = global_timer_ns() - t0 > limit_ns;
+    }
+    if (!__all_sync(0xFFFFFFFFu, ok)) {
+      record_error(err, 1);
+      return false;
+    }
+  }
+  return true;
+}
+
+// One lane of the (converged) warp, always the same.  Code that a whole warp runs up to
+// an instruction that one lane issues keeps the instruction's descriptors and addresses
+// in uniform registers; under `lane == 0` each tcgen05 instruction cost about 45 cycles
+// to issue (12 scale copies and 4 MMAs: 808 cycles, issued so 513, the MMAs' own time).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
 }
 
 // ---- TMA --------------------------------------------------------------------
