@@ -57,57 +57,128 @@ __device__ __forceinline__ uint32_t to_e4m3(float v) {
   return r & 0xFFu;
 }
 __device__ __forceinline__ float from_e4m3(uint32_t b) {
-  const uint32_t e = (b >> 3) & 15u, f = b & 7u;
-  if ((b & 0x7Fu) == 0x7Fu) return __int_as_float(0x7FFFFFFF);
-  const float a = e ? __uint_as_float(((e + 120u) << 23) | (f << 20)) : (float)f * 0.001953125f;
-  return (b & 0x80u) ? -a : a;
+  float v;
+  asm("{\n\t.reg .b32 h;\n\t.reg .b16 lo, hi;\n\t"
+      "cvt.rn.f16x2.e4m3x2 h, %1;\n\t"
+      "mov.b32 {lo, hi}, h;\n\t"
+      "cvt.f32.f16 %0, lo;\n\t}"
+      : "=f"(v)
+      : "h"((uint16_t)b));
+  return v;
 }
 
-// The scale byte of a block from its largest magnitude, and the quotients of its
-// elements.  NV divides by t = s * tensor_scale: with r = 1 / t rounded to nearest,
-// q0 = v r and the exact remainder v - q0 t (one fma) correct each other to the
-// rounded quotient (Markstein's correction), so that a quotient that lies on a
-// tie of E2M1 arrives there exactly; three operations an element where an IEEE
-// division takes about ten.
+// Two fp32 values in one register pair: a packed operation is one instruction.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// About 2^-23 relative; 1 / 0 = inf, 1 / inf = 0.
+__device__ __forceinline__ float rcp_approx(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float ex2_approx(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+// max(|a|, |b|, |c|); a NaN stays.
+__device__ __forceinline__ float max_abs(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// max and min of two values; a NaN stays.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+// v cut to [-lim, lim], lim >= 0
+__device__ __forceinline__ float clamp_abs(float v, float lim) {
+  float r;
+  asm("min.xorsign.abs.f32 %0, %1, %2;" : "=f"(r) : "f"(v), "f"(lim));
+  return r;
+}
+
+// A tensor scale g with what NV blocks need of it: t6 = 6 g and r6 = 1 / t6, rounded.
+struct TensorScale {
+  float g, t6, r6;
+};
+inline TensorScale tensor_scale(float g) {
+  const float t6 = 6.0f * g;
+  return {g, t6, 1.0f / t6};
+}
+
+// v / t rounded to nearest, from r = 1 / t: q0 = v r and the exact remainder
+// v - q0 t (one fma) correct each other (Markstein's correction), so that a quotient
+// that is a tie of E2M1 or E4M3 arrives there exactly.  Quotients above most come out
+// as some value above most (v r may overflow).
+__device__ __forceinline__ float quotient(float v, float t, float r, float most) {
+  const float q0 = clamp_abs(v * r, most);
+  return __fmaf_rn(__fmaf_rn(-q0, t, v), r, q0);
+}
+
+// The scale byte of a block from its largest magnitude, and its codes.
 template <int FMT>
 struct BlockScale {
   uint32_t byte;
-  float t, r;  // MX: r alone, a power of two
+  float t, r;  // MX: r alone, a power of two; NV: the divisor s * g and its reciprocal
 
-  __device__ __forceinline__ BlockScale(float amax, float tensor_scale) {
-    const uint32_t e = __float_as_uint(amax) >> 23;  // amax >= 0 (a NaN: its sign dropped)
-    const bool bad = (e & 255u) == 255u;
+  __device__ __forceinline__ BlockScale(float amax, const TensorScale& ts) {
+    const uint32_t e = (__float_as_uint(amax) >> 23) & 255u;  // amax >= 0 or a NaN
+    const bool bad = e == 255u;
     if (FMT == CONV_FP4_MX) {
       // floor(log2 amax) = e - 127 for normal numbers; e <= 2 and subnormals: 2^-127
       byte = bad ? 255u : (e > 2u ? e - 2u : 0u);
       r = bad ? 0.0f : __uint_as_float((254u - byte) << 23);  // 2^(127 - byte)
-      t = r;
     } else {
-      byte = bad ? 0x7Fu : to_e4m3(__fdiv_rn(amax, __fmul_rn(6.0f, tensor_scale)));
-      t = bad ? 0.0f : __fmul_rn(from_e4m3(byte), tensor_scale);
-      r = __frcp_rn(t);
+      byte = bad ? 0x7Fu : to_e4m3(quotient(amax, ts.t6, ts.r6, 1024.0f));
+      t = from_e4m3(byte) * ts.g;
+      // 1 / t, one Newton step from the approximation
+      const float r0 = rcp_approx(t);
+      r = __fmaf_rn(__fmaf_rn(-t, r0, 1.0f), r0, r0);
+      if (bad || byte == 0u) t = r = 0.0f;  // all codes 0
     }
   }
   // codes of eight elements of the block
   __device__ __forceinline__ uint32_t codes(const float (&v)[8]) const {
     float q[8];
-    if (t == 0.0f) return 0u;
-    if (FMT == CONV_FP4_MX) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) q[i] = v[i] * r;
-    } else if (byte == 0x7Eu) {
-      // the largest scale: elements may lie far above 6 t, where the product with r
-      // could overflow
-#pragma unroll
-      for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(v[i], t);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float q0 = v[i] * r;
-        q[i] = __fmaf_rn(__fmaf_rn(-q0, t, v[i]), r, q0);
+    for (int i = 0; i < 8; i += 2) {
+      const uint64_t q0 = mul2(pack2(v[i], v[i + 1]), pack2(r, r));
+      unpack2(q0, q[i], q[i + 1]);
+      if (FMT == CONV_FP4_NV) {
+        // quotient() on pairs
+        q[i] = clamp_abs(q[i], 8.0f);
+        q[i + 1] = clamp_abs(q[i + 1], 8.0f);
+        const uint64_t c = pack2(q[i], q[i + 1]);
+        const uint64_t e = fma2(pack2(-q[i], -q[i + 1]), pack2(t, t), pack2(v[i], v[i + 1]));
+        unpack2(fma2(e, pack2(r, r), c), q[i], q[i + 1]);
       }
     }
-    return pack8_e2m1(q);
+    const uint32_t packed = pack8_e2m1(q);
+    return r == 0.0f ? 0u : packed;  // Inf * 0 in a block that is not finite
   }
 };
 
@@ -121,25 +192,21 @@ __device__ __forceinline__ float scale_value(uint32_t byte, float tensor_scale) 
   return __fmul_rn(from_e4m3(byte), tensor_scale);
 }
 
-// max of magnitudes that keeps a NaN: compared as bit patterns, where every NaN
-// and infinity lies above every finite magnitude.
-__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
-
 // One warp turns 256 consecutive columns of a row, eight to a lane (v; zero past
 // the last column), into codes and scales.  c0: the warp's first column.  All lanes
 // call it.  MX: 4 lanes share a block and 16 a scale tile; NV: 2 and 8.
 template <int FMT>
-__device__ __forceinline__ void store_warp_row(const float (&v)[8], float tensor_scale, long long r,
+__device__ __forceinline__ void store_warp_row(const float (&v)[8], const TensorScale& ts, long long r,
                                                int c0, int cols, uint8_t* __restrict__ codes,
                                                uint8_t* __restrict__ scales) {
   const int lane = threadIdx.x & 31;
   constexpr int LB = kBlock<FMT> / 8;  // lanes per block
-  uint32_t top = 0;
+  float top = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) top = max(top, abs_bits(v[i]));
+  for (int i = 0; i < 8; i += 2) top = max_abs(top, v[i], v[i + 1]);
 #pragma unroll
-  for (int o = 1; o < LB; o <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-  const BlockScale<FMT> s(__uint_as_float(top), tensor_scale);
+  for (int o = 1; o < LB; o <<= 1) top = max_abs(top, top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+  const BlockScale<FMT> s(top, ts);
   const uint32_t packed = s.codes(v);
   uint32_t word = s.byte << (8 * ((lane / LB) & 3));
   word |= __shfl_xor_sync(0xFFFFFFFFu, word, LB);
@@ -220,17 +287,26 @@ inline bool rows_vec(const void* p, long long ld) {
   return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (ld * (long long)sizeof(T)) % 16 == 0;
 }
 
-// GELU, x Phi(x).  Phi(-|x|) = 1/2 (a1 u + .. + a5 u^5) exp(-x^2 / 2) with
-// u = 1 / (1 + p |x| / sqrt 2): Abramowitz and Stegun 7.1.26, within 0.75e-7 of Phi
-// (the product's own rounding is larger), one reciprocal and one exponential.
-__device__ __forceinline__ float gelu(float x) {
-  const float u = __fdividef(1.0f, fmaf(0.3275911f * 0.70710678f, fabsf(x), 1.0f));
-  float q = fmaf(1.061405429f, u, -1.453152027f);
-  q = fmaf(q, u, 1.421413741f);
-  q = fmaf(q, u, -0.284496736f);
-  q = fmaf(q, u, 0.254829592f);
-  q = 0.5f * q * u * __expf(-0.5f * x * x);
-  return x * (x < 0.0f ? q : 1.0f - q);
+// GELU of two values, x Phi(x).  -Phi(-|x|) = q = -1/2 (a1 u + .. + a5 u^5) exp(-x^2 / 2)
+// with u = 1 / (1 + p |x| / sqrt 2): Abramowitz and Stegun 7.1.26, within 0.75e-7 of
+// Phi (the product's own rounding is larger).  x Phi(x) = max(x, 0) + |x| q for either sign.
+__device__ __forceinline__ void gelu2(float& x0, float& x1) {
+  // q is 0 well below 64: an infinity must not meet it
+  const float a0 = fminf(fabsf(x0), 64.0f), a1 = fminf(fabsf(x1), 64.0f);
+  const uint64_t x = pack2(x0, x1), a = pack2(a0, a1);
+  const float p = 0.3275911f * 0.70710678f;
+  float d0, d1, e0, e1;
+  unpack2(fma2(a, pack2(p, p), pack2(1.0f, 1.0f)), d0, d1);
+  const uint64_t u = pack2(rcp_approx(d0), rcp_approx(d1));
+  uint64_t q = fma2(u, pack2(-0.5f * 1.061405429f, -0.5f * 1.061405429f),
+                    pack2(0.5f * 1.453152027f, 0.5f * 1.453152027f));
+  q = fma2(q, u, pack2(-0.5f * 1.421413741f, -0.5f * 1.421413741f));
+  q = fma2(q, u, pack2(0.5f * 0.284496736f, 0.5f * 0.284496736f));
+  q = fma2(q, u, pack2(-0.5f * 0.254829592f, -0.5f * 0.254829592f));
+  const float k = -0.5f * 1.4426950408889634f;  // exp(-x^2 / 2) = 2^(k x^2)
+  unpack2(mul2(mul2(x, pack2(k, k)), x), e0, e1);
+  q = mul2(mul2(q, u), pack2(ex2_approx(e0), ex2_approx(e1)));
+  unpack2(fma2(a, q, pack2(max_nan(x0, 0.0f), max_nan(x1, 0.0f))), x0, x1);
 }
 
 // The epilogue's activation over N values.  SiLU: x / (1 + exp(-x)) (exp overflows to
@@ -239,16 +315,17 @@ template <int N>
 __device__ __forceinline__ void activate(float (&v)[N], int act) {
   if (act == CONV_ACT_RELU) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = v[i] < 0.0f ? 0.0f : v[i];
+    for (int i = 0; i < N; ++i) v[i] = max_nan(v[i], 0.0f);
   } else if (act == CONV_ACT_RELU6) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = v[i] < 0.0f ? 0.0f : (v[i] > 6.0f ? 6.0f : v[i]);
+    for (int i = 0; i < N; ++i) v[i] = min_nan(max_nan(v[i], 0.0f), 6.0f);
   } else if (act == CONV_ACT_GELU) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = gelu(v[i]);
+    for (int i = 0; i < N; i += 2) gelu2(v[i], v[i + 1]);
   } else if (act == CONV_ACT_SILU) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = __fdividef(v[i], 1.0f + __expf(-v[i]));
+    for (int i = 0; i < N; ++i)
+      v[i] = v[i] * rcp_approx(1.0f + ex2_approx(v[i] * -1.4426950408889634f));
   }
 }
 

@@ -14,7 +14,7 @@ constexpr int THREADS = 256;
 template <int FMT, typename T>
 __global__ void __launch_bounds__(THREADS)
     quantize_kernel(const T* __restrict__ x, long long ldx, int rows, int cols, int vec,
-                    float tensor_scale, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+                    const TensorScale ts, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
   const int chunks = (cols + 255) / 256;
   const long long tasks = (long long)rows * chunks;
   const long long step = (long long)gridDim.x * (THREADS / 32);
@@ -24,7 +24,7 @@ __global__ void __launch_bounds__(THREADS)
     const int c0 = (int)(t - r * chunks) * 256;
     float v[8];
     load8(x + r * ldx, c0 + (threadIdx.x & 31) * 8, cols, vec, v);
-    store_warp_row<FMT>(v, tensor_scale, r, c0, cols, codes, scales);
+    store_warp_row<FMT>(v, ts, r, c0, cols, codes, scales);
   }
 }
 
@@ -82,7 +82,7 @@ cudaError_t quantize_t(int rows, int cols, const void* x, long long ldx, float t
                        void* scales, cudaStream_t st) {
   const long long tasks = (long long)rows * ((cols + 255) / 256);
   quantize_kernel<FMT, T><<<grid_for(gb_ceil_div_ll(tasks, THREADS / 32)), THREADS, 0, st>>>(
-      static_cast<const T*>(x), ldx, rows, cols, rows_vec<T>(x, ldx), ts,
+      static_cast<const T*>(x), ldx, rows, cols, rows_vec<T>(x, ldx), tensor_scale(ts),
       static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales));
   gb_count_launch();
   return cudaGetLastError();

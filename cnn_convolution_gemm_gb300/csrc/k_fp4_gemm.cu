@@ -2,8 +2,8 @@
 // on the block-scaled tcgen05 MMAs.
 //
 // GEMM names here: M rows of X, N rows of W (the layer's outputs), KR the reduction.
-// Persistent CTAs of three warpgroups: warp 0 loads (TMA), warp 1 copies the block
-// scales to TMEM and issues the MMAs (one elected lane), warps 4..11 run the epilogue.  A k-step is
+// Persistent CTAs: warp 0 loads (TMA), warp 1 copies the block
+// scales to TMEM and issues the MMAs (one elected lane), warps 4 and up run the epilogue.  A k-step is
 // 256 elements: 128-byte rows of codes (128-byte swizzle) and 512-byte scale tiles.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -20,10 +20,11 @@ using namespace gb::fp4;
 
 constexpr int BM = 128;
 constexpr int BKB = 128;  // bytes of a row per k-step: 256 codes
-constexpr int THREADS = 384;
 
-template <int FMT, int BN, bool PAIR>
+template <int FMT, int BN, bool PAIR, int YIO>
 struct Cfg {
+  static constexpr int EPI_WARPS = BN / 16;  // 4 lane quarters x 64 columns each
+  static constexpr int THREADS = 128 + 32 * EPI_WARPS;
   static constexpr int ATOMS = FMT == CONV_FP4_MX ? 2 : 4;  // scale tiles per panel and k-step
   static constexpr int PB = (BN + 127) / 128;               // 128-row panels of W
   static constexpr int BROWS = PAIR ? BN / 2 : BN;          // rows of W this CTA loads
@@ -37,8 +38,9 @@ struct Cfg {
   // scale columns of a stage, in a slot of its own per stage: a slot is written again
   // only after the MMAs that read it have committed the stage
   static constexpr int SF_COLS = ATOMS * 4 * (1 + PB);
-  static constexpr int EPI_WARP = 4096 + 128;  // a warp's staging buffer and 32 biases
-  static constexpr int EPI_BYTES = 8 * EPI_WARP;
+  // a warp's staging buffer and 32 biases
+  static constexpr int EPI_WARP = (YIO == CONV_FP4_IO_CODES ? 0 : 2048) + 128;
+  static constexpr int EPI_BYTES = EPI_WARPS * EPI_WARP;
   static constexpr int SMEM = STAGES * STAGE_BYTES + EPI_BYTES + 256 + 1024;
   static_assert(NACC * BN + STAGES * SF_COLS <= 512, "TMEM");
   static_assert(SMEM <= 232448, "shared memory");
@@ -48,7 +50,8 @@ struct GemmParams {
   int M, N, ksteps, kmmas_last;  // 64-element MMAs of the last k-step
   int m_tiles, n_tiles;          // PAIR: m_tiles counts 256-row units
   int act, vec_y, vec_r;  // 16-byte accesses to rows of y / of the residual
-  float alpha, y_scale;
+  float alpha;
+  TensorScale y_scale;
   const float* bias;
   const void* res;
   void* y;
@@ -58,88 +61,75 @@ struct GemmParams {
   unsigned long long wait_ns;
 };
 
-// ---- epilogue of a 32 x 32 block: a lane holds a row's 32 fp32 accumulators --------
+// ---- epilogue: a lane holds a row's fp32 accumulators ----------------------------------
 //
 // Rows of the output (and of the residual) pass through a staging buffer of the warp,
-// so that global accesses are whole row segments: 32 rows of 32 elements, their
-// 16-byte pieces swizzled (a quarter-warp's accesses hit all banks once, by row and
-// by piece alike).
+// so that global accesses are whole row segments: 32 rows of 64 bytes (COLS elements),
+// their 16-byte pieces swizzled so that a quarter-warp's accesses hit all banks once,
+// by row and by piece alike.
 
 template <typename T>
 struct Block {
   static constexpr int ES = sizeof(T);
-  static constexpr int PIECES = 32 * ES / 16;  // 16-byte pieces of a row
-  static constexpr int RPI = 32 / PIECES;      // rows of one warp-wide access
+  static constexpr int COLS = 64 / ES;
 
   static __device__ __forceinline__ uint8_t* at(uint8_t* buf, int row, int piece) {
-    if constexpr (ES == 2)
-      return buf + row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
-    else
-      return buf + row * 128 + ((piece ^ (row & 7)) << 4);
+    return buf + row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
   }
   static __device__ __forceinline__ T* elem(uint8_t* buf, int row, int col) {
     return reinterpret_cast<T*>(at(buf, row, col * ES / 16) + col * ES % 16);
   }
-  // 16-byte pieces of a 32 x 32 block of global memory into registers; rows < rows
-  static __device__ __forceinline__ void fetch(uint4 (&r)[PIECES], const T* g, long long ld,
-                                               int rows) {
+  // a block of global memory into registers, four lanes to a row; rows < rows
+  static __device__ __forceinline__ void fetch(uint4 (&r)[4], const T* g, long long ld, int rows) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int i = 0; i < PIECES; ++i) {
-      const int row = i * RPI + lane / PIECES;
+    for (int i = 0; i < 4; ++i) {
+      const int row = i * 8 + lane / 4;
       r[i] = make_uint4(0, 0, 0, 0);
-      if (row < rows)
-        r[i] = *reinterpret_cast<const uint4*>(g + row * ld + lane % PIECES * (16 / ES));
+      if (row < rows) r[i] = *reinterpret_cast<const uint4*>(g + row * ld + lane % 4 * (16 / ES));
     }
   }
 };
 
-template <typename T>
-__device__ __forceinline__ void unpack(float (&v)[32], const uint8_t* buf) {
-  using B = Block<T>;
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int i = 0; i < B::PIECES; ++i) {
-    const uint4 u = *reinterpret_cast<const uint4*>(B::at(const_cast<uint8_t*>(buf), lane, i));
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if constexpr (B::ES == 2) {
-        v[i * 8 + 2 * k] += __uint_as_float(w[k] << 16);
-        v[i * 8 + 2 * k + 1] += __uint_as_float(w[k] & 0xFFFF0000u);
-      } else {
-        v[i * 4 + k] += __uint_as_float(w[k]);
-      }
-    }
-  }
-}
-
 // v (acc * alpha + bias) of rows m0.. and columns n0..: residual, activation, store.
 // pre: the residual's pieces, fetched ahead (vec_r and a whole block of columns).
 template <typename T>
-__device__ __forceinline__ void finish_float(const GemmParams& p, float (&v)[32], uint8_t* buf,
-                                             int m0, int n0, uint4 (&pre)[Block<T>::PIECES]) {
+__device__ __forceinline__ void finish_float(const GemmParams& p, float (&v)[Block<T>::COLS],
+                                             uint8_t* buf, int m0, int n0, const uint4 (&pre)[4]) {
   using B = Block<T>;
   const int lane = threadIdx.x & 31;
-  const int rows = min(32, p.M - m0), cols = min(32, p.N - n0);
+  const int rows = min(32, p.M - m0), cols = min(B::COLS, p.N - n0);
+  const bool whole = cols == B::COLS;
   if (p.res) {
-    if (p.vec_r && cols == 32) {
+    if (p.vec_r && whole) {
 #pragma unroll
-      for (int i = 0; i < B::PIECES; ++i)
-        *reinterpret_cast<uint4*>(B::at(buf, i * B::RPI + lane / B::PIECES, lane % B::PIECES)) =
-            pre[i];
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<uint4*>(B::at(buf, i * 8 + lane / 4, lane % 4)) = pre[i];
     } else if (lane < cols) {
       const T* g = static_cast<const T*>(p.res) + (long long)m0 * p.ldr + n0 + lane;
 #pragma unroll 4
       for (int r = 0; r < rows; ++r) *B::elem(buf, r, lane) = g[r * p.ldr];
     }
     __syncwarp();
-    unpack<T>(v, buf);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint4 u = *reinterpret_cast<const uint4*>(B::at(buf, lane, i));
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if constexpr (B::ES == 2) {
+          v[i * 8 + 2 * k] += __uint_as_float(w[k] << 16);
+          v[i * 8 + 2 * k + 1] += __uint_as_float(w[k] & 0xFFFF0000u);
+        } else {
+          v[i * 4 + k] += __uint_as_float(w[k]);
+        }
+      }
+    }
     __syncwarp();
   }
   activate(v, p.act);
 #pragma unroll
-  for (int i = 0; i < B::PIECES; ++i) {
+  for (int i = 0; i < 4; ++i) {
     uint32_t w[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -154,13 +144,13 @@ __device__ __forceinline__ void finish_float(const GemmParams& p, float (&v)[32]
   }
   __syncwarp();
   T* y = static_cast<T*>(p.y) + (long long)m0 * p.ldy + n0;
-  if (p.vec_y && cols == 32) {
+  if (p.vec_y && whole) {
 #pragma unroll
-    for (int i = 0; i < B::PIECES; ++i) {
-      const int row = i * B::RPI + lane / B::PIECES;
+    for (int i = 0; i < 4; ++i) {
+      const int row = i * 8 + lane / 4;
       if (row < rows)
-        *reinterpret_cast<uint4*>(y + row * p.ldy + lane % B::PIECES * (16 / B::ES)) =
-            *reinterpret_cast<const uint4*>(B::at(buf, row, lane % B::PIECES));
+        *reinterpret_cast<uint4*>(y + row * p.ldy + lane % 4 * (16 / B::ES)) =
+            *reinterpret_cast<const uint4*>(B::at(buf, row, lane % 4));
     }
   } else if (lane < cols) {
 #pragma unroll 4
@@ -169,8 +159,7 @@ __device__ __forceinline__ void finish_float(const GemmParams& p, float (&v)[32]
   __syncwarp();
 }
 
-// The same block as 4-bit codes: a row's 32 columns are one MX block or two NV blocks,
-// and lie in one lane.
+// 32 columns as 4-bit codes: one MX block or two NV blocks of the lane's row.
 template <int FMT>
 __device__ __forceinline__ void finish_codes(const GemmParams& p, float (&v)[32], int m0, int n0) {
   const long long m = m0 + (threadIdx.x & 31);
@@ -186,10 +175,10 @@ __device__ __forceinline__ void finish_codes(const GemmParams& p, float (&v)[32]
   uint32_t bytes = 0, code[4];
 #pragma unroll
   for (int k = 0; k < 32 / B; ++k) {
-    uint32_t top = 0;
+    float top = 0.0f;
 #pragma unroll
-    for (int i = 0; i < B; ++i) top = max(top, abs_bits(v[k * B + i]));
-    const BlockScale<FMT> s(__uint_as_float(top), p.y_scale);
+    for (int i = 0; i < B; i += 2) top = max_abs(top, v[k * B + i], v[k * B + i + 1]);
+    const BlockScale<FMT> s(top, p.y_scale);
     bytes |= s.byte << (8 * k);
 #pragma unroll
     for (int i = 0; i < B / 8; ++i) {
@@ -216,11 +205,11 @@ __device__ __forceinline__ void finish_codes(const GemmParams& p, float (&v)[32]
 }
 
 template <int FMT, int BN, bool PAIR, int YIO>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__(Cfg<FMT, BN, PAIR, YIO>::THREADS, 1)
     fp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_xs,
                     const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_ws,
                     const GemmParams p) {
-  using C = Cfg<FMT, BN, PAIR>;
+  using C = Cfg<FMT, BN, PAIR, YIO>;
   constexpr bool MX = FMT == CONV_FP4_MX;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -250,7 +239,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     for (int b = 0; b < C::NACC; ++b) {
       gb::mbar_init(&tfull[b], 1);
-      gb::mbar_init(&tempty[b], PAIR ? 16 : 8);  // one arrival per epilogue warp
+      gb::mbar_init(&tempty[b], C::EPI_WARPS * (PAIR ? 2 : 1));  // one arrival per epilogue warp
     }
     gb::mbar_init(mma_done, 1);
     gb::fence_barrier_init();
@@ -276,10 +265,9 @@ __global__ void __launch_bounds__(THREADS, 1)
   gb::allow_dependents();
 
   const int units = p.m_tiles * p.n_tiles;
-  // The registers of the launch, 384 x 168, as 128 x 40 + 256 x 232: the epilogue holds
-  // half a row of the tile.
+  // 256 columns: the launch's registers, 640 x 96, as 128 x 40 + 512 x 104 (at most)
   if (warp < 4) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+  if constexpr (BN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
   if (warp == 0) {
     // ---------------- TMA producer ----------------
     const bool one = gb::elect_one();
@@ -345,8 +333,6 @@ __global__ void __launch_bounds__(THREADS, 1)
     uint32_t phase = 0, acc_phase = 0;
     bool ok = true;
     for (int u = unit0; u < units && ok; u += ustep) {
-      if (!gb::mbar_wait_bounded_warp<PAIR>(&tempty[acc], acc_phase ^ 1, p.wait_ns, p.err)) break;
-      gb::tc_fence_after();
       const uint32_t d = tmem + acc * BN;
       for (int it = 0; it < p.ksteps; ++it) {
         if (!gb::mbar_wait_bounded_warp<PAIR>(&full[stage], phase, p.wait_ns, p.err)) {
@@ -354,13 +340,11 @@ __global__ void __launch_bounds__(THREADS, 1)
           break;
         }
         gb::tc_fence_after();
+        const uint32_t sfa = tmem + C::NACC * BN + stage * C::SF_COLS;
+        const uint32_t sfb = sfa + C::ATOMS * 4;
         if (one) {
-          const uint64_t ad = gb::sw128_kmajor_desc(gb::smem_u32(sA + stage * C::A_BYTES));
-          const uint64_t bd = gb::sw128_kmajor_desc(gb::smem_u32(sB + stage * C::B_BYTES));
           const uint32_t fa = gb::smem_u32(sFA + stage * C::SFA_BYTES);
           const uint32_t fb = gb::smem_u32(sFB + stage * C::SFB_BYTES);
-          const uint32_t sfa = tmem + C::NACC * BN + stage * C::SF_COLS;
-          const uint32_t sfb = sfa + C::ATOMS * 4;
           // scale tiles (32 rows x 16 bytes): A's tile j at columns 4 j, B's panel q of
           // tile j at 4 (j PB + q), so that an MMA's B scales are consecutive
 #pragma unroll
@@ -372,6 +356,19 @@ __global__ void __launch_bounds__(THREADS, 1)
                   sfb + 4 * (j * C::PB + q),
                   gb::noswz_kmajor_desc(fb + (q * C::ATOMS + j) * 512, 128, 128));
           }
+        }
+        __syncwarp();
+        // the tile's accumulator is needed only now
+        if (it == 0) {
+          if (!gb::mbar_wait_bounded_warp<PAIR>(&tempty[acc], acc_phase ^ 1, p.wait_ns, p.err)) {
+            ok = false;
+            break;
+          }
+          gb::tc_fence_after();
+        }
+        if (one) {
+          const uint64_t ad = gb::sw128_kmajor_desc(gb::smem_u32(sA + stage * C::A_BYTES));
+          const uint64_t bd = gb::sw128_kmajor_desc(gb::smem_u32(sB + stage * C::B_BYTES));
           const int mmas = it + 1 < p.ksteps ? 4 : p.kmmas_last;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -416,34 +413,43 @@ __global__ void __launch_bounds__(THREADS, 1)
     gb::mbar_wait_bounded_warp<PAIR>(mma_done, 0, p.wait_ns, p.err);
   }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
-    // ---------------- epilogue (warps 4..11) ----------------
-    // A warp owns 32 rows (the TMEM lane quarter it may access) and half the tile's
-    // columns.  It takes all its accumulators into registers and frees the TMEM
+    if constexpr (BN == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+    // ---------------- epilogue (warps 4 and up) ----------------
+    // A warp owns 32 rows (the TMEM lane quarter it may access) and 64 of the tile's
+    // columns.  It takes its accumulators into registers and frees the TMEM
     // accumulator before it works on them: the next tile's MMAs wait for TMEM reads only.
+    // (With 128 columns to a warp, two warps per scheduler left it idle 65 % of the time:
+    // 8192 x 4096 x 16384 with GELU 197 us.)
     using T = std::conditional_t<YIO == CONV_FP4_IO_BF16, __nv_bfloat16, float>;
-    constexpr int COLS = BN / 2, NCH = COLS / 32;
     constexpr bool FLOAT = YIO != CONV_FP4_IO_CODES;
-    const int q = warp & 3, half = (warp - 4) >> 2;
+    constexpr int PC = FLOAT ? Block<T>::COLS : 32;  // columns of a pass
+    constexpr int NP = 64 / PC;
+    const int q = warp & 3, group = (warp - 4) >> 2;
     uint8_t* const buf = sEpi + (warp - 4) * C::EPI_WARP;
-    float* const sbias = reinterpret_cast<float*>(buf + 4096);
+    float* const sbias = reinterpret_cast<float*>(buf + C::EPI_WARP - 128);
     const uint32_t tempty_pair = PAIR ? gb::mapa_shared(gb::smem_u32(tempty), 0) : 0u;
     int acc = 0;
     uint32_t acc_phase = 0;
-    uint4 pre[Block<T>::PIECES] = {};
+    uint4 pre[4] = {};
     asm volatile("griddepcontrol.wait;" ::: "memory");
     for (int u = unit0; u < units; u += ustep) {
       const int mt = (u / p.n_tiles) * (PAIR ? 2 : 1) + (int)rank, nt = u % p.n_tiles;
-      const int m0 = mt * BM + q * 32, nb = nt * BN + half * COLS;
+      const int m0 = mt * BM + q * 32, nb = nt * BN + group * 64;
       const bool ahead = FLOAT && p.res && p.vec_r;
       const T* res = static_cast<const T*>(p.res) + (long long)m0 * p.ldr + nb;
-      if (ahead && nb + 32 <= p.N) Block<T>::fetch(pre, res, p.ldr, p.M - m0);
+      if (ahead && nb + PC <= p.N) Block<T>::fetch(pre, res, p.ldr, p.M - m0);
+      float bias[2];  // of the lane's column in each half
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int n = nb + 32 * i + lane;
+        bias[i] = p.bias && n < p.N ? p.bias[n] : 0.0f;
+      }
       if (!gb::mbar_wait_bounded(&tfull[acc], acc_phase, p.wait_ns, p.err)) break;
       gb::tc_fence_after();
-      const uint32_t t = tmem + ((uint32_t)(q * 32) << 16) + acc * BN + half * COLS;
-      uint32_t r[NCH][32];
-#pragma unroll
-      for (int c = 0; c < NCH; ++c) gb::tmem_ld_x32(t + 32 * c, r[c]);
+      const uint32_t t = tmem + ((uint32_t)(q * 32) << 16) + acc * BN + group * 64;
+      uint32_t r[2][32];
+      gb::tmem_ld_x32(t, r[0]);
+      gb::tmem_ld_x32(t + 32, r[1]);
       gb::tmem_ld_wait();
       gb::tc_fence_before();
       __syncwarp();
@@ -454,39 +460,33 @@ __global__ void __launch_bounds__(THREADS, 1)
           gb::mbar_arrive(&tempty[acc]);
       }
       if (m0 < p.M) {
-#pragma unroll 1
-        for (int c = 0; c < NCH; ++c) {
-          const int n0 = nb + 32 * c;
+#pragma unroll
+        for (int s = 0; s < NP; ++s) {
+          const int n0 = nb + PC * s;
           if (n0 >= p.N) break;
-          float v[32];
-          if (p.bias) {
-            sbias[lane] = n0 + lane < p.N ? p.bias[n0 + lane] : 0.0f;
+          if (PC * s % 32 == 0) {
+            sbias[lane] = bias[PC * s / 32];
             __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float4 b = reinterpret_cast<const float4*>(sbias)[i];
-              v[4 * i] = fmaf(__uint_as_float(r[0][4 * i]), p.alpha, b.x);
-              v[4 * i + 1] = fmaf(__uint_as_float(r[0][4 * i + 1]), p.alpha, b.y);
-              v[4 * i + 2] = fmaf(__uint_as_float(r[0][4 * i + 2]), p.alpha, b.z);
-              v[4 * i + 3] = fmaf(__uint_as_float(r[0][4 * i + 3]), p.alpha, b.w);
-            }
-            __syncwarp();
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[0][i]) * p.alpha;
           }
-          // the next block of columns moves to the front: registers are not indexed
+          float v[PC];
+          const uint64_t al = pack2(p.alpha, p.alpha);
 #pragma unroll
-          for (int k = 0; k + 1 < NCH; ++k)
-#pragma unroll
-            for (int i = 0; i < 32; ++i) r[k][i] = r[k + 1][i];
+          for (int i = 0; i < PC; i += 4) {
+            const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(sbias + PC * s % 32 + i);
+            const uint32_t* const a = &r[PC * s / 32][PC * s % 32 + i];
+            unpack2(fma2(pack2(__uint_as_float(a[0]), __uint_as_float(a[1])), al, b.x), v[i],
+                    v[i + 1]);
+            unpack2(fma2(pack2(__uint_as_float(a[2]), __uint_as_float(a[3])), al, b.y), v[i + 2],
+                    v[i + 3]);
+          }
           if constexpr (FLOAT) {
             finish_float<T>(p, v, buf, m0, n0, pre);
-            if (ahead && c + 1 < NCH && n0 + 64 <= p.N)
-              Block<T>::fetch(pre, res + 32 * (c + 1), p.ldr, p.M - m0);
+            if (ahead && s + 1 < NP && n0 + 2 * PC <= p.N)
+              Block<T>::fetch(pre, res + PC * (s + 1), p.ldr, p.M - m0);
           } else {
             finish_codes<FMT>(p, v, m0, n0);
           }
+          __syncwarp();
         }
       }
       if (++acc == C::NACC) {
@@ -530,7 +530,7 @@ bool scales_map(CUtensorMap* map, const uint8_t* p, int fmt, int rows, int cols,
 
 template <int FMT, int BN, bool PAIR, int YIO>
 cudaError_t launch_tile(const Fp4Gemm& g, cudaStream_t st) {
-  using C = Cfg<FMT, BN, PAIR>;
+  using C = Cfg<FMT, BN, PAIR, YIO>;
   CUtensorMap tx, txs, tw, tws;
   if (!codes_map(&tx, g.x, g.M, g.C, BM) || !codes_map(&tw, g.w, g.K, g.C, C::BROWS) ||
       !scales_map(&txs, g.xs, FMT, g.M, g.C, C::ATOMS, 1) ||
@@ -545,7 +545,7 @@ cudaError_t launch_tile(const Fp4Gemm& g, cudaStream_t st) {
   p.n_tiles = gb_ceil_div(g.K, BN);
   p.act = g.act;
   p.alpha = g.alpha;
-  p.y_scale = g.y_scale;
+  p.y_scale = tensor_scale(g.y_scale);
   p.bias = g.bias;
   p.res = g.res;
   p.y = g.y;
@@ -569,14 +569,14 @@ cudaError_t launch_tile(const Fp4Gemm& g, cudaStream_t st) {
     cudaFuncAttributes fa = {};
     return cudaFuncGetAttributes(&fa, kern) == cudaSuccess ? fa.numRegs : 0;
   }();
-  if (regs * THREADS < 128 * 40 + 256 * 232) return cudaErrorLaunchOutOfResources;
+  if (BN == 256 && regs * C::THREADS < 128 * 40 + 512 * 104) return cudaErrorLaunchOutOfResources;
   const long long units = (long long)p.m_tiles * p.n_tiles;
   if (units >= (1LL << 31)) return cudaErrorInvalidValue;
   const int slots = PAIR ? gb_num_sms() / 2 : gb_num_sms();
   const int grid = (int)std::min<long long>(units, slots) * (PAIR ? 2 : 1);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(THREADS);
+  cfg.blockDim = dim3(C::THREADS);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];

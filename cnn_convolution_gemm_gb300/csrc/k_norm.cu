@@ -41,7 +41,7 @@ __device__ void row_stats(const float* row, int C, int kind, float eps, float* r
 
 // One block per row; the row stays in shared memory as fp32.
 template <typename TX, typename TZ>
-__global__ void __launch_bounds__(THREADS) norm_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(THREADS) norm_kernel(const NormArgs a, const TensorScale ts) {
   extern __shared__ float row[];
   __shared__ float red[THREADS / 32];
   const int C = a.C;
@@ -95,9 +95,9 @@ __global__ void __launch_bounds__(THREADS) norm_kernel(const NormArgs a) {
         if (a.out == CONV_NORM_OUT_FLOAT)
           store8(static_cast<TZ*>(a.h) + r * a.ldh, c, C, false, v);
         else if (a.out == CONV_NORM_OUT_FP4_MX)
-          store_warp_row<CONV_FP4_MX>(v, a.h_scale, r, c0, C, static_cast<uint8_t*>(a.h), a.hs);
+          store_warp_row<CONV_FP4_MX>(v, ts, r, c0, C, static_cast<uint8_t*>(a.h), a.hs);
         else
-          store_warp_row<CONV_FP4_NV>(v, a.h_scale, r, c0, C, static_cast<uint8_t*>(a.h), a.hs);
+          store_warp_row<CONV_FP4_NV>(v, ts, r, c0, C, static_cast<uint8_t*>(a.h), a.hs);
       }
     }
     __syncthreads();
@@ -111,7 +111,7 @@ cudaError_t norm_t(const NormArgs& a, cudaStream_t st) {
   const cudaError_t e = gb_set_smem_once(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
   const int most = gb_num_sms() * 8;
-  kern<<<a.rows < most ? a.rows : most, THREADS, smem, st>>>(a);
+  kern<<<a.rows < most ? a.rows : most, THREADS, smem, st>>>(a, tensor_scale(a.h_scale));
   gb_count_launch();
   return cudaGetLastError();
 }
