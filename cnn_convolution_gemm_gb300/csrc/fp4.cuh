@@ -42,12 +42,21 @@ __device__ __forceinline__ uint32_t pack8_e2m1(const float (&v)[8]) {
   return r;
 }
 
-// The value of an E2M1 code, times 2.
-__device__ __forceinline__ float e2m1_twice(uint32_t code) {
-  const uint32_t m = code & 7u;
-  // 0 1 2 3 4 6 8 12: below 4 the code itself, from there (2 + m % 2) << (m / 2 - 1)
-  const int t = m < 4u ? (int)m : (int)((2u + (m & 1u)) << ((m >> 1) - 1u));
-  return (float)((code & 8u) ? -t : t);
+// The values of the eight codes in w.
+__device__ __forceinline__ void unpack8_e2m1(uint32_t w, float (&v)[8]) {
+  asm("{\n\t.reg .b8 t0, t1, t2, t3;\n\t.reg .b32 h0, h1, h2, h3;\n\t"
+      ".reg .b16 a0, a1, a2, a3, a4, a5, a6, a7;\n\t"
+      "mov.b32 {t0, t1, t2, t3}, %8;\n\t"
+      "cvt.rn.f16x2.e2m1x2 h0, t0;\n\tcvt.rn.f16x2.e2m1x2 h1, t1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 h2, t2;\n\tcvt.rn.f16x2.e2m1x2 h3, t3;\n\t"
+      "mov.b32 {a0, a1}, h0;\n\tmov.b32 {a2, a3}, h1;\n\t"
+      "mov.b32 {a4, a5}, h2;\n\tmov.b32 {a6, a7}, h3;\n\t"
+      "cvt.f32.f16 %0, a0;\n\tcvt.f32.f16 %1, a1;\n\tcvt.f32.f16 %2, a2;\n\t"
+      "cvt.f32.f16 %3, a3;\n\tcvt.f32.f16 %4, a4;\n\tcvt.f32.f16 %5, a5;\n\t"
+      "cvt.f32.f16 %6, a6;\n\tcvt.f32.f16 %7, a7;\n\t}"
+      : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+        "=f"(v[7])
+      : "r"(w));
 }
 
 // The E4M3 byte nearest to v (>= 0; above 448: 448), and the value of such a byte.

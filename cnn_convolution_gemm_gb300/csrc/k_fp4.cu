@@ -1,56 +1,92 @@
 // Microscaled 4-bit quantisation, its inverse, and the packing of row-by-row scales.
 #include <cuda_runtime.h>
 
+#include <algorithm>
+
 #include "fp4.cuh"
 #include "internal.h"
+#include "ptx.cuh"
 
 namespace {
 using namespace gb::fp4;
 
 constexpr int THREADS = 256;
+constexpr int ROWS = 4;  // rows whose loads a warp issues together
 
-// One warp per 256 columns of a row: 8 elements a lane, the block's largest
-// magnitude by shuffles, codes stored as 4 bytes a lane (128 a warp).
+// A warp works on 256 columns of a row, 8 to a lane, and walks over rows.  Both
+// directions move bytes only: the loads of four rows are in flight per warp, an
+// element costs about eight instructions.  wx (a power of two up to 8) warps of a block
+// lie side by side along a row, the others below one another.
+struct Walk {
+  int c;               // the lane's first column
+  long long row, step; // first row, and rows between the warp's rows
+};
+__device__ __forceinline__ Walk walk(int wx_log2) {
+  const int warp = threadIdx.x >> 5, wy = (THREADS / 32) >> wx_log2;
+  Walk w;
+  w.c = (((int)blockIdx.x << wx_log2) + (warp & ((1 << wx_log2) - 1))) * 256 +
+        (threadIdx.x & 31) * 8;
+  w.row = (long long)blockIdx.y * wy + (warp >> wx_log2);
+  w.step = (long long)gridDim.y * wy;
+  return w;
+}
+
 template <int FMT, typename T>
 __global__ void __launch_bounds__(THREADS)
     quantize_kernel(const T* __restrict__ x, long long ldx, int rows, int cols, int vec,
-                    const TensorScale ts, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
-  const int chunks = (cols + 255) / 256;
-  const long long tasks = (long long)rows * chunks;
-  const long long step = (long long)gridDim.x * (THREADS / 32);
-  for (long long t = (long long)blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5); t < tasks;
-       t += step) {
-    const long long r = t / chunks;
-    const int c0 = (int)(t - r * chunks) * 256;
-    float v[8];
-    load8(x + r * ldx, c0 + (threadIdx.x & 31) * 8, cols, vec, v);
-    store_warp_row<FMT>(v, ts, r, c0, cols, codes, scales);
+                    int wx_log2, const TensorScale ts, uint8_t* __restrict__ codes,
+                    uint8_t* __restrict__ scales) {
+  gb::allow_dependents();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Walk w = walk(wx_log2);
+  const int c0 = w.c - (int)(threadIdx.x & 31) * 8;
+  if (c0 >= cols) return;
+  for (long long r0 = w.row; r0 < rows; r0 += ROWS * w.step) {
+    float v[ROWS][8];
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+      const long long r = r0 + i * w.step;
+      if (r < rows) load8(x + r * ldx, w.c, cols, vec, v[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+      const long long r = r0 + i * w.step;
+      if (r < rows) store_warp_row<FMT>(v[i], ts, r, c0, cols, codes, scales);
+    }
   }
 }
 
 template <int FMT, typename T>
 __global__ void __launch_bounds__(THREADS)
     dequantize_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
-                      int rows, int cols, int vec, float tensor_scale, T* __restrict__ y,
-                      long long ldy) {
-  const int chunks = (cols + 255) / 256;
-  const long long tasks = (long long)rows * chunks;
-  const long long step = (long long)gridDim.x * (THREADS / 32);
+                      int rows, int cols, int vec, int wx_log2, float tensor_scale,
+                      T* __restrict__ y, long long ldy) {
+  gb::allow_dependents();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Walk w = walk(wx_log2);
+  if (w.c >= cols) return;
   const long long pitch = code_pitch(cols);
-  const int tiles = tiles_per_row(FMT, cols);
-  for (long long t = (long long)blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5); t < tasks;
-       t += step) {
-    const long long r = t / chunks;
-    const int c = (int)(t - r * chunks) * 256 + (threadIdx.x & 31) * 8;
-    if (c >= cols) continue;
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(codes + r * pitch + c / 2);
-    const int b = c / kBlock<FMT>;
-    const float s =
-        scale_value<FMT>(scales[scale_word_offset(r, b >> 2, tiles) + (b & 3)], tensor_scale);
-    float v[8];
+  const int tiles = tiles_per_row(FMT, cols), b = w.c / kBlock<FMT>;
+  for (long long r0 = w.row; r0 < rows; r0 += ROWS * w.step) {
+    uint32_t code[ROWS], byte[ROWS];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 0.5f * e2m1_twice((w >> (4 * i)) & 15u) * s;
-    store8(y + r * ldy, c, cols, vec, v);
+    for (int i = 0; i < ROWS; ++i) {
+      const long long r = r0 + i * w.step;
+      if (r >= rows) continue;
+      code[i] = *reinterpret_cast<const uint32_t*>(codes + r * pitch + w.c / 2);
+      byte[i] = scales[scale_word_offset(r, b >> 2, tiles) + (b & 3)];
+    }
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+      const long long r = r0 + i * w.step;
+      if (r >= rows) continue;
+      const float s = scale_value<FMT>(byte[i], tensor_scale);
+      float v[8];
+      unpack8_e2m1(code[i], v);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] *= s;
+      store8(y + r * ldy, w.c, cols, vec, v);
+    }
   }
 }
 
@@ -77,26 +113,58 @@ int grid_for(long long blocks) {
   return (int)(blocks < most ? blocks : most);
 }
 
+// Grid of a walk over rows x cols: the columns covered once, as many rows at a time as
+// fill the SMs (8 blocks each) with ROWS rows to a warp.
+struct Shape {
+  dim3 grid;
+  int wx_log2;
+};
+Shape walk_shape(int rows, int cols) {
+  Shape s;
+  const int chunks = (int)gb_ceil_div_ll(cols, 256);
+  s.wx_log2 = 0;
+  while (s.wx_log2 < 3 && (1 << s.wx_log2) < chunks) ++s.wx_log2;
+  const int gx = gb_ceil_div(chunks, 1 << s.wx_log2);
+  const long long need = gb_ceil_div_ll(rows, ROWS * ((THREADS / 32) >> s.wx_log2));
+  const long long gy = std::min<long long>(need, std::max(1, gb_num_sms() * 8 / gx));
+  s.grid = dim3((unsigned)gx, (unsigned)gy);
+  return s;
+}
+
+// Launch that may set up while the kernel before it drains (it waits for that kernel's
+// end before it touches global memory).
+template <typename... P, typename... A>
+cudaError_t launch_walk(void (*kern)(P...), dim3 grid, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(THREADS);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+  if (e == cudaSuccess) gb_count_launch();
+  return e;
+}
+
 template <int FMT, typename T>
 cudaError_t quantize_t(int rows, int cols, const void* x, long long ldx, float ts, void* codes,
                        void* scales, cudaStream_t st) {
-  const long long tasks = (long long)rows * ((cols + 255) / 256);
-  quantize_kernel<FMT, T><<<grid_for(gb_ceil_div_ll(tasks, THREADS / 32)), THREADS, 0, st>>>(
-      static_cast<const T*>(x), ldx, rows, cols, rows_vec<T>(x, ldx), tensor_scale(ts),
-      static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales));
-  gb_count_launch();
-  return cudaGetLastError();
+  const Shape s = walk_shape(rows, cols);
+  return launch_walk(quantize_kernel<FMT, T>, s.grid, st, static_cast<const T*>(x), ldx, rows, cols,
+                     (int)rows_vec<T>(x, ldx), s.wx_log2, tensor_scale(ts),
+                     static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales));
 }
 
 template <int FMT, typename T>
 cudaError_t dequantize_t(int rows, int cols, const void* codes, const void* scales, float ts,
                          void* y, long long ldy, cudaStream_t st) {
-  const long long tasks = (long long)rows * ((cols + 255) / 256);
-  dequantize_kernel<FMT, T><<<grid_for(gb_ceil_div_ll(tasks, THREADS / 32)), THREADS, 0, st>>>(
-      static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scales), rows, cols,
-      rows_vec<T>(y, ldy), ts, static_cast<T*>(y), ldy);
-  gb_count_launch();
-  return cudaGetLastError();
+  const Shape s = walk_shape(rows, cols);
+  return launch_walk(dequantize_kernel<FMT, T>, s.grid, st, static_cast<const uint8_t*>(codes),
+                     static_cast<const uint8_t*>(scales), rows, cols, (int)rows_vec<T>(y, ldy),
+                     s.wx_log2, ts, static_cast<T*>(y), ldy);
 }
 
 }  // namespace
