@@ -133,6 +133,8 @@ _lib = None
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     """Load libgbconv.so (built by build.py) and declare every signature."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(path):

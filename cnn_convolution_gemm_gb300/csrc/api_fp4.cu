@@ -385,5 +385,9 @@ extern "C" conv_status_t conv_norm_fwd(conv_norm_t d, int rows, const void* x, c
   a.x_out = x_out;
   a.h = h;
   a.hs = static_cast<uint8_t*>(h_scales);
-  return cuda_status(launch_norm(a, static_cast<cudaStream_t>(stream)), "norm");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool xb16 = a.x_dtype == CONV_BF16, zb16 = a.z_dtype == CONV_BF16;
+  return cuda_status(xb16 ? (zb16 ? launch_norm_bb(a, st) : launch_norm_bf(a, st))
+                          : (zb16 ? launch_norm_fb(a, st) : launch_norm_ff(a, st)),
+                     "norm");
 }

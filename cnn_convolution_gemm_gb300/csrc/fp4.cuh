@@ -201,28 +201,34 @@ __device__ __forceinline__ float scale_value(uint32_t byte, float tensor_scale) 
   return __fmul_rn(from_e4m3(byte), tensor_scale);
 }
 
-// One warp turns 256 consecutive columns of a row, eight to a lane (v; zero past
-// the last column), into codes and scales.  c0: the warp's first column.  All lanes
-// call it.  MX: 4 lanes share a block and 16 a scale tile; NV: 2 and 8.
+// One warp turns 512 consecutive columns of a row, 16 to a lane (v; zero past the last
+// column), into codes and scales.  c0: the warp's first column.  All lanes call it.
+// MX: two lanes share a block and eight a scale tile; NV: one and four.
 template <int FMT>
-__device__ __forceinline__ void store_warp_row(const float (&v)[8], const TensorScale& ts, long long r,
-                                               int c0, int cols, uint8_t* __restrict__ codes,
+__device__ __forceinline__ void store_warp_row(const float (&v)[16], const TensorScale& ts,
+                                               long long r, int c0, int cols,
+                                               uint8_t* __restrict__ codes,
                                                uint8_t* __restrict__ scales) {
   const int lane = threadIdx.x & 31;
-  constexpr int LB = kBlock<FMT> / 8;  // lanes per block
+  constexpr int LB = kBlock<FMT> / 16;  // lanes per block
   float top = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 8; i += 2) top = max_abs(top, v[i], v[i + 1]);
-#pragma unroll
-  for (int o = 1; o < LB; o <<= 1) top = max_abs(top, top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+  for (int i = 0; i < 16; i += 2) top = max_abs(top, v[i], v[i + 1]);
+  if (LB == 2) top = max_abs(top, top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
   const BlockScale<FMT> s(top, ts);
-  const uint32_t packed = s.codes(v);
+  float lo[8], hi[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    lo[i] = v[i];
+    hi[i] = v[8 + i];
+  }
+  const uint2 packed = make_uint2(s.codes(lo), s.codes(hi));
   uint32_t word = s.byte << (8 * ((lane / LB) & 3));
   word |= __shfl_xor_sync(0xFFFFFFFFu, word, LB);
   word |= __shfl_xor_sync(0xFFFFFFFFu, word, 2 * LB);
-  const int c = c0 + lane * 8;
+  const int c = c0 + lane * 16;
   const long long pitch = code_pitch(cols);
-  if (c < 2 * pitch) *reinterpret_cast<uint32_t*>(codes + r * pitch + c / 2) = packed;
+  if (c < 2 * pitch) *reinterpret_cast<uint2*>(codes + r * pitch + c / 2) = packed;
   const int tiles = tiles_per_row(FMT, cols), tj = c / (4 * kBlock<FMT>);
   if (lane % (4 * LB) == 0 && tj < tiles)
     *reinterpret_cast<uint32_t*>(scales + scale_word_offset(r, tj, tiles)) = word;
@@ -243,57 +249,96 @@ __device__ __forceinline__ void store_f32(T* p, float v) {
     *p = v;
 }
 
-// Eight consecutive elements from column c (zero from column cols on).  vec: the
-// row's address and c allow 16-byte loads.
-template <typename T>
-__device__ __forceinline__ void load8(const T* row, int c, int cols, bool vec, float (&v)[8]) {
-  if (vec && c + 8 <= cols) {
-    if constexpr (sizeof(T) == 2) {
-      const uint4 u = *reinterpret_cast<const uint4*>(row + c);
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-      }
-    } else {
-      const float4 a = *reinterpret_cast<const float4*>(row + c);
-      const float4 b = *reinterpret_cast<const float4*>(row + c + 4);
-      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? load_f32(row + c + i) : 0.0f;
-  }
+// 32 and 16 bytes of global memory, past L1 (read once; L1 is left to what is reused).
+struct alignas(32) Bytes32 {
+  uint32_t w[8];
+};
+__device__ __forceinline__ Bytes32 load_stream32(const void* p) {
+  Bytes32 r;
+  asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]), "=r"(r.w[4]),
+                 "=r"(r.w[5]), "=r"(r.w[6]), "=r"(r.w[7])
+               : "l"(p));
+  return r;
 }
+__device__ __forceinline__ void store32(void* p, const Bytes32& v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v.w[0]),
+               "r"(v.w[1]), "r"(v.w[2]), "r"(v.w[3]), "r"(v.w[4]), "r"(v.w[5]), "r"(v.w[6]),
+               "r"(v.w[7])
+               : "memory");
+}
+
+// 16 consecutive elements of a row as they lie in memory.
 template <typename T>
-__device__ __forceinline__ void store8(T* row, int c, int cols, bool vec, const float (&v)[8]) {
-  if (vec && c + 8 <= cols) {
-    if constexpr (sizeof(T) == 2) {
-      uint32_t w[4];
+struct Raw16 {
+  static constexpr int N = sizeof(T) / 2;  // 32-byte pieces
+  Bytes32 b[N];
+
+  // Elements from column c (zero from column cols on).  vec: the row allows 32-byte
+  // accesses at columns that are multiples of 16.
+  __device__ __forceinline__ void load(const T* row, int c, int cols, bool vec) {
+    if (vec && c + 16 <= cols) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t*>(&h);
-      }
-      *reinterpret_cast<uint4*>(row + c) = make_uint4(w[0], w[1], w[2], w[3]);
+      for (int i = 0; i < N; ++i) b[i] = load_stream32(row + c + i * (16 / N));
     } else {
-      *reinterpret_cast<float4*>(row + c) = make_float4(v[0], v[1], v[2], v[3]);
-      *reinterpret_cast<float4*>(row + c + 4) = make_float4(v[4], v[5], v[6], v[7]);
+#pragma unroll
+      for (int i = 0; i < 8 * N; ++i) {
+        uint32_t w = 0;
+        if constexpr (sizeof(T) == 2) {
+          const uint16_t* p = reinterpret_cast<const uint16_t*>(row);
+          if (c + 2 * i < cols) w = p[c + 2 * i];
+          if (c + 2 * i + 1 < cols) w |= (uint32_t)p[c + 2 * i + 1] << 16;
+        } else {
+          if (c + i < cols) w = reinterpret_cast<const uint32_t*>(row)[c + i];
+        }
+        b[i / 8].w[i % 8] = w;
+      }
+    }
+  }
+  __device__ __forceinline__ void get(float (&v)[16]) const {
+#pragma unroll
+    for (int i = 0; i < 8 * N; ++i) {
+      const uint32_t w = b[i / 8].w[i % 8];
+      if constexpr (sizeof(T) == 2) {
+        v[2 * i] = __uint_as_float(w << 16);
+        v[2 * i + 1] = __uint_as_float(w & 0xFFFF0000u);
+      } else {
+        v[i] = __uint_as_float(w);
+      }
+    }
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ void store16(T* row, int c, int cols, bool vec, const float (&v)[16]) {
+  if (vec && c + 16 <= cols) {
+    constexpr int N = sizeof(T) / 2;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      Bytes32 b;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if constexpr (sizeof(T) == 2) {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
+          b.w[k] = *reinterpret_cast<const uint32_t*>(&h);
+        } else {
+          b.w[k] = __float_as_uint(v[8 * i + k]);
+        }
+      }
+      store32(row + c + i * (16 / N), b);
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 16; ++i)
       if (c + i < cols) store_f32(row + c + i, v[i]);
   }
 }
 
-// Whether rows of T at p, ld elements apart, allow 16-byte accesses at columns that
-// are multiples of 8.
+// Whether rows of T at p, ld elements apart, allow accesses of so many bytes at columns
+// that are multiples of them.
 template <typename T>
-inline bool rows_vec(const void* p, long long ld) {
-  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (ld * (long long)sizeof(T)) % 16 == 0;
+inline bool rows_vec(const void* p, long long ld, int bytes) {
+  return reinterpret_cast<uintptr_t>(p) % bytes == 0 && (ld * (long long)sizeof(T)) % bytes == 0;
 }
 
 // GELU of two values, x Phi(x).  -Phi(-|x|) = q = -1/2 (a1 u + .. + a5 u^5) exp(-x^2 / 2)

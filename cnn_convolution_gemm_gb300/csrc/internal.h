@@ -299,4 +299,8 @@ struct NormArgs {
   uint8_t* hs;
   long long ldx, ldz, ldg, ldxo, ldh;
 };
-cudaError_t launch_norm(const NormArgs& a, cudaStream_t st);
+// by the types of (x, x') and of (z, gate, h): b bf16, f fp32
+cudaError_t launch_norm_bb(const NormArgs& a, cudaStream_t st);
+cudaError_t launch_norm_bf(const NormArgs& a, cudaStream_t st);
+cudaError_t launch_norm_fb(const NormArgs& a, cudaStream_t st);
+cudaError_t launch_norm_ff(const NormArgs& a, cudaStream_t st);

@@ -11,11 +11,11 @@ namespace {
 using namespace gb::fp4;
 
 constexpr int THREADS = 256;
-constexpr int ROWS = 4;  // rows whose loads a warp issues together
+constexpr int ROWS = 2;  // rows whose loads a warp issues together
 
-// A warp works on 256 columns of a row, 8 to a lane, and walks over rows.  Both
-// directions move bytes only: the loads of four rows are in flight per warp, an
-// element costs about eight instructions.  wx (a power of two up to 8) warps of a block
+// A warp works on 512 columns of a row, 16 to a lane (32 bytes of bf16), and walks over
+// rows.  Both directions should move bytes only: the loads of several rows are in flight
+// per warp, and the instructions of an element are few.  wx (a power of two up to 8) warps of a block
 // lie side by side along a row, the others below one another.
 struct Walk {
   int c;               // the lane's first column
@@ -24,8 +24,8 @@ struct Walk {
 __device__ __forceinline__ Walk walk(int wx_log2) {
   const int warp = threadIdx.x >> 5, wy = (THREADS / 32) >> wx_log2;
   Walk w;
-  w.c = (((int)blockIdx.x << wx_log2) + (warp & ((1 << wx_log2) - 1))) * 256 +
-        (threadIdx.x & 31) * 8;
+  w.c = (((int)blockIdx.x << wx_log2) + (warp & ((1 << wx_log2) - 1))) * 512 +
+        (threadIdx.x & 31) * 16;
   w.row = (long long)blockIdx.y * wy + (warp >> wx_log2);
   w.step = (long long)gridDim.y * wy;
   return w;
@@ -39,19 +39,22 @@ __global__ void __launch_bounds__(THREADS)
   gb::allow_dependents();
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Walk w = walk(wx_log2);
-  const int c0 = w.c - (int)(threadIdx.x & 31) * 8;
+  const int c0 = w.c - (int)(threadIdx.x & 31) * 16;
   if (c0 >= cols) return;
   for (long long r0 = w.row; r0 < rows; r0 += ROWS * w.step) {
-    float v[ROWS][8];
+    Raw16<T> raw[ROWS];
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
       const long long r = r0 + i * w.step;
-      if (r < rows) load8(x + r * ldx, w.c, cols, vec, v[i]);
+      if (r < rows) raw[i].load(x + r * ldx, w.c, cols, vec);
     }
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
       const long long r = r0 + i * w.step;
-      if (r < rows) store_warp_row<FMT>(v[i], ts, r, c0, cols, codes, scales);
+      if (r >= rows) break;
+      float v[16];
+      raw[i].get(v);
+      store_warp_row<FMT>(v, ts, r, c0, cols, codes, scales);
     }
   }
 }
@@ -68,12 +71,13 @@ __global__ void __launch_bounds__(THREADS)
   const long long pitch = code_pitch(cols);
   const int tiles = tiles_per_row(FMT, cols), b = w.c / kBlock<FMT>;
   for (long long r0 = w.row; r0 < rows; r0 += ROWS * w.step) {
-    uint32_t code[ROWS], byte[ROWS];
+    uint2 code[ROWS];
+    uint32_t byte[ROWS];
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
       const long long r = r0 + i * w.step;
       if (r >= rows) continue;
-      code[i] = *reinterpret_cast<const uint32_t*>(codes + r * pitch + w.c / 2);
+      code[i] = *reinterpret_cast<const uint2*>(codes + r * pitch + w.c / 2);
       byte[i] = scales[scale_word_offset(r, b >> 2, tiles) + (b & 3)];
     }
 #pragma unroll
@@ -81,11 +85,15 @@ __global__ void __launch_bounds__(THREADS)
       const long long r = r0 + i * w.step;
       if (r >= rows) continue;
       const float s = scale_value<FMT>(byte[i], tensor_scale);
-      float v[8];
-      unpack8_e2m1(code[i], v);
+      float lo[8], hi[8], v[16];
+      unpack8_e2m1(code[i].x, lo);
+      unpack8_e2m1(code[i].y, hi);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] *= s;
-      store8(y + r * ldy, w.c, cols, vec, v);
+      for (int k = 0; k < 8; ++k) {
+        v[k] = lo[k] * s;
+        v[8 + k] = hi[k] * s;
+      }
+      store16(y + r * ldy, w.c, cols, vec, v);
     }
   }
 }
@@ -121,7 +129,7 @@ struct Shape {
 };
 Shape walk_shape(int rows, int cols) {
   Shape s;
-  const int chunks = (int)gb_ceil_div_ll(cols, 256);
+  const int chunks = (int)gb_ceil_div_ll(cols, 512);
   s.wx_log2 = 0;
   while (s.wx_log2 < 3 && (1 << s.wx_log2) < chunks) ++s.wx_log2;
   const int gx = gb_ceil_div(chunks, 1 << s.wx_log2);
@@ -154,7 +162,7 @@ cudaError_t quantize_t(int rows, int cols, const void* x, long long ldx, float t
                        void* scales, cudaStream_t st) {
   const Shape s = walk_shape(rows, cols);
   return launch_walk(quantize_kernel<FMT, T>, s.grid, st, static_cast<const T*>(x), ldx, rows, cols,
-                     (int)rows_vec<T>(x, ldx), s.wx_log2, tensor_scale(ts),
+                     (int)rows_vec<T>(x, ldx, 32), s.wx_log2, tensor_scale(ts),
                      static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales));
 }
 
@@ -163,7 +171,7 @@ cudaError_t dequantize_t(int rows, int cols, const void* codes, const void* scal
                          void* y, long long ldy, cudaStream_t st) {
   const Shape s = walk_shape(rows, cols);
   return launch_walk(dequantize_kernel<FMT, T>, s.grid, st, static_cast<const uint8_t*>(codes),
-                     static_cast<const uint8_t*>(scales), rows, cols, (int)rows_vec<T>(y, ldy),
+                     static_cast<const uint8_t*>(scales), rows, cols, (int)rows_vec<T>(y, ldy, 32),
                      s.wx_log2, ts, static_cast<T*>(y), ldy);
 }
 

@@ -553,11 +553,11 @@ cudaError_t launch_tile(const Fp4Gemm& g, cudaStream_t st) {
   p.ldr = g.ldr;
   p.ldy = g.ldy;
   if (YIO == CONV_FP4_IO_BF16) {
-    p.vec_y = rows_vec<__nv_bfloat16>(g.y, g.ldy);
-    p.vec_r = rows_vec<__nv_bfloat16>(g.res, g.ldr);
+    p.vec_y = rows_vec<__nv_bfloat16>(g.y, g.ldy, 16);
+    p.vec_r = rows_vec<__nv_bfloat16>(g.res, g.ldr, 16);
   } else {
-    p.vec_y = rows_vec<float>(g.y, g.ldy);
-    p.vec_r = rows_vec<float>(g.res, g.ldr);
+    p.vec_y = rows_vec<float>(g.y, g.ldy, 16);
+    p.vec_r = rows_vec<float>(g.res, g.ldr, 16);
   }
   p.err = gb_device_error_word();
   p.wait_ns = gb_wait_limit_ns();

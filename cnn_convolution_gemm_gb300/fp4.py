@@ -15,8 +15,10 @@ CONV_DTYPE = {torch.bfloat16: B.CONV_BF16, torch.float32: B.CONV_F32}
 BLOCK = {B.CONV_FP4_MX: 32, B.CONV_FP4_NV: 16}
 
 
-def stream_handle(stream) -> int:
-    return torch.cuda.current_stream().cuda_stream if stream is None else stream
+def stream_handle(stream, device: torch.device) -> int:
+    """stream, or the handle of the device's current stream (without building a
+    torch.cuda.Stream: a call's host time is a few microseconds in all)."""
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream
 
 
 def allocating_on(stream):
@@ -31,14 +33,14 @@ def rows_of(t: torch.Tensor, cols: int, what: str):
     """(rows, elements between rows) of a tensor [..., cols] whose rows are evenly spaced."""
     if t.shape[-1] != cols:
         raise ValueError(f"{what}: last dimension {t.shape[-1]}, expected {cols}")
+    if t.is_contiguous():
+        return t.numel() // cols, cols
     if t.dim() == 2:
         rows, ld = t.shape[0], t.stride(0)
         if t.stride(1) != 1 and cols > 1 and rows:
             raise ValueError(f"{what}: the elements of a row must be contiguous")
         return rows, ld if rows > 1 else cols
-    if not t.is_contiguous():
-        raise ValueError(f"{what}: must be contiguous (or 2-D with contiguous rows)")
-    return t.numel() // cols, cols
+    raise ValueError(f"{what}: must be contiguous (or 2-D with contiguous rows)")
 
 
 class Fp4Tensor:
@@ -70,7 +72,8 @@ def quantize(x: torch.Tensor, fmt, tensor_scale=1.0, out: Fp4Tensor | None = Non
     elif (out.rows, out.cols, out.fmt) != (rows, cols, fmt):
         raise ValueError("out: a 4-bit matrix of another shape or format")
     B.conv_fp4_quantize(fmt, CONV_DTYPE[x.dtype], rows, cols, x.data_ptr(), ld, tensor_scale,
-                        out.codes.data_ptr(), out.scales.data_ptr(), stream_handle(stream))
+                        out.codes.data_ptr(), out.scales.data_ptr(),
+                        stream_handle(stream, x.device))
     out.tensor_scale = tensor_scale
     return out
 
@@ -86,7 +89,7 @@ def dequantize(t: Fp4Tensor, dtype=torch.bfloat16, out: torch.Tensor | None = No
         raise ValueError(f"out: {rows} rows, expected {t.rows}")
     B.conv_fp4_dequantize(t.fmt, CONV_DTYPE[out.dtype], rows, t.cols, t.codes.data_ptr(),
                           t.scales.data_ptr(), t.tensor_scale, out.data_ptr(), ld,
-                          stream_handle(stream))
+                          stream_handle(stream, out.device))
     return out
 
 
@@ -140,7 +143,7 @@ class Fp4Linear:
         with allocating_on(stream):
             tiled = torch.empty(sb, dtype=torch.uint8, device=codes.device)
         B.conv_fp4_pack_scales(self.fmt, self.K, self.C, scales.data_ptr(), tiled.data_ptr(),
-                               stream_handle(stream))
+                               stream_handle(stream, codes.device))
         self._set(Fp4Tensor(self.K, self.C, self.fmt, w_scale, codes, tiled))
 
     def _set(self, w: Fp4Tensor):
@@ -148,64 +151,69 @@ class Fp4Linear:
         self.w = w
 
     def _workspace(self, rows, stream, handle):
+        """(address, bytes) of the stream's workspace for so many rows."""
         need = self._sizes.get(rows)
         if need is None:
             need = self._sizes[rows] = B.conv_fp4_workspace_size(self.desc, rows)
+        if not need:
+            return None, 0
         ws = self._ws.get(handle)
-        if need and (ws is None or ws.numel() < need):
+        if ws is None or ws.numel() < need:
             with allocating_on(stream):
                 ws = torch.empty(need, dtype=torch.uint8, device=self.w.codes.device)
             self._ws[handle] = ws
-        return ws
+        return ws.data_ptr(), ws.numel()
 
     def forward(self, x, bias=None, residual=None, out=None, stream=None):
-        if self.w is None:
+        w = self.w
+        if w is None:
             raise RuntimeError("prepack() or load() the weights first")
-        handle = stream_handle(stream)
+        C, K, y_dtype = self.C, self.K, self.y_dtype
+        device = w.codes.device
+        handle = stream_handle(stream, device)
         if self.x_dtype is None:
-            if (x.cols, x.fmt, x.tensor_scale) != (self.C, self.fmt, self.x_scale):
+            if (x.cols, x.fmt, x.tensor_scale) != (C, self.fmt, self.x_scale):
                 raise ValueError("x: a 4-bit matrix of another width, format or tensor scale")
-            rows, ldx, lead = x.rows, self.C, (x.rows,)
+            rows, ldx, lead = x.rows, C, (x.rows,)
             xp, xsp = x.codes.data_ptr(), x.scales.data_ptr()
         else:
-            if x.dtype != self.x_dtype:
+            if x.dtype is not self.x_dtype:
                 raise ValueError(f"x: {x.dtype}, expected {self.x_dtype}")
-            (rows, ldx), lead = rows_of(x, self.C, "x"), x.shape[:-1]
+            (rows, ldx), lead = rows_of(x, C, "x"), None
             xp, xsp = x.data_ptr(), None
-        if bias is not None and (bias.dtype != torch.float32 or bias.numel() != self.K
-                                 or not bias.is_contiguous()):
-            raise ValueError("bias: expected contiguous fp32 [K]")
-        ldr = ldy = self.K
-        ysp = None
-        if self.y_dtype is None:
+        bp = rp = ysp = None
+        if bias is not None:
+            if bias.dtype is not torch.float32 or bias.numel() != K or not bias.is_contiguous():
+                raise ValueError("bias: expected contiguous fp32 [K]")
+            bp = bias.data_ptr()
+        ldr = ldy = K
+        if y_dtype is None:
             if out is None:
-                out = empty(rows, self.K, self.fmt, self.w.codes.device, self.y_scale, stream)
-            elif (out.rows, out.cols, out.fmt) != (rows, self.K, self.fmt):
+                out = empty(rows, K, self.fmt, device, self.y_scale, stream)
+            elif (out.rows, out.cols, out.fmt) != (rows, K, self.fmt):
                 raise ValueError("out: a 4-bit matrix of another shape or format")
             out.tensor_scale = self.y_scale
             yp, ysp = out.codes.data_ptr(), out.scales.data_ptr()
         else:
             if out is None:
                 with allocating_on(stream):
-                    out = torch.empty(*lead, self.K, dtype=self.y_dtype,
-                                      device=self.w.codes.device)
-            got, ldy = rows_of(out, self.K, "out")
-            if got != rows or out.dtype != self.y_dtype:
+                    out = torch.empty(*(x.shape[:-1] if lead is None else lead), K, dtype=y_dtype,
+                                      device=device)
+            got, ldy = rows_of(out, K, "out")
+            if got != rows or out.dtype is not y_dtype:
                 raise ValueError("out: another number of rows or type")
             yp = out.data_ptr()
         if residual is not None:
-            got, ldr = rows_of(residual, self.K, "residual")
-            if got != rows or residual.dtype != self.y_dtype:
+            got, ldr = rows_of(residual, K, "residual")
+            if got != rows or residual.dtype is not y_dtype:
                 raise ValueError("residual: another number of rows or type than y")
+            rp = residual.data_ptr()
         if (ldx, ldr, ldy) != self._strides:
             B.conv_fp4_set_strides(self.desc, ldx, ldr, ldy)
             self._strides = (ldx, ldr, ldy)
-        ws = self._workspace(rows, stream, handle)
-        B.conv_fp4_fwd(self.desc, rows, xp, xsp, self.w.codes.data_ptr(),
-                       self.w.scales.data_ptr(), None if bias is None else bias.data_ptr(),
-                       None if residual is None else residual.data_ptr(), yp, ysp,
-                       None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
-                       handle)
+        wsp, ws_bytes = self._workspace(rows, stream, handle)
+        B.conv_fp4_fwd(self.desc, rows, xp, xsp, w.codes.data_ptr(), w.scales.data_ptr(), bp, rp,
+                       yp, ysp, wsp, ws_bytes, handle)
         return out
 
     __call__ = forward

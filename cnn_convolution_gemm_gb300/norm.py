@@ -47,28 +47,39 @@ class ResidualNorm:
 
     def _tensor(self, t, dtype, rows, what):
         got, ld = rows_of(t, self.C, what)
-        if t.dtype != dtype or got != rows:
+        if t.dtype is not dtype or got != rows:
             raise ValueError(f"{what}: {got} rows of {t.dtype}, expected {rows} of {dtype}")
         return t.data_ptr(), ld
 
     def forward(self, x, z=None, gate=None, x_out=None, h_out=None, want_x=True, stream=None):
         """Returns (x', h).  x' is None when want_x is false, h when there is no norm_pre.
         x_out may be x itself."""
-        C = self.C
+        C, dtype, z_dtype = self.C, self.dtype, self.z_dtype
         rows, ldx = rows_of(x, C, "x")
-        if x.dtype != self.dtype:
-            raise ValueError(f"x: {x.dtype}, expected {self.dtype}")
+        if x.dtype is not dtype:
+            raise ValueError(f"x: {x.dtype}, expected {dtype}")
+        shape = x.shape
         zp = gp = xop = hp = hsp = None
         ldz = ldg = ldxo = ldh = C
+
+        def same(t, dt):  # the usual tensor: x's shape, contiguous
+            return t.dtype is dt and t.is_contiguous() and t.shape == shape
+
         if z is not None:
-            zp, ldz = self._tensor(z, self.z_dtype, rows, "z")
+            if same(z, z_dtype):
+                zp = z.data_ptr()
+            else:
+                zp, ldz = self._tensor(z, z_dtype, rows, "z")
         if gate is not None:
-            gp, ldg = self._tensor(gate, self.z_dtype, -(-rows // self.gate_rows), "gate")
+            gp, ldg = self._tensor(gate, z_dtype, -(-rows // self.gate_rows), "gate")
         if want_x:
             if x_out is None:
                 with allocating_on(stream):
-                    x_out = torch.empty(x.shape, dtype=self.dtype, device=x.device)
-            xop, ldxo = self._tensor(x_out, self.dtype, rows, "x_out")
+                    x_out = torch.empty(shape, dtype=dtype, device=x.device)
+            if same(x_out, dtype):
+                xop = x_out.data_ptr()
+            else:
+                xop, ldxo = self._tensor(x_out, dtype, rows, "x_out")
         else:
             x_out = None
         if self.pre == B.CONV_NORM_NONE:
@@ -83,14 +94,17 @@ class ResidualNorm:
         else:
             if h_out is None:
                 with allocating_on(stream):
-                    h_out = torch.empty(x.shape, dtype=self.z_dtype, device=x.device)
-            hp, ldh = self._tensor(h_out, self.z_dtype, rows, "h_out")
+                    h_out = torch.empty(shape, dtype=z_dtype, device=x.device)
+            if same(h_out, z_dtype):
+                hp = h_out.data_ptr()
+            else:
+                hp, ldh = self._tensor(h_out, z_dtype, rows, "h_out")
         strides = (ldx, ldz, ldg, ldxo, ldh)
         if strides != self._strides:
             B.conv_norm_set_strides(self.desc, *strides)
             self._strides = strides
         B.conv_norm_fwd(self.desc, rows, x.data_ptr(), zp, gp, xop, hp, hsp,
-                        stream_handle(stream))
+                        stream_handle(stream, x.device))
         return x_out, h_out
 
     __call__ = forward

@@ -68,7 +68,7 @@ class Fp4ResidualBlock:
         """x [..., C] -> (x', h').  h: norm_pre(x) in 4 bits when the block before handed
         it on, else None."""
         rows, _ = fp4.rows_of(x, self.C, "x")
-        handle = fp4.stream_handle(stream)
+        handle = fp4.stream_handle(stream, x.device)
         hb, t, z = self._buffers(rows, x.device, stream, handle)
         if h is None:
             _, h = self.norm_in(x, h_out=hb, want_x=False, stream=stream)
