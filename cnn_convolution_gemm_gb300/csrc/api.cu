@@ -106,6 +106,21 @@ cudaError_t gb_set_smem_once(const void* func, int bytes) {
   return e;
 }
 
+int gb_blocks_per_sm(const void* func, int threads, int smem) {
+  const int dev = current_device();
+  static std::mutex mu;
+  static std::map<std::pair<const void*, std::pair<int, int>>, int> known;  // (smem, device)
+  std::lock_guard<std::mutex> lk(mu);
+  auto it = known.find({func, {smem, dev}});
+  if (it != known.end()) return it->second;
+  int n = 0;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, func, threads, smem) != cudaSuccess) {
+    cudaGetLastError();  // clear a failed query, which is not remembered
+    return 0;
+  }
+  return known[{func, {smem, dev}}] = n;
+}
+
 unsigned long long gb_wait_limit_ns() {
   static unsigned long long v = [] {
     const char* e = getenv("GBCONV_WAIT_LIMIT_MS");

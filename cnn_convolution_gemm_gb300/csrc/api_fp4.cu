@@ -385,6 +385,8 @@ extern "C" conv_status_t conv_norm_fwd(conv_norm_t d, int rows, const void* x, c
   a.x_out = x_out;
   a.h = h;
   a.hs = static_cast<uint8_t*>(h_scales);
+  a.err = gb_device_error_word();
+  a.wait_ns = gb_wait_limit_ns();
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool xb16 = a.x_dtype == CONV_BF16, zb16 = a.z_dtype == CONV_BF16;
   return cuda_status(xb16 ? (zb16 ? launch_norm_bb(a, st) : launch_norm_bf(a, st))

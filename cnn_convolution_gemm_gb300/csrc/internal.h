@@ -48,6 +48,9 @@ cudaError_t launch_selftest_wait_timeout(int* err, unsigned long long limit_ns, 
 // Raise a kernel's dynamic shared-memory limit, once per (kernel, device): the
 // attribute call costs host time on every launch otherwise.
 cudaError_t gb_set_smem_once(const void* func, int bytes);
+// Blocks of so many threads and dynamic shared memory that an SM holds at once (cached
+// per kernel, size and device; 0 if the query failed).
+int gb_blocks_per_sm(const void* func, int threads, int smem);
 // Wait limit for device-side bounded waits, in nanoseconds (GBCONV_WAIT_LIMIT_MS).
 unsigned long long gb_wait_limit_ns();
 
@@ -298,6 +301,8 @@ struct NormArgs {
   void *x_out, *h;
   uint8_t* hs;
   long long ldx, ldz, ldg, ldxo, ldh;
+  int* err;
+  unsigned long long wait_ns;
 };
 // by the types of (x, x') and of (z, gate, h): b bf16, f fp32
 cudaError_t launch_norm_bb(const NormArgs& a, cudaStream_t st);

@@ -3,8 +3,9 @@
 // Bound by HBM: x and z are read once and x' and h written once; a row stays in
 // registers between its up to four reductions (a mean and a sum of squared deviations
 // per layer norm: two passes over registers, so that a large mean does not cancel the
-// variance's digits).  The loads of a row are issued together; several blocks on an SM
-// cover each other's reductions.  x and z pass L1 by, so that the weights stay there.
+// variance's digits).  Blocks that take several rows fetch x and z two rows ahead into
+// shared memory (bulk copies); otherwise a row's loads are issued together, past L1, so
+// that the weights stay there.
 // One translation unit per pair of types includes this file.
 #pragma once
 
@@ -64,6 +65,31 @@ struct RowRegs {
   }
 };
 
+// The same from a row in shared memory (VEC; columns past C read as 0).
+template <typename E, int T, int N>
+__device__ __forceinline__ void read_shared(float (&v)[N], const uint8_t* row, int t, int C) {
+#pragma unroll
+  for (int i = 0; i < N / 16; ++i) {
+    const int c = 16 * (i * T + t);
+    Raw16<E> raw;
+#pragma unroll
+    for (int k = 0; k < (int)sizeof(E); ++k) {
+      uint4 u = make_uint4(0, 0, 0, 0);
+      if (c + k * (16 / (int)sizeof(E)) < C)  // C is a multiple of 16 bytes of elements
+        u = *reinterpret_cast<const uint4*>(row + (size_t)c * sizeof(E) + 16 * k);
+      uint32_t* const w = &raw.b[k / 2].w[k % 2 * 4];
+      w[0] = u.x;
+      w[1] = u.y;
+      w[2] = u.z;
+      w[3] = u.w;
+    }
+    float e[16];
+    raw.get(e);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) v[16 * i + k] = e[k];
+  }
+}
+
 template <typename E, int T, int N, bool VEC>
 __device__ __forceinline__ void store_row(E* row, int t, int C, bool vec, const float (&v)[N]) {
   using L = Lay<T, N, VEC>;
@@ -80,180 +106,317 @@ __device__ __forceinline__ void store_row(E* row, int t, int C, bool vec, const 
   }
 }
 
-// Sum over the T threads of a row (a warp, or the block), the same in each.  red: two
-// buffers used in turn, so that one barrier a sum is enough.
-template <int T>
-__device__ __forceinline__ float row_sum(float v, float (*red)[32], int& turn) {
+// Sums over the T threads of each of R rows (a warp, or the block), the same in each
+// thread.  red: two buffers used in turn, so that one barrier a sum is enough.
+template <int T, int R>
+__device__ __forceinline__ void row_sum(float (&v)[R], float (*red)[32 * R], int& turn) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  for (int o = 16; o; o >>= 1)
+#pragma unroll
+    for (int k = 0; k < R; ++k) v[k] += __shfl_xor_sync(0xFFFFFFFFu, v[k], o);
   if constexpr (T > 32) {
     constexpr int W = T / 32;
     const int lane = threadIdx.x & 31;
-    if (lane == 0) red[turn][threadIdx.x >> 5] = v;
+#pragma unroll
+    for (int k = 0; k < R; ++k)
+      if (lane == k) red[turn][32 * k + (threadIdx.x >> 5)] = v[k];
     __syncthreads();
-    v = red[turn][lane & (W - 1)];
+#pragma unroll
+    for (int k = 0; k < R; ++k) v[k] = red[turn][32 * k + (lane & (W - 1))];
     turn ^= 1;
 #pragma unroll
-    for (int o = W / 2; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-  }
-  return v;
-}
-
-// v = v * f * w (scale and weight) or v + b, w or b a row of fp32 that stays in L1
-template <int T, int N, bool VEC, bool ADD>
-__device__ __forceinline__ void apply(float (&v)[N], float f, const float* w, int t, int C,
-                                      bool vec) {
-  using L = Lay<T, N, VEC>;
-  const uint64_t f2 = pack2(f, f);
+    for (int o = W / 2; o; o >>= 1)
 #pragma unroll
-  for (int i = 0; i < L::G; ++i) {
-    const int c = L::col(i, t);
-    if constexpr (VEC) {
-#pragma unroll
-      for (int k = 0; k < 16; k += 4) {
-        float4 e = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (vec && c + 16 <= C) {
-          e = *reinterpret_cast<const float4*>(w + c + k);
-        } else {
-          if (c + k < C) e.x = w[c + k];
-          if (c + k + 1 < C) e.y = w[c + k + 1];
-          if (c + k + 2 < C) e.z = w[c + k + 2];
-          if (c + k + 3 < C) e.w = w[c + k + 3];
-        }
-        float* const a = &v[16 * i + k];
-        if (ADD) {
-          a[0] += e.x;
-          a[1] += e.y;
-          a[2] += e.z;
-          a[3] += e.w;
-        } else {
-          unpack2(mul2(mul2(pack2(a[0], a[1]), f2), pack2(e.x, e.y)), a[0], a[1]);
-          unpack2(mul2(mul2(pack2(a[2], a[3]), f2), pack2(e.z, e.w)), a[2], a[3]);
-        }
-      }
-    } else {
-      const float e = L::has(i, t, C) ? w[c] : 0.0f;
-      v[i] = ADD ? v[i] + e : v[i] * f * e;
-    }
+      for (int k = 0; k < R; ++k) v[k] += __shfl_xor_sync(0xFFFFFFFFu, v[k], o);
   }
 }
 
-// v = norm(v) with weight and bias; elements past the row's end come and stay 0.
+// Four of the thread's elements of a row of weights or biases (fp32; 0 past the row's
+// end), from element k of its N.
 template <int T, int N, bool VEC>
-__device__ __forceinline__ void norm_row(float (&v)[N], int kind, float eps, const float* w,
-                                         const float* b, int t, int C, bool vec_w, float inv,
-                                         float (*red)[32], int& turn) {
+__device__ __forceinline__ float4 load_weights(const float* w, int k, int t, int C, bool vec) {
   using L = Lay<T, N, VEC>;
-  if (kind == CONV_NORM_LAYER) {
-    float s0 = 0.0f, s1 = 0.0f;
-#pragma unroll
-    for (int i = 0; i < N; i += 2) {
-      s0 += v[i];
-      s1 += v[i + 1];
-    }
-    const float mean = row_sum<T>(s0 + s1, red, turn) * inv;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const bool in = VEC ? L::col(i / 16, t) + i % 16 < C : L::has(i, t, C);
-      v[i] = in ? v[i] - mean : 0.0f;
-    }
-  }
-  uint64_t s = 0;
-#pragma unroll
-  for (int i = 0; i < N; i += 2) {
-    const uint64_t p = pack2(v[i], v[i + 1]);
-    s = fma2(p, p, s);
-  }
-  float s0, s1;
-  unpack2(s, s0, s1);
-  const float rstd = rsqrtf(fmaf(row_sum<T>(s0 + s1, red, turn), inv, eps));
-  if (w) {
-    apply<T, N, VEC, false>(v, rstd, w, t, C, vec_w);
+  float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if constexpr (VEC) {
+    const int c = L::col(k / 16, t) + k % 16;
+    if (vec && c + 4 <= C) return *reinterpret_cast<const float4*>(w + c);
+    if (c < C) f.x = w[c];
+    if (c + 1 < C) f.y = w[c + 1];
+    if (c + 2 < C) f.z = w[c + 2];
+    if (c + 3 < C) f.w = w[c + 3];
   } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] *= rstd;
+    if (L::has(k, t, C)) f.x = w[L::col(k, t)];
+    if (L::has(k + 1, t, C)) f.y = w[L::col(k + 1, t)];
+    if (L::has(k + 2, t, C)) f.z = w[L::col(k + 2, t)];
+    if (L::has(k + 3, t, C)) f.w = w[L::col(k + 3, t)];
   }
-  if (b) apply<T, N, VEC, true>(v, 0.0f, b, t, C, vec_w);
+  return f;
+}
+
+// v = norm(v) with weight and bias, for R rows; elements past a row's end come and stay 0.
+template <int T, int N, bool VEC, int R>
+__device__ __forceinline__ void norm_rows(float (&v)[R][N], int kind, float eps, const float* w,
+                                          const float* b, int t, int C, bool vec_w, float inv,
+                                          float (*red)[32 * R], int& turn) {
+  using L = Lay<T, N, VEC>;
+  float sum[R];
+  if (kind == CONV_NORM_LAYER) {
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+      for (int i = 0; i < N; i += 2) {
+        s0 += v[k][i];
+        s1 += v[k][i + 1];
+      }
+      sum[k] = s0 + s1;
+    }
+    row_sum<T, R>(sum, red, turn);
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      const float mean = sum[k] * inv;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const bool in = VEC ? L::col(i / 16, t) + i % 16 < C : L::has(i, t, C);
+        v[k][i] = in ? v[k][i] - mean : 0.0f;
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    uint64_t s = 0, s2 = 0;
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const uint64_t p = pack2(v[k][i], v[k][i + 1]), q = pack2(v[k][i + 2], v[k][i + 3]);
+      s = fma2(p, p, s);
+      s2 = fma2(q, q, s2);
+    }
+    float s0, s1, s3, s4;
+    unpack2(s, s0, s1);
+    unpack2(s2, s3, s4);
+    sum[k] = (s0 + s1) + (s3 + s4);
+  }
+  row_sum<T, R>(sum, red, turn);
+  uint64_t f[R];
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    const float rstd = rsqrtf(fmaf(sum[k], inv, eps));
+    f[k] = pack2(rstd, rstd);
+  }
+#pragma unroll
+  for (int i = 0; i < N; i += 4) {
+    uint64_t p[R], q[R];
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      p[k] = mul2(pack2(v[k][i], v[k][i + 1]), f[k]);
+      q[k] = mul2(pack2(v[k][i + 2], v[k][i + 3]), f[k]);
+    }
+    if (w) {
+      const float4 e = load_weights<T, N, VEC>(w, i, t, C, vec_w);
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        p[k] = mul2(p[k], pack2(e.x, e.y));
+        q[k] = mul2(q[k], pack2(e.z, e.w));
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      unpack2(p[k], v[k][i], v[k][i + 1]);
+      unpack2(q[k], v[k][i + 2], v[k][i + 3]);
+    }
+    if (b) {
+      const float4 e = load_weights<T, N, VEC>(b, i, t, C, vec_w);
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        v[k][i] += e.x;
+        v[k][i + 1] += e.y;
+        v[k][i + 2] += e.z;
+        v[k][i + 3] += e.w;
+      }
+    }
+  }
 }
 
 struct Vec {
   bool x, z, g, xo, h, w;  // 32-byte accesses to rows; 16-byte ones to weights
 };
 
-// T == 32: one row per warp (4 in a block), else one per block of T threads.
-template <typename TX, typename TZ, int T, int N, bool VEC>
-__global__ void __launch_bounds__(T < 128 && T == 32 ? 128 : T)
+constexpr int RING = 2;  // stages of R rows in shared memory
+
+// Stores h of one row.
+template <typename TZ, int T, int N, bool VEC>
+__device__ __forceinline__ void store_h(const NormArgs& a, const TensorScale& ts, const Vec& vec,
+                                        long long r, int t, const float (&v)[N]) {
+  const int C = a.C;
+  if (a.out == CONV_NORM_OUT_FLOAT) {
+    store_row<TZ, T, N, VEC>(static_cast<TZ*>(a.h) + r * a.ldh, t, C, vec.h, v);
+  } else if constexpr (VEC) {
+#pragma unroll
+    for (int i = 0; i < N / 16; ++i) {
+      const int c0 = 16 * (i * T + (t & ~31));  // the warp's first column
+      if (c0 >= C) break;
+      float e[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) e[k] = v[16 * i + k];
+      if (16 * (i * T + t) + 16 > C) {  // padding is 0 in a row of NaN too
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+          if (16 * (i * T + t) + k >= C) e[k] = 0.0f;
+      }
+      if (a.out == CONV_NORM_OUT_FP4_MX)
+        store_warp_row<CONV_FP4_MX>(e, ts, r, c0, C, static_cast<uint8_t*>(a.h), a.hs);
+      else
+        store_warp_row<CONV_FP4_NV>(e, ts, r, c0, C, static_cast<uint8_t*>(a.h), a.hs);
+    }
+  }
+}
+
+// T == 32: one row per warp (4 in a block), else R rows at a time per block of T threads.
+// AHEAD (VEC, T > 32, z given): x and z come through the ring; else R is 1.
+template <typename TX, typename TZ, int T, int N, bool VEC, bool AHEAD, int R>
+__global__ void __launch_bounds__(T == 32 ? 128 : T)
     norm_kernel(const NormArgs a, const TensorScale ts, const Vec vec) {
-  __shared__ float red[2][32];
+  static_assert(AHEAD || R == 1, "rows of a step");
+  __shared__ float red[2][32 * R];
+  __shared__ uint64_t full[RING];
+  extern __shared__ uint4 ring[];  // RING x R x (a row of z, a row of x)
   gb::allow_dependents();
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int C = a.C;
   const int t = T == 32 ? (int)(threadIdx.x & 31) : (int)threadIdx.x;
-  const long long step = T == 32 ? gridDim.x * 4LL : gridDim.x;
+  const long long step = T == 32 ? gridDim.x * 4LL : (long long)gridDim.x * R;
+  const long long first = T == 32 ? blockIdx.x * 4LL + (threadIdx.x >> 5) : (long long)blockIdx.x * R;
   const float inv = 1.0f / (float)C;
-  int turn = 0;
-  for (long long r = T == 32 ? blockIdx.x * 4LL + (threadIdx.x >> 5) : blockIdx.x; r < a.rows;
-       r += step) {
+  const uint32_t zb = (uint32_t)C * sizeof(TZ), xb = (uint32_t)C * sizeof(TX);
+  const auto fetch = [&](long long r, int stage) {  // one thread
+    uint8_t* to = reinterpret_cast<uint8_t*>(ring) + stage * (size_t)(zb + xb) * R;
+    const int rows = (int)(a.rows - r < R ? a.rows - r : R);
+    gb::mbar_arrive_expect_tx(&full[stage], (zb + xb) * rows);
+    for (int k = 0; k < rows; ++k, to += zb + xb) {
+      gb::bulk_load(to, static_cast<const TZ*>(a.z) + (r + k) * a.ldz, &full[stage], zb);
+      gb::bulk_load(to + zb, static_cast<const TX*>(a.x) + (r + k) * a.ldx, &full[stage], xb);
+    }
+  };
+  if (AHEAD && t == 0) {
+    for (int i = 0; i < RING; ++i) gb::mbar_init(&full[i], 1);
+    gb::fence_barrier_init();
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (AHEAD) {
+    if (t == 0)
+      for (int i = 0; i < RING && first + i * step < a.rows; ++i) fetch(first + i * step, i);
+    __syncthreads();
+  }
+  int turn = 0, stage = 0;
+  uint32_t phase = 0;
+  bool ok = true;  // after a wait that ran out nothing is waited for again (the rows are
+                   // then wrong, and the error word says so); the barriers stay in step
+  for (long long r = first; r < a.rows; r += step) {
     RowRegs<TX, T, N, VEC> rx;
     RowRegs<TZ, T, N, VEC> rz;
-    if (a.z) rz.load(static_cast<const TZ*>(a.z) + r * a.ldz, t, C, vec.z);
-    rx.load(static_cast<const TX*>(a.x) + r * a.ldx, t, C, vec.x);
-    float v[N];
-    if (a.z) {
-      float u[N];
-      rz.get(u);
-      if (a.gate_kind != CONV_GATE_NONE)  // in z's place
-        rz.load(static_cast<const TZ*>(a.gate) + r / a.gate_rows * a.ldg, t, C, vec.g);
-      if (a.post != CONV_NORM_NONE)
-        norm_row<T, N, VEC>(u, a.post, a.eps_post, a.w_post, a.b_post, t, C, vec.w, inv, red, turn);
-      if (a.gate_kind != CONV_GATE_NONE) {
-        rz.get(v);
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          // the logistic function within 2^-21
-          if (a.gate_kind == CONV_GATE_SIGMOID)
-            v[i] = rcp_approx(1.0f + ex2_approx(v[i] * -1.4426950408889634f));
-          u[i] *= v[i];
-        }
-      }
-      rx.get(v);
-      const uint64_t rs = pack2(a.rs, a.rs);
-#pragma unroll
-      for (int i = 0; i < N; i += 2)
-        unpack2(fma2(pack2(u[i], u[i + 1]), rs, pack2(v[i], v[i + 1])), v[i], v[i + 1]);
+    const uint8_t* const sz = reinterpret_cast<const uint8_t*>(ring) + stage * (size_t)(zb + xb) * R;
+    if constexpr (AHEAD) {
+      if (ok) ok = gb::mbar_wait_bounded(&full[stage], phase, a.wait_ns, a.err);
     } else {
-      rx.get(v);
+      if (a.z) rz.load(static_cast<const TZ*>(a.z) + r * a.ldz, t, C, vec.z);
+      rx.load(static_cast<const TX*>(a.x) + r * a.ldx, t, C, vec.x);
     }
-    if (a.x_out)
-      store_row<TX, T, N, VEC>(static_cast<TX*>(a.x_out) + r * a.ldxo, t, C, vec.xo, v);
-    if (a.pre == CONV_NORM_NONE) continue;
-    norm_row<T, N, VEC>(v, a.pre, a.eps_pre, a.w_pre, a.b_pre, t, C, vec.w, inv, red, turn);
-    if (a.out == CONV_NORM_OUT_FLOAT) {
-      store_row<TZ, T, N, VEC>(static_cast<TZ*>(a.h) + r * a.ldh, t, C, vec.h, v);
-    } else if constexpr (VEC) {
+    float v[R][N];
+    if (AHEAD || a.z) {
+      float u[R][N];
 #pragma unroll
-      for (int i = 0; i < N / 16; ++i) {
-        const int c0 = 16 * (i * T + (t & ~31));  // the warp's first column
-        if (c0 >= C) break;
-        float e[16];
-#pragma unroll
-        for (int k = 0; k < 16; ++k) e[k] = v[16 * i + k];
-        if (16 * (i * T + t) + 16 > C) {  // padding is 0 in a row of NaN too
-#pragma unroll
-          for (int k = 0; k < 16; ++k)
-            if (16 * (i * T + t) + k >= C) e[k] = 0.0f;
-        }
-        if (a.out == CONV_NORM_OUT_FP4_MX)
-          store_warp_row<CONV_FP4_MX>(e, ts, r, c0, C, static_cast<uint8_t*>(a.h), a.hs);
+      for (int k = 0; k < R; ++k) {
+        if constexpr (AHEAD)
+          read_shared<TZ, T, N>(u[k], sz + k * (zb + xb), t, C);
         else
-          store_warp_row<CONV_FP4_NV>(e, ts, r, c0, C, static_cast<uint8_t*>(a.h), a.hs);
+          rz.get(u[k]);
+      }
+      if (a.post != CONV_NORM_NONE)
+        norm_rows<T, N, VEC, R>(u, a.post, a.eps_post, a.w_post, a.b_post, t, C, vec.w, inv, red,
+                                turn);
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        if (a.gate_kind != CONV_GATE_NONE) {
+          const long long row = r + k < a.rows ? r + k : r;
+          rz.load(static_cast<const TZ*>(a.gate) + row / a.gate_rows * a.ldg, t, C, vec.g);
+          rz.get(v[k]);
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            // the logistic function within 2^-21
+            if (a.gate_kind == CONV_GATE_SIGMOID)
+              v[k][i] = rcp_approx(1.0f + ex2_approx(v[k][i] * -1.4426950408889634f));
+            u[k][i] *= v[k][i];
+          }
+        }
+        if constexpr (AHEAD)
+          read_shared<TX, T, N>(v[k], sz + k * (zb + xb) + zb, t, C);
+        else
+          rx.get(v[k]);
+        const uint64_t rs = pack2(a.rs, a.rs);
+#pragma unroll
+        for (int i = 0; i < N; i += 2)
+          unpack2(fma2(pack2(u[k][i], u[k][i + 1]), rs, pack2(v[k][i], v[k][i + 1])), v[k][i],
+                  v[k][i + 1]);
+      }
+    } else {
+      rx.get(v[0]);
+    }
+    if (a.x_out) {
+#pragma unroll
+      for (int k = 0; k < R; ++k)
+        if (r + k < a.rows)
+          store_row<TX, T, N, VEC>(static_cast<TX*>(a.x_out) + (r + k) * a.ldxo, t, C, vec.xo, v[k]);
+    }
+    if (a.pre != CONV_NORM_NONE) {
+      norm_rows<T, N, VEC, R>(v, a.pre, a.eps_pre, a.w_pre, a.b_pre, t, C, vec.w, inv, red, turn);
+#pragma unroll
+      for (int k = 0; k < R; ++k)
+        if (r + k < a.rows) store_h<TZ, T, N, VEC>(a, ts, vec, r + k, t, v[k]);
+    }
+    if constexpr (AHEAD) {
+      // every thread has read the rows before a barrier: norm_pre's, or this one
+      if (a.pre == CONV_NORM_NONE) __syncthreads();
+      if (t == 0 && ok && r + RING * step < a.rows) fetch(r + RING * step, stage);
+      if (++stage == RING) {
+        stage = 0;
+        phase ^= 1;
+      }
+    }
+  }
+  if (AHEAD && t == 0 && !ok) {
+    // copies that were on their way when a wait ran out
+    for (int i = 0; i < RING; ++i) {
+      gb::mbar_wait_bounded(&full[stage], phase, a.wait_ns, a.err);
+      if (++stage == RING) {
+        stage = 0;
+        phase ^= 1;
       }
     }
   }
 }
 
-template <typename TX, typename TZ, int T, int N, bool VEC>
-cudaError_t launch_t(const NormArgs& a, cudaStream_t st) {
+// Blocks of T threads that walk over the rows, as many as the SMs hold.
+template <typename K>
+cudaError_t launch_rows(K* kern, const NormArgs& a, const Vec& vec, int block, int rows_per_block,
+                        int smem, cudaStream_t st) {
+  const long long per_sm = gb_blocks_per_sm(reinterpret_cast<const void*>(kern), block, smem);
+  const long long most = (long long)gb_num_sms() * std::max(1LL, per_sm);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)std::min<long long>(gb_ceil_div_ll(a.rows, rows_per_block), most));
+  cfg.blockDim = dim3((unsigned)block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, tensor_scale(a.h_scale), vec);
+  if (e == cudaSuccess) gb_count_launch();
+  return e;
+}
+
+template <typename TX, typename TZ>
+Vec vec_of(const NormArgs& a) {
   const auto vec_w = [](const float* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
   Vec vec;
   vec.x = rows_vec<TX>(a.x, a.ldx, 32);
@@ -262,44 +425,53 @@ cudaError_t launch_t(const NormArgs& a, cudaStream_t st) {
   vec.xo = rows_vec<TX>(a.x_out, a.ldxo, 32);
   vec.h = rows_vec<TZ>(a.h, a.ldh, 32);
   vec.w = vec_w(a.w_post) && vec_w(a.b_post) && vec_w(a.w_pre) && vec_w(a.b_pre);
-  const int block = T == 32 ? 128 : T;
-  // as many blocks as the SMs hold: each then walks over rows
-  const long long most = (long long)gb_num_sms() * (2048 / block);
-  const long long blocks = std::min<long long>(gb_ceil_div_ll(a.rows, T == 32 ? 4 : 1), most);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)blocks);
-  cfg.blockDim = dim3((unsigned)block);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, norm_kernel<TX, TZ, T, N, VEC>, a,
-                                           tensor_scale(a.h_scale), vec);
-  if (e == cudaSuccess) gb_count_launch();
-  return e;
+  return vec;
 }
 
-// 16 columns a thread up to 4096 channels (as few dependent steps as the row allows), 32
-// above (a thread's part of the reductions is then a smaller share)
+template <typename TX, typename TZ, int T, int N, bool VEC>
+cudaError_t launch_direct(const NormArgs& a, cudaStream_t st) {
+  return launch_rows(norm_kernel<TX, TZ, T, N, VEC, false, 1>, a, vec_of<TX, TZ>(a),
+                     T == 32 ? 128 : T, T == 32 ? 4 : 1, 0, st);
+}
+
+// 16 columns a thread up to 4096 channels (as few dependent steps as a row allows), 32
+// above
 template <typename TX, typename TZ, bool VEC>
-cudaError_t launch_c(const NormArgs& a, cudaStream_t st) {
-  if (a.C <= 512) return launch_t<TX, TZ, 32, 16, VEC>(a, st);
-  if (a.C <= 1024) return launch_t<TX, TZ, 64, 16, VEC>(a, st);
-  if (a.C <= 2048) return launch_t<TX, TZ, 128, 16, VEC>(a, st);
-  if (a.C <= 4096) return launch_t<TX, TZ, 256, 16, VEC>(a, st);
-  if (a.C <= 8192) return launch_t<TX, TZ, 256, 32, VEC>(a, st);
-  if (a.C <= 16384) return launch_t<TX, TZ, 512, 32, VEC>(a, st);
-  return launch_t<TX, TZ, 1024, 32, VEC>(a, st);
+cudaError_t launch_few(const NormArgs& a, cudaStream_t st) {
+  if (a.C <= 512) return launch_direct<TX, TZ, 32, 16, VEC>(a, st);
+  if (a.C <= 1024) return launch_direct<TX, TZ, 64, 16, VEC>(a, st);
+  if (a.C <= 2048) return launch_direct<TX, TZ, 128, 16, VEC>(a, st);
+  if (a.C <= 4096) return launch_direct<TX, TZ, 256, 16, VEC>(a, st);
+  if (a.C <= 8192) return launch_direct<TX, TZ, 256, 32, VEC>(a, st);
+  if (a.C <= 16384) return launch_direct<TX, TZ, 512, 32, VEC>(a, st);
+  return launch_direct<TX, TZ, 1024, 32, VEC>(a, st);
+}
+
+template <typename TX, typename TZ, int T, int R>
+cudaError_t launch_ahead(const NormArgs& a, cudaStream_t st) {
+  auto* kern = norm_kernel<TX, TZ, T, 16, true, true, R>;
+  const int smem = RING * R * a.C * (int)(sizeof(TX) + sizeof(TZ));
+  const cudaError_t e = gb_set_smem_once(reinterpret_cast<const void*>(kern), smem);
+  if (e != cudaSuccess) return e;
+  return launch_rows(kern, a, vec_of<TX, TZ>(a), T, R, smem, st);
 }
 
 template <typename TX, typename TZ>
 cudaError_t launch(const NormArgs& a, cudaStream_t st) {
   // 16 consecutive columns a thread where that makes 32-byte loads, or codes
   const bool vec = rows_vec<TX>(a.x, a.ldx, 32) && (!a.z || rows_vec<TZ>(a.z, a.ldz, 32));
-  return vec || a.out != CONV_NORM_OUT_FLOAT ? launch_c<TX, TZ, true>(a, st)
-                                             : launch_c<TX, TZ, false>(a, st);
+  // many rows of whole 16-byte pieces: two at a time, through the ring
+  if (vec && a.z && a.C > 512 && a.C <= 8192 && a.C * sizeof(TX) % 16 == 0 &&
+      a.C * sizeof(TZ) % 16 == 0 && a.rows >= 2LL * gb_num_sms() * (8192 / a.C) * 4) {
+    // fp32 on both sides: one row at a time above 4096 channels (shared memory)
+    constexpr int BIG = sizeof(TX) + sizeof(TZ) > 6 ? 1 : 2;
+    if (a.C <= 1024) return launch_ahead<TX, TZ, 64, 2>(a, st);
+    if (a.C <= 2048) return launch_ahead<TX, TZ, 128, 2>(a, st);
+    if (a.C <= 4096) return launch_ahead<TX, TZ, 256, 2>(a, st);
+    return launch_ahead<TX, TZ, 512, BIG>(a, st);
+  }
+  return vec || a.out != CONV_NORM_OUT_FLOAT ? launch_few<TX, TZ, true>(a, st)
+                                             : launch_few<TX, TZ, false>(a, st);
 }
 
 }  // namespace norm

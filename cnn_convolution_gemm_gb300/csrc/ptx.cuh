@@ -138,6 +138,17 @@ __device__ __forceinline__ void tma_prefetch_desc(const void* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 
+// bytes (a multiple of 16, both addresses 16-byte aligned) of global memory into shared
+// memory, completion on bar.
+__device__ __forceinline__ void bulk_load(void* smem, const void* global, uint64_t* bar,
+                                          uint32_t bytes) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_u32(smem)),
+      "l"(global), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
 // 2-D tiled load: box at (c0 inner, c1 outer) into smem, completion on bar.
 __device__ __forceinline__ void tma_load_2d(void* smem, const void* map, uint64_t* bar, int c0,
                                             int c1) {
