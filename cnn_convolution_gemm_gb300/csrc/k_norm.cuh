@@ -153,11 +153,26 @@ __device__ __forceinline__ float4 load_weights(const float* w, int k, int t, int
   return f;
 }
 
+// A row of weights or biases.  Blocks that walk over many rows hold each thread's own
+// elements in shared memory, four at a time and thread by thread (a thread reads back only
+// what it wrote): beside the ring, L1 is too small for them (32768 x 8192 bf16: 35 % of
+// the weights' sectors missed, 386 us; a deeper ring was slower still).
+template <int T, int N, bool VEC>
+struct Weights {
+  const float* w;      // nullptr: none
+  const float4* held;  // nullptr: not held
+
+  __device__ __forceinline__ float4 get(int k, int t, int C, bool vec) const {
+    return held ? held[k / 4 * T + t] : load_weights<T, N, VEC>(w, k, t, C, vec);
+  }
+};
+
 // v = norm(v) with weight and bias, for R rows; elements past a row's end come and stay 0.
 template <int T, int N, bool VEC, int R>
-__device__ __forceinline__ void norm_rows(float (&v)[R][N], int kind, float eps, const float* w,
-                                          const float* b, int t, int C, bool vec_w, float inv,
-                                          float (*red)[32 * R], int& turn) {
+__device__ __forceinline__ void norm_rows(float (&v)[R][N], int kind, float eps,
+                                          const Weights<T, N, VEC>& w,
+                                          const Weights<T, N, VEC>& b, int t, int C, bool vec_w,
+                                          float inv, float (*red)[32 * R], int& turn) {
   using L = Lay<T, N, VEC>;
   float sum[R];
   if (kind == CONV_NORM_LAYER) {
@@ -184,55 +199,29 @@ __device__ __forceinline__ void norm_rows(float (&v)[R][N], int kind, float eps,
   }
 #pragma unroll
   for (int k = 0; k < R; ++k) {
-    uint64_t s = 0, s2 = 0;
+    float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
-    for (int i = 0; i < N; i += 4) {
-      const uint64_t p = pack2(v[k][i], v[k][i + 1]), q = pack2(v[k][i + 2], v[k][i + 3]);
-      s = fma2(p, p, s);
-      s2 = fma2(q, q, s2);
+    for (int i = 0; i < N; i += 2) {
+      s0 = fmaf(v[k][i], v[k][i], s0);
+      s1 = fmaf(v[k][i + 1], v[k][i + 1], s1);
     }
-    float s0, s1, s3, s4;
-    unpack2(s, s0, s1);
-    unpack2(s2, s3, s4);
-    sum[k] = (s0 + s1) + (s3 + s4);
+    sum[k] = s0 + s1;
   }
   row_sum<T, R>(sum, red, turn);
-  uint64_t f[R];
+  float f[R];
 #pragma unroll
-  for (int k = 0; k < R; ++k) {
-    const float rstd = rsqrtf(fmaf(sum[k], inv, eps));
-    f[k] = pack2(rstd, rstd);
-  }
+  for (int k = 0; k < R; ++k) f[k] = rsqrtf(fmaf(sum[k], inv, eps));
 #pragma unroll
   for (int i = 0; i < N; i += 4) {
-    uint64_t p[R], q[R];
+    float4 e = make_float4(1.0f, 1.0f, 1.0f, 1.0f), d = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (w.w) e = w.get(i, t, C, vec_w);
+    if (b.w) d = b.get(i, t, C, vec_w);
 #pragma unroll
     for (int k = 0; k < R; ++k) {
-      p[k] = mul2(pack2(v[k][i], v[k][i + 1]), f[k]);
-      q[k] = mul2(pack2(v[k][i + 2], v[k][i + 3]), f[k]);
-    }
-    if (w) {
-      const float4 e = load_weights<T, N, VEC>(w, i, t, C, vec_w);
-#pragma unroll
-      for (int k = 0; k < R; ++k) {
-        p[k] = mul2(p[k], pack2(e.x, e.y));
-        q[k] = mul2(q[k], pack2(e.z, e.w));
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < R; ++k) {
-      unpack2(p[k], v[k][i], v[k][i + 1]);
-      unpack2(q[k], v[k][i + 2], v[k][i + 3]);
-    }
-    if (b) {
-      const float4 e = load_weights<T, N, VEC>(b, i, t, C, vec_w);
-#pragma unroll
-      for (int k = 0; k < R; ++k) {
-        v[k][i] += e.x;
-        v[k][i + 1] += e.y;
-        v[k][i + 2] += e.z;
-        v[k][i + 3] += e.w;
-      }
+      v[k][i] = fmaf(v[k][i] * f[k], e.x, d.x);
+      v[k][i + 1] = fmaf(v[k][i + 1] * f[k], e.y, d.y);
+      v[k][i + 2] = fmaf(v[k][i + 2] * f[k], e.z, d.z);
+      v[k][i + 3] = fmaf(v[k][i + 3] * f[k], e.w, d.w);
     }
   }
 }
@@ -279,7 +268,7 @@ __global__ void __launch_bounds__(T == 32 ? 128 : T)
   static_assert(AHEAD || R == 1, "rows of a step");
   __shared__ float red[2][32 * R];
   __shared__ uint64_t full[RING];
-  extern __shared__ uint4 ring[];  // RING x R x (a row of z, a row of x)
+  extern __shared__ uint4 ring[];  // RING x R x (a row of z, a row of x); weights
   gb::allow_dependents();
   const int C = a.C;
   const int t = T == 32 ? (int)(threadIdx.x & 31) : (int)threadIdx.x;
@@ -296,6 +285,8 @@ __global__ void __launch_bounds__(T == 32 ? 128 : T)
       gb::bulk_load(to + zb, static_cast<const TX*>(a.x) + (r + k) * a.ldx, &full[stage], xb);
     }
   };
+  Weights<T, N, VEC> w_post{a.w_post, nullptr}, b_post{a.b_post, nullptr},
+      w_pre{a.w_pre, nullptr}, b_pre{a.b_pre, nullptr};
   if (AHEAD && t == 0) {
     for (int i = 0; i < RING; ++i) gb::mbar_init(&full[i], 1);
     gb::fence_barrier_init();
@@ -304,6 +295,20 @@ __global__ void __launch_bounds__(T == 32 ? 128 : T)
   if (AHEAD) {
     if (t == 0)
       for (int i = 0; i < RING && first + i * step < a.rows; ++i) fetch(first + i * step, i);
+    float4* to = reinterpret_cast<float4*>(reinterpret_cast<uint8_t*>(ring) +
+                                           RING * R * (size_t)(zb + xb));
+    const auto hold = [&](Weights<T, N, VEC>& w) {
+      if (!w.w) return;
+#pragma unroll
+      for (int k = 0; k < N; k += 4)
+        to[k / 4 * T + t] = load_weights<T, N, VEC>(w.w, k, t, C, vec.w);
+      w.held = to;
+      to += T * N / 4;
+    };
+    hold(w_post);
+    hold(b_post);
+    hold(w_pre);
+    hold(b_pre);
     __syncthreads();
   }
   int turn = 0, stage = 0;
@@ -331,8 +336,7 @@ __global__ void __launch_bounds__(T == 32 ? 128 : T)
           rz.get(u[k]);
       }
       if (a.post != CONV_NORM_NONE)
-        norm_rows<T, N, VEC, R>(u, a.post, a.eps_post, a.w_post, a.b_post, t, C, vec.w, inv, red,
-                                turn);
+        norm_rows<T, N, VEC, R>(u, a.post, a.eps_post, w_post, b_post, t, C, vec.w, inv, red, turn);
 #pragma unroll
       for (int k = 0; k < R; ++k) {
         if (a.gate_kind != CONV_GATE_NONE) {
@@ -351,11 +355,8 @@ __global__ void __launch_bounds__(T == 32 ? 128 : T)
           read_shared<TX, T, N>(v[k], sz + k * (zb + xb) + zb, t, C);
         else
           rx.get(v[k]);
-        const uint64_t rs = pack2(a.rs, a.rs);
 #pragma unroll
-        for (int i = 0; i < N; i += 2)
-          unpack2(fma2(pack2(u[k][i], u[k][i + 1]), rs, pack2(v[k][i], v[k][i + 1])), v[k][i],
-                  v[k][i + 1]);
+        for (int i = 0; i < N; ++i) v[k][i] = fmaf(a.rs, u[k][i], v[k][i]);
       }
     } else {
       rx.get(v[0]);
@@ -367,7 +368,7 @@ __global__ void __launch_bounds__(T == 32 ? 128 : T)
           store_row<TX, T, N, VEC>(static_cast<TX*>(a.x_out) + (r + k) * a.ldxo, t, C, vec.xo, v[k]);
     }
     if (a.pre != CONV_NORM_NONE) {
-      norm_rows<T, N, VEC, R>(v, a.pre, a.eps_pre, a.w_pre, a.b_pre, t, C, vec.w, inv, red, turn);
+      norm_rows<T, N, VEC, R>(v, a.pre, a.eps_pre, w_pre, b_pre, t, C, vec.w, inv, red, turn);
 #pragma unroll
       for (int k = 0; k < R; ++k)
         if (r + k < a.rows) store_h<TZ, T, N, VEC>(a, ts, vec, r + k, t, v[k]);
@@ -447,10 +448,19 @@ cudaError_t launch_few(const NormArgs& a, cudaStream_t st) {
   return launch_direct<TX, TZ, 1024, 32, VEC>(a, st);
 }
 
+// 0: does not fit shared memory
+template <typename TX, typename TZ, int T, int R>
+int ahead_smem(const NormArgs& a) {
+  const int n = (a.w_post != nullptr) + (a.b_post != nullptr) + (a.w_pre != nullptr) +
+                (a.b_pre != nullptr);
+  const int smem = RING * R * a.C * (int)(sizeof(TX) + sizeof(TZ)) + n * T * 64;
+  return smem <= 224 * 1024 ? smem : 0;
+}
+
 template <typename TX, typename TZ, int T, int R>
 cudaError_t launch_ahead(const NormArgs& a, cudaStream_t st) {
   auto* kern = norm_kernel<TX, TZ, T, 16, true, true, R>;
-  const int smem = RING * R * a.C * (int)(sizeof(TX) + sizeof(TZ));
+  const int smem = ahead_smem<TX, TZ, T, R>(a);
   const cudaError_t e = gb_set_smem_once(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
   return launch_rows(kern, a, vec_of<TX, TZ>(a), T, R, smem, st);
@@ -463,12 +473,14 @@ cudaError_t launch(const NormArgs& a, cudaStream_t st) {
   // many rows of whole 16-byte pieces: two at a time, through the ring
   if (vec && a.z && a.C > 512 && a.C <= 8192 && a.C * sizeof(TX) % 16 == 0 &&
       a.C * sizeof(TZ) % 16 == 0 && a.rows >= 2LL * gb_num_sms() * (8192 / a.C) * 4) {
-    // fp32 on both sides: one row at a time above 4096 channels (shared memory)
-    constexpr int BIG = sizeof(TX) + sizeof(TZ) > 6 ? 1 : 2;
     if (a.C <= 1024) return launch_ahead<TX, TZ, 64, 2>(a, st);
     if (a.C <= 2048) return launch_ahead<TX, TZ, 128, 2>(a, st);
-    if (a.C <= 4096) return launch_ahead<TX, TZ, 256, 2>(a, st);
-    return launch_ahead<TX, TZ, 512, BIG>(a, st);
+    if (a.C <= 4096) {
+      if (ahead_smem<TX, TZ, 256, 2>(a)) return launch_ahead<TX, TZ, 256, 2>(a, st);
+    } else {
+      if (ahead_smem<TX, TZ, 512, 2>(a)) return launch_ahead<TX, TZ, 512, 2>(a, st);
+      if (ahead_smem<TX, TZ, 512, 1>(a)) return launch_ahead<TX, TZ, 512, 1>(a, st);
+    }
   }
   return vec || a.out != CONV_NORM_OUT_FLOAT ? launch_few<TX, TZ, true>(a, st)
                                              : launch_few<TX, TZ, false>(a, st);
