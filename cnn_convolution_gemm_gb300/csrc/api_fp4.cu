@@ -175,9 +175,10 @@ extern "C" conv_status_t conv_fp4_set_strides(conv_fp4_t d, long long ldx, long 
   return gb_ok();
 }
 
-// workspace: codes of a float x, then its scales
+// workspace: codes of a float x, then its scales; none where the product quantises
 static size_t fp4_workspace(const gbconv_fp4_s& d, int M) {
-  return d.x_io == CONV_FP4_IO_CODES ? 0 : code_bytes(M, d.C) + scale_bytes(d.fmt, M, d.C);
+  if (d.x_io == CONV_FP4_IO_CODES || M <= FUSED_ROWS) return 0;
+  return code_bytes(M, d.C) + scale_bytes(d.fmt, M, d.C);
 }
 
 extern "C" conv_status_t conv_fp4_workspace_size(conv_fp4_t d, int M, size_t* bytes) {
@@ -231,7 +232,12 @@ extern "C" conv_status_t conv_fp4_fwd(conv_fp4_t d, int M, const void* x, const 
   g.ldy = d->ldy;
   g.y = y;
   g.ys = static_cast<uint8_t*>(y_scales);
-  if (xc) {
+  g.x_scale = d->x_scale;
+  if (!xc && M <= FUSED_ROWS) {
+    g.xf = x;
+    g.x_io = d->x_io;
+    g.ldx = d->ldx;
+  } else if (xc) {
     g.x = static_cast<const uint8_t*>(x);
     g.xs = static_cast<const uint8_t*>(x_scales);
   } else {
@@ -243,7 +249,8 @@ extern "C" conv_status_t conv_fp4_fwd(conv_fp4_t d, int M, const void* x, const 
     g.x = codes;
     g.xs = scales;
   }
-  return cuda_status(launch_fp4_gemm(g, st), "4-bit product");
+  return cuda_status(M <= FEW_ROWS ? launch_fp4_few(g, st) : launch_fp4_gemm(g, st),
+                     "4-bit product");
 }
 
 // ---------------------------------------------------------------------------

@@ -201,15 +201,12 @@ __device__ __forceinline__ float scale_value(uint32_t byte, float tensor_scale) 
   return __fmul_rn(from_e4m3(byte), tensor_scale);
 }
 
-// One warp turns 512 consecutive columns of a row, 16 to a lane (v; zero past the last
-// column), into codes and scales.  c0: the warp's first column.  All lanes call it.
-// MX: two lanes share a block and eight a scale tile; NV: one and four.
+// A lane's 16 consecutive elements of a row: their codes, and the scale word of their
+// tile (complete in each of the tile's lanes).  MX: two lanes share a block and eight a
+// scale tile; NV: one and four; all lanes call it.
 template <int FMT>
-__device__ __forceinline__ void store_warp_row(const float (&v)[16], const TensorScale& ts,
-                                               long long r, int c0, int cols,
-                                               uint8_t* __restrict__ codes,
-                                               uint8_t* __restrict__ scales) {
-  const int lane = threadIdx.x & 31;
+__device__ __forceinline__ void quantize16(const float (&v)[16], const TensorScale& ts, uint2& codes,
+                                           uint32_t& word) {
   constexpr int LB = kBlock<FMT> / 16;  // lanes per block
   float top = 0.0f;
 #pragma unroll
@@ -222,15 +219,28 @@ __device__ __forceinline__ void store_warp_row(const float (&v)[16], const Tenso
     lo[i] = v[i];
     hi[i] = v[8 + i];
   }
-  const uint2 packed = make_uint2(s.codes(lo), s.codes(hi));
-  uint32_t word = s.byte << (8 * ((lane / LB) & 3));
+  codes = make_uint2(s.codes(lo), s.codes(hi));
+  word = s.byte << (8 * (((threadIdx.x & 31) / LB) & 3));
   word |= __shfl_xor_sync(0xFFFFFFFFu, word, LB);
   word |= __shfl_xor_sync(0xFFFFFFFFu, word, 2 * LB);
+}
+
+// One warp turns 512 consecutive columns of a row, 16 to a lane (v; zero past the last
+// column), into codes and scales.  c0: the warp's first column.  All lanes call it.
+template <int FMT>
+__device__ __forceinline__ void store_warp_row(const float (&v)[16], const TensorScale& ts,
+                                               long long r, int c0, int cols,
+                                               uint8_t* __restrict__ codes,
+                                               uint8_t* __restrict__ scales) {
+  const int lane = threadIdx.x & 31;
+  uint2 packed;
+  uint32_t word;
+  quantize16<FMT>(v, ts, packed, word);
   const int c = c0 + lane * 16;
   const long long pitch = code_pitch(cols);
   if (c < 2 * pitch) *reinterpret_cast<uint2*>(codes + r * pitch + c / 2) = packed;
   const int tiles = tiles_per_row(FMT, cols), tj = c / (4 * kBlock<FMT>);
-  if (lane % (4 * LB) == 0 && tj < tiles)
+  if (c % (4 * kBlock<FMT>) == 0 && tj < tiles)
     *reinterpret_cast<uint32_t*>(scales + scale_word_offset(r, tj, tiles)) = word;
 }
 

@@ -281,7 +281,10 @@ cudaError_t launch_fp4_pack_scales(int fmt, int rows, int cols, const void* src,
 struct Fp4Gemm {
   int fmt, M, C, K, act, y_io;
   const uint8_t *x, *xs, *w, *ws;  // codes and tiled scales
-  float alpha, y_scale;
+  const void* xf;                  // floating x of type x_io (launch_fp4_few), else nullptr
+  int x_io;
+  long long ldx;
+  float alpha, x_scale, y_scale;
   const float* bias;
   const void* res;  // of y's type
   long long ldr, ldy;
@@ -289,6 +292,9 @@ struct Fp4Gemm {
   uint8_t* ys;
 };
 cudaError_t launch_fp4_gemm(const Fp4Gemm& g, cudaStream_t st);
+// Up to FEW_ROWS rows; up to FUSED_ROWS of them floating (xf), quantised on the way in.
+constexpr int FEW_ROWS = 128, FUSED_ROWS = 16;
+cudaError_t launch_fp4_few(const Fp4Gemm& g, cudaStream_t st);
 
 // ---- norms around a residual block ----------------------------------------------
 

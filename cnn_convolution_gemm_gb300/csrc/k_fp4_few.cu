@@ -1,0 +1,416 @@
+// Product of microscaled 4-bit matrices for few rows of X (one token to a small batch):
+// y^T = W X^T, so that the tensor core's 128 rows are outputs and its N the few rows.
+//
+// Bound by the weights' bytes and by latency: a CTA streams 128 rows of W over a range of
+// the reduction; the ranges of one tile are the CTAs of a cluster (up to 8), which
+// add their partial sums through distributed shared memory in a fixed order.  Up to
+// FUSED_ROWS rows of floating x are quantised on the way in, k-step by k-step, by
+// the warps that later run the epilogue: one launch and no workspace.
+//
+// Warp 0 loads (TMA), warp 1 copies block scales and issues the MMAs (one elected lane),
+// warps 4..7 quantise and run the epilogue.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "fp4.cuh"
+#include "fp4_gemm.cuh"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace {
+using namespace gb::fp4;
+
+constexpr int THREADS = 256;
+constexpr int STAGES = 4;
+constexpr int TMEM_COLS = 256;  // up to 128 of accumulator, 4 x 32 of scales
+
+template <int FMT>
+struct Cfg {
+  static constexpr int ATOMS = FMT == CONV_FP4_MX ? 2 : 4;
+  static constexpr int W_BYTES = 128 * BKB;
+  static constexpr int SF_BYTES = ATOMS * 512;
+  static constexpr int SF_COLS = ATOMS * 8;  // of W, then of X
+  static constexpr int stage_bytes(int nt) { return W_BYTES + nt * BKB + 2 * SF_BYTES; }
+  // ring, partial sums of the cluster, barriers, alignment
+  static int smem(int nt, int split) {
+    return STAGES * stage_bytes(nt) + (split > 1 ? 128 * 4 * nt : 0) + 256 + 1024;
+  }
+};
+
+struct FewParams {
+  int M, N, KR, nt;      // rows, outputs, reduction; rows rounded up to 8
+  int ksteps, kmmas_last;
+  int split;             // CTAs of a cluster
+  int act;
+  float alpha;
+  TensorScale x_scale, y_scale;
+  const float* bias;
+  const void *x, *res;   // x: floating x of the fused kernels
+  int vec_x;
+  void* y;
+  uint8_t* ys;
+  long long ldx, ldr, ldy;
+  int* err;
+  unsigned long long wait_ns;
+};
+
+// An output of row m: lanes of a warp are 32 consecutive outputs.
+template <int FMT, int YIO>
+__device__ __forceinline__ void finish(const FewParams& p, float acc, int m, int n, float bias) {
+  const bool live = n < p.N;
+  float v[1] = {fmaf(acc, p.alpha, bias)};
+  if constexpr (YIO != CONV_FP4_IO_CODES) {
+    using T = std::conditional_t<YIO == CONV_FP4_IO_BF16, __nv_bfloat16, float>;
+    if (!live) return;
+    if (p.res) v[0] += load_f32(static_cast<const T*>(p.res) + m * p.ldr + n);
+    activate(v, p.act);
+    store_f32(static_cast<T*>(p.y) + m * p.ldy + n, v[0]);
+  } else {
+    activate(v, p.act);
+    if (!live) v[0] = 0.0f;
+    const int lane = threadIdx.x & 31;
+    constexpr int B = kBlock<FMT>;
+    float top = fabsf(v[0]);
+#pragma unroll
+    for (int o = 1; o < B; o <<= 1) top = max_abs(top, top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    const BlockScale<FMT> s(top, p.y_scale);
+    // eight lanes' codes in each of them
+    float e[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) e[k] = __shfl_sync(0xFFFFFFFFu, v[0], (lane & 24) + k);
+    const uint32_t code = s.codes(e);
+    const int n0 = n - lane, b = n / B, tiles = tiles_per_row(FMT, p.N);
+    if ((lane & 7) == 0 && n0 < p.N)
+      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.y) + m * code_pitch(p.N) + n / 2) = code;
+    if (lane % B == 0 && (b >> 2) < tiles)
+      p.ys[scale_word_offset(m, b >> 2, tiles) + (b & 3)] = (uint8_t)s.byte;
+  }
+}
+
+// XIO: CONV_FP4_IO_CODES (tm_x, tm_xs) or the type of a floating x (M <= FUSED_ROWS).
+template <int FMT, int XIO, int YIO>
+__global__ void __launch_bounds__(THREADS)
+    fp4_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_ws,
+                   const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_xs,
+                   const FewParams p) {
+  using C = Cfg<FMT>;
+  constexpr bool MX = FMT == CONV_FP4_MX;
+  constexpr bool FUSED = XIO != CONV_FP4_IO_CODES;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int x_bytes = p.nt * BKB;
+  uint8_t* const sW = smem;
+  uint8_t* const sX = sW + STAGES * C::W_BYTES;
+  uint8_t* const sFW = sX + STAGES * x_bytes;
+  uint8_t* const sFX = sFW + STAGES * C::SF_BYTES;
+  float* const part = reinterpret_cast<float*>(sFX + STAGES * C::SF_BYTES);
+  uint64_t* const full =
+      reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(part) + (p.split > 1 ? 512 * p.nt : 0));
+  uint64_t* const empty = full + STAGES;
+  uint64_t* const tfull = empty + STAGES;
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(tfull + 1);
+
+  const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0);  // uniform
+  const int lane = threadIdx.x & 31;
+  const int rank = blockIdx.x % p.split, tile = blockIdx.x / p.split;
+  // this CTA's k-steps
+  const int k0 = (int)((long long)p.ksteps * rank / p.split);
+  const int k1 = (int)((long long)p.ksteps * (rank + 1) / p.split);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      gb::mbar_init(&full[s], FUSED ? 1 + 4 : 1);  // the loads, and the quantising warps
+      gb::mbar_init(&empty[s], 1);
+    }
+    gb::mbar_init(tfull, 1);
+    gb::fence_barrier_init();
+    gb::tma_prefetch_desc(&tm_w);
+    gb::tma_prefetch_desc(&tm_ws);
+    if (!FUSED) {
+      gb::tma_prefetch_desc(&tm_x);
+      gb::tma_prefetch_desc(&tm_xs);
+    }
+  }
+  if (warp == 0) {
+    gb::tmem_alloc(tmem_slot, TMEM_COLS);
+    gb::tmem_relinquish();
+  }
+  gb::tc_fence_before();
+  __syncthreads();
+  if (p.split > 1) gb::cluster_sync();  // every CTA runs before another stores into it
+  gb::tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
+  gb::allow_dependents();
+
+  if (warp == 0) {
+    // ---------------- TMA producer ----------------
+    const bool one = gb::elect_one();
+    int stage = 0;
+    uint32_t phase = 0;
+    int issued = 0;
+    const uint32_t tx = C::W_BYTES + C::SF_BYTES + (FUSED ? 0 : x_bytes + C::SF_BYTES);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (int it = k0; it < k1; ++it) {
+      if (!gb::mbar_wait_bounded_warp<false>(&empty[stage], phase ^ 1, p.wait_ns, p.err)) break;
+      if (one) {
+        const int sc = it * (C::ATOMS * 64);  // scale tiles as 8-byte elements
+        gb::mbar_arrive_expect_tx(&full[stage], tx);
+        gb::tma_load_2d(sW + stage * C::W_BYTES, &tm_w, &full[stage], it * BKB, tile * 128);
+        gb::tma_load_2d(sFW + stage * C::SF_BYTES, &tm_ws, &full[stage], sc, tile);
+        if (!FUSED) {
+          gb::tma_load_2d(sX + stage * x_bytes, &tm_x, &full[stage], it * BKB, 0);
+          gb::tma_load_2d(sFX + stage * C::SF_BYTES, &tm_xs, &full[stage], sc, 0);
+        }
+      }
+      __syncwarp();
+      ++issued;
+      if (++stage == STAGES) {
+        stage = 0;
+        phase ^= 1;
+      }
+    }
+    // no copy into shared memory may be in flight at exit
+    for (int i = issued < STAGES ? issued : STAGES; i > 0; --i) {
+      if (--stage < 0) {
+        stage = STAGES - 1;
+        phase ^= 1;
+      }
+      gb::mbar_wait_bounded_warp<false>(&full[stage], phase, p.wait_ns, p.err);
+    }
+  } else if (warp == 1) {
+    // ---------------- scale copies and MMAs ----------------
+    const bool one = gb::elect_one();
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int it = k0; it < k1; ++it) {
+      if (!gb::mbar_wait_bounded_warp<false>(&full[stage], phase, p.wait_ns, p.err)) break;
+      gb::tc_fence_after();
+      if (one) {
+        const uint64_t wd = gb::sw128_kmajor_desc(gb::smem_u32(sW + stage * C::W_BYTES));
+        const uint64_t xd = gb::sw128_kmajor_desc(gb::smem_u32(sX + stage * x_bytes));
+        const uint32_t fw = gb::smem_u32(sFW + stage * C::SF_BYTES);
+        const uint32_t fx = gb::smem_u32(sFX + stage * C::SF_BYTES);
+        const uint32_t sfw = tmem + 128 + stage * C::SF_COLS, sfx = sfw + C::ATOMS * 4;
+#pragma unroll
+        for (int j = 0; j < C::ATOMS; ++j) {
+          gb::tc_copy_scales<false>(sfw + 4 * j, gb::noswz_kmajor_desc(fw + j * 512, 128, 128));
+          gb::tc_copy_scales<false>(sfx + 4 * j, gb::noswz_kmajor_desc(fx + j * 512, 128, 128));
+        }
+        const int mmas = it + 1 < p.ksteps ? 4 : p.kmmas_last;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int j = MX ? k / 2 : k;
+          const uint32_t id = gb::idesc_fp4(128, p.nt, MX, MX ? (k & 1) * 2 : 0);
+          if (k < mmas)
+            gb::tc_mma_fp4<MX, false>(tmem, wd + k * 2, xd + k * 2, id, sfw + 4 * j, sfx + 4 * j,
+                                      it > k0 || k > 0 ? 1u : 0u);
+        }
+        gb::tc_commit(&empty[stage]);
+      }
+      __syncwarp();
+      if (++stage == STAGES) {
+        stage = 0;
+        phase ^= 1;
+      }
+    }
+    if (one) gb::tc_commit(tfull);
+    __syncwarp();
+    gb::mbar_wait_bounded_warp<false>(tfull, 0, p.wait_ns, p.err);
+  } else if (warp >= 4) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if constexpr (FUSED) {
+      // ---------------- quantise x ----------------
+      // 16 columns to a lane: a half-warp takes a row's 256 columns, the four warps eight
+      // rows at a time.  The next k-step's loads go out before this one's arithmetic.
+      using T = std::conditional_t<XIO == CONV_FP4_IO_BF16, __nv_bfloat16, float>;
+      constexpr int PASSES = FUSED_ROWS / 8;
+      const int row0 = (warp - 4) * 2 + (lane >> 4), gc = lane & 15;
+      const T* const x = static_cast<const T*>(p.x);
+      Raw16<T> raw[PASSES];
+      const auto load = [&](int it) {
+#pragma unroll
+        for (int i = 0; i < PASSES; ++i)
+          if (row0 + 8 * i < p.M)
+            raw[i].load(x + (row0 + 8 * i) * p.ldx, it * 256 + gc * 16, p.KR, p.vec_x);
+      };
+      int stage = 0;
+      uint32_t phase = 0;
+      if (k0 < k1) load(k0);
+      for (int it = k0; it < k1; ++it) {
+        Raw16<T> now[PASSES];
+#pragma unroll
+        for (int i = 0; i < PASSES; ++i) now[i] = raw[i];
+        if (it + 1 < k1) load(it + 1);
+        if (!gb::mbar_wait_bounded_warp<false>(&empty[stage], phase ^ 1, p.wait_ns, p.err)) break;
+#pragma unroll
+        for (int i = 0; i < PASSES; ++i) {
+          const int r = row0 + 8 * i;
+          if ((warp - 4) * 2 + 8 * i >= p.M) break;  // the warp's rows are past the last
+          float v[16];
+          now[i].get(v);
+          if (r >= p.M) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) v[k] = 0.0f;
+          }
+          uint2 code;
+          uint32_t word;
+          quantize16<FMT>(v, p.x_scale, code, word);
+          // row r of a 128-byte-swizzled tile; its scale words in tiles of 512 bytes
+          *reinterpret_cast<uint2*>(sX + stage * x_bytes + r * BKB +
+                                    (((gc >> 1) ^ (r & 7)) << 4) + (gc & 1) * 8) = code;
+          constexpr int LT = 4 * kBlock<FMT> / 16;  // lanes of a scale tile
+          if (gc % LT == 0)
+            *reinterpret_cast<uint32_t*>(sFX + stage * C::SF_BYTES + gc / LT * 512 + r * 16) = word;
+        }
+        gb::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) gb::mbar_arrive(&full[stage]);
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+    }
+    // ---------------- accumulators: to the epilogue, or to the cluster ----------------
+    gb::mbar_wait_bounded_warp<false>(tfull, 0, p.wait_ns, p.err);
+    gb::tc_fence_after();
+    const uint32_t t = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const int o = (warp & 3) * 32 + lane, n = tile * 128 + o;
+    if (p.split == 1) {
+      const float bias = p.bias && n < p.N ? p.bias[n] : 0.0f;
+      for (int c = 0; c < p.M; c += 8) {
+        uint32_t r[8];
+        gb::tmem_ld_x8(t + c, r);
+        gb::tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (c + i < p.M) finish<FMT, YIO>(p, __uint_as_float(r[i]), c + i, n, bias);
+      }
+    } else {
+      // row m goes to CTA m % split, place m / split; source rank, place, output
+      const uint32_t mine = gb::smem_u32(part) + 4 * o;
+      const int places = (p.M + p.split - 1) / p.split;
+      for (int c = 0; c < p.M; c += 8) {
+        uint32_t r[8];
+        gb::tmem_ld_x8(t + c, r);
+        gb::tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int m = c + i;
+          if (m < p.M)
+            gb::store_cluster(gb::mapa_shared(mine + 512 * (rank * places + m / p.split),
+                                              (uint32_t)(m % p.split)),
+                              k0 < k1 ? r[i] : 0u);
+        }
+      }
+    }
+    gb::tc_fence_before();
+  }
+  __syncthreads();
+  if (p.split > 1) {
+    gb::cluster_sync();
+    if (warp >= 4) {
+      const int o = (warp & 3) * 32 + lane, n = tile * 128 + o;
+      const float bias = p.bias && n < p.N ? p.bias[n] : 0.0f;
+      const int places = (p.M + p.split - 1) / p.split;
+      for (int m = rank, i = 0; m < p.M; m += p.split, ++i) {
+        float s = 0.0f;
+        for (int r = 0; r < p.split; ++r) s += part[128 * (r * places + i) + o];
+        finish<FMT, YIO>(p, s, m, n, bias);
+      }
+    }
+  }
+  if (warp == 0) {
+    gb::tc_fence_after();
+    gb::tmem_dealloc(tmem, TMEM_COLS);
+  }
+}
+
+template <int FMT, int XIO, int YIO>
+cudaError_t launch_t(const Fp4Gemm& g, cudaStream_t st) {
+  using C = Cfg<FMT>;
+  constexpr bool FUSED = XIO != CONV_FP4_IO_CODES;
+  FewParams p{};
+  p.M = g.M;
+  p.N = g.K;
+  p.KR = g.C;
+  p.nt = gb_ceil_div(g.M, 8) * 8;
+  p.ksteps = gb_ceil_div(g.C, 256);
+  p.kmmas_last = gb_ceil_div(g.C - (p.ksteps - 1) * 256, 64);
+  p.act = g.act;
+  p.alpha = g.alpha;
+  p.x_scale = tensor_scale(g.x_scale);
+  p.y_scale = tensor_scale(g.y_scale);
+  p.bias = g.bias;
+  p.x = g.xf;
+  p.res = g.res;
+  p.y = g.y;
+  p.ys = g.ys;
+  p.ldx = g.ldx;
+  p.ldr = g.ldr;
+  p.ldy = g.ldy;
+  p.vec_x = XIO == CONV_FP4_IO_BF16 ? rows_vec<__nv_bfloat16>(g.xf, g.ldx, 32)
+                                    : rows_vec<float>(g.xf, g.ldx, 32);
+  p.err = gb_device_error_word();
+  p.wait_ns = gb_wait_limit_ns();
+  // split the reduction while the tiles leave SMs idle and each CTA keeps two k-steps
+  const int tiles = gb_ceil_div(g.K, 128);
+  p.split = 1;
+  while (p.split < 8 && tiles * p.split * 2 <= gb_num_sms() && p.ksteps >= p.split * 4) p.split *= 2;
+  CUtensorMap tw, tws, tx, txs;
+  if (!codes_map(&tw, g.w, g.K, g.C, 128) ||
+      !scales_map(&tws, g.ws, FMT, g.K, g.C, C::ATOMS, 1))
+    return cudaErrorInvalidValue;
+  if (FUSED) {
+    tx = tw;
+    txs = tws;
+  } else if (!codes_map(&tx, g.x, g.M, g.C, p.nt) ||
+             !scales_map(&txs, g.xs, FMT, g.M, g.C, C::ATOMS, 1)) {
+    return cudaErrorInvalidValue;
+  }
+  auto* kern = fp4_few_kernel<FMT, XIO, YIO>;
+  const int smem = C::smem(p.nt, p.split);
+  cudaError_t e = gb_set_smem_once(reinterpret_cast<const void*>(kern), smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tiles * p.split));
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = p.split;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, kern, tw, tws, tx, txs, p);
+  if (e == cudaSuccess) gb_count_launch();
+  return e;
+}
+
+template <int FMT, int YIO>
+cudaError_t launch_x(const Fp4Gemm& g, cudaStream_t st) {
+  if (!g.xf) return launch_t<FMT, CONV_FP4_IO_CODES, YIO>(g, st);
+  return g.x_io == CONV_FP4_IO_BF16 ? launch_t<FMT, CONV_FP4_IO_BF16, YIO>(g, st)
+                                    : launch_t<FMT, CONV_FP4_IO_F32, YIO>(g, st);
+}
+
+template <int FMT>
+cudaError_t launch_fmt(const Fp4Gemm& g, cudaStream_t st) {
+  if (g.y_io == CONV_FP4_IO_BF16) return launch_x<FMT, CONV_FP4_IO_BF16>(g, st);
+  if (g.y_io == CONV_FP4_IO_F32) return launch_x<FMT, CONV_FP4_IO_F32>(g, st);
+  return launch_x<FMT, CONV_FP4_IO_CODES>(g, st);
+}
+
+}  // namespace
+
+cudaError_t launch_fp4_few(const Fp4Gemm& g, cudaStream_t st) {
+  return g.fmt == CONV_FP4_MX ? launch_fmt<CONV_FP4_MX>(g, st) : launch_fmt<CONV_FP4_NV>(g, st);
+}

@@ -12,6 +12,7 @@
 #include <type_traits>
 
 #include "fp4.cuh"
+#include "fp4_gemm.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -19,7 +20,6 @@ namespace {
 using namespace gb::fp4;
 
 constexpr int BM = 128;
-constexpr int BKB = 128;  // bytes of a row per k-step: 256 codes
 
 template <int FMT, int BN, bool PAIR, int YIO>
 struct Cfg {
@@ -505,27 +505,6 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR, YIO>::THREADS, 1)
     else
       gb::tmem_dealloc(tmem, 512);
   }
-}
-
-// [rows][pitch] bytes of codes in boxes of 128 bytes x box_rows
-bool codes_map(CUtensorMap* map, const uint8_t* p, int rows, int cols, int box_rows) {
-  cuuint64_t dims[2] = {(cuuint64_t)code_pitch(cols), (cuuint64_t)rows};
-  cuuint64_t strides[1] = {(cuuint64_t)code_pitch(cols)};
-  cuuint32_t box[2] = {BKB, (cuuint32_t)box_rows};
-  cuuint32_t estr[2] = {1, 1};
-  return gb_encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(p), dims,
-                         strides, box, estr, CU_TENSOR_MAP_SWIZZLE_128B) == CUDA_SUCCESS;
-}
-// scale tiles as [panels][tiles * 64] 8-byte elements, boxes of `atoms` tiles x `panels`
-bool scales_map(CUtensorMap* map, const uint8_t* p, int fmt, int rows, int cols, int atoms,
-                int box_panels) {
-  const cuuint64_t w = (cuuint64_t)tiles_per_row(fmt, cols) * 64;
-  cuuint64_t dims[2] = {w, (cuuint64_t)((rows + 127LL) / 128)};
-  cuuint64_t strides[1] = {w * 8};
-  cuuint32_t box[2] = {(cuuint32_t)(atoms * 64), (cuuint32_t)box_panels};
-  cuuint32_t estr[2] = {1, 1};
-  return gb_encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_UINT64, 2, const_cast<uint8_t*>(p), dims,
-                         strides, box, estr, CU_TENSOR_MAP_SWIZZLE_NONE) == CUDA_SUCCESS;
 }
 
 template <int FMT, int BN, bool PAIR, int YIO>

@@ -267,6 +267,11 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster) {
                : "memory");
 }
 
+// A 32-bit store to the shared memory of a CTA of the cluster (shared::cluster address).
+__device__ __forceinline__ void store_cluster(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
 // TMA loads into this CTA's shared memory whose completion is signalled on an
 // mbarrier of either CTA of the pair (bar_cluster: a shared::cluster address).
 __device__ __forceinline__ void tma_load_2d_pair(void* smem, const void* map, uint32_t bar_cluster,
