@@ -43,7 +43,8 @@ struct Cfg {
 struct FewParams {
   int M, N, KR, nt;      // rows, outputs, reduction; rows rounded up to 8
   int ksteps, kmmas_last;
-  int split;             // CTAs of a cluster
+  int split_log2;        // CTAs of a cluster
+  int warps_log2;        // FUSED: warps that quantise a k-step, two rows each
   int act;
   float alpha;
   TensorScale x_scale, y_scale;
@@ -57,36 +58,53 @@ struct FewParams {
   unsigned long long wait_ns;
 };
 
-// An output of row m: lanes of a warp are 32 consecutive outputs.
+// Output n of rows m, m + step, .. (rows of them); lanes of a warp are 32 consecutive
+// outputs.
 template <int FMT, int YIO>
-__device__ __forceinline__ void finish(const FewParams& p, float acc, int m, int n, float bias) {
+__device__ __forceinline__ void finish(const FewParams& p, float (&v)[8], int m, int step, int rows,
+                                       int n, float bias) {
   const bool live = n < p.N;
-  float v[1] = {fmaf(acc, p.alpha, bias)};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = fmaf(v[i], p.alpha, bias);
   if constexpr (YIO != CONV_FP4_IO_CODES) {
     using T = std::conditional_t<YIO == CONV_FP4_IO_BF16, __nv_bfloat16, float>;
     if (!live) return;
-    if (p.res) v[0] += load_f32(static_cast<const T*>(p.res) + m * p.ldr + n);
+    if (p.res) {
+      const T* const res = static_cast<const T*>(p.res) + m * p.ldr + n;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < rows) v[i] += load_f32(res + i * step * p.ldr);
+    }
     activate(v, p.act);
-    store_f32(static_cast<T*>(p.y) + m * p.ldy + n, v[0]);
+    T* const y = static_cast<T*>(p.y) + m * p.ldy + n;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < rows) store_f32(y + i * step * p.ldy, v[i]);
   } else {
     activate(v, p.act);
-    if (!live) v[0] = 0.0f;
     const int lane = threadIdx.x & 31;
     constexpr int B = kBlock<FMT>;
-    float top = fabsf(v[0]);
-#pragma unroll
-    for (int o = 1; o < B; o <<= 1) top = max_abs(top, top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    const BlockScale<FMT> s(top, p.y_scale);
-    // eight lanes' codes in each of them
-    float e[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) e[k] = __shfl_sync(0xFFFFFFFFu, v[0], (lane & 24) + k);
-    const uint32_t code = s.codes(e);
     const int n0 = n - lane, b = n / B, tiles = tiles_per_row(FMT, p.N);
-    if ((lane & 7) == 0 && n0 < p.N)
-      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.y) + m * code_pitch(p.N) + n / 2) = code;
-    if (lane % B == 0 && (b >> 2) < tiles)
-      p.ys[scale_word_offset(m, b >> 2, tiles) + (b & 3)] = (uint8_t)s.byte;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (i >= rows) break;
+      const long long row = m + i * step;
+      if (!live) v[i] = 0.0f;
+      float top = fabsf(v[i]);
+#pragma unroll
+      for (int o = 1; o < B; o <<= 1) top = max_abs(top, top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+      const BlockScale<FMT> s(top, p.y_scale);
+      // eight lanes' values in each of them
+      float e[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) e[k] = __shfl_sync(0xFFFFFFFFu, v[i], (lane & 24) + k);
+      const uint32_t code = s.codes(e);
+      if ((lane & 7) == 0 && n0 < p.N)
+        *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.y) + row * code_pitch(p.N) + n / 2) =
+            code;
+      if (lane % B == 0 && (b >> 2) < tiles)
+        p.ys[scale_word_offset(row, b >> 2, tiles) + (b & 3)] = (uint8_t)s.byte;
+    }
   }
 }
 
@@ -103,27 +121,28 @@ __global__ void __launch_bounds__(THREADS)
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int x_bytes = p.nt * BKB;
+  const int split = 1 << p.split_log2;
   uint8_t* const sW = smem;
   uint8_t* const sX = sW + STAGES * C::W_BYTES;
   uint8_t* const sFW = sX + STAGES * x_bytes;
   uint8_t* const sFX = sFW + STAGES * C::SF_BYTES;
   float* const part = reinterpret_cast<float*>(sFX + STAGES * C::SF_BYTES);
   uint64_t* const full =
-      reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(part) + (p.split > 1 ? 512 * p.nt : 0));
+      reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(part) + (split > 1 ? 512 * p.nt : 0));
   uint64_t* const empty = full + STAGES;
   uint64_t* const tfull = empty + STAGES;
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(tfull + 1);
 
   const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0);  // uniform
   const int lane = threadIdx.x & 31;
-  const int rank = blockIdx.x % p.split, tile = blockIdx.x / p.split;
+  const int rank = blockIdx.x & (split - 1), tile = blockIdx.x >> p.split_log2;
   // this CTA's k-steps
-  const int k0 = (int)((long long)p.ksteps * rank / p.split);
-  const int k1 = (int)((long long)p.ksteps * (rank + 1) / p.split);
+  const int k0 = (int)((long long)p.ksteps * rank >> p.split_log2);
+  const int k1 = (int)((long long)p.ksteps * (rank + 1) >> p.split_log2);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      gb::mbar_init(&full[s], FUSED ? 1 + 4 : 1);  // the loads, and the quantising warps
+      gb::mbar_init(&full[s], FUSED ? 1 + (1 << p.warps_log2) : 1);  // the loads, the quantising warps
       gb::mbar_init(&empty[s], 1);
     }
     gb::mbar_init(tfull, 1);
@@ -141,7 +160,7 @@ __global__ void __launch_bounds__(THREADS)
   }
   gb::tc_fence_before();
   __syncthreads();
-  if (p.split > 1) gb::cluster_sync();  // every CTA runs before another stores into it
+  if (split > 1) gb::cluster_sync();  // every CTA runs before another stores into it
   gb::tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
   gb::allow_dependents();
@@ -224,41 +243,29 @@ __global__ void __launch_bounds__(THREADS)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if constexpr (FUSED) {
       // ---------------- quantise x ----------------
-      // 16 columns to a lane: a half-warp takes a row's 256 columns, the four warps eight
-      // rows at a time.  The next k-step's loads go out before this one's arithmetic.
+      // 16 columns to a lane: a half-warp takes a row's 256 columns of a k-step, a warp two
+      // rows; warps that are left over take other k-steps.  The next k-step's loads go out
+      // before this one's arithmetic.
       using T = std::conditional_t<XIO == CONV_FP4_IO_BF16, __nv_bfloat16, float>;
-      constexpr int PASSES = FUSED_ROWS / 8;
-      const int row0 = (warp - 4) * 2 + (lane >> 4), gc = lane & 15;
-      const T* const x = static_cast<const T*>(p.x);
-      Raw16<T> raw[PASSES];
-      const auto load = [&](int it) {
-#pragma unroll
-        for (int i = 0; i < PASSES; ++i)
-          if (row0 + 8 * i < p.M)
-            raw[i].load(x + (row0 + 8 * i) * p.ldx, it * 256 + gc * 16, p.KR, p.vec_x);
-      };
-      int stage = 0;
-      uint32_t phase = 0;
-      if (k0 < k1) load(k0);
-      for (int it = k0; it < k1; ++it) {
-        Raw16<T> now[PASSES];
-#pragma unroll
-        for (int i = 0; i < PASSES; ++i) now[i] = raw[i];
-        if (it + 1 < k1) load(it + 1);
+      const int w = warp - 4, groups_log2 = 2 - p.warps_log2;
+      const int r = (w & ((1 << p.warps_log2) - 1)) * 2 + (lane >> 4), gc = lane & 15;
+      const T* const x = static_cast<const T*>(p.x) + (r < p.M ? r * p.ldx : 0);
+      Raw16<T> next;
+      int it = k0 + (w >> p.warps_log2);
+      if (it < k1) next.load(x, it * 256 + gc * 16, p.KR, p.vec_x);
+      for (; it < k1; it += 1 << groups_log2) {
+        const Raw16<T> raw = next;
+        const int stage = (it - k0) % STAGES;
+        const uint32_t phase = ((it - k0) / STAGES) & 1;
+        if (it + (1 << groups_log2) < k1)
+          next.load(x, (it + (1 << groups_log2)) * 256 + gc * 16, p.KR, p.vec_x);
         if (!gb::mbar_wait_bounded_warp<false>(&empty[stage], phase ^ 1, p.wait_ns, p.err)) break;
-#pragma unroll
-        for (int i = 0; i < PASSES; ++i) {
-          const int r = row0 + 8 * i;
-          if ((warp - 4) * 2 + 8 * i >= p.M) break;  // the warp's rows are past the last
-          float v[16];
-          now[i].get(v);
-          if (r >= p.M) {
-#pragma unroll
-            for (int k = 0; k < 16; ++k) v[k] = 0.0f;
-          }
-          uint2 code;
-          uint32_t word;
-          quantize16<FMT>(v, p.x_scale, code, word);
+        float v[16];
+        raw.get(v);
+        uint2 code;
+        uint32_t word;
+        quantize16<FMT>(v, p.x_scale, code, word);
+        if (r < p.M) {
           // row r of a 128-byte-swizzled tile; its scale words in tiles of 512 bytes
           *reinterpret_cast<uint2*>(sX + stage * x_bytes + r * BKB +
                                     (((gc >> 1) ^ (r & 7)) << 4) + (gc & 1) * 8) = code;
@@ -269,10 +276,6 @@ __global__ void __launch_bounds__(THREADS)
         gb::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) gb::mbar_arrive(&full[stage]);
-        if (++stage == STAGES) {
-          stage = 0;
-          phase ^= 1;
-        }
       }
     }
     // ---------------- accumulators: to the epilogue, or to the cluster ----------------
@@ -280,20 +283,21 @@ __global__ void __launch_bounds__(THREADS)
     gb::tc_fence_after();
     const uint32_t t = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const int o = (warp & 3) * 32 + lane, n = tile * 128 + o;
-    if (p.split == 1) {
+    if (split == 1) {
       const float bias = p.bias && n < p.N ? p.bias[n] : 0.0f;
       for (int c = 0; c < p.M; c += 8) {
         uint32_t r[8];
         gb::tmem_ld_x8(t + c, r);
         gb::tmem_ld_wait();
+        float v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (c + i < p.M) finish<FMT, YIO>(p, __uint_as_float(r[i]), c + i, n, bias);
+        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+        finish<FMT, YIO>(p, v, c, 1, min(8, p.M - c), n, bias);
       }
     } else {
       // row m goes to CTA m % split, place m / split; source rank, place, output
-      const uint32_t mine = gb::smem_u32(part) + 4 * o;
-      const int places = (p.M + p.split - 1) / p.split;
+      const int places = (p.M + split - 1) >> p.split_log2;
+      const uint32_t mine = gb::smem_u32(part) + 4 * o + 512 * rank * places;
       for (int c = 0; c < p.M; c += 8) {
         uint32_t r[8];
         gb::tmem_ld_x8(t + c, r);
@@ -302,25 +306,31 @@ __global__ void __launch_bounds__(THREADS)
         for (int i = 0; i < 8; ++i) {
           const int m = c + i;
           if (m < p.M)
-            gb::store_cluster(gb::mapa_shared(mine + 512 * (rank * places + m / p.split),
-                                              (uint32_t)(m % p.split)),
-                              k0 < k1 ? r[i] : 0u);
+            gb::store_cluster(gb::mapa_shared(mine + 512 * (m >> p.split_log2),
+                                              (uint32_t)(m & (split - 1))),
+                              r[i]);
         }
       }
     }
     gb::tc_fence_before();
   }
   __syncthreads();
-  if (p.split > 1) {
+  if (split > 1) {
     gb::cluster_sync();
     if (warp >= 4) {
       const int o = (warp & 3) * 32 + lane, n = tile * 128 + o;
       const float bias = p.bias && n < p.N ? p.bias[n] : 0.0f;
-      const int places = (p.M + p.split - 1) / p.split;
-      for (int m = rank, i = 0; m < p.M; m += p.split, ++i) {
-        float s = 0.0f;
-        for (int r = 0; r < p.split; ++r) s += part[128 * (r * places + i) + o];
-        finish<FMT, YIO>(p, s, m, n, bias);
+      const int places = (p.M + split - 1) >> p.split_log2;
+      for (int i = 0; rank + i * split < p.M; i += 8) {
+        float v[8] = {};
+        const int rows = min(8, (p.M - rank - i * split + split - 1) >> p.split_log2);
+        for (int r = 0; r < split; ++r) {
+          const float* const from = part + 128 * (r * places + i) + o;
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (k < rows) v[k] += from[128 * k];
+        }
+        finish<FMT, YIO>(p, v, rank + i * split, split, rows, n, bias);
       }
     }
   }
@@ -359,8 +369,15 @@ cudaError_t launch_t(const Fp4Gemm& g, cudaStream_t st) {
   p.wait_ns = gb_wait_limit_ns();
   // split the reduction while the tiles leave SMs idle and each CTA keeps two k-steps
   const int tiles = gb_ceil_div(g.K, 128);
-  p.split = 1;
-  while (p.split < 8 && tiles * p.split * 2 <= gb_num_sms() && p.ksteps >= p.split * 4) p.split *= 2;
+  // (up to 8 CTAs; 4 where only one of them fits an SM: clusters of 8 then do not all find
+  // room at once, 64 x 8192 x 2048 11.0 us against 5.3 with half the rows)
+  const int most = 2 * (C::smem(p.nt, 8) + 1024) <= 228 * 1024 ? 3 : 2;
+  p.split_log2 = 0;
+  while (p.split_log2 < most && (tiles << (p.split_log2 + 1)) <= gb_num_sms() &&
+         p.ksteps >> (p.split_log2 + 2))
+    ++p.split_log2;
+  const int split = 1 << p.split_log2;
+  p.warps_log2 = g.M <= 2 ? 0 : g.M <= 4 ? 1 : 2;
   CUtensorMap tw, tws, tx, txs;
   if (!codes_map(&tw, g.w, g.K, g.C, 128) ||
       !scales_map(&tws, g.ws, FMT, g.K, g.C, C::ATOMS, 1))
@@ -373,11 +390,11 @@ cudaError_t launch_t(const Fp4Gemm& g, cudaStream_t st) {
     return cudaErrorInvalidValue;
   }
   auto* kern = fp4_few_kernel<FMT, XIO, YIO>;
-  const int smem = C::smem(p.nt, p.split);
+  const int smem = C::smem(p.nt, split);
   cudaError_t e = gb_set_smem_once(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(tiles * p.split));
+  cfg.gridDim = dim3((unsigned)(tiles * split));
   cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
@@ -385,7 +402,7 @@ cudaError_t launch_t(const Fp4Gemm& g, cudaStream_t st) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = p.split;
+  attr[1].val.clusterDim.x = split;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;

@@ -107,7 +107,7 @@ __device__ __forceinline__ void finish_float(const GemmParams& p, float (&v)[Blo
         *reinterpret_cast<uint4*>(B::at(buf, i * 8 + lane / 4, lane % 4)) = pre[i];
     } else if (lane < cols) {
       const T* g = static_cast<const T*>(p.res) + (long long)m0 * p.ldr + n0 + lane;
-#pragma unroll 4
+#pragma unroll 16
       for (int r = 0; r < rows; ++r) *B::elem(buf, r, lane) = g[r * p.ldr];
     }
     __syncwarp();
@@ -574,8 +574,11 @@ cudaError_t launch_tile(const Fp4Gemm& g, cudaStream_t st) {
 
 template <int FMT, int YIO>
 cudaError_t launch_y(const Fp4Gemm& g, cudaStream_t st) {
-  if (g.M > 128 && g.K > 128) return launch_tile<FMT, 256, true, YIO>(g, st);
-  return launch_tile<FMT, 128, false, YIO>(g, st);
+  // one wave of 128 x 128 tiles is faster than fewer, larger tiles (256 x 2048 x 1000: 5.5
+  // us against 7.7); beyond it the SM pairs' tiles read half the operands per product
+  const long long tiles = gb_ceil_div_ll(g.M, 128) * gb_ceil_div_ll(g.K, 128);
+  return tiles <= gb_num_sms() || g.K <= 128 ? launch_tile<FMT, 128, false, YIO>(g, st)
+                                             : launch_tile<FMT, 256, true, YIO>(g, st);
 }
 
 template <int FMT>
