@@ -23,7 +23,8 @@ constexpr int BM = 128;
 
 template <int FMT, int BN, bool PAIR, int YIO>
 struct Cfg {
-  static constexpr int EPI_WARPS = BN / 16;  // 4 lane quarters x 64 columns each
+  static constexpr int CW = BN / 4;       // columns of an epilogue warp
+  static constexpr int EPI_WARPS = 16;    // 4 lane quarters x 4 column ranges
   static constexpr int THREADS = 128 + 32 * EPI_WARPS;
   static constexpr int ATOMS = FMT == CONV_FP4_MX ? 2 : 4;  // scale tiles per panel and k-step
   static constexpr int PB = (BN + 127) / 128;               // 128-row panels of W
@@ -79,37 +80,74 @@ struct Block {
   static __device__ __forceinline__ T* elem(uint8_t* buf, int row, int col) {
     return reinterpret_cast<T*>(at(buf, row, col * ES / 16) + col * ES % 16);
   }
-  // a block of global memory into registers, four lanes to a row; rows < rows
-  static __device__ __forceinline__ void fetch(uint4 (&r)[4], const T* g, long long ld, int rows) {
+  // A block of global memory (rows < rows, columns < cols) into registers, and from
+  // there into the buffer.  vec: four lanes to a row, 16 bytes each; else an element at a
+  // time: a lane takes a column (bf16: all rows, two to a register; fp32: half the rows).
+  static __device__ __forceinline__ void fetch(uint32_t (&r)[16], const T* g, long long ld,
+                                               int rows, int cols, bool vec) {
     const int lane = threadIdx.x & 31;
+    if (vec && cols >= COLS) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = i * 8 + lane / 4;
-      r[i] = make_uint4(0, 0, 0, 0);
-      if (row < rows) r[i] = *reinterpret_cast<const uint4*>(g + row * ld + lane % 4 * (16 / ES));
+      for (int i = 0; i < 4; ++i) {
+        const int row = i * 8 + lane / 4;
+        uint4 u = make_uint4(0, 0, 0, 0);
+        if (row < rows) u = *reinterpret_cast<const uint4*>(g + row * ld + lane % 4 * (16 / ES));
+        r[4 * i] = u.x;
+        r[4 * i + 1] = u.y;
+        r[4 * i + 2] = u.z;
+        r[4 * i + 3] = u.w;
+      }
+    } else {
+      const int col = lane % COLS, row0 = lane / COLS * 16;
+      const bool in = col < cols;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        r[i] = 0;
+        if constexpr (ES == 2) {
+          const uint16_t* const h = reinterpret_cast<const uint16_t*>(g) + col;
+          if (in && 2 * i < rows) r[i] = h[2 * i * ld];
+          if (in && 2 * i + 1 < rows) r[i] |= (uint32_t)h[(2 * i + 1) * ld] << 16;
+        } else {
+          if (in && row0 + i < rows)
+            r[i] = reinterpret_cast<const uint32_t*>(g)[(row0 + i) * ld + col];
+        }
+      }
+    }
+  }
+  static __device__ __forceinline__ void put(uint8_t* buf, const uint32_t (&r)[16], int cols,
+                                             bool vec) {
+    const int lane = threadIdx.x & 31;
+    if (vec && cols >= COLS) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<uint4*>(at(buf, i * 8 + lane / 4, lane % 4)) =
+            make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+    } else {
+      const int col = lane % COLS, row0 = lane / COLS * 16;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        if constexpr (ES == 2) {
+          *reinterpret_cast<uint16_t*>(elem(buf, 2 * i, col)) = (uint16_t)r[i];
+          *reinterpret_cast<uint16_t*>(elem(buf, 2 * i + 1, col)) = (uint16_t)(r[i] >> 16);
+        } else {
+          *reinterpret_cast<uint32_t*>(elem(buf, row0 + i, col)) = r[i];
+        }
+      }
     }
   }
 };
 
 // v (acc * alpha + bias) of rows m0.. and columns n0..: residual, activation, store.
-// pre: the residual's pieces, fetched ahead (vec_r and a whole block of columns).
+// pre: the residual, fetched ahead.
 template <typename T>
 __device__ __forceinline__ void finish_float(const GemmParams& p, float (&v)[Block<T>::COLS],
-                                             uint8_t* buf, int m0, int n0, const uint4 (&pre)[4]) {
+                                             uint8_t* buf, int m0, int n0, const uint32_t (&pre)[16]) {
   using B = Block<T>;
   const int lane = threadIdx.x & 31;
   const int rows = min(32, p.M - m0), cols = min(B::COLS, p.N - n0);
   const bool whole = cols == B::COLS;
   if (p.res) {
-    if (p.vec_r && whole) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<uint4*>(B::at(buf, i * 8 + lane / 4, lane % 4)) = pre[i];
-    } else if (lane < cols) {
-      const T* g = static_cast<const T*>(p.res) + (long long)m0 * p.ldr + n0 + lane;
-#pragma unroll 16
-      for (int r = 0; r < rows; ++r) *B::elem(buf, r, lane) = g[r * p.ldr];
-    }
+    B::put(buf, pre, cols, p.vec_r);
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -415,41 +453,41 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR, YIO>::THREADS, 1)
   } else {
     if constexpr (BN == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
     // ---------------- epilogue (warps 4 and up) ----------------
-    // A warp owns 32 rows (the TMEM lane quarter it may access) and 64 of the tile's
+    // A warp owns 32 rows (the TMEM lane quarter it may access) and a quarter of the tile's
     // columns.  It takes its accumulators into registers and frees the TMEM
     // accumulator before it works on them: the next tile's MMAs wait for TMEM reads only.
-    // (With 128 columns to a warp, two warps per scheduler left it idle 65 % of the time:
-    // 8192 x 4096 x 16384 with GELU 197 us.)
+    // (With half the warps, two per scheduler, it was idle 65 % of the time:
+    // 8192 x 4096 x 16384 with GELU 197 us against 186.)
     using T = std::conditional_t<YIO == CONV_FP4_IO_BF16, __nv_bfloat16, float>;
     constexpr bool FLOAT = YIO != CONV_FP4_IO_CODES;
     constexpr int PC = FLOAT ? Block<T>::COLS : 32;  // columns of a pass
-    constexpr int NP = 64 / PC;
+    constexpr int CW = C::CW, NP = CW / PC;
     const int q = warp & 3, group = (warp - 4) >> 2;
     uint8_t* const buf = sEpi + (warp - 4) * C::EPI_WARP;
     float* const sbias = reinterpret_cast<float*>(buf + C::EPI_WARP - 128);
     const uint32_t tempty_pair = PAIR ? gb::mapa_shared(gb::smem_u32(tempty), 0) : 0u;
     int acc = 0;
     uint32_t acc_phase = 0;
-    uint4 pre[4] = {};
+    uint32_t pre[16] = {};
     asm volatile("griddepcontrol.wait;" ::: "memory");
     for (int u = unit0; u < units; u += ustep) {
       const int mt = (u / p.n_tiles) * (PAIR ? 2 : 1) + (int)rank, nt = u % p.n_tiles;
-      const int m0 = mt * BM + q * 32, nb = nt * BN + group * 64;
-      const bool ahead = FLOAT && p.res && p.vec_r;
+      const int m0 = mt * BM + q * 32, nb = nt * BN + group * CW;
+      const bool ahead = FLOAT && p.res && m0 < p.M;
       const T* res = static_cast<const T*>(p.res) + (long long)m0 * p.ldr + nb;
-      if (ahead && nb + PC <= p.N) Block<T>::fetch(pre, res, p.ldr, p.M - m0);
-      float bias[2];  // of the lane's column in each half
+      if (ahead && nb < p.N) Block<T>::fetch(pre, res, p.ldr, p.M - m0, p.N - nb, p.vec_r);
+      float bias[CW / 32];  // of the lane's column in each 32
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < CW / 32; ++i) {
         const int n = nb + 32 * i + lane;
         bias[i] = p.bias && n < p.N ? p.bias[n] : 0.0f;
       }
       if (!gb::mbar_wait_bounded(&tfull[acc], acc_phase, p.wait_ns, p.err)) break;
       gb::tc_fence_after();
-      const uint32_t t = tmem + ((uint32_t)(q * 32) << 16) + acc * BN + group * 64;
-      uint32_t r[2][32];
-      gb::tmem_ld_x32(t, r[0]);
-      gb::tmem_ld_x32(t + 32, r[1]);
+      const uint32_t t = tmem + ((uint32_t)(q * 32) << 16) + acc * BN + group * CW;
+      uint32_t r[CW / 32][32];
+#pragma unroll
+      for (int i = 0; i < CW / 32; ++i) gb::tmem_ld_x32(t + 32 * i, r[i]);
       gb::tmem_ld_wait();
       gb::tc_fence_before();
       __syncwarp();
@@ -481,8 +519,8 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR, YIO>::THREADS, 1)
           }
           if constexpr (FLOAT) {
             finish_float<T>(p, v, buf, m0, n0, pre);
-            if (ahead && s + 1 < NP && n0 + 2 * PC <= p.N)
-              Block<T>::fetch(pre, res + PC * (s + 1), p.ldr, p.M - m0);
+            if (ahead && s + 1 < NP && n0 + PC < p.N)
+              Block<T>::fetch(pre, res + PC * (s + 1), p.ldr, p.M - m0, p.N - n0 - PC, p.vec_r);
           } else {
             finish_codes<FMT>(p, v, m0, n0);
           }
