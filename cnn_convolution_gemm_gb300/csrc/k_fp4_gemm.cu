@@ -39,9 +39,9 @@ struct Cfg {
   // scale columns of a stage, in a slot of its own per stage: a slot is written again
   // only after the MMAs that read it have committed the stage
   static constexpr int SF_COLS = ATOMS * 4 * (1 + PB);
-  // a warp's staging buffer and 32 biases
-  static constexpr int EPI_WARP = (YIO == CONV_FP4_IO_CODES ? 0 : 2048) + 128;
-  static constexpr int EPI_BYTES = EPI_WARPS * EPI_WARP;
+  // of each epilogue warp: a staging buffer; 32 biases
+  static constexpr int BUF = YIO == CONV_FP4_IO_CODES ? 0 : 2048;
+  static constexpr int EPI_BYTES = EPI_WARPS * (BUF + 128);
   static constexpr int SMEM = STAGES * STAGE_BYTES + EPI_BYTES + 256 + 1024;
   static_assert(NACC * BN + STAGES * SF_COLS <= 512, "TMEM");
   static_assert(SMEM <= 232448, "shared memory");
@@ -50,7 +50,7 @@ struct Cfg {
 struct GemmParams {
   int M, N, ksteps, kmmas_last;  // 64-element MMAs of the last k-step
   int m_tiles, n_tiles;          // PAIR: m_tiles counts 256-row units
-  int act, vec_y, vec_r;  // 16-byte accesses to rows of y / of the residual
+  int act, vec_y, vec_r;         // rows of y for the TMA, of the residual for 16-byte loads
   float alpha;
   TensorScale y_scale;
   const float* bias;
@@ -64,10 +64,11 @@ struct GemmParams {
 
 // ---- epilogue: a lane holds a row's fp32 accumulators ----------------------------------
 //
-// Rows of the output (and of the residual) pass through a staging buffer of the warp,
-// so that global accesses are whole row segments: 32 rows of 64 bytes (COLS elements),
-// their 16-byte pieces swizzled so that a quarter-warp's accesses hit all banks once,
-// by row and by piece alike.
+// Rows of the output (and of the residual) pass through a staging buffer of the warp: 32
+// rows of 64 bytes (COLS elements), their 16-byte pieces in the TMA's 64-byte swizzle, so
+// that a quarter-warp's accesses hit all banks once, by row and by piece alike.  Where
+// the output's rows allow it the TMA stores the buffer (and drops what lies outside):
+// copied by the warp, 64 bytes a row, L1 was the bound (8192 x 256 x 4096: 73 % busy).
 
 template <typename T>
 struct Block {
@@ -137,17 +138,23 @@ struct Block {
   }
 };
 
-// v (acc * alpha + bias) of rows m0.. and columns n0..: residual, activation, store.
-// pre: the residual, fetched ahead.
-template <typename T>
-__device__ __forceinline__ void finish_float(const GemmParams& p, float (&v)[Block<T>::COLS],
-                                             uint8_t* buf, int m0, int n0, const uint32_t (&pre)[16]) {
+// v (acc * alpha + bias) of rows m0.. and columns n0..: residual, activation, store (by
+// the TMA: committed, and the buffer waited for before it is written again).
+// pre: the residual, fetched ahead; refill() fetches what the warp needs next.
+template <typename T, typename F>
+__device__ __forceinline__ void finish_float(const GemmParams& p, const CUtensorMap* tm_y, float (&v)[Block<T>::COLS],
+                                             uint8_t* buf, int m0, int n0, const uint32_t (&pre)[16],
+                                             F refill) {
   using B = Block<T>;
   const int lane = threadIdx.x & 31;
   const int rows = min(32, p.M - m0), cols = min(B::COLS, p.N - n0);
-  const bool whole = cols == B::COLS;
+  if (p.vec_y) {  // the buffer's last store has read it
+    if (lane == 0) gb::bulk_wait_read<0>();
+    __syncwarp();
+  }
   if (p.res) {
     B::put(buf, pre, cols, p.vec_r);
+    refill();
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -180,21 +187,22 @@ __device__ __forceinline__ void finish_float(const GemmParams& p, float (&v)[Blo
     }
     *reinterpret_cast<uint4*>(B::at(buf, lane, i)) = make_uint4(w[0], w[1], w[2], w[3]);
   }
-  __syncwarp();
-  T* y = static_cast<T*>(p.y) + (long long)m0 * p.ldy + n0;
-  if (p.vec_y && whole) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = i * 8 + lane / 4;
-      if (row < rows)
-        *reinterpret_cast<uint4*>(y + row * p.ldy + lane % 4 * (16 / B::ES)) =
-            *reinterpret_cast<const uint4*>(B::at(buf, row, lane % 4));
+  if (p.vec_y) {
+    gb::fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      gb::tma_store_2d(tm_y, buf, n0, m0);
+      gb::bulk_commit();
     }
-  } else if (lane < cols) {
+  } else {
+    __syncwarp();
+    T* y = static_cast<T*>(p.y) + (long long)m0 * p.ldy + n0;
+    if (lane < cols) {
 #pragma unroll 4
-    for (int r = 0; r < rows; ++r) y[r * p.ldy + lane] = *B::elem(buf, r, lane);
+      for (int r = 0; r < rows; ++r) y[r * p.ldy + lane] = *B::elem(buf, r, lane);
+    }
+    __syncwarp();
   }
-  __syncwarp();
 }
 
 // 32 columns as 4-bit codes: one MX block or two NV blocks of the lane's row.
@@ -246,7 +254,7 @@ template <int FMT, int BN, bool PAIR, int YIO>
 __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR, YIO>::THREADS, 1)
     fp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_xs,
                     const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_ws,
-                    const GemmParams p) {
+                    const __grid_constant__ CUtensorMap tm_y, const GemmParams p) {
   using C = Cfg<FMT, BN, PAIR, YIO>;
   constexpr bool MX = FMT == CONV_FP4_MX;
   extern __shared__ uint8_t smem_raw[];
@@ -285,6 +293,7 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR, YIO>::THREADS, 1)
     gb::tma_prefetch_desc(&tm_w);
     gb::tma_prefetch_desc(&tm_xs);
     gb::tma_prefetch_desc(&tm_ws);
+    if (YIO != CONV_FP4_IO_CODES && p.vec_y) gb::tma_prefetch_desc(&tm_y);
   }
   if (warp == 0) {
     if constexpr (PAIR) {
@@ -463,25 +472,40 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR, YIO>::THREADS, 1)
     constexpr int PC = FLOAT ? Block<T>::COLS : 32;  // columns of a pass
     constexpr int CW = C::CW, NP = CW / PC;
     const int q = warp & 3, group = (warp - 4) >> 2;
-    uint8_t* const buf = sEpi + (warp - 4) * C::EPI_WARP;
-    float* const sbias = reinterpret_cast<float*>(buf + C::EPI_WARP - 128);
+    uint8_t* const buf = sEpi + (warp - 4) * C::BUF;
+    float* const sbias =
+        reinterpret_cast<float*>(sEpi + C::EPI_WARPS * C::BUF + (warp - 4) * 128);
     const uint32_t tempty_pair = PAIR ? gb::mapa_shared(gb::smem_u32(tempty), 0) : 0u;
     int acc = 0;
     uint32_t acc_phase = 0;
+    // what a tile reads is on its way before the tile's turn: its first block of the
+    // residual and its biases (of the lane's column in each 32)
     uint32_t pre[16] = {};
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    for (int u = unit0; u < units; u += ustep) {
-      const int mt = (u / p.n_tiles) * (PAIR ? 2 : 1) + (int)rank, nt = u % p.n_tiles;
-      const int m0 = mt * BM + q * 32, nb = nt * BN + group * CW;
-      const bool ahead = FLOAT && p.res && m0 < p.M;
-      const T* res = static_cast<const T*>(p.res) + (long long)m0 * p.ldr + nb;
-      if (ahead && nb < p.N) Block<T>::fetch(pre, res, p.ldr, p.M - m0, p.N - nb, p.vec_r);
-      float bias[CW / 32];  // of the lane's column in each 32
+    float bias[CW / 32];
+    const auto row_of = [&](int u) {
+      return ((u / p.n_tiles) * (PAIR ? 2 : 1) + (int)rank) * BM + q * 32;
+    };
+    const auto fetch_res = [&](int m0, int n0) {
+      if (FLOAT && p.res && m0 < p.M && n0 < p.N)
+        Block<T>::fetch(pre, static_cast<const T*>(p.res) + (long long)m0 * p.ldr + n0, p.ldr,
+                        p.M - m0, p.N - n0, p.vec_r);
+    };
+    const auto fetch_bias = [&](int nb) {
 #pragma unroll
       for (int i = 0; i < CW / 32; ++i) {
         const int n = nb + 32 * i + lane;
         bias[i] = p.bias && n < p.N ? p.bias[n] : 0.0f;
       }
+    };
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    int m0 = row_of(unit0), nb = unit0 % p.n_tiles * BN + group * CW;
+    if (unit0 < units) {
+      fetch_res(m0, nb);
+      fetch_bias(nb);
+    }
+    for (int u = unit0; u < units; u += ustep) {
+      const int un = u + ustep, m_next = un < units ? row_of(un) : p.M;
+      const int nb_next = un % p.n_tiles * BN + group * CW;
       if (!gb::mbar_wait_bounded(&tfull[acc], acc_phase, p.wait_ns, p.err)) break;
       gb::tc_fence_after();
       const uint32_t t = tmem + ((uint32_t)(q * 32) << 16) + acc * BN + group * CW;
@@ -506,6 +530,8 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR, YIO>::THREADS, 1)
             sbias[lane] = bias[PC * s / 32];
             __syncwarp();
           }
+          const bool last = s + 1 == NP || n0 + PC >= p.N;  // of the tile's blocks
+          if (last && un < units) fetch_bias(nb_next);
           float v[PC];
           const uint64_t al = pack2(p.alpha, p.alpha);
 #pragma unroll
@@ -518,20 +544,30 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR, YIO>::THREADS, 1)
                     v[i + 3]);
           }
           if constexpr (FLOAT) {
-            finish_float<T>(p, v, buf, m0, n0, pre);
-            if (ahead && s + 1 < NP && n0 + PC < p.N)
-              Block<T>::fetch(pre, res + PC * (s + 1), p.ldr, p.M - m0, p.N - n0 - PC, p.vec_r);
+            finish_float<T>(p, &tm_y, v, buf, m0, n0, pre, [&] {
+              if (last)
+                fetch_res(m_next, nb_next);
+              else
+                fetch_res(m0, n0 + PC);
+            });
           } else {
             finish_codes<FMT>(p, v, m0, n0);
           }
           __syncwarp();
         }
       }
+      if (m0 >= p.M || nb >= p.N) {  // nothing was read for this tile
+        fetch_res(m_next, nb_next);
+        if (un < units) fetch_bias(nb_next);
+      }
+      m0 = m_next;
+      nb = nb_next;
       if (++acc == C::NACC) {
         acc = 0;
         acc_phase ^= 1;
       }
     }
+    if (FLOAT && lane == 0) gb::bulk_wait_all();  // stores done before exit
   }
   gb::tc_fence_before();
   __syncthreads();
@@ -576,6 +612,18 @@ cudaError_t launch_tile(const Fp4Gemm& g, cudaStream_t st) {
     p.vec_y = rows_vec<float>(g.y, g.ldy, 16);
     p.vec_r = rows_vec<float>(g.res, g.ldr, 16);
   }
+  CUtensorMap ty = tx;
+  if (YIO != CONV_FP4_IO_CODES && p.vec_y) {  // boxes of 32 rows x 64 bytes
+    constexpr cuuint64_t es = YIO == CONV_FP4_IO_BF16 ? 2 : 4;
+    cuuint64_t dims[2] = {(cuuint64_t)g.K, (cuuint64_t)g.M};
+    cuuint64_t strides[1] = {(cuuint64_t)g.ldy * es};
+    cuuint32_t box[2] = {(cuuint32_t)(64 / es), 32};
+    cuuint32_t estr[2] = {1, 1};
+    if (gb_encode_tiled(&ty, es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+                        2, g.y, dims, strides, box, estr,
+                        CU_TENSOR_MAP_SWIZZLE_64B) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  }
   p.err = gb_device_error_word();
   p.wait_ns = gb_wait_limit_ns();
   auto* kern = fp4_gemm_kernel<FMT, BN, PAIR, YIO>;
@@ -605,18 +653,22 @@ cudaError_t launch_tile(const Fp4Gemm& g, cudaStream_t st) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = PAIR ? 2 : 1;
-  e = cudaLaunchKernelEx(&cfg, kern, tx, txs, tw, tws, p);
+  e = cudaLaunchKernelEx(&cfg, kern, tx, txs, tw, tws, ty, p);
   if (e == cudaSuccess) gb_count_launch();
   return e;
 }
 
 template <int FMT, int YIO>
 cudaError_t launch_y(const Fp4Gemm& g, cudaStream_t st) {
-  // one wave of 128 x 128 tiles is faster than fewer, larger tiles (256 x 2048 x 1000: 5.5
-  // us against 7.7); beyond it the SM pairs' tiles read half the operands per product
+  // 128 x 128 tiles where they take one wave (256 x 2048 x 1000: 5.5 us against 7.7), or two
+  // of up to 8 k-steps, or where the epilogue bounds (up to 4 k-steps: 8192 x 1024 x 4096
+  // 23.6 us against 27.9); the SM pairs' tiles read half the operands per product
+  // (8192 x 4096 x 4096 49.5 us against 63.5)
   const long long tiles = gb_ceil_div_ll(g.M, 128) * gb_ceil_div_ll(g.K, 128);
-  return tiles <= gb_num_sms() || g.K <= 128 ? launch_tile<FMT, 128, false, YIO>(g, st)
-                                             : launch_tile<FMT, 256, true, YIO>(g, st);
+  const int sms = gb_num_sms();
+  const bool small = tiles <= sms || g.C <= 1024 || (tiles <= 2 * sms && g.C <= 2048) || g.K <= 128;
+  return small ? launch_tile<FMT, 128, false, YIO>(g, st)
+               : launch_tile<FMT, 256, true, YIO>(g, st);
 }
 
 template <int FMT>
