@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(THREADS)
     const uint32_t tx = C::W_BYTES + C::SF_BYTES + (FUSED ? 0 : x_bytes + C::SF_BYTES);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     for (int it = k0; it < k1; ++it) {
-      if (!gb::mbar_wait_bounded_warp<false>(&empty[stage], phase ^ 1, p.wait_ns, p.err)) break;
+      if (!gb::mbar_wait_bounded_warp(&empty[stage], phase ^ 1, p.wait_ns, p.err)) break;
       if (one) {
         const int sc = it * (C::ATOMS * 64);  // scale tiles as 8-byte elements
         gb::mbar_arrive_expect_tx(&full[stage], tx);
@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(THREADS)
         stage = STAGES - 1;
         phase ^= 1;
       }
-      gb::mbar_wait_bounded_warp<false>(&full[stage], phase, p.wait_ns, p.err);
+      gb::mbar_wait_bounded_warp(&full[stage], phase, p.wait_ns, p.err);
     }
   } else if (warp == 1) {
     // ---------------- scale copies and MMAs ----------------
@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(THREADS)
     int stage = 0;
     uint32_t phase = 0;
     for (int it = k0; it < k1; ++it) {
-      if (!gb::mbar_wait_bounded_warp<false>(&full[stage], phase, p.wait_ns, p.err)) break;
+      if (!gb::mbar_wait_bounded_warp(&full[stage], phase, p.wait_ns, p.err)) break;
       gb::tc_fence_after();
       if (one) {
         const uint64_t wd = gb::sw128_kmajor_desc(gb::smem_u32(sW + stage * C::W_BYTES));
@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(THREADS)
     }
     if (one) gb::tc_commit(tfull);
     __syncwarp();
-    gb::mbar_wait_bounded_warp<false>(tfull, 0, p.wait_ns, p.err);
+    gb::mbar_wait_bounded_warp(tfull, 0, p.wait_ns, p.err);
   } else if (warp >= 4) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if constexpr (FUSED) {
@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(THREADS)
         const uint32_t phase = ((it - k0) / STAGES) & 1;
         if (it + (1 << groups_log2) < k1)
           next.load(x, (it + (1 << groups_log2)) * 256 + gc * 16, p.KR, p.vec_x);
-        if (!gb::mbar_wait_bounded_warp<false>(&empty[stage], phase ^ 1, p.wait_ns, p.err)) break;
+        if (!gb::mbar_wait_bounded_warp(&empty[stage], phase ^ 1, p.wait_ns, p.err)) break;
         float v[16];
         raw.get(v);
         uint2 code;
@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(THREADS)
       }
     }
     // ---------------- accumulators: to the epilogue, or to the cluster ----------------
-    gb::mbar_wait_bounded_warp<false>(tfull, 0, p.wait_ns, p.err);
+    gb::mbar_wait_bounded_warp(tfull, 0, p.wait_ns, p.err);
     gb::tc_fence_after();
     const uint32_t t = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const int o = (warp & 3) * 32 + lane, n = tile * 128 + o;

@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR, YIO>::THREADS, 1)
       const int mt = (u / p.n_tiles) * (PAIR ? 2 : 1) + (int)rank, nt = u % p.n_tiles;
       const int brow = nt * BN + (PAIR ? (int)rank * C::BROWS : 0);
       for (int it = 0; it < p.ksteps; ++it) {
-        if (!gb::mbar_wait_bounded_warp<PAIR>(&empty[stage], phase ^ 1, p.wait_ns, p.err)) {
+        if (!gb::mbar_wait_bounded_warp(&empty[stage], phase ^ 1, p.wait_ns, p.err)) {
           ok = false;
           break;
         }
@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR, YIO>::THREADS, 1)
         stage = C::STAGES - 1;
         phase ^= 1;
       }
-      gb::mbar_wait_bounded_warp<PAIR>(&full[stage], phase, p.wait_ns, p.err);
+      gb::mbar_wait_bounded_warp(&full[stage], phase, p.wait_ns, p.err);
     }
   } else if (warp == 1 && rank == 0) {
     // ---------------- scale copies and MMAs ----------------
@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR, YIO>::THREADS, 1)
     for (int u = unit0; u < units && ok; u += ustep) {
       const uint32_t d = tmem + acc * BN;
       for (int it = 0; it < p.ksteps; ++it) {
-        if (!gb::mbar_wait_bounded_warp<PAIR>(&full[stage], phase, p.wait_ns, p.err)) {
+        if (!gb::mbar_wait_bounded_warp(&full[stage], phase, p.wait_ns, p.err)) {
           ok = false;
           break;
         }
@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR, YIO>::THREADS, 1)
         __syncwarp();
         // the tile's accumulator is needed only now
         if (it == 0) {
-          if (!gb::mbar_wait_bounded_warp<PAIR>(&tempty[acc], acc_phase ^ 1, p.wait_ns, p.err)) {
+          if (!gb::mbar_wait_bounded_warp(&tempty[acc], acc_phase ^ 1, p.wait_ns, p.err)) {
             ok = false;
             break;
           }
@@ -457,7 +457,7 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR, YIO>::THREADS, 1)
         gb::tc_commit(mma_done);
     }
     __syncwarp();
-    gb::mbar_wait_bounded_warp<PAIR>(mma_done, 0, p.wait_ns, p.err);
+    gb::mbar_wait_bounded_warp(mma_done, 0, p.wait_ns, p.err);
   }
   } else {
     if constexpr (BN == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
@@ -517,7 +517,7 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR, YIO>::THREADS, 1)
       __syncwarp();
       if (lane == 0) {
         if constexpr (PAIR)
-          gb::mbar_arrive_cluster(tempty_pair + acc * 8);
+          gb::mbar_arrive_cluster_control(tempty_pair + acc * 8);
         else
           gb::mbar_arrive(&tempty[acc]);
       }

@@ -69,19 +69,6 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
-// mbar_try_wait for a barrier on which other CTAs of the cluster arrive too.
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
 // Wait for the phase with the given parity to complete, giving up after
 // limit_ns of wall time.  Returns false (and records DEV timeout in *err) if
 // the limit ran out.
@@ -99,15 +86,14 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity
 }
 
 // The same, by a whole warp that goes on together.
-template <bool CLUSTER>
 __device__ __forceinline__ bool mbar_wait_bounded_warp(uint64_t* bar, uint32_t parity,
                                                        unsigned long long limit_ns, int* err) {
-  bool ok = CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity);
+  bool ok = mbar_try_wait(bar, parity);
   if (!__all_sync(0xFFFFFFFFu, ok)) {
     const uint64_t t0 = global_timer_ns();
     bool late = false;
     while (!ok && !late) {
-      ok = CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity);
+      ok = mbar_try_wait(bar, parity);
       late = global_timer_ns() - t0 > limit_ns;
     }
     if (!__all_sync(0xFFFFFFFFu, ok)) {
@@ -270,6 +256,13 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster) {
 // A 32-bit store to the shared memory of a CTA of the cluster (shared::cluster address).
 __device__ __forceinline__ void store_cluster(uint32_t addr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+// The same for a barrier that guards tensor memory or operand tiles alone: nothing that
+// this thread wrote is read behind it, so the arrival needs no release across the
+// cluster (which waits for the thread's outstanding stores).
+__device__ __forceinline__ void mbar_arrive_cluster_control(uint32_t bar_cluster) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
 
 // TMA loads into this CTA's shared memory whose completion is signalled on an
