@@ -225,6 +225,18 @@ __device__ __forceinline__ void quantize16(const float (&v)[16], const TensorSca
   word |= __shfl_xor_sync(0xFFFFFFFFu, word, 2 * LB);
 }
 
+// Stores such a lane's part of row r, from column c.
+template <int FMT>
+__device__ __forceinline__ void store_quantized16(const uint2& packed, uint32_t word, long long r,
+                                                  int c, int cols, uint8_t* __restrict__ codes,
+                                                  uint8_t* __restrict__ scales) {
+  const long long pitch = code_pitch(cols);
+  if (c < 2 * pitch) *reinterpret_cast<uint2*>(codes + r * pitch + c / 2) = packed;
+  const int tiles = tiles_per_row(FMT, cols), tj = c / (4 * kBlock<FMT>);
+  if (c % (4 * kBlock<FMT>) == 0 && tj < tiles)
+    *reinterpret_cast<uint32_t*>(scales + scale_word_offset(r, tj, tiles)) = word;
+}
+
 // One warp turns 512 consecutive columns of a row, 16 to a lane (v; zero past the last
 // column), into codes and scales.  c0: the warp's first column.  All lanes call it.
 template <int FMT>
@@ -232,16 +244,10 @@ __device__ __forceinline__ void store_warp_row(const float (&v)[16], const Tenso
                                                long long r, int c0, int cols,
                                                uint8_t* __restrict__ codes,
                                                uint8_t* __restrict__ scales) {
-  const int lane = threadIdx.x & 31;
   uint2 packed;
   uint32_t word;
   quantize16<FMT>(v, ts, packed, word);
-  const int c = c0 + lane * 16;
-  const long long pitch = code_pitch(cols);
-  if (c < 2 * pitch) *reinterpret_cast<uint2*>(codes + r * pitch + c / 2) = packed;
-  const int tiles = tiles_per_row(FMT, cols), tj = c / (4 * kBlock<FMT>);
-  if (c % (4 * kBlock<FMT>) == 0 && tj < tiles)
-    *reinterpret_cast<uint32_t*>(scales + scale_word_offset(r, tj, tiles)) = word;
+  store_quantized16<FMT>(packed, word, r, c0 + (int)(threadIdx.x & 31) * 16, cols, codes, scales);
 }
 
 template <typename T>

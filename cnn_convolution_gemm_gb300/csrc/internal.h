@@ -292,8 +292,8 @@ struct Fp4Gemm {
   uint8_t* ys;
 };
 cudaError_t launch_fp4_gemm(const Fp4Gemm& g, cudaStream_t st);
-// Up to FEW_ROWS rows; up to FUSED_ROWS of them floating (xf), quantised on the way in.
-constexpr int FEW_ROWS = 32, FUSED_ROWS = 8;
+// Up to 64 rows; up to FUSED_ROWS of them floating (xf), quantised on the way in.
+constexpr int FUSED_ROWS = 8;
 cudaError_t launch_fp4_few(const Fp4Gemm& g, cudaStream_t st);
 
 // ---- norms around a residual block ----------------------------------------------

@@ -15,15 +15,27 @@ constexpr int ROWS = 2;  // rows whose loads a warp issues together
 
 // A warp works on 512 columns of a row, 16 to a lane (32 bytes of bf16), and walks over
 // rows.  Both directions should move bytes only: the loads of several rows are in flight
-// per warp, and the instructions of an element are few.  wx (a power of two up to 8) warps of a block
+// per warp, and the instructions of an element are few.  Rows of up to 256 (128) columns
+// share a warp two (four) at a time.  wx (a power of two up to 8) warps of a block
 // lie side by side along a row, the others below one another.
 struct Walk {
   int c;               // the lane's first column
-  long long row, step; // first row, and rows between the warp's rows
+  long long row, step; // the lane's first row, and rows between its rows
 };
+// NARROW: wx_log2 < 0, 1 << -wx_log2 rows to a warp
+template <bool NARROW>
 __device__ __forceinline__ Walk walk(int wx_log2) {
-  const int warp = threadIdx.x >> 5, wy = (THREADS / 32) >> wx_log2;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   Walk w;
+  if constexpr (NARROW) {
+    const int lanes_log2 = 5 + wx_log2;  // lanes of a row
+    const int wy = (THREADS / 32) << -wx_log2;
+    w.c = (lane & ((1 << lanes_log2) - 1)) * 16;
+    w.row = (long long)blockIdx.y * wy + (warp << -wx_log2) + (lane >> lanes_log2);
+    w.step = (long long)gridDim.y * wy;
+    return w;
+  }
+  const int wy = (THREADS / 32) >> wx_log2;
   w.c = (((int)blockIdx.x << wx_log2) + (warp & ((1 << wx_log2) - 1))) * 512 +
         (threadIdx.x & 31) * 16;
   w.row = (long long)blockIdx.y * wy + (warp >> wx_log2);
@@ -31,17 +43,18 @@ __device__ __forceinline__ Walk walk(int wx_log2) {
   return w;
 }
 
-template <int FMT, typename T>
+template <int FMT, typename T, bool NARROW>
 __global__ void __launch_bounds__(THREADS)
     quantize_kernel(const T* __restrict__ x, long long ldx, int rows, int cols, int vec,
                     int wx_log2, const TensorScale ts, uint8_t* __restrict__ codes,
                     uint8_t* __restrict__ scales) {
   gb::allow_dependents();
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const Walk w = walk(wx_log2);
-  const int c0 = w.c - (int)(threadIdx.x & 31) * 16;
-  if (c0 >= cols) return;
-  for (long long r0 = w.row; r0 < rows; r0 += ROWS * w.step) {
+  const Walk w = walk<NARROW>(wx_log2);
+  if (!NARROW && w.c - (int)(threadIdx.x & 31) * 16 >= cols) return;  // the whole warp
+  // the lanes of a warp go round together: the shuffles below are the warp's
+  const long long lead = w.row - (NARROW ? (threadIdx.x & 31) >> (5 + wx_log2) : 0);
+  for (long long r0 = w.row, l0 = lead; l0 < rows; r0 += ROWS * w.step, l0 += ROWS * w.step) {
     Raw16<T> raw[ROWS];
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
@@ -51,22 +64,25 @@ __global__ void __launch_bounds__(THREADS)
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
       const long long r = r0 + i * w.step;
-      if (r >= rows) break;
+      if (l0 + i * w.step >= rows) break;
       float v[16];
       raw[i].get(v);
-      store_warp_row<FMT>(v, ts, r, c0, cols, codes, scales);
+      uint2 packed;
+      uint32_t word;
+      quantize16<FMT>(v, ts, packed, word);
+      if (!NARROW || r < rows) store_quantized16<FMT>(packed, word, r, w.c, cols, codes, scales);
     }
   }
 }
 
-template <int FMT, typename T>
+template <int FMT, typename T, bool NARROW>
 __global__ void __launch_bounds__(THREADS)
     dequantize_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
                       int rows, int cols, int vec, int wx_log2, float tensor_scale,
                       T* __restrict__ y, long long ldy) {
   gb::allow_dependents();
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const Walk w = walk(wx_log2);
+  const Walk w = walk<NARROW>(wx_log2);
   if (w.c >= cols) return;
   const long long pitch = code_pitch(cols);
   const int tiles = tiles_per_row(FMT, cols), b = w.c / kBlock<FMT>;
@@ -130,10 +146,11 @@ struct Shape {
 Shape walk_shape(int rows, int cols) {
   Shape s;
   const int chunks = (int)gb_ceil_div_ll(cols, 512);
-  s.wx_log2 = 0;
-  while (s.wx_log2 < 3 && (1 << s.wx_log2) < chunks) ++s.wx_log2;
-  const int gx = gb_ceil_div(chunks, 1 << s.wx_log2);
-  const long long need = gb_ceil_div_ll(rows, ROWS * ((THREADS / 32) >> s.wx_log2));
+  s.wx_log2 = cols <= 128 ? -2 : cols <= 256 ? -1 : 0;
+  while (s.wx_log2 >= 0 && s.wx_log2 < 3 && (1 << s.wx_log2) < chunks) ++s.wx_log2;
+  const int wy = s.wx_log2 < 0 ? (THREADS / 32) << -s.wx_log2 : (THREADS / 32) >> s.wx_log2;
+  const int gx = s.wx_log2 < 0 ? 1 : gb_ceil_div(chunks, 1 << s.wx_log2);
+  const long long need = gb_ceil_div_ll(rows, ROWS * wy);
   const long long gy = std::min<long long>(need, std::max(1, gb_num_sms() * 8 / gx));
   s.grid = dim3((unsigned)gx, (unsigned)gy);
   return s;
@@ -161,7 +178,7 @@ template <int FMT, typename T>
 cudaError_t quantize_t(int rows, int cols, const void* x, long long ldx, float ts, void* codes,
                        void* scales, cudaStream_t st) {
   const Shape s = walk_shape(rows, cols);
-  return launch_walk(quantize_kernel<FMT, T>, s.grid, st, static_cast<const T*>(x), ldx, rows, cols,
+  return launch_walk(s.wx_log2 < 0 ? quantize_kernel<FMT, T, true> : quantize_kernel<FMT, T, false>, s.grid, st, static_cast<const T*>(x), ldx, rows, cols,
                      (int)rows_vec<T>(x, ldx, 32), s.wx_log2, tensor_scale(ts),
                      static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales));
 }
@@ -170,7 +187,7 @@ template <int FMT, typename T>
 cudaError_t dequantize_t(int rows, int cols, const void* codes, const void* scales, float ts,
                          void* y, long long ldy, cudaStream_t st) {
   const Shape s = walk_shape(rows, cols);
-  return launch_walk(dequantize_kernel<FMT, T>, s.grid, st, static_cast<const uint8_t*>(codes),
+  return launch_walk(s.wx_log2 < 0 ? dequantize_kernel<FMT, T, true> : dequantize_kernel<FMT, T, false>, s.grid, st, static_cast<const uint8_t*>(codes),
                      static_cast<const uint8_t*>(scales), rows, cols, (int)rows_vec<T>(y, ldy, 32),
                      s.wx_log2, ts, static_cast<T*>(y), ldy);
 }

@@ -661,12 +661,12 @@ cudaError_t launch_tile(const Fp4Gemm& g, cudaStream_t st) {
 template <int FMT, int YIO>
 cudaError_t launch_y(const Fp4Gemm& g, cudaStream_t st) {
   // 128 x 128 tiles where they take one wave (256 x 2048 x 1000: 5.5 us against 7.7), or two
-  // of up to 8 k-steps, or where the epilogue bounds (up to 4 k-steps: 8192 x 1024 x 4096
-  // 23.6 us against 27.9); the SM pairs' tiles read half the operands per product
-  // (8192 x 4096 x 4096 49.5 us against 63.5)
+  // of up to 4 k-steps (2048 x 1024 x 2048 5.5 against 6.3); the SM pairs' tiles read half
+  // the operands per product (8192 x 1024 x 4096 18.1 us against 21.3, 8192 x 4096 x 4096
+  // 44.0 against 64.2)
   const long long tiles = gb_ceil_div_ll(g.M, 128) * gb_ceil_div_ll(g.K, 128);
   const int sms = gb_num_sms();
-  const bool small = tiles <= sms || g.C <= 1024 || (tiles <= 2 * sms && g.C <= 2048) || g.K <= 128;
+  const bool small = tiles <= sms || (tiles <= 2 * sms && g.C <= 1024) || g.K <= 128;
   return small ? launch_tile<FMT, 128, false, YIO>(g, st)
                : launch_tile<FMT, 256, true, YIO>(g, st);
 }

@@ -145,6 +145,14 @@ __device__ __forceinline__ void tma_load_2d(void* smem, const void* map, uint64_
       : "memory");
 }
 
+// The same box into L2 only.
+__device__ __forceinline__ void tma_prefetch_2d(const void* map, int c0, int c1) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(c0), "r"(c1)
+               : "memory");
+}
+
 // 3-D tiled load.
 __device__ __forceinline__ void tma_load_3d(void* smem, const void* map, uint64_t* bar, int c0,
                                             int c1, int c2) {

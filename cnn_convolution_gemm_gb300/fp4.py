@@ -31,8 +31,9 @@ def allocating_on(stream):
 
 def rows_of(t: torch.Tensor, cols: int, what: str):
     """(rows, elements between rows) of a tensor [..., cols] whose rows are evenly spaced."""
-    if t.shape[-1] != cols:
-        raise ValueError(f"{what}: last dimension {t.shape[-1]}, expected {cols}")
+    shape = t.shape
+    if shape[-1] != cols:
+        raise ValueError(f"{what}: last dimension {shape[-1]}, expected {cols}")
     if t.is_contiguous():
         return t.numel() // cols, cols
     if t.dim() == 2:

@@ -55,18 +55,16 @@ class ResidualNorm:
         """Returns (x', h).  x' is None when want_x is false, h when there is no norm_pre.
         x_out may be x itself."""
         C, dtype, z_dtype = self.C, self.dtype, self.z_dtype
-        rows, ldx = rows_of(x, C, "x")
+        shape = x.shape
+        device = x.device
+        rows, ldx = (x.numel() // C, C) if shape[-1] == C and x.is_contiguous() else rows_of(x, C, "x")
         if x.dtype is not dtype:
             raise ValueError(f"x: {x.dtype}, expected {dtype}")
-        shape = x.shape
         zp = gp = xop = hp = hsp = None
         ldz = ldg = ldxo = ldh = C
-
-        def same(t, dt):  # the usual tensor: x's shape, contiguous
-            return t.dtype is dt and t.is_contiguous() and t.shape == shape
-
+        # of each tensor first the usual case: x's shape, contiguous
         if z is not None:
-            if same(z, z_dtype):
+            if z.dtype is z_dtype and z.is_contiguous() and z.shape == shape:
                 zp = z.data_ptr()
             else:
                 zp, ldz = self._tensor(z, z_dtype, rows, "z")
@@ -75,8 +73,8 @@ class ResidualNorm:
         if want_x:
             if x_out is None:
                 with allocating_on(stream):
-                    x_out = torch.empty(shape, dtype=dtype, device=x.device)
-            if same(x_out, dtype):
+                    x_out = torch.empty(shape, dtype=dtype, device=device)
+            if x_out.dtype is dtype and x_out.is_contiguous() and x_out.shape == shape:
                 xop = x_out.data_ptr()
             else:
                 xop, ldxo = self._tensor(x_out, dtype, rows, "x_out")
@@ -86,7 +84,7 @@ class ResidualNorm:
             h_out = None
         elif self.h_fmt is not None:
             if h_out is None:
-                h_out = fp4.empty(rows, C, self.h_fmt, x.device, self.h_scale, stream)
+                h_out = fp4.empty(rows, C, self.h_fmt, device, self.h_scale, stream)
             elif (h_out.rows, h_out.cols, h_out.fmt) != (rows, C, self.h_fmt):
                 raise ValueError("h_out: a 4-bit matrix of another shape or format")
             h_out.tensor_scale = self.h_scale
@@ -94,8 +92,8 @@ class ResidualNorm:
         else:
             if h_out is None:
                 with allocating_on(stream):
-                    h_out = torch.empty(shape, dtype=z_dtype, device=x.device)
-            if same(h_out, z_dtype):
+                    h_out = torch.empty(shape, dtype=z_dtype, device=device)
+            if h_out.dtype is z_dtype and h_out.is_contiguous() and h_out.shape == shape:
                 hp = h_out.data_ptr()
             else:
                 hp, ldh = self._tensor(h_out, z_dtype, rows, "h_out")
@@ -104,7 +102,7 @@ class ResidualNorm:
             B.conv_norm_set_strides(self.desc, *strides)
             self._strides = strides
         B.conv_norm_fwd(self.desc, rows, x.data_ptr(), zp, gp, xop, hp, hsp,
-                        stream_handle(stream, x.device))
+                        stream_handle(stream, device))
         return x_out, h_out
 
     __call__ = forward

@@ -31,6 +31,10 @@ class Fp4ResidualBlock:
                  next_scale=1.0):
         self.C, self.hidden, self.fmt, self.dtype = C, hidden, fmt, dtype
         self.h_scale, self.t_scale = h_scale, t_scale
+        for b, n in ((b1, hidden), (b2, C)):
+            if b is not None and (b.dtype != torch.float32 or b.numel() != n
+                                  or not b.is_contiguous()):
+                raise ValueError("b1, b2: expected contiguous fp32 [hidden], [C]")
         self.b1, self.b2 = b1, b2
         self.norm_in = ResidualNorm(C, dtype, torch.bfloat16, eps=eps, pre=B.CONV_NORM_RMS,
                                     w_pre=w_pre, h_fmt=fmt, h_scale=h_scale)
@@ -42,7 +46,7 @@ class Fp4ResidualBlock:
                                      w_post=w_post, pre=B.CONV_NORM_RMS, w_pre=w_next, gate=gate,
                                      gate_rows=gate_rows, residual_scale=residual_scale,
                                      h_fmt=fmt if chain else None, h_scale=next_scale)
-        self._bufs = {}  # stream handle -> (rows, h, t, z)
+        self._bufs = {}  # stream handle -> (rows, h, t, z, their addresses)
 
     def prepack(self, w1, w2, w1_scale=1.0, w2_scale=1.0, stream=None):
         """Quantise the weights w1 [hidden][C], w2 [C][hidden] once."""
@@ -58,22 +62,36 @@ class Fp4ResidualBlock:
         got = self._bufs.get(handle)
         if got is None or got[0] != rows:
             with fp4.allocating_on(stream):
-                got = (rows, fp4.empty(rows, self.C, self.fmt, device, self.h_scale),
-                       fp4.empty(rows, self.hidden, self.fmt, device, self.t_scale),
-                       torch.empty(rows, self.C, dtype=torch.bfloat16, device=device))
+                h = fp4.empty(rows, self.C, self.fmt, device, self.h_scale)
+                t = fp4.empty(rows, self.hidden, self.fmt, device, self.t_scale)
+                z = torch.empty(rows, self.C, dtype=torch.bfloat16, device=device)
+            got = (rows, h, t, z, t.codes.data_ptr(), t.scales.data_ptr(), z.data_ptr())
             self._bufs[handle] = got
-        return got[1:]
+        return got
 
     def forward(self, x, gate=None, h=None, x_out=None, h_out=None, stream=None):
         """x [..., C] -> (x', h').  h: norm_pre(x) in 4 bits when the block before handed
         it on, else None."""
+        w1, w2 = self.fc1.w, self.fc2.w
+        if w1 is None or w2 is None:
+            raise RuntimeError("prepack() or load() the weights first")
         rows, _ = fp4.rows_of(x, self.C, "x")
         handle = fp4.stream_handle(stream, x.device)
-        hb, t, z = self._buffers(rows, x.device, stream, handle)
+        _, hb, _, z, tp, tsp, zp = self._buffers(rows, x.device, stream, handle)
         if h is None:
-            _, h = self.norm_in(x, h_out=hb, want_x=False, stream=stream)
-        self.fc1(h, bias=self.b1, out=t, stream=stream)
-        self.fc2(t, bias=self.b2, out=z, stream=stream)
-        return self.norm_out(x, z, gate=gate, x_out=x_out, h_out=h_out, stream=stream)
+            h = self.norm_in(x, h_out=hb, want_x=False, stream=handle)[1]
+        elif (h.rows, h.cols, h.fmt, h.tensor_scale) != (rows, self.C, self.fmt, self.h_scale):
+            raise ValueError("h: a 4-bit matrix of another shape, format or tensor scale")
+        # the two products between the block's own buffers: the layers' C calls, without
+        # their checks of tensors
+        b1, b2 = self.b1, self.b2
+        B.conv_fp4_fwd(self.fc1.desc, rows, h.codes.data_ptr(), h.scales.data_ptr(),
+                       w1.codes.data_ptr(), w1.scales.data_ptr(),
+                       None if b1 is None else b1.data_ptr(), None, tp, tsp, None, 0, handle)
+        B.conv_fp4_fwd(self.fc2.desc, rows, tp, tsp, w2.codes.data_ptr(), w2.scales.data_ptr(),
+                       None if b2 is None else b2.data_ptr(), None, zp, None, None, 0, handle)
+        if z.dim() != x.dim():
+            z = z.view(x.shape)
+        return self.norm_out(x, z, gate=gate, x_out=x_out, h_out=h_out, stream=handle)
 
     __call__ = forward
