@@ -9,6 +9,8 @@
 
 namespace {
 
+constexpr int MOST = 1 << 30;  // rows and columns: tile arithmetic stays within an int
+
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 size_t elem_bytes(int dtype) { return dtype == CONV_BF16 ? 2 : 4; }
 bool is_float(int dtype) { return dtype == CONV_BF16 || dtype == CONV_F32; }
@@ -41,6 +43,7 @@ conv_status_t check_matrix(int fmt, int dtype, int rows, int cols, const void* t
   if (!is_float(dtype)) return gb_fail(CONV_ERR_BAD_PARAM, "%s must be bf16 or fp32", tname);
   if (rows < 0 || cols <= 0)
     return gb_fail(CONV_ERR_BAD_PARAM, "rows must be >= 0 and cols > 0");
+  if (rows > MOST || cols > MOST) return gb_fail(CONV_ERR_UNSUPPORTED, "more than 2^30 rows or cols");
   if (*ld == 0) *ld = cols;
   if (*ld < cols) return gb_fail(CONV_ERR_BAD_PARAM, "row stride of %s below its row", tname);
   if (rows == 0) return CONV_OK;
@@ -60,6 +63,7 @@ extern "C" conv_status_t conv_fp4_size(conv_fp4_format_t fmt, int rows, int cols
   if (!is_format(fmt)) return gb_fail(CONV_ERR_BAD_PARAM, "unknown 4-bit format %d", (int)fmt);
   if (rows < 0 || cols <= 0)
     return gb_fail(CONV_ERR_BAD_PARAM, "rows must be >= 0 and cols > 0");
+  if (rows > MOST || cols > MOST) return gb_fail(CONV_ERR_UNSUPPORTED, "more than 2^30 rows or cols");
   *cb = code_bytes(rows, cols);
   *sb = scale_bytes(fmt, rows, cols);
   return gb_ok();
@@ -96,6 +100,7 @@ extern "C" conv_status_t conv_fp4_pack_scales(conv_fp4_format_t fmt, int rows, i
   if (!is_format(fmt)) return gb_fail(CONV_ERR_BAD_PARAM, "unknown 4-bit format %d", (int)fmt);
   if (rows < 0 || cols <= 0)
     return gb_fail(CONV_ERR_BAD_PARAM, "rows must be >= 0 and cols > 0");
+  if (rows > MOST || cols > MOST) return gb_fail(CONV_ERR_UNSUPPORTED, "more than 2^30 rows or cols");
   if (rows == 0) return gb_ok();
   if (!src || !scales) return gb_fail(CONV_ERR_BAD_PARAM, "NULL tensor");
   if (!aligned(scales, 16)) return gb_fail(CONV_ERR_ALIGNMENT, "scales must be 16-byte aligned");
@@ -113,6 +118,7 @@ extern "C" conv_status_t conv_fp4_create(conv_fp4_t* out, conv_fp4_format_t fmt,
   *out = nullptr;
   if (!is_format(fmt)) return gb_fail(CONV_ERR_BAD_PARAM, "unknown 4-bit format %d", (int)fmt);
   if (C <= 0 || K <= 0) return gb_fail(CONV_ERR_BAD_PARAM, "sizes must be positive");
+  if (C > MOST || K > MOST) return gb_fail(CONV_ERR_UNSUPPORTED, "more than 2^30 inputs or outputs");
   if (x_io < CONV_FP4_IO_BF16 || x_io > CONV_FP4_IO_CODES || y_io < CONV_FP4_IO_BF16 ||
       y_io > CONV_FP4_IO_CODES)
     return gb_fail(CONV_ERR_BAD_PARAM, "x_io and y_io must be 0, 1 or 2");
@@ -194,6 +200,7 @@ extern "C" conv_status_t conv_fp4_fwd(conv_fp4_t d, int M, const void* x, const 
                                       size_t ws_bytes, void* stream) {
   if (!d) return gb_fail(CONV_ERR_BAD_PARAM, "desc is NULL");
   if (M < 0) return gb_fail(CONV_ERR_BAD_PARAM, "M must be >= 0");
+  if (M > MOST) return gb_fail(CONV_ERR_UNSUPPORTED, "more than 2^30 rows");
   if (M == 0) return gb_ok();
   const bool xc = d->x_io == CONV_FP4_IO_CODES, yc = d->y_io == CONV_FP4_IO_CODES;
   if (!x || !w_codes || !w_scales || !y) return gb_fail(CONV_ERR_BAD_PARAM, "NULL tensor");

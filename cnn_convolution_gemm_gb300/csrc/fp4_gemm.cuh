@@ -9,6 +9,15 @@ namespace fp4 {
 
 constexpr int BKB = 128;  // bytes of a row per k-step: 256 codes
 
+// Rows that a load of a 128-row tile brings: 64 where no more are left of total, none past
+// its end.  A box whose second 64 rows lie outside the matrix altogether is slow (33 .. 63
+// x 4096 x 16384 10.5 us with boxes of 128 rows, 64 or more rows 7.0).
+__host__ __device__ constexpr int box_rows(int row0, int total) {
+  return total - row0 > 64 ? 128 : total - row0 > 0 ? 64 : 0;
+}
+// Whether the last tile of so many rows takes a 64-row box.
+inline bool short_tail(int total) { return box_rows((total - 1) / 128 * 128, total) == 64; }
+
 // [rows][pitch] bytes of codes in boxes of 128 bytes x box_rows
 inline bool codes_map(CUtensorMap* map, const uint8_t* p, int rows, int cols, int box_rows) {
   cuuint64_t dims[2] = {(cuuint64_t)code_pitch(cols), (cuuint64_t)rows};

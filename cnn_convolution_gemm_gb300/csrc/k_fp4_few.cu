@@ -113,7 +113,7 @@ template <int FMT, int XIO, int YIO>
 __global__ void __launch_bounds__(THREADS)
     fp4_few_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_ws,
                    const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_xs,
-                   const FewParams p) {
+                   const __grid_constant__ CUtensorMap tm_w64, const FewParams p) {
   using C = Cfg<FMT>;
   constexpr bool MX = FMT == CONV_FP4_MX;
   constexpr bool FUSED = XIO != CONV_FP4_IO_CODES;
@@ -176,14 +176,16 @@ __global__ void __launch_bounds__(THREADS)
     for (int it = k0; it < k1 && it < k0 + STAGES; ++it)
       if (one) gb::tma_prefetch_2d(&tm_w, it * BKB, tile * 128);
     __syncwarp();
-    const uint32_t tx = C::W_BYTES + C::SF_BYTES + (FUSED ? 0 : x_bytes + C::SF_BYTES);
+    const int wr = box_rows(tile * 128, p.N);
+    const CUtensorMap* const wmap = wr == 64 ? &tm_w64 : &tm_w;
+    const uint32_t tx = wr * BKB + C::SF_BYTES + (FUSED ? 0 : x_bytes + C::SF_BYTES);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     for (int it = k0; it < k1; ++it) {
       if (!gb::mbar_wait_bounded_warp(&empty[stage], phase ^ 1, p.wait_ns, p.err)) break;
       if (one) {
         const int sc = it * (C::ATOMS * 64);  // scale tiles as 8-byte elements
         gb::mbar_arrive_expect_tx(&full[stage], tx);
-        gb::tma_load_2d(sW + stage * C::W_BYTES, &tm_w, &full[stage], it * BKB, tile * 128);
+        gb::tma_load_2d(sW + stage * C::W_BYTES, wmap, &full[stage], it * BKB, tile * 128);
         gb::tma_load_2d(sFW + stage * C::SF_BYTES, &tm_ws, &full[stage], sc, tile);
         if (!FUSED) {
           gb::tma_load_2d(sX + stage * x_bytes, &tm_x, &full[stage], it * BKB, 0);
@@ -394,6 +396,8 @@ cudaError_t launch_t(const Fp4Gemm& g, cudaStream_t st) {
              !scales_map(&txs, g.xs, FMT, g.M, g.C, C::ATOMS, 1)) {
     return cudaErrorInvalidValue;
   }
+  CUtensorMap tw64 = tw;
+  if (short_tail(g.K) && !codes_map(&tw64, g.w, g.K, g.C, 64)) return cudaErrorInvalidValue;
   auto* kern = fp4_few_kernel<FMT, XIO, YIO>;
   const int smem = C::smem(p.nt, split);
   cudaError_t e = gb_set_smem_once(reinterpret_cast<const void*>(kern), smem);
@@ -412,7 +416,7 @@ cudaError_t launch_t(const Fp4Gemm& g, cudaStream_t st) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, kern, tw, tws, tx, txs, p);
+  e = cudaLaunchKernelEx(&cfg, kern, tw, tws, tx, txs, tw64, p);
   if (e == cudaSuccess) gb_count_launch();
   return e;
 }

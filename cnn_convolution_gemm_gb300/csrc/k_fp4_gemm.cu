@@ -29,6 +29,7 @@ struct Cfg {
   static constexpr int ATOMS = FMT == CONV_FP4_MX ? 2 : 4;  // scale tiles per panel and k-step
   static constexpr int PB = (BN + 127) / 128;               // 128-row panels of W
   static constexpr int BROWS = PAIR ? BN / 2 : BN;          // rows of W this CTA loads
+  static_assert(BROWS == 128, "box_rows");
   static constexpr int A_BYTES = BM * BKB;
   static constexpr int B_BYTES = BROWS * BKB;
   static constexpr int SFA_BYTES = ATOMS * 512;
@@ -254,7 +255,8 @@ template <int FMT, int BN, bool PAIR, int YIO>
 __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR, YIO>::THREADS, 1)
     fp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_xs,
                     const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_ws,
-                    const __grid_constant__ CUtensorMap tm_y, const GemmParams p) {
+                    const __grid_constant__ CUtensorMap tm_y, const __grid_constant__ CUtensorMap tm_x64,
+                    const __grid_constant__ CUtensorMap tm_w64, const GemmParams p) {
   using C = Cfg<FMT, BN, PAIR, YIO>;
   constexpr bool MX = FMT == CONV_FP4_MX;
   extern __shared__ uint8_t smem_raw[];
@@ -327,6 +329,15 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR, YIO>::THREADS, 1)
     for (int u = unit0; u < units && ok; u += ustep) {
       const int mt = (u / p.n_tiles) * (PAIR ? 2 : 1) + (int)rank, nt = u % p.n_tiles;
       const int brow = nt * BN + (PAIR ? (int)rank * C::BROWS : 0);
+      // rows past the ends are not loaded: what the tile's memory holds there reaches
+      // accumulators of rows and columns that nobody stores
+      const int ar = box_rows(mt * BM, p.M), br = box_rows(brow, p.N);
+      const CUtensorMap* const xmap = ar == 64 ? &tm_x64 : &tm_x;
+      const CUtensorMap* const wmap = br == 64 ? &tm_w64 : &tm_w;
+      uint32_t tx = (ar + br) * BKB + (ar ? C::SFA_BYTES : 0) + C::SFB_BYTES;
+      if (PAIR)  // of both CTAs
+        tx += (box_rows((mt + 1) * BM, p.M) + box_rows(brow + C::BROWS, p.N)) * BKB +
+              ((mt + 1) * BM < p.M ? C::SFA_BYTES : 0) + C::SFB_BYTES;
       for (int it = 0; it < p.ksteps; ++it) {
         if (!gb::mbar_wait_bounded_warp(&empty[stage], phase ^ 1, p.wait_ns, p.err)) {
           ok = false;
@@ -339,16 +350,16 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR, YIO>::THREADS, 1)
           uint8_t* const fb = sFB + stage * C::SFB_BYTES;
           const int sc = it * (C::ATOMS * 64);  // scale tiles as 8-byte elements
           if constexpr (PAIR) {
-            if (rank == 0) gb::mbar_arrive_expect_tx(&full[stage], 2 * C::STAGE_BYTES);
+            if (rank == 0) gb::mbar_arrive_expect_tx(&full[stage], tx);
             const uint32_t bar = full_pair + stage * 8;
-            gb::tma_load_2d_pair(a, &tm_x, bar, it * BKB, mt * BM);
-            gb::tma_load_2d_pair(b, &tm_w, bar, it * BKB, brow);
-            gb::tma_load_2d_pair(fa, &tm_xs, bar, sc, mt);
+            if (ar) gb::tma_load_2d_pair(a, xmap, bar, it * BKB, mt * BM);
+            if (br) gb::tma_load_2d_pair(b, wmap, bar, it * BKB, brow);
+            if (ar) gb::tma_load_2d_pair(fa, &tm_xs, bar, sc, mt);
             gb::tma_load_2d_pair(fb, &tm_ws, bar, sc, nt * BN / 128);
           } else {
-            gb::mbar_arrive_expect_tx(&full[stage], C::STAGE_BYTES);
-            gb::tma_load_2d(a, &tm_x, &full[stage], it * BKB, mt * BM);
-            gb::tma_load_2d(b, &tm_w, &full[stage], it * BKB, brow);
+            gb::mbar_arrive_expect_tx(&full[stage], tx);
+            gb::tma_load_2d(a, xmap, &full[stage], it * BKB, mt * BM);
+            gb::tma_load_2d(b, wmap, &full[stage], it * BKB, brow);
             gb::tma_load_2d(fa, &tm_xs, &full[stage], sc, mt);
             gb::tma_load_2d(fb, &tm_ws, &full[stage], sc, nt * BN / 128);
           }
@@ -612,7 +623,10 @@ cudaError_t launch_tile(const Fp4Gemm& g, cudaStream_t st) {
     p.vec_y = rows_vec<float>(g.y, g.ldy, 16);
     p.vec_r = rows_vec<float>(g.res, g.ldr, 16);
   }
-  CUtensorMap ty = tx;
+  CUtensorMap ty = tx, tx64 = tx, tw64 = tw;
+  if ((short_tail(g.M) && !codes_map(&tx64, g.x, g.M, g.C, 64)) ||
+      (short_tail(g.K) && !codes_map(&tw64, g.w, g.K, g.C, 64)))
+    return cudaErrorInvalidValue;
   if (YIO != CONV_FP4_IO_CODES && p.vec_y) {  // boxes of 32 rows x 64 bytes
     constexpr cuuint64_t es = YIO == CONV_FP4_IO_BF16 ? 2 : 4;
     cuuint64_t dims[2] = {(cuuint64_t)g.K, (cuuint64_t)g.M};
@@ -653,7 +667,7 @@ cudaError_t launch_tile(const Fp4Gemm& g, cudaStream_t st) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = PAIR ? 2 : 1;
-  e = cudaLaunchKernelEx(&cfg, kern, tx, txs, tw, tws, ty, p);
+  e = cudaLaunchKernelEx(&cfg, kern, tx, txs, tw, tws, ty, tx64, tw64, p);
   if (e == cudaSuccess) gb_count_launch();
   return e;
 }

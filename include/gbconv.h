@@ -358,7 +358,8 @@ conv_status_t conv_global_avgpool_nhwc_bf16(const void* x, void* y, int N, int C
  * magnitudes above 6 become 6; 0 where the scale is 0).  A block that holds an
  * infinity or a NaN gets the scale NaN (byte 0xFF; 0x7F for NV) and codes 0: its
  * values are NaN, so the fault stays visible in every product it enters.
- * tensor_scale: 1e-30 .. 1e30; it must be 1 for CONV_FP4_MX.
+ * tensor_scale: 1e-30 .. 1e30; it must be 1 for CONV_FP4_MX.  Up to 2^30 rows and
+ * columns.
  *
  * In memory:
  *   codes   [rows][P] bytes, P = 16 * ceil(cols / 32); element c of a row is the

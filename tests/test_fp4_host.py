@@ -34,6 +34,9 @@ def test_sizes(B):
     assert B.conv_fp4_size(B.CONV_FP4_NV, 0, 64) == (0, 0)
     # past 32 bits
     assert B.conv_fp4_size(B.CONV_FP4_MX, 1 << 20, 1 << 14) == (1 << 33, 1 << 29)
+    refused(B, UNSUP, B.conv_fp4_size, B.CONV_FP4_MX, (1 << 30) + 1, 4)
+    refused(B, UNSUP, B.conv_fp4_quantize, B.CONV_FP4_MX, B.CONV_BF16, 4, (1 << 30) + 1, P, 0, 1.0, P, P)
+    refused(B, UNSUP, B.conv_fp4_create, B.CONV_FP4_MX, (1 << 30) + 1, 64)
     refused(B, BAD, B.conv_fp4_size, 2, 4, 4)
     refused(B, BAD, B.conv_fp4_size, B.CONV_FP4_MX, -1, 4)
     refused(B, BAD, B.conv_fp4_size, B.CONV_FP4_MX, 4, 0)
@@ -82,6 +85,7 @@ def test_product_refusals(B):
     assert need >= sum(B.conv_fp4_size(NV, 200, 96))
     f = B.conv_fp4_fwd
     refused(B, BAD, f, d, -1, P, None, P, P, None, None, P, None, P, need)
+    refused(B, UNSUP, f, d, (1 << 30) + 1, P, None, P, P, None, None, P, None, P, 1 << 60)
     refused(B, BAD, f, d, 200, None, None, P, P, None, None, P, None, P, need)
     refused(B, BAD, f, d, 200, P, P, P, P, None, None, P, None, P, need)      # scales of a float x
     refused(B, BAD, f, d, 200, P, None, P, P, None, None, P, P, P, need)      # scales of a float y

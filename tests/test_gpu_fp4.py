@@ -41,7 +41,8 @@ def _f32(t):
 @pytest.mark.parametrize("fmt", FMTS, ids=NAMES.get)
 @pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
 @pytest.mark.parametrize("rows,cols", [(1, 1), (1, 4096), (3, 16), (5, 31), (2, 33), (130, 64),
-                                       (7, 100), (257, 272), (64, 1000), (33, 2080), (300, 129)])
+                                       (7, 100), (257, 272), (64, 1000), (33, 2080), (300, 129),
+                                       (5000, 96), (2000, 200), (700, 5000)])
 def test_quantize_is_the_definition(fmt, dtype, rows, cols):
     torch, fp4 = _fp4()
     rng = np.random.default_rng(rows * 10007 + cols)
@@ -216,8 +217,39 @@ def test_product_strided_rows(fmt, M, C, K, dtype):
     _product(fmt, M, C, K, dtype, dtype, 1, True, True, strided=True)
 
 
+# more tiles than the SMs take at once: 256 x 256 tiles over SM pairs, several to a pair; a
+# second half of a pair's rows or columns that is empty, or up to 64 of 128; one and
+# several k-steps
 @pytest.mark.parametrize("fmt", FMTS, ids=NAMES.get)
-@pytest.mark.parametrize("M,C,K", [(4, 256, 96), (150, 512, 300)])
+@pytest.mark.parametrize("M,C,K,x,y,act,bias,residual", [
+    (2600, 1100, 1100, "bfloat16", "bfloat16", 1, True, True),
+    (2600, 1100, 1104, None, "float32", 3, True, False),
+    (5200, 64, 1025, "bfloat16", "bfloat16", 0, True, False),
+    (4097, 200, 1300, "float32", "bfloat16", 4, False, True),
+    (5250, 520, 1160, "bfloat16", None, 3, True, False),
+    (3000, 272, 2096, None, None, 0, False, False),
+    (2688, 2100, 1056, None, "float32", 2, True, True),
+    (33, 96, 20000, "bfloat16", "bfloat16", 0, True, True)])
+def test_product_of_many_tiles(fmt, M, C, K, x, y, act, bias, residual):
+    _product(fmt, M, C, K, x, y, act, bias, residual)
+
+
+@pytest.mark.parametrize("fmt", FMTS, ids=NAMES.get)
+def test_product_of_many_tiles_strided(fmt):
+    _product(fmt, 2700, 1090, 1115, "bfloat16", "bfloat16", 1, True, True, strided=True)
+    _product(fmt, 2700, 1090, 1115, "float32", "float32", 0, True, True, strided=True)
+
+
+@pytest.mark.parametrize("fmt", FMTS, ids=NAMES.get)
+@pytest.mark.parametrize("M", [1, 2, 3, 4, 5, 8, 9, 31, 32, 33, 40, 64, 65, 127, 160, 192])
+@pytest.mark.parametrize("C,K", [(4500, 200), (1024, 1100)])
+def test_product_of_few_rows(fmt, M, C, K):
+    """Every way that rows are shared out, with the reduction split and whole."""
+    _product(fmt, M, C, K, "bfloat16", "float32", 0, True, M % 2 == 0)
+
+
+@pytest.mark.parametrize("fmt", FMTS, ids=NAMES.get)
+@pytest.mark.parametrize("M,C,K", [(4, 256, 96), (150, 512, 300), (2600, 1100, 1100)])
 def test_product_infinities_stay_in_their_rows(fmt, M, C, K):
     """A row of x that holds an Inf or a NaN gives a row of NaN; the other rows, and the
     rows of zeros, are untouched.  The same for a row of the weights and its column."""
@@ -252,17 +284,21 @@ def test_product_rows_do_not_depend_on_their_neighbours(fmt):
     y = layer(x)
     assert torch.equal(y, layer(x))
     assert torch.equal(y[200:], layer(x[200:]))
+    wide = fp4.Fp4Linear(C, 3100, fmt, y_dtype=torch.float32)
+    wide.prepack(_to(torch, rng.standard_normal((3100, C)), torch.bfloat16))
+    xx = torch.cat([x] * 5)
+    yy = wide(xx)
+    assert torch.equal(yy, wide(xx)) and torch.equal(yy[:600], yy[2400:])
     small = layer(x[:9])
     assert torch.equal(small, layer(x[:9]))
     assert torch.equal(small[4:], layer(x[4:9]))
 
 
 @pytest.mark.parametrize("fmt", FMTS, ids=NAMES.get)
-@pytest.mark.parametrize("M", [2, 200])
-def test_product_into_its_residual(fmt, M):
+@pytest.mark.parametrize("M,C,K", [(2, 192, 136), (200, 192, 136), (200, 192, 135), (2600, 1100, 1104)])
+def test_product_into_its_residual(fmt, M, C, K):
     torch, fp4 = _fp4()
     rng = np.random.default_rng(8)
-    C, K = 192, 136
     x, r = _to(torch, _activations(rng, M, C), torch.bfloat16), _to(
         torch, rng.standard_normal((M, K)), torch.bfloat16)
     layer = fp4.Fp4Linear(C, K, fmt, has_residual=True)

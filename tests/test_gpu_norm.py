@@ -129,6 +129,18 @@ def test_quantized_output(h_fmt, rows, C):
     _case(LN, LN, rows, C, dt="float32", zdt="bfloat16", h_fmt=h_fmt, gate=2)
 
 
+@pytest.mark.parametrize("post,pre,rows,C,kw", [
+    (RMS, RMS, 1301, 8192, {}), (LN, LN, 1301, 8192, {}), (LN, LN, 1300, 8192, {"dt": "float32"}),
+    (RMS, LN, 2501, 4096, {"gate": 2, "gate_rows": 7}), (LN, RMS, 2501, 4096, {"dt": "float32"}),
+    (N, RMS, 10001, 1024, {}), (RMS, N, 10001, 1024, {"gate": 1, "gate_rows": 196}),
+    (RMS, RMS, 5003, 2048, {"h_fmt": R.MX}), (LN, LN, 5003, 2040, {"h_fmt": R.NV, "gate": 1}),
+    (RMS, RMS, 1303, 7000, {"in_place": True}), (RMS, RMS, 2501, 4096, {"dt": "float32", "zdt": "bfloat16"}),
+    (RMS, RMS, 1303, 8192, {"weights": False}), (RMS, RMS, 3001, 4001, {}), (N, LN, 3001, 4096, {"with_z": False})])
+def test_many_rows(post, pre, rows, C, kw):
+    """Rows that come ahead of their turn, two at a time, and an odd one last."""
+    _case(post, pre, rows, C, **kw)
+
+
 def test_mixed_types_strides_in_place_and_first_norm():
     _case(RMS, LN, 20, 320, dt="float32", zdt="bfloat16")
     _case(RMS, LN, 20, 320, dt="bfloat16", zdt="float32")
