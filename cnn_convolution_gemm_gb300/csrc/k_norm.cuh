@@ -211,17 +211,35 @@ __device__ __forceinline__ void norm_rows(float (&v)[R][N], int kind, float eps,
   float f[R];
 #pragma unroll
   for (int k = 0; k < R; ++k) f[k] = rsqrtf(fmaf(sum[k], inv, eps));
+  if (w.w) {
 #pragma unroll
-  for (int i = 0; i < N; i += 4) {
-    float4 e = make_float4(1.0f, 1.0f, 1.0f, 1.0f), d = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (w.w) e = w.get(i, t, C, vec_w);
-    if (b.w) d = b.get(i, t, C, vec_w);
+    for (int i = 0; i < N; i += 4) {
+      const float4 e = w.get(i, t, C, vec_w);
 #pragma unroll
-    for (int k = 0; k < R; ++k) {
-      v[k][i] = fmaf(v[k][i] * f[k], e.x, d.x);
-      v[k][i + 1] = fmaf(v[k][i + 1] * f[k], e.y, d.y);
-      v[k][i + 2] = fmaf(v[k][i + 2] * f[k], e.z, d.z);
-      v[k][i + 3] = fmaf(v[k][i + 3] * f[k], e.w, d.w);
+      for (int k = 0; k < R; ++k) {
+        v[k][i] *= f[k] * e.x;
+        v[k][i + 1] *= f[k] * e.y;
+        v[k][i + 2] *= f[k] * e.z;
+        v[k][i + 3] *= f[k] * e.w;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < R; ++k)
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[k][i] *= f[k];
+  }
+  if (b.w) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const float4 e = b.get(i, t, C, vec_w);
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        v[k][i] += e.x;
+        v[k][i + 1] += e.y;
+        v[k][i + 2] += e.z;
+        v[k][i + 3] += e.w;
+      }
     }
   }
 }
@@ -261,7 +279,7 @@ __device__ __forceinline__ void store_h(const NormArgs& a, const TensorScale& ts
 }
 
 // T == 32: one row per warp (4 in a block), else R rows at a time per block of T threads.
-// AHEAD (VEC, T > 32, z given): x and z come through the ring; else R is 1.
+// AHEAD (VEC, T > 32): x and z (if given) come through the ring; else R is 1.
 template <typename TX, typename TZ, int T, int N, bool VEC, bool AHEAD, int R>
 __global__ void __launch_bounds__(T == 32 ? 128 : T)
     norm_kernel(const NormArgs a, const TensorScale ts, const Vec vec) {
@@ -275,13 +293,13 @@ __global__ void __launch_bounds__(T == 32 ? 128 : T)
   const long long step = T == 32 ? gridDim.x * 4LL : (long long)gridDim.x * R;
   const long long first = T == 32 ? blockIdx.x * 4LL + (threadIdx.x >> 5) : (long long)blockIdx.x * R;
   const float inv = 1.0f / (float)C;
-  const uint32_t zb = (uint32_t)C * sizeof(TZ), xb = (uint32_t)C * sizeof(TX);
+  const uint32_t zb = a.z ? (uint32_t)C * sizeof(TZ) : 0u, xb = (uint32_t)C * sizeof(TX);
   const auto fetch = [&](long long r, int stage) {  // one thread
     uint8_t* to = reinterpret_cast<uint8_t*>(ring) + stage * (size_t)(zb + xb) * R;
     const int rows = (int)(a.rows - r < R ? a.rows - r : R);
     gb::mbar_arrive_expect_tx(&full[stage], (zb + xb) * rows);
     for (int k = 0; k < rows; ++k, to += zb + xb) {
-      gb::bulk_load(to, static_cast<const TZ*>(a.z) + (r + k) * a.ldz, &full[stage], zb);
+      if (a.z) gb::bulk_load(to, static_cast<const TZ*>(a.z) + (r + k) * a.ldz, &full[stage], zb);
       gb::bulk_load(to + zb, static_cast<const TX*>(a.x) + (r + k) * a.ldx, &full[stage], xb);
     }
   };
@@ -326,25 +344,28 @@ __global__ void __launch_bounds__(T == 32 ? 128 : T)
       rx.load(static_cast<const TX*>(a.x) + r * a.ldx, t, C, vec.x);
     }
     float v[R][N];
-    if (AHEAD || a.z) {
+    if (a.z) {
       float u[R][N];
+      RowRegs<TZ, T, N, VEC> rg[R];
 #pragma unroll
       for (int k = 0; k < R; ++k) {
         if constexpr (AHEAD)
           read_shared<TZ, T, N>(u[k], sz + k * (zb + xb), t, C);
         else
           rz.get(u[k]);
+        if (a.gate_kind != CONV_GATE_NONE) {
+          // rows and gate_rows are ints: a 32-bit division
+          const unsigned row = (unsigned)(r + k < a.rows ? r + k : r);
+          rg[k].load(static_cast<const TZ*>(a.gate) + (long long)(row / (unsigned)a.gate_rows) * a.ldg,
+                     t, C, vec.g);
+        }
       }
       if (a.post != CONV_NORM_NONE)
         norm_rows<T, N, VEC, R>(u, a.post, a.eps_post, w_post, b_post, t, C, vec.w, inv, red, turn);
 #pragma unroll
       for (int k = 0; k < R; ++k) {
         if (a.gate_kind != CONV_GATE_NONE) {
-          // rows and gate_rows are ints: a 32-bit division
-          const unsigned row = (unsigned)(r + k < a.rows ? r + k : r);
-          rz.load(static_cast<const TZ*>(a.gate) + (long long)(row / (unsigned)a.gate_rows) * a.ldg,
-                  t, C, vec.g);
-          rz.get(v[k]);
+          rg[k].get(v[k]);
 #pragma unroll
           for (int i = 0; i < N; ++i) {
             // the logistic function within 2^-21
@@ -361,7 +382,13 @@ __global__ void __launch_bounds__(T == 32 ? 128 : T)
         for (int i = 0; i < N; ++i) v[k][i] = fmaf(a.rs, u[k][i], v[k][i]);
       }
     } else {
-      rx.get(v[0]);
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        if constexpr (AHEAD)
+          read_shared<TX, T, N>(v[k], sz + k * (zb + xb), t, C);
+        else
+          rx.get(v[k]);
+      }
     }
     if (a.x_out) {
 #pragma unroll
@@ -470,7 +497,7 @@ template <typename TX, typename TZ, int T, int R>
 int ahead_smem(const NormArgs& a) {
   const int n = (a.w_post != nullptr) + (a.b_post != nullptr) + (a.w_pre != nullptr) +
                 (a.b_pre != nullptr);
-  const int smem = RING * R * a.C * (int)(sizeof(TX) + sizeof(TZ)) + n * T * 64;
+  const int smem = RING * R * a.C * (int)(sizeof(TX) + (a.z ? sizeof(TZ) : 0)) + n * T * 64;
   return smem <= 224 * 1024 ? smem : 0;
 }
 
@@ -488,7 +515,7 @@ cudaError_t launch(const NormArgs& a, cudaStream_t st) {
   // 16 consecutive columns a thread where that makes 32-byte loads, or codes
   const bool vec = rows_vec<TX>(a.x, a.ldx, 32) && (!a.z || rows_vec<TZ>(a.z, a.ldz, 32));
   // many rows of whole 16-byte pieces: two at a time, through the ring
-  if (vec && a.z && a.C > 512 && a.C <= 8192 && a.C * sizeof(TX) % 16 == 0 &&
+  if (vec && a.C > 512 && a.C <= 8192 && a.C * sizeof(TX) % 16 == 0 &&
       a.C * sizeof(TZ) % 16 == 0 && a.rows >= 2LL * gb_num_sms() * (8192 / a.C) * 4) {
     if (a.C <= 1024) return launch_ahead<TX, TZ, 64, 2>(a, st);
     if (a.C <= 2048) return launch_ahead<TX, TZ, 128, 2>(a, st);
