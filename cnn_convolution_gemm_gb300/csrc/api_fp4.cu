@@ -43,7 +43,8 @@ conv_status_t check_matrix(int fmt, int dtype, int rows, int cols, const void* t
   if (!is_float(dtype)) return gb_fail(CONV_ERR_BAD_PARAM, "%s must be bf16 or fp32", tname);
   if (rows < 0 || cols <= 0)
     return gb_fail(CONV_ERR_BAD_PARAM, "rows must be >= 0 and cols > 0");
-  if (rows > MOST || cols > MOST) return gb_fail(CONV_ERR_UNSUPPORTED, "more than 2^30 rows or cols");
+  if (rows > MOST || cols > MOST)
+    return gb_fail(CONV_ERR_UNSUPPORTED, "more than 2^30 rows or cols");
   if (*ld == 0) *ld = cols;
   if (*ld < cols) return gb_fail(CONV_ERR_BAD_PARAM, "row stride of %s below its row", tname);
   if (rows == 0) return CONV_OK;
@@ -63,7 +64,8 @@ extern "C" conv_status_t conv_fp4_size(conv_fp4_format_t fmt, int rows, int cols
   if (!is_format(fmt)) return gb_fail(CONV_ERR_BAD_PARAM, "unknown 4-bit format %d", (int)fmt);
   if (rows < 0 || cols <= 0)
     return gb_fail(CONV_ERR_BAD_PARAM, "rows must be >= 0 and cols > 0");
-  if (rows > MOST || cols > MOST) return gb_fail(CONV_ERR_UNSUPPORTED, "more than 2^30 rows or cols");
+  if (rows > MOST || cols > MOST)
+    return gb_fail(CONV_ERR_UNSUPPORTED, "more than 2^30 rows or cols");
   *cb = code_bytes(rows, cols);
   *sb = scale_bytes(fmt, rows, cols);
   return gb_ok();
@@ -100,7 +102,8 @@ extern "C" conv_status_t conv_fp4_pack_scales(conv_fp4_format_t fmt, int rows, i
   if (!is_format(fmt)) return gb_fail(CONV_ERR_BAD_PARAM, "unknown 4-bit format %d", (int)fmt);
   if (rows < 0 || cols <= 0)
     return gb_fail(CONV_ERR_BAD_PARAM, "rows must be >= 0 and cols > 0");
-  if (rows > MOST || cols > MOST) return gb_fail(CONV_ERR_UNSUPPORTED, "more than 2^30 rows or cols");
+  if (rows > MOST || cols > MOST)
+    return gb_fail(CONV_ERR_UNSUPPORTED, "more than 2^30 rows or cols");
   if (rows == 0) return gb_ok();
   if (!src || !scales) return gb_fail(CONV_ERR_BAD_PARAM, "NULL tensor");
   if (!aligned(scales, 16)) return gb_fail(CONV_ERR_ALIGNMENT, "scales must be 16-byte aligned");
@@ -118,7 +121,8 @@ extern "C" conv_status_t conv_fp4_create(conv_fp4_t* out, conv_fp4_format_t fmt,
   *out = nullptr;
   if (!is_format(fmt)) return gb_fail(CONV_ERR_BAD_PARAM, "unknown 4-bit format %d", (int)fmt);
   if (C <= 0 || K <= 0) return gb_fail(CONV_ERR_BAD_PARAM, "sizes must be positive");
-  if (C > MOST || K > MOST) return gb_fail(CONV_ERR_UNSUPPORTED, "more than 2^30 inputs or outputs");
+  if (C > MOST || K > MOST)
+    return gb_fail(CONV_ERR_UNSUPPORTED, "more than 2^30 inputs or outputs");
   if (x_io < CONV_FP4_IO_BF16 || x_io > CONV_FP4_IO_CODES || y_io < CONV_FP4_IO_BF16 ||
       y_io > CONV_FP4_IO_CODES)
     return gb_fail(CONV_ERR_BAD_PARAM, "x_io and y_io must be 0, 1 or 2");
@@ -258,7 +262,8 @@ extern "C" conv_status_t conv_fp4_fwd(conv_fp4_t d, int M, const void* x, const 
   }
   // up to 32 rows on the kernel that splits the reduction; up to 64 where it is long and
   // the outputs few (64 x 8192 x 2048: 128 x 128 tiles 10.5 us)
-  const bool few = M <= 32 || (M <= 64 && d->C >= 4096 && 4LL * ((d->K + 127) / 128) <= gb_num_sms());
+  const bool few =
+      M <= 32 || (M <= 64 && d->C >= 4096 && 4LL * ((d->K + 127) / 128) <= gb_num_sms());
   return cuda_status(few ? launch_fp4_few(g, st) : launch_fp4_gemm(g, st), "4-bit product");
 }
 

@@ -205,8 +205,8 @@ __device__ __forceinline__ float scale_value(uint32_t byte, float tensor_scale) 
 // tile (complete in each of the tile's lanes).  MX: two lanes share a block and eight a
 // scale tile; NV: one and four; all lanes call it.
 template <int FMT>
-__device__ __forceinline__ void quantize16(const float (&v)[16], const TensorScale& ts, uint2& codes,
-                                           uint32_t& word) {
+__device__ __forceinline__ void quantize16(const float (&v)[16], const TensorScale& ts,
+                                           uint2& codes, uint32_t& word) {
   constexpr int LB = kBlock<FMT> / 16;  // lanes per block
   float top = 0.0f;
 #pragma unroll

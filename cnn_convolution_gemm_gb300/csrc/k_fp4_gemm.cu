@@ -2,9 +2,16 @@
 // on the block-scaled tcgen05 MMAs.
 //
 // GEMM names here: M rows of X, N rows of W (the layer's outputs), KR the reduction.
-// Persistent CTAs: warp 0 loads (TMA), warp 1 copies the block
-// scales to TMEM and issues the MMAs (one elected lane), warps 4 and up run the epilogue.  A k-step is
-// 256 elements: 128-byte rows of codes (128-byte swizzle) and 512-byte scale tiles.
+// Persistent CTAs: warp 0 loads (TMA), warp 1 copies the block scales to TMEM and issues
+// the MMAs (one elected lane), warps 4 and up run the epilogue.  A k-step is 256 elements:
+// 128-byte rows of codes (128-byte swizzle) and 512-byte scale tiles.
+//
+// Bound: shared memory.  A k-step of a 256 x 256 tile over an SM pair takes 513 cycles of
+// MMAs (K = 64 each, measured alone); its 35 KB of operands (MX; NV 38 KB) are written by
+// the TMA and read by the MMAs and scale copies at 128 bytes a cycle together: 547 (594).
+// An MMA with K = 96 would not change that, which is why there is none here.  Measured:
+// 8192 x 16384 x 4096 133 us MX, 140 NV (8.3, 7.9 PFLOP/s) at 2.07 GHz; under a long dense
+// load the power limit lowers the clock to about 1.75 GHz.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -143,9 +150,9 @@ struct Block {
 // the TMA: committed, and the buffer waited for before it is written again).
 // pre: the residual, fetched ahead; refill() fetches what the warp needs next.
 template <typename T, typename F>
-__device__ __forceinline__ void finish_float(const GemmParams& p, const CUtensorMap* tm_y, float (&v)[Block<T>::COLS],
-                                             uint8_t* buf, int m0, int n0, const uint32_t (&pre)[16],
-                                             F refill) {
+__device__ __forceinline__ void finish_float(const GemmParams& p, const CUtensorMap* tm_y,
+                                             float (&v)[Block<T>::COLS], uint8_t* buf, int m0,
+                                             int n0, const uint32_t (&pre)[16], F refill) {
   using B = Block<T>;
   const int lane = threadIdx.x & 31;
   const int rows = min(32, p.M - m0), cols = min(B::COLS, p.N - n0);
@@ -253,9 +260,12 @@ __device__ __forceinline__ void finish_codes(const GemmParams& p, float (&v)[32]
 
 template <int FMT, int BN, bool PAIR, int YIO>
 __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR, YIO>::THREADS, 1)
-    fp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_xs,
-                    const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_ws,
-                    const __grid_constant__ CUtensorMap tm_y, const __grid_constant__ CUtensorMap tm_x64,
+    fp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_x,
+                    const __grid_constant__ CUtensorMap tm_xs,
+                    const __grid_constant__ CUtensorMap tm_w,
+                    const __grid_constant__ CUtensorMap tm_ws,
+                    const __grid_constant__ CUtensorMap tm_y,
+                    const __grid_constant__ CUtensorMap tm_x64,
                     const __grid_constant__ CUtensorMap tm_w64, const GemmParams p) {
   using C = Cfg<FMT, BN, PAIR, YIO>;
   constexpr bool MX = FMT == CONV_FP4_MX;
@@ -316,160 +326,160 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR, YIO>::THREADS, 1)
   const int units = p.m_tiles * p.n_tiles;
   // 256 columns: the launch's registers, 640 x 96, as 128 x 40 + 512 x 104 (at most)
   if (warp < 4) {
-  if constexpr (BN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-  if (warp == 0) {
-    // ---------------- TMA producer ----------------
-    const bool one = gb::elect_one();
-    int stage = 0;
-    uint32_t phase = 0;
-    long long issued = 0;
-    bool ok = true;
-    const uint32_t full_pair = PAIR ? gb::mapa_shared(gb::smem_u32(full), 0) : 0u;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    for (int u = unit0; u < units && ok; u += ustep) {
-      const int mt = (u / p.n_tiles) * (PAIR ? 2 : 1) + (int)rank, nt = u % p.n_tiles;
-      const int brow = nt * BN + (PAIR ? (int)rank * C::BROWS : 0);
-      // rows past the ends are not loaded: what the tile's memory holds there reaches
-      // accumulators of rows and columns that nobody stores
-      const int ar = box_rows(mt * BM, p.M), br = box_rows(brow, p.N);
-      const CUtensorMap* const xmap = ar == 64 ? &tm_x64 : &tm_x;
-      const CUtensorMap* const wmap = br == 64 ? &tm_w64 : &tm_w;
-      uint32_t tx = (ar + br) * BKB + (ar ? C::SFA_BYTES : 0) + C::SFB_BYTES;
-      if (PAIR)  // of both CTAs
-        tx += (box_rows((mt + 1) * BM, p.M) + box_rows(brow + C::BROWS, p.N)) * BKB +
-              ((mt + 1) * BM < p.M ? C::SFA_BYTES : 0) + C::SFB_BYTES;
-      for (int it = 0; it < p.ksteps; ++it) {
-        if (!gb::mbar_wait_bounded_warp(&empty[stage], phase ^ 1, p.wait_ns, p.err)) {
-          ok = false;
-          break;
-        }
-        if (one) {
-          uint8_t* const a = sA + stage * C::A_BYTES;
-          uint8_t* const b = sB + stage * C::B_BYTES;
-          uint8_t* const fa = sFA + stage * C::SFA_BYTES;
-          uint8_t* const fb = sFB + stage * C::SFB_BYTES;
-          const int sc = it * (C::ATOMS * 64);  // scale tiles as 8-byte elements
-          if constexpr (PAIR) {
-            if (rank == 0) gb::mbar_arrive_expect_tx(&full[stage], tx);
-            const uint32_t bar = full_pair + stage * 8;
-            if (ar) gb::tma_load_2d_pair(a, xmap, bar, it * BKB, mt * BM);
-            if (br) gb::tma_load_2d_pair(b, wmap, bar, it * BKB, brow);
-            if (ar) gb::tma_load_2d_pair(fa, &tm_xs, bar, sc, mt);
-            gb::tma_load_2d_pair(fb, &tm_ws, bar, sc, nt * BN / 128);
-          } else {
-            gb::mbar_arrive_expect_tx(&full[stage], tx);
-            gb::tma_load_2d(a, xmap, &full[stage], it * BKB, mt * BM);
-            gb::tma_load_2d(b, wmap, &full[stage], it * BKB, brow);
-            gb::tma_load_2d(fa, &tm_xs, &full[stage], sc, mt);
-            gb::tma_load_2d(fb, &tm_ws, &full[stage], sc, nt * BN / 128);
+    if constexpr (BN == 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if (warp == 0) {
+      // ---------------- TMA producer ----------------
+      const bool one = gb::elect_one();
+      int stage = 0;
+      uint32_t phase = 0;
+      long long issued = 0;
+      bool ok = true;
+      const uint32_t full_pair = PAIR ? gb::mapa_shared(gb::smem_u32(full), 0) : 0u;
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      for (int u = unit0; u < units && ok; u += ustep) {
+        const int mt = (u / p.n_tiles) * (PAIR ? 2 : 1) + (int)rank, nt = u % p.n_tiles;
+        const int brow = nt * BN + (PAIR ? (int)rank * C::BROWS : 0);
+        // rows past the ends are not loaded: what the tile's memory holds there reaches
+        // accumulators of rows and columns that nobody stores
+        const int ar = box_rows(mt * BM, p.M), br = box_rows(brow, p.N);
+        const CUtensorMap* const xmap = ar == 64 ? &tm_x64 : &tm_x;
+        const CUtensorMap* const wmap = br == 64 ? &tm_w64 : &tm_w;
+        uint32_t tx = (ar + br) * BKB + (ar ? C::SFA_BYTES : 0) + C::SFB_BYTES;
+        if (PAIR)  // of both CTAs
+          tx += (box_rows((mt + 1) * BM, p.M) + box_rows(brow + C::BROWS, p.N)) * BKB +
+                ((mt + 1) * BM < p.M ? C::SFA_BYTES : 0) + C::SFB_BYTES;
+        for (int it = 0; it < p.ksteps; ++it) {
+          if (!gb::mbar_wait_bounded_warp(&empty[stage], phase ^ 1, p.wait_ns, p.err)) {
+            ok = false;
+            break;
+          }
+          if (one) {
+            uint8_t* const a = sA + stage * C::A_BYTES;
+            uint8_t* const b = sB + stage * C::B_BYTES;
+            uint8_t* const fa = sFA + stage * C::SFA_BYTES;
+            uint8_t* const fb = sFB + stage * C::SFB_BYTES;
+            const int sc = it * (C::ATOMS * 64);  // scale tiles as 8-byte elements
+            if constexpr (PAIR) {
+              if (rank == 0) gb::mbar_arrive_expect_tx(&full[stage], tx);
+              const uint32_t bar = full_pair + stage * 8;
+              if (ar) gb::tma_load_2d_pair(a, xmap, bar, it * BKB, mt * BM);
+              if (br) gb::tma_load_2d_pair(b, wmap, bar, it * BKB, brow);
+              if (ar) gb::tma_load_2d_pair(fa, &tm_xs, bar, sc, mt);
+              gb::tma_load_2d_pair(fb, &tm_ws, bar, sc, nt * BN / 128);
+            } else {
+              gb::mbar_arrive_expect_tx(&full[stage], tx);
+              gb::tma_load_2d(a, xmap, &full[stage], it * BKB, mt * BM);
+              gb::tma_load_2d(b, wmap, &full[stage], it * BKB, brow);
+              gb::tma_load_2d(fa, &tm_xs, &full[stage], sc, mt);
+              gb::tma_load_2d(fb, &tm_ws, &full[stage], sc, nt * BN / 128);
+            }
+          }
+          __syncwarp();
+          ++issued;
+          if (++stage == C::STAGES) {
+            stage = 0;
+            phase ^= 1;
           }
         }
-        __syncwarp();
-        ++issued;
-        if (++stage == C::STAGES) {
-          stage = 0;
+      }
+      // no copy into shared memory may be in flight at exit (pair: the even CTA's
+      // barriers count both CTAs' bytes, so it drains for both)
+      long long pending = issued < C::STAGES ? issued : C::STAGES;
+      if (PAIR && rank != 0) pending = 0;
+      for (long long i = 0; i < pending; ++i) {
+        if (--stage < 0) {
+          stage = C::STAGES - 1;
           phase ^= 1;
         }
+        gb::mbar_wait_bounded_warp(&full[stage], phase, p.wait_ns, p.err);
       }
-    }
-    // no copy into shared memory may be in flight at exit (pair: the even CTA's
-    // barriers count both CTAs' bytes, so it drains for both)
-    long long pending = issued < C::STAGES ? issued : C::STAGES;
-    if (PAIR && rank != 0) pending = 0;
-    for (long long i = 0; i < pending; ++i) {
-      if (--stage < 0) {
-        stage = C::STAGES - 1;
-        phase ^= 1;
-      }
-      gb::mbar_wait_bounded_warp(&full[stage], phase, p.wait_ns, p.err);
-    }
-  } else if (warp == 1 && rank == 0) {
-    // ---------------- scale copies and MMAs ----------------
-    const bool one = gb::elect_one();
-    constexpr int MM = PAIR ? 2 * BM : BM;
-    int stage = 0, acc = 0;
-    uint32_t phase = 0, acc_phase = 0;
-    bool ok = true;
-    for (int u = unit0; u < units && ok; u += ustep) {
-      const uint32_t d = tmem + acc * BN;
-      for (int it = 0; it < p.ksteps; ++it) {
-        if (!gb::mbar_wait_bounded_warp(&full[stage], phase, p.wait_ns, p.err)) {
-          ok = false;
-          break;
-        }
-        gb::tc_fence_after();
-        const uint32_t sfa = tmem + C::NACC * BN + stage * C::SF_COLS;
-        const uint32_t sfb = sfa + C::ATOMS * 4;
-        if (one) {
-          const uint32_t fa = gb::smem_u32(sFA + stage * C::SFA_BYTES);
-          const uint32_t fb = gb::smem_u32(sFB + stage * C::SFB_BYTES);
-          // scale tiles (32 rows x 16 bytes): A's tile j at columns 4 j, B's panel q of
-          // tile j at 4 (j PB + q), so that an MMA's B scales are consecutive
-#pragma unroll
-          for (int j = 0; j < C::ATOMS; ++j) {
-            gb::tc_copy_scales<PAIR>(sfa + 4 * j, gb::noswz_kmajor_desc(fa + j * 512, 128, 128));
-#pragma unroll
-            for (int q = 0; q < C::PB; ++q)
-              gb::tc_copy_scales<PAIR>(
-                  sfb + 4 * (j * C::PB + q),
-                  gb::noswz_kmajor_desc(fb + (q * C::ATOMS + j) * 512, 128, 128));
-          }
-        }
-        __syncwarp();
-        // the tile's accumulator is needed only now
-        if (it == 0) {
-          if (!gb::mbar_wait_bounded_warp(&tempty[acc], acc_phase ^ 1, p.wait_ns, p.err)) {
+    } else if (warp == 1 && rank == 0) {
+      // ---------------- scale copies and MMAs ----------------
+      const bool one = gb::elect_one();
+      constexpr int MM = PAIR ? 2 * BM : BM;
+      int stage = 0, acc = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true;
+      for (int u = unit0; u < units && ok; u += ustep) {
+        const uint32_t d = tmem + acc * BN;
+        for (int it = 0; it < p.ksteps; ++it) {
+          if (!gb::mbar_wait_bounded_warp(&full[stage], phase, p.wait_ns, p.err)) {
             ok = false;
             break;
           }
           gb::tc_fence_after();
-        }
-        if (one) {
-          const uint64_t ad = gb::sw128_kmajor_desc(gb::smem_u32(sA + stage * C::A_BYTES));
-          const uint64_t bd = gb::sw128_kmajor_desc(gb::smem_u32(sB + stage * C::B_BYTES));
-          const int mmas = it + 1 < p.ksteps ? 4 : p.kmmas_last;
+          const uint32_t sfa = tmem + C::NACC * BN + stage * C::SF_COLS;
+          const uint32_t sfb = sfa + C::ATOMS * 4;
+          if (one) {
+            const uint32_t fa = gb::smem_u32(sFA + stage * C::SFA_BYTES);
+            const uint32_t fb = gb::smem_u32(sFB + stage * C::SFB_BYTES);
+            // scale tiles (32 rows x 16 bytes): A's tile j at columns 4 j, B's panel q of
+            // tile j at 4 (j PB + q), so that an MMA's B scales are consecutive
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            // MX: a scale word (4 blocks of 32) serves two MMAs; NV: (4 of 16) one
-            const int j = MX ? k / 2 : k;
-            const uint32_t id = gb::idesc_fp4(MM, BN, MX, MX ? (k & 1) * 2 : 0);
-            if (k < mmas)
-              gb::tc_mma_fp4<MX, PAIR>(d, ad + k * 2, bd + k * 2, id, sfa + 4 * j,
-                                       sfb + 4 * j * C::PB, it > 0 || k > 0 ? 1u : 0u);
+            for (int j = 0; j < C::ATOMS; ++j) {
+              gb::tc_copy_scales<PAIR>(sfa + 4 * j, gb::noswz_kmajor_desc(fa + j * 512, 128, 128));
+#pragma unroll
+              for (int q = 0; q < C::PB; ++q)
+                gb::tc_copy_scales<PAIR>(
+                    sfb + 4 * (j * C::PB + q),
+                    gb::noswz_kmajor_desc(fb + (q * C::ATOMS + j) * 512, 128, 128));
+            }
           }
+          __syncwarp();
+          // the tile's accumulator is needed only now
+          if (it == 0) {
+            if (!gb::mbar_wait_bounded_warp(&tempty[acc], acc_phase ^ 1, p.wait_ns, p.err)) {
+              ok = false;
+              break;
+            }
+            gb::tc_fence_after();
+          }
+          if (one) {
+            const uint64_t ad = gb::sw128_kmajor_desc(gb::smem_u32(sA + stage * C::A_BYTES));
+            const uint64_t bd = gb::sw128_kmajor_desc(gb::smem_u32(sB + stage * C::B_BYTES));
+            const int mmas = it + 1 < p.ksteps ? 4 : p.kmmas_last;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              // MX: a scale word (4 blocks of 32) serves two MMAs; NV: (4 of 16) one
+              const int j = MX ? k / 2 : k;
+              const uint32_t id = gb::idesc_fp4(MM, BN, MX, MX ? (k & 1) * 2 : 0);
+              if (k < mmas)
+                gb::tc_mma_fp4<MX, PAIR>(d, ad + k * 2, bd + k * 2, id, sfa + 4 * j,
+                                         sfb + 4 * j * C::PB, it > 0 || k > 0 ? 1u : 0u);
+            }
+            if constexpr (PAIR)
+              gb::tc_commit_pair_multicast(&empty[stage], 0x3);
+            else
+              gb::tc_commit(&empty[stage]);
+          }
+          __syncwarp();
+          if (++stage == C::STAGES) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+        if (!ok) break;
+        if (one) {
           if constexpr (PAIR)
-            gb::tc_commit_pair_multicast(&empty[stage], 0x3);
+            gb::tc_commit_pair_multicast(&tfull[acc], 0x3);
           else
-            gb::tc_commit(&empty[stage]);
+            gb::tc_commit(&tfull[acc]);
         }
         __syncwarp();
-        if (++stage == C::STAGES) {
-          stage = 0;
-          phase ^= 1;
+        if (++acc == C::NACC) {
+          acc = 0;
+          acc_phase ^= 1;
         }
       }
-      if (!ok) break;
       if (one) {
         if constexpr (PAIR)
-          gb::tc_commit_pair_multicast(&tfull[acc], 0x3);
+          gb::tc_commit_pair_multicast(mma_done, 0x1);
         else
-          gb::tc_commit(&tfull[acc]);
+          gb::tc_commit(mma_done);
       }
       __syncwarp();
-      if (++acc == C::NACC) {
-        acc = 0;
-        acc_phase ^= 1;
-      }
+      gb::mbar_wait_bounded_warp(mma_done, 0, p.wait_ns, p.err);
     }
-    if (one) {
-      if constexpr (PAIR)
-        gb::tc_commit_pair_multicast(mma_done, 0x1);
-      else
-        gb::tc_commit(mma_done);
-    }
-    __syncwarp();
-    gb::mbar_wait_bounded_warp(mma_done, 0, p.wait_ns, p.err);
-  }
   } else {
     if constexpr (BN == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
     // ---------------- epilogue (warps 4 and up) ----------------
@@ -633,9 +643,10 @@ cudaError_t launch_tile(const Fp4Gemm& g, cudaStream_t st) {
     cuuint64_t strides[1] = {(cuuint64_t)g.ldy * es};
     cuuint32_t box[2] = {(cuuint32_t)(64 / es), 32};
     cuuint32_t estr[2] = {1, 1};
-    if (gb_encode_tiled(&ty, es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
-                        2, g.y, dims, strides, box, estr,
-                        CU_TENSOR_MAP_SWIZZLE_64B) != CUDA_SUCCESS)
+    const CUtensorMapDataType dt =
+        es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+    if (gb_encode_tiled(&ty, dt, 2, g.y, dims, strides, box, estr, CU_TENSOR_MAP_SWIZZLE_64B) !=
+        CUDA_SUCCESS)
       return cudaErrorInvalidValue;
   }
   p.err = gb_device_error_word();

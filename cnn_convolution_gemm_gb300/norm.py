@@ -57,7 +57,7 @@ class ResidualNorm:
         C, dtype, z_dtype = self.C, self.dtype, self.z_dtype
         shape = x.shape
         device = x.device
-        rows, ldx = (x.numel() // C, C) if shape[-1] == C and x.is_contiguous() else rows_of(x, C, "x")
+        rows, ldx = rows_of(x, C, "x")
         if x.dtype is not dtype:
             raise ValueError(f"x: {x.dtype}, expected {dtype}")
         zp = gp = xop = hp = hsp = None
