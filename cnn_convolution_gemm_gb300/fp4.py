@@ -15,10 +15,13 @@ CONV_DTYPE = {torch.bfloat16: B.CONV_BF16, torch.float32: B.CONV_F32}
 BLOCK = {B.CONV_FP4_MX: 32, B.CONV_FP4_NV: 16}
 
 
+# a call's host time is a few microseconds in all, so its path here is kept short
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def stream_handle(stream, device: torch.device) -> int:
-    """stream, or the handle of the device's current stream (without building a
-    torch.cuda.Stream: a call's host time is a few microseconds in all)."""
-    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream
+    """stream, or the handle of the device's current stream."""
+    return _current_stream(device.index) if stream is None else stream
 
 
 def allocating_on(stream):
@@ -40,18 +43,25 @@ def rows_of(t: torch.Tensor, cols: int, what: str):
         rows, ld = t.shape[0], t.stride(0)
         if t.stride(1) != 1 and cols > 1 and rows:
             raise ValueError(f"{what}: the elements of a row must be contiguous")
+        if rows > 1 and ld < cols:
+            raise ValueError(f"{what}: its rows overlap (an expanded tensor?)")
         return rows, ld if rows > 1 else cols
     raise ValueError(f"{what}: must be contiguous (or 2-D with contiguous rows)")
 
 
 class Fp4Tensor:
-    """A 4-bit matrix [rows][cols]: codes, scales (tiled, as conv_fp4_size says), tensor scale."""
+    """A 4-bit matrix [rows][cols]: codes, scales (tiled, as conv_fp4_size says), tensor
+    scale.  The tensors stay the ones it was made with (their addresses are kept)."""
 
-    __slots__ = ("rows", "cols", "fmt", "tensor_scale", "codes", "scales")
+    __slots__ = ("rows", "cols", "fmt", "tensor_scale", "codes", "scales", "shape", "codes_ptr",
+                 "scales_ptr", "device")
 
     def __init__(self, rows, cols, fmt, tensor_scale, codes, scales):
         self.rows, self.cols, self.fmt, self.tensor_scale = rows, cols, fmt, tensor_scale
         self.codes, self.scales = codes, scales
+        self.shape = (rows, cols, fmt)
+        self.codes_ptr, self.scales_ptr = codes.data_ptr(), scales.data_ptr()
+        self.device = codes.device
 
 
 def empty(rows, cols, fmt, device, tensor_scale=1.0, stream=None) -> Fp4Tensor:
@@ -70,11 +80,12 @@ def quantize(x: torch.Tensor, fmt, tensor_scale=1.0, out: Fp4Tensor | None = Non
     rows, ld = rows_of(x, cols, "x")
     if out is None:
         out = empty(rows, cols, fmt, x.device, tensor_scale, stream)
-    elif (out.rows, out.cols, out.fmt) != (rows, cols, fmt):
+    elif out.shape != (rows, cols, fmt):
         raise ValueError("out: a 4-bit matrix of another shape or format")
+    if not x.is_cuda or x.get_device() != out.device.index:
+        raise ValueError("x: must be on the GPU, and on out's")
     B.conv_fp4_quantize(fmt, CONV_DTYPE[x.dtype], rows, cols, x.data_ptr(), ld, tensor_scale,
-                        out.codes.data_ptr(), out.scales.data_ptr(),
-                        stream_handle(stream, x.device))
+                        out.codes_ptr, out.scales_ptr, stream_handle(stream, out.device))
     out.tensor_scale = tensor_scale
     return out
 
@@ -84,13 +95,14 @@ def dequantize(t: Fp4Tensor, dtype=torch.bfloat16, out: torch.Tensor | None = No
     """The values that t stands for, [rows][cols] in dtype (or out's)."""
     if out is None:
         with allocating_on(stream):
-            out = torch.empty(t.rows, t.cols, dtype=dtype, device=t.codes.device)
+            out = torch.empty(t.rows, t.cols, dtype=dtype, device=t.device)
     rows, ld = rows_of(out, t.cols, "out")
     if rows != t.rows:
         raise ValueError(f"out: {rows} rows, expected {t.rows}")
-    B.conv_fp4_dequantize(t.fmt, CONV_DTYPE[out.dtype], rows, t.cols, t.codes.data_ptr(),
-                          t.scales.data_ptr(), t.tensor_scale, out.data_ptr(), ld,
-                          stream_handle(stream, out.device))
+    if out.get_device() != t.device.index:
+        raise ValueError("out: on another device than t")
+    B.conv_fp4_dequantize(t.fmt, CONV_DTYPE[out.dtype], rows, t.cols, t.codes_ptr, t.scales_ptr,
+                          t.tensor_scale, out.data_ptr(), ld, stream_handle(stream, t.device))
     return out
 
 
@@ -161,7 +173,7 @@ class Fp4Linear:
         ws = self._ws.get(handle)
         if ws is None or ws.numel() < need:
             with allocating_on(stream):
-                ws = torch.empty(need, dtype=torch.uint8, device=self.w.codes.device)
+                ws = torch.empty(need, dtype=torch.uint8, device=self.w.device)
             self._ws[handle] = ws
         return ws.data_ptr(), ws.numel()
 
@@ -169,20 +181,21 @@ class Fp4Linear:
         w = self.w
         if w is None:
             raise RuntimeError("prepack() or load() the weights first")
-        C, K, y_dtype = self.C, self.K, self.y_dtype
-        device = w.codes.device
+        C, K, y_dtype, device = self.C, self.K, self.y_dtype, w.device
         handle = stream_handle(stream, device)
+        bp = rp = xsp = ysp = None
         if self.x_dtype is None:
             if (x.cols, x.fmt, x.tensor_scale) != (C, self.fmt, self.x_scale):
                 raise ValueError("x: a 4-bit matrix of another width, format or tensor scale")
-            rows, ldx, lead = x.rows, C, (x.rows,)
-            xp, xsp = x.codes.data_ptr(), x.scales.data_ptr()
+            rows, ldx = x.rows, C
+            xp, xsp = x.codes_ptr, x.scales_ptr
         else:
             if x.dtype is not self.x_dtype:
                 raise ValueError(f"x: {x.dtype}, expected {self.x_dtype}")
-            (rows, ldx), lead = rows_of(x, C, "x"), None
-            xp, xsp = x.data_ptr(), None
-        bp = rp = ysp = None
+            if x.get_device() != device.index:
+                raise ValueError("x: on another device than the weights")
+            rows, ldx = rows_of(x, C, "x")
+            xp = x.data_ptr()
         if bias is not None:
             if bias.dtype is not torch.float32 or bias.numel() != K or not bias.is_contiguous():
                 raise ValueError("bias: expected contiguous fp32 [K]")
@@ -191,15 +204,15 @@ class Fp4Linear:
         if y_dtype is None:
             if out is None:
                 out = empty(rows, K, self.fmt, device, self.y_scale, stream)
-            elif (out.rows, out.cols, out.fmt) != (rows, K, self.fmt):
+            elif out.shape != (rows, K, self.fmt):
                 raise ValueError("out: a 4-bit matrix of another shape or format")
             out.tensor_scale = self.y_scale
-            yp, ysp = out.codes.data_ptr(), out.scales.data_ptr()
+            yp, ysp = out.codes_ptr, out.scales_ptr
         else:
             if out is None:
+                lead = (rows,) if self.x_dtype is None else x.shape[:-1]
                 with allocating_on(stream):
-                    out = torch.empty(*(x.shape[:-1] if lead is None else lead), K, dtype=y_dtype,
-                                      device=device)
+                    out = torch.empty(*lead, K, dtype=y_dtype, device=device)
             got, ldy = rows_of(out, K, "out")
             if got != rows or out.dtype is not y_dtype:
                 raise ValueError("out: another number of rows or type")
@@ -209,12 +222,13 @@ class Fp4Linear:
             if got != rows or residual.dtype is not y_dtype:
                 raise ValueError("residual: another number of rows or type than y")
             rp = residual.data_ptr()
-        if (ldx, ldr, ldy) != self._strides:
-            B.conv_fp4_set_strides(self.desc, ldx, ldr, ldy)
-            self._strides = (ldx, ldr, ldy)
+        strides = (ldx, ldr, ldy)
+        if strides != self._strides:
+            B.conv_fp4_set_strides(self.desc, *strides)
+            self._strides = strides
         wsp, ws_bytes = self._workspace(rows, stream, handle)
-        B.conv_fp4_fwd(self.desc, rows, xp, xsp, w.codes.data_ptr(), w.scales.data_ptr(), bp, rp,
-                       yp, ysp, wsp, ws_bytes, handle)
+        B.conv_fp4_fwd(self.desc, rows, xp, xsp, w.codes_ptr, w.scales_ptr, bp, rp, yp, ysp, wsp,
+                       ws_bytes, handle)
         return out
 
     __call__ = forward

@@ -60,6 +60,8 @@ class ResidualNorm:
         rows, ldx = rows_of(x, C, "x")
         if x.dtype is not dtype:
             raise ValueError(f"x: {x.dtype}, expected {dtype}")
+        if not x.is_cuda:
+            raise ValueError("x: must be on the GPU")
         zp = gp = xop = hp = hsp = None
         ldz = ldg = ldxo = ldh = C
         # of each tensor first the usual case: x's shape, contiguous
@@ -85,10 +87,10 @@ class ResidualNorm:
         elif self.h_fmt is not None:
             if h_out is None:
                 h_out = fp4.empty(rows, C, self.h_fmt, device, self.h_scale, stream)
-            elif (h_out.rows, h_out.cols, h_out.fmt) != (rows, C, self.h_fmt):
+            elif h_out.shape != (rows, C, self.h_fmt):
                 raise ValueError("h_out: a 4-bit matrix of another shape or format")
             h_out.tensor_scale = self.h_scale
-            hp, hsp = h_out.codes.data_ptr(), h_out.scales.data_ptr()
+            hp, hsp = h_out.codes_ptr, h_out.scales_ptr
         else:
             if h_out is None:
                 with allocating_on(stream):

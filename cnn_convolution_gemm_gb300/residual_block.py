@@ -65,7 +65,7 @@ class Fp4ResidualBlock:
                 h = fp4.empty(rows, self.C, self.fmt, device, self.h_scale)
                 t = fp4.empty(rows, self.hidden, self.fmt, device, self.t_scale)
                 z = torch.empty(rows, self.C, dtype=torch.bfloat16, device=device)
-            got = (rows, h, t, z, t.codes.data_ptr(), t.scales.data_ptr(), z.data_ptr())
+            got = (rows, h, t, z, t.codes_ptr, t.scales_ptr, z.data_ptr())
             self._bufs[handle] = got
         return got
 
@@ -80,15 +80,14 @@ class Fp4ResidualBlock:
         _, hb, _, z, tp, tsp, zp = self._buffers(rows, x.device, stream, handle)
         if h is None:
             h = self.norm_in(x, h_out=hb, want_x=False, stream=handle)[1]
-        elif (h.rows, h.cols, h.fmt, h.tensor_scale) != (rows, self.C, self.fmt, self.h_scale):
+        elif (h.shape, h.tensor_scale) != ((rows, self.C, self.fmt), self.h_scale):
             raise ValueError("h: a 4-bit matrix of another shape, format or tensor scale")
         # the two products between the block's own buffers: the layers' C calls, without
         # their checks of tensors
         b1, b2 = self.b1, self.b2
-        B.conv_fp4_fwd(self.fc1.desc, rows, h.codes.data_ptr(), h.scales.data_ptr(),
-                       w1.codes.data_ptr(), w1.scales.data_ptr(),
+        B.conv_fp4_fwd(self.fc1.desc, rows, h.codes_ptr, h.scales_ptr, w1.codes_ptr, w1.scales_ptr,
                        None if b1 is None else b1.data_ptr(), None, tp, tsp, None, 0, handle)
-        B.conv_fp4_fwd(self.fc2.desc, rows, tp, tsp, w2.codes.data_ptr(), w2.scales.data_ptr(),
+        B.conv_fp4_fwd(self.fc2.desc, rows, tp, tsp, w2.codes_ptr, w2.scales_ptr,
                        None if b2 is None else b2.data_ptr(), None, zp, None, None, 0, handle)
         if z.dim() != x.dim():
             z = z.view(x.shape)

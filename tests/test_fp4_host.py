@@ -178,6 +178,8 @@ def test_torch_layers_check_their_tensors(B):
         fp4.rows_of(torch.zeros(4, 6).t(), 4, "x")       # columns not contiguous
     with pytest.raises(ValueError):
         fp4.rows_of(torch.zeros(2, 3, 4)[:, :, :3], 3, "x")
+    with pytest.raises(ValueError):
+        fp4.rows_of(torch.zeros(1, 6).expand(4, 6), 6, "x")  # rows that overlap
     assert fp4.rows_of(torch.zeros(5, 9)[:, 2:8], 6, "x") == (5, 9)
     assert fp4.rows_of(torch.zeros(2, 3, 4), 4, "x") == (6, 4)
     layer = fp4.Fp4Linear(64, 32)
@@ -187,3 +189,8 @@ def test_torch_layers_check_their_tensors(B):
         layer.load(torch.zeros(32, 33, dtype=torch.uint8), torch.zeros(32, 2, dtype=torch.uint8))
     with pytest.raises(ValueError):
         ResidualNorm(64, w_pre=torch.zeros(63), pre=B.CONV_NORM_RMS)
+    with pytest.raises(ValueError):
+        ResidualNorm(64, w_pre=torch.ones(64), pre=B.CONV_NORM_RMS)(
+            torch.zeros(1, 64, dtype=torch.bfloat16))    # a tensor in host memory
+    with pytest.raises(ValueError):
+        fp4.quantize(torch.zeros(1, 64), B.CONV_FP4_MX)
