@@ -417,7 +417,8 @@ conv_status_t conv_fp4_set_tensor_scales(conv_fp4_t desc, float x, float w, floa
 /* Elements between rows of x, residual and y (0: contiguous; codes are always
  * contiguous).  At least the row's length. */
 conv_status_t conv_fp4_set_strides(conv_fp4_t desc, long long ldx, long long ldr, long long ldy);
-/* Bytes of device workspace conv_fp4_fwd needs for M rows on the current device. */
+/* Bytes of device workspace conv_fp4_fwd needs for M rows on the current device: 0 for an
+ * x in codes and for up to 8 rows, else the codes and scales of x. */
 conv_status_t conv_fp4_workspace_size(conv_fp4_t desc, int M, size_t* bytes);
 /* x: device, per x_io and strides, aligned to its element (codes: 16 bytes);
  * x_scales: the tiled scales of codes, else NULL.  w_codes, w_scales: the weights as
