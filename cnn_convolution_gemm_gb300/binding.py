@@ -109,6 +109,11 @@ SIGNATURES = {
     "conv_norm_set_output": (_i, [_p, _i, _f]),
     "conv_norm_set_strides": (_i, [_p, _ll, _ll, _ll, _ll, _ll]),
     "conv_norm_fwd": (_i, [_p, _i, _p, _p, _p, _p, _p, _p, _p]),
+    "conv_fp4_block_create": (_i, [ctypes.POINTER(_p), _p, _p, _p, _p]),
+    "conv_fp4_block_destroy": (_i, [_p]),
+    "conv_fp4_block_set_weights": (_i, [_p, _p, _p, _p, _p, _p, _p]),
+    "conv_fp4_block_workspace_size": (_i, [_p, _i, ctypes.POINTER(_sz)]),
+    "conv_fp4_block_fwd": (_i, [_p, _i, _p, _p, _p, _p, _p, _p, _p, _p, _sz, _p]),
     "conv_sync_status": (_i, [_p]),
     "conv_selftest_wait_timeout": (_i, [ctypes.c_uint, _p]),
     "conv_status_string": (_cp, [_i]),
@@ -450,6 +455,36 @@ def conv_norm_fwd(desc, rows, x_ptr, z_ptr, gate_ptr, x_out_ptr, h_ptr, h_scales
                   stream=None):
     _check(load_library().conv_norm_fwd(desc, rows, x_ptr, z_ptr, gate_ptr, x_out_ptr, h_ptr,
                                         h_scales_ptr, stream), "conv_norm_fwd")
+
+
+def conv_fp4_block_create(norm_in, fc1, fc2, norm_out):
+    d = ctypes.c_void_p()
+    _check(load_library().conv_fp4_block_create(ctypes.byref(d), norm_in, fc1, fc2, norm_out),
+           "conv_fp4_block_create")
+    return d
+
+
+def conv_fp4_block_destroy(desc):
+    _check(load_library().conv_fp4_block_destroy(desc), "conv_fp4_block_destroy")
+
+
+def conv_fp4_block_set_weights(desc, w1_ptr, s1_ptr, b1_ptr, w2_ptr, s2_ptr, b2_ptr):
+    _check(load_library().conv_fp4_block_set_weights(desc, w1_ptr, s1_ptr, b1_ptr, w2_ptr, s2_ptr,
+                                                     b2_ptr), "conv_fp4_block_set_weights")
+
+
+def conv_fp4_block_workspace_size(desc, M):
+    n = _sz(0)
+    _check(load_library().conv_fp4_block_workspace_size(desc, M, ctypes.byref(n)),
+           "conv_fp4_block_workspace_size")
+    return n.value
+
+
+def conv_fp4_block_fwd(desc, M, x_ptr, h_ptr, h_scales_ptr, gate_ptr, x_out_ptr, h_out_ptr,
+                       h_out_scales_ptr, ws_ptr, ws_bytes, stream=None):
+    _check(load_library().conv_fp4_block_fwd(desc, M, x_ptr, h_ptr, h_scales_ptr, gate_ptr,
+                                             x_out_ptr, h_out_ptr, h_out_scales_ptr, ws_ptr,
+                                             ws_bytes, stream), "conv_fp4_block_fwd")
 
 
 def conv_sync_status(stream=None):

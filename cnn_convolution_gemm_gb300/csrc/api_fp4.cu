@@ -376,13 +376,12 @@ extern "C" conv_status_t conv_norm_set_strides(conv_norm_t d, long long ldx, lon
   return gb_ok();
 }
 
-extern "C" conv_status_t conv_norm_fwd(conv_norm_t d, int rows, const void* x, const void* z,
-                                       const void* gate, void* x_out, void* h, void* h_scales,
-                                       void* stream) {
-  if (!d) return gb_fail(CONV_ERR_BAD_PARAM, "desc is NULL");
-  if (rows < 0) return gb_fail(CONV_ERR_BAD_PARAM, "rows must be >= 0");
-  if (rows == 0) return gb_ok();
-  NormArgs a = d->a;
+// the arguments of a norm's launch, or why there is none
+static conv_status_t check_norm_call(conv_norm_t d, int rows, const void* x, const void* z,
+                                     const void* gate, void* x_out, void* h, void* h_scales,
+                                     NormArgs* to) {
+  NormArgs& a = *to;
+  a = d->a;
   if (!x) return gb_fail(CONV_ERR_BAD_PARAM, "x is NULL");
   if (!x_out && !h) return gb_fail(CONV_ERR_BAD_PARAM, "no output");
   if ((h != nullptr) != (a.pre != CONV_NORM_NONE))
@@ -409,9 +408,170 @@ extern "C" conv_status_t conv_norm_fwd(conv_norm_t d, int rows, const void* x, c
   a.hs = static_cast<uint8_t*>(h_scales);
   a.err = gb_device_error_word();
   a.wait_ns = gb_wait_limit_ns();
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return CONV_OK;
+}
+
+static conv_status_t launch_norm(const NormArgs& a, cudaStream_t st) {
   const bool xb16 = a.x_dtype == CONV_BF16, zb16 = a.z_dtype == CONV_BF16;
   return cuda_status(xb16 ? (zb16 ? launch_norm_bb(a, st) : launch_norm_bf(a, st))
                           : (zb16 ? launch_norm_fb(a, st) : launch_norm_ff(a, st)),
                      "norm");
+}
+
+extern "C" conv_status_t conv_norm_fwd(conv_norm_t d, int rows, const void* x, const void* z,
+                                       const void* gate, void* x_out, void* h, void* h_scales,
+                                       void* stream) {
+  if (!d) return gb_fail(CONV_ERR_BAD_PARAM, "desc is NULL");
+  if (rows < 0) return gb_fail(CONV_ERR_BAD_PARAM, "rows must be >= 0");
+  if (rows == 0) return gb_ok();
+  NormArgs a;
+  const conv_status_t st = check_norm_call(d, rows, x, z, gate, x_out, h, h_scales, &a);
+  return st != CONV_OK ? st : launch_norm(a, static_cast<cudaStream_t>(stream));
+}
+
+// ---------------------------------------------------------------------------
+// a residual block
+
+struct gbconv_fp4_block_s {
+  conv_norm_t norm_in, norm_out;
+  conv_fp4_t fc1, fc2;
+  const void *w1, *s1, *w2, *s2;
+  const float *b1, *b2;
+};
+
+namespace {
+
+// parts of the workspace, each on a 256-byte boundary
+struct BlockParts {
+  size_t h, hs, t, ts, z, bytes;
+};
+BlockParts block_parts(const gbconv_fp4_block_s& b, int M) {
+  BlockParts p;
+  size_t at = 0;
+  const auto take = [&](size_t bytes) {
+    const size_t from = at;
+    at += (bytes + 255) / 256 * 256;
+    return from;
+  };
+  p.h = take(code_bytes(M, b.fc1->C));
+  p.hs = take(scale_bytes(b.fc1->fmt, M, b.fc1->C));
+  p.t = take(code_bytes(M, b.fc1->K));
+  p.ts = take(scale_bytes(b.fc1->fmt, M, b.fc1->K));
+  p.z = take((size_t)M * b.fc2->K * elem_bytes(b.fc2->y_io));
+  p.bytes = at;
+  return p;
+}
+
+// whether the descriptors, as they are now, fit together
+conv_status_t check_block(const gbconv_fp4_block_s& b) {
+  const NormArgs &in = b.norm_in->a, &out = b.norm_out->a;
+  const gbconv_fp4_s &f1 = *b.fc1, &f2 = *b.fc2;
+  const char* wrong = nullptr;
+  if (in.C != f1.C || f1.K != f2.C || f2.K != out.C || in.C != out.C)
+    wrong = "widths do not fit";
+  else if (f1.x_io != CONV_FP4_IO_CODES || f1.y_io != CONV_FP4_IO_CODES ||
+           f2.x_io != CONV_FP4_IO_CODES || f2.y_io == CONV_FP4_IO_CODES)
+    wrong = "the layers pass 4 bits on, the second gives floats";
+  else if (f1.fmt != f2.fmt ||
+           in.out != (f1.fmt == CONV_FP4_MX ? CONV_NORM_OUT_FP4_MX : CONV_NORM_OUT_FP4_NV))
+    wrong = "formats do not fit";
+  else if (in.h_scale != f1.x_scale || f1.y_scale != f2.x_scale)
+    wrong = "tensor scales do not fit";
+  else if (in.pre == CONV_NORM_NONE || in.x_dtype != out.x_dtype || in.ldx != out.ldx)
+    wrong = "the norms do not read the same x";
+  else if (f2.y_io != out.z_dtype || f2.ldy != out.C || out.ldz != out.C)
+    wrong = "z is contiguous, in the second norm's z_dtype";
+  else if (f1.has_residual || f2.has_residual)
+    wrong = "a layer has a residual of its own";
+  return wrong ? gb_fail(CONV_ERR_BAD_PARAM, "residual block: %s", wrong) : CONV_OK;
+}
+
+}  // namespace
+
+static_assert((int)CONV_FP4_IO_BF16 == (int)CONV_BF16 && (int)CONV_FP4_IO_F32 == (int)CONV_F32,
+              "check_block, elem_bytes");
+
+extern "C" conv_status_t conv_fp4_block_create(conv_fp4_block_t* out, conv_norm_t norm_in,
+                                               conv_fp4_t fc1, conv_fp4_t fc2,
+                                               conv_norm_t norm_out) {
+  if (!out) return gb_fail(CONV_ERR_BAD_PARAM, "out is NULL");
+  *out = nullptr;
+  if (!norm_in || !fc1 || !fc2 || !norm_out)
+    return gb_fail(CONV_ERR_BAD_PARAM, "a descriptor is NULL");
+  const gbconv_fp4_block_s b{norm_in, norm_out, fc1, fc2};
+  const conv_status_t st = check_block(b);
+  if (st != CONV_OK) return st;
+  *out = new (std::nothrow) gbconv_fp4_block_s(b);
+  return *out ? gb_ok() : gb_fail(CONV_ERR_BAD_PARAM, "out of host memory");
+}
+
+extern "C" conv_status_t conv_fp4_block_destroy(conv_fp4_block_t d) {
+  delete d;
+  return gb_ok();
+}
+
+extern "C" conv_status_t conv_fp4_block_set_weights(conv_fp4_block_t d, const void* w1,
+                                                    const void* s1, const float* b1,
+                                                    const void* w2, const void* s2,
+                                                    const float* b2) {
+  if (!d) return gb_fail(CONV_ERR_BAD_PARAM, "desc is NULL");
+  if (!w1 || !s1 || !w2 || !s2) return gb_fail(CONV_ERR_BAD_PARAM, "NULL tensor");
+  if (!aligned(w1, 16) || !aligned(s1, 16) || !aligned(w2, 16) || !aligned(s2, 16))
+    return gb_fail(CONV_ERR_ALIGNMENT, "codes and scales must be 16-byte aligned");
+  if (!aligned(b1, 4) || !aligned(b2, 4))
+    return gb_fail(CONV_ERR_ALIGNMENT, "biases must be aligned to their elements");
+  d->w1 = w1;
+  d->s1 = s1;
+  d->b1 = b1;
+  d->w2 = w2;
+  d->s2 = s2;
+  d->b2 = b2;
+  return gb_ok();
+}
+
+extern "C" conv_status_t conv_fp4_block_workspace_size(conv_fp4_block_t d, int M, size_t* bytes) {
+  if (!d || !bytes) return gb_fail(CONV_ERR_BAD_PARAM, "NULL argument");
+  if (M < 0) return gb_fail(CONV_ERR_BAD_PARAM, "M must be >= 0");
+  if (M > MOST) return gb_fail(CONV_ERR_UNSUPPORTED, "more than 2^30 rows");
+  *bytes = block_parts(*d, M).bytes;
+  return gb_ok();
+}
+
+extern "C" conv_status_t conv_fp4_block_fwd(conv_fp4_block_t d, int M, const void* x,
+                                            const void* h, const void* h_scales, const void* gate,
+                                            void* x_out, void* h_out, void* h_out_scales, void* ws,
+                                            size_t ws_bytes, void* stream) {
+  if (!d) return gb_fail(CONV_ERR_BAD_PARAM, "desc is NULL");
+  if (M < 0) return gb_fail(CONV_ERR_BAD_PARAM, "M must be >= 0");
+  if (M > MOST) return gb_fail(CONV_ERR_UNSUPPORTED, "more than 2^30 rows");
+  conv_status_t st = check_block(*d);
+  if (st != CONV_OK) return st;
+  if (M == 0) return gb_ok();
+  if (!d->w1) return gb_fail(CONV_ERR_BAD_PARAM, "no weights yet");
+  if ((h != nullptr) != (h_scales != nullptr))
+    return gb_fail(CONV_ERR_BAD_PARAM, "h and h_scales come together");
+  const BlockParts p = block_parts(*d, M);
+  if (!ws || ws_bytes < p.bytes)
+    return gb_fail(CONV_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", p.bytes,
+                   ws ? ws_bytes : (size_t)0);
+  if (!aligned(ws, 16)) return gb_fail(CONV_ERR_ALIGNMENT, "workspace must be 16-byte aligned");
+  // the last call's checks first, so that a refusal enqueues nothing
+  char* const w = static_cast<char*>(ws);
+  NormArgs out;
+  if ((st = check_norm_call(d->norm_out, M, x, w + p.z, gate, x_out, h_out, h_out_scales, &out)) !=
+      CONV_OK)
+    return st;
+  if (!h) {
+    if ((st = conv_norm_fwd(d->norm_in, M, x, nullptr, nullptr, nullptr, w + p.h, w + p.hs,
+                            stream)) != CONV_OK)
+      return st;
+    h = w + p.h;
+    h_scales = w + p.hs;
+  }
+  if ((st = conv_fp4_fwd(d->fc1, M, h, h_scales, d->w1, d->s1, d->b1, nullptr, w + p.t, w + p.ts,
+                         nullptr, 0, stream)) != CONV_OK ||
+      (st = conv_fp4_fwd(d->fc2, M, w + p.t, w + p.ts, d->w2, d->s2, d->b2, nullptr, w + p.z,
+                         nullptr, nullptr, 0, stream)) != CONV_OK)
+    return st;
+  return launch_norm(out, static_cast<cudaStream_t>(stream));
 }

@@ -123,6 +123,7 @@ class Fp4Linear:
               None: B.CONV_FP4_IO_CODES}
         self.desc = B.conv_fp4_create(fmt, C, K, io[x_dtype], io[y_dtype])
         B.conv_fp4_set_epilogue(self.desc, act, has_residual)
+        B.conv_fp4_set_tensor_scales(self.desc, x_scale, 1.0, y_scale)  # w's: with the weights
         self.w = None
         self._strides = (C, K, K)
         self._sizes = {}  # rows -> workspace bytes

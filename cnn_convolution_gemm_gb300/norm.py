@@ -51,31 +51,23 @@ class ResidualNorm:
             raise ValueError(f"{what}: {got} rows of {t.dtype}, expected {rows} of {dtype}")
         return t.data_ptr(), ld
 
-    def forward(self, x, z=None, gate=None, x_out=None, h_out=None, want_x=True, stream=None):
-        """Returns (x', h).  x' is None when want_x is false, h when there is no norm_pre.
-        x_out may be x itself."""
-        C, dtype, z_dtype = self.C, self.dtype, self.z_dtype
-        shape = x.shape
-        device = x.device
-        rows, ldx = rows_of(x, C, "x")
+    def _bind(self, x, rows, ldx, ldz, gate, x_out, h_out, want_x, stream):
+        """Checks and allocates what a call needs besides x and z, and gives the descriptor
+        the strides: (x_out, h_out, addresses of gate, x_out, h_out and its scales)."""
+        C, dtype, z_dtype, shape = self.C, self.dtype, self.z_dtype, x.shape
         if x.dtype is not dtype:
             raise ValueError(f"x: {x.dtype}, expected {dtype}")
         if not x.is_cuda:
             raise ValueError("x: must be on the GPU")
-        zp = gp = xop = hp = hsp = None
-        ldz = ldg = ldxo = ldh = C
-        # of each tensor first the usual case: x's shape, contiguous
-        if z is not None:
-            if z.dtype is z_dtype and z.is_contiguous() and z.shape == shape:
-                zp = z.data_ptr()
-            else:
-                zp, ldz = self._tensor(z, z_dtype, rows, "z")
+        gp = xop = hp = hsp = None
+        ldg = ldxo = ldh = C
         if gate is not None:
             gp, ldg = self._tensor(gate, z_dtype, -(-rows // self.gate_rows), "gate")
+        # of each output first the usual case: x's shape, contiguous
         if want_x:
             if x_out is None:
                 with allocating_on(stream):
-                    x_out = torch.empty(shape, dtype=dtype, device=device)
+                    x_out = torch.empty(shape, dtype=dtype, device=x.device)
             if x_out.dtype is dtype and x_out.is_contiguous() and x_out.shape == shape:
                 xop = x_out.data_ptr()
             else:
@@ -86,7 +78,7 @@ class ResidualNorm:
             h_out = None
         elif self.h_fmt is not None:
             if h_out is None:
-                h_out = fp4.empty(rows, C, self.h_fmt, device, self.h_scale, stream)
+                h_out = fp4.empty(rows, C, self.h_fmt, x.device, self.h_scale, stream)
             elif h_out.shape != (rows, C, self.h_fmt):
                 raise ValueError("h_out: a 4-bit matrix of another shape or format")
             h_out.tensor_scale = self.h_scale
@@ -94,7 +86,7 @@ class ResidualNorm:
         else:
             if h_out is None:
                 with allocating_on(stream):
-                    h_out = torch.empty(shape, dtype=z_dtype, device=device)
+                    h_out = torch.empty(shape, dtype=z_dtype, device=x.device)
             if h_out.dtype is z_dtype and h_out.is_contiguous() and h_out.shape == shape:
                 hp = h_out.data_ptr()
             else:
@@ -103,8 +95,23 @@ class ResidualNorm:
         if strides != self._strides:
             B.conv_norm_set_strides(self.desc, *strides)
             self._strides = strides
+        return x_out, h_out, gp, xop, hp, hsp
+
+    def forward(self, x, z=None, gate=None, x_out=None, h_out=None, want_x=True, stream=None):
+        """Returns (x', h).  x' is None when want_x is false, h when there is no norm_pre.
+        x_out may be x itself."""
+        C = self.C
+        rows, ldx = rows_of(x, C, "x")
+        zp, ldz = None, C
+        if z is not None:
+            if z.dtype is self.z_dtype and z.is_contiguous() and z.shape == x.shape:
+                zp = z.data_ptr()
+            else:
+                zp, ldz = self._tensor(z, self.z_dtype, rows, "z")
+        x_out, h_out, gp, xop, hp, hsp = self._bind(x, rows, ldx, ldz, gate, x_out, h_out, want_x,
+                                                    stream)
         B.conv_norm_fwd(self.desc, rows, x.data_ptr(), zp, gp, xop, hp, hsp,
-                        stream_handle(stream, device))
+                        stream_handle(stream, x.device))
         return x_out, h_out
 
     __call__ = forward

@@ -1,4 +1,4 @@
-"""A residual block in 4 bits: two fully connected layers (1x1 convolutions over NHWC
+"""A residual block in 4 bits (conv_fp4_block_* of gbconv.h): two fully connected layers (1x1 convolutions over NHWC
 pixels) between the norms around them.
 
   h  = norm_pre(x), 4 bits             one pass over x
@@ -46,7 +46,18 @@ class Fp4ResidualBlock:
                                      w_post=w_post, pre=B.CONV_NORM_RMS, w_pre=w_next, gate=gate,
                                      gate_rows=gate_rows, residual_scale=residual_scale,
                                      h_fmt=fmt if chain else None, h_scale=next_scale)
-        self._bufs = {}  # stream handle -> (rows, h, t, z, their addresses)
+        self.desc = B.conv_fp4_block_create(self.norm_in.desc, self.fc1.desc, self.fc2.desc,
+                                            self.norm_out.desc)
+        self._held = (None, None)  # the weights that desc has the addresses of
+        self._sizes, self._ws = {}, {}  # rows -> bytes; stream handle -> (tensor, address)
+
+    def __del__(self):
+        d = getattr(self, "desc", None)
+        if d is not None:
+            try:
+                B.conv_fp4_block_destroy(d)
+            except Exception:
+                pass
 
     def prepack(self, w1, w2, w1_scale=1.0, w2_scale=1.0, stream=None):
         """Quantise the weights w1 [hidden][C], w2 [C][hidden] once."""
@@ -58,39 +69,49 @@ class Fp4ResidualBlock:
         self.fc1.load(w1, s1, g1, stream)
         self.fc2.load(w2, s2, g2, stream)
 
-    def _buffers(self, rows, device, stream, handle):
-        got = self._bufs.get(handle)
-        if got is None or got[0] != rows:
+    def _hold(self, w1, w2):
+        if w1 is None or w2 is None:
+            raise RuntimeError("prepack() or load() the weights first")
+        b1, b2 = (None if b is None else b.data_ptr() for b in (self.b1, self.b2))
+        B.conv_fp4_block_set_weights(self.desc, w1.codes_ptr, w1.scales_ptr, b1, w2.codes_ptr,
+                                     w2.scales_ptr, b2)
+        self._held = (w1, w2)
+
+    def _workspace(self, rows, stream, handle):
+        """(address, bytes) of the stream's workspace for so many rows."""
+        need = self._sizes.get(rows)
+        if need is None:
+            need = self._sizes[rows] = B.conv_fp4_block_workspace_size(self.desc, rows)
+        got = self._ws.get(handle)
+        if got is None or got[0].numel() < need:
             with fp4.allocating_on(stream):
-                h = fp4.empty(rows, self.C, self.fmt, device, self.h_scale)
-                t = fp4.empty(rows, self.hidden, self.fmt, device, self.t_scale)
-                z = torch.empty(rows, self.C, dtype=torch.bfloat16, device=device)
-            got = (rows, h, t, z, t.codes_ptr, t.scales_ptr, z.data_ptr())
-            self._bufs[handle] = got
-        return got
+                ws = torch.empty(max(need, 256), dtype=torch.uint8, device=self.fc1.w.device)
+            got = self._ws[handle] = (ws, ws.data_ptr())
+        return got[1], need
 
     def forward(self, x, gate=None, h=None, x_out=None, h_out=None, stream=None):
         """x [..., C] -> (x', h').  h: norm_pre(x) in 4 bits when the block before handed
         it on, else None."""
-        w1, w2 = self.fc1.w, self.fc2.w
-        if w1 is None or w2 is None:
-            raise RuntimeError("prepack() or load() the weights first")
-        rows, _ = fp4.rows_of(x, self.C, "x")
-        handle = fp4.stream_handle(stream, x.device)
-        _, hb, _, z, tp, tsp, zp = self._buffers(rows, x.device, stream, handle)
-        if h is None:
-            h = self.norm_in(x, h_out=hb, want_x=False, stream=handle)[1]
-        elif (h.shape, h.tensor_scale) != ((rows, self.C, self.fmt), self.h_scale):
-            raise ValueError("h: a 4-bit matrix of another shape, format or tensor scale")
-        # the two products between the block's own buffers: the layers' C calls, without
-        # their checks of tensors
-        b1, b2 = self.b1, self.b2
-        B.conv_fp4_fwd(self.fc1.desc, rows, h.codes_ptr, h.scales_ptr, w1.codes_ptr, w1.scales_ptr,
-                       None if b1 is None else b1.data_ptr(), None, tp, tsp, None, 0, handle)
-        B.conv_fp4_fwd(self.fc2.desc, rows, tp, tsp, w2.codes_ptr, w2.scales_ptr,
-                       None if b2 is None else b2.data_ptr(), None, zp, None, None, 0, handle)
-        if z.dim() != x.dim():
-            z = z.view(x.shape)
-        return self.norm_out(x, z, gate=gate, x_out=x_out, h_out=h_out, stream=handle)
+        C, w1, w2, norm_in = self.C, self.fc1.w, self.fc2.w, self.norm_in
+        if w1 is None or (w1, w2) != self._held:
+            self._hold(w1, w2)
+        rows, ldx = fp4.rows_of(x, C, "x")
+        hp = hsp = None
+        if h is not None:
+            if (h.shape, h.tensor_scale) != ((rows, C, self.fmt), self.h_scale):
+                raise ValueError("h: a 4-bit matrix of another shape, format or tensor scale")
+            hp, hsp = h.codes_ptr, h.scales_ptr
+        handle = fp4.stream_handle(stream, w1.device)
+        if x.get_device() != w1.device.index:
+            raise ValueError("x: on another device than the weights")
+        x_out, h_out, gp, xop, hop, hosp = self.norm_out._bind(x, rows, ldx, C, gate, x_out, h_out,
+                                                               True, stream)
+        if norm_in._strides[0] != ldx:
+            norm_in._strides = (ldx, C, C, C, C)
+            B.conv_norm_set_strides(norm_in.desc, *norm_in._strides)
+        wsp, ws_bytes = self._workspace(rows, stream, handle)
+        B.conv_fp4_block_fwd(self.desc, rows, x.data_ptr(), hp, hsp, gp, xop, hop, hosp, wsp,
+                             ws_bytes, handle)
+        return x_out, h_out
 
     __call__ = forward

@@ -481,6 +481,36 @@ conv_status_t conv_norm_fwd(conv_norm_t desc, int rows, const void* x, const voi
                             const void* gate, void* x_out, void* h, void* h_scales,
                             void* stream);
 
+/* ---- a residual block in 4 bits ------------------------------------------------ */
+
+/* The calls above as a residual block in one call:
+ *   h = norm_in(x);  z = fc2(fc1(h));  (x', h') = norm_out(x, z, gate)
+ * where h and what lies between the layers stay in the workspace.  Made from
+ * descriptors that stay the caller's, keep their settings and strides, and must outlive
+ * it: norm_in has a norm_pre alone and gives h in 4 bits; fc1 takes these and gives 4
+ * bits; fc2 takes these and gives z in norm_out's z_dtype, contiguous; neither has a
+ * residual.  The norms share C and x_dtype, and formats, widths and tensor scales fit
+ * from call to call; conv_fp4_block_fwd checks all of it. */
+typedef struct gbconv_fp4_block_s* conv_fp4_block_t;
+conv_status_t conv_fp4_block_create(conv_fp4_block_t* out, conv_norm_t norm_in, conv_fp4_t fc1,
+                                    conv_fp4_t fc2, conv_norm_t norm_out);
+conv_status_t conv_fp4_block_destroy(conv_fp4_block_t desc);
+/* Weights and biases (NULL: none) as in conv_fp4_fwd; they must stay valid while the
+ * descriptor is used. */
+conv_status_t conv_fp4_block_set_weights(conv_fp4_block_t desc, const void* w1_codes,
+                                         const void* w1_scales, const float* b1,
+                                         const void* w2_codes, const void* w2_scales,
+                                         const float* b2);
+/* Bytes of device workspace for M rows. */
+conv_status_t conv_fp4_block_workspace_size(conv_fp4_block_t desc, int M, size_t* bytes);
+/* x, gate, x_out, h_out, h_out_scales: as x, gate, x_out, h, h_scales of norm_out's
+ * conv_norm_fwd.  h, h_scales: norm_in(x) where the block before handed it on, else NULL.
+ * ws: 16-byte aligned.  M may be 0.  Stream-ordered. */
+conv_status_t conv_fp4_block_fwd(conv_fp4_block_t desc, int M, const void* x, const void* h,
+                                 const void* h_scales, const void* gate, void* x_out,
+                                 void* h_out, void* h_out_scales, void* ws, size_t ws_bytes,
+                                 void* stream);
+
 /* ---- status ------------------------------------------------------------- */
 
 /* Synchronizes the stream, then reads and clears the device error word:

@@ -153,6 +153,53 @@ def test_norm_refusals(B):
     B.conv_norm_destroy(d)
 
 
+def test_block_refusals(B):
+    MX, RMS, CODES = B.CONV_FP4_MX, B.CONV_NORM_RMS, B.CONV_FP4_IO_CODES
+
+    def norm(C=64, out=B.CONV_NORM_OUT_FLOAT, **kw):
+        d = B.conv_norm_create(C, **kw)
+        B.conv_norm_set_pre(d, RMS)
+        if out:
+            B.conv_norm_set_output(d, out)
+        return d
+    n_in, n_out = norm(out=B.CONV_NORM_OUT_FP4_MX), norm()
+    fc1, fc2 = B.conv_fp4_create(MX, 64, 96, CODES, CODES), B.conv_fp4_create(MX, 96, 64, CODES)
+    make = B.conv_fp4_block_create
+    refused(B, BAD, make, None, fc1, fc2, n_out)
+    refused(B, BAD, make, n_in, fc2, fc1, n_out)                           # widths
+    refused(B, BAD, make, norm(), fc1, fc2, n_out)                         # h not in 4 bits
+    refused(B, BAD, make, norm(out=B.CONV_NORM_OUT_FP4_NV), fc1, fc2, n_out)
+    refused(B, BAD, make, n_in, B.conv_fp4_create(MX, 64, 96, CODES), fc2, n_out)
+    refused(B, BAD, make, n_in, fc1, B.conv_fp4_create(MX, 96, 64, CODES, B.CONV_FP4_IO_F32), n_out)
+    refused(B, BAD, make, n_in, fc1, fc2, norm(x_dtype=B.CONV_F32))
+    d = make(n_in, fc1, fc2, n_out)
+    fwd, size = B.conv_fp4_block_fwd, B.conv_fp4_block_workspace_size
+    # h 5 x 64 and t 5 x 96 (codes of 160 and 240 bytes, one row of scale tiles each), z: each
+    # from a 256-byte boundary
+    assert size(d, 5) == 256 + 512 + 256 + 512 + 768 and size(d, 0) == 0
+    refused(B, BAD, size, d, -1)
+    refused(B, UNSUP, size, d, (1 << 30) + 1)
+    refused(B, BAD, fwd, d, 5, P, None, None, None, P, P, None, P, 1 << 20)      # no weights
+    refused(B, BAD, B.conv_fp4_block_set_weights, d, P, None, None, P, P, None)
+    refused(B, ALIGN, B.conv_fp4_block_set_weights, d, P, P + 8, None, P, P, None)
+    refused(B, ALIGN, B.conv_fp4_block_set_weights, d, P, P, P + 2, P, P, None)
+    B.conv_fp4_block_set_weights(d, P, P, None, P, P, None)
+    fwd(d, 0, None, None, None, None, None, None, None, None, 0)
+    refused(B, WS, fwd, d, 5, P, None, None, None, P, P, None, P, size(d, 5) - 1)
+    refused(B, ALIGN, fwd, d, 5, P, None, None, None, P, P, None, P + 8, 1 << 20)
+    refused(B, BAD, fwd, d, 5, P, P, None, None, P, P, None, P, 1 << 20)         # h without scales
+    refused(B, BAD, fwd, d, 5, P, None, None, P, P, P, None, P, 1 << 20)         # a gate without need
+    refused(B, BAD, fwd, d, 5, P, None, None, None, P, P, P, P, 1 << 20)         # scales of a float h
+    refused(B, BAD, fwd, d, 5, None, None, None, None, P, P, None, P, 1 << 20)
+    # a descriptor changed afterwards
+    B.conv_fp4_set_epilogue(fc2, 0, 1)
+    refused(B, BAD, fwd, d, 5, P, None, None, None, P, P, None, P, 1 << 20)
+    B.conv_fp4_set_epilogue(fc2, 0, 0)
+    B.conv_norm_set_strides(n_in, 70)
+    refused(B, BAD, fwd, d, 5, P, None, None, None, P, P, None, P, 1 << 20)
+    B.conv_fp4_block_destroy(d)
+
+
 def test_reference_rounding():
     """The tests' own reference: levels, ties and saturation of E2M1 and E4M3."""
     v = np.array([0.25, 0.2501, 0.75, 0.7499, 1.25, 1.75, 2.5, 3.5, 5.0, 5.001, 7.0, -0.3, -9.0])

@@ -231,3 +231,46 @@ def test_residual_block(fmt, rows, C, hidden):
     for got, want in ((xo, v), (h, hh)):
         off = np.linalg.norm(got.double().cpu().numpy() - want) / np.linalg.norm(want)
         assert off <= 0.01, off
+
+
+def test_residual_block_is_its_parts():
+    """The block's one call against the layers called one by one: bit for bit; strided x and
+    outputs, x' in place, another stream, weights exchanged in a layer of the block."""
+    torch = need_gpu()
+    from cnn_convolution_gemm_gb300.residual_block import Fp4ResidualBlock
+    torch.manual_seed(3)
+    rows, C, hidden = 37, 160, 352
+    w = [1 + 0.1 * torch.randn(C, device="cuda") for _ in range(3)]
+    blk = Fp4ResidualBlock(C, hidden, B.CONV_FP4_MX, residual_scale=0.5, gate=B.CONV_GATE_SIGMOID, gate_rows=10,
+                           w_pre=w[0], w_post=w[1], w_next=w[2], b1=torch.randn(hidden, device="cuda"))
+    rand = lambda *s: torch.randn(*s, device="cuda").bfloat16()  # noqa: E731
+    blk.prepack(rand(hidden, C), rand(C, hidden))
+    gate = rand(4, C)
+
+    def parts(x, x_out=None):
+        h = blk.norm_in(x, want_x=False)[1]
+        z = blk.fc2(blk.fc1(h, bias=blk.b1))
+        return blk.norm_out(x, z, gate=gate, x_out=x_out)
+
+    def same(got, want):
+        return all(torch.equal(a.view(torch.int16), b.view(torch.int16)) for a, b in zip(got, want))
+    x = rand(rows, C)
+    want = [t.clone() for t in parts(x)]
+    assert same(blk(x, gate=gate), want)
+    wide, out = rand(rows, C + 9), torch.empty(rows, C + 5, dtype=torch.bfloat16, device="cuda")
+    wide[:, 3:3 + C] = x
+    at, to = wide[:, 3:3 + C], out[:, 2:2 + C]
+    strided = [t.clone() for t in parts(at, to)]
+    to.zero_()
+    assert same([t.contiguous() for t in blk(at, gate=gate, x_out=to)], strided)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        y = x.clone()
+        got = blk(y, gate=gate, x_out=y)
+    s.synchronize()
+    assert got[0] is y and same(got, want)
+    blk.fc1.prepack(rand(hidden, C))
+    want = [t.clone() for t in parts(x)]
+    assert same(blk(x, gate=gate), want)
+    B.conv_sync_status(torch.cuda.current_stream().cuda_stream)
