@@ -325,9 +325,74 @@ struct Raw16 {
   }
 };
 
+// 16 bytes of global memory that a neighbouring lane may load too.
+__device__ __forceinline__ uint4 load16_cached(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p));
+  return r;
+}
+
+// Raw16 of rows at any alignment: the 16-byte words that hold the elements, and how far
+// into the first of them they start.  Single elements at the tensor's two ends, so that
+// no word reaches outside it.
 template <typename T>
-__device__ __forceinline__ void store16(T* row, int c, int cols, bool vec, const float (&v)[16]) {
-  if (vec && c + 16 <= cols) {
+struct RawAny16 {
+  static constexpr int N = sizeof(T) / 2, WORDS = 8 * N;
+  uint32_t w[WORDS + 4];
+  uint32_t shift;  // bytes
+
+  // first, last: the tensor's first and last rows (at least 16 columns, rows no closer)
+  __device__ __forceinline__ void load(const T* row, int c, int cols, bool first, bool last) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(row + c);
+    // a word starts up to 14 bytes before the elements and ends up to 14 bytes after them:
+    // in this row, or in the one before or after
+    if (c + 16 <= cols && (c > 0 || !first) && (c + 24 <= cols || !last)) {
+      shift = at & 15;
+      const char* const p = reinterpret_cast<const char*>(at - shift);
+#pragma unroll
+      for (int i = 0; i <= 2 * N; ++i) {
+        // the last word holds nothing where the elements start on a word
+        const uint4 v = i < 2 * N || shift ? load16_cached(p + 16 * i) : make_uint4(0, 0, 0, 0);
+        w[4 * i] = v.x;
+        w[4 * i + 1] = v.y;
+        w[4 * i + 2] = v.z;
+        w[4 * i + 3] = v.w;
+      }
+    } else {
+      shift = 0;
+      Raw16<T> raw;
+      raw.load(row, c, cols, false);
+#pragma unroll
+      for (int i = 0; i < WORDS; ++i) w[i] = raw.b[i / 8].w[i % 8];
+#pragma unroll
+      for (int i = WORDS; i < WORDS + 4; ++i) w[i] = 0;
+    }
+  }
+  __device__ __forceinline__ void get(float (&v)[16]) const {
+    uint32_t a[WORDS + 2], b[WORDS + 1];
+#pragma unroll
+    for (int i = 0; i < WORDS + 2; ++i) a[i] = shift & 8 ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < WORDS + 1; ++i) b[i] = shift & 4 ? a[i + 1] : a[i];
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) {
+      if constexpr (sizeof(T) == 2) {
+        const uint32_t h = __funnelshift_r(b[i], b[i + 1], (shift & 2) * 8);
+        v[2 * i] = __uint_as_float(h << 16);
+        v[2 * i + 1] = __uint_as_float(h & 0xFFFF0000u);
+      } else {
+        v[i] = __uint_as_float(b[i]);
+      }
+    }
+  }
+};
+
+// 16 consecutive columns of a row that allows 32-byte accesses.
+template <typename T>
+__device__ __forceinline__ void store16(T* row, int c, int cols, const float (&v)[16]) {
+  if (c + 16 <= cols) {
     constexpr int N = sizeof(T) / 2;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -347,6 +412,72 @@ __device__ __forceinline__ void store16(T* row, int c, int cols, bool vec, const
 #pragma unroll
     for (int i = 0; i < 16; ++i)
       if (c + i < cols) store_f32(row + c + i, v[i]);
+  }
+}
+
+// Stores consecutive columns of a row at any alignment, from column c0, 16 to a lane (v), up
+// to column cols.  lane, lanes: which of the lanes that share the row (a warp, or a part of
+// it).  A lane hands the elements that lie in its neighbour's 16-byte words on to it, and
+// stores the words that its own elements and the ones it got fill; single elements where
+// the lanes' columns begin and end inside a word.  All lanes of the warp call it; cols <= c0
+// stores nothing.
+template <typename T>
+__device__ __forceinline__ void store_warp_any16(T* row, int c0, int cols, const float (&v)[16],
+                                                 int lane, int lanes) {
+  constexpr int WORDS = 4 * sizeof(T), PER = 16 / sizeof(T);  // 32-bit words, elements of 16 bytes
+  const int c = c0 + lane * 16;
+  const int end = c0 + 16 * lanes < cols ? c0 + 16 * lanes : cols;
+  const uint32_t shift = reinterpret_cast<uintptr_t>(row + c0) & 15;
+  const int ahead = (int)(shift / sizeof(T));  // elements in front of the first in its word
+  uint32_t a[WORDS + 4];
+#pragma unroll
+  for (int i = 0; i < WORDS; ++i) {
+    if constexpr (sizeof(T) == 2) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      a[4 + i] = *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+      a[4 + i] = __float_as_uint(v[i]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) a[i] = __shfl_up_sync(0xFFFFFFFFu, a[WORDS + i], 1);
+  // the words from 16 - shift bytes on
+  const uint32_t from = 16 - shift;
+  uint32_t b[WORDS + 2], d[WORDS + 1];
+  if (from & 16) {
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) a[i] = a[i + 4];
+  }
+#pragma unroll
+  for (int i = 0; i < WORDS + 2; ++i) b[i] = from & 8 ? a[i + 2] : a[i];
+#pragma unroll
+  for (int i = 0; i < WORDS + 1; ++i) d[i] = from & 4 ? b[i + 1] : b[i];
+  if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) d[i] = __funnelshift_r(d[i], d[i + 1], (from & 2) * 8);
+  }
+#pragma unroll
+  for (int k = 0; k < WORDS / 4; ++k) {
+    const int first = c - ahead + k * PER;
+    if (first >= c0 && first + PER <= end) {
+      *reinterpret_cast<uint4*>(row + first) =
+          make_uint4(d[4 * k], d[4 * k + 1], d[4 * k + 2], d[4 * k + 3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        if (first + i < c0 || first + i >= end) continue;
+        if constexpr (sizeof(T) == 2)
+          reinterpret_cast<uint16_t*>(row)[first + i] =
+              (uint16_t)(d[4 * k + i / 2] >> (16 * (i & 1)));
+        else
+          reinterpret_cast<uint32_t*>(row)[first + i] = d[4 * k + i];
+      }
+    }
+  }
+  if (lane == lanes - 1) {  // what would have been handed on
+#pragma unroll
+    for (int i = 16 - PER; i < 16; ++i)
+      if (i >= 16 - ahead && c + i < cols) store_f32(row + c + i, v[i]);
   }
 }
 

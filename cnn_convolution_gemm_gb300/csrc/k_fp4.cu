@@ -2,6 +2,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "fp4.cuh"
 #include "internal.h"
@@ -44,10 +45,11 @@ __device__ __forceinline__ Walk walk(int wx_log2) {
   return w;
 }
 
-template <int FMT, typename T, bool NARROW>
+// ANY: rows that 32-byte accesses do not fit
+template <int FMT, typename T, bool NARROW, bool ANY>
 __global__ void __launch_bounds__(THREADS)
-    quantize_kernel(const T* __restrict__ x, long long ldx, int rows, int cols, int vec,
-                    int wx_log2, const TensorScale ts, uint8_t* __restrict__ codes,
+    quantize_kernel(const T* __restrict__ x, long long ldx, int rows, int cols, int wx_log2,
+                    const TensorScale ts, uint8_t* __restrict__ codes,
                     uint8_t* __restrict__ scales) {
   gb::allow_dependents();
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -56,11 +58,15 @@ __global__ void __launch_bounds__(THREADS)
   // the lanes of a warp go round together: the shuffles below are the warp's
   const long long lead = w.row - (NARROW ? (threadIdx.x & 31) >> (5 + wx_log2) : 0);
   for (long long r0 = w.row, l0 = lead; l0 < rows; r0 += ROWS * w.step, l0 += ROWS * w.step) {
-    Raw16<T> raw[ROWS];
+    std::conditional_t<ANY, RawAny16<T>, Raw16<T>> raw[ROWS];
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
       const long long r = r0 + i * w.step;
-      if (r < rows) raw[i].load(x + r * ldx, w.c, cols, vec);
+      if (r >= rows) continue;
+      if constexpr (ANY)
+        raw[i].load(x + r * ldx, w.c, cols, r == 0, r == rows - 1);
+      else
+        raw[i].load(x + r * ldx, w.c, cols, true);
     }
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
@@ -76,31 +82,35 @@ __global__ void __launch_bounds__(THREADS)
   }
 }
 
-template <int FMT, typename T, bool NARROW>
+template <int FMT, typename T, bool NARROW, bool ANY>
 __global__ void __launch_bounds__(THREADS)
     dequantize_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
-                      int rows, int cols, int vec, int wx_log2, float tensor_scale,
+                      int rows, int cols, int wx_log2, float tensor_scale,
                       T* __restrict__ y, long long ldy) {
   gb::allow_dependents();
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Walk w = walk<NARROW>(wx_log2);
-  if (w.c >= cols) return;
+  const int lane = NARROW ? w.c / 16 : (int)(threadIdx.x & 31);  // of the row's in this warp
+  // ANY: the lanes of a warp hand elements to one another, and go round together
+  if (w.c - (ANY ? lane * 16 : 0) >= cols) return;
+  const long long lead =
+      w.row - (NARROW && ANY ? (int)(threadIdx.x & 31) >> (5 + wx_log2) : 0);
   const long long pitch = code_pitch(cols);
   const int tiles = tiles_per_row(FMT, cols), b = w.c / kBlock<FMT>;
-  for (long long r0 = w.row; r0 < rows; r0 += ROWS * w.step) {
+  for (long long r0 = w.row, l0 = lead; l0 < rows; r0 += ROWS * w.step, l0 += ROWS * w.step) {
     uint2 code[ROWS];
     uint32_t byte[ROWS];
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
       const long long r = r0 + i * w.step;
-      if (r >= rows) continue;
+      if (r >= rows || w.c >= cols) continue;
       code[i] = *reinterpret_cast<const uint2*>(codes + r * pitch + w.c / 2);
       byte[i] = scales[scale_word_offset(r, b >> 2, tiles) + (b & 3)];
     }
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
       const long long r = r0 + i * w.step;
-      if (r >= rows) continue;
+      if ((ANY ? l0 + i * w.step : r) >= rows) continue;
       const float s = scale_value<FMT>(byte[i], tensor_scale);
       float lo[8], hi[8], v[16];
       unpack8_e2m1(code[i].x, lo);
@@ -110,7 +120,11 @@ __global__ void __launch_bounds__(THREADS)
         v[k] = lo[k] * s;
         v[8 + k] = hi[k] * s;
       }
-      store16(y + r * ldy, w.c, cols, vec, v);
+      if constexpr (ANY)
+        store_warp_any16(y + r * ldy, w.c - lane * 16, r < rows ? cols : 0, v, lane,
+                         NARROW ? 32 >> -wx_log2 : 32);
+      else
+        store16(y + r * ldy, w.c, cols, v);
     }
   }
 }
@@ -179,20 +193,30 @@ template <int FMT, typename T>
 cudaError_t quantize_t(int rows, int cols, const void* x, long long ldx, float ts, void* codes,
                        void* scales, cudaStream_t st) {
   const Shape s = walk_shape(rows, cols);
-  auto* kern = s.wx_log2 < 0 ? quantize_kernel<FMT, T, true> : quantize_kernel<FMT, T, false>;
-  return launch_walk(kern, s.grid, st, static_cast<const T*>(x), ldx, rows, cols,
-                     (int)rows_vec<T>(x, ldx, 32), s.wx_log2, tensor_scale(ts),
-                     static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales));
+  const bool narrow = s.wx_log2 < 0;
+  auto* kern = rows_vec<T>(x, ldx, 32)
+                   ? (narrow ? quantize_kernel<FMT, T, true, false>
+                             : quantize_kernel<FMT, T, false, false>)
+                   : (narrow ? quantize_kernel<FMT, T, true, true>
+                             : quantize_kernel<FMT, T, false, true>);
+  return launch_walk(kern, s.grid, st, static_cast<const T*>(x), ldx, rows, cols, s.wx_log2,
+                     tensor_scale(ts), static_cast<uint8_t*>(codes),
+                     static_cast<uint8_t*>(scales));
 }
 
 template <int FMT, typename T>
 cudaError_t dequantize_t(int rows, int cols, const void* codes, const void* scales, float ts,
                          void* y, long long ldy, cudaStream_t st) {
   const Shape s = walk_shape(rows, cols);
-  auto* kern = s.wx_log2 < 0 ? dequantize_kernel<FMT, T, true> : dequantize_kernel<FMT, T, false>;
+  const bool narrow = s.wx_log2 < 0;
+  auto* kern = rows_vec<T>(y, ldy, 32)
+                   ? (narrow ? dequantize_kernel<FMT, T, true, false>
+                             : dequantize_kernel<FMT, T, false, false>)
+                   : (narrow ? dequantize_kernel<FMT, T, true, true>
+                             : dequantize_kernel<FMT, T, false, true>);
   return launch_walk(kern, s.grid, st, static_cast<const uint8_t*>(codes),
-                     static_cast<const uint8_t*>(scales), rows, cols, (int)rows_vec<T>(y, ldy, 32),
-                     s.wx_log2, ts, static_cast<T*>(y), ldy);
+                     static_cast<const uint8_t*>(scales), rows, cols, s.wx_log2, ts,
+                     static_cast<T*>(y), ldy);
 }
 
 }  // namespace

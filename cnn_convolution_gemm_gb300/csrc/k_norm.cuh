@@ -22,12 +22,16 @@ namespace gb {
 namespace norm {
 using namespace gb::fp4;
 
-// How a row lies over its T threads, N columns each.  VEC: groups of 16 consecutive
-// columns, group i of thread t at 16 (i T + t); else single columns at i T + t
+// How a row lies over its T threads, N columns each.  SINGLE: single columns at i T + t
 // (coalesced at any alignment; the first half of them exists in every thread, since a
-// row has more than T N / 2 columns).
-template <int T, int N, bool VEC>
+// row has more than T N / 2 columns).  Else groups of 16 consecutive columns, group i of
+// thread t at 16 (i T + t): GROUPS of rows that allow 32-byte accesses, ANY of others
+// (which costs instructions: 12544 x 1001 fp32 79 us, SINGLE 40; for codes, which need
+// their blocks in one place).
+enum Layout { SINGLE, GROUPS, ANY };
+template <int T, int N, Layout L>
 struct Lay {
+  static constexpr bool VEC = L != SINGLE;
   static constexpr int G = VEC ? N / 16 : N;  // groups
   static constexpr int GC = VEC ? 16 : 1;     // columns of a group
   static __device__ __forceinline__ int col(int i, int t) { return GC * (i * T + t); }
@@ -36,17 +40,22 @@ struct Lay {
   }
 };
 
-// A thread's elements as loaded.
-template <typename E, int T, int N, bool VEC>
+// A thread's elements as loaded, from row r of rows.
+template <typename E, int T, int N, Layout LAY>
 struct RowRegs {
-  using L = Lay<T, N, VEC>;
-  std::conditional_t<VEC, Raw16<E>, E> raw[L::G];
+  using L = Lay<T, N, LAY>;
+  std::conditional_t<LAY == GROUPS, Raw16<E>, std::conditional_t<LAY == ANY, RawAny16<E>, E>>
+      raw[L::G];
 
-  __device__ __forceinline__ void load(const E* row, int t, int C, bool vec) {
+  __device__ __forceinline__ void load(const void* t0, long long ld, long long r, long long rows,
+                                       int t, int C) {
+    const E* const row = static_cast<const E*>(t0) + r * ld;
 #pragma unroll
     for (int i = 0; i < L::G; ++i) {
-      if constexpr (VEC)
-        raw[i].load(row, L::col(i, t), C, vec);
+      if constexpr (LAY == GROUPS)
+        raw[i].load(row, L::col(i, t), C, true);
+      else if constexpr (LAY == ANY)
+        raw[i].load(row, L::col(i, t), C, r == 0, r == rows - 1);
       else
         raw[i] = L::has(i, t, C) ? row[L::col(i, t)] : E(0.0f);
     }
@@ -54,7 +63,7 @@ struct RowRegs {
   __device__ __forceinline__ void get(float (&v)[N]) const {
 #pragma unroll
     for (int i = 0; i < L::G; ++i) {
-      if constexpr (VEC) {
+      if constexpr (LAY != SINGLE) {
         float e[16];
         raw[i].get(e);
 #pragma unroll
@@ -66,7 +75,7 @@ struct RowRegs {
   }
 };
 
-// The same from a row in shared memory (VEC; columns past C read as 0).
+// The same from a row in shared memory (GROUPS; columns past C read as 0).
 template <typename E, int T, int N>
 __device__ __forceinline__ void read_shared(float (&v)[N], const uint8_t* row, int t, int C) {
 #pragma unroll
@@ -91,18 +100,22 @@ __device__ __forceinline__ void read_shared(float (&v)[N], const uint8_t* row, i
   }
 }
 
-template <typename E, int T, int N, bool VEC>
-__device__ __forceinline__ void store_row(E* row, int t, int C, bool vec, const float (&v)[N]) {
-  using L = Lay<T, N, VEC>;
+template <typename E, int T, int N, Layout LAY>
+__device__ __forceinline__ void store_row(E* row, int t, int C, const float (&v)[N]) {
+  using L = Lay<T, N, LAY>;
 #pragma unroll
   for (int i = 0; i < L::G; ++i) {
-    if constexpr (VEC) {
+    if constexpr (LAY == SINGLE) {
+      if (L::has(i, t, C)) store_f32(row + L::col(i, t), v[i]);
+    } else {
       float e[16];
 #pragma unroll
       for (int k = 0; k < 16; ++k) e[k] = v[16 * i + k];
-      store16(row, L::col(i, t), C, vec, e);
-    } else {
-      if (L::has(i, t, C)) store_f32(row + L::col(i, t), v[i]);
+      const int c0 = L::col(i, t & ~31);  // the warp's first column
+      if constexpr (LAY == GROUPS)
+        store16(row, L::col(i, t), C, e);
+      else if (c0 < C)
+        store_warp_any16(row, c0, C, e, t & 31, 32);
     }
   }
 }
@@ -134,11 +147,11 @@ __device__ __forceinline__ void row_sum(float (&v)[R], float (*red)[32 * R], int
 
 // Four of the thread's elements of a row of weights or biases (fp32; 0 past the row's
 // end), from element k of its N.
-template <int T, int N, bool VEC>
+template <int T, int N, Layout LAY>
 __device__ __forceinline__ float4 load_weights(const float* w, int k, int t, int C, bool vec) {
-  using L = Lay<T, N, VEC>;
+  using L = Lay<T, N, LAY>;
   float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  if constexpr (VEC) {
+  if constexpr (LAY != SINGLE) {
     const int c = L::col(k / 16, t) + k % 16;
     if (vec && c + 4 <= C) return *reinterpret_cast<const float4*>(w + c);
     if (c < C) f.x = w[c];
@@ -158,23 +171,23 @@ __device__ __forceinline__ float4 load_weights(const float* w, int k, int t, int
 // elements in shared memory, four at a time and thread by thread (a thread reads back only
 // what it wrote): beside the ring, L1 is too small for them (32768 x 8192 bf16: 35 % of
 // the weights' sectors missed, 386 us; a deeper ring was slower still).
-template <int T, int N, bool VEC>
+template <int T, int N, Layout LAY>
 struct Weights {
   const float* w;      // nullptr: none
   const float4* held;  // nullptr: not held
 
   __device__ __forceinline__ float4 get(int k, int t, int C, bool vec) const {
-    return held ? held[k / 4 * T + t] : load_weights<T, N, VEC>(w, k, t, C, vec);
+    return held ? held[k / 4 * T + t] : load_weights<T, N, LAY>(w, k, t, C, vec);
   }
 };
 
 // v = norm(v) with weight and bias, for R rows; elements past a row's end come and stay 0.
-template <int T, int N, bool VEC, int R>
+template <int T, int N, Layout LAY, int R>
 __device__ __forceinline__ void norm_rows(float (&v)[R][N], int kind, float eps,
-                                          const Weights<T, N, VEC>& w,
-                                          const Weights<T, N, VEC>& b, int t, int C, bool vec_w,
+                                          const Weights<T, N, LAY>& w,
+                                          const Weights<T, N, LAY>& b, int t, int C, bool vec_w,
                                           float inv, float (*red)[32 * R], int& turn) {
-  using L = Lay<T, N, VEC>;
+  using L = Lay<T, N, LAY>;
   float sum[R];
   if (kind == CONV_NORM_LAYER) {
 #pragma unroll
@@ -193,7 +206,7 @@ __device__ __forceinline__ void norm_rows(float (&v)[R][N], int kind, float eps,
       const float mean = sum[k] * inv;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const bool in = VEC ? L::col(i / 16, t) + i % 16 < C : L::has(i, t, C);
+        const bool in = LAY != SINGLE ? L::col(i / 16, t) + i % 16 < C : L::has(i, t, C);
         v[k][i] = in ? v[k][i] - mean : 0.0f;
       }
     }
@@ -245,20 +258,16 @@ __device__ __forceinline__ void norm_rows(float (&v)[R][N], int kind, float eps,
   }
 }
 
-struct Vec {
-  bool x, z, g, xo, h, w;  // 32-byte accesses to rows; 16-byte ones to weights
-};
-
 constexpr int RING = 2;  // stages of R rows in shared memory
 
 // Stores h of one row.
-template <typename TZ, int T, int N, bool VEC>
-__device__ __forceinline__ void store_h(const NormArgs& a, const TensorScale& ts, const Vec& vec,
-                                        long long r, int t, const float (&v)[N]) {
+template <typename TZ, int T, int N, Layout LAY>
+__device__ __forceinline__ void store_h(const NormArgs& a, const TensorScale& ts, long long r,
+                                        int t, const float (&v)[N]) {
   const int C = a.C;
   if (a.out == CONV_NORM_OUT_FLOAT) {
-    store_row<TZ, T, N, VEC>(static_cast<TZ*>(a.h) + r * a.ldh, t, C, vec.h, v);
-  } else if constexpr (VEC) {
+    store_row<TZ, T, N, LAY>(static_cast<TZ*>(a.h) + r * a.ldh, t, C, v);
+  } else if constexpr (LAY != SINGLE) {
 #pragma unroll
     for (int i = 0; i < N / 16; ++i) {
       const int c0 = 16 * (i * T + (t & ~31));  // the warp's first column
@@ -280,11 +289,12 @@ __device__ __forceinline__ void store_h(const NormArgs& a, const TensorScale& ts
 }
 
 // T == 32: one row per warp (4 in a block), else R rows at a time per block of T threads.
-// AHEAD (VEC, T > 32): x and z (if given) come through the ring; else R is 1.
-template <typename TX, typename TZ, int T, int N, bool VEC, bool AHEAD, int R>
+// AHEAD (GROUPS, T > 32): x and z (if given) come through the ring; else R is 1.
+// vec_w: 16-byte accesses to weights.
+template <typename TX, typename TZ, int T, int N, Layout LAY, bool AHEAD, int R>
 __global__ void __launch_bounds__(T == 32 ? 128 : T)
-    norm_kernel(const NormArgs a, const TensorScale ts, const Vec vec) {
-  static_assert(AHEAD || R == 1, "rows of a step");
+    norm_kernel(const NormArgs a, const TensorScale ts, const bool vec_w) {
+  static_assert(AHEAD ? LAY == GROUPS : R == 1, "rows of a step");
   __shared__ float red[2][32 * R];
   __shared__ uint64_t full[RING];
   extern __shared__ uint4 ring[];  // RING x R x (a row of z, a row of x); weights
@@ -305,7 +315,7 @@ __global__ void __launch_bounds__(T == 32 ? 128 : T)
       gb::bulk_load(to + zb, static_cast<const TX*>(a.x) + (r + k) * a.ldx, &full[stage], xb);
     }
   };
-  Weights<T, N, VEC> w_post{a.w_post, nullptr}, b_post{a.b_post, nullptr},
+  Weights<T, N, LAY> w_post{a.w_post, nullptr}, b_post{a.b_post, nullptr},
       w_pre{a.w_pre, nullptr}, b_pre{a.b_pre, nullptr};
   if (AHEAD && t == 0) {
     for (int i = 0; i < RING; ++i) gb::mbar_init(&full[i], 1);
@@ -317,11 +327,11 @@ __global__ void __launch_bounds__(T == 32 ? 128 : T)
       for (int i = 0; i < RING && first + i * step < a.rows; ++i) fetch(first + i * step, i);
     float4* to = reinterpret_cast<float4*>(reinterpret_cast<uint8_t*>(ring) +
                                            RING * R * (size_t)(zb + xb));
-    const auto hold = [&](Weights<T, N, VEC>& w) {
+    const auto hold = [&](Weights<T, N, LAY>& w) {
       if (!w.w) return;
 #pragma unroll
       for (int k = 0; k < N; k += 4)
-        to[k / 4 * T + t] = load_weights<T, N, VEC>(w.w, k, t, C, vec.w);
+        to[k / 4 * T + t] = load_weights<T, N, LAY>(w.w, k, t, C, vec_w);
       w.held = to;
       to += T * N / 4;
     };
@@ -331,25 +341,26 @@ __global__ void __launch_bounds__(T == 32 ? 128 : T)
     hold(b_pre);
     __syncthreads();
   }
+  const unsigned gates = (unsigned)(a.rows - 1) / (unsigned)a.gate_rows + 1;  // rows of them
   int turn = 0, stage = 0;
   uint32_t phase = 0;
   bool ok = true;  // after a wait that ran out nothing is waited for again (the rows are
                    // then wrong, and the error word says so); the barriers stay in step
   for (long long r = first; r < a.rows; r += step) {
-    RowRegs<TX, T, N, VEC> rx;
-    RowRegs<TZ, T, N, VEC> rz;
+    RowRegs<TX, T, N, LAY> rx;
+    RowRegs<TZ, T, N, LAY> rz;
     const uint8_t* const sz =
         reinterpret_cast<const uint8_t*>(ring) + stage * (size_t)(zb + xb) * R;
     if constexpr (AHEAD) {
       if (ok) ok = gb::mbar_wait_bounded(&full[stage], phase, a.wait_ns, a.err);
     } else {
-      if (a.z) rz.load(static_cast<const TZ*>(a.z) + r * a.ldz, t, C, vec.z);
-      rx.load(static_cast<const TX*>(a.x) + r * a.ldx, t, C, vec.x);
+      if (a.z) rz.load(a.z, a.ldz, r, a.rows, t, C);
+      rx.load(a.x, a.ldx, r, a.rows, t, C);
     }
     float v[R][N];
     if (a.z) {
       float u[R][N];
-      RowRegs<TZ, T, N, VEC> rg[R];
+      RowRegs<TZ, T, N, LAY> rg[R];
 #pragma unroll
       for (int k = 0; k < R; ++k) {
         if constexpr (AHEAD)
@@ -359,12 +370,11 @@ __global__ void __launch_bounds__(T == 32 ? 128 : T)
         if (a.gate_kind != CONV_GATE_NONE) {
           // rows and gate_rows are ints: a 32-bit division
           const unsigned row = (unsigned)(r + k < a.rows ? r + k : r);
-          const long long at = (long long)(row / (unsigned)a.gate_rows) * a.ldg;
-          rg[k].load(static_cast<const TZ*>(a.gate) + at, t, C, vec.g);
+          rg[k].load(a.gate, a.ldg, row / (unsigned)a.gate_rows, gates, t, C);
         }
       }
       if (a.post != CONV_NORM_NONE)
-        norm_rows<T, N, VEC, R>(u, a.post, a.eps_post, w_post, b_post, t, C, vec.w, inv, red, turn);
+        norm_rows<T, N, LAY, R>(u, a.post, a.eps_post, w_post, b_post, t, C, vec_w, inv, red, turn);
 #pragma unroll
       for (int k = 0; k < R; ++k) {
         if (a.gate_kind != CONV_GATE_NONE) {
@@ -397,14 +407,13 @@ __global__ void __launch_bounds__(T == 32 ? 128 : T)
 #pragma unroll
       for (int k = 0; k < R; ++k)
         if (r + k < a.rows)
-          store_row<TX, T, N, VEC>(static_cast<TX*>(a.x_out) + (r + k) * a.ldxo, t, C, vec.xo,
-                                   v[k]);
+          store_row<TX, T, N, LAY>(static_cast<TX*>(a.x_out) + (r + k) * a.ldxo, t, C, v[k]);
     }
     if (a.pre != CONV_NORM_NONE) {
-      norm_rows<T, N, VEC, R>(v, a.pre, a.eps_pre, w_pre, b_pre, t, C, vec.w, inv, red, turn);
+      norm_rows<T, N, LAY, R>(v, a.pre, a.eps_pre, w_pre, b_pre, t, C, vec_w, inv, red, turn);
 #pragma unroll
       for (int k = 0; k < R; ++k)
-        if (r + k < a.rows) store_h<TZ, T, N, VEC>(a, ts, vec, r + k, t, v[k]);
+        if (r + k < a.rows) store_h<TZ, T, N, LAY>(a, ts, r + k, t, v[k]);
     }
     if constexpr (AHEAD) {
       // every thread has read the rows before a barrier: norm_pre's, or this one
@@ -430,10 +439,11 @@ __global__ void __launch_bounds__(T == 32 ? 128 : T)
 
 // Blocks of T threads that walk over the rows, as many as the SMs hold.
 template <typename K>
-cudaError_t launch_rows(K* kern, const NormArgs& a, const Vec& vec, int block, int rows_per_block,
-                        int smem, cudaStream_t st) {
+cudaError_t launch_rows(K* kern, const NormArgs& a, int block, int rows_per_block, int smem,
+                        cudaStream_t st) {
   const long long per_sm = gb_blocks_per_sm(reinterpret_cast<const void*>(kern), block, smem);
   const long long most = (long long)gb_num_sms() * std::max(1LL, per_sm);
+  const auto vec = [](const float* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)std::min<long long>(gb_ceil_div_ll(a.rows, rows_per_block), most));
   cfg.blockDim = dim3((unsigned)block);
@@ -444,41 +454,29 @@ cudaError_t launch_rows(K* kern, const NormArgs& a, const Vec& vec, int block, i
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, tensor_scale(a.h_scale), vec);
+  const bool vec_w = vec(a.w_post) && vec(a.b_post) && vec(a.w_pre) && vec(a.b_pre);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, tensor_scale(a.h_scale), vec_w);
   if (e == cudaSuccess) gb_count_launch();
   return e;
 }
 
-template <typename TX, typename TZ>
-Vec vec_of(const NormArgs& a) {
-  const auto vec_w = [](const float* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
-  Vec vec;
-  vec.x = rows_vec<TX>(a.x, a.ldx, 32);
-  vec.z = rows_vec<TZ>(a.z, a.ldz, 32);
-  vec.g = rows_vec<TZ>(a.gate, a.ldg, 32);
-  vec.xo = rows_vec<TX>(a.x_out, a.ldxo, 32);
-  vec.h = rows_vec<TZ>(a.h, a.ldh, 32);
-  vec.w = vec_w(a.w_post) && vec_w(a.b_post) && vec_w(a.w_pre) && vec_w(a.b_pre);
-  return vec;
-}
-
-template <typename TX, typename TZ, int T, int N, bool VEC>
+template <typename TX, typename TZ, int T, int N, Layout LAY>
 cudaError_t launch_direct(const NormArgs& a, cudaStream_t st) {
-  return launch_rows(norm_kernel<TX, TZ, T, N, VEC, false, 1>, a, vec_of<TX, TZ>(a),
-                     T == 32 ? 128 : T, T == 32 ? 4 : 1, 0, st);
+  return launch_rows(norm_kernel<TX, TZ, T, N, LAY, false, 1>, a, T == 32 ? 128 : T,
+                     T == 32 ? 4 : 1, 0, st);
 }
 
 // 16 consecutive columns a thread up to 4096 channels (as few dependent steps as a row
 // allows), 32 above
-template <typename TX, typename TZ>
+template <typename TX, typename TZ, Layout LAY>
 cudaError_t launch_groups(const NormArgs& a, cudaStream_t st) {
-  if (a.C <= 512) return launch_direct<TX, TZ, 32, 16, true>(a, st);
-  if (a.C <= 1024) return launch_direct<TX, TZ, 64, 16, true>(a, st);
-  if (a.C <= 2048) return launch_direct<TX, TZ, 128, 16, true>(a, st);
-  if (a.C <= 4096) return launch_direct<TX, TZ, 256, 16, true>(a, st);
-  if (a.C <= 8192) return launch_direct<TX, TZ, 256, 32, true>(a, st);
-  if (a.C <= 16384) return launch_direct<TX, TZ, 512, 32, true>(a, st);
-  return launch_direct<TX, TZ, 1024, 32, true>(a, st);
+  if (a.C <= 512) return launch_direct<TX, TZ, 32, 16, LAY>(a, st);
+  if (a.C <= 1024) return launch_direct<TX, TZ, 64, 16, LAY>(a, st);
+  if (a.C <= 2048) return launch_direct<TX, TZ, 128, 16, LAY>(a, st);
+  if (a.C <= 4096) return launch_direct<TX, TZ, 256, 16, LAY>(a, st);
+  if (a.C <= 8192) return launch_direct<TX, TZ, 256, 32, LAY>(a, st);
+  if (a.C <= 16384) return launch_direct<TX, TZ, 512, 32, LAY>(a, st);
+  return launch_direct<TX, TZ, 1024, 32, LAY>(a, st);
 }
 
 // 8 single columns a thread (an access is one element: with more of them registers, not
@@ -486,14 +484,14 @@ cudaError_t launch_groups(const NormArgs& a, cudaStream_t st) {
 // row needs them
 template <typename TX, typename TZ>
 cudaError_t launch_single(const NormArgs& a, cudaStream_t st) {
-  if (a.C <= 256) return launch_direct<TX, TZ, 32, 8, false>(a, st);
-  if (a.C <= 512) return launch_direct<TX, TZ, 64, 8, false>(a, st);
-  if (a.C <= 1024) return launch_direct<TX, TZ, 128, 8, false>(a, st);
-  if (a.C <= 2048) return launch_direct<TX, TZ, 256, 8, false>(a, st);
-  if (a.C <= 4096) return launch_direct<TX, TZ, 512, 8, false>(a, st);
-  if (a.C <= 8192) return launch_direct<TX, TZ, 1024, 8, false>(a, st);
-  if (a.C <= 16384) return launch_direct<TX, TZ, 1024, 16, false>(a, st);
-  return launch_direct<TX, TZ, 1024, 32, false>(a, st);
+  if (a.C <= 256) return launch_direct<TX, TZ, 32, 8, SINGLE>(a, st);
+  if (a.C <= 512) return launch_direct<TX, TZ, 64, 8, SINGLE>(a, st);
+  if (a.C <= 1024) return launch_direct<TX, TZ, 128, 8, SINGLE>(a, st);
+  if (a.C <= 2048) return launch_direct<TX, TZ, 256, 8, SINGLE>(a, st);
+  if (a.C <= 4096) return launch_direct<TX, TZ, 512, 8, SINGLE>(a, st);
+  if (a.C <= 8192) return launch_direct<TX, TZ, 1024, 8, SINGLE>(a, st);
+  if (a.C <= 16384) return launch_direct<TX, TZ, 1024, 16, SINGLE>(a, st);
+  return launch_direct<TX, TZ, 1024, 32, SINGLE>(a, st);
 }
 
 // 0: does not fit shared memory
@@ -507,17 +505,20 @@ int ahead_smem(const NormArgs& a) {
 
 template <typename TX, typename TZ, int T, int R>
 cudaError_t launch_ahead(const NormArgs& a, cudaStream_t st) {
-  auto* kern = norm_kernel<TX, TZ, T, 16, true, true, R>;
+  auto* kern = norm_kernel<TX, TZ, T, 16, GROUPS, true, R>;
   const int smem = ahead_smem<TX, TZ, T, R>(a);
   const cudaError_t e = gb_set_smem_once(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
-  return launch_rows(kern, a, vec_of<TX, TZ>(a), T, R, smem, st);
+  return launch_rows(kern, a, T, R, smem, st);
 }
 
 template <typename TX, typename TZ>
 cudaError_t launch(const NormArgs& a, cudaStream_t st) {
-  // 16 consecutive columns a thread where that makes 32-byte loads, or codes
-  const bool vec = rows_vec<TX>(a.x, a.ldx, 32) && (!a.z || rows_vec<TZ>(a.z, a.ldz, 32));
+  const bool codes = a.out != CONV_NORM_OUT_FLOAT;
+  const auto fit_x = [](const void* p, long long ld) { return !p || rows_vec<TX>(p, ld, 32); };
+  const auto fit_z = [](const void* p, long long ld) { return !p || rows_vec<TZ>(p, ld, 32); };
+  const bool vec = fit_x(a.x, a.ldx) && fit_x(a.x_out, a.ldxo) && fit_z(a.z, a.ldz) &&
+                   fit_z(a.gate, a.ldg) && (codes || fit_z(a.h, a.ldh));
   // many rows of whole 16-byte pieces: two at a time, through the ring
   if (vec && a.C > 512 && a.C <= 8192 && a.C * sizeof(TX) % 16 == 0 &&
       a.C * sizeof(TZ) % 16 == 0 && a.rows >= 2LL * gb_num_sms() * (8192 / a.C) * 4) {
@@ -530,8 +531,8 @@ cudaError_t launch(const NormArgs& a, cudaStream_t st) {
       if (ahead_smem<TX, TZ, 512, 1>(a)) return launch_ahead<TX, TZ, 512, 1>(a, st);
     }
   }
-  return vec || a.out != CONV_NORM_OUT_FLOAT ? launch_groups<TX, TZ>(a, st)
-                                             : launch_single<TX, TZ>(a, st);
+  if (vec) return launch_groups<TX, TZ, GROUPS>(a, st);
+  return codes ? launch_groups<TX, TZ, ANY>(a, st) : launch_single<TX, TZ>(a, st);
 }
 
 }  // namespace norm

@@ -366,3 +366,33 @@ def test_offsets_past_32_bits():
     err = R.product_bound(xv, wv, want, 0, 24)
     assert (np.abs(y[-5:].double().cpu().numpy() - want) <= err).all()
     assert not y[:-5].any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("cols", [23, 300, 1001, 1536, 2420])
+def test_quantize_at_every_alignment(dtype, cols):
+    """Rows that start anywhere: the codes of aligned rows, and values that go back to their
+    places and no others."""
+    torch, fp4 = _fp4()
+    torch.manual_seed(cols)
+    dt, rows = (torch.bfloat16 if dtype == "bf16" else torch.float32), 21
+    wide = torch.zeros(rows, -(-cols // 16) * 16, dtype=dt, device="cuda")
+    wide[:, :cols] = torch.randn(rows, cols, device="cuda").to(dt)
+    for fmt, g in ((R.MX, 1.0), (R.NV, 0.003)):
+        want = fp4.quantize(wide[:, :cols], fmt, g)
+        blocks = -(-cols // R.BLOCK[fmt])
+        scales = R.unpack(want)[1][:, :blocks]
+        values = fp4.dequantize(want, dtype=dt, out=torch.empty_like(wide)[:, :cols])
+        for offset in range(9):
+            for ld in (cols, cols + 1, cols + 5):
+                buf = torch.full((offset + rows * ld + 9,), 7.5, dtype=dt, device="cuda")
+                at = buf.as_strided((rows, cols), (ld, 1), offset)
+                at.copy_(wide[:, :cols])
+                got = fp4.quantize(at, fmt, g)
+                assert torch.equal(got.codes, want.codes)
+                np.testing.assert_array_equal(R.unpack(got)[1][:, :blocks], scales)
+                buf.fill_(7.5)
+                fp4.dequantize(got, out=at)
+                assert torch.equal(at, values)
+                at.fill_(7.5)
+                assert bool((buf == 7.5).all())
