@@ -121,6 +121,33 @@ int gb_blocks_per_sm(const void* func, int threads, int smem) {
   return known[{func, {smem, dev}}] = n;
 }
 
+int gb_active_clusters(const void* func, int threads, int smem, int cluster) {
+  const int dev = current_device();
+  static std::mutex mu;
+  static std::map<std::pair<const void*, std::pair<int, int>>, int> known;  // (cluster, device)
+  std::lock_guard<std::mutex> lk(mu);
+  auto it = known.find({func, {cluster, dev}});
+  if (it != known.end()) return it->second;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)cluster);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (gb_set_smem_once(func, smem) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, func, &cfg) != cudaSuccess) {
+    cudaGetLastError();  // clear a failed query, which is not remembered
+    return 0;
+  }
+  return known[{func, {cluster, dev}}] = n;
+}
+
 unsigned long long gb_wait_limit_ns() {
   static unsigned long long v = [] {
     const char* e = getenv("GBCONV_WAIT_LIMIT_MS");

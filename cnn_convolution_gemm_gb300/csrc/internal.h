@@ -51,6 +51,9 @@ cudaError_t gb_set_smem_once(const void* func, int bytes);
 // Blocks of so many threads and dynamic shared memory that an SM holds at once (cached
 // per kernel, size and device; 0 if the query failed).
 int gb_blocks_per_sm(const void* func, int threads, int smem);
+// Clusters of so many blocks that the device holds at once (0: unknown); one smem size per
+// kernel.
+int gb_active_clusters(const void* func, int threads, int smem, int cluster);
 // Wait limit for device-side bounded waits, in nanoseconds (GBCONV_WAIT_LIMIT_MS).
 unsigned long long gb_wait_limit_ns();
 

@@ -27,6 +27,7 @@ namespace {
 using namespace gb::fp4;
 
 constexpr int BM = 128;
+constexpr int SPLIT_MOST = 8;  // CTAs of a cluster
 
 template <int FMT, int BN, bool PAIR, int YIO>
 struct Cfg {
@@ -58,6 +59,7 @@ struct Cfg {
 struct GemmParams {
   int M, N, ksteps, kmmas_last;  // 64-element MMAs of the last k-step
   int m_tiles, n_tiles;          // PAIR: m_tiles counts 256-row units
+  int split;                     // SPLIT: CTAs of a cluster
   int act, vec_y, vec_r;         // rows of y for the TMA, of the residual for 16-byte loads
   float alpha;
   TensorScale y_scale;
@@ -258,7 +260,11 @@ __device__ __forceinline__ void finish_codes(const GemmParams& p, float (&v)[32]
       p.ys[scale_word_offset(m, b >> 2, tiles) + (b & 3)] = 0;
 }
 
-template <int FMT, int BN, bool PAIR, int YIO>
+// SPLIT (128 x 128 tiles): the CTAs of a cluster share one tile, each with a range of the
+// reduction.  An epilogue warp's block of 32 x 32 belongs to one of them, which gets the
+// others' partial sums through distributed shared memory (in the ring, whose last
+// operands are read by then) and adds them in the order of the ranges.
+template <int FMT, int BN, bool PAIR, int YIO, bool SPLIT>
 __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR, YIO>::THREADS, 1)
     fp4_gemm_kernel(const __grid_constant__ CUtensorMap tm_x,
                     const __grid_constant__ CUtensorMap tm_xs,
@@ -287,8 +293,14 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR, YIO>::THREADS, 1)
   const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0);  // uniform
   const int lane = threadIdx.x & 31;
   const uint32_t rank = PAIR ? gb::cluster_ctarank() : 0u;
-  const int unit0 = PAIR ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
-  const int ustep = PAIR ? (int)(gridDim.x >> 1) : (int)gridDim.x;
+  const int part = SPLIT ? (int)gb::cluster_ctarank() : 0;
+  const int unit0 = PAIR ? (int)(blockIdx.x >> 1)
+                    : SPLIT ? (int)blockIdx.x / p.split : (int)blockIdx.x;
+  const int ustep = PAIR ? (int)(gridDim.x >> 1)
+                    : SPLIT ? p.m_tiles * p.n_tiles : (int)gridDim.x;
+  // this CTA's k-steps
+  const int k0 = SPLIT ? (int)((long long)p.ksteps * part / p.split) : 0;
+  const int k1 = SPLIT ? (int)((long long)p.ksteps * (part + 1) / p.split) : p.ksteps;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
@@ -348,7 +360,7 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR, YIO>::THREADS, 1)
         if (PAIR)  // of both CTAs
           tx += (box_rows((mt + 1) * BM, p.M) + box_rows(brow + C::BROWS, p.N)) * BKB +
                 ((mt + 1) * BM < p.M ? C::SFA_BYTES : 0) + C::SFB_BYTES;
-        for (int it = 0; it < p.ksteps; ++it) {
+        for (int it = k0; it < k1; ++it) {
           if (!gb::mbar_wait_bounded_warp(&empty[stage], phase ^ 1, p.wait_ns, p.err)) {
             ok = false;
             break;
@@ -402,7 +414,7 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR, YIO>::THREADS, 1)
       bool ok = true;
       for (int u = unit0; u < units && ok; u += ustep) {
         const uint32_t d = tmem + acc * BN;
-        for (int it = 0; it < p.ksteps; ++it) {
+        for (int it = k0; it < k1; ++it) {
           if (!gb::mbar_wait_bounded_warp(&full[stage], phase, p.wait_ns, p.err)) {
             ok = false;
             break;
@@ -427,7 +439,7 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR, YIO>::THREADS, 1)
           }
           __syncwarp();
           // the tile's accumulator is needed only now
-          if (it == 0) {
+          if (it == k0) {
             if (!gb::mbar_wait_bounded_warp(&tempty[acc], acc_phase ^ 1, p.wait_ns, p.err)) {
               ok = false;
               break;
@@ -445,7 +457,7 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR, YIO>::THREADS, 1)
               const uint32_t id = gb::idesc_fp4(MM, BN, MX, MX ? (k & 1) * 2 : 0);
               if (k < mmas)
                 gb::tc_mma_fp4<MX, PAIR>(d, ad + k * 2, bd + k * 2, id, sfa + 4 * j,
-                                         sfb + 4 * j * C::PB, it > 0 || k > 0 ? 1u : 0u);
+                                         sfb + 4 * j * C::PB, it > k0 || k > 0 ? 1u : 0u);
             }
             if constexpr (PAIR)
               gb::tc_commit_pair_multicast(&empty[stage], 0x3);
@@ -479,6 +491,11 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR, YIO>::THREADS, 1)
       }
       __syncwarp();
       gb::mbar_wait_bounded_warp(mma_done, 0, p.wait_ns, p.err);
+    }
+    if constexpr (SPLIT) {  // the epilogue's two barriers
+      __syncwarp();
+      gb::cluster_sync();
+      gb::cluster_sync();
     }
   } else {
     if constexpr (BN == 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
@@ -518,16 +535,18 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR, YIO>::THREADS, 1)
         bias[i] = p.bias && n < p.N ? p.bias[n] : 0.0f;
       }
     };
+    const bool mine = !SPLIT || (warp - 4) % p.split == part;  // the block of the tile
     asm volatile("griddepcontrol.wait;" ::: "memory");
     int m0 = row_of(unit0), nb = unit0 % p.n_tiles * BN + group * CW;
-    if (unit0 < units) {
+    if (mine && unit0 < units) {
       fetch_res(m0, nb);
       fetch_bias(nb);
     }
     for (int u = unit0; u < units; u += ustep) {
       const int un = u + ustep, m_next = un < units ? row_of(un) : p.M;
       const int nb_next = un % p.n_tiles * BN + group * CW;
-      if (!gb::mbar_wait_bounded(&tfull[acc], acc_phase, p.wait_ns, p.err)) break;
+      // SPLIT: a wait that ran out is in the error word, and the barriers are still met
+      if (!gb::mbar_wait_bounded(&tfull[acc], acc_phase, p.wait_ns, p.err) && !SPLIT) break;
       gb::tc_fence_after();
       const uint32_t t = tmem + ((uint32_t)(q * 32) << 16) + acc * BN + group * CW;
       uint32_t r[CW / 32][32];
@@ -542,7 +561,33 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR, YIO>::THREADS, 1)
         else
           gb::mbar_arrive(&tempty[acc]);
       }
-      if (m0 < p.M) {
+      if constexpr (SPLIT) {
+        static_assert(CW == 32, "a block");
+        const int block = warp - 4, slots = (C::EPI_WARPS + p.split - 1) / p.split;
+        const int owner = block % p.split, slot = block / p.split;
+        // [range][slot][column][row]: a warp's store is 128 bytes in one piece (as 16-byte
+        // pieces of rows 65 x 8192 x 2048 took 9.0 us, so 8.2)
+        float* const sums = reinterpret_cast<float*>(smem);
+        static_assert(C::STAGES * C::STAGE_BYTES >= (16 + SPLIT_MOST - 1) * 4096, "sums");
+        __syncwarp();
+        gb::cluster_sync();  // every CTA's operands are read, and every CTA runs
+        const uint32_t to = gb::mapa_shared(
+            gb::smem_u32(sums + (part * slots + slot) * 1024 + lane), (uint32_t)owner);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) gb::store_cluster(to + 128 * i, r[0][i]);
+        gb::cluster_sync();
+        if (mine) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) r[0][i] = 0u;
+          for (int k = 0; k < p.split; ++k) {
+            const float* const from = sums + (k * slots + slot) * 1024 + lane;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              r[0][i] = __float_as_uint(__uint_as_float(r[0][i]) + from[32 * i]);
+          }
+        }
+      }
+      if (mine && m0 < p.M) {
 #pragma unroll
         for (int s = 0; s < NP; ++s) {
           const int n0 = nb + PC * s;
@@ -602,8 +647,8 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR, YIO>::THREADS, 1)
   }
 }
 
-template <int FMT, int BN, bool PAIR, int YIO>
-cudaError_t launch_tile(const Fp4Gemm& g, cudaStream_t st) {
+template <int FMT, int BN, bool PAIR, int YIO, bool SPLIT>
+cudaError_t launch_tile(const Fp4Gemm& g, int split, cudaStream_t st) {
   using C = Cfg<FMT, BN, PAIR, YIO>;
   CUtensorMap tx, txs, tw, tws;
   if (!codes_map(&tx, g.x, g.M, g.C, BM) || !codes_map(&tw, g.w, g.K, g.C, C::BROWS) ||
@@ -617,6 +662,7 @@ cudaError_t launch_tile(const Fp4Gemm& g, cudaStream_t st) {
   p.kmmas_last = gb_ceil_div(g.C - (p.ksteps - 1) * 256, 64);
   p.m_tiles = (int)gb_ceil_div_ll(g.M, PAIR ? 2 * BM : BM);
   p.n_tiles = gb_ceil_div(g.K, BN);
+  p.split = split;
   p.act = g.act;
   p.alpha = g.alpha;
   p.y_scale = tensor_scale(g.y_scale);
@@ -651,7 +697,7 @@ cudaError_t launch_tile(const Fp4Gemm& g, cudaStream_t st) {
   }
   p.err = gb_device_error_word();
   p.wait_ns = gb_wait_limit_ns();
-  auto* kern = fp4_gemm_kernel<FMT, BN, PAIR, YIO>;
+  auto* kern = fp4_gemm_kernel<FMT, BN, PAIR, YIO, SPLIT>;
   cudaError_t e = gb_set_smem_once(reinterpret_cast<const void*>(kern), C::SMEM);
   if (e != cudaSuccess) return e;
   // the kernel's register split waits forever if it was launched with fewer
@@ -662,8 +708,9 @@ cudaError_t launch_tile(const Fp4Gemm& g, cudaStream_t st) {
   if (BN == 256 && regs * C::THREADS < 128 * 40 + 512 * 104) return cudaErrorLaunchOutOfResources;
   const long long units = (long long)p.m_tiles * p.n_tiles;
   if (units >= (1LL << 31)) return cudaErrorInvalidValue;
-  const int slots = PAIR ? gb_num_sms() / 2 : gb_num_sms();
-  const int grid = (int)std::min<long long>(units, slots) * (PAIR ? 2 : 1);
+  const int cluster = PAIR ? 2 : split;  // split 1: no cluster
+  const int grid =
+      (int)std::min<long long>(units, SPLIT ? units : gb_num_sms() / cluster) * cluster;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(C::THREADS);
@@ -673,14 +720,30 @@ cudaError_t launch_tile(const Fp4Gemm& g, cudaStream_t st) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = PAIR ? 2 : 1;
+  attr[1].val.clusterDim.x = cluster;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = PAIR ? 2 : 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   e = cudaLaunchKernelEx(&cfg, kern, tx, txs, tw, tws, ty, tx64, tw64, p);
   if (e == cudaSuccess) gb_count_launch();
   return e;
+}
+
+// CTAs that share a tile: as many as all tiles' clusters find room for at once (more, and
+// they run one after another: 65 x 8192 x 2048 by 8 14.6 us, by 4 8.2), if they save 14
+// k-steps (0.2 us each); the exchange costs 2.5 us.
+template <int FMT, int YIO>
+int split_of(const Fp4Gemm& g, long long tiles) {
+  using C = Cfg<FMT, 128, false, YIO>;
+  auto* kern = fp4_gemm_kernel<FMT, 128, false, YIO, true>;
+  const int ksteps = gb_ceil_div(g.C, 256);
+  for (int s = SPLIT_MOST; s > 1; --s) {
+    if (tiles * s > gb_num_sms() || ksteps - gb_ceil_div(ksteps, s) < 14) continue;
+    if (tiles <= gb_active_clusters(reinterpret_cast<const void*>(kern), C::THREADS, C::SMEM, s))
+      return s;
+  }
+  return 1;
 }
 
 template <int FMT, int YIO>
@@ -692,8 +755,10 @@ cudaError_t launch_y(const Fp4Gemm& g, cudaStream_t st) {
   const long long tiles = gb_ceil_div_ll(g.M, 128) * gb_ceil_div_ll(g.K, 128);
   const int sms = gb_num_sms();
   const bool small = tiles <= sms || (tiles <= 2 * sms && g.C <= 1024) || g.K <= 128;
-  return small ? launch_tile<FMT, 128, false, YIO>(g, st)
-               : launch_tile<FMT, 256, true, YIO>(g, st);
+  if (!small) return launch_tile<FMT, 256, true, YIO, false>(g, 1, st);
+  const int split = split_of<FMT, YIO>(g, tiles);
+  return split > 1 ? launch_tile<FMT, 128, false, YIO, true>(g, split, st)
+                   : launch_tile<FMT, 128, false, YIO, false>(g, 1, st);
 }
 
 template <int FMT>

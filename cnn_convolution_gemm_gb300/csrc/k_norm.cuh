@@ -288,11 +288,27 @@ __device__ __forceinline__ void store_h(const NormArgs& a, const TensorScale& ts
   }
 }
 
+// Blocks an SM has to hold, which caps the registers: the compiler otherwise spends more on
+// loads it spreads between the sums (8192 x 4096 with gates 52 us, uncapped 74; 14552 x 2579
+// bf16 145, 223).  Without z more fit: 16384 x 8192 bf16 to MX 106 -> 91 us.
+constexpr int least_blocks(int T, int N, Layout lay, bool ahead, bool has_z) {
+  const int block = T == 32 ? 128 : T;
+  int threads = 1;
+  if (ahead)
+    threads = has_z ? 512 : 1024;
+  else if (N == 8)
+    threads = has_z ? (T >= 512 ? 1024 : 768) : 1;
+  else if (N == 16)
+    threads = lay == ANY ? 1 : 512;
+  return threads > block ? threads / block : 1;
+}
+
 // T == 32: one row per warp (4 in a block), else R rows at a time per block of T threads.
 // AHEAD (GROUPS, T > 32): x and z (if given) come through the ring; else R is 1.
+// HASZ false: z is not given (the first norm of a network or block).
 // vec_w: 16-byte accesses to weights.
-template <typename TX, typename TZ, int T, int N, Layout LAY, bool AHEAD, int R>
-__global__ void __launch_bounds__(T == 32 ? 128 : T)
+template <typename TX, typename TZ, int T, int N, Layout LAY, bool AHEAD, int R, bool HASZ>
+__global__ void __launch_bounds__(T == 32 ? 128 : T, least_blocks(T, N, LAY, AHEAD, HASZ))
     norm_kernel(const NormArgs a, const TensorScale ts, const bool vec_w) {
   static_assert(AHEAD ? LAY == GROUPS : R == 1, "rows of a step");
   __shared__ float red[2][32 * R];
@@ -305,13 +321,13 @@ __global__ void __launch_bounds__(T == 32 ? 128 : T)
   const long long first =
       T == 32 ? blockIdx.x * 4LL + (threadIdx.x >> 5) : (long long)blockIdx.x * R;
   const float inv = 1.0f / (float)C;
-  const uint32_t zb = a.z ? (uint32_t)C * sizeof(TZ) : 0u, xb = (uint32_t)C * sizeof(TX);
+  const uint32_t zb = HASZ ? (uint32_t)C * sizeof(TZ) : 0u, xb = (uint32_t)C * sizeof(TX);
   const auto fetch = [&](long long r, int stage) {  // one thread
     uint8_t* to = reinterpret_cast<uint8_t*>(ring) + stage * (size_t)(zb + xb) * R;
     const int rows = (int)(a.rows - r < R ? a.rows - r : R);
     gb::mbar_arrive_expect_tx(&full[stage], (zb + xb) * rows);
     for (int k = 0; k < rows; ++k, to += zb + xb) {
-      if (a.z) gb::bulk_load(to, static_cast<const TZ*>(a.z) + (r + k) * a.ldz, &full[stage], zb);
+      if (HASZ) gb::bulk_load(to, static_cast<const TZ*>(a.z) + (r + k) * a.ldz, &full[stage], zb);
       gb::bulk_load(to + zb, static_cast<const TX*>(a.x) + (r + k) * a.ldx, &full[stage], xb);
     }
   };
@@ -354,11 +370,11 @@ __global__ void __launch_bounds__(T == 32 ? 128 : T)
     if constexpr (AHEAD) {
       if (ok) ok = gb::mbar_wait_bounded(&full[stage], phase, a.wait_ns, a.err);
     } else {
-      if (a.z) rz.load(a.z, a.ldz, r, a.rows, t, C);
+      if constexpr (HASZ) rz.load(a.z, a.ldz, r, a.rows, t, C);
       rx.load(a.x, a.ldx, r, a.rows, t, C);
     }
     float v[R][N];
-    if (a.z) {
+    if constexpr (HASZ) {
       float u[R][N];
       RowRegs<TZ, T, N, LAY> rg[R];
 #pragma unroll
@@ -462,8 +478,9 @@ cudaError_t launch_rows(K* kern, const NormArgs& a, int block, int rows_per_bloc
 
 template <typename TX, typename TZ, int T, int N, Layout LAY>
 cudaError_t launch_direct(const NormArgs& a, cudaStream_t st) {
-  return launch_rows(norm_kernel<TX, TZ, T, N, LAY, false, 1>, a, T == 32 ? 128 : T,
-                     T == 32 ? 4 : 1, 0, st);
+  auto* kern = a.z ? norm_kernel<TX, TZ, T, N, LAY, false, 1, true>
+                   : norm_kernel<TX, TZ, T, N, LAY, false, 1, false>;
+  return launch_rows(kern, a, T == 32 ? 128 : T, T == 32 ? 4 : 1, 0, st);
 }
 
 // 16 consecutive columns a thread up to 4096 channels (as few dependent steps as a row
@@ -505,7 +522,8 @@ int ahead_smem(const NormArgs& a) {
 
 template <typename TX, typename TZ, int T, int R>
 cudaError_t launch_ahead(const NormArgs& a, cudaStream_t st) {
-  auto* kern = norm_kernel<TX, TZ, T, 16, GROUPS, true, R>;
+  auto* kern = a.z ? norm_kernel<TX, TZ, T, 16, GROUPS, true, R, true>
+                   : norm_kernel<TX, TZ, T, 16, GROUPS, true, R, false>;
   const int smem = ahead_smem<TX, TZ, T, R>(a);
   const cudaError_t e = gb_set_smem_once(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;

@@ -248,6 +248,39 @@ def test_product_of_few_rows(fmt, M, C, K):
     _product(fmt, M, C, K, "bfloat16", "float32", 0, True, M % 2 == 0)
 
 
+# the reduction shared out over 2, 3 and 4 CTAs, evenly and not; empty blocks; a last k-step
+# of one MMA
+@pytest.mark.parametrize("fmt", FMTS, ids=NAMES.get)
+@pytest.mark.parametrize("M,C,K,x,y,act,bias,residual", [
+    (65, 2048, 64, "bfloat16", "bfloat16", 0, True, True),
+    (130, 3301, 201, "float32", "float32", 1, True, True),
+    (300, 4500, 72, "bfloat16", None, 3, True, False),
+    (257, 2600, 1000, None, None, 0, False, False),
+    (140, 9000, 400, None, "bfloat16", 4, False, True),
+    (129, 3090, 2100, "bfloat16", "float32", 2, True, False),
+    (390, 4160, 1300, "bfloat16", "bfloat16", 1, False, True)])
+def test_product_of_split_reductions(fmt, M, C, K, x, y, act, bias, residual):
+    _product(fmt, M, C, K, x, y, act, bias, residual)
+
+
+@pytest.mark.parametrize("fmt", FMTS, ids=NAMES.get)
+def test_product_of_split_reductions_again(fmt):
+    """The same bits every time, strided rows, and the output over the residual."""
+    _product(fmt, 150, 4200, 203, "bfloat16", "bfloat16", 1, True, True, strided=True)
+    torch, fp4 = _fp4()
+    rng = np.random.default_rng(10)
+    M, C, K = 200, 5000, 264
+    x, r = _to(torch, _activations(rng, M, C), torch.bfloat16), _to(
+        torch, rng.standard_normal((M, K)), torch.bfloat16)
+    layer = fp4.Fp4Linear(C, K, fmt, has_residual=True)
+    layer.prepack(_to(torch, rng.standard_normal((K, C)), torch.bfloat16))
+    want = layer(x, residual=r)
+    for _ in range(5):
+        assert torch.equal(layer(x, residual=r), want)
+    assert torch.equal(layer(x, residual=r, out=r), want)
+    _sync(torch)
+
+
 @pytest.mark.parametrize("fmt", FMTS, ids=NAMES.get)
 @pytest.mark.parametrize("M,C,K", [(4, 256, 96), (150, 512, 300), (2600, 1100, 1100)])
 def test_product_infinities_stay_in_their_rows(fmt, M, C, K):
