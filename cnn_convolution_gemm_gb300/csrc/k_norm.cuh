@@ -362,17 +362,34 @@ __global__ void __launch_bounds__(T == 32 ? 128 : T, least_blocks(T, N, LAY, AHE
   uint32_t phase = 0;
   bool ok = true;  // after a wait that ran out nothing is waited for again (the rows are
                    // then wrong, and the error word says so); the barriers stay in step
+  // without the ring: the next row's z and x are on their way from the moment on that
+  // their registers are free (12544 x 1001 fp32 40 -> 38 us, 14552 x 2579 146 -> 134; rows
+  // above 8192 have none to spare: 2656 x 12544 fp32 176, so 214)
+  constexpr bool NEXT = !AHEAD && N <= 16 && T * N <= 8192;
+  RowRegs<TX, T, N, LAY> next_x;
+  RowRegs<TZ, T, N, LAY> next_z;
+  const auto load_z = [&](RowRegs<TZ, T, N, LAY>& to, long long r) {
+    if (HASZ && r < a.rows) to.load(a.z, a.ldz, r, a.rows, t, C);
+  };
+  const auto load_x = [&](RowRegs<TX, T, N, LAY>& to, long long r) {
+    if (r < a.rows) to.load(a.x, a.ldx, r, a.rows, t, C);
+  };
+  if constexpr (NEXT) {
+    load_z(next_z, first);
+    load_x(next_x, first);
+  }
   for (long long r = first; r < a.rows; r += step) {
-    RowRegs<TX, T, N, LAY> rx;
-    RowRegs<TZ, T, N, LAY> rz;
     const uint8_t* const sz =
         reinterpret_cast<const uint8_t*>(ring) + stage * (size_t)(zb + xb) * R;
-    if constexpr (AHEAD) {
-      if (ok) ok = gb::mbar_wait_bounded(&full[stage], phase, a.wait_ns, a.err);
-    } else {
+    RowRegs<TX, T, N, LAY> own_x;
+    RowRegs<TZ, T, N, LAY> own_z;
+    RowRegs<TX, T, N, LAY>& rx = NEXT ? next_x : own_x;
+    RowRegs<TZ, T, N, LAY>& rz = NEXT ? next_z : own_z;
+    if constexpr (!AHEAD && !NEXT) {
       if constexpr (HASZ) rz.load(a.z, a.ldz, r, a.rows, t, C);
       rx.load(a.x, a.ldx, r, a.rows, t, C);
     }
+    if (AHEAD && ok) ok = gb::mbar_wait_bounded(&full[stage], phase, a.wait_ns, a.err);
     float v[R][N];
     if constexpr (HASZ) {
       float u[R][N];
@@ -383,6 +400,7 @@ __global__ void __launch_bounds__(T == 32 ? 128 : T, least_blocks(T, N, LAY, AHE
           read_shared<TZ, T, N>(u[k], sz + k * (zb + xb), t, C);
         else
           rz.get(u[k]);
+        if constexpr (NEXT) load_z(rz, r + step);
         if (a.gate_kind != CONV_GATE_NONE) {
           // rows and gate_rows are ints: a 32-bit division
           const unsigned row = (unsigned)(r + k < a.rows ? r + k : r);
@@ -407,6 +425,7 @@ __global__ void __launch_bounds__(T == 32 ? 128 : T, least_blocks(T, N, LAY, AHE
           read_shared<TX, T, N>(v[k], sz + k * (zb + xb) + zb, t, C);
         else
           rx.get(v[k]);
+        if constexpr (NEXT) load_x(rx, r + step);
 #pragma unroll
         for (int i = 0; i < N; ++i) v[k][i] = fmaf(a.rs, u[k][i], v[k][i]);
       }
@@ -417,6 +436,7 @@ __global__ void __launch_bounds__(T == 32 ? 128 : T, least_blocks(T, N, LAY, AHE
           read_shared<TX, T, N>(v[k], sz + k * (zb + xb), t, C);
         else
           rx.get(v[k]);
+        if constexpr (NEXT) load_x(rx, r + step);
       }
     }
     if (a.x_out) {
