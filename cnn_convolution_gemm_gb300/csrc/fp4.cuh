@@ -237,19 +237,6 @@ __device__ __forceinline__ void store_quantized16(const uint2& packed, uint32_t 
     *reinterpret_cast<uint32_t*>(scales + scale_word_offset(r, tj, tiles)) = word;
 }
 
-// One warp turns 512 consecutive columns of a row, 16 to a lane (v; zero past the last
-// column), into codes and scales.  c0: the warp's first column.  All lanes call it.
-template <int FMT>
-__device__ __forceinline__ void store_warp_row(const float (&v)[16], const TensorScale& ts,
-                                               long long r, int c0, int cols,
-                                               uint8_t* __restrict__ codes,
-                                               uint8_t* __restrict__ scales) {
-  uint2 packed;
-  uint32_t word;
-  quantize16<FMT>(v, ts, packed, word);
-  store_quantized16<FMT>(packed, word, r, c0 + (int)(threadIdx.x & 31) * 16, cols, codes, scales);
-}
-
 template <typename T>
 __device__ __forceinline__ float load_f32(const T* p) {
   if constexpr (sizeof(T) == 2)

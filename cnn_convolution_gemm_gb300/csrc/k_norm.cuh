@@ -100,22 +100,24 @@ __device__ __forceinline__ void read_shared(float (&v)[N], const uint8_t* row, i
   }
 }
 
+// valid: whether the row exists (lanes of a warp may share it with other rows).
 template <typename E, int T, int N, Layout LAY>
-__device__ __forceinline__ void store_row(E* row, int t, int C, const float (&v)[N]) {
+__device__ __forceinline__ void store_row(E* row, bool valid, int t, int C, const float (&v)[N]) {
   using L = Lay<T, N, LAY>;
 #pragma unroll
   for (int i = 0; i < L::G; ++i) {
     if constexpr (LAY == SINGLE) {
-      if (L::has(i, t, C)) store_f32(row + L::col(i, t), v[i]);
+      if (valid && L::has(i, t, C)) store_f32(row + L::col(i, t), v[i]);
     } else {
       float e[16];
 #pragma unroll
       for (int k = 0; k < 16; ++k) e[k] = v[16 * i + k];
       const int c0 = L::col(i, t & ~31);  // the warp's first column
-      if constexpr (LAY == GROUPS)
-        store16(row, L::col(i, t), C, e);
-      else if (c0 < C)
-        store_warp_any16(row, c0, C, e, t & 31, 32);
+      if constexpr (LAY == GROUPS) {
+        if (valid) store16(row, L::col(i, t), C, e);
+      } else if (c0 < C) {
+        store_warp_any16(row, c0, valid ? C : 0, e, t & 31, T < 32 ? T : 32);
+      }
     }
   }
 }
@@ -125,7 +127,7 @@ __device__ __forceinline__ void store_row(E* row, int t, int C, const float (&v)
 template <int T, int R>
 __device__ __forceinline__ void row_sum(float (&v)[R], float (*red)[32 * R], int& turn) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1)
+  for (int o = (T < 32 ? T : 32) / 2; o; o >>= 1)
 #pragma unroll
     for (int k = 0; k < R; ++k) v[k] += __shfl_xor_sync(0xFFFFFFFFu, v[k], o);
   if constexpr (T > 32) {
@@ -264,9 +266,10 @@ constexpr int RING = 2;  // stages of R rows in shared memory
 template <typename TZ, int T, int N, Layout LAY>
 __device__ __forceinline__ void store_h(const NormArgs& a, const TensorScale& ts, long long r,
                                         int t, const float (&v)[N]) {
+  const bool valid = T >= 32 || r < a.rows;
   const int C = a.C;
   if (a.out == CONV_NORM_OUT_FLOAT) {
-    store_row<TZ, T, N, LAY>(static_cast<TZ*>(a.h) + r * a.ldh, t, C, v);
+    store_row<TZ, T, N, LAY>(static_cast<TZ*>(a.h) + r * a.ldh, valid, t, C, v);
   } else if constexpr (LAY != SINGLE) {
 #pragma unroll
     for (int i = 0; i < N / 16; ++i) {
@@ -280,10 +283,17 @@ __device__ __forceinline__ void store_h(const NormArgs& a, const TensorScale& ts
         for (int k = 0; k < 16; ++k)
           if (16 * (i * T + t) + k >= C) e[k] = 0.0f;
       }
-      if (a.out == CONV_NORM_OUT_FP4_MX)
-        store_warp_row<CONV_FP4_MX>(e, ts, r, c0, C, static_cast<uint8_t*>(a.h), a.hs);
-      else
-        store_warp_row<CONV_FP4_NV>(e, ts, r, c0, C, static_cast<uint8_t*>(a.h), a.hs);
+      uint2 packed;
+      uint32_t word;
+      uint8_t* const codes = static_cast<uint8_t*>(a.h);
+      const int c = 16 * (i * T + t);
+      if (a.out == CONV_NORM_OUT_FP4_MX) {
+        quantize16<CONV_FP4_MX>(e, ts, packed, word);
+        if (valid) store_quantized16<CONV_FP4_MX>(packed, word, r, c, C, codes, a.hs);
+      } else {
+        quantize16<CONV_FP4_NV>(e, ts, packed, word);
+        if (valid) store_quantized16<CONV_FP4_NV>(packed, word, r, c, C, codes, a.hs);
+      }
     }
   }
 }
@@ -292,7 +302,7 @@ __device__ __forceinline__ void store_h(const NormArgs& a, const TensorScale& ts
 // loads it spreads between the sums (8192 x 4096 with gates 52 us, uncapped 74; 14552 x 2579
 // bf16 145, 223).  Without z more fit: 16384 x 8192 bf16 to MX 106 -> 91 us.
 constexpr int least_blocks(int T, int N, Layout lay, bool ahead, bool has_z) {
-  const int block = T == 32 ? 128 : T;
+  const int block = T <= 32 ? 128 : T;
   int threads = 1;
   if (ahead)
     threads = has_z ? 512 : 1024;
@@ -303,12 +313,13 @@ constexpr int least_blocks(int T, int N, Layout lay, bool ahead, bool has_z) {
   return threads > block ? threads / block : 1;
 }
 
-// T == 32: one row per warp (4 in a block), else R rows at a time per block of T threads.
+// T <= 32: 32 / T rows per warp (4 warps in a block), else R rows at a time per block of T
+// threads.
 // AHEAD (GROUPS, T > 32): x and z (if given) come through the ring; else R is 1.
 // HASZ false: z is not given (the first norm of a network or block).
 // vec_w: 16-byte accesses to weights.
 template <typename TX, typename TZ, int T, int N, Layout LAY, bool AHEAD, int R, bool HASZ>
-__global__ void __launch_bounds__(T == 32 ? 128 : T, least_blocks(T, N, LAY, AHEAD, HASZ))
+__global__ void __launch_bounds__(T <= 32 ? 128 : T, least_blocks(T, N, LAY, AHEAD, HASZ))
     norm_kernel(const NormArgs a, const TensorScale ts, const bool vec_w) {
   static_assert(AHEAD ? LAY == GROUPS : R == 1, "rows of a step");
   __shared__ float red[2][32 * R];
@@ -316,10 +327,13 @@ __global__ void __launch_bounds__(T == 32 ? 128 : T, least_blocks(T, N, LAY, AHE
   extern __shared__ uint4 ring[];  // RING x R x (a row of z, a row of x); weights
   gb::allow_dependents();
   const int C = a.C;
-  const int t = T == 32 ? (int)(threadIdx.x & 31) : (int)threadIdx.x;
-  const long long step = T == 32 ? gridDim.x * 4LL : (long long)gridDim.x * R;
+  constexpr int AT_ONCE = T <= 32 ? 128 / T : R;  // rows of a block
+  const int t = T <= 32 ? (int)threadIdx.x & (T - 1) : (int)threadIdx.x;
+  const long long step = (long long)gridDim.x * AT_ONCE;
   const long long first =
-      T == 32 ? blockIdx.x * 4LL + (threadIdx.x >> 5) : (long long)blockIdx.x * R;
+      (long long)blockIdx.x * AT_ONCE + (T <= 32 ? (int)threadIdx.x / T : 0);
+  // the lanes of a warp go round together, as long as its first row exists
+  const int after = T < 32 ? (int)(threadIdx.x & 31) / T : 0;
   const float inv = 1.0f / (float)C;
   const uint32_t zb = HASZ ? (uint32_t)C * sizeof(TZ) : 0u, xb = (uint32_t)C * sizeof(TX);
   const auto fetch = [&](long long r, int stage) {  // one thread
@@ -378,7 +392,7 @@ __global__ void __launch_bounds__(T == 32 ? 128 : T, least_blocks(T, N, LAY, AHE
     load_z(next_z, first);
     load_x(next_x, first);
   }
-  for (long long r = first; r < a.rows; r += step) {
+  for (long long r = first; r - after < a.rows; r += step) {
     const uint8_t* const sz =
         reinterpret_cast<const uint8_t*>(ring) + stage * (size_t)(zb + xb) * R;
     RowRegs<TX, T, N, LAY> own_x;
@@ -403,7 +417,7 @@ __global__ void __launch_bounds__(T == 32 ? 128 : T, least_blocks(T, N, LAY, AHE
         if constexpr (NEXT) load_z(rz, r + step);
         if (a.gate_kind != CONV_GATE_NONE) {
           // rows and gate_rows are ints: a 32-bit division
-          const unsigned row = (unsigned)(r + k < a.rows ? r + k : r);
+          const unsigned row = (unsigned)(r + k < a.rows ? r + k : a.rows - 1);
           rg[k].load(a.gate, a.ldg, row / (unsigned)a.gate_rows, gates, t, C);
         }
       }
@@ -442,14 +456,15 @@ __global__ void __launch_bounds__(T == 32 ? 128 : T, least_blocks(T, N, LAY, AHE
     if (a.x_out) {
 #pragma unroll
       for (int k = 0; k < R; ++k)
-        if (r + k < a.rows)
-          store_row<TX, T, N, LAY>(static_cast<TX*>(a.x_out) + (r + k) * a.ldxo, t, C, v[k]);
+        if (T < 32 || r + k < a.rows)
+          store_row<TX, T, N, LAY>(static_cast<TX*>(a.x_out) + (r + k) * a.ldxo,
+                                   T >= 32 || r < a.rows, t, C, v[k]);
     }
     if (a.pre != CONV_NORM_NONE) {
       norm_rows<T, N, LAY, R>(v, a.pre, a.eps_pre, w_pre, b_pre, t, C, vec_w, inv, red, turn);
 #pragma unroll
       for (int k = 0; k < R; ++k)
-        if (r + k < a.rows) store_h<TZ, T, N, LAY>(a, ts, r + k, t, v[k]);
+        if (T < 32 || r + k < a.rows) store_h<TZ, T, N, LAY>(a, ts, r + k, t, v[k]);
     }
     if constexpr (AHEAD) {
       // every thread has read the rows before a barrier: norm_pre's, or this one
@@ -500,13 +515,15 @@ template <typename TX, typename TZ, int T, int N, Layout LAY>
 cudaError_t launch_direct(const NormArgs& a, cudaStream_t st) {
   auto* kern = a.z ? norm_kernel<TX, TZ, T, N, LAY, false, 1, true>
                    : norm_kernel<TX, TZ, T, N, LAY, false, 1, false>;
-  return launch_rows(kern, a, T == 32 ? 128 : T, T == 32 ? 4 : 1, 0, st);
+  return launch_rows(kern, a, T <= 32 ? 128 : T, T <= 32 ? 128 / T : 1, 0, st);
 }
 
 // 16 consecutive columns a thread up to 4096 channels (as few dependent steps as a row
 // allows), 32 above
 template <typename TX, typename TZ, Layout LAY>
 cudaError_t launch_groups(const NormArgs& a, cudaStream_t st) {
+  if (a.C <= 128) return launch_direct<TX, TZ, 8, 16, LAY>(a, st);
+  if (a.C <= 256) return launch_direct<TX, TZ, 16, 16, LAY>(a, st);
   if (a.C <= 512) return launch_direct<TX, TZ, 32, 16, LAY>(a, st);
   if (a.C <= 1024) return launch_direct<TX, TZ, 64, 16, LAY>(a, st);
   if (a.C <= 2048) return launch_direct<TX, TZ, 128, 16, LAY>(a, st);

@@ -141,6 +141,13 @@ def test_many_rows(post, pre, rows, C, kw):
     _case(post, pre, rows, C, **kw)
 
 
+@pytest.mark.parametrize("rows,C", [(1, 16), (3, 128), (1037, 48), (20003, 112), (5, 144), (2051, 256), (1037, 90), (517, 250)])
+@pytest.mark.parametrize("kw", [{}, {"dt": "float32", "gate": 2, "gate_rows": 5}, {"h_fmt": R.MX, "gate": 1},
+                                {"h_fmt": R.NV, "dt": "float32", "zdt": "bfloat16"}, {"in_place": True}], ids=str)
+def test_narrow_rows_share_warps(rows, C, kw):
+    _case(LN, RMS, rows, C, **kw)
+
+
 def test_mixed_types_strides_in_place_and_first_norm():
     _case(RMS, LN, 20, 320, dt="float32", zdt="bfloat16")
     _case(RMS, LN, 20, 320, dt="bfloat16", zdt="float32")
