@@ -215,26 +215,24 @@ __device__ __forceinline__ void finish_float(const GemmParams& p, const CUtensor
   }
 }
 
-// 32 columns as 4-bit codes: one MX block or two NV blocks of the lane's row.
+// 32 columns of the lane's row (one MX block or two NV blocks): codes and scale bytes.
+// cols: how many of the columns exist.
 template <int FMT>
-__device__ __forceinline__ void finish_codes(const GemmParams& p, float (&v)[32], int m0, int n0) {
-  const long long m = m0 + (threadIdx.x & 31);
-  const int cols = min(32, p.N - n0);
-  activate(v, p.act);
-  if (m >= p.M) return;
+__device__ __forceinline__ void quantize32(const TensorScale& ts, float (&v)[32], int cols,
+                                           uint32_t (&code)[4], uint32_t& bytes) {
   if (cols < 32) {
 #pragma unroll
     for (int i = 0; i < 32; ++i)
       if (i >= cols) v[i] = 0.0f;
   }
   constexpr int B = kBlock<FMT>;
-  uint32_t bytes = 0, code[4];
+  bytes = 0;
 #pragma unroll
   for (int k = 0; k < 32 / B; ++k) {
     float top = 0.0f;
 #pragma unroll
     for (int i = 0; i < B; i += 2) top = max_abs(top, v[k * B + i], v[k * B + i + 1]);
-    const BlockScale<FMT> s(top, p.y_scale);
+    const BlockScale<FMT> s(top, ts);
     bytes |= s.byte << (8 * k);
 #pragma unroll
     for (int i = 0; i < B / 8; ++i) {
@@ -244,19 +242,41 @@ __device__ __forceinline__ void finish_codes(const GemmParams& p, float (&v)[32]
       code[k * (B / 8) + i] = s.codes(e);
     }
   }
+}
+
+// Stores such codes of row m, W columns from n0 on (32, or 64: whole 32-byte sectors), and
+// the scales.
+template <int FMT, int W>
+__device__ __forceinline__ void store_codes(const GemmParams& p, long long m, int n0,
+                                            const uint32_t (&code)[W / 8], uint32_t bytes) {
+  constexpr int B = kBlock<FMT>;
   const long long pitch = code_pitch(p.N);
   const int tiles = tiles_per_row(FMT, p.N);
-  *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.y) + m * pitch + n0 / 2) =
-      make_uint4(code[0], code[1], code[2], code[3]);
+  uint8_t* const to = static_cast<uint8_t*>(p.y) + m * pitch + n0 / 2;
+  // rows of codes are multiples of 16 bytes
+  if (W == 64 && pitch % 32 == 0 && n0 + 32 < p.N) {
+    Bytes32 b;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) b.w[i] = code[i % (W / 8)];
+    store32(to, b);
+  } else {
+#pragma unroll
+    for (int i = 0; i < W / 32; ++i)
+      if (n0 + 32 * i < p.N)
+        *reinterpret_cast<uint4*>(to + 16 * i) =
+            make_uint4(code[4 * i], code[4 * i + 1], code[4 * i + 2], code[4 * i + 3]);
+  }
   const int b0 = n0 / B;
-  uint8_t* word = p.ys + scale_word_offset(m, b0 >> 2, tiles);
-  if (FMT == CONV_FP4_MX)
-    word[b0 & 3] = (uint8_t)bytes;
+  uint8_t* word = p.ys + scale_word_offset(m, b0 >> 2, tiles) + (b0 & 3);
+  if constexpr (W / B == 4)
+    *reinterpret_cast<uint32_t*>(word) = bytes;
+  else if constexpr (W / B == 2)
+    *reinterpret_cast<uint16_t*>(word) = (uint16_t)bytes;
   else
-    *reinterpret_cast<uint16_t*>(word + (b0 & 3)) = (uint16_t)bytes;
+    *word = (uint8_t)bytes;
   // padding blocks of the row's last tile
-  if (n0 + 32 >= p.N)
-    for (int b = (n0 + 32) / B; (b >> 2) < tiles; ++b)
+  if (n0 + W >= p.N)
+    for (int b = (n0 + W) / B; (b >> 2) < tiles; ++b)
       p.ys[scale_word_offset(m, b >> 2, tiles) + (b & 3)] = 0;
 }
 
@@ -588,10 +608,16 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR, YIO>::THREADS, 1)
         }
       }
       if (mine && m0 < p.M) {
+        uint32_t code[CW / 8], bytes = 0;  // of 4-bit outputs
 #pragma unroll
         for (int s = 0; s < NP; ++s) {
           const int n0 = nb + PC * s;
-          if (n0 >= p.N) break;
+          if (n0 >= p.N) {
+            if (FLOAT) break;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) code[4 * s + i] = 0;
+            continue;
+          }
           if (PC * s % 32 == 0) {
             sbias[lane] = bias[PC * s / 32];
             __syncwarp();
@@ -617,10 +643,17 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR, YIO>::THREADS, 1)
                 fetch_res(m0, n0 + PC);
             });
           } else {
-            finish_codes<FMT>(p, v, m0, n0);
+            activate(v, p.act);
+            uint32_t c[4], b;
+            quantize32<FMT>(p.y_scale, v, p.N - n0, c, b);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) code[4 * s + i] = c[i];
+            bytes |= b << (s * (32 / kBlock<FMT>) * 8);
           }
           __syncwarp();
         }
+        if (!FLOAT && m0 + lane < p.M && nb < p.N)
+          store_codes<FMT, CW>(p, m0 + lane, nb, code, bytes);
       }
       if (m0 >= p.M || nb >= p.N) {  // nothing was read for this tile
         fetch_res(m_next, nb_next);
