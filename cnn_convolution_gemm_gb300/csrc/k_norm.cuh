@@ -3,10 +3,11 @@
 // Bound by HBM: x and z are read once and x' and h written once; a row stays in
 // registers between its up to four reductions (a mean and a sum of squared deviations
 // per layer norm: two passes over registers, so that a large mean does not cancel the
-// variance's digits).  Blocks that take several rows fetch x and z two rows ahead into
-// shared memory (bulk copies); otherwise a row's loads are issued together, past L1, so
-// that the weights stay there.  Measured: 32768 x 8192 bf16 339 us (6.3 TB/s), 12544 x 1001
-// fp32 with gates 43 us (4.7 TB/s; single elements), one row of 4096 3.5 us.
+// variance's digits).  Blocks that take many rows fetch x and z two rows ahead into shared
+// memory (bulk copies); otherwise a row's loads are issued together, past L1, so that the
+// weights stay there.  Measured: 32768 x 8192 bf16 325 us (6.6 TB/s), 12544 x 1001 fp32
+// with gates 40 us (5.0 TB/s; single elements), 26400 x 256 bf16 with gates 10, one row of
+// 4096 3.3 us.
 // One translation unit per pair of types includes this file.
 #pragma once
 
