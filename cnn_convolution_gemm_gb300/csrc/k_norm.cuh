@@ -318,10 +318,10 @@ constexpr int least_blocks(int T, int N, Layout lay, bool ahead, bool has_z) {
 // threads.
 // AHEAD (GROUPS, T > 32): x and z (if given) come through the ring; else R is 1.
 // HASZ false: z is not given (the first norm of a network or block).
-// vec_w: 16-byte accesses to weights.
+// vec_w: 16-byte accesses to weights.  held: how many of their rows shared memory has room for.
 template <typename TX, typename TZ, int T, int N, Layout LAY, bool AHEAD, int R, bool HASZ>
 __global__ void __launch_bounds__(T <= 32 ? 128 : T, least_blocks(T, N, LAY, AHEAD, HASZ))
-    norm_kernel(const NormArgs a, const TensorScale ts, const bool vec_w) {
+    norm_kernel(const NormArgs a, const TensorScale ts, const bool vec_w, const int held) {
   static_assert(AHEAD ? LAY == GROUPS : R == 1, "rows of a step");
   __shared__ float red[2][32 * R];
   __shared__ uint64_t full[RING];
@@ -358,8 +358,9 @@ __global__ void __launch_bounds__(T <= 32 ? 128 : T, least_blocks(T, N, LAY, AHE
       for (int i = 0; i < RING && first + i * step < a.rows; ++i) fetch(first + i * step, i);
     float4* to = reinterpret_cast<float4*>(reinterpret_cast<uint8_t*>(ring) +
                                            RING * R * (size_t)(zb + xb));
+    int room = held;
     const auto hold = [&](Weights<T, N, LAY>& w) {
-      if (!w.w) return;
+      if (!w.w || room-- <= 0) return;
 #pragma unroll
       for (int k = 0; k < N; k += 4)
         to[k / 4 * T + t] = load_weights<T, N, LAY>(w.w, k, t, C, vec_w);
@@ -492,7 +493,7 @@ __global__ void __launch_bounds__(T <= 32 ? 128 : T, least_blocks(T, N, LAY, AHE
 // Blocks of T threads that walk over the rows, as many as the SMs hold.
 template <typename K>
 cudaError_t launch_rows(K* kern, const NormArgs& a, int block, int rows_per_block, int smem,
-                        cudaStream_t st) {
+                        int held, cudaStream_t st) {
   const long long per_sm = gb_blocks_per_sm(reinterpret_cast<const void*>(kern), block, smem);
   const long long most = (long long)gb_num_sms() * std::max(1LL, per_sm);
   const auto vec = [](const float* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
@@ -507,7 +508,7 @@ cudaError_t launch_rows(K* kern, const NormArgs& a, int block, int rows_per_bloc
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   const bool vec_w = vec(a.w_post) && vec(a.b_post) && vec(a.w_pre) && vec(a.b_pre);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, tensor_scale(a.h_scale), vec_w);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, tensor_scale(a.h_scale), vec_w, held);
   if (e == cudaSuccess) gb_count_launch();
   return e;
 }
@@ -516,11 +517,11 @@ template <typename TX, typename TZ, int T, int N, Layout LAY>
 cudaError_t launch_direct(const NormArgs& a, cudaStream_t st) {
   auto* kern = a.z ? norm_kernel<TX, TZ, T, N, LAY, false, 1, true>
                    : norm_kernel<TX, TZ, T, N, LAY, false, 1, false>;
-  return launch_rows(kern, a, T <= 32 ? 128 : T, T <= 32 ? 128 / T : 1, 0, st);
+  return launch_rows(kern, a, T <= 32 ? 128 : T, T <= 32 ? 128 / T : 1, 0, 0, st);
 }
 
-// 16 consecutive columns a thread up to 4096 channels (as few dependent steps as a row
-// allows), 32 above
+// 16 consecutive columns a thread up to 8192 channels (152 rows of 4160 bf16 with gates
+// 5.4 us, 32 columns 6.7), 32 above
 template <typename TX, typename TZ, Layout LAY>
 cudaError_t launch_groups(const NormArgs& a, cudaStream_t st) {
   if (a.C <= 128) return launch_direct<TX, TZ, 8, 16, LAY>(a, st);
@@ -529,7 +530,7 @@ cudaError_t launch_groups(const NormArgs& a, cudaStream_t st) {
   if (a.C <= 1024) return launch_direct<TX, TZ, 64, 16, LAY>(a, st);
   if (a.C <= 2048) return launch_direct<TX, TZ, 128, 16, LAY>(a, st);
   if (a.C <= 4096) return launch_direct<TX, TZ, 256, 16, LAY>(a, st);
-  if (a.C <= 8192) return launch_direct<TX, TZ, 256, 32, LAY>(a, st);
+  if (a.C <= 8192) return launch_direct<TX, TZ, 512, 16, LAY>(a, st);
   if (a.C <= 16384) return launch_direct<TX, TZ, 512, 32, LAY>(a, st);
   return launch_direct<TX, TZ, 1024, 32, LAY>(a, st);
 }
@@ -549,23 +550,30 @@ cudaError_t launch_single(const NormArgs& a, cudaStream_t st) {
   return launch_direct<TX, TZ, 1024, 32, SINGLE>(a, st);
 }
 
-// 0: does not fit shared memory
+// Shared memory of the ring and the weights beside it; the latter as far as they fit.
+struct AheadSmem {
+  int bytes, held;
+  bool all;
+};
 template <typename TX, typename TZ, int T, int R>
-int ahead_smem(const NormArgs& a) {
+AheadSmem ahead_smem(const NormArgs& a) {
+  const int most = 224 * 1024, row = T * 64;
   const int n = (a.w_post != nullptr) + (a.b_post != nullptr) + (a.w_pre != nullptr) +
                 (a.b_pre != nullptr);
-  const int smem = RING * R * a.C * (int)(sizeof(TX) + (a.z ? sizeof(TZ) : 0)) + n * T * 64;
-  return smem <= 224 * 1024 ? smem : 0;
+  const int ring = RING * R * a.C * (int)(sizeof(TX) + (a.z ? sizeof(TZ) : 0));
+  if (ring > most) return {0, 0, false};
+  const int held = std::min(n, (most - ring) / row);
+  return {ring + held * row, held, held == n};
 }
 
 template <typename TX, typename TZ, int T, int R>
 cudaError_t launch_ahead(const NormArgs& a, cudaStream_t st) {
   auto* kern = a.z ? norm_kernel<TX, TZ, T, 16, GROUPS, true, R, true>
                    : norm_kernel<TX, TZ, T, 16, GROUPS, true, R, false>;
-  const int smem = ahead_smem<TX, TZ, T, R>(a);
-  const cudaError_t e = gb_set_smem_once(reinterpret_cast<const void*>(kern), smem);
+  const AheadSmem smem = ahead_smem<TX, TZ, T, R>(a);
+  const cudaError_t e = gb_set_smem_once(reinterpret_cast<const void*>(kern), smem.bytes);
   if (e != cudaSuccess) return e;
-  return launch_rows(kern, a, T, R, smem, st);
+  return launch_rows(kern, a, T, R, smem.bytes, smem.held, st);
 }
 
 template <typename TX, typename TZ>
@@ -575,16 +583,22 @@ cudaError_t launch(const NormArgs& a, cudaStream_t st) {
   const auto fit_z = [](const void* p, long long ld) { return !p || rows_vec<TZ>(p, ld, 32); };
   const bool vec = fit_x(a.x, a.ldx) && fit_x(a.x_out, a.ldxo) && fit_z(a.z, a.ldz) &&
                    fit_z(a.gate, a.ldg) && (codes || fit_z(a.h, a.ldh));
-  // many rows of whole 16-byte pieces: two at a time, through the ring
-  if (vec && a.C > 512 && a.C <= 8192 && a.C * sizeof(TX) % 16 == 0 &&
-      a.C * sizeof(TZ) % 16 == 0 && a.rows >= 2LL * gb_num_sms() * (8192 / a.C) * 4) {
+  // many rows of whole 16-byte pieces: through the ring, two at a time where they fit.  Above
+  // 4096 channels three to an SM are many (608 x 8192 bf16 9.3 us, else 10.5; 304 6.3 and
+  // 6.1), below so many that a block has several steps
+  const long long many =
+      gb_num_sms() * (a.C > 4096 ? 3LL : 8192 / std::max(a.C, 512) * 8);
+  if (vec && a.C > 512 && a.C * sizeof(TX) % 16 == 0 && a.C * sizeof(TZ) % 16 == 0 &&
+      a.rows >= many) {
     if (a.C <= 1024) return launch_ahead<TX, TZ, 64, 2>(a, st);
     if (a.C <= 2048) return launch_ahead<TX, TZ, 128, 2>(a, st);
     if (a.C <= 4096) {
-      if (ahead_smem<TX, TZ, 256, 2>(a)) return launch_ahead<TX, TZ, 256, 2>(a, st);
-    } else {
-      if (ahead_smem<TX, TZ, 512, 2>(a)) return launch_ahead<TX, TZ, 512, 2>(a, st);
-      if (ahead_smem<TX, TZ, 512, 1>(a)) return launch_ahead<TX, TZ, 512, 1>(a, st);
+      if (ahead_smem<TX, TZ, 256, 2>(a).all) return launch_ahead<TX, TZ, 256, 2>(a, st);
+    } else if (a.C <= 8192) {
+      if (ahead_smem<TX, TZ, 512, 2>(a).all) return launch_ahead<TX, TZ, 512, 2>(a, st);
+      if (ahead_smem<TX, TZ, 512, 1>(a).all) return launch_ahead<TX, TZ, 512, 1>(a, st);
+    } else if (a.C <= 16384 && ahead_smem<TX, TZ, 1024, 1>(a).bytes) {
+      return launch_ahead<TX, TZ, 1024, 1>(a, st);
     }
   }
   if (vec) return launch_groups<TX, TZ, GROUPS>(a, st);

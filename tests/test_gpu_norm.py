@@ -135,6 +135,8 @@ def test_quantized_output(h_fmt, rows, C):
     (N, RMS, 10001, 1024, {}), (RMS, N, 10001, 1024, {"gate": 1, "gate_rows": 196}),
     (RMS, RMS, 5003, 2048, {"h_fmt": R.MX}), (LN, LN, 5003, 2040, {"h_fmt": R.NV, "gate": 1}),
     (RMS, RMS, 1303, 7000, {"in_place": True}), (RMS, RMS, 2501, 4096, {"dt": "float32", "zdt": "bfloat16"}),
+    (RMS, RMS, 701, 12296, {}), (LN, LN, 611, 16384, {"gate": 1}), (LN, LN, 500, 9000, {"dt": "float32", "h_fmt": R.NV}),
+    (N, LN, 600, 16376, {"with_z": False, "h_fmt": R.MX}), (LN, LN, 520, 4104, {"gate": 2, "gate_rows": 3}),
     (RMS, RMS, 1303, 8192, {"weights": False}), (RMS, RMS, 3001, 4001, {}), (N, LN, 3001, 4096, {"with_z": False})])
 def test_many_rows(post, pre, rows, C, kw):
     """Rows that come ahead of their turn, two at a time, and an odd one last."""
