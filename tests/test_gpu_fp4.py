@@ -248,8 +248,8 @@ def test_product_of_few_rows(fmt, M, C, K):
     _product(fmt, M, C, K, "bfloat16", "float32", 0, True, M % 2 == 0)
 
 
-# the reduction shared out over 2, 3 and 4 CTAs, evenly and not; empty blocks; a last k-step
-# of one MMA
+# long reductions of 2 to 72 tiles, shared out over as many CTAs as find room, evenly and
+# not, and too short ones; empty blocks; a last k-step of one MMA
 @pytest.mark.parametrize("fmt", FMTS, ids=NAMES.get)
 @pytest.mark.parametrize("M,C,K,x,y,act,bias,residual", [
     (65, 2048, 64, "bfloat16", "bfloat16", 0, True, True),
@@ -258,7 +258,10 @@ def test_product_of_few_rows(fmt, M, C, K):
     (257, 2600, 1000, None, None, 0, False, False),
     (140, 9000, 400, None, "bfloat16", 4, False, True),
     (129, 3090, 2100, "bfloat16", "float32", 2, True, False),
-    (390, 4160, 1300, "bfloat16", "bfloat16", 1, False, True)])
+    (390, 4160, 1300, "bfloat16", "bfloat16", 1, False, True),
+    (640, 5000, 512, "bfloat16", "bfloat16", 0, True, True), (520, 5200, 620, None, "float32", 3, True, False),
+    (641, 5300, 641, "float32", None, 4, True, False), (700, 6210, 700, None, "bfloat16", 0, False, True),
+    (768, 6500, 1024, "bfloat16", "float32", 1, True, True), (1000, 7600, 1100, None, None, 3, True, False)])
 def test_product_of_split_reductions(fmt, M, C, K, x, y, act, bias, residual):
     _product(fmt, M, C, K, x, y, act, bias, residual)
 
