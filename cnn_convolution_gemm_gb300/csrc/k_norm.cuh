@@ -132,17 +132,18 @@ __device__ __forceinline__ void row_sum(float (&v)[R], float (*red)[32 * R], int
 #pragma unroll
     for (int k = 0; k < R; ++k) v[k] += __shfl_xor_sync(0xFFFFFFFFu, v[k], o);
   if constexpr (T > 32) {
-    constexpr int W = T / 32;
+    constexpr int W = T / 32, P = W <= 2 ? 2 : W <= 4 ? 4 : W <= 8 ? 8 : W <= 16 ? 16 : 32;
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int k = 0; k < R; ++k)
       if (lane == k) red[turn][32 * k + (threadIdx.x >> 5)] = v[k];
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < R; ++k) v[k] = red[turn][32 * k + (lane & (W - 1))];
+    for (int k = 0; k < R; ++k)
+      v[k] = W == P || (lane & (P - 1)) < W ? red[turn][32 * k + (lane & (P - 1))] : 0.0f;
     turn ^= 1;
 #pragma unroll
-    for (int o = W / 2; o; o >>= 1)
+    for (int o = P / 2; o; o >>= 1)
 #pragma unroll
       for (int k = 0; k < R; ++k) v[k] += __shfl_xor_sync(0xFFFFFFFFu, v[k], o);
   }
@@ -306,7 +307,7 @@ constexpr int least_blocks(int T, int N, Layout lay, bool ahead, bool has_z) {
   const int block = T <= 32 ? 128 : T;
   int threads = 1;
   if (ahead)
-    threads = has_z ? 512 : 1024;
+    threads = T % 192 == 0 ? 768 : has_z ? 512 : 1024;
   else if (N == 8)
     threads = has_z ? (T >= 512 ? 1024 : 768) : 1;
   else if (N == 16)
@@ -553,7 +554,7 @@ cudaError_t launch_single(const NormArgs& a, cudaStream_t st) {
 // Shared memory of the ring and the weights beside it; the latter as far as they fit.
 struct AheadSmem {
   int bytes, held;
-  bool all;
+  bool all, twice;  // all weights; and two blocks on an SM
 };
 template <typename TX, typename TZ, int T, int R>
 AheadSmem ahead_smem(const NormArgs& a) {
@@ -561,9 +562,10 @@ AheadSmem ahead_smem(const NormArgs& a) {
   const int n = (a.w_post != nullptr) + (a.b_post != nullptr) + (a.w_pre != nullptr) +
                 (a.b_pre != nullptr);
   const int ring = RING * R * a.C * (int)(sizeof(TX) + (a.z ? sizeof(TZ) : 0));
-  if (ring > most) return {0, 0, false};
+  if (ring > most) return {};
   const int held = std::min(n, (most - ring) / row);
-  return {ring + held * row, held, held == n};
+  const int bytes = ring + held * row;
+  return {bytes, held, held == n, held == n && 2 * bytes <= most};
 }
 
 template <typename TX, typename TZ, int T, int R>
@@ -585,15 +587,22 @@ cudaError_t launch(const NormArgs& a, cudaStream_t st) {
                    fit_z(a.gate, a.ldg) && (codes || fit_z(a.h, a.ldh));
   // many rows of whole 16-byte pieces: through the ring, two at a time where they fit.  Above
   // 4096 channels three to an SM are many (608 x 8192 bf16 9.3 us, else 10.5; 304 6.3 and
-  // 6.1), below so many that a block has several steps
+  // 6.1), above 2048 eight, below so many that a block has several steps
   const long long many =
-      gb_num_sms() * (a.C > 4096 ? 3LL : 8192 / std::max(a.C, 512) * 8);
+      gb_num_sms() * (a.C > 4096 ? 3LL : a.C > 2048 ? 8LL : 8192 / std::max(a.C, 512) * 8);
   if (vec && a.C > 512 && a.C * sizeof(TX) % 16 == 0 && a.C * sizeof(TZ) % 16 == 0 &&
       a.rows >= many) {
     if (a.C <= 1024) return launch_ahead<TX, TZ, 64, 2>(a, st);
     if (a.C <= 2048) return launch_ahead<TX, TZ, 128, 2>(a, st);
+    // one row of 192 threads, four blocks to an SM (12442 x 2560 bf16 46 us, 256 threads and
+    // two rows 64)
+    if (a.C <= 16 * 192) return launch_ahead<TX, TZ, 192, 1>(a, st);
     if (a.C <= 4096) {
       if (ahead_smem<TX, TZ, 256, 2>(a).all) return launch_ahead<TX, TZ, 256, 2>(a, st);
+    } else if (a.C <= 16 * 384 && ahead_smem<TX, TZ, 384, 1>(a).twice) {
+      // the same of 384 threads where two blocks fit (12442 x 4768 bf16 93 us, else 125; one
+      // block with four weights 200, else 187)
+      return launch_ahead<TX, TZ, 384, 1>(a, st);
     } else if (a.C <= 8192) {
       if (ahead_smem<TX, TZ, 512, 2>(a).all) return launch_ahead<TX, TZ, 512, 2>(a, st);
       if (ahead_smem<TX, TZ, 512, 1>(a).all) return launch_ahead<TX, TZ, 512, 1>(a, st);
