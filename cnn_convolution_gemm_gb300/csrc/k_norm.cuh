@@ -303,11 +303,11 @@ __device__ __forceinline__ void store_h(const NormArgs& a, const TensorScale& ts
 // Blocks an SM has to hold, which caps the registers: the compiler otherwise spends more on
 // loads it spreads between the sums (8192 x 4096 with gates 52 us, uncapped 74; 14552 x 2579
 // bf16 145, 223).  Without z more fit: 16384 x 8192 bf16 to MX 106 -> 91 us.
-constexpr int least_blocks(int T, int N, Layout lay, bool ahead, bool has_z) {
+constexpr int least_blocks(int T, int N, Layout lay, bool ahead, int R, bool has_z) {
   const int block = T <= 32 ? 128 : T;
   int threads = 1;
   if (ahead)
-    threads = T % 192 == 0 ? 768 : has_z ? 512 : 1024;
+    threads = T % 192 == 0 || (T == 256 && R == 1) ? 768 : has_z ? 512 : 1024;
   else if (N == 8)
     threads = has_z ? (T >= 512 ? 1024 : 768) : 1;
   else if (N == 16)
@@ -321,7 +321,7 @@ constexpr int least_blocks(int T, int N, Layout lay, bool ahead, bool has_z) {
 // HASZ false: z is not given (the first norm of a network or block).
 // vec_w: 16-byte accesses to weights.  held: how many of their rows shared memory has room for.
 template <typename TX, typename TZ, int T, int N, Layout LAY, bool AHEAD, int R, bool HASZ>
-__global__ void __launch_bounds__(T <= 32 ? 128 : T, least_blocks(T, N, LAY, AHEAD, HASZ))
+__global__ void __launch_bounds__(T <= 32 ? 128 : T, least_blocks(T, N, LAY, AHEAD, R, HASZ))
     norm_kernel(const NormArgs a, const TensorScale ts, const bool vec_w, const int held) {
   static_assert(AHEAD ? LAY == GROUPS : R == 1, "rows of a step");
   __shared__ float red[2][32 * R];
@@ -598,6 +598,9 @@ cudaError_t launch(const NormArgs& a, cudaStream_t st) {
     // two rows 64)
     if (a.C <= 16 * 192) return launch_ahead<TX, TZ, 192, 1>(a, st);
     if (a.C <= 4096) {
+      // likewise (24384 x 4096 bf16, layer norms 220 us, two rows 266; fp32, one block: 427
+      // and 343)
+      if (a.z && ahead_smem<TX, TZ, 256, 1>(a).twice) return launch_ahead<TX, TZ, 256, 1>(a, st);
       if (ahead_smem<TX, TZ, 256, 2>(a).all) return launch_ahead<TX, TZ, 256, 2>(a, st);
     } else if (a.C <= 16 * 384 && ahead_smem<TX, TZ, 384, 1>(a).twice) {
       // the same of 384 threads where two blocks fit (12442 x 4768 bf16 93 us, else 125; one
