@@ -364,15 +364,18 @@ def conv_fp4_size(fmt, rows, cols):
 
 def conv_fp4_quantize(fmt, dtype, rows, cols, x_ptr, ldx, tensor_scale, codes_ptr, scales_ptr,
                       stream=None):
-    _check(load_library().conv_fp4_quantize(fmt, dtype, rows, cols, x_ptr, ldx, tensor_scale,
-                                            codes_ptr, scales_ptr, stream), "conv_fp4_quantize")
+    st = (_lib or load_library()).conv_fp4_quantize(fmt, dtype, rows, cols, x_ptr, ldx,
+                                                    tensor_scale, codes_ptr, scales_ptr, stream)
+    if st:
+        _check(st, "conv_fp4_quantize")
 
 
 def conv_fp4_dequantize(fmt, dtype, rows, cols, codes_ptr, scales_ptr, tensor_scale, y_ptr, ldy,
                         stream=None):
-    _check(load_library().conv_fp4_dequantize(fmt, dtype, rows, cols, codes_ptr, scales_ptr,
-                                              tensor_scale, y_ptr, ldy, stream),
-           "conv_fp4_dequantize")
+    st = (_lib or load_library()).conv_fp4_dequantize(fmt, dtype, rows, cols, codes_ptr, scales_ptr,
+                                                      tensor_scale, y_ptr, ldy, stream)
+    if st:
+        _check(st, "conv_fp4_dequantize")
 
 
 def conv_fp4_pack_scales(fmt, rows, cols, src_ptr, scales_ptr, stream=None):
@@ -413,9 +416,11 @@ def conv_fp4_workspace_size(desc, M):
 
 def conv_fp4_fwd(desc, M, x_ptr, x_scales_ptr, w_codes_ptr, w_scales_ptr, bias_ptr, residual_ptr,
                  y_ptr, y_scales_ptr, ws_ptr=None, ws_bytes=0, stream=None):
-    _check(load_library().conv_fp4_fwd(desc, M, x_ptr, x_scales_ptr, w_codes_ptr, w_scales_ptr,
-                                       bias_ptr, residual_ptr, y_ptr, y_scales_ptr, ws_ptr,
-                                       ws_bytes, stream), "conv_fp4_fwd")
+    st = (_lib or load_library()).conv_fp4_fwd(desc, M, x_ptr, x_scales_ptr, w_codes_ptr,
+                                               w_scales_ptr, bias_ptr, residual_ptr, y_ptr,
+                                               y_scales_ptr, ws_ptr, ws_bytes, stream)
+    if st:
+        _check(st, "conv_fp4_fwd")
 
 
 def conv_norm_create(C, x_dtype=CONV_BF16, z_dtype=CONV_BF16):
@@ -453,8 +458,10 @@ def conv_norm_set_strides(desc, ldx=0, ldz=0, ldg=0, ldxo=0, ldh=0):
 
 def conv_norm_fwd(desc, rows, x_ptr, z_ptr, gate_ptr, x_out_ptr, h_ptr, h_scales_ptr=None,
                   stream=None):
-    _check(load_library().conv_norm_fwd(desc, rows, x_ptr, z_ptr, gate_ptr, x_out_ptr, h_ptr,
-                                        h_scales_ptr, stream), "conv_norm_fwd")
+    st = (_lib or load_library()).conv_norm_fwd(desc, rows, x_ptr, z_ptr, gate_ptr, x_out_ptr,
+                                                h_ptr, h_scales_ptr, stream)
+    if st:
+        _check(st, "conv_norm_fwd")
 
 
 def conv_fp4_block_create(norm_in, fc1, fc2, norm_out):
@@ -482,9 +489,11 @@ def conv_fp4_block_workspace_size(desc, M):
 
 def conv_fp4_block_fwd(desc, M, x_ptr, h_ptr, h_scales_ptr, gate_ptr, x_out_ptr, h_out_ptr,
                        h_out_scales_ptr, ws_ptr, ws_bytes, stream=None):
-    _check(load_library().conv_fp4_block_fwd(desc, M, x_ptr, h_ptr, h_scales_ptr, gate_ptr,
-                                             x_out_ptr, h_out_ptr, h_out_scales_ptr, ws_ptr,
-                                             ws_bytes, stream), "conv_fp4_block_fwd")
+    st = (_lib or load_library()).conv_fp4_block_fwd(desc, M, x_ptr, h_ptr, h_scales_ptr, gate_ptr,
+                                                     x_out_ptr, h_out_ptr, h_out_scales_ptr, ws_ptr,
+                                                     ws_bytes, stream)
+    if st:
+        _check(st, "conv_fp4_block_fwd")
 
 
 def conv_sync_status(stream=None):

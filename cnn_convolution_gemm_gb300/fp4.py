@@ -15,13 +15,9 @@ CONV_DTYPE = {torch.bfloat16: B.CONV_BF16, torch.float32: B.CONV_F32}
 BLOCK = {B.CONV_FP4_MX: 32, B.CONV_FP4_NV: 16}
 
 
-# a call's host time is a few microseconds in all, so its path here is kept short
-_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
-def stream_handle(stream, device: torch.device) -> int:
-    """stream, or the handle of the device's current stream."""
-    return _current_stream(device.index) if stream is None else stream
+# Handle of a device's current stream, without building a torch.cuda.Stream: a call's host
+# time is a few microseconds in all, so its path here is kept short.
+current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def allocating_on(stream):
@@ -54,14 +50,14 @@ class Fp4Tensor:
     scale.  The tensors stay the ones it was made with (their addresses are kept)."""
 
     __slots__ = ("rows", "cols", "fmt", "tensor_scale", "codes", "scales", "shape", "codes_ptr",
-                 "scales_ptr", "device")
+                 "scales_ptr", "device", "index")
 
     def __init__(self, rows, cols, fmt, tensor_scale, codes, scales):
         self.rows, self.cols, self.fmt, self.tensor_scale = rows, cols, fmt, tensor_scale
         self.codes, self.scales = codes, scales
         self.shape = (rows, cols, fmt)
         self.codes_ptr, self.scales_ptr = codes.data_ptr(), scales.data_ptr()
-        self.device = codes.device
+        self.device, self.index = codes.device, codes.get_device()
 
 
 def empty(rows, cols, fmt, device, tensor_scale=1.0, stream=None) -> Fp4Tensor:
@@ -77,15 +73,20 @@ def quantize(x: torch.Tensor, fmt, tensor_scale=1.0, out: Fp4Tensor | None = Non
              stream=None) -> Fp4Tensor:
     """x [..., cols] (bf16 or fp32) in 4 bits."""
     cols = x.shape[-1]
-    rows, ld = rows_of(x, cols, "x")
+    if x.is_contiguous() and cols:
+        rows, ld = x.numel() // cols, cols
+    else:
+        rows, ld = rows_of(x, cols, "x")
     if out is None:
         out = empty(rows, cols, fmt, x.device, tensor_scale, stream)
     elif out.shape != (rows, cols, fmt):
         raise ValueError("out: a 4-bit matrix of another shape or format")
-    if not x.is_cuda or x.get_device() != out.device.index:
+    index = out.index
+    if x.get_device() != index or index < 0:
         raise ValueError("x: must be on the GPU, and on out's")
     B.conv_fp4_quantize(fmt, CONV_DTYPE[x.dtype], rows, cols, x.data_ptr(), ld, tensor_scale,
-                        out.codes_ptr, out.scales_ptr, stream_handle(stream, out.device))
+                        out.codes_ptr, out.scales_ptr,
+                        current_stream(index) if stream is None else stream)
     out.tensor_scale = tensor_scale
     return out
 
@@ -99,10 +100,12 @@ def dequantize(t: Fp4Tensor, dtype=torch.bfloat16, out: torch.Tensor | None = No
     rows, ld = rows_of(out, t.cols, "out")
     if rows != t.rows:
         raise ValueError(f"out: {rows} rows, expected {t.rows}")
-    if out.get_device() != t.device.index:
+    index = t.index
+    if out.get_device() != index:
         raise ValueError("out: on another device than t")
     B.conv_fp4_dequantize(t.fmt, CONV_DTYPE[out.dtype], rows, t.cols, t.codes_ptr, t.scales_ptr,
-                          t.tensor_scale, out.data_ptr(), ld, stream_handle(stream, t.device))
+                          t.tensor_scale, out.data_ptr(), ld,
+                          current_stream(index) if stream is None else stream)
     return out
 
 
@@ -157,7 +160,7 @@ class Fp4Linear:
         with allocating_on(stream):
             tiled = torch.empty(sb, dtype=torch.uint8, device=codes.device)
         B.conv_fp4_pack_scales(self.fmt, self.K, self.C, scales.data_ptr(), tiled.data_ptr(),
-                               stream_handle(stream, codes.device))
+                               current_stream(codes.get_device()) if stream is None else stream)
         self._set(Fp4Tensor(self.K, self.C, self.fmt, w_scale, codes, tiled))
 
     def _set(self, w: Fp4Tensor):
@@ -182,8 +185,8 @@ class Fp4Linear:
         w = self.w
         if w is None:
             raise RuntimeError("prepack() or load() the weights first")
-        C, K, y_dtype, device = self.C, self.K, self.y_dtype, w.device
-        handle = stream_handle(stream, device)
+        C, K, y_dtype, index = self.C, self.K, self.y_dtype, w.index
+        handle = current_stream(index) if stream is None else stream
         bp = rp = xsp = ysp = None
         if self.x_dtype is None:
             if (x.cols, x.fmt, x.tensor_scale) != (C, self.fmt, self.x_scale):
@@ -193,7 +196,7 @@ class Fp4Linear:
         else:
             if x.dtype is not self.x_dtype:
                 raise ValueError(f"x: {x.dtype}, expected {self.x_dtype}")
-            if x.get_device() != device.index:
+            if x.get_device() != index:
                 raise ValueError("x: on another device than the weights")
             rows, ldx = rows_of(x, C, "x")
             xp = x.data_ptr()
@@ -204,7 +207,7 @@ class Fp4Linear:
         ldr = ldy = K
         if y_dtype is None:
             if out is None:
-                out = empty(rows, K, self.fmt, device, self.y_scale, stream)
+                out = empty(rows, K, self.fmt, w.device, self.y_scale, stream)
             elif out.shape != (rows, K, self.fmt):
                 raise ValueError("out: a 4-bit matrix of another shape or format")
             out.tensor_scale = self.y_scale
@@ -213,7 +216,7 @@ class Fp4Linear:
             if out is None:
                 lead = (rows,) if self.x_dtype is None else x.shape[:-1]
                 with allocating_on(stream):
-                    out = torch.empty(*lead, K, dtype=y_dtype, device=device)
+                    out = torch.empty(*lead, K, dtype=y_dtype, device=w.device)
             got, ldy = rows_of(out, K, "out")
             if got != rows or out.dtype is not y_dtype:
                 raise ValueError("out: another number of rows or type")
@@ -227,7 +230,9 @@ class Fp4Linear:
         if strides != self._strides:
             B.conv_fp4_set_strides(self.desc, *strides)
             self._strides = strides
-        wsp, ws_bytes = self._workspace(rows, stream, handle)
+        wsp, ws_bytes = None, 0
+        if self._sizes.get(rows) != 0:
+            wsp, ws_bytes = self._workspace(rows, stream, handle)
         B.conv_fp4_fwd(self.desc, rows, xp, xsp, w.codes_ptr, w.scales_ptr, bp, rp, yp, ysp, wsp,
                        ws_bytes, handle)
         return out

@@ -5,7 +5,7 @@ import torch
 
 from . import binding as B
 from . import fp4
-from .fp4 import CONV_DTYPE, allocating_on, rows_of, stream_handle
+from .fp4 import CONV_DTYPE, allocating_on, current_stream, rows_of
 
 
 class ResidualNorm:
@@ -57,8 +57,6 @@ class ResidualNorm:
         C, dtype, z_dtype, shape = self.C, self.dtype, self.z_dtype, x.shape
         if x.dtype is not dtype:
             raise ValueError(f"x: {x.dtype}, expected {dtype}")
-        if not x.is_cuda:
-            raise ValueError("x: must be on the GPU")
         gp = xop = hp = hsp = None
         ldg = ldxo = ldh = C
         if gate is not None:
@@ -108,10 +106,13 @@ class ResidualNorm:
                 zp = z.data_ptr()
             else:
                 zp, ldz = self._tensor(z, self.z_dtype, rows, "z")
+        index = x.get_device()
+        if index < 0:
+            raise ValueError("x: must be on the GPU")
         x_out, h_out, gp, xop, hp, hsp = self._bind(x, rows, ldx, ldz, gate, x_out, h_out, want_x,
                                                     stream)
         B.conv_norm_fwd(self.desc, rows, x.data_ptr(), zp, gp, xop, hp, hsp,
-                        stream_handle(stream, x.device))
+                        current_stream(index) if stream is None else stream)
         return x_out, h_out
 
     __call__ = forward

@@ -78,16 +78,14 @@ class Fp4ResidualBlock:
         self._held = (w1, w2)
 
     def _workspace(self, rows, stream, handle):
-        """(address, bytes) of the stream's workspace for so many rows."""
-        need = self._sizes.get(rows)
-        if need is None:
-            need = self._sizes[rows] = B.conv_fp4_block_workspace_size(self.desc, rows)
+        """(bytes for so many rows, the stream's workspace and its address)"""
+        need = self._sizes[rows] = B.conv_fp4_block_workspace_size(self.desc, rows)
         got = self._ws.get(handle)
         if got is None or got[0].numel() < need:
             with fp4.allocating_on(stream):
                 ws = torch.empty(max(need, 256), dtype=torch.uint8, device=self.fc1.w.device)
             got = self._ws[handle] = (ws, ws.data_ptr())
-        return got[1], need
+        return need, got
 
     def forward(self, x, gate=None, h=None, x_out=None, h_out=None, stream=None):
         """x [..., C] -> (x', h').  h: norm_pre(x) in 4 bits when the block before handed
@@ -101,17 +99,19 @@ class Fp4ResidualBlock:
             if (h.shape, h.tensor_scale) != ((rows, C, self.fmt), self.h_scale):
                 raise ValueError("h: a 4-bit matrix of another shape, format or tensor scale")
             hp, hsp = h.codes_ptr, h.scales_ptr
-        handle = fp4.stream_handle(stream, w1.device)
-        if x.get_device() != w1.device.index:
+        handle = fp4.current_stream(w1.index) if stream is None else stream
+        if x.get_device() != w1.index:
             raise ValueError("x: on another device than the weights")
         x_out, h_out, gp, xop, hop, hosp = self.norm_out._bind(x, rows, ldx, C, gate, x_out, h_out,
                                                                True, stream)
         if norm_in._strides[0] != ldx:
             norm_in._strides = (ldx, C, C, C, C)
             B.conv_norm_set_strides(norm_in.desc, *norm_in._strides)
-        wsp, ws_bytes = self._workspace(rows, stream, handle)
-        B.conv_fp4_block_fwd(self.desc, rows, x.data_ptr(), hp, hsp, gp, xop, hop, hosp, wsp,
-                             ws_bytes, handle)
+        need, got = self._sizes.get(rows), self._ws.get(handle)
+        if need is None or got is None or got[0].numel() < need:
+            need, got = self._workspace(rows, stream, handle)
+        B.conv_fp4_block_fwd(self.desc, rows, x.data_ptr(), hp, hsp, gp, xop, hop, hosp,
+                             got[1], need, handle)
         return x_out, h_out
 
     __call__ = forward
