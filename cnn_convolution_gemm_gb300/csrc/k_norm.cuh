@@ -568,10 +568,12 @@ AheadSmem ahead_smem(const NormArgs& a) {
   return {bytes, held, held == n, held == n && 2 * bytes <= most};
 }
 
-template <typename TX, typename TZ, int T, int R>
+// Z_ONLY: called with z alone.
+template <typename TX, typename TZ, int T, int R, bool Z_ONLY = false>
 cudaError_t launch_ahead(const NormArgs& a, cudaStream_t st) {
-  auto* kern = a.z ? norm_kernel<TX, TZ, T, 16, GROUPS, true, R, true>
-                   : norm_kernel<TX, TZ, T, 16, GROUPS, true, R, false>;
+  auto* kern = norm_kernel<TX, TZ, T, 16, GROUPS, true, R, true>;
+  if constexpr (!Z_ONLY)
+    if (!a.z) kern = norm_kernel<TX, TZ, T, 16, GROUPS, true, R, false>;
   const AheadSmem smem = ahead_smem<TX, TZ, T, R>(a);
   const cudaError_t e = gb_set_smem_once(reinterpret_cast<const void*>(kern), smem.bytes);
   if (e != cudaSuccess) return e;
@@ -600,7 +602,8 @@ cudaError_t launch(const NormArgs& a, cudaStream_t st) {
     if (a.C <= 4096) {
       // likewise (24384 x 4096 bf16, layer norms 220 us, two rows 266; fp32, one block: 427
       // and 343)
-      if (a.z && ahead_smem<TX, TZ, 256, 1>(a).twice) return launch_ahead<TX, TZ, 256, 1>(a, st);
+      if (a.z && ahead_smem<TX, TZ, 256, 1>(a).twice)
+        return launch_ahead<TX, TZ, 256, 1, true>(a, st);
       if (ahead_smem<TX, TZ, 256, 2>(a).all) return launch_ahead<TX, TZ, 256, 2>(a, st);
     } else if (a.C <= 16 * 384 && ahead_smem<TX, TZ, 384, 1>(a).twice) {
       // the same of 384 threads where two blocks fit (12442 x 4768 bf16 93 us, else 125; one

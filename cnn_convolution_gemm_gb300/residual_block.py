@@ -1,5 +1,5 @@
-"""A residual block in 4 bits (conv_fp4_block_* of gbconv.h): two fully connected layers (1x1 convolutions over NHWC
-pixels) between the norms around them.
+"""A residual block in 4 bits (conv_fp4_block_* of gbconv.h): two fully connected layers
+(1x1 convolutions over NHWC pixels) between the norms around them.
 
   h  = norm_pre(x), 4 bits             one pass over x
   t  = gelu(h W1^T + b1), 4 bits       quantised in the product's epilogue
