@@ -60,7 +60,8 @@ struct GemmParams {
   int M, N, ksteps, kmmas_last;  // 64-element MMAs of the last k-step
   int m_tiles, n_tiles;          // PAIR: m_tiles counts 256-row units
   int split;                     // SPLIT: CTAs of a cluster
-  int act, vec_y, vec_r;         // rows of y for the TMA, of the residual for 16-byte loads
+  int act, vec_y, vec_r;         // rows of y for the TMA (4-bit y: for 32-byte stores), of the
+                                 // residual for 16-byte loads
   float alpha;
   TensorScale y_scale;
   const float* bias;
@@ -253,8 +254,8 @@ __device__ __forceinline__ void store_codes(const GemmParams& p, long long m, in
   const long long pitch = code_pitch(p.N);
   const int tiles = tiles_per_row(FMT, p.N);
   uint8_t* const to = static_cast<uint8_t*>(p.y) + m * pitch + n0 / 2;
-  // rows of codes are multiples of 16 bytes
-  if (W == 64 && pitch % 32 == 0 && n0 + 32 < p.N) {
+  // codes start and their rows lie on multiples of 16 bytes, not always of 32
+  if (W == 64 && p.vec_y && n0 + 32 < p.N) {
     Bytes32 b;
 #pragma unroll
     for (int i = 0; i < 8; ++i) b.w[i] = code[i % (W / 8)];
@@ -705,7 +706,9 @@ cudaError_t launch_tile(const Fp4Gemm& g, int split, cudaStream_t st) {
   p.ys = g.ys;
   p.ldr = g.ldr;
   p.ldy = g.ldy;
-  if (YIO == CONV_FP4_IO_BF16) {
+  if (YIO == CONV_FP4_IO_CODES) {
+    p.vec_y = rows_vec<uint8_t>(g.y, code_pitch(g.K), 32);
+  } else if (YIO == CONV_FP4_IO_BF16) {
     p.vec_y = rows_vec<__nv_bfloat16>(g.y, g.ldy, 16);
     p.vec_r = rows_vec<__nv_bfloat16>(g.res, g.ldr, 16);
   } else {

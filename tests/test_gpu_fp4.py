@@ -432,3 +432,32 @@ def test_quantize_at_every_alignment(dtype, cols):
                 assert torch.equal(at, values)
                 at.fill_(7.5)
                 assert bool((buf == 7.5).all())
+
+
+def _at_16_of_32(torch, n):
+    """n bytes at an address that is a multiple of 16, not of 32, and the buffer around them."""
+    buf = torch.full((n + 64,), 0xA5, dtype=torch.uint8, device="cuda")
+    start = 16 + -buf.data_ptr() % 32
+    return buf, buf[start:start + n], start
+
+
+@pytest.mark.parametrize("fmt", FMTS, ids=NAMES.get)
+@pytest.mark.parametrize("M,C,K", [(3000, 272, 2096), (2600, 256, 2112), (130, 96, 192), (5, 300, 64)])
+def test_product_into_codes_at_16_bytes(fmt, M, C, K):
+    """4-bit outputs need 16-byte alignment only: rows of whole 32-byte pieces that start
+    between two of them, in the tiles of both sizes and in the kernel for few rows."""
+    torch, fp4 = _fp4()
+    rng = np.random.default_rng(M)
+    layer = fp4.Fp4Linear(C, K, fmt, y_dtype=None, act=R.B.CONV_ACT_RELU)
+    layer.prepack(_to(torch, rng.standard_normal((K, C)), torch.bfloat16))
+    x = _to(torch, _activations(rng, M, C), torch.bfloat16)
+    want = layer(x)
+    cb, sb = R.B.conv_fp4_size(fmt, M, K)
+    cbuf, codes, c0 = _at_16_of_32(torch, cb)
+    sbuf, scales, s0 = _at_16_of_32(torch, sb)
+    got = layer(x, out=fp4.Fp4Tensor(M, K, fmt, 1.0, codes, scales))
+    _sync(torch)
+    assert got.codes_ptr % 32 == 16 and torch.equal(codes, want.codes)
+    np.testing.assert_array_equal(R.unpack(got)[1], R.unpack(want)[1])
+    for buf, at, n in ((cbuf, c0, cb), (sbuf, s0, sb)):
+        assert (buf[:at] == 0xA5).all() and (buf[at + n:] == 0xA5).all()

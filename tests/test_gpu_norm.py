@@ -283,3 +283,35 @@ def test_residual_block_is_its_parts():
     want = [t.clone() for t in parts(x)]
     assert same(blk(x, gate=gate), want)
     B.conv_sync_status(torch.cuda.current_stream().cuda_stream)
+
+
+@pytest.mark.parametrize("fmt", [B.CONV_FP4_MX, B.CONV_FP4_NV])
+@pytest.mark.parametrize("rows", [2, 2600])
+def test_residual_block_workspace_at_16_bytes(fmt, rows):
+    """A workspace that lies on 16 bytes and not on 32 holds the same bits of h, t and z.  The
+    norm behind takes z's rows by single columns then, and adds their squares in another order
+    (2^-20 of |x| + |u| < 32): x' and h' may round to the next bf16 value."""
+    torch = need_gpu()
+    from cnn_convolution_gemm_gb300.residual_block import Fp4ResidualBlock
+    torch.manual_seed(5)
+    C, hidden = 256, 2112
+    blk = Fp4ResidualBlock(C, hidden, fmt)
+    blk.prepack(torch.randn(hidden, C, device="cuda"), torch.randn(C, hidden, device="cuda"))
+    x = torch.randn(rows, C, device="cuda").bfloat16()
+    blk(x)  # gives the descriptor its weights
+    need = B.conv_fp4_block_workspace_size(blk.desc, rows)
+    stream = torch.cuda.current_stream().cuda_stream
+    runs = []
+    for off in (0, 16):
+        buf = torch.zeros(need + 64, dtype=torch.uint8, device="cuda")
+        at = off + -buf.data_ptr() % 32
+        out = [torch.empty_like(x) for _ in range(2)]
+        B.conv_fp4_block_fwd(blk.desc, rows, x.data_ptr(), None, None, None, out[0].data_ptr(),
+                             out[1].data_ptr(), None, buf.data_ptr() + at, need, stream)
+        B.conv_sync_status(stream)
+        assert not buf[:at].any() and not buf[at + need:].any()
+        runs.append((buf[at:at + need], out))
+    assert torch.equal(runs[0][0], runs[1][0])
+    for a, b in zip(runs[0][1], runs[1][1]):
+        a, b = a.float(), b.float()
+        assert ((a - b).abs() <= 2.0 ** -7 * torch.maximum(a.abs(), b.abs()) + 2.0 ** -15).all()
