@@ -28,6 +28,32 @@ def allocating_on(stream):
     return torch.cuda.stream(torch.cuda.ExternalStream(stream))
 
 
+class Workspaces:
+    """Scratch memory of a layer's calls: a buffer per device and stream, whose calls follow
+    each other.  A call that is captured into a CUDA graph gets memory of its own, from the
+    graph's pool: the graph keeps the address, so it can be neither a buffer that a larger call
+    replaces nor one that calls outside the graph write into."""
+
+    __slots__ = ("_held",)
+
+    def __init__(self):
+        self._held = {}
+
+    def get(self, need, device, index, stream, handle) -> torch.Tensor:
+        if stream is None:
+            return self._get(need, device, (index, handle))
+        with allocating_on(stream):
+            return self._get(need, device, (index, handle))
+
+    def _get(self, need, device, key):
+        if torch.cuda.is_current_stream_capturing():
+            return torch.empty(need, dtype=torch.uint8, device=device)
+        ws = self._held.get(key)
+        if ws is None or ws.numel() < need:
+            ws = self._held[key] = torch.empty(need, dtype=torch.uint8, device=device)
+        return ws
+
+
 def rows_of(t: torch.Tensor, cols: int, what: str):
     """(rows, elements between rows) of a tensor [..., cols] whose rows are evenly spaced."""
     shape = t.shape
@@ -130,7 +156,7 @@ class Fp4Linear:
         self.w = None
         self._strides = (C, K, K)
         self._sizes = {}  # rows -> workspace bytes
-        self._ws = {}     # stream handle -> workspace (calls on one stream follow each other)
+        self._ws = Workspaces()
 
     def __del__(self):
         d = getattr(self, "desc", None)
@@ -166,20 +192,6 @@ class Fp4Linear:
     def _set(self, w: Fp4Tensor):
         B.conv_fp4_set_tensor_scales(self.desc, self.x_scale, w.tensor_scale, self.y_scale)
         self.w = w
-
-    def _workspace(self, rows, stream, handle):
-        """(address, bytes) of the stream's workspace for so many rows."""
-        need = self._sizes.get(rows)
-        if need is None:
-            need = self._sizes[rows] = B.conv_fp4_workspace_size(self.desc, rows)
-        if not need:
-            return None, 0
-        ws = self._ws.get(handle)
-        if ws is None or ws.numel() < need:
-            with allocating_on(stream):
-                ws = torch.empty(need, dtype=torch.uint8, device=self.w.device)
-            self._ws[handle] = ws
-        return ws.data_ptr(), ws.numel()
 
     def forward(self, x, bias=None, residual=None, out=None, stream=None):
         w = self.w
@@ -230,11 +242,13 @@ class Fp4Linear:
         if strides != self._strides:
             B.conv_fp4_set_strides(self.desc, *strides)
             self._strides = strides
-        wsp, ws_bytes = None, 0
-        if self._sizes.get(rows) != 0:
-            wsp, ws_bytes = self._workspace(rows, stream, handle)
-        B.conv_fp4_fwd(self.desc, rows, xp, xsp, w.codes_ptr, w.scales_ptr, bp, rp, yp, ysp, wsp,
-                       ws_bytes, handle)
+        need = self._sizes.get(rows)
+        if need is None:
+            need = self._sizes[rows] = B.conv_fp4_workspace_size(self.desc, rows)
+        # held until the launches are enqueued
+        ws = self._ws.get(need, w.device, index, stream, handle) if need else None
+        B.conv_fp4_fwd(self.desc, rows, xp, xsp, w.codes_ptr, w.scales_ptr, bp, rp, yp, ysp,
+                       ws.data_ptr() if need else None, need, handle)
         return out
 
     __call__ = forward

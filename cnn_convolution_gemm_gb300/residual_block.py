@@ -49,7 +49,7 @@ class Fp4ResidualBlock:
         self.desc = B.conv_fp4_block_create(self.norm_in.desc, self.fc1.desc, self.fc2.desc,
                                             self.norm_out.desc)
         self._held = (None, None)  # the weights that desc has the addresses of
-        self._sizes, self._ws = {}, {}  # rows -> bytes; stream handle -> (tensor, address)
+        self._sizes, self._ws = {}, fp4.Workspaces()  # sizes: rows -> workspace bytes
 
     def __del__(self):
         d = getattr(self, "desc", None)
@@ -77,16 +77,6 @@ class Fp4ResidualBlock:
                                      w2.scales_ptr, b2)
         self._held = (w1, w2)
 
-    def _workspace(self, rows, stream, handle):
-        """(bytes for so many rows, the stream's workspace and its address)"""
-        need = self._sizes[rows] = B.conv_fp4_block_workspace_size(self.desc, rows)
-        got = self._ws.get(handle)
-        if got is None or got[0].numel() < need:
-            with fp4.allocating_on(stream):
-                ws = torch.empty(max(need, 256), dtype=torch.uint8, device=self.fc1.w.device)
-            got = self._ws[handle] = (ws, ws.data_ptr())
-        return need, got
-
     def forward(self, x, gate=None, h=None, x_out=None, h_out=None, stream=None):
         """x [..., C] -> (x', h').  h: norm_pre(x) in 4 bits when the block before handed
         it on, else None."""
@@ -107,11 +97,13 @@ class Fp4ResidualBlock:
         if norm_in._strides[0] != ldx:
             norm_in._strides = (ldx, C, C, C, C)
             B.conv_norm_set_strides(norm_in.desc, *norm_in._strides)
-        need, got = self._sizes.get(rows), self._ws.get(handle)
-        if need is None or got is None or got[0].numel() < need:
-            need, got = self._workspace(rows, stream, handle)
+        need = self._sizes.get(rows)
+        if need is None:
+            need = self._sizes[rows] = B.conv_fp4_block_workspace_size(self.desc, rows)
+        # held until the launches are enqueued
+        ws = self._ws.get(need, w1.device, w1.index, stream, handle) if need else None
         B.conv_fp4_block_fwd(self.desc, rows, x.data_ptr(), hp, hsp, gp, xop, hop, hosp,
-                             got[1], need, handle)
+                             ws.data_ptr() if need else None, need, handle)
         return x_out, h_out
 
     __call__ = forward

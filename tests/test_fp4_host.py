@@ -241,3 +241,73 @@ def test_torch_layers_check_their_tensors(B):
             torch.zeros(1, 64, dtype=torch.bfloat16))    # a tensor in host memory
     with pytest.raises(ValueError):
         fp4.quantize(torch.zeros(1, 64), B.CONV_FP4_MX)
+
+
+# ---- the torch layers up to their launch, without a GPU -------------------------
+
+
+@pytest.fixture
+def host_layers(B, monkeypatch):
+    """The torch layers over tensors in host memory that say they are on GPU 0, with launches
+    that are only written down: (torch, fp4, up, calls, allocated).  Every buffer that the
+    layers allocate is kept, so that addresses are not used twice."""
+    torch = pytest.importorskip("torch")
+    from cnn_convolution_gemm_gb300 import fp4, norm
+
+    class OnGpu(torch.Tensor):
+        def get_device(self):
+            return 0
+
+    def up(t):
+        return t.as_subclass(OnGpu)
+    calls, allocated = [], []
+    empty = torch.empty
+
+    def kept_empty(*args, **kw):
+        t = up(empty(*args, **kw))
+        allocated.append(t)
+        return t
+    monkeypatch.setattr(torch, "empty", kept_empty)
+    for module in (fp4, norm):
+        monkeypatch.setattr(module, "current_stream", lambda index: 7)
+    for name in ("conv_fp4_fwd", "conv_fp4_block_fwd", "conv_norm_fwd", "conv_fp4_quantize",
+                 "conv_fp4_dequantize", "conv_fp4_pack_scales"):
+        monkeypatch.setattr(B, name, lambda *a, name=name: calls.append((name, a)))
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    return torch, fp4, up, calls, allocated
+
+
+def _host_block(torch, up, **kw):
+    from cnn_convolution_gemm_gb300.residual_block import Fp4ResidualBlock
+    blk = Fp4ResidualBlock(64, 96, **kw)
+    blk.prepack(up(torch.zeros(96, 64)), up(torch.zeros(64, 96)))
+    return blk
+
+
+@pytest.mark.parametrize("what", ["layer", "block"])
+def test_captured_calls_have_workspaces_of_their_own(host_layers, monkeypatch, what):
+    """A captured call's workspace is no other call's, before or after it; calls outside captures
+    keep one, replaced by a larger one when it is too small."""
+    torch, fp4, up, calls, allocated = host_layers
+    if what == "layer":
+        layer = fp4.Fp4Linear(64, 32)
+        layer.prepack(up(torch.zeros(32, 64)))
+    else:
+        layer = _host_block(torch, up)
+
+    def workspace(rows, capturing):
+        monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing)
+        layer(up(torch.zeros(rows, 64, dtype=torch.bfloat16)))
+        name, args = calls[-1]
+        at, size = (args[10], args[11]) if what == "layer" else (args[9], args[10])
+        found = [t for t in allocated if t.data_ptr() <= at < t.data_ptr() + t.numel()]
+        assert len(found) == 1 and at + size <= found[0].data_ptr() + found[0].numel()
+        return id(found[0])
+    small = workspace(20, False)
+    captured = [workspace(20, True), workspace(20, True), workspace(300, True)]
+    assert workspace(20, False) == small
+    large = workspace(400, False)
+    after = [workspace(20, True), workspace(400, False), workspace(300, False)]
+    assert after[1] == after[2] == large != small
+    captured.append(after[0])
+    assert len({small, large, *captured}) == 6

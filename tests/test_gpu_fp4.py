@@ -461,3 +461,47 @@ def test_product_into_codes_at_16_bytes(fmt, M, C, K):
     np.testing.assert_array_equal(R.unpack(got)[1], R.unpack(want)[1])
     for buf, at, n in ((cbuf, c0, cb), (sbuf, s0, sb)):
         assert (buf[:at] == 0xA5).all() and (buf[at + n:] == 0xA5).all()
+
+
+@pytest.mark.parametrize("what", ["layer", "block"])
+def test_graphs_keep_their_workspaces(what):
+    """A graph of few rows replays to the same bits after the layer served more rows on the same
+    stream and other tensors took what that freed; and leaves those tensors alone."""
+    torch, fp4 = _fp4()
+    from cnn_convolution_gemm_gb300.residual_block import Fp4ResidualBlock
+    rng = np.random.default_rng(11)
+    C, K = 256, 320
+    if what == "layer":
+        layer = fp4.Fp4Linear(C, K, R.MX)
+        layer.prepack(_to(torch, rng.standard_normal((K, C)), torch.bfloat16))
+        call = layer
+    else:
+        layer = Fp4ResidualBlock(C, K, R.MX)
+        layer.prepack(_to(torch, rng.standard_normal((K, C)), torch.bfloat16),
+                      _to(torch, rng.standard_normal((C, K)), torch.bfloat16))
+        call = lambda x: layer(x)[1]  # noqa: E731
+    x = _to(torch, _activations(rng, 40, C), torch.bfloat16)
+    many = _to(torch, _activations(rng, 3000, C), torch.bfloat16)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        want = call(x).clone()
+        side.synchronize()
+        graphs, outs = [], []
+        for _ in range(2):
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=side):
+                outs.append(call(x))
+            graphs.append(g)
+        call(many)
+        taken = [torch.full((n,), 0x5A, dtype=torch.uint8, device="cuda")
+                 for n in (512, 4096, 8192, 16384, 1 << 20) for _ in range(64)]
+        for _ in range(3):
+            for g, out in zip(graphs, outs):
+                out.zero_()
+                g.replay()
+                call(many)
+        side.synchronize()
+    for out in outs:
+        assert torch.equal(out, want)
+    assert all(bool((t == 0x5A).all()) for t in taken)
