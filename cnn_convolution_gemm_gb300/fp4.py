@@ -18,6 +18,17 @@ BLOCK = {B.CONV_FP4_MX: 32, B.CONV_FP4_NV: 16}
 # Handle of a device's current stream, without building a torch.cuda.Stream: a call's host
 # time is a few microseconds in all, so its path here is kept short.
 current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+current_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
+def call_stream(index, stream):
+    """Stream handle (stream, or the current one for None) of a call on tensors of device
+    index, which has to be the current GPU: the library launches there."""
+    if index < 0:
+        raise ValueError("tensors must be on the GPU")
+    if index != current_device():
+        raise ValueError(f"tensors on GPU {index}, but GPU {current_device()} is current")
+    return current_stream(index) if stream is None else stream
 
 
 def allocating_on(stream):
@@ -79,6 +90,8 @@ class Fp4Tensor:
                  "scales_ptr", "device", "index")
 
     def __init__(self, rows, cols, fmt, tensor_scale, codes, scales):
+        if scales.get_device() != codes.get_device():
+            raise ValueError("codes and scales: on different devices")
         self.rows, self.cols, self.fmt, self.tensor_scale = rows, cols, fmt, tensor_scale
         self.codes, self.scales = codes, scales
         self.shape = (rows, cols, fmt)
@@ -108,11 +121,10 @@ def quantize(x: torch.Tensor, fmt, tensor_scale=1.0, out: Fp4Tensor | None = Non
     elif out.shape != (rows, cols, fmt):
         raise ValueError("out: a 4-bit matrix of another shape or format")
     index = out.index
-    if x.get_device() != index or index < 0:
-        raise ValueError("x: must be on the GPU, and on out's")
+    if x.get_device() != index:
+        raise ValueError("x: on another device than out")
     B.conv_fp4_quantize(fmt, CONV_DTYPE[x.dtype], rows, cols, x.data_ptr(), ld, tensor_scale,
-                        out.codes_ptr, out.scales_ptr,
-                        current_stream(index) if stream is None else stream)
+                        out.codes_ptr, out.scales_ptr, call_stream(index, stream))
     out.tensor_scale = tensor_scale
     return out
 
@@ -130,8 +142,7 @@ def dequantize(t: Fp4Tensor, dtype=torch.bfloat16, out: torch.Tensor | None = No
     if out.get_device() != index:
         raise ValueError("out: on another device than t")
     B.conv_fp4_dequantize(t.fmt, CONV_DTYPE[out.dtype], rows, t.cols, t.codes_ptr, t.scales_ptr,
-                          t.tensor_scale, out.data_ptr(), ld,
-                          current_stream(index) if stream is None else stream)
+                          t.tensor_scale, out.data_ptr(), ld, call_stream(index, stream))
     return out
 
 
@@ -182,11 +193,13 @@ class Fp4Linear:
         if (tuple(scales.shape) != (self.K, blocks) or scales.dtype != torch.uint8
                 or not scales.is_contiguous()):
             raise ValueError("scales: expected contiguous uint8 [K][ceil(C / block)]")
+        if scales.get_device() != codes.get_device():
+            raise ValueError("codes and scales: on different devices")
+        handle = call_stream(codes.get_device(), stream)
         _, sb = B.conv_fp4_size(self.fmt, self.K, self.C)
         with allocating_on(stream):
             tiled = torch.empty(sb, dtype=torch.uint8, device=codes.device)
-        B.conv_fp4_pack_scales(self.fmt, self.K, self.C, scales.data_ptr(), tiled.data_ptr(),
-                               current_stream(codes.get_device()) if stream is None else stream)
+        B.conv_fp4_pack_scales(self.fmt, self.K, self.C, scales.data_ptr(), tiled.data_ptr(), handle)
         self._set(Fp4Tensor(self.K, self.C, self.fmt, w_scale, codes, tiled))
 
     def _set(self, w: Fp4Tensor):
@@ -198,11 +211,13 @@ class Fp4Linear:
         if w is None:
             raise RuntimeError("prepack() or load() the weights first")
         C, K, y_dtype, index = self.C, self.K, self.y_dtype, w.index
-        handle = current_stream(index) if stream is None else stream
+        handle = call_stream(index, stream)
         bp = rp = xsp = ysp = None
         if self.x_dtype is None:
             if (x.cols, x.fmt, x.tensor_scale) != (C, self.fmt, self.x_scale):
                 raise ValueError("x: a 4-bit matrix of another width, format or tensor scale")
+            if x.index != index:
+                raise ValueError("x: on another device than the weights")
             rows, ldx = x.rows, C
             xp, xsp = x.codes_ptr, x.scales_ptr
         else:
@@ -215,6 +230,8 @@ class Fp4Linear:
         if bias is not None:
             if bias.dtype is not torch.float32 or bias.numel() != K or not bias.is_contiguous():
                 raise ValueError("bias: expected contiguous fp32 [K]")
+            if bias.get_device() != index:
+                raise ValueError("bias: on another device than the weights")
             bp = bias.data_ptr()
         ldr = ldy = K
         if y_dtype is None:
@@ -222,6 +239,8 @@ class Fp4Linear:
                 out = empty(rows, K, self.fmt, w.device, self.y_scale, stream)
             elif out.shape != (rows, K, self.fmt):
                 raise ValueError("out: a 4-bit matrix of another shape or format")
+            elif out.index != index:
+                raise ValueError("out: on another device than the weights")
             out.tensor_scale = self.y_scale
             yp, ysp = out.codes_ptr, out.scales_ptr
         else:
@@ -229,6 +248,8 @@ class Fp4Linear:
                 lead = (rows,) if self.x_dtype is None else x.shape[:-1]
                 with allocating_on(stream):
                     out = torch.empty(*lead, K, dtype=y_dtype, device=w.device)
+            elif out.get_device() != index:
+                raise ValueError("out: on another device than the weights")
             got, ldy = rows_of(out, K, "out")
             if got != rows or out.dtype is not y_dtype:
                 raise ValueError("out: another number of rows or type")
@@ -237,6 +258,8 @@ class Fp4Linear:
             got, ldr = rows_of(residual, K, "residual")
             if got != rows or residual.dtype is not y_dtype:
                 raise ValueError("residual: another number of rows or type than y")
+            if residual.get_device() != index:
+                raise ValueError("residual: on another device than the weights")
             rp = residual.data_ptr()
         strides = (ldx, ldr, ldy)
         if strides != self._strides:

@@ -35,6 +35,8 @@ class Fp4ResidualBlock:
             if b is not None and (b.dtype != torch.float32 or b.numel() != n
                                   or not b.is_contiguous()):
                 raise ValueError("b1, b2: expected contiguous fp32 [hidden], [C]")
+            if b is not None and b.get_device() < 0:
+                raise ValueError("b1, b2: must be on the GPU")
         self.b1, self.b2 = b1, b2
         self.norm_in = ResidualNorm(C, dtype, torch.bfloat16, eps=eps, pre=B.CONV_NORM_RMS,
                                     w_pre=w_pre, h_fmt=fmt, h_scale=h_scale)
@@ -72,6 +74,10 @@ class Fp4ResidualBlock:
     def _hold(self, w1, w2):
         if w1 is None or w2 is None:
             raise RuntimeError("prepack() or load() the weights first")
+        held = (w1.index, w2.index, self.norm_in.index, self.norm_out.index,
+                *(b.get_device() for b in (self.b1, self.b2) if b is not None))
+        if set(held) - {None, w1.index}:
+            raise ValueError("weights and biases: on different devices")
         b1, b2 = (None if b is None else b.data_ptr() for b in (self.b1, self.b2))
         B.conv_fp4_block_set_weights(self.desc, w1.codes_ptr, w1.scales_ptr, b1, w2.codes_ptr,
                                      w2.scales_ptr, b2)
@@ -84,16 +90,19 @@ class Fp4ResidualBlock:
         if w1 is None or (w1, w2) != self._held:
             self._hold(w1, w2)
         rows, ldx = fp4.rows_of(x, C, "x")
+        index = w1.index
+        handle = fp4.call_stream(index, stream)
+        if x.get_device() != index:
+            raise ValueError("x: on another device than the weights")
         hp = hsp = None
         if h is not None:
             if (h.shape, h.tensor_scale) != ((rows, C, self.fmt), self.h_scale):
                 raise ValueError("h: a 4-bit matrix of another shape, format or tensor scale")
+            if h.index != index:
+                raise ValueError("h: on another device than the weights")
             hp, hsp = h.codes_ptr, h.scales_ptr
-        handle = fp4.current_stream(w1.index) if stream is None else stream
-        if x.get_device() != w1.index:
-            raise ValueError("x: on another device than the weights")
-        x_out, h_out, gp, xop, hop, hosp = self.norm_out._bind(x, rows, ldx, C, gate, x_out, h_out,
-                                                               True, stream)
+        x_out, h_out, gp, xop, hop, hosp = self.norm_out._bind(x, index, rows, ldx, C, gate, x_out,
+                                                               h_out, True, stream)
         if norm_in._strides[0] != ldx:
             norm_in._strides = (ldx, C, C, C, C)
             B.conv_norm_set_strides(norm_in.desc, *norm_in._strides)
@@ -101,7 +110,7 @@ class Fp4ResidualBlock:
         if need is None:
             need = self._sizes[rows] = B.conv_fp4_block_workspace_size(self.desc, rows)
         # held until the launches are enqueued
-        ws = self._ws.get(need, w1.device, w1.index, stream, handle) if need else None
+        ws = self._ws.get(need, w1.device, index, stream, handle) if need else None
         B.conv_fp4_block_fwd(self.desc, rows, x.data_ptr(), hp, hsp, gp, xop, hop, hosp,
                              ws.data_ptr() if need else None, need, handle)
         return x_out, h_out

@@ -252,7 +252,7 @@ def host_layers(B, monkeypatch):
     that are only written down: (torch, fp4, up, calls, allocated).  Every buffer that the
     layers allocate is kept, so that addresses are not used twice."""
     torch = pytest.importorskip("torch")
-    from cnn_convolution_gemm_gb300 import fp4, norm
+    from cnn_convolution_gemm_gb300 import fp4
 
     class OnGpu(torch.Tensor):
         def get_device(self):
@@ -268,8 +268,8 @@ def host_layers(B, monkeypatch):
         allocated.append(t)
         return t
     monkeypatch.setattr(torch, "empty", kept_empty)
-    for module in (fp4, norm):
-        monkeypatch.setattr(module, "current_stream", lambda index: 7)
+    monkeypatch.setattr(fp4, "current_stream", lambda index: 7)
+    monkeypatch.setattr(fp4, "current_device", lambda: 0, raising=False)
     for name in ("conv_fp4_fwd", "conv_fp4_block_fwd", "conv_norm_fwd", "conv_fp4_quantize",
                  "conv_fp4_dequantize", "conv_fp4_pack_scales"):
         monkeypatch.setattr(B, name, lambda *a, name=name: calls.append((name, a)))
@@ -311,3 +311,89 @@ def test_captured_calls_have_workspaces_of_their_own(host_layers, monkeypatch, w
     assert after[1] == after[2] == large != small
     captured.append(after[0])
     assert len({small, large, *captured}) == 6
+
+
+def test_tensors_on_other_devices_are_refused(host_layers, monkeypatch):
+    """Every tensor of a call in host memory, or on a GPU that the call does not run on, and every
+    tensor that a layer keeps."""
+    torch, fp4, up, calls, _ = host_layers
+    from cnn_convolution_gemm_gb300 import binding as B
+    from cnn_convolution_gemm_gb300.norm import ResidualNorm
+    from cnn_convolution_gemm_gb300.residual_block import Fp4ResidualBlock
+    RMS, LN, MX = B.CONV_NORM_RMS, B.CONV_NORM_LAYER, B.CONV_FP4_MX
+    bf, f32, u8 = torch.bfloat16, torch.float32, torch.uint8
+
+    class OnOther(torch.Tensor):
+        def get_device(self):
+            return 1
+
+    def here(*shape, dtype=bf):
+        return up(torch.zeros(*shape, dtype=dtype))
+
+    def elsewhere(t):
+        host = torch.zeros(t.shape, dtype=t.dtype)
+        return host, host.as_subclass(OnOther)
+
+    def held(rows, cols, to=lambda t: t):
+        cb, sb = B.conv_fp4_size(MX, rows, cols)
+        return fp4.Fp4Tensor(rows, cols, MX, 1.0, to(here(cb, dtype=u8)), to(here(sb, dtype=u8)))
+
+    def refused_elsewhere(call, **tensors):
+        """call takes the tensors where they are, and none of them elsewhere."""
+        call(**tensors)
+        for name, t in tensors.items():
+            for k in range(2):
+                if isinstance(t, fp4.Fp4Tensor):
+                    bad = held(t.rows, t.cols, lambda v, k=k: elsewhere(v)[k])
+                else:
+                    bad = elsewhere(t)[k]
+                n = len(calls)
+                with pytest.raises(ValueError):
+                    call(**{**tensors, name: bad})
+                assert len(calls) == n, name
+    layer = fp4.Fp4Linear(64, 32, has_residual=True)
+    layer.load(here(32, 32, dtype=u8), here(32, 2, dtype=u8))
+    refused_elsewhere(layer, x=here(4, 64), bias=here(32, dtype=f32), residual=here(4, 32), out=here(4, 32))
+    refused_elsewhere(layer.load, codes=here(32, 32, dtype=u8), scales=here(32, 2, dtype=u8))
+    codes = fp4.Fp4Linear(64, 32, x_dtype=None, y_dtype=None)
+    codes.load(here(32, 32, dtype=u8), here(32, 2, dtype=u8))
+    refused_elsewhere(codes, x=held(4, 64), out=held(4, 32))
+    refused_elsewhere(lambda x, out: fp4.quantize(x, MX, out=out), x=here(4, 64), out=held(4, 64))
+    refused_elsewhere(lambda t, out: fp4.dequantize(t, out=out), t=held(4, 64), out=here(4, 64))
+    with pytest.raises(ValueError):
+        fp4.Fp4Tensor(4, 64, MX, 1.0, here(128, dtype=u8), torch.zeros(512, dtype=u8))
+    with pytest.raises(ValueError):
+        layer.load(*(here(32, n, dtype=u8).as_subclass(torch.Tensor) for n in (32, 2)))
+    w = [here(64, dtype=f32) for _ in range(4)]
+    for h_fmt in (None, MX):
+        norm = ResidualNorm(64, post=LN, pre=LN, gate=B.CONV_GATE_LINEAR, h_fmt=h_fmt,
+                            w_post=w[0], b_post=w[1], w_pre=w[2], b_pre=w[3])
+        refused_elsewhere(norm, x=here(4, 64), z=here(4, 64), gate=here(4, 64), x_out=here(4, 64),
+                          h_out=held(4, 64) if h_fmt is not None else here(4, 64))
+    refused_elsewhere(ResidualNorm(64, pre=RMS), x=here(4, 64), h_out=here(4, 64))
+    for t in elsewhere(w[0]):
+        for i in range(4):
+            with pytest.raises(ValueError):
+                p = w[:i] + [t] + w[i + 1:]
+                ResidualNorm(64, post=LN, pre=LN, w_post=p[0], b_post=p[1], w_pre=p[2], b_pre=p[3])
+    for chain in (False, True):
+        blk = _host_block(torch, up, gate=B.CONV_GATE_LINEAR, w_pre=w[0], w_post=w[1], w_next=w[2],
+                          b1=here(96, dtype=f32), b2=here(64, dtype=f32), chain=chain)
+        refused_elsewhere(blk, x=here(4, 64), gate=here(4, 64), h=held(4, 64), x_out=here(4, 64),
+                          h_out=held(4, 64) if chain else here(4, 64))
+    n = len(calls)
+    for name, size in (("b1", 96), ("b2", 64), ("w_pre", 64), ("w_post", 64), ("w_next", 64)):
+        for t in elsewhere(here(size, dtype=f32)):
+            with pytest.raises(ValueError):
+                _host_block(torch, up, **{name: t})(here(4, 64))
+    assert not any(name == "conv_fp4_block_fwd" for name, _ in calls[n:])
+    # all of it on a GPU that is not the current one
+    monkeypatch.setattr(fp4, "current_device", lambda: 1)
+    n = len(calls)
+    for call in (lambda: layer(here(4, 64), residual=here(4, 32)), lambda: norm(here(4, 64)),
+                 lambda: blk(here(4, 64), gate=here(4, 64)), lambda: fp4.quantize(here(4, 64), MX),
+                 lambda: fp4.dequantize(held(4, 64)),
+                 lambda: layer.load(here(32, 32, dtype=u8), here(32, 2, dtype=u8))):
+        with pytest.raises(ValueError):
+            call()
+    assert len(calls) == n
