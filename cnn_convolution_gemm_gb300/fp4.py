@@ -6,6 +6,7 @@ their layout in memory: include/gbconv.h); memory and streams come from PyTorch.
 from __future__ import annotations
 
 import contextlib
+import threading
 
 import torch
 
@@ -152,7 +153,8 @@ class Fp4Linear:
 
     x_dtype: torch.bfloat16 or torch.float32 (quantised on the way in with tensor scale
     x_scale), or None for an ``Fp4Tensor``.  y_dtype: likewise, None gives an ``Fp4Tensor``
-    with tensor scale y_scale.  Row strides of the tensors are followed."""
+    with tensor scale y_scale.  Row strides of the tensors are followed.  Threads may share a
+    layer."""
 
     def __init__(self, C, K, fmt=B.CONV_FP4_MX, x_dtype=torch.bfloat16, y_dtype=torch.bfloat16,
                  act=B.CONV_ACT_NONE, has_residual=False, x_scale=1.0, y_scale=1.0):
@@ -165,6 +167,9 @@ class Fp4Linear:
         B.conv_fp4_set_epilogue(self.desc, act, has_residual)
         B.conv_fp4_set_tensor_scales(self.desc, x_scale, 1.0, y_scale)  # w's: with the weights
         self.w = None
+        # a call gives the descriptor its strides and launches before another call, or other
+        # weights, change them; calls on one stream share its workspace
+        self._lock = threading.Lock()
         self._strides = (C, K, K)
         self._sizes = {}  # rows -> workspace bytes
         self._ws = Workspaces()
@@ -199,79 +204,82 @@ class Fp4Linear:
         _, sb = B.conv_fp4_size(self.fmt, self.K, self.C)
         with allocating_on(stream):
             tiled = torch.empty(sb, dtype=torch.uint8, device=codes.device)
-        B.conv_fp4_pack_scales(self.fmt, self.K, self.C, scales.data_ptr(), tiled.data_ptr(), handle)
+        B.conv_fp4_pack_scales(self.fmt, self.K, self.C, scales.data_ptr(), tiled.data_ptr(),
+                               handle)
         self._set(Fp4Tensor(self.K, self.C, self.fmt, w_scale, codes, tiled))
 
     def _set(self, w: Fp4Tensor):
-        B.conv_fp4_set_tensor_scales(self.desc, self.x_scale, w.tensor_scale, self.y_scale)
-        self.w = w
+        with self._lock:
+            B.conv_fp4_set_tensor_scales(self.desc, self.x_scale, w.tensor_scale, self.y_scale)
+            self.w = w
 
     def forward(self, x, bias=None, residual=None, out=None, stream=None):
-        w = self.w
-        if w is None:
-            raise RuntimeError("prepack() or load() the weights first")
-        C, K, y_dtype, index = self.C, self.K, self.y_dtype, w.index
-        handle = call_stream(index, stream)
-        bp = rp = xsp = ysp = None
-        if self.x_dtype is None:
-            if (x.cols, x.fmt, x.tensor_scale) != (C, self.fmt, self.x_scale):
-                raise ValueError("x: a 4-bit matrix of another width, format or tensor scale")
-            if x.index != index:
-                raise ValueError("x: on another device than the weights")
-            rows, ldx = x.rows, C
-            xp, xsp = x.codes_ptr, x.scales_ptr
-        else:
-            if x.dtype is not self.x_dtype:
-                raise ValueError(f"x: {x.dtype}, expected {self.x_dtype}")
-            if x.get_device() != index:
-                raise ValueError("x: on another device than the weights")
-            rows, ldx = rows_of(x, C, "x")
-            xp = x.data_ptr()
-        if bias is not None:
-            if bias.dtype is not torch.float32 or bias.numel() != K or not bias.is_contiguous():
-                raise ValueError("bias: expected contiguous fp32 [K]")
-            if bias.get_device() != index:
-                raise ValueError("bias: on another device than the weights")
-            bp = bias.data_ptr()
-        ldr = ldy = K
-        if y_dtype is None:
-            if out is None:
-                out = empty(rows, K, self.fmt, w.device, self.y_scale, stream)
-            elif out.shape != (rows, K, self.fmt):
-                raise ValueError("out: a 4-bit matrix of another shape or format")
-            elif out.index != index:
-                raise ValueError("out: on another device than the weights")
-            out.tensor_scale = self.y_scale
-            yp, ysp = out.codes_ptr, out.scales_ptr
-        else:
-            if out is None:
-                lead = (rows,) if self.x_dtype is None else x.shape[:-1]
-                with allocating_on(stream):
-                    out = torch.empty(*lead, K, dtype=y_dtype, device=w.device)
-            elif out.get_device() != index:
-                raise ValueError("out: on another device than the weights")
-            got, ldy = rows_of(out, K, "out")
-            if got != rows or out.dtype is not y_dtype:
-                raise ValueError("out: another number of rows or type")
-            yp = out.data_ptr()
-        if residual is not None:
-            got, ldr = rows_of(residual, K, "residual")
-            if got != rows or residual.dtype is not y_dtype:
-                raise ValueError("residual: another number of rows or type than y")
-            if residual.get_device() != index:
-                raise ValueError("residual: on another device than the weights")
-            rp = residual.data_ptr()
-        strides = (ldx, ldr, ldy)
-        if strides != self._strides:
-            B.conv_fp4_set_strides(self.desc, *strides)
-            self._strides = strides
-        need = self._sizes.get(rows)
-        if need is None:
-            need = self._sizes[rows] = B.conv_fp4_workspace_size(self.desc, rows)
-        # held until the launches are enqueued
-        ws = self._ws.get(need, w.device, index, stream, handle) if need else None
-        B.conv_fp4_fwd(self.desc, rows, xp, xsp, w.codes_ptr, w.scales_ptr, bp, rp, yp, ysp,
-                       ws.data_ptr() if need else None, need, handle)
-        return out
+        with self._lock:
+            w = self.w
+            if w is None:
+                raise RuntimeError("prepack() or load() the weights first")
+            C, K, y_dtype, index = self.C, self.K, self.y_dtype, w.index
+            handle = call_stream(index, stream)
+            bp = rp = xsp = ysp = None
+            if self.x_dtype is None:
+                if (x.cols, x.fmt, x.tensor_scale) != (C, self.fmt, self.x_scale):
+                    raise ValueError("x: a 4-bit matrix of another width, format or tensor scale")
+                if x.index != index:
+                    raise ValueError("x: on another device than the weights")
+                rows, ldx = x.rows, C
+                xp, xsp = x.codes_ptr, x.scales_ptr
+            else:
+                if x.dtype is not self.x_dtype:
+                    raise ValueError(f"x: {x.dtype}, expected {self.x_dtype}")
+                if x.get_device() != index:
+                    raise ValueError("x: on another device than the weights")
+                rows, ldx = rows_of(x, C, "x")
+                xp = x.data_ptr()
+            if bias is not None:
+                if bias.dtype is not torch.float32 or bias.numel() != K or not bias.is_contiguous():
+                    raise ValueError("bias: expected contiguous fp32 [K]")
+                if bias.get_device() != index:
+                    raise ValueError("bias: on another device than the weights")
+                bp = bias.data_ptr()
+            ldr = ldy = K
+            if y_dtype is None:
+                if out is None:
+                    out = empty(rows, K, self.fmt, w.device, self.y_scale, stream)
+                elif out.shape != (rows, K, self.fmt):
+                    raise ValueError("out: a 4-bit matrix of another shape or format")
+                elif out.index != index:
+                    raise ValueError("out: on another device than the weights")
+                out.tensor_scale = self.y_scale
+                yp, ysp = out.codes_ptr, out.scales_ptr
+            else:
+                if out is None:
+                    lead = (rows,) if self.x_dtype is None else x.shape[:-1]
+                    with allocating_on(stream):
+                        out = torch.empty(*lead, K, dtype=y_dtype, device=w.device)
+                elif out.get_device() != index:
+                    raise ValueError("out: on another device than the weights")
+                got, ldy = rows_of(out, K, "out")
+                if got != rows or out.dtype is not y_dtype:
+                    raise ValueError("out: another number of rows or type")
+                yp = out.data_ptr()
+            if residual is not None:
+                got, ldr = rows_of(residual, K, "residual")
+                if got != rows or residual.dtype is not y_dtype:
+                    raise ValueError("residual: another number of rows or type than y")
+                if residual.get_device() != index:
+                    raise ValueError("residual: on another device than the weights")
+                rp = residual.data_ptr()
+            strides = (ldx, ldr, ldy)
+            if strides != self._strides:
+                B.conv_fp4_set_strides(self.desc, *strides)
+                self._strides = strides
+            need = self._sizes.get(rows)
+            if need is None:
+                need = self._sizes[rows] = B.conv_fp4_workspace_size(self.desc, rows)
+            # held until the launches are enqueued
+            ws = self._ws.get(need, w.device, index, stream, handle) if need else None
+            B.conv_fp4_fwd(self.desc, rows, xp, xsp, w.codes_ptr, w.scales_ptr, bp, rp, yp, ysp,
+                           ws.data_ptr() if need else None, need, handle)
+            return out
 
     __call__ = forward

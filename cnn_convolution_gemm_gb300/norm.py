@@ -1,6 +1,8 @@
 """The pass between two residual blocks as a torch-facing layer (conv_norm_* of gbconv.h)."""
 from __future__ import annotations
 
+import threading
+
 import torch
 
 from . import binding as B
@@ -14,7 +16,8 @@ class ResidualNorm:
     post, pre: binding.CONV_NORM_*; w_*, b_*: fp32 [C] or None.  gate: binding.CONV_GATE_*,
     one row of gates for gate_rows consecutive rows.  dtype: of x and x'; z_dtype: of z,
     gate and h (dtype if None).  h_fmt: binding.CONV_FP4_* gives h as an ``Fp4Tensor`` with
-    tensor scale h_scale.  Row strides of 2-D tensors are followed."""
+    tensor scale h_scale.  Row strides of 2-D tensors are followed.  Threads may share a
+    layer."""
 
     def __init__(self, C, dtype=torch.bfloat16, z_dtype=None, eps=1e-6, post=B.CONV_NORM_NONE,
                  w_post=None, b_post=None, pre=B.CONV_NORM_NONE, w_pre=None, b_pre=None,
@@ -40,6 +43,8 @@ class ResidualNorm:
         if h_fmt is not None:
             B.conv_norm_set_output(self.desc, B.CONV_NORM_OUT_FP4_MX if h_fmt == B.CONV_FP4_MX
                                    else B.CONV_NORM_OUT_FP4_NV, h_scale)
+        # a call gives the descriptor its strides and launches before another call changes them
+        self._lock = threading.Lock()
         self._strides = (C,) * 5
 
     def __del__(self):
@@ -60,7 +65,8 @@ class ResidualNorm:
 
     def _bind(self, x, index, rows, ldx, ldz, gate, x_out, h_out, want_x, stream):
         """Checks and allocates what a call needs besides x (on device index) and z, and gives
-        the descriptor the strides: (x_out, h_out, addresses of gate, x_out, h_out and its scales)."""
+        the descriptor the strides: (x_out, h_out, addresses of gate, x_out, h_out and its
+        scales)."""
         C, dtype, z_dtype, shape = self.C, self.dtype, self.z_dtype, x.shape
         if x.dtype is not dtype:
             raise ValueError(f"x: {x.dtype}, expected {dtype}")
@@ -111,20 +117,21 @@ class ResidualNorm:
     def forward(self, x, z=None, gate=None, x_out=None, h_out=None, want_x=True, stream=None):
         """Returns (x', h).  x' is None when want_x is false, h when there is no norm_pre.
         x_out may be x itself."""
-        C = self.C
-        rows, ldx = rows_of(x, C, "x")
-        index = x.get_device()
-        handle = call_stream(index, stream)
-        zp, ldz = None, C
-        if z is not None:
-            if (z.dtype is self.z_dtype and z.is_contiguous() and z.shape == x.shape
-                    and z.get_device() == index):
-                zp = z.data_ptr()
-            else:
-                zp, ldz = self._tensor(z, self.z_dtype, rows, index, "z")
-        x_out, h_out, gp, xop, hp, hsp = self._bind(x, index, rows, ldx, ldz, gate, x_out, h_out,
-                                                    want_x, stream)
-        B.conv_norm_fwd(self.desc, rows, x.data_ptr(), zp, gp, xop, hp, hsp, handle)
-        return x_out, h_out
+        with self._lock:
+            C = self.C
+            rows, ldx = rows_of(x, C, "x")
+            index = x.get_device()
+            handle = call_stream(index, stream)
+            zp, ldz = None, C
+            if z is not None:
+                if (z.dtype is self.z_dtype and z.is_contiguous() and z.shape == x.shape
+                        and z.get_device() == index):
+                    zp = z.data_ptr()
+                else:
+                    zp, ldz = self._tensor(z, self.z_dtype, rows, index, "z")
+            x_out, h_out, gp, xop, hp, hsp = self._bind(x, index, rows, ldx, ldz, gate, x_out,
+                                                        h_out, want_x, stream)
+            B.conv_norm_fwd(self.desc, rows, x.data_ptr(), zp, gp, xop, hp, hsp, handle)
+            return x_out, h_out
 
     __call__ = forward

@@ -23,7 +23,8 @@ class Fp4ResidualBlock:
     """RMS norms throughout; gate, gate_rows, residual_scale as in ``ResidualNorm``.
     w_next: weight of the norm behind the block (the next block's, or the final one);
     chain: give h' in 4 bits with tensor scale next_scale instead of dtype.
-    h_scale, t_scale: tensor scales of h and t (CONV_FP4_NV)."""
+    h_scale, t_scale: tensor scales of h and t (CONV_FP4_NV).  Threads may share a block and
+    its parts."""
 
     def __init__(self, C, hidden, fmt=B.CONV_FP4_MX, dtype=torch.bfloat16, eps=1e-6,
                  residual_scale=1.0, gate=B.CONV_GATE_NONE, gate_rows=1, w_pre=None, w_post=None,
@@ -50,6 +51,10 @@ class Fp4ResidualBlock:
                                      h_fmt=fmt if chain else None, h_scale=next_scale)
         self.desc = B.conv_fp4_block_create(self.norm_in.desc, self.fc1.desc, self.fc2.desc,
                                             self.norm_out.desc)
+        # one lock for the descriptors, which the parts' own calls change too
+        self._lock = self.norm_in._lock
+        for part in (self.fc1, self.fc2, self.norm_out):
+            part._lock = self._lock
         self._held = (None, None)  # the weights that desc has the addresses of
         self._sizes, self._ws = {}, fp4.Workspaces()  # sizes: rows -> workspace bytes
 
@@ -86,33 +91,34 @@ class Fp4ResidualBlock:
     def forward(self, x, gate=None, h=None, x_out=None, h_out=None, stream=None):
         """x [..., C] -> (x', h').  h: norm_pre(x) in 4 bits when the block before handed
         it on, else None."""
-        C, w1, w2, norm_in = self.C, self.fc1.w, self.fc2.w, self.norm_in
-        if w1 is None or (w1, w2) != self._held:
-            self._hold(w1, w2)
-        rows, ldx = fp4.rows_of(x, C, "x")
-        index = w1.index
-        handle = fp4.call_stream(index, stream)
-        if x.get_device() != index:
-            raise ValueError("x: on another device than the weights")
-        hp = hsp = None
-        if h is not None:
-            if (h.shape, h.tensor_scale) != ((rows, C, self.fmt), self.h_scale):
-                raise ValueError("h: a 4-bit matrix of another shape, format or tensor scale")
-            if h.index != index:
-                raise ValueError("h: on another device than the weights")
-            hp, hsp = h.codes_ptr, h.scales_ptr
-        x_out, h_out, gp, xop, hop, hosp = self.norm_out._bind(x, index, rows, ldx, C, gate, x_out,
-                                                               h_out, True, stream)
-        if norm_in._strides[0] != ldx:
-            norm_in._strides = (ldx, C, C, C, C)
-            B.conv_norm_set_strides(norm_in.desc, *norm_in._strides)
-        need = self._sizes.get(rows)
-        if need is None:
-            need = self._sizes[rows] = B.conv_fp4_block_workspace_size(self.desc, rows)
-        # held until the launches are enqueued
-        ws = self._ws.get(need, w1.device, index, stream, handle) if need else None
-        B.conv_fp4_block_fwd(self.desc, rows, x.data_ptr(), hp, hsp, gp, xop, hop, hosp,
-                             ws.data_ptr() if need else None, need, handle)
-        return x_out, h_out
+        with self._lock:
+            C, w1, w2, norm_in = self.C, self.fc1.w, self.fc2.w, self.norm_in
+            if w1 is None or (w1, w2) != self._held:
+                self._hold(w1, w2)
+            rows, ldx = fp4.rows_of(x, C, "x")
+            index = w1.index
+            handle = fp4.call_stream(index, stream)
+            if x.get_device() != index:
+                raise ValueError("x: on another device than the weights")
+            hp = hsp = None
+            if h is not None:
+                if (h.shape, h.tensor_scale) != ((rows, C, self.fmt), self.h_scale):
+                    raise ValueError("h: a 4-bit matrix of another shape, format or tensor scale")
+                if h.index != index:
+                    raise ValueError("h: on another device than the weights")
+                hp, hsp = h.codes_ptr, h.scales_ptr
+            x_out, h_out, gp, xop, hop, hosp = self.norm_out._bind(
+                x, index, rows, ldx, C, gate, x_out, h_out, True, stream)
+            if norm_in._strides[0] != ldx:
+                norm_in._strides = (ldx, C, C, C, C)
+                B.conv_norm_set_strides(norm_in.desc, *norm_in._strides)
+            need = self._sizes.get(rows)
+            if need is None:
+                need = self._sizes[rows] = B.conv_fp4_block_workspace_size(self.desc, rows)
+            # held until the launches are enqueued
+            ws = self._ws.get(need, w1.device, index, stream, handle) if need else None
+            B.conv_fp4_block_fwd(self.desc, rows, x.data_ptr(), hp, hsp, gp, xop, hop, hosp,
+                                 ws.data_ptr() if need else None, need, handle)
+            return x_out, h_out
 
     __call__ = forward

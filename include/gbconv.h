@@ -405,7 +405,9 @@ typedef enum {
 typedef struct gbconv_fp4_s* conv_fp4_t;
 
 /* C inputs, K outputs (both > 0).  Defaults: no activation, no residual, tensor
- * scales 1, contiguous rows.  The descriptor is owned by the caller. */
+ * scales 1, contiguous rows.  The descriptor is owned by the caller.  Calls read it and
+ * setters change it: host threads that share one, here and with conv_norm_*, keep a setter
+ * and the calls that rely on it together. */
 conv_status_t conv_fp4_create(conv_fp4_t* out, conv_fp4_format_t fmt, int C, int K, int x_io,
                               int y_io);
 conv_status_t conv_fp4_destroy(conv_fp4_t desc);

@@ -397,3 +397,47 @@ def test_tensors_on_other_devices_are_refused(host_layers, monkeypatch):
         with pytest.raises(ValueError):
             call()
     assert len(calls) == n
+
+
+@pytest.mark.parametrize("what", ["layer", "norm", "block", "part"])
+def test_threads_share_a_layer(host_layers, monkeypatch, what):
+    """Two threads whose tensors have other row strides: each launch finds its own.  A thread that
+    has set its strides gives the other every chance to set others before it launches."""
+    import threading
+    torch, fp4, up, calls, _ = host_layers
+    from cnn_convolution_gemm_gb300 import binding as B
+    from cnn_convolution_gemm_gb300.norm import ResidualNorm
+    if what == "layer":
+        layer = fp4.Fp4Linear(64, 32)
+        layer.load(up(torch.zeros(32, 32, dtype=torch.uint8)), up(torch.zeros(32, 2, dtype=torch.uint8)))
+        run = [layer] * 2
+    elif what == "norm":
+        run = [ResidualNorm(64, pre=B.CONV_NORM_RMS)] * 2
+    else:  # the block in both threads, or in one of them its norm behind
+        blk = _host_block(torch, up)
+        run = [blk, blk.norm_out if what == "part" else blk]
+    now, seen = {}, {}
+    meeting = threading.Barrier(2)
+
+    def set_strides(desc, *strides):
+        now[desc.value] = strides[0]
+        try:
+            meeting.wait(0.3)
+        except threading.BrokenBarrierError:
+            pass
+
+    def launch(desc, *args):
+        used = [blk.norm_in.desc, blk.norm_out.desc] if desc is getattr(run[0], "desc", None) and (
+            what in ("block", "part")) else [desc]
+        seen[threading.current_thread().name] = [now[d.value] for d in used]
+    for name in ("conv_fp4_set_strides", "conv_norm_set_strides"):
+        monkeypatch.setattr(B, name, set_strides)
+    for name in ("conv_fp4_fwd", "conv_norm_fwd", "conv_fp4_block_fwd"):
+        monkeypatch.setattr(B, name, launch)
+    wide = [up(torch.zeros(4, ld, dtype=torch.bfloat16)) for ld in (72, 80)]
+    threads = [threading.Thread(target=lambda i=i: run[i](wide[i][:, :64]), name=str(i)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert set(seen["0"]) == {72} and set(seen["1"]) == {80}, seen
