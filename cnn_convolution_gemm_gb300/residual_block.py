@@ -92,7 +92,8 @@ class Fp4ResidualBlock:
         """x [..., C] -> (x', h').  h: norm_pre(x) in 4 bits when the block before handed
         it on, else None."""
         with self._lock:
-            C, w1, w2, norm_in = self.C, self.fc1.w, self.fc2.w, self.norm_in
+            C, norm_in, fc2 = self.C, self.norm_in, self.fc2
+            w1, w2 = self.fc1.w, fc2.w
             if w1 is None or (w1, w2) != self._held:
                 self._hold(w1, w2)
             rows, ldx = fp4.rows_of(x, C, "x")
@@ -109,9 +110,13 @@ class Fp4ResidualBlock:
                 hp, hsp = h.codes_ptr, h.scales_ptr
             x_out, h_out, gp, xop, hop, hosp = self.norm_out._bind(
                 x, index, rows, ldx, C, gate, x_out, h_out, True, stream)
-            if norm_in._strides[0] != ldx:
+            # the strides of the block's own calls: those of a part's own call stay in its descriptor
+            if norm_in._strides != (ldx, C, C, C, C):
                 norm_in._strides = (ldx, C, C, C, C)
                 B.conv_norm_set_strides(norm_in.desc, *norm_in._strides)
+            if fc2._strides != (self.hidden, C, C):
+                fc2._strides = (self.hidden, C, C)
+                B.conv_fp4_set_strides(fc2.desc, *fc2._strides)
             need = self._sizes.get(rows)
             if need is None:
                 need = self._sizes[rows] = B.conv_fp4_block_workspace_size(self.desc, rows)

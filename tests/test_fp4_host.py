@@ -441,3 +441,21 @@ def test_threads_share_a_layer(host_layers, monkeypatch, what):
     for t in threads:
         t.join()
     assert set(seen["0"]) == {72} and set(seen["1"]) == {80}, seen
+
+
+def test_block_sets_the_strides_that_its_parts_leave(host_layers, monkeypatch):
+    """What the descriptors of a block hold when it launches, after strided calls of each part."""
+    torch, fp4, up, calls, _ = host_layers
+    from cnn_convolution_gemm_gb300 import binding as B
+    blk = _host_block(torch, up)
+    now = {}
+    for name in ("conv_fp4_set_strides", "conv_norm_set_strides"):
+        monkeypatch.setattr(B, name, lambda desc, *strides: now.__setitem__(desc.value, strides))
+    wide = lambda dtype=torch.bfloat16: up(torch.zeros(4, 80, dtype=dtype))[:, :64]  # noqa: E731
+    h = blk.norm_in(wide(), x_out=wide())[1]
+    z = blk.fc2(blk.fc1(h), out=wide(blk.fc2.y_dtype))
+    blk.norm_out(wide(), z, x_out=wide(), h_out=wide())
+    blk(up(torch.zeros(4, 64, dtype=torch.bfloat16)))
+    assert now[blk.norm_in.desc.value] == (64,) * 5
+    assert now[blk.fc2.desc.value] == (96, 64, 64)
+    assert now[blk.norm_out.desc.value] == (64,) * 5

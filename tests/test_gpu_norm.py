@@ -315,3 +315,23 @@ def test_residual_block_workspace_at_16_bytes(fmt, rows):
     for a, b in zip(runs[0][1], runs[1][1]):
         a, b = a.float(), b.float()
         assert ((a - b).abs() <= 2.0 ** -7 * torch.maximum(a.abs(), b.abs()) + 2.0 ** -15).all()
+
+
+def test_residual_block_after_strided_calls_of_its_parts():
+    """Parts called with strided tensors leave the block's own calls as they were."""
+    torch = need_gpu()
+    from cnn_convolution_gemm_gb300.residual_block import Fp4ResidualBlock
+    torch.manual_seed(6)
+    rows, C, hidden = 20, 96, 160
+    blk = Fp4ResidualBlock(C, hidden, B.CONV_FP4_MX, gate=B.CONV_GATE_LINEAR)
+    rand = lambda *s: torch.randn(*s, device="cuda").bfloat16()  # noqa: E731
+    blk.prepack(rand(hidden, C), rand(C, hidden))
+    x, gate = rand(rows, C), rand(rows, C)
+    want = [t.clone() for t in blk(x, gate=gate)]
+    at = lambda t: torch.cat([t, t], 1)[:, :C]  # noqa: E731
+    h = blk.norm_in(at(x), x_out=at(x))[1]
+    z = blk.fc2(blk.fc1(h), out=torch.zeros(rows, 2 * C, dtype=blk.fc2.y_dtype, device="cuda")[:, :C])
+    blk.norm_out(at(x), z, gate=at(gate), x_out=at(x), h_out=at(x))
+    got = blk(x, gate=gate)
+    B.conv_sync_status(torch.cuda.current_stream().cuda_stream)
+    assert all(torch.equal(a.view(torch.int16), b.view(torch.int16)) for a, b in zip(got, want))
