@@ -335,3 +335,61 @@ def test_residual_block_after_strided_calls_of_its_parts():
     got = blk(x, gate=gate)
     B.conv_sync_status(torch.cuda.current_stream().cuda_stream)
     assert all(torch.equal(a.view(torch.int16), b.view(torch.int16)) for a, b in zip(got, want))
+
+
+def _block_behind_its_codes(dt, fmt, rows, C, hidden, gate_rows, strided=False):
+    """x' and h' of a block against 64 bits over the 4-bit t that its own first layer gives, so
+    that no code can fall to another side: z within the product's bound, whose share reaches u
+    directly and through the row's norm (relative rstd * rms(error)); sums of at most C / 32 + 22
+    steps of 2^-24 as in _case; one rounding to dt at the end."""
+    torch = need_gpu()
+    from cnn_convolution_gemm_gb300.residual_block import Fp4ResidualBlock
+    rng = np.random.default_rng(rows + C)
+    dtype = getattr(torch, dt)
+    up = lambda a, d=torch.float32: torch.from_numpy(np.ascontiguousarray(a)).to(d).cuda()  # noqa: E731
+    n64 = lambda t: t.double().cpu().numpy()  # noqa: E731
+    g = 1.0 if fmt == R.MX else float(np.float32(0.0052))
+    gw = 1.0 if fmt == R.MX else float(np.float32(0.00037))
+    x = up(0.05 * rng.standard_normal((rows, C)), dtype)
+    gate = up(rng.standard_normal((-(-rows // gate_rows), C)), dtype)
+    w = [up(1 + 0.1 * rng.standard_normal(C)) for _ in range(3)]
+    b1, b2 = up(0.1 * rng.standard_normal(hidden)), up(0.1 * rng.standard_normal(C))
+    blk = Fp4ResidualBlock(C, hidden, fmt, dtype, residual_scale=0.5, gate=B.CONV_GATE_LINEAR,
+                           gate_rows=gate_rows, w_pre=w[0], w_post=w[1], w_next=w[2], b1=b1, b2=b2,
+                           h_scale=g, t_scale=g)
+    blk.prepack(up(rng.standard_normal((hidden, C)) / np.sqrt(C)),
+                up(rng.standard_normal((C, hidden)) / np.sqrt(hidden)), gw, gw)
+    if strided:
+        x = torch.cat([x, x[:, :3]], 1)[:, :C]
+    xo, h = blk(x, gate=gate)
+    t = blk.fc1(blk.norm_in(x, want_x=False)[1], bias=b1)
+    B.conv_sync_status(torch.cuda.current_stream().cuda_stream)
+    assert xo.dtype is dtype and h.dtype is dtype
+    tv, wv = R.tensor_values(t), R.tensor_values(blk.fc2.w)
+    z = tv @ wv.T + n64(b2)
+    z_err = R.product_bound(tv, wv, z, np.abs(n64(b2)), 24)
+    steps = (C / 32 + 22) * 2.0 ** -24
+    rms = lambda v: np.sqrt((v ** 2).mean(axis=1, keepdims=True))  # noqa: E731
+
+    def normed(v, err, weight):
+        rstd = _rstd(v, RMS)
+        n = v * rstd * weight
+        return n, np.abs(weight) * rstd * (err + np.abs(v) * rstd * rms(err)) + steps * np.abs(n)
+    u, u_err = normed(z, z_err, n64(w[1]))
+    gg = 0.5 * n64(gate)[np.arange(rows) // gate_rows]
+    want = n64(x) + gg * u
+    err = np.abs(gg) * (u_err + 8 * 2.0 ** -24 * np.abs(u)) + 4 * 2.0 ** -24 * (
+        np.abs(n64(x)) + np.abs(want))
+    want_h, h_err = normed(want, err, n64(w[2]))
+    half = 2.0 ** -9 if dt == "bfloat16" else 2.0 ** -24
+    for got, v, e in ((xo, want, err), (h, want_h, h_err)):
+        off = np.abs(n64(got) - v)
+        assert (off <= e + half * (np.abs(v) + e) + 1e-37).all(), (off / (e + half * np.abs(v))).max()
+
+
+@pytest.mark.parametrize("fmt", [R.MX, R.NV])
+@pytest.mark.parametrize("rows,C,hidden,gate_rows,strided", [(1, 256, 512, 1, False), (70, 96, 200, 7, False),
+                                                             (300, 250, 640, 300, True), (2000, 1024, 512, 1, False)])
+def test_residual_block_of_an_fp32_stream(fmt, rows, C, hidden, gate_rows, strided):
+    """The stream, the gates and h' in fp32, and nothing between them in fewer bits but h and t."""
+    _block_behind_its_codes("float32", fmt, rows, C, hidden, gate_rows, strided)
