@@ -103,6 +103,7 @@ SIGNATURES = {
     "conv_fp4_fwd": (_i, [_p, _i, _p, _p, _p, _p, _p, _p, _p, _p, _p, _sz, _p]),
     "conv_norm_create": (_i, [ctypes.POINTER(_p), _i, _i, _i]),
     "conv_norm_destroy": (_i, [_p]),
+    "conv_norm_set_z_dtype": (_i, [_p, _i]),
     "conv_norm_set_post": (_i, [_p, _i, _f, _p, _p]),
     "conv_norm_set_pre": (_i, [_p, _i, _f, _p, _p]),
     "conv_norm_set_gate": (_i, [_p, _i, _i, _f]),
@@ -432,6 +433,10 @@ def conv_norm_create(C, x_dtype=CONV_BF16, z_dtype=CONV_BF16):
 
 def conv_norm_destroy(desc):
     _check(load_library().conv_norm_destroy(desc), "conv_norm_destroy")
+
+
+def conv_norm_set_z_dtype(desc, z_dtype):
+    _check(load_library().conv_norm_set_z_dtype(desc, z_dtype), "conv_norm_set_z_dtype")
 
 
 def conv_norm_set_post(desc, kind, eps=1e-6, w_ptr=None, b_ptr=None):

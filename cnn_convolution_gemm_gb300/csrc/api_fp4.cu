@@ -288,7 +288,7 @@ extern "C" conv_status_t conv_norm_create(conv_norm_t* out, int C, conv_dtype_t 
   NormArgs& a = d->a;
   a.C = C;
   a.x_dtype = x_dtype;
-  a.z_dtype = z_dtype;
+  a.z_dtype = a.h_dtype = z_dtype;
   a.gate_rows = 1;
   a.rs = a.h_scale = 1.0f;
   a.ldx = a.ldz = a.ldg = a.ldxo = a.ldh = C;
@@ -298,6 +298,16 @@ extern "C" conv_status_t conv_norm_create(conv_norm_t* out, int C, conv_dtype_t 
 
 extern "C" conv_status_t conv_norm_destroy(conv_norm_t d) {
   delete d;
+  return gb_ok();
+}
+
+extern "C" conv_status_t conv_norm_set_z_dtype(conv_norm_t d, conv_dtype_t z_dtype) {
+  if (!d) return gb_fail(CONV_ERR_BAD_PARAM, "desc is NULL");
+  if (!is_float(z_dtype)) return gb_fail(CONV_ERR_BAD_PARAM, "z_dtype must be bf16 or fp32");
+  if (z_dtype != d->a.h_dtype && (z_dtype != CONV_F32 || d->a.x_dtype != CONV_BF16))
+    return gb_fail(CONV_ERR_UNSUPPORTED,
+                   "z in another type than gate and h: fp32 with bf16 x, gate and h only");
+  d->a.z_dtype = z_dtype;
   return gb_ok();
 }
 
@@ -393,9 +403,9 @@ static conv_status_t check_norm_call(conv_norm_t d, int rows, const void* x, con
     return gb_fail(CONV_ERR_BAD_PARAM,
                    "gate must be given exactly when the descriptor has one and z is given");
   if (codes && a.ldh != a.C) return gb_fail(CONV_ERR_UNSUPPORTED, "4-bit h is contiguous");
-  const size_t xb = elem_bytes(a.x_dtype), zb = elem_bytes(a.z_dtype);
-  if (!aligned(x, xb) || !aligned(x_out, xb) || !aligned(z, zb) || !aligned(gate, zb) ||
-      !aligned(h, codes ? 16 : zb) || !aligned(h_scales, 16))
+  const size_t xb = elem_bytes(a.x_dtype), hb = elem_bytes(a.h_dtype);
+  if (!aligned(x, xb) || !aligned(x_out, xb) || !aligned(z, elem_bytes(a.z_dtype)) ||
+      !aligned(gate, hb) || !aligned(h, codes ? 16 : hb) || !aligned(h_scales, 16))
     return gb_fail(CONV_ERR_ALIGNMENT, "a tensor is not aligned to its element (codes: 16 bytes)");
   if (x_out == x && a.ldxo != a.ldx)
     return gb_fail(CONV_ERR_BAD_PARAM, "x_out may be x only with x's row stride");
@@ -412,7 +422,9 @@ static conv_status_t check_norm_call(conv_norm_t d, int rows, const void* x, con
 }
 
 static conv_status_t launch_norm(const NormArgs& a, cudaStream_t st) {
-  const bool xb16 = a.x_dtype == CONV_BF16, zb16 = a.z_dtype == CONV_BF16;
+  // without z its type does not matter
+  if (a.z && a.z_dtype != a.h_dtype) return cuda_status(launch_norm_bfb(a, st), "norm");
+  const bool xb16 = a.x_dtype == CONV_BF16, zb16 = a.h_dtype == CONV_BF16;
   return cuda_status(xb16 ? (zb16 ? launch_norm_bb(a, st) : launch_norm_bf(a, st))
                           : (zb16 ? launch_norm_fb(a, st) : launch_norm_ff(a, st)),
                      "norm");

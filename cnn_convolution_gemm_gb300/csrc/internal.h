@@ -302,7 +302,7 @@ cudaError_t launch_fp4_few(const Fp4Gemm& g, cudaStream_t st);
 // ---- norms around a residual block ----------------------------------------------
 
 struct NormArgs {
-  int C, rows, x_dtype, z_dtype;
+  int C, rows, x_dtype, z_dtype, h_dtype;  // h's: of the gates too
   int post, pre, gate_kind, gate_rows, out;
   float eps_post, eps_pre, rs, h_scale;
   const float *w_post, *b_post, *w_pre, *b_pre;
@@ -313,8 +313,9 @@ struct NormArgs {
   int* err;
   unsigned long long wait_ns;
 };
-// by the types of (x, x') and of (z, gate, h): b bf16, f fp32
+// by the types of (x, x') and of (z, gate, h), or of z and of (gate, h): b bf16, f fp32
 cudaError_t launch_norm_bb(const NormArgs& a, cudaStream_t st);
 cudaError_t launch_norm_bf(const NormArgs& a, cudaStream_t st);
 cudaError_t launch_norm_fb(const NormArgs& a, cudaStream_t st);
 cudaError_t launch_norm_ff(const NormArgs& a, cudaStream_t st);
+cudaError_t launch_norm_bfb(const NormArgs& a, cudaStream_t st);  // z given

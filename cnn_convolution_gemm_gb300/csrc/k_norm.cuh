@@ -14,6 +14,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "fp4.cuh"
 #include "internal.h"
@@ -265,13 +266,13 @@ __device__ __forceinline__ void norm_rows(float (&v)[R][N], int kind, float eps,
 constexpr int RING = 2;  // stages of R rows in shared memory
 
 // Stores h of one row.
-template <typename TZ, int T, int N, Layout LAY>
+template <typename TG, int T, int N, Layout LAY>
 __device__ __forceinline__ void store_h(const NormArgs& a, const TensorScale& ts, long long r,
                                         int t, const float (&v)[N]) {
   const bool valid = T >= 32 || r < a.rows;
   const int C = a.C;
   if (a.out == CONV_NORM_OUT_FLOAT) {
-    store_row<TZ, T, N, LAY>(static_cast<TZ*>(a.h) + r * a.ldh, valid, t, C, v);
+    store_row<TG, T, N, LAY>(static_cast<TG*>(a.h) + r * a.ldh, valid, t, C, v);
   } else if constexpr (LAY != SINGLE) {
 #pragma unroll
     for (int i = 0; i < N / 16; ++i) {
@@ -319,8 +320,10 @@ constexpr int least_blocks(int T, int N, Layout lay, bool ahead, int R, bool has
 // threads.
 // AHEAD (GROUPS, T > 32): x and z (if given) come through the ring; else R is 1.
 // HASZ false: z is not given (the first norm of a network or block).
+// Types: TX of x and x', TZ of z, TG of the gates and h.
 // vec_w: 16-byte accesses to weights.  held: how many of their rows shared memory has room for.
-template <typename TX, typename TZ, int T, int N, Layout LAY, bool AHEAD, int R, bool HASZ>
+template <typename TX, typename TZ, typename TG, int T, int N, Layout LAY, bool AHEAD, int R,
+          bool HASZ>
 __global__ void __launch_bounds__(T <= 32 ? 128 : T, least_blocks(T, N, LAY, AHEAD, R, HASZ))
     norm_kernel(const NormArgs a, const TensorScale ts, const bool vec_w, const int held) {
   static_assert(AHEAD ? LAY == GROUPS : R == 1, "rows of a step");
@@ -410,7 +413,7 @@ __global__ void __launch_bounds__(T <= 32 ? 128 : T, least_blocks(T, N, LAY, AHE
     float v[R][N];
     if constexpr (HASZ) {
       float u[R][N];
-      RowRegs<TZ, T, N, LAY> rg[R];
+      RowRegs<TG, T, N, LAY> rg[R];
 #pragma unroll
       for (int k = 0; k < R; ++k) {
         if constexpr (AHEAD)
@@ -467,7 +470,7 @@ __global__ void __launch_bounds__(T <= 32 ? 128 : T, least_blocks(T, N, LAY, AHE
       norm_rows<T, N, LAY, R>(v, a.pre, a.eps_pre, w_pre, b_pre, t, C, vec_w, inv, red, turn);
 #pragma unroll
       for (int k = 0; k < R; ++k)
-        if (T < 32 || r + k < a.rows) store_h<TZ, T, N, LAY>(a, ts, r + k, t, v[k]);
+        if (T < 32 || r + k < a.rows) store_h<TG, T, N, LAY>(a, ts, r + k, t, v[k]);
     }
     if constexpr (AHEAD) {
       // every thread has read the rows before a barrier: norm_pre's, or this one
@@ -514,41 +517,42 @@ cudaError_t launch_rows(K* kern, const NormArgs& a, int block, int rows_per_bloc
   return e;
 }
 
-template <typename TX, typename TZ, int T, int N, Layout LAY>
+template <typename TX, typename TZ, typename TG, int T, int N, Layout LAY>
 cudaError_t launch_direct(const NormArgs& a, cudaStream_t st) {
-  auto* kern = a.z ? norm_kernel<TX, TZ, T, N, LAY, false, 1, true>
-                   : norm_kernel<TX, TZ, T, N, LAY, false, 1, false>;
+  auto* kern = norm_kernel<TX, TZ, TG, T, N, LAY, false, 1, true>;
+  if constexpr (std::is_same_v<TZ, TG>)  // launch(): without z the types are equal
+    if (!a.z) kern = norm_kernel<TX, TZ, TG, T, N, LAY, false, 1, false>;
   return launch_rows(kern, a, T <= 32 ? 128 : T, T <= 32 ? 128 / T : 1, 0, 0, st);
 }
 
 // 16 consecutive columns a thread up to 8192 channels (152 rows of 4160 bf16 with gates
 // 5.4 us, 32 columns 6.7), 32 above
-template <typename TX, typename TZ, Layout LAY>
+template <typename TX, typename TZ, typename TG, Layout LAY>
 cudaError_t launch_groups(const NormArgs& a, cudaStream_t st) {
-  if (a.C <= 128) return launch_direct<TX, TZ, 8, 16, LAY>(a, st);
-  if (a.C <= 256) return launch_direct<TX, TZ, 16, 16, LAY>(a, st);
-  if (a.C <= 512) return launch_direct<TX, TZ, 32, 16, LAY>(a, st);
-  if (a.C <= 1024) return launch_direct<TX, TZ, 64, 16, LAY>(a, st);
-  if (a.C <= 2048) return launch_direct<TX, TZ, 128, 16, LAY>(a, st);
-  if (a.C <= 4096) return launch_direct<TX, TZ, 256, 16, LAY>(a, st);
-  if (a.C <= 8192) return launch_direct<TX, TZ, 512, 16, LAY>(a, st);
-  if (a.C <= 16384) return launch_direct<TX, TZ, 512, 32, LAY>(a, st);
-  return launch_direct<TX, TZ, 1024, 32, LAY>(a, st);
+  if (a.C <= 128) return launch_direct<TX, TZ, TG, 8, 16, LAY>(a, st);
+  if (a.C <= 256) return launch_direct<TX, TZ, TG, 16, 16, LAY>(a, st);
+  if (a.C <= 512) return launch_direct<TX, TZ, TG, 32, 16, LAY>(a, st);
+  if (a.C <= 1024) return launch_direct<TX, TZ, TG, 64, 16, LAY>(a, st);
+  if (a.C <= 2048) return launch_direct<TX, TZ, TG, 128, 16, LAY>(a, st);
+  if (a.C <= 4096) return launch_direct<TX, TZ, TG, 256, 16, LAY>(a, st);
+  if (a.C <= 8192) return launch_direct<TX, TZ, TG, 512, 16, LAY>(a, st);
+  if (a.C <= 16384) return launch_direct<TX, TZ, TG, 512, 32, LAY>(a, st);
+  return launch_direct<TX, TZ, TG, 1024, 32, LAY>(a, st);
 }
 
 // 8 single columns a thread (an access is one element: with more of them registers, not
 // bytes on their way, fill the SM: 12544 x 1001 fp32, 16 columns 52 us), 16 and 32 where a
 // row needs them
-template <typename TX, typename TZ>
+template <typename TX, typename TZ, typename TG>
 cudaError_t launch_single(const NormArgs& a, cudaStream_t st) {
-  if (a.C <= 256) return launch_direct<TX, TZ, 32, 8, SINGLE>(a, st);
-  if (a.C <= 512) return launch_direct<TX, TZ, 64, 8, SINGLE>(a, st);
-  if (a.C <= 1024) return launch_direct<TX, TZ, 128, 8, SINGLE>(a, st);
-  if (a.C <= 2048) return launch_direct<TX, TZ, 256, 8, SINGLE>(a, st);
-  if (a.C <= 4096) return launch_direct<TX, TZ, 512, 8, SINGLE>(a, st);
-  if (a.C <= 8192) return launch_direct<TX, TZ, 1024, 8, SINGLE>(a, st);
-  if (a.C <= 16384) return launch_direct<TX, TZ, 1024, 16, SINGLE>(a, st);
-  return launch_direct<TX, TZ, 1024, 32, SINGLE>(a, st);
+  if (a.C <= 256) return launch_direct<TX, TZ, TG, 32, 8, SINGLE>(a, st);
+  if (a.C <= 512) return launch_direct<TX, TZ, TG, 64, 8, SINGLE>(a, st);
+  if (a.C <= 1024) return launch_direct<TX, TZ, TG, 128, 8, SINGLE>(a, st);
+  if (a.C <= 2048) return launch_direct<TX, TZ, TG, 256, 8, SINGLE>(a, st);
+  if (a.C <= 4096) return launch_direct<TX, TZ, TG, 512, 8, SINGLE>(a, st);
+  if (a.C <= 8192) return launch_direct<TX, TZ, TG, 1024, 8, SINGLE>(a, st);
+  if (a.C <= 16384) return launch_direct<TX, TZ, TG, 1024, 16, SINGLE>(a, st);
+  return launch_direct<TX, TZ, TG, 1024, 32, SINGLE>(a, st);
 }
 
 // Shared memory of the ring and the weights beside it; the latter as far as they fit.
@@ -569,24 +573,27 @@ AheadSmem ahead_smem(const NormArgs& a) {
 }
 
 // Z_ONLY: called with z alone.
-template <typename TX, typename TZ, int T, int R, bool Z_ONLY = false>
+template <typename TX, typename TZ, typename TG, int T, int R, bool Z_ONLY = false>
 cudaError_t launch_ahead(const NormArgs& a, cudaStream_t st) {
-  auto* kern = norm_kernel<TX, TZ, T, 16, GROUPS, true, R, true>;
-  if constexpr (!Z_ONLY)
-    if (!a.z) kern = norm_kernel<TX, TZ, T, 16, GROUPS, true, R, false>;
+  auto* kern = norm_kernel<TX, TZ, TG, T, 16, GROUPS, true, R, true>;
+  if constexpr (!Z_ONLY && std::is_same_v<TZ, TG>)
+    if (!a.z) kern = norm_kernel<TX, TZ, TG, T, 16, GROUPS, true, R, false>;
   const AheadSmem smem = ahead_smem<TX, TZ, T, R>(a);
   const cudaError_t e = gb_set_smem_once(reinterpret_cast<const void*>(kern), smem.bytes);
   if (e != cudaSuccess) return e;
   return launch_rows(kern, a, T, R, smem.bytes, smem.held, st);
 }
 
-template <typename TX, typename TZ>
+template <typename TX, typename TZ, typename TG = TZ>
 cudaError_t launch(const NormArgs& a, cudaStream_t st) {
+  if constexpr (!std::is_same_v<TZ, TG>)
+    if (!a.z) return cudaErrorInvalidValue;  // the caller's to dispatch by TX and TG
   const bool codes = a.out != CONV_NORM_OUT_FLOAT;
   const auto fit_x = [](const void* p, long long ld) { return !p || rows_vec<TX>(p, ld, 32); };
   const auto fit_z = [](const void* p, long long ld) { return !p || rows_vec<TZ>(p, ld, 32); };
+  const auto fit_g = [](const void* p, long long ld) { return !p || rows_vec<TG>(p, ld, 32); };
   const bool vec = fit_x(a.x, a.ldx) && fit_x(a.x_out, a.ldxo) && fit_z(a.z, a.ldz) &&
-                   fit_z(a.gate, a.ldg) && (codes || fit_z(a.h, a.ldh));
+                   fit_g(a.gate, a.ldg) && (codes || fit_g(a.h, a.ldh));
   // many rows of whole 16-byte pieces: through the ring, two at a time where they fit.  Above
   // 4096 channels three to an SM are many (608 x 8192 bf16 9.3 us, else 10.5; 304 6.3 and
   // 6.1), above 2048 eight, below so many that a block has several steps
@@ -594,30 +601,30 @@ cudaError_t launch(const NormArgs& a, cudaStream_t st) {
       gb_num_sms() * (a.C > 4096 ? 3LL : a.C > 2048 ? 8LL : 8192 / std::max(a.C, 512) * 8);
   if (vec && a.C > 512 && a.C * sizeof(TX) % 16 == 0 && a.C * sizeof(TZ) % 16 == 0 &&
       a.rows >= many) {
-    if (a.C <= 1024) return launch_ahead<TX, TZ, 64, 2>(a, st);
-    if (a.C <= 2048) return launch_ahead<TX, TZ, 128, 2>(a, st);
+    if (a.C <= 1024) return launch_ahead<TX, TZ, TG, 64, 2>(a, st);
+    if (a.C <= 2048) return launch_ahead<TX, TZ, TG, 128, 2>(a, st);
     // one row of 192 threads, four blocks to an SM (12442 x 2560 bf16 46 us, 256 threads and
     // two rows 64)
-    if (a.C <= 16 * 192) return launch_ahead<TX, TZ, 192, 1>(a, st);
+    if (a.C <= 16 * 192) return launch_ahead<TX, TZ, TG, 192, 1>(a, st);
     if (a.C <= 4096) {
       // likewise (24384 x 4096 bf16, layer norms 220 us, two rows 266; fp32, one block: 427
       // and 343)
       if (a.z && ahead_smem<TX, TZ, 256, 1>(a).twice)
-        return launch_ahead<TX, TZ, 256, 1, true>(a, st);
-      if (ahead_smem<TX, TZ, 256, 2>(a).all) return launch_ahead<TX, TZ, 256, 2>(a, st);
+        return launch_ahead<TX, TZ, TG, 256, 1, true>(a, st);
+      if (ahead_smem<TX, TZ, 256, 2>(a).all) return launch_ahead<TX, TZ, TG, 256, 2>(a, st);
     } else if (a.C <= 16 * 384 && ahead_smem<TX, TZ, 384, 1>(a).twice) {
       // the same of 384 threads where two blocks fit (12442 x 4768 bf16 93 us, else 125; one
       // block with four weights 200, else 187)
-      return launch_ahead<TX, TZ, 384, 1>(a, st);
+      return launch_ahead<TX, TZ, TG, 384, 1>(a, st);
     } else if (a.C <= 8192) {
-      if (ahead_smem<TX, TZ, 512, 2>(a).all) return launch_ahead<TX, TZ, 512, 2>(a, st);
-      if (ahead_smem<TX, TZ, 512, 1>(a).all) return launch_ahead<TX, TZ, 512, 1>(a, st);
+      if (ahead_smem<TX, TZ, 512, 2>(a).all) return launch_ahead<TX, TZ, TG, 512, 2>(a, st);
+      if (ahead_smem<TX, TZ, 512, 1>(a).all) return launch_ahead<TX, TZ, TG, 512, 1>(a, st);
     } else if (a.C <= 16384 && ahead_smem<TX, TZ, 1024, 1>(a).bytes) {
-      return launch_ahead<TX, TZ, 1024, 1>(a, st);
+      return launch_ahead<TX, TZ, TG, 1024, 1>(a, st);
     }
   }
-  if (vec) return launch_groups<TX, TZ, GROUPS>(a, st);
-  return codes ? launch_groups<TX, TZ, ANY>(a, st) : launch_single<TX, TZ>(a, st);
+  if (vec) return launch_groups<TX, TZ, TG, GROUPS>(a, st);
+  return codes ? launch_groups<TX, TZ, TG, ANY>(a, st) : launch_single<TX, TZ, TG>(a, st);
 }
 
 }  // namespace norm

@@ -14,15 +14,17 @@ class ResidualNorm:
     """u = norm_post(z);  x' = x + residual_scale * g(gate) * u;  h = norm_pre(x').
 
     post, pre: binding.CONV_NORM_*; w_*, b_*: fp32 [C] or None.  gate: binding.CONV_GATE_*,
-    one row of gates for gate_rows consecutive rows.  dtype: of x and x'; z_dtype: of z,
-    gate and h (dtype if None).  h_fmt: binding.CONV_FP4_* gives h as an ``Fp4Tensor`` with
+    one row of gates for gate_rows consecutive rows.  dtype: of x and x'; z_dtype: of z (dtype
+    if None); h_dtype: of gate and h (z_dtype if None, else bf16 with bf16 x and fp32 z).  h_fmt: binding.CONV_FP4_* gives h as an ``Fp4Tensor`` with
     tensor scale h_scale.  Row strides of 2-D tensors are followed.  Threads may share a
     layer."""
 
     def __init__(self, C, dtype=torch.bfloat16, z_dtype=None, eps=1e-6, post=B.CONV_NORM_NONE,
                  w_post=None, b_post=None, pre=B.CONV_NORM_NONE, w_pre=None, b_pre=None,
-                 gate=B.CONV_GATE_NONE, gate_rows=1, residual_scale=1.0, h_fmt=None, h_scale=1.0):
+                 gate=B.CONV_GATE_NONE, gate_rows=1, residual_scale=1.0, h_fmt=None, h_scale=1.0,
+                 h_dtype=None):
         self.C, self.dtype, self.z_dtype = C, dtype, dtype if z_dtype is None else z_dtype
+        self.h_dtype = self.z_dtype if h_dtype is None else h_dtype
         self.post, self.pre, self.gate, self.gate_rows = post, pre, gate, gate_rows
         self.h_fmt, self.h_scale = h_fmt, h_scale
         self._params = (w_post, b_post, w_pre, b_pre)  # the descriptor holds their addresses
@@ -36,7 +38,8 @@ class ResidualNorm:
                 raise ValueError("weights and biases: must be on one GPU")
             self.index = p.get_device()
         wp, bp, wq, bq = (None if p is None else p.data_ptr() for p in self._params)
-        self.desc = B.conv_norm_create(C, CONV_DTYPE[dtype], CONV_DTYPE[self.z_dtype])
+        self.desc = B.conv_norm_create(C, CONV_DTYPE[dtype], CONV_DTYPE[self.h_dtype])
+        B.conv_norm_set_z_dtype(self.desc, CONV_DTYPE[self.z_dtype])
         B.conv_norm_set_post(self.desc, post, eps, wp, bp)
         B.conv_norm_set_pre(self.desc, pre, eps, wq, bq)
         B.conv_norm_set_gate(self.desc, gate, gate_rows, residual_scale)
@@ -67,7 +70,7 @@ class ResidualNorm:
         """Checks and allocates what a call needs besides x (on device index) and z, and gives
         the descriptor the strides: (x_out, h_out, addresses of gate, x_out, h_out and its
         scales)."""
-        C, dtype, z_dtype, shape = self.C, self.dtype, self.z_dtype, x.shape
+        C, dtype, h_dtype, shape = self.C, self.dtype, self.h_dtype, x.shape
         if x.dtype is not dtype:
             raise ValueError(f"x: {x.dtype}, expected {dtype}")
         if self.index is not None and self.index != index:
@@ -75,7 +78,7 @@ class ResidualNorm:
         gp = xop = hp = hsp = None
         ldg = ldxo = ldh = C
         if gate is not None:
-            gp, ldg = self._tensor(gate, z_dtype, -(-rows // self.gate_rows), index, "gate")
+            gp, ldg = self._tensor(gate, h_dtype, -(-rows // self.gate_rows), index, "gate")
         # of each output first the usual case: x's shape, contiguous
         if want_x:
             if x_out is None:
@@ -102,12 +105,12 @@ class ResidualNorm:
         else:
             if h_out is None:
                 with allocating_on(stream):
-                    h_out = torch.empty(shape, dtype=z_dtype, device=x.device)
-            if (h_out.dtype is z_dtype and h_out.is_contiguous() and h_out.shape == shape
+                    h_out = torch.empty(shape, dtype=h_dtype, device=x.device)
+            if (h_out.dtype is h_dtype and h_out.is_contiguous() and h_out.shape == shape
                     and h_out.get_device() == index):
                 hp = h_out.data_ptr()
             else:
-                hp, ldh = self._tensor(h_out, z_dtype, rows, index, "h_out")
+                hp, ldh = self._tensor(h_out, h_dtype, rows, index, "h_out")
         strides = (ldx, ldz, ldg, ldxo, ldh)
         if strides != self._strides:
             B.conv_norm_set_strides(self.desc, *strides)

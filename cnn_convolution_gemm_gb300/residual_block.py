@@ -21,7 +21,7 @@ from .norm import ResidualNorm
 
 class Fp4ResidualBlock:
     """RMS norms throughout; gate, gate_rows, residual_scale as in ``ResidualNorm``.  dtype: of
-    x, gate, x' and h', and of z between the second layer and the norm behind it.
+    x, gate, x' and h'; z, between the second layer and the norm behind it, is fp32.
     w_next: weight of the norm behind the block (the next block's, or the final one);
     chain: give h' in 4 bits with tensor scale next_scale instead of dtype.
     h_scale, t_scale: tensor scales of h and t (CONV_FP4_NV).  Threads may share a block and
@@ -44,11 +44,12 @@ class Fp4ResidualBlock:
                                     w_pre=w_pre, h_fmt=fmt, h_scale=h_scale)
         self.fc1 = Fp4Linear(C, hidden, fmt, x_dtype=None, y_dtype=None, act=B.CONV_ACT_GELU,
                              x_scale=h_scale, y_scale=t_scale)
-        self.fc2 = Fp4Linear(hidden, C, fmt, x_dtype=None, y_dtype=dtype, x_scale=t_scale)
-        self.norm_out = ResidualNorm(C, dtype, eps=eps, post=B.CONV_NORM_RMS,
+        self.fc2 = Fp4Linear(hidden, C, fmt, x_dtype=None, y_dtype=torch.float32, x_scale=t_scale)
+        self.norm_out = ResidualNorm(C, dtype, torch.float32, eps=eps, post=B.CONV_NORM_RMS,
                                      w_post=w_post, pre=B.CONV_NORM_RMS, w_pre=w_next, gate=gate,
                                      gate_rows=gate_rows, residual_scale=residual_scale,
-                                     h_fmt=fmt if chain else None, h_scale=next_scale)
+                                     h_fmt=fmt if chain else None, h_scale=next_scale,
+                                     h_dtype=dtype)
         self.desc = B.conv_fp4_block_create(self.norm_in.desc, self.fc1.desc, self.fc2.desc,
                                             self.norm_out.desc)
         # one lock for the descriptors, which the parts' own calls change too

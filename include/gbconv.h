@@ -446,7 +446,7 @@ conv_status_t conv_fp4_fwd(conv_fp4_t desc, int M, const void* x, const void* x_
 typedef enum { CONV_NORM_NONE = 0, CONV_NORM_RMS = 1, CONV_NORM_LAYER = 2 } conv_norm_kind_t;
 typedef enum { CONV_GATE_NONE = 0, CONV_GATE_LINEAR = 1, CONV_GATE_SIGMOID = 2 } conv_gate_t;
 typedef enum {
-  CONV_NORM_OUT_FLOAT = 0,   /* h in z_dtype                                        */
+  CONV_NORM_OUT_FLOAT = 0,   /* h in create's z_dtype                               */
   CONV_NORM_OUT_FP4_MX = 1,  /* h as 4-bit codes and scales (conv_fp4_size)         */
   CONV_NORM_OUT_FP4_NV = 2
 } conv_norm_out_t;
@@ -458,6 +458,10 @@ typedef struct gbconv_norm_s* conv_norm_t;
 conv_status_t conv_norm_create(conv_norm_t* out, int C, conv_dtype_t x_dtype,
                                conv_dtype_t z_dtype);
 conv_status_t conv_norm_destroy(conv_norm_t desc);
+/* The type of z alone; gate and h keep create's.  CONV_F32 with bf16 x, gate and h: a
+ * product's fp32 sums then need not be rounded before they are normalised.  Other mixtures
+ * are CONV_ERR_UNSUPPORTED. */
+conv_status_t conv_norm_set_z_dtype(conv_norm_t desc, conv_dtype_t z_dtype);
 /* The norm of z / of x': kind, eps (>= 0), w and b device fp32 [C] that must stay
  * valid while the descriptor is used (NULL: ones / zeros; b: layer norms only). */
 conv_status_t conv_norm_set_post(conv_norm_t desc, int kind, float eps, const float* w,

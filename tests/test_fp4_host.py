@@ -459,3 +459,33 @@ def test_block_sets_the_strides_that_its_parts_leave(host_layers, monkeypatch):
     assert now[blk.norm_in.desc.value] == (64,) * 5
     assert now[blk.fc2.desc.value] == (96, 64, 64)
     assert now[blk.norm_out.desc.value] == (64,) * 5
+
+
+def test_type_of_z_alone(B):
+    f = B.conv_norm_set_z_dtype
+    d = B.conv_norm_create(64, B.CONV_BF16, B.CONV_BF16)
+    f(d, B.CONV_F32)
+    # z is aligned to its own element, gate and h to theirs
+    B.conv_norm_set_gate(d, B.CONV_GATE_LINEAR)
+    refused(B, ALIGN, B.conv_norm_fwd, d, 4, P, P + 2, P, P, None)
+    refused(B, ALIGN, B.conv_norm_fwd, d, 4, P, P, P + 1, P, None)
+    f(d, B.CONV_BF16)
+    refused(B, BAD, f, d, B.CONV_INT8)
+    refused(B, BAD, f, None, B.CONV_F32)
+    B.conv_norm_destroy(d)
+    for x, h, z in ((B.CONV_F32, B.CONV_BF16, B.CONV_F32), (B.CONV_F32, B.CONV_F32, B.CONV_BF16),
+                    (B.CONV_BF16, B.CONV_F32, B.CONV_BF16)):
+        d = B.conv_norm_create(64, x, h)
+        refused(B, UNSUP, f, d, z)
+        f(d, h)
+        B.conv_norm_destroy(d)
+    # a block's second layer gives what the norm behind takes
+    CODES = B.CONV_FP4_IO_CODES
+    n_in, n_out = B.conv_norm_create(64), B.conv_norm_create(64)
+    B.conv_norm_set_pre(n_in, B.CONV_NORM_RMS)
+    B.conv_norm_set_output(n_in, B.CONV_NORM_OUT_FP4_MX)
+    fc1 = B.conv_fp4_create(B.CONV_FP4_MX, 64, 96, CODES, CODES)
+    fc2 = B.conv_fp4_create(B.CONV_FP4_MX, 96, 64, CODES, B.CONV_FP4_IO_F32)
+    refused(B, BAD, B.conv_fp4_block_create, n_in, fc1, fc2, n_out)
+    f(n_out, B.CONV_F32)
+    B.conv_fp4_block_destroy(B.conv_fp4_block_create(n_in, fc1, fc2, n_out))

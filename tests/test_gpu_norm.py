@@ -337,6 +337,12 @@ def test_residual_block_after_strided_calls_of_its_parts():
     assert all(torch.equal(a.view(torch.int16), b.view(torch.int16)) for a, b in zip(got, want))
 
 
+def _half_spacing(v, dt):
+    """The most that one rounding to dt moves a value of up to this magnitude: half the distance of
+    its neighbours, of 8 or 24 significant bits."""
+    return np.ldexp(1.0, np.frexp(v + 1e-37)[1] - {"bfloat16": 9, "float32": 25}[dt])
+
+
 def _block_behind_its_codes(dt, fmt, rows, C, hidden, gate_rows, strided=False):
     """x' and h' of a block against 64 bits over the 4-bit t that its own first layer gives, so
     that no code can fall to another side: z within the product's bound, whose share reaches u
@@ -381,10 +387,9 @@ def _block_behind_its_codes(dt, fmt, rows, C, hidden, gate_rows, strided=False):
     err = np.abs(gg) * (u_err + 8 * 2.0 ** -24 * np.abs(u)) + 4 * 2.0 ** -24 * (
         np.abs(n64(x)) + np.abs(want))
     want_h, h_err = normed(want, err, n64(w[2]))
-    half = 2.0 ** -9 if dt == "bfloat16" else 2.0 ** -24
     for got, v, e in ((xo, want, err), (h, want_h, h_err)):
         off = np.abs(n64(got) - v)
-        assert (off <= e + half * (np.abs(v) + e) + 1e-37).all(), (off / (e + half * np.abs(v))).max()
+        assert (off <= e + _half_spacing(np.abs(v) + e, dt)).all()
 
 
 @pytest.mark.parametrize("fmt", [R.MX, R.NV])
@@ -393,3 +398,63 @@ def _block_behind_its_codes(dt, fmt, rows, C, hidden, gate_rows, strided=False):
 def test_residual_block_of_an_fp32_stream(fmt, rows, C, hidden, gate_rows, strided):
     """The stream, the gates and h' in fp32, and nothing between them in fewer bits but h and t."""
     _block_behind_its_codes("float32", fmt, rows, C, hidden, gate_rows, strided)
+
+
+@pytest.mark.parametrize("fmt", [R.MX, R.NV])
+@pytest.mark.parametrize("rows,C,hidden,gate_rows,strided", [(1, 256, 512, 1, False), (70, 96, 200, 7, False),
+                                                             (300, 250, 640, 300, True), (2000, 1024, 512, 1, False)])
+def test_residual_block_holds_z_in_32_bits(fmt, rows, C, hidden, gate_rows, strided):
+    """x' and h' of a bf16 stream are rounded once, at the end."""
+    _block_behind_its_codes("bfloat16", fmt, rows, C, hidden, gate_rows, strided)
+
+
+@pytest.mark.parametrize("post,pre,rows,C,kw", [
+    (RMS, RMS, 1, 4096, {"gate": 2}), (LN, LN, 33, 257, {"gate": 1}), (RMS, LN, 5, 96, {}), (N, N, 9, 100, {}),
+    (RMS, RMS, 1301, 8192, {}), (LN, LN, 2501, 4096, {"gate": 2, "gate_rows": 7}), (LN, RMS, 10001, 1024, {}),
+    (RMS, RMS, 5003, 2040, {"h_fmt": R.NV, "gate": 1}), (RMS, RMS, 1303, 6000, {"in_place": True}),
+    (LN, RMS, 701, 12296, {}), (RMS, N, 3, 20000, {}), (RMS, RMS, 4, 9001, {"h_fmt": R.MX}),
+    (RMS, LN, 12, 256, {"strided": True}), (LN, RMS, 1037, 112, {"h_fmt": R.MX}), (RMS, RMS, 40, 2500, {}),
+    (LN, RMS, 12, 256, {"with_z": False}), (LN, RMS, 12, 95, {"with_z": False, "h_fmt": R.NV})])
+def test_z_in_another_type(post, pre, rows, C, kw):
+    """fp32 z with bf16 x, gate and h, against the layer that has gate and h in fp32 too (and its
+    own test against 64 bits).  Sums may be added in another order: (C / 32 + 22) steps of 2^-24
+    of a row's largest magnitude, up to 4 (largest u or h + 1) with the weights and biases here.
+    x' differs by 0.5 |g| of that (|g| <= 5, |u| <= 8: 90 steps), then may be the next bf16 value
+    (2^-7); h by its own sums, by that of x' (whose deviation is 4: less than half) and by its
+    rounding."""
+    torch, ResidualNorm = _norm()
+    kw = dict(kw)
+    gate, gate_rows, h_fmt = kw.pop("gate", 0), kw.pop("gate_rows", 1), kw.pop("h_fmt", None)
+    with_z, strided, in_place = (kw.pop(k, d) for k, d in (("with_z", True), ("strided", False),
+                                                           ("in_place", False)))
+    assert not kw
+    gen = torch.Generator(device="cuda").manual_seed(rows + C)
+    rand = lambda *s: torch.randn(*s, generator=gen, device="cuda")  # noqa: E731
+    x, z = (4 * rand(rows, C)).bfloat16(), rand(rows, C) if with_z else None
+    g = rand(-(-rows // gate_rows), C).bfloat16() if gate and with_z else None
+    if strided:
+        x, z = torch.cat([x, x], 1)[:, :C], torch.cat([z, z[:, :1]], 1)[:, :C]
+    vec = lambda o, there: o + 0.1 * rand(C) if there else None  # noqa: E731
+    scale = 1.0 if h_fmt != R.NV else float(np.float32(0.0041))
+    p = dict(post=post, pre=pre, gate=gate, gate_rows=gate_rows, residual_scale=0.5,
+             w_post=vec(1, post), b_post=vec(0, post == LN), w_pre=vec(1, pre), b_pre=vec(0, pre == LN))
+    want_x, want_h = ResidualNorm(C, torch.bfloat16, torch.float32, **p)(
+        x, z, gate=None if g is None else g.float())
+    layer = ResidualNorm(C, torch.bfloat16, torch.float32, h_dtype=torch.bfloat16, h_fmt=h_fmt,
+                         h_scale=scale, **p)
+    xo, h = layer(x, z, gate=g, x_out=x if in_place else None)
+    B.conv_sync_status(torch.cuda.current_stream().cuda_stream)
+    a, b = xo.float(), want_x.float()
+    steps = (C / 32 + 22) * 2.0 ** -24
+    assert ((a - b).abs() <= 2.0 ** -7 * torch.maximum(a.abs(), b.abs()) + 90 * steps).all()
+    if not pre:
+        assert h is None
+        return
+    want = want_h.double().cpu().numpy()
+    err = steps * (4 * (np.abs(want).max(axis=1, keepdims=True) + 1) + 45) + 0 * want
+    if h_fmt is not None:
+        R.check_quantized(h, want, err, h_fmt, scale)
+        return
+    assert h.dtype is torch.bfloat16
+    off = np.abs(h.double().cpu().numpy() - want)
+    assert (off <= err + _half_spacing(np.abs(want) + err, "bfloat16")).all()
