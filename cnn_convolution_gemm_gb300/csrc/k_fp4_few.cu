@@ -77,13 +77,13 @@ __device__ __forceinline__ void finish(const FewParams& p, float (&v)[8], int m,
       for (int i = 0; i < 8; ++i)
         if (i < rows) v[i] += load_f32(res + i * step * p.ldr);
     }
-    activate(v, p.act);
+    activate<YIO == CONV_FP4_IO_F32>(v, p.act);
     T* const y = static_cast<T*>(p.y) + m * p.ldy + n;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (i < rows) store_f32(y + i * step * p.ldy, v[i]);
   } else {
-    activate(v, p.act);
+    activate<false>(v, p.act);
     const int lane = threadIdx.x & 31;
     constexpr int B = kBlock<FMT>;
     const int n0 = n - lane, b = n / B, tiles = tiles_per_row(FMT, p.N);

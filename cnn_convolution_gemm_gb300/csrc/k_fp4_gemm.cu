@@ -183,7 +183,7 @@ __device__ __forceinline__ void finish_float(const GemmParams& p, const CUtensor
     }
     __syncwarp();
   }
-  activate(v, p.act);
+  activate<B::ES == 4>(v, p.act);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     uint32_t w[4];
@@ -644,7 +644,7 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR, YIO>::THREADS, 1)
                 fetch_res(m0, n0 + PC);
             });
           } else {
-            activate(v, p.act);
+            activate<false>(v, p.act);
             uint32_t c[4], b;
             quantize32<FMT>(p.y_scale, v, p.N - n0, c, b);
 #pragma unroll

@@ -195,3 +195,9 @@ def check_quantized(t, y, err, fmt, g):
     assert (-away <= below * s + slack).all()
     wrong = (np.sign(v) * np.sign(yb) < 0) & (np.abs(v) > 0) & (np.abs(yb) > slack)
     assert not wrong.any()
+
+
+def half_spacing(v, dt):
+    """The most that one rounding to dt moves a value of up to this magnitude: half the distance of
+    its neighbours, of 8 or 24 significant bits."""
+    return np.ldexp(1.0, np.frexp(v + 1e-37)[1] - {"bfloat16": 9, "float32": 25}[dt])

@@ -505,3 +505,86 @@ def test_graphs_keep_their_workspaces(what):
     for out in outs:
         assert torch.equal(out, want)
     assert all(bool((t == 0x5A).all()) for t in taken)
+
+
+def _activation_case(act, M, K, y_dtype, fmt, bound):
+    """act of known values, which a product of zeros takes from its bias: outputs within bound(v,
+    result) of the result (and 1e-35, where fp32 cannot hold it in full), then rounded to y's type.
+    Infinities and NaN give what the definition's arithmetic gives, in their columns alone (4
+    bits: a NaN scale for their block)."""
+    torch, fp4 = _fp4()
+    rng = np.random.default_rng(act)
+    C, n = 64, K - 64
+    v = np.concatenate([np.linspace(-14, 14, n - n // 4), -np.exp(rng.uniform(-20, 5, n // 8)),
+                        np.exp(rng.uniform(-20, 5, n // 4 - n // 8)), np.zeros(64)]).astype(np.float32)
+    special = np.array([np.inf, -np.inf, np.nan, -np.nan, 3e38, -3e38, 0.0, -0.0], np.float32)
+    v[n + 5:n + 13] = special
+    if y_dtype is None:
+        v[n:] = np.where(np.isfinite(v[n:]), v[n:], 0)  # a second run has them
+    layer = fp4.Fp4Linear(C, K, fmt, y_dtype=getattr(torch, y_dtype) if y_dtype else None, act=act)
+    layer.prepack(_to(torch, rng.standard_normal((K, C)), torch.bfloat16))
+    x = torch.zeros(M, C, dtype=torch.bfloat16, device="cuda")
+    y = layer(x, bias=torch.from_numpy(v).cuda())
+    _sync(torch)
+    d = v.astype(np.float64)
+    with np.errstate(all="ignore"):
+        if act == R.B.CONV_ACT_GELU:
+            from scipy.special import ndtr
+            want = d * ndtr(d)
+        elif act == R.B.CONV_ACT_SILU:
+            want = d / (1 + np.exp(-d))
+        else:
+            want = R.activate(d, act)
+        err = bound(np.clip(d, -1e3, 1e3), np.abs(want)) + 1e-35
+    if y_dtype is None:
+        keep = slice(0, min(M, 130))
+        part = fp4.Fp4Tensor(y.rows, K, fmt, 1.0, y.codes, y.scales)
+        R.check_quantized(part, np.tile(want, (M, 1)), np.tile(err, (M, 1)), fmt, 1.0)
+        v[n + 5:n + 8] = special[:3]
+        bad = layer(x, bias=torch.from_numpy(v).cuda())
+        _sync(torch)
+        code, byte = R.unpack(bad)
+        code0, byte0 = R.unpack(y)
+        b, nan = R.BLOCK[fmt], 0xFF if fmt == R.MX else 0x7F
+        blocks = n // b  # of the values before the special ones
+        np.testing.assert_array_equal(byte[:, :blocks], byte0[:, :blocks])
+        np.testing.assert_array_equal(code[:, :n], code0[:, :n])
+        # relu6 leaves the first infinity finite; a NaN stays
+        assert (byte[keep, blocks] == nan).all() and not code[:, n:n + b].any()
+        return
+    got = y.double().cpu().numpy()
+    odd = ~np.isfinite(want)
+    np.testing.assert_array_equal(got[:, odd], np.tile(want[odd], (M, 1)))
+    off = np.abs(got[:, ~odd] - want[~odd])
+    limit = err[~odd] + R.half_spacing(np.abs(want[~odd]) + err[~odd], y_dtype)
+    assert (off <= limit).all(), (off / limit).max()
+
+
+# one row, the tiles of both sizes
+ACT_SHAPES = [(3, 1088), (130, 1088), (2600, 2112)]
+
+
+def _gelu_bound(v, want, y_dtype):
+    """fp32 outputs, in units of 2^-23 of the result: the polynomial 1, that evaluated 4,
+    1 / (1 + p |x|) and how the polynomial goes with it 4, the exponential 2 and its argument's
+    rounding 0.6 x^2, products 2.  Others: 4.2e-7 (0.75e-7 of Phi from the polynomial, the rest
+    roundings), and what the polynomial is off by relatively above -3 and -5."""
+    if y_dtype == "float32":
+        return want * (v * v + 14) * 2.0 ** -23
+    rel = np.where(v > -3, 6e-5, np.where(v > -5, 2e-3, np.inf))
+    with np.errstate(invalid="ignore"):
+        return np.fmin(4.2e-7, np.where(np.isinf(rel), np.inf, want * np.where(np.isinf(rel), 0, rel)))
+
+
+@pytest.mark.parametrize("fmt", FMTS, ids=NAMES.get)
+@pytest.mark.parametrize("y_dtype", ["float32", "bfloat16", None])
+@pytest.mark.parametrize("M,K", ACT_SHAPES)
+def test_gelu_values(M, K, y_dtype, fmt):
+    _activation_case(R.B.CONV_ACT_GELU, M, K, y_dtype, fmt, lambda v, w: _gelu_bound(v, w, y_dtype))
+
+
+@pytest.mark.parametrize("act", [R.B.CONV_ACT_NONE, R.B.CONV_ACT_RELU, R.B.CONV_ACT_RELU6])
+@pytest.mark.parametrize("y_dtype", ["float32", "bfloat16", None])
+@pytest.mark.parametrize("M,K", ACT_SHAPES)
+def test_exact_activations_values(M, K, y_dtype, act):
+    _activation_case(act, M, K, y_dtype, R.NV, lambda v, w: 0.0 * v)

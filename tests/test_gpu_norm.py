@@ -337,12 +337,6 @@ def test_residual_block_after_strided_calls_of_its_parts():
     assert all(torch.equal(a.view(torch.int16), b.view(torch.int16)) for a, b in zip(got, want))
 
 
-def _half_spacing(v, dt):
-    """The most that one rounding to dt moves a value of up to this magnitude: half the distance of
-    its neighbours, of 8 or 24 significant bits."""
-    return np.ldexp(1.0, np.frexp(v + 1e-37)[1] - {"bfloat16": 9, "float32": 25}[dt])
-
-
 def _block_behind_its_codes(dt, fmt, rows, C, hidden, gate_rows, strided=False):
     """x' and h' of a block against 64 bits over the 4-bit t that its own first layer gives, so
     that no code can fall to another side: z within the product's bound, whose share reaches u
@@ -389,7 +383,7 @@ def _block_behind_its_codes(dt, fmt, rows, C, hidden, gate_rows, strided=False):
     want_h, h_err = normed(want, err, n64(w[2]))
     for got, v, e in ((xo, want, err), (h, want_h, h_err)):
         off = np.abs(n64(got) - v)
-        assert (off <= e + _half_spacing(np.abs(v) + e, dt)).all()
+        assert (off <= e + R.half_spacing(np.abs(v) + e, dt)).all()
 
 
 @pytest.mark.parametrize("fmt", [R.MX, R.NV])
@@ -457,4 +451,4 @@ def test_z_in_another_type(post, pre, rows, C, kw):
         return
     assert h.dtype is torch.bfloat16
     off = np.abs(h.double().cpu().numpy() - want)
-    assert (off <= err + _half_spacing(np.abs(want) + err, "bfloat16")).all()
+    assert (off <= err + R.half_spacing(np.abs(want) + err, "bfloat16")).all()
