@@ -511,6 +511,13 @@ __device__ __forceinline__ void gelu2(float& x0, float& x1) {
   unpack2(fma2(a, q, pack2(max_nan(x0, 0.0f), max_nan(x1, 0.0f))), x0, x1);
 }
 
+// 1 / (1 + exp(-v)), 0 below about -87.  FP32: within 2^-21 of its value.  Else the rounding of
+// v log2 e enters, and it is within (|v| + 8) 2^-23, as outputs of 16 and 4 bits need it.
+template <bool FP32>
+__device__ __forceinline__ float logistic(float v) {
+  return rcp_approx(1.0f + (FP32 ? expf(-v) : ex2_approx(v * -1.4426950408889634f)));
+}
+
 // The epilogue's activation over N values.  FP32: for an fp32 output.  SiLU: x / (1 + exp(-x))
 // (exp overflows to infinity for very negative x, the quotient is then -0).  Comparisons keep a
 // NaN; GELU and SiLU of -inf are one (inf * 0).
@@ -527,8 +534,7 @@ __device__ __forceinline__ void activate(float (&v)[N], int act) {
     for (int i = 0; i < N; i += 2) gelu2<FP32>(v[i], v[i + 1]);
   } else if (act == CONV_ACT_SILU) {
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-      v[i] = v[i] * rcp_approx(1.0f + ex2_approx(v[i] * -1.4426950408889634f));
+    for (int i = 0; i < N; ++i) v[i] *= logistic<FP32>(v[i]);
   }
 }
 

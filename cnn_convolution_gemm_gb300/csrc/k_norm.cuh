@@ -332,6 +332,7 @@ __global__ void __launch_bounds__(T <= 32 ? 128 : T, least_blocks(T, N, LAY, AHE
   extern __shared__ uint4 ring[];  // RING x R x (a row of z, a row of x); weights
   gb::allow_dependents();
   const int C = a.C;
+  constexpr bool FP32 = sizeof(TX) == 4 || sizeof(TG) == 4;  // outputs of 32 bits
   constexpr int AT_ONCE = T <= 32 ? 128 / T : R;  // rows of a block
   const int t = T <= 32 ? (int)threadIdx.x & (T - 1) : (int)threadIdx.x;
   const long long step = (long long)gridDim.x * AT_ONCE;
@@ -435,9 +436,7 @@ __global__ void __launch_bounds__(T <= 32 ? 128 : T, least_blocks(T, N, LAY, AHE
           rg[k].get(v[k]);
 #pragma unroll
           for (int i = 0; i < N; ++i) {
-            // the logistic function within 2^-21
-            if (a.gate_kind == CONV_GATE_SIGMOID)
-              v[k][i] = rcp_approx(1.0f + ex2_approx(v[k][i] * -1.4426950408889634f));
+            if (a.gate_kind == CONV_GATE_SIGMOID) v[k][i] = logistic<FP32>(v[k][i]);
             u[k][i] *= v[k][i];
           }
         }

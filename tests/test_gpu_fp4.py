@@ -588,3 +588,13 @@ def test_gelu_values(M, K, y_dtype, fmt):
 @pytest.mark.parametrize("M,K", ACT_SHAPES)
 def test_exact_activations_values(M, K, y_dtype, act):
     _activation_case(act, M, K, y_dtype, R.NV, lambda v, w: 0.0 * v)
+
+
+@pytest.mark.parametrize("fmt", FMTS, ids=NAMES.get)
+@pytest.mark.parametrize("y_dtype", ["float32", "bfloat16", None])
+@pytest.mark.parametrize("M,K", ACT_SHAPES)
+def test_silu_values(M, K, y_dtype, fmt):
+    """In units of 2^-23 of the result.  fp32 outputs: exp 2, 1 + exp and the product 0.5 each,
+    the reciprocal 1.  Others: exp2 2 and its argument's rounding 0.75 |x| instead."""
+    exp = (lambda v: 2.0) if y_dtype == "float32" else (lambda v: 2 + 0.75 * np.abs(v))
+    _activation_case(R.B.CONV_ACT_SILU, M, K, y_dtype, fmt, lambda v, w: w * (exp(v) + 2) * 2.0 ** -23)

@@ -452,3 +452,25 @@ def test_z_in_another_type(post, pre, rows, C, kw):
     assert h.dtype is torch.bfloat16
     off = np.abs(h.double().cpu().numpy() - want)
     assert (off <= err + R.half_spacing(np.abs(want) + err, "bfloat16")).all()
+
+
+@pytest.mark.parametrize("dt,zdt,hdt", [("float32", "float32", None), ("float32", "bfloat16", None),
+                                        ("bfloat16", "float32", None), ("bfloat16", "bfloat16", None),
+                                        ("bfloat16", "float32", "bfloat16")])
+@pytest.mark.parametrize("C", [96, 257, 1024])
+def test_sigmoid_gates_keep_their_digits(dt, zdt, hdt, C):
+    """Gates down to -80, where the sigmoid is exp(-80), against u so large that x' shows them:
+    x' = u * sigmoid.  In units of 2^-23: exp 2 (its argument's rounding 0.75 |x| where every
+    output has 16 bits), 1 + exp 0.5, the reciprocal 1, products 1.5; then one rounding."""
+    torch, ResidualNorm = _norm()
+    gd = getattr(torch, hdt or zdt)
+    gate = torch.linspace(-80, 20, 5 * C).view(5, C).to(gd).cuda()
+    z = torch.full((5, C), 2.0 ** 60, device="cuda").to(getattr(torch, zdt))
+    x = torch.zeros(5, C, device="cuda").to(getattr(torch, dt))
+    xo, _ = ResidualNorm(C, x.dtype, z.dtype, gate=B.CONV_GATE_SIGMOID, h_dtype=gd)(x, z, gate=gate)
+    B.conv_sync_status(torch.cuda.current_stream().cuda_stream)
+    g = gate.double().cpu().numpy()
+    want = 2.0 ** 60 / (1 + np.exp(-g))
+    exact = dt == "float32" or (hdt or zdt) == "float32"
+    err = want * (5 + (0 if exact else 0.75 * np.abs(g))) * 2.0 ** -23
+    assert (np.abs(xo.double().cpu().numpy() - want) <= err + R.half_spacing(want + err, dt)).all()
