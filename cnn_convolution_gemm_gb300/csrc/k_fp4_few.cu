@@ -27,6 +27,8 @@ using namespace gb::fp4;
 
 constexpr int THREADS = 256;
 constexpr int STAGES = 4;
+constexpr int QUANT_WARPS = 4;  // that quantise a floating x, two rows each at a time
+static_assert(FUSED_ROWS <= 2 * QUANT_WARPS, "rows past them would never be quantised");
 constexpr int TMEM_COLS = 256;  // up to 128 of accumulator, 4 x 32 of scales
 
 template <int FMT>
@@ -46,7 +48,7 @@ struct FewParams {
   int M, N, KR, nt;      // rows, outputs, reduction; rows rounded up to 8
   int ksteps, kmmas_last;
   int split_log2;        // CTAs of a cluster
-  int warps_log2;        // FUSED: warps that quantise a k-step, two rows each
+  int warps_log2;        // FUSED: warps that quantise a k-step, up to QUANT_WARPS
   int act;
   float alpha;
   TensorScale x_scale, y_scale;
@@ -259,6 +261,7 @@ __global__ void __launch_bounds__(THREADS)
       // rows; warps that are left over take other k-steps.  The next k-step's loads go out
       // before this one's arithmetic.
       using T = std::conditional_t<XIO == CONV_FP4_IO_BF16, __nv_bfloat16, float>;
+      static_assert(QUANT_WARPS == 1 << 2 && QUANT_WARPS == THREADS / 32 - 4, "warps 4 and up");
       const int w = warp - 4, groups_log2 = 2 - p.warps_log2;
       const int r = (w & ((1 << p.warps_log2) - 1)) * 2 + (lane >> 4), gc = lane & 15;
       const T* const x = static_cast<const T*>(p.x) + (r < p.M ? r * p.ldx : 0);
@@ -389,7 +392,8 @@ cudaError_t launch_t(const Fp4Gemm& g, cudaStream_t st) {
          p.ksteps >> (p.split_log2 + 2))
     ++p.split_log2;
   const int split = 1 << p.split_log2;
-  p.warps_log2 = g.M <= 2 ? 0 : g.M <= 4 ? 1 : 2;
+  p.warps_log2 = 0;
+  while ((1 << p.warps_log2) < QUANT_WARPS && (2 << p.warps_log2) < g.M) ++p.warps_log2;
   CUtensorMap tw, tws, tx, txs;
   if (!codes_map(&tw, g.w, g.K, g.C, 128) ||
       !scales_map(&tws, g.ws, FMT, g.K, g.C, C::ATOMS, 1))
