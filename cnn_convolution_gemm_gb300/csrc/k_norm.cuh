@@ -382,7 +382,8 @@ __global__ void __launch_bounds__(T <= 32 ? 128 : T, least_blocks(T, N, LAY, AHE
   int turn = 0, stage = 0;
   uint32_t phase = 0;
   bool ok = true;  // after a wait that ran out nothing is waited for again (the rows are
-                   // then wrong, and the error word says so); the barriers stay in step
+                   // then wrong, and the error word says so); the barriers stay in step, and
+                   // stage and phase those of the copies that are still on their way
   // without the ring: the next row's z and x are on their way from the moment on that
   // their registers are free (12544 x 1001 fp32 40 -> 38 us, 14552 x 2579 146 -> 134; rows
   // above 8192 have none to spare: 2656 x 12544 fp32 176, so 214)
@@ -475,7 +476,7 @@ __global__ void __launch_bounds__(T <= 32 ? 128 : T, least_blocks(T, N, LAY, AHE
       // every thread has read the rows before a barrier: norm_pre's, or this one
       if (a.pre == CONV_NORM_NONE) __syncthreads();
       if (t == 0 && ok && r + RING * step < a.rows) fetch(r + RING * step, stage);
-      if (++stage == RING) {
+      if (ok && ++stage == RING) {
         stage = 0;
         phase ^= 1;
       }
