@@ -474,3 +474,12 @@ def test_sigmoid_gates_keep_their_digits(dt, zdt, hdt, C):
     exact = dt == "float32" or (hdt or zdt) == "float32"
     err = want * (5 + (0 if exact else 0.75 * np.abs(g))) * 2.0 ** -23
     assert (np.abs(xo.double().cpu().numpy() - want) <= err + R.half_spacing(want + err, dt)).all()
+
+
+@pytest.mark.parametrize("h_fmt", [R.MX, R.NV])
+@pytest.mark.parametrize("rows,C", [(1, 9001), (3, 16383), (2, 20001), (2, 32767), (400, 9999)])
+def test_quantized_output_of_wide_odd_rows(h_fmt, rows, C):
+    """Rows above 8192 channels at addresses that allow no vector accesses, into 4 bits."""
+    _case(RMS, RMS, rows, C, h_fmt=h_fmt)
+    _case(LN, LN, rows, C, dt="float32", zdt="bfloat16", h_fmt=h_fmt, gate=2)
+    _case(N, LN, rows, C, dt="float32", h_fmt=h_fmt, with_z=False)
