@@ -84,8 +84,9 @@ def rows_of(t: torch.Tensor, cols: int, what: str):
 
 
 class Fp4Tensor:
-    """A 4-bit matrix [rows][cols]: codes, scales (tiled, as conv_fp4_size says), tensor
-    scale.  The tensors stay the ones it was made with (their addresses are kept)."""
+    """A 4-bit matrix [rows][cols]: codes, scales (tiled, as conv_fp4_size says; contiguous
+    uint8, of its bytes or more), tensor scale.  The tensors stay the ones it was made with
+    (their addresses are kept)."""
 
     __slots__ = ("rows", "cols", "fmt", "tensor_scale", "codes", "scales", "shape", "codes_ptr",
                  "scales_ptr", "device", "index")
@@ -93,6 +94,11 @@ class Fp4Tensor:
     def __init__(self, rows, cols, fmt, tensor_scale, codes, scales):
         if scales.get_device() != codes.get_device():
             raise ValueError("codes and scales: on different devices")
+        if (codes.dtype is not torch.uint8 or scales.dtype is not torch.uint8
+                or not codes.is_contiguous() or not scales.is_contiguous()
+                or codes.numel() < rows * 16 * -(-cols // 32)
+                or scales.numel() < -(-rows // 128) * -(-cols // (4 * BLOCK[fmt])) * 512):
+            raise ValueError("codes, scales: expected contiguous uint8 of conv_fp4_size's bytes")
         self.rows, self.cols, self.fmt, self.tensor_scale = rows, cols, fmt, tensor_scale
         self.codes, self.scales = codes, scales
         self.shape = (rows, cols, fmt)

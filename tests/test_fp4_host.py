@@ -489,3 +489,20 @@ def test_type_of_z_alone(B):
     refused(B, BAD, B.conv_fp4_block_create, n_in, fc1, fc2, n_out)
     f(n_out, B.CONV_F32)
     B.conv_fp4_block_destroy(B.conv_fp4_block_create(n_in, fc1, fc2, n_out))
+
+
+@pytest.mark.parametrize("rows,cols", [(1, 1), (4, 64), (129, 65), (128, 4097), (0, 7)])
+def test_fp4_tensors_have_their_bytes(B, rows, cols):
+    torch = pytest.importorskip("torch")
+    from cnn_convolution_gemm_gb300 import fp4
+    for fmt in (B.CONV_FP4_MX, B.CONV_FP4_NV):
+        cb, sb = B.conv_fp4_size(fmt, rows, cols)
+        u8 = lambda n: torch.zeros(n, dtype=torch.uint8)  # noqa: E731
+        t = fp4.Fp4Tensor(rows, cols, fmt, 1.0, u8(cb), u8(sb))
+        assert t.shape == (rows, cols, fmt)
+        fp4.Fp4Tensor(rows, cols, fmt, 1.0, u8(cb + 16), u8(sb + 16))
+        bad = [(u8(2 * cb)[::2], u8(sb)), (u8(cb), u8(2 * sb)[::2]), (u8(cb).view(torch.int8), u8(sb)),
+               (u8(cb - 1), u8(sb)), (u8(cb), u8(sb - 1))] if rows else []
+        for codes, scales in bad:
+            with pytest.raises(ValueError):
+                fp4.Fp4Tensor(rows, cols, fmt, 1.0, codes, scales)
