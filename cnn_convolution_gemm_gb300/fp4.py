@@ -12,7 +12,15 @@ import torch
 
 from . import binding as B
 
-CONV_DTYPE = {torch.bfloat16: B.CONV_BF16, torch.float32: B.CONV_F32}
+
+class Types(dict):
+    def __missing__(self, t):
+        raise ValueError(f"{t}: expected {', '.join(map(str, self))}")
+
+
+CONV_DTYPE = Types({torch.bfloat16: B.CONV_BF16, torch.float32: B.CONV_F32})
+IO = Types({torch.bfloat16: B.CONV_FP4_IO_BF16, torch.float32: B.CONV_FP4_IO_F32,
+            None: B.CONV_FP4_IO_CODES})
 BLOCK = {B.CONV_FP4_MX: 32, B.CONV_FP4_NV: 16}
 
 
@@ -167,9 +175,7 @@ class Fp4Linear:
         self.C, self.K, self.fmt = C, K, fmt
         self.x_dtype, self.y_dtype = x_dtype, y_dtype
         self.x_scale, self.y_scale = x_scale, y_scale
-        io = {torch.bfloat16: B.CONV_FP4_IO_BF16, torch.float32: B.CONV_FP4_IO_F32,
-              None: B.CONV_FP4_IO_CODES}
-        self.desc = B.conv_fp4_create(fmt, C, K, io[x_dtype], io[y_dtype])
+        self.desc = B.conv_fp4_create(fmt, C, K, IO[x_dtype], IO[y_dtype])
         B.conv_fp4_set_epilogue(self.desc, act, has_residual)
         B.conv_fp4_set_tensor_scales(self.desc, x_scale, 1.0, y_scale)  # w's: with the weights
         self.w = None

@@ -506,3 +506,18 @@ def test_fp4_tensors_have_their_bytes(B, rows, cols):
         for codes, scales in bad:
             with pytest.raises(ValueError):
                 fp4.Fp4Tensor(rows, cols, fmt, 1.0, codes, scales)
+
+
+def test_other_types_are_refused(host_layers):
+    torch, fp4, up, calls, _ = host_layers
+    from cnn_convolution_gemm_gb300 import binding as B
+    from cnn_convolution_gemm_gb300.norm import ResidualNorm
+    half = torch.float16
+    t = fp4.empty(4, 64, B.CONV_FP4_MX, "cpu")
+    for call in (lambda: fp4.quantize(up(torch.zeros(4, 64, dtype=half)), B.CONV_FP4_MX),
+                 lambda: fp4.dequantize(t, half), lambda: fp4.Fp4Linear(64, 32, x_dtype=half),
+                 lambda: fp4.Fp4Linear(64, 32, y_dtype=half), lambda: ResidualNorm(64, half),
+                 lambda: ResidualNorm(64, z_dtype=half), lambda: ResidualNorm(64, h_dtype=half)):
+        with pytest.raises(ValueError):
+            call()
+    assert not calls
