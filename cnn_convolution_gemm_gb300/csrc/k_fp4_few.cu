@@ -1,9 +1,9 @@
 // Product of microscaled 4-bit matrices for few rows of X (one token to a small batch):
 // y^T = W X^T, so that the tensor core's 128 rows are outputs and its N the few rows.
 //
-// Bound by the weights' bytes and by latency (one token through 4096 x 4096: 4.0 us with
+// Bound by the weights' bytes and by latency (one token through 4096 x 4096: 4.2 us with
 // the weights in L2, 4.3 from HBM, whose bytes take 1.3; through 4096 -> 16384 8.4 from
-// HBM, bytes 5.3; 32 rows through 8192 x 2048 5.3 us): a CTA streams 128 rows of W over a range of
+// HBM, bytes 5.3; 32 rows through 8192 x 2048 5.5 us): a CTA streams 128 rows of W over a range of
 // the reduction; the ranges of one tile are the CTAs of a cluster (up to 8), which
 // add their partial sums through distributed shared memory in a fixed order.  Up to
 // FUSED_ROWS rows of floating x are quantised on the way in, k-step by k-step, by

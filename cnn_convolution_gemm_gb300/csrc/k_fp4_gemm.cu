@@ -9,9 +9,11 @@
 // Bound: shared memory.  A k-step of a 256 x 256 tile over an SM pair takes 513 cycles of
 // MMAs (K = 64 each, measured alone); its 35 KB of operands (MX; NV 38 KB) are written by
 // the TMA and read by the MMAs and scale copies at 128 bytes a cycle together: 547 (594).
-// An MMA with K = 96 would not change that, which is why there is none here.  Measured:
-// 8192 x 16384 x 4096 133 us MX, 140 NV (8.3, 7.9 PFLOP/s) at 2.07 GHz; under a long dense
-// load the power limit lowers the clock to about 1.75 GHz.
+// An MMA with K = 96 would not change that, which is why there is none here.  Beside the
+// loop a tile takes 900 to 4000 cycles (one accumulator of 256 columns, which the epilogue has
+// to read first; staged stores through the same shared memory).  Measured, rows x inputs x
+// outputs: 8192 x 16384 x 4096 139 to 143 us MX, 152 to 154 NV (7.7 to 7.9, 7.1 to 7.3
+// PFLOP/s); after two seconds of it, at the 1.71 and 1.64 GHz of the power limit, 152 and 166.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -587,7 +589,7 @@ __global__ void __launch_bounds__(Cfg<FMT, BN, PAIR, YIO>::THREADS, 1)
         const int block = warp - 4, slots = (C::EPI_WARPS + p.split - 1) / p.split;
         const int owner = block % p.split, slot = block / p.split;
         // [range][slot][column][row]: a warp's store is 128 bytes in one piece (as 16-byte
-        // pieces of rows 65 x 8192 x 2048 took 9.0 us, so 8.2)
+        // pieces of rows 65 x 8192 x 2048 took 9.0 us, so 8.2 then, 7.6 now)
         float* const sums = reinterpret_cast<float*>(smem);
         static_assert(C::STAGES * C::STAGE_BYTES >= (16 + SPLIT_MOST - 1) * 4096, "sums");
         __syncwarp();
@@ -767,7 +769,7 @@ cudaError_t launch_tile(const Fp4Gemm& g, int split, cudaStream_t st) {
 }
 
 // CTAs that share a tile: as many as all tiles' clusters find room for at once (more, and
-// they run one after another: 65 x 8192 x 2048 by 8 14.6 us, by 4 8.2), if they save 14
+// they run one after another: 65 x 8192 x 2048 by 8 14.6 us, by 4 7.6), if they save 14
 // k-steps (0.2 us each); the exchange costs 2.5 us.
 template <int FMT, int YIO>
 int split_of(const Fp4Gemm& g, long long tiles) {

@@ -6,9 +6,9 @@
 // variance's digits).  Blocks that take many rows fetch x and z two rows ahead into shared
 // memory (bulk copies); otherwise a row's loads are issued together, past L1, so that the
 // weights stay there.  Measured: 32768 x 8192 bf16 325 us (6.6 TB/s), 12544 x 1001 fp32
-// with gates 40 us (5.0 TB/s; single elements), 26400 x 256 bf16 with gates 10, one row of
-// 4096 3.3 us.
-// One translation unit per pair of types includes this file.
+// with gates 40 us (5.0 TB/s; single elements), 26400 x 256 bf16 with gates 10, 8192 x 4096 bf16
+// with fp32 z 66 (5.1 TB/s), one row of 4096 3.1 us.
+// One translation unit per set of types includes this file.
 #pragma once
 
 #include <cuda_runtime.h>

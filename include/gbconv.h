@@ -63,7 +63,7 @@ typedef enum { CONV_BF16 = 0, CONV_F32 = 1, CONV_INT8 = 2 } conv_dtype_t;
  * multiples of 32; weights stay [K][R][S][C]. */
 typedef enum { CONV_NHWC = 0, CONV_NCHW = 1, CONV_NC32HW32 = 2 } conv_layout_t;
 
-/* GELU (x Phi(x), through erf) and SILU (x / (1 + exp(-x))): conv_fp4_* only. */
+/* GELU (x Phi(x)) and SILU (x / (1 + exp(-x))): conv_fp4_* only; NaN for -inf (inf * 0). */
 typedef enum {
   CONV_ACT_NONE = 0,
   CONV_ACT_RELU = 1,
