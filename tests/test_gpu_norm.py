@@ -483,3 +483,39 @@ def test_quantized_output_of_wide_odd_rows(h_fmt, rows, C):
     _case(RMS, RMS, rows, C, h_fmt=h_fmt)
     _case(LN, LN, rows, C, dt="float32", zdt="bfloat16", h_fmt=h_fmt, gate=2)
     _case(N, LN, rows, C, dt="float32", h_fmt=h_fmt, with_z=False)
+
+
+def test_threads_share_layers_and_blocks():
+    """Two threads on one stream, whose tensors have other row strides and numbers of rows: every
+    result is the one that a single thread gets, bit for bit.  And blocks of no rows."""
+    import threading
+    torch = need_gpu()
+    from cnn_convolution_gemm_gb300 import fp4
+    from cnn_convolution_gemm_gb300.norm import ResidualNorm
+    from cnn_convolution_gemm_gb300.residual_block import Fp4ResidualBlock
+    torch.manual_seed(7)
+    C, K = 160, 288
+    rand = lambda *s: torch.randn(*s, device="cuda").bfloat16()  # noqa: E731
+    layer, norm, blk = fp4.Fp4Linear(C, K, R.NV, x_scale=0.004), ResidualNorm(C, pre=LN), Fp4ResidualBlock(C, K)
+    layer.prepack(rand(K, C), 0.01)
+    blk.prepack(rand(K, C), rand(C, K))
+    xs = [rand(40, C), rand(75, C + 24)[:, 8:8 + C]]
+    calls = [layer, lambda x: norm(x)[1], lambda x: blk(x)[1], lambda x: blk.norm_in(x)[1].codes]
+    want = [[f(x).clone() for f in calls] for x in xs]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        for _ in range(100):
+            for f, w in zip(calls, want[i]):
+                if not torch.equal(f(xs[i]), w):
+                    wrong.append(i)
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    B.conv_sync_status(torch.cuda.current_stream().cuda_stream)
+    assert not wrong
+    x, h = blk(xs[0][:0])
+    assert x.shape == h.shape == (0, C)
