@@ -1,0 +1,462 @@
+"""Cases and plain forms of the library's 8-bit and integer 4-bit language-model operators.
+
+What serves a transformer whose weights are held in 4 bits as whole numbers:
+
+quantize  8-bit matrices: the codes of a row, or of each 128 consecutive columns of it, share one
+          fp32 scale s = max(max |x| / T, 2^-100), T = 448 (E4M3) or 127 (whole numbers); a code
+          is the value nearest to x / s, ties to the even one.  Measured with the way back.
+norm      x' = x + z;  h = x' / sqrt(mean(x'^2) + eps) * w in such 8 bits (returned as the values
+          that its codes stand for).
+linear    y = act(X W^T + bias + residual) with W[k][c] = (code - zero) * scale: codes 0 .. 15,
+          zero and scale for each `group` consecutive inputs of an output; X in bf16, fp32 or 8 bits.
+mlp       the path: x' = x + z; h = Q(norm(x')); t = silu(h W1^T + b1); y = x' + Q(t) W2^T + b2.
+
+``run`` computes them from elementary operations in 32 bits (quotients that decide a code in 64),
+or calls the library where ``own``.
+"""
+import math
+
+import torch
+
+own = False  # True: run() calls the library's operators
+
+EPS = 1e-6
+TOP = {"e4m3": 448.0, "int8": 127.0}
+LEAST = 2.0 ** -100
+DTYPE = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+# ---- cases -------------------------------------------------------------------
+
+
+def listed():
+    return [
+        # one token's hidden layer and back: only latency
+        quantize_case("e4m3", 0, 1, 16384, "f32", name="quantize_row_e4m3"),
+        # a long prompt's activations: memory rate
+        quantize_case("int8", 128, 16384, 8192, "bf16", name="quantize_large_int8"),
+        # one token between two blocks
+        norm_case("e4m3", 128, 1, 4096, "bf16", name="norm_token"),
+        # an fp32 stream of odd width: rows at any 4-byte address
+        norm_case("int8", 0, 777, 1001, "f32", name="norm_odd"),
+        # a long prompt's residual stream
+        norm_case("e4m3", 0, 16384, 8192, "bf16", name="norm_prompt"),
+        # one token through a square projection: latency, then the weights' bytes
+        linear_case(1, 4096, 4096, "bf16", "bf16", 128, True, "bf16", "none", True, False,
+                    name="linear_token"),
+        # one token through a wide projection, weights larger than L2: their bytes
+        linear_case(1, 8192, 32768, "e4m3", "bf16", 128, True, "bf16", "none", False, False,
+                    name="linear_token_wide"),
+        # a few sequences, everything ragged, all of it fp32, small groups without zeros
+        linear_case(13, 1456, 1111, "f32", "f32", 32, False, "f32", "relu", True, True,
+                    name="linear_ragged"),
+        # a batch of 64 sequences decoding
+        linear_case(64, 8192, 8192, "bf16", "bf16", 64, True, "bf16", "none", True, True,
+                    name="linear_batch"),
+        # a prompt's expanding projection with its activation, x from a norm with scales per 128
+        linear_case(4096, 4096, 16384, "e4m3", "bf16", 128, True, "bf16", "silu", True, False,
+                    x_group=128, name="linear_prompt"),
+        # the path for one token
+        mlp_case("e4m3", 0, 1, 4096, 16384, 128, name="mlp_token"),
+        # the path for a prompt
+        mlp_case("int8", 128, 1024, 4096, 16384, 128, name="mlp_prompt"),
+    ]
+
+
+def quantize_case(fmt, x_group, m, k, x, **more):
+    return {"op": "quantize", "fmt": fmt, "x_group": x_group, "m": m, "k": k, "x": x, **more}
+
+
+def norm_case(fmt, x_group, m, c, x, **more):
+    return {"op": "norm", "fmt": fmt, "x_group": x_group, "m": m, "c": c, "x": x, **more}
+
+
+def linear_case(m, c, k, x, y, group, zeros, scale, act, bias, residual, x_group=0, **more):
+    """x: bf16, f32, or an 8-bit format with scales per row (x_group 0) or per 128 columns."""
+    return {"op": "linear", "m": m, "c": c, "k": k, "x": x, "x_group": x_group, "y": y,
+            "group": group, "zeros": zeros, "scale": scale, "act": act, "bias": bias,
+            "residual": residual, **more}
+
+
+def mlp_case(fmt, x_group, m, c, hidden, group, **more):
+    return {"op": "mlp", "fmt": fmt, "x_group": x_group, "m": m, "c": c, "hidden": hidden,
+            "group": group, "zeros": True, "scale": "bf16", **more}
+
+
+def _between(rng, lo, hi):
+    """A whole number in [lo, hi], spread over its logarithm; two of three large ones are
+    multiples of 32."""
+    v = int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+    if v >= 64 and rng.random() < 0.67:
+        v = v // 32 * 32
+    return min(max(v, lo), hi)
+
+
+def draw(rng):
+    op = rng.choice(["quantize", "norm", "linear", "linear", "linear", "mlp"])
+    fmt, x_group = rng.choice(["e4m3", "int8"]), rng.choice([0, 128])
+    if op == "quantize":
+        k = _between(rng, 16, 16384)
+        return quantize_case(fmt, x_group, _between(rng, 1, min(32768, (1 << 27) // k)), k,
+                             rng.choice(["bf16", "bf16", "f32"]))
+    if op == "norm":
+        c = _between(rng, 32, 16384)
+        return norm_case(fmt, x_group, _between(rng, 1, min(32768, (1 << 27) // c)), c,
+                         rng.choice(["bf16", "bf16", "f32"]))
+    if op == "linear":
+        c, k = _between(rng, 64, 16384), _between(rng, 32, 32768)
+        rows = min(16384, (1 << 38) // (c * k), (1 << 27) // max(c, k))
+        if rng.random() < 0.6:  # tokens of a few sequences
+            rows = min(rows, 128)
+        x = rng.choice(["bf16", "bf16", "f32", "e4m3", "int8"])
+        return linear_case(_between(rng, 1, rows), c, k, x, rng.choice(["bf16", "bf16", "f32"]),
+                           rng.choice([32, 64, 128, 128, 0]), rng.random() < 0.6,
+                           rng.choice(["bf16", "f32"]), rng.choice(["none", "relu", "gelu", "silu"]),
+                           rng.random() < 0.6, rng.random() < 0.4,
+                           x_group=x_group if x in TOP else 0)
+    c, hidden = _between(rng, 64, 4096), _between(rng, 128, 16384)
+    rows = min(8192, (1 << 37) // (c * hidden))
+    if rng.random() < 0.6:
+        rows = min(rows, 64)
+    return mlp_case(fmt, x_group, _between(rng, 1, rows), c, hidden, rng.choice([32, 64, 128]))
+
+
+_SIZE = {"bf16": 2, "f32": 4, "e4m3": 1, "int8": 1}
+
+
+def _weight_bytes(case, c, k):
+    groups = -(-c // (case["group"] or c))
+    return k * c / 2 + k * groups * (_SIZE[case["scale"]] + 0.5 * case["zeros"])
+
+
+def _scale_bytes(case, m, c):
+    return 4 * m * (-(-c // 128) if case["x_group"] else 1)
+
+
+def work(case):
+    op, m = case["op"], case["m"]
+    if op == "quantize":  # in, codes and scales out and in again, values out
+        return {"bytes": m * case["k"] * (2 * _SIZE[case["x"]] + 2)
+                + 2 * _scale_bytes(case, m, case["k"]), "flops": 4.0 * m * case["k"]}
+    c = case["c"]
+    if op == "norm":  # x, z in; x' out; codes out and in again, values out
+        return {"bytes": m * c * (4 * _SIZE[case["x"]] + 2) + 2 * _scale_bytes(case, m, c) + 4 * c,
+                "flops": 10.0 * m * c}
+    if op == "linear":
+        k = case["k"]
+        moved = _SIZE[case["x"]] * m * c + _SIZE[case["y"]] * m * k * (1 + case["residual"])
+        moved += _scale_bytes(case, m, c) * (case["x"] in TOP) + 4 * k * case["bias"]
+        return {"bytes": moved + _weight_bytes(case, c, k), "flops": 2.0 * m * c * k}
+    h = case["hidden"]  # x, z in; x', y out; the hidden layer need not leave the chip
+    return {"bytes": 4 * 2 * m * c + 4 * (2 * c + h) + _weight_bytes(case, c, h)
+            + _weight_bytes(case, h, c), "flops": 4.0 * m * c * h + 12.0 * m * c}
+
+
+# ---- plain forms ---------------------------------------------------------------
+
+
+def _grouped(v, group):
+    """[m, groups, columns of a group], zeros behind the last column."""
+    m, k = v.shape
+    g = group or k
+    return torch.nn.functional.pad(v, (0, -k % g)).reshape(m, -1, g)
+
+
+def _quantize(x, fmt, group):
+    """Codes' values and scales of x [m, k], both in 64 bits: [m, groups, columns], [m, groups, 1]."""
+    v = _grouped(x.float(), group)
+    s = (v.abs().amax(dim=2, keepdim=True).double() / TOP[fmt]).float().clamp(min=LEAST).double()
+    q = v.double() / s
+    if fmt == "int8":
+        return torch.round(q).clamp(-127, 127), s
+    a = q.abs().clamp(max=448.0)
+    unit = torch.exp2((torch.frexp(a)[1] - 1).clamp(min=-6).double() - 3)
+    return torch.copysign((torch.round(a / unit) * unit).clamp(max=448.0), q), s
+
+
+def _values(q, s, k):
+    return (q * s).reshape(q.shape[0], -1)[:, :k]
+
+
+def _through(x, fmt, group):
+    q, s = _quantize(x, fmt, group)
+    return _values(q, s, x.shape[1])
+
+
+def _codes_of(packed, c):
+    """Two to a byte, the even one in the low half."""
+    return torch.stack([packed & 15, packed >> 4], dim=2).view(packed.shape[0], -1)[:, :c]
+
+
+def _weights(w, group):
+    """What held weights stand for, [k, c] in 32 bits."""
+    codes, scales, zeros, c = w
+    spread = torch.arange(c, device=codes.device) // (group or c)
+    q = _codes_of(codes, c).float() - (8.0 if zeros is None else zeros.float()[:, spread])
+    return q * scales.float()[:, spread]
+
+
+def _act(v, act):
+    if act == "relu":
+        return v.clamp(min=0)
+    if act == "gelu":
+        return 0.5 * v * (1 + torch.erf(v * math.sqrt(0.5)))
+    if act == "silu":
+        return v / (1 + torch.exp(-v))
+    return v
+
+
+def _norm(v, w):
+    return v / torch.sqrt((v * v).mean(dim=1, keepdim=True) + EPS) * w
+
+
+def run(state):
+    return (_run_own if own else _run_plain)(state)
+
+
+def _run_plain(s):
+    c = s["case"]
+    op = c["op"]
+    if op == "quantize":
+        return _through(s["x"], c["fmt"], c["x_group"]).to(s["x"].dtype)
+    if op == "linear":
+        if c["x"] in TOP:
+            x = _values(s["xq"].double(), s["xs"].double().unsqueeze(2), c["c"]).float()
+        else:
+            x = s["x"].float()
+        y = x @ _weights(s["w"], c["group"]).t()
+        y = y if s["bias"] is None else y + s["bias"]
+        y = y if s["residual"] is None else y + s["residual"].float()
+        return _act(y, c["act"]).to(DTYPE[c["y"]])
+    x = s["x"].float() + s["z"].float()
+    h = _through(_norm(x, s["w_norm"]), c["fmt"], c["x_group"])
+    if op == "norm":
+        return [x.to(s["x"].dtype), h.to(s["x"].dtype)]
+    t = _act(h.float() @ _weights(s["w1"], c["group"]).t() + s["b1"], "silu")
+    t = _through(t, c["fmt"], c["x_group"]).float()
+    y = t @ _weights(s["w2"], c["group"]).t() + s["b2"] + x
+    return [x.to(s["x"].dtype), y.to(s["x"].dtype)]
+
+
+# ---- the library's operators ------------------------------------------------------
+
+
+def _run_own(s):
+    from cnn_convolution_gemm_gb300 import q8
+    c = s["case"]
+    op = c["op"]
+    if op == "quantize":
+        q8.quantize(s["x"], s["fmt"], c["x_group"], out=s["held"])
+        return q8.dequantize(s["held"], out=s["y"])
+    if op == "norm":
+        x, h = s["norm"](s["x"], s["z"], x_out=s["x_out"], h_out=s["h"])
+        return [x, q8.dequantize(h, out=s["y"])]
+    if op == "linear":
+        return s["layer"](s["x"], bias=s["bias"], residual=s["residual"], out=s["y"])
+    x, h = s["norm"](s["x"], s["z"], x_out=s["x_out"], h_out=s["h"])
+    t = s["fc1"](h, bias=s["b1"], out=s["t"])
+    q8.quantize(t, s["fmt"], c["x_group"], out=s["held"])
+    return [x, s["fc2"](s["held"], bias=s["b2"], residual=x, out=s["y"])]
+
+
+def _own_handles(s):
+    """The layers and buffers that a program of the library keeps."""
+    from cnn_convolution_gemm_gb300 import binding as B
+    from cnn_convolution_gemm_gb300 import q8
+    from cnn_convolution_gemm_gb300.norm import ResidualNorm
+    from cnn_convolution_gemm_gb300.w4 import W4Linear
+    c = s["case"]
+    op, m = c["op"], c["m"]
+    formats = {"e4m3": B.CONV_Q8_E4M3, "int8": B.CONV_Q8_INT8}
+    acts = {"none": B.CONV_ACT_NONE, "relu": B.CONV_ACT_RELU, "gelu": B.CONV_ACT_GELU,
+            "silu": B.CONV_ACT_SILU}
+    s["fmt"] = formats.get(c.get("fmt"))
+
+    def linear(inputs, outputs, w, x, **more):
+        more["x_q8"] = formats.get(x)
+        layer = W4Linear(inputs, outputs, c["group"], x_dtype=DTYPE.get(x), x_group=c["x_group"],
+                         scale_dtype=DTYPE[c["scale"]], **more)
+        layer.load(*w[:3])
+        return layer
+
+    def empty(cols, dtype):
+        return torch.empty(m, cols, dtype=dtype, device="cuda")
+
+    if op == "quantize":
+        s["held"] = q8.empty(m, c["k"], s["fmt"], "cuda", c["x_group"])
+        s["y"] = torch.empty_like(s["x"])
+    elif op == "linear":
+        if c["x"] in TOP:
+            s["x"] = q8.Q8Tensor(m, c["c"], formats[c["x"]], c["x_group"],
+                                 _held_codes(s["xq"], c["x"], c["c"]), s["xs"].contiguous())
+        s["layer"] = linear(c["c"], c["k"], s["w"], c["x"], y_dtype=DTYPE[c["y"]],
+                            act=acts[c["act"]], has_residual=c["residual"])
+        s["y"] = empty(c["k"], DTYPE[c["y"]])
+    else:
+        dt = s["x"].dtype
+        s["norm"] = ResidualNorm(c["c"], dt, eps=EPS, pre=B.CONV_NORM_RMS, w_pre=s["w_norm"],
+                                 h_q8=s["fmt"], h_group=c["x_group"])
+        s["x_out"], s["y"] = torch.empty_like(s["x"]), torch.empty_like(s["x"])
+        s["h"] = q8.empty(m, c["c"], s["fmt"], "cuda", c["x_group"])
+        if op == "mlp":
+            s["fc1"] = linear(c["c"], c["hidden"], s["w1"], c["fmt"], y_dtype=torch.float32,
+                              act=B.CONV_ACT_SILU)
+            s["fc2"] = linear(c["hidden"], c["c"], s["w2"], c["fmt"], y_dtype=dt,
+                              has_residual=True)
+            s["t"] = empty(c["hidden"], torch.float32)
+            s["held"] = q8.empty(m, c["hidden"], s["fmt"], "cuda", c["x_group"])
+
+
+def _held_codes(q, fmt, k):
+    """Values of codes [m, groups, columns] as the library holds them: a byte each, rows of a
+    multiple of 16 bytes."""
+    q = q.reshape(q.shape[0], -1)[:, :k]
+    q = torch.nn.functional.pad(q, (0, -k % 16))
+    return (q.to(torch.float8_e4m3fn) if fmt == "e4m3" else q.to(torch.int8)).view(torch.uint8)
+
+
+# ---- inputs --------------------------------------------------------------------
+
+
+def _inputs(case, seed):
+    """What the operators read, from the seed alone: normal activations whose channels differ in
+    size, with a few large ones; weights of a usual initialisation, quantised around their zeros."""
+    dev = "cuda"
+    gen = torch.Generator(device=dev)
+    gen.manual_seed(seed)
+
+    def normal(*shape):
+        return torch.randn(*shape, generator=gen, device=dev)
+
+    def activations(m, k, dtype):
+        return (normal(m, k) * torch.exp(0.5 * normal(k))).to(dtype)
+
+    def weights(k, c):
+        """Codes [k, ceil(c / 2)] bytes, scales and zeros [k, groups], inputs."""
+        group = case["group"] or c
+        groups = -(-c // group)
+        scale = (0.2 + 0.4 * torch.rand(k, groups, generator=gen, device=dev)) / math.sqrt(c)
+        zeros = torch.randint(5, 11, (k, groups), generator=gen, device=dev, dtype=torch.uint8)
+        base = zeros.repeat_interleave(group, dim=1)[:, :c].float() if case["zeros"] else 8.0
+        code = torch.round(2.5 * normal(k, c) + base).clamp(0, 15).to(torch.uint8)
+        code = torch.nn.functional.pad(code, (0, c % 2))
+        packed = code[:, 0::2] + 16 * code[:, 1::2]
+        return (packed.contiguous(), scale.to(DTYPE[case["scale"]]),
+                zeros if case["zeros"] else None, c)
+
+    op, m = case["op"], case["m"]
+    s = {"case": dict(case)}
+    if op == "quantize":
+        s["x"] = activations(m, case["k"], DTYPE[case["x"]])
+    elif op == "linear":
+        if case["x"] in TOP:
+            q, scale = _quantize(activations(m, case["c"], torch.float32), case["x"], case["x_group"])
+            s["xq"], s["xs"] = q.float(), scale[:, :, 0].float()
+        else:
+            s["x"] = activations(m, case["c"], DTYPE[case["x"]])
+        s["w"] = weights(case["k"], case["c"])
+        s["bias"] = 0.1 * normal(case["k"]) if case["bias"] else None
+        s["residual"] = normal(m, case["k"]).to(DTYPE[case["y"]]) if case["residual"] else None
+    else:
+        c, dt = case["c"], DTYPE[case.get("x", "bf16")]
+        s |= {"x": 4 * activations(m, c, dt), "z": activations(m, c, dt), "w_norm": 1 + 0.1 * normal(c)}
+        if op == "mlp":
+            h = case["hidden"]
+            s["w1"], s["w2"] = weights(h, c), weights(c, h)
+            s["b1"], s["b2"] = 0.1 * normal(h), 0.1 * normal(c)
+    return s
+
+
+def prepare(case, seed):
+    s = _inputs(case, seed)
+    if own:
+        _own_handles(s)
+    return s
+
+
+# ---- the definitions in 64 bits ---------------------------------------------------
+
+
+def _levels():
+    """The positive E4M3 values, in order."""
+    small = [i * 2.0 ** -9 for i in range(8)]
+    return small + [(1 + f / 8) * 2.0 ** e for e in range(-6, 9) for f in range(8)][:-1]
+
+
+def _exact_through(x, fmt, group):
+    """Q(x) in 64 bits: the nearest code by the midpoints between them."""
+    x = x.double()
+    m, k = x.shape
+    g = group if group else k
+    full = torch.zeros(m, -(-k // g) * g, dtype=torch.float64, device=x.device)
+    full[:, :k] = x
+    full = full.reshape(m, -1, g)
+    top = full.abs().max(dim=2, keepdim=True).values
+    scale = torch.maximum((top / TOP[fmt]).float(), torch.full_like(top, LEAST).float()).double()
+    size = (full / scale).abs()
+    if fmt == "int8":
+        level = torch.floor(size)
+        rest = size - level
+        level = level + ((rest > 0.5) | ((rest == 0.5) & (torch.remainder(level, 2) == 1))).double()
+        level = torch.minimum(level, torch.full_like(level, 127.0))
+    else:
+        table = torch.tensor(_levels(), dtype=torch.float64, device=x.device)
+        middles = (table[1:] + table[:-1]) / 2
+        size = torch.minimum(size, torch.full_like(size, 448.0))
+        below = torch.searchsorted(middles, size, right=False)
+        upto = torch.searchsorted(middles, size, right=True)
+        index = torch.where((below != upto) & (upto % 2 == 1), below, upto)
+        level = table[index]
+    return (torch.sign(full) * level * scale).reshape(m, -1)[:, :k]
+
+
+def _exact_weights(w, group):
+    codes, scales, zeros, c = w
+    k = codes.shape[0]
+    q = torch.empty(k, 2 * codes.shape[1], dtype=torch.float64, device=codes.device)
+    q[:, 0::2] = (codes % 16).double()
+    q[:, 1::2] = torch.div(codes, 16, rounding_mode="floor").double()
+    q = q[:, :c]
+    g = group if group else c
+    zero = torch.full_like(scales, 8.0).double() if zeros is None else zeros.double()
+    for i in range(scales.shape[1]):
+        part = q[:, i * g:(i + 1) * g]
+        part.sub_(zero[:, i:i + 1]).mul_(scales[:, i:i + 1].double())
+    return q
+
+
+def _exact_act(v, act):
+    if act == "gelu":
+        return v * torch.special.ndtr(v)
+    if act == "silu":
+        return v * torch.sigmoid(v)
+    return torch.maximum(v, torch.zeros_like(v)) if act == "relu" else v
+
+
+def _exact_product(x, w, group):
+    return torch.matmul(x, _exact_weights(w, group).t())
+
+
+def exact(case, seed):
+    s = _inputs(case, seed)
+    op = case["op"]
+    if op == "quantize":
+        return _exact_through(s["x"], case["fmt"], case["x_group"])
+    if op == "linear":
+        if case["x"] in TOP:
+            x = s["xq"].double() * s["xs"].double()[:, :, None]
+            x = x.flatten(1)[:, :case["c"]]
+        else:
+            x = s["x"].double()
+        y = _exact_product(x, s["w"], case["group"])
+        for more in (s["bias"], s["residual"]):
+            y = y if more is None else y + more.double()
+        return _exact_act(y, case["act"])
+    x = s["x"].double() + s["z"].double()
+    h = x * ((x ** 2).sum(1, keepdim=True) / x.shape[1] + EPS) ** -0.5 * s["w_norm"].double()
+    h = _exact_through(h, case["fmt"], case["x_group"])
+    if op == "norm":
+        return [x, h]
+    t = _exact_act(_exact_product(h, s["w1"], case["group"]) + s["b1"].double(), "silu")
+    t = _exact_through(t, case["fmt"], case["x_group"])
+    return [x, _exact_product(t, s["w2"], case["group"]) + s["b2"].double() + x]
