@@ -26,6 +26,8 @@ CONV_FP4_MX, CONV_FP4_NV = 0, 1
 CONV_FP4_IO_BF16, CONV_FP4_IO_F32, CONV_FP4_IO_CODES = 0, 1, 2
 CONV_NORM_NONE, CONV_NORM_RMS, CONV_NORM_LAYER = 0, 1, 2
 CONV_GATE_NONE, CONV_GATE_LINEAR, CONV_GATE_SIGMOID = 0, 1, 2
+CONV_Q8_E4M3, CONV_Q8_INT8 = 0, 1
+CONV_W4_IO_BF16, CONV_W4_IO_F32, CONV_W4_IO_E4M3, CONV_W4_IO_INT8 = 0, 1, 2, 3
 CONV_NORM_OUT_FLOAT, CONV_NORM_OUT_FP4_MX, CONV_NORM_OUT_FP4_NV = 0, 1, 2
 
 CONV_ALGO_AUTO = -1
@@ -101,6 +103,18 @@ SIGNATURES = {
     "conv_fp4_set_strides": (_i, [_p, _ll, _ll, _ll]),
     "conv_fp4_workspace_size": (_i, [_p, _i, ctypes.POINTER(_sz)]),
     "conv_fp4_fwd": (_i, [_p, _i, _p, _p, _p, _p, _p, _p, _p, _p, _p, _sz, _p]),
+    "conv_q8_size": (_i, [_i, _i, _i, _i, ctypes.POINTER(_sz), ctypes.POINTER(_sz)]),
+    "conv_q8_quantize": (_i, [_i, _i, _i, _i, _i, _p, _ll, _p, _p, _p]),
+    "conv_q8_dequantize": (_i, [_i, _i, _i, _i, _i, _p, _p, _p, _ll, _p]),
+    "conv_w4_create": (_i, [ctypes.POINTER(_p)] + [_i] * 6),
+    "conv_w4_destroy": (_i, [_p]),
+    "conv_w4_set_input_group": (_i, [_p, _i]),
+    "conv_w4_set_epilogue": (_i, [_p, _i, _i]),
+    "conv_w4_set_strides": (_i, [_p, _ll, _ll, _ll]),
+    "conv_w4_packed_size": (_i, [_p, ctypes.POINTER(_sz)]),
+    "conv_w4_prepack": (_i, [_p] * 6),
+    "conv_w4_workspace_size": (_i, [_p, _i, ctypes.POINTER(_sz)]),
+    "conv_w4_fwd": (_i, [_p, _i, _p, _p, _p, _p, _p, _p, _p, _sz, _p]),
     "conv_norm_create": (_i, [ctypes.POINTER(_p), _i, _i, _i]),
     "conv_norm_destroy": (_i, [_p]),
     "conv_norm_set_z_dtype": (_i, [_p, _i]),
@@ -108,6 +122,7 @@ SIGNATURES = {
     "conv_norm_set_pre": (_i, [_p, _i, _f, _p, _p]),
     "conv_norm_set_gate": (_i, [_p, _i, _i, _f]),
     "conv_norm_set_output": (_i, [_p, _i, _f]),
+    "conv_norm_set_output_q8": (_i, [_p, _i, _i]),
     "conv_norm_set_strides": (_i, [_p, _ll, _ll, _ll, _ll, _ll]),
     "conv_norm_fwd": (_i, [_p, _i, _p, _p, _p, _p, _p, _p, _p]),
     "conv_fp4_block_create": (_i, [ctypes.POINTER(_p), _p, _p, _p, _p]),
@@ -424,6 +439,81 @@ def conv_fp4_fwd(desc, M, x_ptr, x_scales_ptr, w_codes_ptr, w_scales_ptr, bias_p
         _check(st, "conv_fp4_fwd")
 
 
+def conv_q8_size(fmt, group, rows, cols):
+    """(bytes of the codes, bytes of the scales)."""
+    cb, sb = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(load_library().conv_q8_size(fmt, group, rows, cols, ctypes.byref(cb),
+                                       ctypes.byref(sb)), "conv_q8_size")
+    return cb.value, sb.value
+
+
+def conv_q8_quantize(fmt, group, dtype, rows, cols, x_ptr, ldx, codes_ptr, scales_ptr,
+                     stream=None):
+    st = (_lib or load_library()).conv_q8_quantize(fmt, group, dtype, rows, cols, x_ptr, ldx,
+                                                   codes_ptr, scales_ptr, stream)
+    if st:
+        _check(st, "conv_q8_quantize")
+
+
+def conv_q8_dequantize(fmt, group, dtype, rows, cols, codes_ptr, scales_ptr, y_ptr, ldy=0,
+                       stream=None):
+    st = (_lib or load_library()).conv_q8_dequantize(fmt, group, dtype, rows, cols, codes_ptr,
+                                                     scales_ptr, y_ptr, ldy, stream)
+    if st:
+        _check(st, "conv_q8_dequantize")
+
+
+def conv_w4_create(C, K, group=128, scale_dtype=CONV_BF16, x_io=CONV_W4_IO_BF16,
+                   y_dtype=CONV_BF16):
+    d = ctypes.c_void_p()
+    _check(load_library().conv_w4_create(ctypes.byref(d), C, K, group, scale_dtype, x_io,
+                                         y_dtype), "conv_w4_create")
+    return d
+
+
+def conv_w4_destroy(desc):
+    _check(load_library().conv_w4_destroy(desc), "conv_w4_destroy")
+
+
+def conv_w4_set_input_group(desc, x_group):
+    _check(load_library().conv_w4_set_input_group(desc, x_group), "conv_w4_set_input_group")
+
+
+def conv_w4_set_epilogue(desc, act, has_residual):
+    _check(load_library().conv_w4_set_epilogue(desc, act, 1 if has_residual else 0),
+           "conv_w4_set_epilogue")
+
+
+def conv_w4_set_strides(desc, ldx=0, ldr=0, ldy=0):
+    _check(load_library().conv_w4_set_strides(desc, ldx, ldr, ldy), "conv_w4_set_strides")
+
+
+def conv_w4_packed_size(desc):
+    n = ctypes.c_size_t()
+    _check(load_library().conv_w4_packed_size(desc, ctypes.byref(n)), "conv_w4_packed_size")
+    return n.value
+
+
+def conv_w4_prepack(desc, codes_ptr, scales_ptr, zeros_ptr, packed_ptr, stream=None):
+    _check(load_library().conv_w4_prepack(desc, codes_ptr, scales_ptr, zeros_ptr, packed_ptr,
+                                          stream), "conv_w4_prepack")
+
+
+def conv_w4_workspace_size(desc, M):
+    n = ctypes.c_size_t()
+    _check(load_library().conv_w4_workspace_size(desc, M, ctypes.byref(n)),
+           "conv_w4_workspace_size")
+    return n.value
+
+
+def conv_w4_fwd(desc, M, x_ptr, x_scales_ptr, packed_ptr, bias_ptr, residual_ptr, y_ptr,
+                ws_ptr=None, ws_bytes=0, stream=None):
+    st = (_lib or load_library()).conv_w4_fwd(desc, M, x_ptr, x_scales_ptr, packed_ptr, bias_ptr,
+                                              residual_ptr, y_ptr, ws_ptr, ws_bytes, stream)
+    if st:
+        _check(st, "conv_w4_fwd")
+
+
 def conv_norm_create(C, x_dtype=CONV_BF16, z_dtype=CONV_BF16):
     d = ctypes.c_void_p()
     _check(load_library().conv_norm_create(ctypes.byref(d), C, x_dtype, z_dtype),
@@ -454,6 +544,10 @@ def conv_norm_set_gate(desc, gate, gate_rows=1, residual_scale=1.0):
 
 def conv_norm_set_output(desc, out, tensor_scale=1.0):
     _check(load_library().conv_norm_set_output(desc, out, tensor_scale), "conv_norm_set_output")
+
+
+def conv_norm_set_output_q8(desc, fmt, group=0):
+    _check(load_library().conv_norm_set_output_q8(desc, fmt, group), "conv_norm_set_output_q8")
 
 
 def conv_norm_set_strides(desc, ldx=0, ldz=0, ldg=0, ldxo=0, ldh=0):

@@ -6,6 +6,7 @@
 
 #include "fp4.cuh"
 #include "internal.h"
+#include "q8.cuh"
 
 namespace {
 
@@ -375,6 +376,18 @@ extern "C" conv_status_t conv_norm_set_output(conv_norm_t d, int out, float tens
   return gb_ok();
 }
 
+extern "C" conv_status_t conv_norm_set_output_q8(conv_norm_t d, conv_q8_format_t fmt, int group) {
+  if (!d) return gb_fail(CONV_ERR_BAD_PARAM, "desc is NULL");
+  if (fmt != CONV_Q8_E4M3 && fmt != CONV_Q8_INT8)
+    return gb_fail(CONV_ERR_BAD_PARAM, "unknown 8-bit format %d", (int)fmt);
+  if (group != 0 && group != gb::q8::GROUP)
+    return gb_fail(CONV_ERR_BAD_PARAM, "group must be 0 or 128");
+  d->a.out = fmt == CONV_Q8_E4M3 ? NORM_OUT_Q8_E4M3 : NORM_OUT_Q8_INT8;
+  d->a.h_group = group;
+  d->a.h_scale = 1.0f;
+  return gb_ok();
+}
+
 extern "C" conv_status_t conv_norm_set_strides(conv_norm_t d, long long ldx, long long ldz,
                                                long long ldg, long long ldxo, long long ldh) {
   if (!d) return gb_fail(CONV_ERR_BAD_PARAM, "desc is NULL");
@@ -398,11 +411,11 @@ static conv_status_t check_norm_call(conv_norm_t d, int rows, const void* x, con
     return gb_fail(CONV_ERR_BAD_PARAM, "h must be given exactly when there is a norm before");
   const bool codes = a.out != CONV_NORM_OUT_FLOAT;
   if ((h_scales != nullptr) != (h != nullptr && codes))
-    return gb_fail(CONV_ERR_BAD_PARAM, "h_scales must be given exactly for a 4-bit h");
+    return gb_fail(CONV_ERR_BAD_PARAM, "h_scales must be given exactly for a 4- or 8-bit h");
   if ((gate != nullptr) != (z != nullptr && a.gate_kind != CONV_GATE_NONE))
     return gb_fail(CONV_ERR_BAD_PARAM,
                    "gate must be given exactly when the descriptor has one and z is given");
-  if (codes && a.ldh != a.C) return gb_fail(CONV_ERR_UNSUPPORTED, "4-bit h is contiguous");
+  if (codes && a.ldh != a.C) return gb_fail(CONV_ERR_UNSUPPORTED, "4- and 8-bit h are contiguous");
   const size_t xb = elem_bytes(a.x_dtype), hb = elem_bytes(a.h_dtype);
   if (!aligned(x, xb) || !aligned(x_out, xb) || !aligned(z, elem_bytes(a.z_dtype)) ||
       !aligned(gate, hb) || !aligned(h, codes ? 16 : hb) || !aligned(h_scales, 16))
@@ -422,9 +435,15 @@ static conv_status_t check_norm_call(conv_norm_t d, int rows, const void* x, con
 }
 
 static conv_status_t launch_norm(const NormArgs& a, cudaStream_t st) {
+  const bool q8 = a.out == NORM_OUT_Q8_E4M3 || a.out == NORM_OUT_Q8_INT8;
   // without z its type does not matter
-  if (a.z && a.z_dtype != a.h_dtype) return cuda_status(launch_norm_bfb(a, st), "norm");
+  if (a.z && a.z_dtype != a.h_dtype)
+    return cuda_status(q8 ? launch_norm_q8_bfb(a, st) : launch_norm_bfb(a, st), "norm");
   const bool xb16 = a.x_dtype == CONV_BF16, zb16 = a.h_dtype == CONV_BF16;
+  if (q8)
+    return cuda_status(xb16 ? (zb16 ? launch_norm_q8_bb(a, st) : launch_norm_q8_bf(a, st))
+                            : (zb16 ? launch_norm_q8_fb(a, st) : launch_norm_q8_ff(a, st)),
+                       "norm");
   return cuda_status(xb16 ? (zb16 ? launch_norm_bb(a, st) : launch_norm_bf(a, st))
                           : (zb16 ? launch_norm_fb(a, st) : launch_norm_ff(a, st)),
                      "norm");

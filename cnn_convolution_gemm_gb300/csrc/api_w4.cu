@@ -1,0 +1,254 @@
+// C-ABI entry points of the 8-bit matrices with scales and of the layers with integer 4-bit
+// weights: argument checks, workspace layout, dispatch.
+#include <new>
+
+#include "internal.h"
+#include "q8.cuh"
+#include "w4.cuh"
+
+namespace {
+
+constexpr int MOST = 1 << 30;          // rows, and columns of a matrix
+constexpr int MOST_CHANNELS = 1 << 28; // inputs and outputs of a layer
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+size_t elem_bytes(int dtype) { return dtype == CONV_BF16 ? 2 : 4; }
+bool is_float(int dtype) { return dtype == CONV_BF16 || dtype == CONV_F32; }
+
+conv_status_t cuda_status(cudaError_t e, const char* what) {
+  return e == cudaSuccess ? gb_ok()
+                          : gb_fail(CONV_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+
+conv_status_t check_format(int fmt, int group) {
+  if (fmt != CONV_Q8_E4M3 && fmt != CONV_Q8_INT8)
+    return gb_fail(CONV_ERR_BAD_PARAM, "unknown 8-bit format %d", fmt);
+  if (group != 0 && group != gb::q8::GROUP)
+    return gb_fail(CONV_ERR_BAD_PARAM, "group must be 0 or 128");
+  return CONV_OK;
+}
+
+conv_status_t check_size(int rows, int cols) {
+  if (rows < 0 || cols <= 0)
+    return gb_fail(CONV_ERR_BAD_PARAM, "rows must be >= 0 and cols > 0");
+  if (rows > MOST || cols > MOST)
+    return gb_fail(CONV_ERR_UNSUPPORTED, "more than 2^30 rows or cols");
+  return CONV_OK;
+}
+
+// the checks that quantising and reading back share
+conv_status_t check_matrix(int fmt, int group, int dtype, int rows, int cols, const void* t,
+                           long long* ld, const char* tname, const void* codes,
+                           const void* scales) {
+  conv_status_t st = check_format(fmt, group);
+  if (st != CONV_OK) return st;
+  if (!is_float(dtype)) return gb_fail(CONV_ERR_BAD_PARAM, "%s must be bf16 or fp32", tname);
+  if ((st = check_size(rows, cols)) != CONV_OK) return st;
+  if (*ld == 0) *ld = cols;
+  if (*ld < cols) return gb_fail(CONV_ERR_BAD_PARAM, "row stride of %s below its row", tname);
+  if (rows == 0) return CONV_OK;
+  if (!t || !codes || !scales) return gb_fail(CONV_ERR_BAD_PARAM, "NULL tensor");
+  if (!aligned(t, elem_bytes(dtype)))
+    return gb_fail(CONV_ERR_ALIGNMENT, "%s must be aligned to its element", tname);
+  if (!aligned(codes, 16) || !aligned(scales, 16))
+    return gb_fail(CONV_ERR_ALIGNMENT, "codes and scales must be 16-byte aligned");
+  return CONV_OK;
+}
+
+}  // namespace
+
+extern "C" conv_status_t conv_q8_size(conv_q8_format_t fmt, int group, int rows, int cols,
+                                      size_t* cb, size_t* sb) {
+  if (!cb || !sb) return gb_fail(CONV_ERR_BAD_PARAM, "NULL argument");
+  conv_status_t st = check_format(fmt, group);
+  if (st != CONV_OK) return st;
+  if ((st = check_size(rows, cols)) != CONV_OK) return st;
+  *cb = (size_t)rows * gb::q8::code_pitch(cols);
+  *sb = (size_t)rows * gb::q8::scales_per_row(group, cols) * 4;
+  return gb_ok();
+}
+
+extern "C" conv_status_t conv_q8_quantize(conv_q8_format_t fmt, int group, conv_dtype_t dtype,
+                                          int rows, int cols, const void* x, long long ldx,
+                                          void* codes, void* scales, void* stream) {
+  const conv_status_t st =
+      check_matrix(fmt, group, dtype, rows, cols, x, &ldx, "x", codes, scales);
+  if (st != CONV_OK) return st;
+  if (rows == 0) return gb_ok();
+  return cuda_status(launch_q8_quantize(fmt, group, dtype, rows, cols, x, ldx, codes, scales,
+                                        static_cast<cudaStream_t>(stream)),
+                     "8-bit quantisation");
+}
+
+extern "C" conv_status_t conv_q8_dequantize(conv_q8_format_t fmt, int group, conv_dtype_t dtype,
+                                            int rows, int cols, const void* codes,
+                                            const void* scales, void* y, long long ldy,
+                                            void* stream) {
+  const conv_status_t st =
+      check_matrix(fmt, group, dtype, rows, cols, y, &ldy, "y", codes, scales);
+  if (st != CONV_OK) return st;
+  if (rows == 0) return gb_ok();
+  return cuda_status(launch_q8_dequantize(fmt, group, dtype, rows, cols, codes, scales, y, ldy,
+                                          static_cast<cudaStream_t>(stream)),
+                     "8-bit dequantisation");
+}
+
+// ---------------------------------------------------------------------------
+// the layer
+
+struct gbconv_w4_s {
+  int C, K, group, scale_dtype, x_io, x_group, y_dtype, act, has_residual;
+  long long ldx, ldr, ldy;  // resolved: never 0
+};
+
+namespace {
+bool x_codes(const gbconv_w4_s& d) {
+  return d.x_io == CONV_W4_IO_E4M3 || d.x_io == CONV_W4_IO_INT8;
+}
+W4Gemm problem(const gbconv_w4_s& d, int M) {
+  W4Gemm g{};
+  g.M = M;
+  g.C = d.C;
+  g.K = d.K;
+  g.group = d.group;
+  g.scale_f32 = d.scale_dtype == CONV_F32;
+  g.x_io = d.x_io;
+  g.x_group = d.x_group;
+  g.y_f32 = d.y_dtype == CONV_F32;
+  g.act = d.act;
+  g.ldx = x_codes(d) ? gb::q8::code_pitch(d.C) : d.ldx;
+  g.ldr = d.ldr;
+  g.ldy = d.ldy;
+  return g;
+}
+size_t workspace(const W4Gemm& g) { return w4_few_applicable(g) ? 0 : w4_gemm_workspace(g); }
+}  // namespace
+
+extern "C" conv_status_t conv_w4_create(conv_w4_t* out, int C, int K, int group,
+                                        conv_dtype_t scale_dtype, int x_io,
+                                        conv_dtype_t y_dtype) {
+  if (!out) return gb_fail(CONV_ERR_BAD_PARAM, "out is NULL");
+  *out = nullptr;
+  if (C <= 0 || K <= 0) return gb_fail(CONV_ERR_BAD_PARAM, "sizes must be positive");
+  if (C > MOST_CHANNELS || K > MOST_CHANNELS)
+    return gb_fail(CONV_ERR_UNSUPPORTED, "more than 2^28 inputs or outputs");
+  if (group != 0 && group != 32 && group != 64 && group != 128)
+    return gb_fail(CONV_ERR_UNSUPPORTED, "group must be 0, 32, 64 or 128");
+  if (!is_float(scale_dtype) || !is_float(y_dtype))
+    return gb_fail(CONV_ERR_BAD_PARAM, "scale_dtype and y_dtype must be bf16 or fp32");
+  if (x_io < CONV_W4_IO_BF16 || x_io > CONV_W4_IO_INT8)
+    return gb_fail(CONV_ERR_BAD_PARAM, "x_io must be 0 .. 3");
+  gbconv_w4_s* d = new (std::nothrow) gbconv_w4_s{};
+  if (!d) return gb_fail(CONV_ERR_BAD_PARAM, "out of host memory");
+  d->C = C;
+  d->K = K;
+  d->group = group;
+  d->scale_dtype = scale_dtype;
+  d->x_io = x_io;
+  d->y_dtype = y_dtype;
+  d->ldx = C;
+  d->ldr = d->ldy = K;
+  *out = d;
+  return gb_ok();
+}
+
+extern "C" conv_status_t conv_w4_destroy(conv_w4_t d) {
+  delete d;
+  return gb_ok();
+}
+
+extern "C" conv_status_t conv_w4_set_input_group(conv_w4_t d, int x_group) {
+  if (!d) return gb_fail(CONV_ERR_BAD_PARAM, "desc is NULL");
+  if (x_group != 0 && x_group != gb::q8::GROUP)
+    return gb_fail(CONV_ERR_BAD_PARAM, "x_group must be 0 or 128");
+  if (x_group && !x_codes(*d))
+    return gb_fail(CONV_ERR_UNSUPPORTED, "only an 8-bit x has scales");
+  d->x_group = x_group;
+  return gb_ok();
+}
+
+extern "C" conv_status_t conv_w4_set_epilogue(conv_w4_t d, int act, int has_residual) {
+  if (!d) return gb_fail(CONV_ERR_BAD_PARAM, "desc is NULL");
+  if (act < CONV_ACT_NONE || act > CONV_ACT_SILU)
+    return gb_fail(CONV_ERR_BAD_PARAM, "act must be 0 .. 4");
+  d->act = act;
+  d->has_residual = has_residual ? 1 : 0;
+  return gb_ok();
+}
+
+extern "C" conv_status_t conv_w4_set_strides(conv_w4_t d, long long ldx, long long ldr,
+                                             long long ldy) {
+  if (!d) return gb_fail(CONV_ERR_BAD_PARAM, "desc is NULL");
+  if (ldx && x_codes(*d) && ldx != d->C)
+    return gb_fail(CONV_ERR_UNSUPPORTED, "8-bit x is contiguous");
+  if ((ldx && ldx < d->C) || (ldr && ldr < d->K) || (ldy && ldy < d->K))
+    return gb_fail(CONV_ERR_BAD_PARAM, "row stride below the row");
+  d->ldx = ldx ? ldx : d->C;
+  d->ldr = ldr ? ldr : d->K;
+  d->ldy = ldy ? ldy : d->K;
+  return gb_ok();
+}
+
+extern "C" conv_status_t conv_w4_packed_size(conv_w4_t d, size_t* bytes) {
+  if (!d || !bytes) return gb_fail(CONV_ERR_BAD_PARAM, "NULL argument");
+  *bytes = gb::w4::packed_layout(d->C, d->K, d->group, (int)elem_bytes(d->scale_dtype)).bytes;
+  return gb_ok();
+}
+
+extern "C" conv_status_t conv_w4_prepack(conv_w4_t d, const void* codes, const void* scales,
+                                         const void* zeros, void* packed, void* stream) {
+  if (!d) return gb_fail(CONV_ERR_BAD_PARAM, "desc is NULL");
+  if (!codes || !scales || !packed) return gb_fail(CONV_ERR_BAD_PARAM, "NULL tensor");
+  if (!aligned(scales, elem_bytes(d->scale_dtype)))
+    return gb_fail(CONV_ERR_ALIGNMENT, "scales must be aligned to their element");
+  if (!aligned(packed, 16)) return gb_fail(CONV_ERR_ALIGNMENT, "packed must be 16-byte aligned");
+  return cuda_status(launch_w4_pack(d->C, d->K, d->group, d->scale_dtype == CONV_F32, codes,
+                                    scales, zeros, packed, static_cast<cudaStream_t>(stream)),
+                     "4-bit weights");
+}
+
+extern "C" conv_status_t conv_w4_workspace_size(conv_w4_t d, int M, size_t* bytes) {
+  if (!d || !bytes) return gb_fail(CONV_ERR_BAD_PARAM, "NULL argument");
+  if (M < 0) return gb_fail(CONV_ERR_BAD_PARAM, "M must be >= 0");
+  if (M > MOST) return gb_fail(CONV_ERR_UNSUPPORTED, "more than 2^30 rows");
+  *bytes = M ? workspace(problem(*d, M)) : 0;
+  return gb_ok();
+}
+
+extern "C" conv_status_t conv_w4_fwd(conv_w4_t d, int M, const void* x, const void* x_scales,
+                                     const void* packed, const float* bias, const void* residual,
+                                     void* y, void* ws, size_t ws_bytes, void* stream) {
+  if (!d) return gb_fail(CONV_ERR_BAD_PARAM, "desc is NULL");
+  if (M < 0) return gb_fail(CONV_ERR_BAD_PARAM, "M must be >= 0");
+  if (M > MOST) return gb_fail(CONV_ERR_UNSUPPORTED, "more than 2^30 rows");
+  if (M == 0) return gb_ok();
+  if (!x || !packed || !y) return gb_fail(CONV_ERR_BAD_PARAM, "NULL tensor");
+  if (x_codes(*d) != (x_scales != nullptr))
+    return gb_fail(CONV_ERR_BAD_PARAM, "x_scales must be given exactly for an 8-bit x");
+  if ((residual != nullptr) != (d->has_residual != 0))
+    return gb_fail(CONV_ERR_BAD_PARAM,
+                   "residual must be given exactly when the descriptor has one");
+  const size_t xa = x_codes(*d) ? 16 : elem_bytes(d->x_io), ya = elem_bytes(d->y_dtype);
+  if (!aligned(x, xa) || !aligned(y, ya) || !aligned(residual, ya) || !aligned(bias, 4) ||
+      !aligned(x_scales, 4))
+    return gb_fail(CONV_ERR_ALIGNMENT, "a tensor is not aligned to its element (codes: 16 bytes)");
+  if (!aligned(packed, 16)) return gb_fail(CONV_ERR_ALIGNMENT, "packed must be 16-byte aligned");
+  if (residual == y && d->ldr != d->ldy)
+    return gb_fail(CONV_ERR_BAD_PARAM, "y may be the residual only with its row stride");
+  W4Gemm g = problem(*d, M);
+  const size_t need = workspace(g);
+  if (need && (!ws || ws_bytes < need))
+    return gb_fail(CONV_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need,
+                   ws ? ws_bytes : (size_t)0);
+  if (!aligned(ws, 16)) return gb_fail(CONV_ERR_ALIGNMENT, "workspace must be 16-byte aligned");
+  g.x = x;
+  g.xs = static_cast<const float*>(x_scales);
+  g.packed = static_cast<const uint8_t*>(packed);
+  g.bias = bias;
+  g.res = residual;
+  g.y = y;
+  g.ws = ws;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return cuda_status(w4_few_applicable(g) ? launch_w4_few(g, st) : launch_w4_gemm(g, st),
+                     "product with 4-bit weights");
+}

@@ -299,10 +299,22 @@ cudaError_t launch_fp4_gemm(const Fp4Gemm& g, cudaStream_t st);
 constexpr int FUSED_ROWS = 8;
 cudaError_t launch_fp4_few(const Fp4Gemm& g, cudaStream_t st);
 
+// ---- 8-bit matrices with scales (formats and layouts: gbconv.h) ----------------
+
+cudaError_t launch_q8_quantize(int fmt, int group, int dtype, int rows, int cols, const void* x,
+                               long long ldx, void* codes, void* scales, cudaStream_t st);
+cudaError_t launch_q8_dequantize(int fmt, int group, int dtype, int rows, int cols,
+                                 const void* codes, const void* scales, void* y, long long ldy,
+                                 cudaStream_t st);
+
 // ---- norms around a residual block ----------------------------------------------
+
+// What conv_norm_set_output_q8 makes of out, behind conv_norm_out_t's values.
+enum : int { NORM_OUT_Q8_E4M3 = 3, NORM_OUT_Q8_INT8 = 4 };
 
 struct NormArgs {
   int C, rows, x_dtype, z_dtype, h_dtype;  // h's: of the gates too
+  int h_group;                             // of an 8-bit h
   int post, pre, gate_kind, gate_rows, out;
   float eps_post, eps_pre, rs, h_scale;
   const float *w_post, *b_post, *w_pre, *b_pre;
@@ -319,3 +331,9 @@ cudaError_t launch_norm_bf(const NormArgs& a, cudaStream_t st);
 cudaError_t launch_norm_fb(const NormArgs& a, cudaStream_t st);
 cudaError_t launch_norm_ff(const NormArgs& a, cudaStream_t st);
 cudaError_t launch_norm_bfb(const NormArgs& a, cudaStream_t st);  // z given
+// the same with h in 8 bits
+cudaError_t launch_norm_q8_bb(const NormArgs& a, cudaStream_t st);
+cudaError_t launch_norm_q8_bf(const NormArgs& a, cudaStream_t st);
+cudaError_t launch_norm_q8_fb(const NormArgs& a, cudaStream_t st);
+cudaError_t launch_norm_q8_ff(const NormArgs& a, cudaStream_t st);
+cudaError_t launch_norm_q8_bfb(const NormArgs& a, cudaStream_t st);  // z given

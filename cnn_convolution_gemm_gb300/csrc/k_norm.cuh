@@ -19,6 +19,7 @@
 #include "fp4.cuh"
 #include "internal.h"
 #include "ptx.cuh"
+#include "q8.cuh"
 
 namespace gb {
 namespace norm {
@@ -147,6 +148,31 @@ __device__ __forceinline__ void row_sum(float (&v)[R], float (*red)[32 * R], int
     for (int o = P / 2; o; o >>= 1)
 #pragma unroll
       for (int k = 0; k < R; ++k) v[k] += __shfl_xor_sync(0xFFFFFFFFu, v[k], o);
+  }
+}
+
+// The largest of the T threads' values of each of R rows (>= 0; a NaN stays), likewise.
+template <int T, int R>
+__device__ __forceinline__ void row_top(float (&v)[R], float (*red)[32 * R], int& turn) {
+#pragma unroll
+  for (int o = (T < 32 ? T : 32) / 2; o; o >>= 1)
+#pragma unroll
+    for (int k = 0; k < R; ++k) v[k] = max_nan(v[k], __shfl_xor_sync(0xFFFFFFFFu, v[k], o));
+  if constexpr (T > 32) {
+    constexpr int W = T / 32, P = W <= 2 ? 2 : W <= 4 ? 4 : W <= 8 ? 8 : W <= 16 ? 16 : 32;
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int k = 0; k < R; ++k)
+      if (lane == k) red[turn][32 * k + (threadIdx.x >> 5)] = v[k];
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < R; ++k)
+      v[k] = W == P || (lane & (P - 1)) < W ? red[turn][32 * k + (lane & (P - 1))] : 0.0f;
+    turn ^= 1;
+#pragma unroll
+    for (int o = P / 2; o; o >>= 1)
+#pragma unroll
+      for (int k = 0; k < R; ++k) v[k] = max_nan(v[k], __shfl_xor_sync(0xFFFFFFFFu, v[k], o));
   }
 }
 
@@ -301,6 +327,52 @@ __device__ __forceinline__ void store_h(const NormArgs& a, const TensorScale& ts
   }
 }
 
+// Stores h of R rows in 8 bits.
+template <int FMT, int T, int N, int R>
+__device__ __forceinline__ void store_q8(const NormArgs& a, long long r, int t,
+                                         const float (&v)[R][N], float (*red)[32 * R],
+                                         int& turn) {
+  const int C = a.C;
+  uint8_t* const codes = static_cast<uint8_t*>(a.h);
+  float* const scales = reinterpret_cast<float*>(a.hs);
+  float top[R];
+  if (!a.h_group) {
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      top[k] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < N; i += 2) top[k] = max_abs(top[k], v[k][i], v[k][i + 1]);
+    }
+    row_top<T, R>(top, red, turn);
+  }
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    const bool valid = r + k < a.rows;
+    if (a.h_group) {
+#pragma unroll
+      for (int i = 0; i < N / 16; ++i) {
+        if (16 * (i * T + (t & ~31)) >= C) break;  // the warp's first column
+        float e[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) e[j] = v[k][16 * i + j];
+        q8::store_grouped16<FMT>(e, valid, r + k, 16 * (i * T + t), C, codes, scales);
+      }
+    } else if (valid) {
+      const q8::Scale<FMT> s(top[k]);
+      if (t == 0) scales[r + k] = s.s;
+#pragma unroll
+      for (int i = 0; i < N / 16; ++i) {
+        const int c = 16 * (i * T + t);
+        if (c >= C) break;
+        float e[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) e[j] = v[k][16 * i + j];
+        *reinterpret_cast<uint4*>(codes + (r + k) * q8::code_pitch(C) + c) = s.codes16(e);
+      }
+    }
+  }
+}
+
 // Blocks an SM has to hold, which caps the registers: the compiler otherwise spends more on
 // loads it spreads between the sums (8192 x 4096 with gates 52 us, uncapped 74; 14552 x 2579
 // bf16 145, 223).  Without z more fit: 16384 x 8192 bf16 to MX 106 -> 91 us.
@@ -321,9 +393,10 @@ constexpr int least_blocks(int T, int N, Layout lay, bool ahead, int R, bool has
 // AHEAD (GROUPS, T > 32): x and z (if given) come through the ring; else R is 1.
 // HASZ false: z is not given (the first norm of a network or block).
 // Types: TX of x and x', TZ of z, TG of the gates and h.
+// Q8: h in 8 bits (a kernel of its own: the others keep their registers).
 // vec_w: 16-byte accesses to weights.  held: how many of their rows shared memory has room for.
 template <typename TX, typename TZ, typename TG, int T, int N, Layout LAY, bool AHEAD, int R,
-          bool HASZ>
+          bool HASZ, bool Q8>
 __global__ void __launch_bounds__(T <= 32 ? 128 : T, least_blocks(T, N, LAY, AHEAD, R, HASZ))
     norm_kernel(const NormArgs a, const TensorScale ts, const bool vec_w, const int held) {
   static_assert(AHEAD ? LAY == GROUPS : R == 1, "rows of a step");
@@ -468,9 +541,16 @@ __global__ void __launch_bounds__(T <= 32 ? 128 : T, least_blocks(T, N, LAY, AHE
     }
     if (a.pre != CONV_NORM_NONE) {
       norm_rows<T, N, LAY, R>(v, a.pre, a.eps_pre, w_pre, b_pre, t, C, vec_w, inv, red, turn);
+      if constexpr (Q8) {
+        if (a.out == NORM_OUT_Q8_E4M3)
+          store_q8<CONV_Q8_E4M3, T, N, R>(a, r, t, v, red, turn);
+        else
+          store_q8<CONV_Q8_INT8, T, N, R>(a, r, t, v, red, turn);
+      } else {
 #pragma unroll
-      for (int k = 0; k < R; ++k)
-        if (T < 32 || r + k < a.rows) store_h<TG, T, N, LAY>(a, ts, r + k, t, v[k]);
+        for (int k = 0; k < R; ++k)
+          if (T < 32 || r + k < a.rows) store_h<TG, T, N, LAY>(a, ts, r + k, t, v[k]);
+      }
     }
     if constexpr (AHEAD) {
       // every thread has read the rows before a barrier: norm_pre's, or this one
@@ -517,27 +597,27 @@ cudaError_t launch_rows(K* kern, const NormArgs& a, int block, int rows_per_bloc
   return e;
 }
 
-template <typename TX, typename TZ, typename TG, int T, int N, Layout LAY>
+template <typename TX, typename TZ, typename TG, bool Q8, int T, int N, Layout LAY>
 cudaError_t launch_direct(const NormArgs& a, cudaStream_t st) {
-  auto* kern = norm_kernel<TX, TZ, TG, T, N, LAY, false, 1, true>;
+  auto* kern = norm_kernel<TX, TZ, TG, T, N, LAY, false, 1, true, Q8>;
   if constexpr (std::is_same_v<TZ, TG>)  // launch(): without z the types are equal
-    if (!a.z) kern = norm_kernel<TX, TZ, TG, T, N, LAY, false, 1, false>;
+    if (!a.z) kern = norm_kernel<TX, TZ, TG, T, N, LAY, false, 1, false, Q8>;
   return launch_rows(kern, a, T <= 32 ? 128 : T, T <= 32 ? 128 / T : 1, 0, 0, st);
 }
 
 // 16 consecutive columns a thread up to 8192 channels (152 rows of 4160 bf16 with gates
 // 5.4 us, 32 columns 6.7), 32 above
-template <typename TX, typename TZ, typename TG, Layout LAY>
+template <typename TX, typename TZ, typename TG, bool Q8, Layout LAY>
 cudaError_t launch_groups(const NormArgs& a, cudaStream_t st) {
-  if (a.C <= 128) return launch_direct<TX, TZ, TG, 8, 16, LAY>(a, st);
-  if (a.C <= 256) return launch_direct<TX, TZ, TG, 16, 16, LAY>(a, st);
-  if (a.C <= 512) return launch_direct<TX, TZ, TG, 32, 16, LAY>(a, st);
-  if (a.C <= 1024) return launch_direct<TX, TZ, TG, 64, 16, LAY>(a, st);
-  if (a.C <= 2048) return launch_direct<TX, TZ, TG, 128, 16, LAY>(a, st);
-  if (a.C <= 4096) return launch_direct<TX, TZ, TG, 256, 16, LAY>(a, st);
-  if (a.C <= 8192) return launch_direct<TX, TZ, TG, 512, 16, LAY>(a, st);
-  if (a.C <= 16384) return launch_direct<TX, TZ, TG, 512, 32, LAY>(a, st);
-  return launch_direct<TX, TZ, TG, 1024, 32, LAY>(a, st);
+  if (a.C <= 128) return launch_direct<TX, TZ, TG, Q8, 8, 16, LAY>(a, st);
+  if (a.C <= 256) return launch_direct<TX, TZ, TG, Q8, 16, 16, LAY>(a, st);
+  if (a.C <= 512) return launch_direct<TX, TZ, TG, Q8, 32, 16, LAY>(a, st);
+  if (a.C <= 1024) return launch_direct<TX, TZ, TG, Q8, 64, 16, LAY>(a, st);
+  if (a.C <= 2048) return launch_direct<TX, TZ, TG, Q8, 128, 16, LAY>(a, st);
+  if (a.C <= 4096) return launch_direct<TX, TZ, TG, Q8, 256, 16, LAY>(a, st);
+  if (a.C <= 8192) return launch_direct<TX, TZ, TG, Q8, 512, 16, LAY>(a, st);
+  if (a.C <= 16384) return launch_direct<TX, TZ, TG, Q8, 512, 32, LAY>(a, st);
+  return launch_direct<TX, TZ, TG, Q8, 1024, 32, LAY>(a, st);
 }
 
 // 8 single columns a thread (an access is one element: with more of them registers, not
@@ -545,14 +625,14 @@ cudaError_t launch_groups(const NormArgs& a, cudaStream_t st) {
 // row needs them
 template <typename TX, typename TZ, typename TG>
 cudaError_t launch_single(const NormArgs& a, cudaStream_t st) {
-  if (a.C <= 256) return launch_direct<TX, TZ, TG, 32, 8, SINGLE>(a, st);
-  if (a.C <= 512) return launch_direct<TX, TZ, TG, 64, 8, SINGLE>(a, st);
-  if (a.C <= 1024) return launch_direct<TX, TZ, TG, 128, 8, SINGLE>(a, st);
-  if (a.C <= 2048) return launch_direct<TX, TZ, TG, 256, 8, SINGLE>(a, st);
-  if (a.C <= 4096) return launch_direct<TX, TZ, TG, 512, 8, SINGLE>(a, st);
-  if (a.C <= 8192) return launch_direct<TX, TZ, TG, 1024, 8, SINGLE>(a, st);
-  if (a.C <= 16384) return launch_direct<TX, TZ, TG, 1024, 16, SINGLE>(a, st);
-  return launch_direct<TX, TZ, TG, 1024, 32, SINGLE>(a, st);
+  if (a.C <= 256) return launch_direct<TX, TZ, TG, false, 32, 8, SINGLE>(a, st);
+  if (a.C <= 512) return launch_direct<TX, TZ, TG, false, 64, 8, SINGLE>(a, st);
+  if (a.C <= 1024) return launch_direct<TX, TZ, TG, false, 128, 8, SINGLE>(a, st);
+  if (a.C <= 2048) return launch_direct<TX, TZ, TG, false, 256, 8, SINGLE>(a, st);
+  if (a.C <= 4096) return launch_direct<TX, TZ, TG, false, 512, 8, SINGLE>(a, st);
+  if (a.C <= 8192) return launch_direct<TX, TZ, TG, false, 1024, 8, SINGLE>(a, st);
+  if (a.C <= 16384) return launch_direct<TX, TZ, TG, false, 1024, 16, SINGLE>(a, st);
+  return launch_direct<TX, TZ, TG, false, 1024, 32, SINGLE>(a, st);
 }
 
 // Shared memory of the ring and the weights beside it; the latter as far as they fit.
@@ -573,18 +653,19 @@ AheadSmem ahead_smem(const NormArgs& a) {
 }
 
 // Z_ONLY: called with z alone.
-template <typename TX, typename TZ, typename TG, int T, int R, bool Z_ONLY = false>
+template <typename TX, typename TZ, typename TG, bool Q8, int T, int R, bool Z_ONLY = false>
 cudaError_t launch_ahead(const NormArgs& a, cudaStream_t st) {
-  auto* kern = norm_kernel<TX, TZ, TG, T, 16, GROUPS, true, R, true>;
+  auto* kern = norm_kernel<TX, TZ, TG, T, 16, GROUPS, true, R, true, Q8>;
   if constexpr (!Z_ONLY && std::is_same_v<TZ, TG>)
-    if (!a.z) kern = norm_kernel<TX, TZ, TG, T, 16, GROUPS, true, R, false>;
+    if (!a.z) kern = norm_kernel<TX, TZ, TG, T, 16, GROUPS, true, R, false, Q8>;
   const AheadSmem smem = ahead_smem<TX, TZ, T, R>(a);
   const cudaError_t e = gb_set_smem_once(reinterpret_cast<const void*>(kern), smem.bytes);
   if (e != cudaSuccess) return e;
   return launch_rows(kern, a, T, R, smem.bytes, smem.held, st);
 }
 
-template <typename TX, typename TZ, typename TG = TZ>
+// Q8: h in 8 bits.
+template <typename TX, typename TZ, typename TG, bool Q8>
 cudaError_t launch(const NormArgs& a, cudaStream_t st) {
   if constexpr (!std::is_same_v<TZ, TG>)
     if (!a.z) return cudaErrorInvalidValue;  // the caller's to dispatch by TX and TG
@@ -601,30 +682,34 @@ cudaError_t launch(const NormArgs& a, cudaStream_t st) {
       gb_num_sms() * (a.C > 4096 ? 3LL : a.C > 2048 ? 8LL : 8192 / std::max(a.C, 512) * 8);
   if (vec && a.C > 512 && a.C * sizeof(TX) % 16 == 0 && a.C * sizeof(TZ) % 16 == 0 &&
       a.rows >= many) {
-    if (a.C <= 1024) return launch_ahead<TX, TZ, TG, 64, 2>(a, st);
-    if (a.C <= 2048) return launch_ahead<TX, TZ, TG, 128, 2>(a, st);
+    if (a.C <= 1024) return launch_ahead<TX, TZ, TG, Q8, 64, 2>(a, st);
+    if (a.C <= 2048) return launch_ahead<TX, TZ, TG, Q8, 128, 2>(a, st);
     // one row of 192 threads, four blocks to an SM (12442 x 2560 bf16 46 us, 256 threads and
     // two rows 64)
-    if (a.C <= 16 * 192) return launch_ahead<TX, TZ, TG, 192, 1>(a, st);
+    if (a.C <= 16 * 192) return launch_ahead<TX, TZ, TG, Q8, 192, 1>(a, st);
     if (a.C <= 4096) {
       // likewise (24384 x 4096 bf16, layer norms 220 us, two rows 266; fp32, one block: 427
       // and 343)
       if (a.z && ahead_smem<TX, TZ, 256, 1>(a).twice)
-        return launch_ahead<TX, TZ, TG, 256, 1, true>(a, st);
-      if (ahead_smem<TX, TZ, 256, 2>(a).all) return launch_ahead<TX, TZ, TG, 256, 2>(a, st);
+        return launch_ahead<TX, TZ, TG, Q8, 256, 1, true>(a, st);
+      if (ahead_smem<TX, TZ, 256, 2>(a).all) return launch_ahead<TX, TZ, TG, Q8, 256, 2>(a, st);
     } else if (a.C <= 16 * 384 && ahead_smem<TX, TZ, 384, 1>(a).twice) {
       // the same of 384 threads where two blocks fit (12442 x 4768 bf16 93 us, else 125; one
       // block with four weights 200, else 187)
-      return launch_ahead<TX, TZ, TG, 384, 1>(a, st);
+      return launch_ahead<TX, TZ, TG, Q8, 384, 1>(a, st);
     } else if (a.C <= 8192) {
-      if (ahead_smem<TX, TZ, 512, 2>(a).all) return launch_ahead<TX, TZ, TG, 512, 2>(a, st);
-      if (ahead_smem<TX, TZ, 512, 1>(a).all) return launch_ahead<TX, TZ, TG, 512, 1>(a, st);
+      if (ahead_smem<TX, TZ, 512, 2>(a).all) return launch_ahead<TX, TZ, TG, Q8, 512, 2>(a, st);
+      if (ahead_smem<TX, TZ, 512, 1>(a).all) return launch_ahead<TX, TZ, TG, Q8, 512, 1>(a, st);
     } else if (a.C <= 16384 && ahead_smem<TX, TZ, 1024, 1>(a).bytes) {
-      return launch_ahead<TX, TZ, TG, 1024, 1>(a, st);
+      return launch_ahead<TX, TZ, TG, Q8, 1024, 1>(a, st);
     }
   }
-  if (vec) return launch_groups<TX, TZ, TG, GROUPS>(a, st);
-  return codes ? launch_groups<TX, TZ, TG, ANY>(a, st) : launch_single<TX, TZ, TG>(a, st);
+  if (vec) return launch_groups<TX, TZ, TG, Q8, GROUPS>(a, st);
+  if constexpr (Q8)
+    return launch_groups<TX, TZ, TG, true, ANY>(a, st);
+  else
+    return codes ? launch_groups<TX, TZ, TG, false, ANY>(a, st)
+                 : launch_single<TX, TZ, TG>(a, st);
 }
 
 }  // namespace norm

@@ -2,5 +2,5 @@
 #include "k_norm.cuh"
 
 cudaError_t launch_norm_bb(const NormArgs& a, cudaStream_t st) {
-  return gb::norm::launch<__nv_bfloat16, __nv_bfloat16>(a, st);
+  return gb::norm::launch<__nv_bfloat16, __nv_bfloat16, __nv_bfloat16, false>(a, st);
 }

@@ -2,5 +2,5 @@
 #include "k_norm.cuh"
 
 cudaError_t launch_norm_bf(const NormArgs& a, cudaStream_t st) {
-  return gb::norm::launch<__nv_bfloat16, float>(a, st);
+  return gb::norm::launch<__nv_bfloat16, float, float, false>(a, st);
 }

@@ -2,5 +2,5 @@
 #include "k_norm.cuh"
 
 cudaError_t launch_norm_bfb(const NormArgs& a, cudaStream_t st) {
-  return gb::norm::launch<__nv_bfloat16, float, __nv_bfloat16>(a, st);
+  return gb::norm::launch<__nv_bfloat16, float, __nv_bfloat16, false>(a, st);
 }

@@ -2,5 +2,5 @@
 #include "k_norm.cuh"
 
 cudaError_t launch_norm_ff(const NormArgs& a, cudaStream_t st) {
-  return gb::norm::launch<float, float>(a, st);
+  return gb::norm::launch<float, float, float, false>(a, st);
 }

@@ -1,0 +1,414 @@
+// Product with integer 4-bit weights for few rows of X (one token to a small batch).
+//
+// Bound by the weights' bytes, and for small layers by latency.  A warp takes 16 outputs and
+// every WC-th tile of 128 inputs; the warps of a block share the reduction and add their sums
+// through shared memory in a fixed order.  x is converted to bf16 (fp32: three parts) once a
+// block and stays in shared memory, so a block walks over many outputs.  The weights come
+// through a ring of a warp's own (bulk copies, up to eight tiles of 1 KB on their way): a
+// lane's 16 bytes of a tile are the A operands of eight m16n8k16 MMAs, taken apart by three
+// instructions a pair of weights, and the same MMAs serve up to eight rows: CUDA cores alone
+// would need an instruction a weight and row more than the SM has while the bytes arrive.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "internal.h"
+#include "ptx.cuh"
+#include "w4.cuh"
+
+namespace {
+using namespace gb::w4;
+
+constexpr int WARPS = 8, THREADS = 32 * WARPS;
+constexpr int MOST_STAGES = 8;
+constexpr int MOST_SMEM = 224 * 1024;
+constexpr int X_PAD = 64;  // bytes between rows of x: two rows' pieces meet no bank twice
+
+struct FewParams {
+  int M, C, K, ct, wc_log2;  // tiles of a row; warps that share a reduction
+  int row_groups;            // of 16 outputs
+  int pitch;                 // bytes of a row of x in shared memory
+  int stages;                // of a warp's ring
+  int x_group, vec_x, y_f32, act;
+  const uint8_t *codes, *zeros;
+  const void* scales;
+  const void* x;
+  const float* xs;
+  long long ldx;
+  const float* bias;
+  const void* res;
+  long long ldr, ldy;
+  void* y;
+  int* err;
+  unsigned long long wait_ns;
+};
+
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                    uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// A stage of a warp's ring: 16 outputs' codes, scales and zeros of a tile.
+template <int PER, bool F32>
+struct Stage {
+  static constexpr int CODES = 1024, SCALES = 16 * PER * (F32 ? 4 : 2), ZEROS = 16 * PER;
+  static constexpr int BYTES = CODES + SCALES + ZEROS;
+
+  // one thread
+  static __device__ __forceinline__ void fetch(uint8_t* to, uint64_t* full, const FewParams& p,
+                                               int rg, int j) {
+    const size_t row = ((size_t)(rg >> 3) * p.ct + j) * TILE + (rg & 7) * 16;
+    gb::mbar_arrive_expect_tx(full, BYTES);
+    gb::bulk_load(to, p.codes + row * 64, full, CODES);
+    if constexpr (PER != 0) {
+      gb::bulk_load(to + CODES, static_cast<const uint8_t*>(p.scales) + row * (SCALES / 16), full,
+                    SCALES);
+      gb::bulk_load(to + CODES + SCALES, p.zeros + row * PER, full, ZEROS);
+    }
+  }
+  static __device__ __forceinline__ float scale(const uint8_t* stage, int r, int g) {
+    const uint8_t* const p = stage + CODES + (r * PER + g) * (F32 ? 4 : 2);
+    if constexpr (F32) return *reinterpret_cast<const float*>(p);
+    return __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t*>(p) << 16);
+  }
+  // the zeros of an output, one a byte
+  static __device__ __forceinline__ uint32_t zeros(const uint8_t* stage, int r) {
+    const uint8_t* const p = stage + CODES + SCALES + r * PER;
+    if constexpr (PER == 4) return *reinterpret_cast<const uint32_t*>(p);
+    if constexpr (PER == 2) return *reinterpret_cast<const uint16_t*>(p);
+    return *p;
+  }
+};
+
+// PER: groups in 128 inputs (0: one per output).  NT: MMAs of eight rows.
+template <int XIO, int PER, bool F32, int NT>
+__global__ void __launch_bounds__(THREADS, 2) w4_few_kernel(const FewParams p) {
+  constexpr int PARTS = kParts<XIO>;
+  constexpr bool Q8 = XIO == CONV_W4_IO_E4M3 || XIO == CONV_W4_IO_INT8;
+  using S = Stage<PER, F32>;
+  extern __shared__ uint4 smem4[];
+  __shared__ uint64_t full_all[WARPS][MOST_STAGES];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, q = lane & 3;
+  uint8_t* const ring = reinterpret_cast<uint8_t*>(smem4) + warp * p.stages * S::BYTES;
+  uint8_t* const sx = reinterpret_cast<uint8_t*>(smem4) + WARPS * p.stages * S::BYTES;
+  const int part_bytes = p.M * p.pitch;  // of one of x's parts
+  float* const sums = reinterpret_cast<float*>(sx + PARTS * part_bytes);  // [2][WARPS][8 NT][16]
+  float* const sxs = sums + 2 * WARPS * NT * 128;                         // [M][ct]: x_group
+  uint64_t* const full = full_all[warp];
+  const int wc = 1 << p.wc_log2, at_once = WARPS >> p.wc_log2;  // row groups of a block
+  const int sub = warp >> p.wc_log2, j0 = warp & (wc - 1);
+  gb::allow_dependents();
+  const int rg0 = blockIdx.x * at_once + sub, rg_step = gridDim.x * at_once;
+  // the first weights on their way to L2 while the kernel before this one ends (whatever it
+  // still writes, L2 holds)
+  if (rg0 < p.row_groups && lane < p.stages && j0 + lane * wc < p.ct) {
+    const uint8_t* const at =
+        p.codes + (((size_t)(rg0 >> 3) * p.ct + j0 + lane * wc) * TILE + (rg0 & 7) * 16) * 64;
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(at), "r"(1024) : "memory");
+  }
+  if (lane == 0) {
+    for (int i = 0; i < p.stages; ++i) gb::mbar_init(&full[i], 1);
+    gb::fence_barrier_init();
+  }
+  __syncwarp();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  // the (row group, tile) pairs of this warp, in order
+  int frg = rg0, fj = j0, issued = 0;
+  const auto fetch = [&](int stage) {  // lane 0
+    S::fetch(ring + stage * S::BYTES, &full[stage], p, frg, fj);
+    ++issued;
+    if ((fj += wc) >= p.ct) {
+      fj = j0;
+      frg += rg_step;
+    }
+  };
+  if (lane == 0)
+    for (int i = 0; i < p.stages && frg < p.row_groups; ++i) fetch(i);
+
+  // x into shared memory
+  const int pieces = p.pitch / 16 - X_PAD / 16, all = p.M * pieces;
+  for (int i0 = threadIdx.x; i0 < all; i0 += 4 * THREADS) {
+    Raw8<XIO> raw[4];
+    int m[4], c[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = i0 + k * THREADS;
+      if (i >= all) break;
+      m[k] = i / pieces;
+      c[k] = (i - m[k] * pieces) * 8;
+      raw[k].load(static_cast<const uint8_t*>(p.x) + m[k] * p.ldx * kElemBytes<XIO>, c[k], p.C,
+                  p.vec_x);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (i0 + k * THREADS >= all) break;
+#pragma unroll
+      for (int h = 0; h < PARTS; ++h)
+        *reinterpret_cast<uint4*>(sx + h * part_bytes + m[k] * p.pitch + c[k] * 2) =
+            raw[k].part(h);
+    }
+  }
+  if (p.x_group)
+    for (int i = threadIdx.x; i < p.M * p.ct; i += THREADS) sxs[i] = p.xs[i];
+  __syncthreads();
+
+  // B operands: row r of x (rows past M: any; their sums are not stored)
+  const uint8_t* bx[NT];
+  int bs[NT][2];  // x_group: the scales of this lane's two columns
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    bx[n] = sx + (8 * n + r < p.M ? 8 * n + r : 0) * p.pitch + 16 * q;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int m = 8 * n + 2 * q + i;
+      bs[n][i] = (m < p.M ? m : 0) * p.ct;
+    }
+  }
+  int turn = 0, stage = 0, taken = 0;
+  uint32_t phase = 0;
+  bool ok = true;  // after a wait that ran out nothing is waited for or fetched again (the
+                   // sums are then wrong, and the error word says so)
+  // all warps go round together
+  for (int rgb = blockIdx.x * at_once; rgb < p.row_groups; rgb += rg_step) {
+    const int rg = rgb + sub;
+    float acc[NT][4] = {};
+    if (rg < p.row_groups) {
+      uint32_t za0 = 0, zb0 = 0;
+      if constexpr (PER == 0) {
+        za0 = p.zeros[rg * 16 + r];
+        zb0 = p.zeros[rg * 16 + r + 8];
+      }
+      for (int j = j0; j < p.ct && ok; j += wc) {
+        ok = gb::mbar_wait_bounded_warp(&full[stage], phase, p.wait_ns, p.err);
+        if (!ok) break;
+        ++taken;
+        {
+          const uint8_t* const w = ring + stage * S::BYTES;
+          const uint4 wa = *reinterpret_cast<const uint4*>(w + r * 64 + 16 * q);
+          const uint4 wb = *reinterpret_cast<const uint4*>(w + (r + 8) * 64 + 16 * q);
+          const uint32_t aw[4] = {wa.x, wa.y, wa.z, wa.w}, bw[4] = {wb.x, wb.y, wb.z, wb.w};
+          uint32_t zas = za0, zbs = zb0;
+          if constexpr (PER != 0) {
+            zas = S::zeros(w, r);
+            zbs = S::zeros(w, r + 8);
+          }
+          float part[NT][4] = {};
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            constexpr int SPAN = PER ? 4 / PER : 4;  // words of a group
+            const uint32_t za = (zas >> (8 * (t / SPAN))) & 15u;
+            const uint32_t zb = (zbs >> (8 * (t / SPAN))) & 15u;
+            const uint32_t zza = zero_pair(za), zzb = zero_pair(zb);
+            const uint32_t a0 = weight_pair<0>(aw[t], zza), a1 = weight_pair<1>(aw[t], zza),
+                           a2 = weight_pair<2>(aw[t], zza), a3 = weight_pair<3>(aw[t], zza);
+            const uint32_t b0 = weight_pair<0>(bw[t], zzb), b1 = weight_pair<1>(bw[t], zzb),
+                           b2 = weight_pair<2>(bw[t], zzb), b3 = weight_pair<3>(bw[t], zzb);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              float(&sum)[4] = PER == 0 && !Q8 ? acc[n] : part[n];
+#pragma unroll
+              for (int h = 0; h < PARTS; ++h) {
+                const uint4 xb = *reinterpret_cast<const uint4*>(bx[n] + h * part_bytes +
+                                                                 j * 256 + 64 * t);
+                mma(sum, a0, b0, a1, b1, xb.x, xb.y);
+                mma(sum, a2, b2, a3, b3, xb.z, xb.w);
+              }
+            }
+            if constexpr (PER != 0) {
+              if (t % SPAN == SPAN - 1) {
+                const float sa = S::scale(w, r, t / SPAN), sb = S::scale(w, r + 8, t / SPAN);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                  float x0 = 1.0f, x1 = 1.0f;
+                  if (Q8 && p.x_group) {
+                    x0 = sxs[bs[n][0] + j];
+                    x1 = sxs[bs[n][1] + j];
+                  }
+                  acc[n][0] = fmaf(part[n][0], sa * x0, acc[n][0]);
+                  acc[n][1] = fmaf(part[n][1], sa * x1, acc[n][1]);
+                  acc[n][2] = fmaf(part[n][2], sb * x0, acc[n][2]);
+                  acc[n][3] = fmaf(part[n][3], sb * x1, acc[n][3]);
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) part[n][i] = 0.0f;
+                }
+              }
+            }
+          }
+          if constexpr (PER == 0 && Q8) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              float x0 = 1.0f, x1 = 1.0f;
+              if (p.x_group) {
+                x0 = sxs[bs[n][0] + j];
+                x1 = sxs[bs[n][1] + j];
+              }
+              acc[n][0] = fmaf(part[n][0], x0, acc[n][0]);
+              acc[n][1] = fmaf(part[n][1], x1, acc[n][1]);
+              acc[n][2] = fmaf(part[n][2], x0, acc[n][2]);
+              acc[n][3] = fmaf(part[n][3], x1, acc[n][3]);
+            }
+          }
+        }
+        __syncwarp();  // every lane has read the stage
+        if (lane == 0 && frg < p.row_groups) fetch(stage);
+        if (++stage == p.stages) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+    }
+    // [turn][warp][column][output of 16]
+    float* const to = sums + (turn * WARPS + warp) * NT * 128;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        to[(8 * n + 2 * q + (i & 1)) * 16 + r + 8 * (i >> 1)] = acc[n][i];
+    __syncthreads();
+    const int o = threadIdx.x & 15, s = (threadIdx.x >> 4) & (at_once - 1);
+    const int k = (rgb + s) * 16 + o;
+    if (k < p.K) {
+      const float row_scale =
+          PER == 0 ? (F32 ? static_cast<const float*>(p.scales)[k]
+                          : __bfloat162float(static_cast<const __nv_bfloat16*>(p.scales)[k]))
+                   : 1.0f;
+      const float bias = p.bias ? p.bias[k] : 0.0f;
+      for (int m = (threadIdx.x >> 4) >> (3 - p.wc_log2); m < p.M; m += 2 * wc) {
+        const float* const from =
+            sums + ((turn * WARPS + (s << p.wc_log2)) * NT * 8 + m) * 16 + o;
+        float v = 0.0f;
+        for (int i = 0; i < wc; ++i) v += from[i * NT * 128];
+        if (PER == 0) v *= row_scale;
+        if (Q8 && !p.x_group) v *= p.xs[m];
+        float e[2] = {v + bias, 0.0f};
+        if (p.y_f32) {
+          if (p.res) e[0] += static_cast<const float*>(p.res)[m * p.ldr + k];
+          gb::fp4::activate<true>(e, p.act);
+          static_cast<float*>(p.y)[m * p.ldy + k] = e[0];
+        } else {
+          if (p.res)
+            e[0] += __bfloat162float(static_cast<const __nv_bfloat16*>(p.res)[m * p.ldr + k]);
+          gb::fp4::activate<false>(e, p.act);
+          static_cast<__nv_bfloat16*>(p.y)[m * p.ldy + k] = __float2bfloat16_rn(e[0]);
+        }
+      }
+    }
+    turn ^= 1;
+  }
+  if (lane == 0 && !ok) {
+    // copies that were on their way when a wait ran out
+    for (; taken < issued; ++taken) {
+      gb::mbar_wait_bounded(&full[stage], phase, p.wait_ns, p.err);
+      if (++stage == p.stages) {
+        stage = 0;
+        phase ^= 1;
+      }
+    }
+  }
+}
+
+// Shared memory: x (and its scales), the warps' sums, and the ring, as deep as there is room
+// for in half an SM's (or, where x is larger, all of it); stages 0: x does not fit.
+struct FewSmem {
+  int bytes, stages;
+};
+FewSmem few_smem(const W4Gemm& g) {
+  const int per = g.group ? TILE / g.group : 0;
+  const long long stage = WARPS * (1024 + 16 * per * (g.scale_f32 ? 5 : 3));
+  const long long ct = gb_ceil_div(g.C, TILE);
+  const long long parts = g.x_io == CONV_W4_IO_F32 ? 3 : 1, nt = g.M > 8 ? 2 : 1;
+  const long long fixed = parts * g.M * (ct * 256 + X_PAD) + 2 * WARPS * nt * 512 +
+                          (g.x_group ? g.M * ct * 4 : 0);
+  for (const long long most : {112 * 1024LL, (long long)MOST_SMEM}) {
+    const long long stages = std::min<long long>(MOST_STAGES, (most - fixed) / stage);
+    if (fixed < most && stages >= 4) return {(int)(fixed + stages * stage), (int)stages};
+  }
+  return {0, 0};
+}
+
+template <int XIO, int PER, bool F32, int NT>
+cudaError_t launch_t(const W4Gemm& g, cudaStream_t st) {
+  const Packed w = packed_layout(g.C, g.K, g.group, g.scale_f32 ? 4 : 2);
+  FewParams p{};
+  p.M = g.M;
+  p.C = g.C;
+  p.K = g.K;
+  p.ct = w.ct;
+  p.wc_log2 = 0;
+  while (p.wc_log2 < 3 && (2 << p.wc_log2) <= w.ct) ++p.wc_log2;
+  p.row_groups = gb_ceil_div(g.K, 16);
+  p.pitch = w.ct * 256 + X_PAD;
+  p.x_group = g.x_group;
+  p.vec_x = rows_vec8(g.x_io, g.x, g.ldx);
+  p.y_f32 = g.y_f32;
+  p.act = g.act;
+  p.codes = g.packed;
+  p.zeros = g.packed + w.zeros;
+  p.scales = g.packed + w.scales;
+  p.x = g.x;
+  p.xs = g.xs;
+  p.ldx = g.ldx;
+  p.bias = g.bias;
+  p.res = g.res;
+  p.ldr = g.ldr;
+  p.ldy = g.ldy;
+  p.y = g.y;
+  p.err = gb_device_error_word();
+  p.wait_ns = gb_wait_limit_ns();
+  auto* kern = w4_few_kernel<XIO, PER, F32, NT>;
+  const FewSmem sm = few_smem(g);
+  const int smem = sm.bytes;
+  p.stages = sm.stages;
+  cudaError_t e = gb_set_smem_once(reinterpret_cast<const void*>(kern), MOST_SMEM);
+  if (e != cudaSuccess) return e;
+  const long long per_sm =
+      std::max(1, std::min(2, gb_blocks_per_sm(reinterpret_cast<const void*>(kern), THREADS, smem)));
+  const long long need = gb_ceil_div(p.row_groups, WARPS >> p.wc_log2);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)std::min(need, per_sm * gb_num_sms()));
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kern, p);
+  if (e == cudaSuccess) gb_count_launch();
+  return e;
+}
+
+template <int XIO, int PER, bool F32>
+cudaError_t launch_rows(const W4Gemm& g, cudaStream_t st) {
+  return g.M > 8 ? launch_t<XIO, PER, F32, 2>(g, st) : launch_t<XIO, PER, F32, 1>(g, st);
+}
+template <int XIO, int PER>
+cudaError_t launch_scales(const W4Gemm& g, cudaStream_t st) {
+  return g.scale_f32 ? launch_rows<XIO, PER, true>(g, st) : launch_rows<XIO, PER, false>(g, st);
+}
+template <int XIO>
+cudaError_t launch_group(const W4Gemm& g, cudaStream_t st) {
+  if (g.group == 0) return launch_scales<XIO, 0>(g, st);
+  if (g.group == 128) return launch_scales<XIO, 1>(g, st);
+  if (g.group == 64) return launch_scales<XIO, 2>(g, st);
+  return launch_scales<XIO, 4>(g, st);
+}
+
+}  // namespace
+
+bool w4_few_applicable(const W4Gemm& g) { return g.M <= 16 && few_smem(g).stages > 0; }
+
+cudaError_t launch_w4_few(const W4Gemm& g, cudaStream_t st) {
+  switch (g.x_io) {
+    case CONV_W4_IO_BF16: return launch_group<CONV_W4_IO_BF16>(g, st);
+    case CONV_W4_IO_F32: return launch_group<CONV_W4_IO_F32>(g, st);
+    case CONV_W4_IO_E4M3: return launch_group<CONV_W4_IO_E4M3>(g, st);
+    default: return launch_group<CONV_W4_IO_INT8>(g, st);
+  }
+}

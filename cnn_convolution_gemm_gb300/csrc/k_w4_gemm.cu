@@ -1,0 +1,678 @@
+// Product with integer 4-bit weights for many rows of X, on tcgen05: y^T = W X^T, so that the
+// tensor core's 128 rows are outputs, whose scales are then a thread's own.
+//
+// A persistent CTA takes tiles of 128 outputs x NT rows of X.  Code - zero is a whole number of
+// at most four bits and a sign, which bf16 holds exactly; so do 8-bit and bf16 x, and three
+// parts of fp32 x.  The weights' scales therefore stay out of the product: the MMAs sum one
+// group of inputs at a time in TMEM (or all of them, where a row has one scale), and the
+// threads that keep the tile's sums in registers add scale * sum to them in fp32.
+//
+// Warp 0 loads X (TMA), warp 2 the packed weights, warp 1 issues the MMAs (one elected lane);
+// one or two warpgroups take the codes apart into swizzled bf16 tiles; the others scale and
+// sum, and run the epilogue (through TMEM, so that it is a loop over columns).  Few tiles with
+// long reductions are split over the CTAs of a cluster, which add their sums through
+// distributed shared memory in a fixed order.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "fp4.cuh"
+#include "internal.h"
+#include "ptx.cuh"
+#include "w4.cuh"
+
+namespace {
+using namespace gb::w4;
+using gb::fp4::fma2;
+using gb::fp4::mul2;
+using gb::fp4::pack2;
+using gb::fp4::unpack2;
+
+constexpr int THREADS = 512;
+constexpr int BK = 64;  // inputs of a step: 128 bytes of bf16
+
+template <int NT>
+struct Cfg {
+  static constexpr int SUM_WGS = NT == 256 ? 2 : 1;   // that scale and sum
+  static constexpr int TAKE_WGS = 3 - SUM_WGS;        // that take codes apart
+  static constexpr int COLS = NT / SUM_WGS;           // columns of a summing thread
+  static constexpr int NB = NT == 256 ? 2 : 4;        // accumulators in TMEM
+  static constexpr int TMEM_COLS = NB * NT;
+  static constexpr int X_BYTES = NT * BK * 2;
+  static constexpr int X_STAGES = NT == 256 ? 4 : NT == 128 ? 5 : 8;
+  static constexpr int A_BYTES = TILE * BK * 2;
+  static constexpr int A_STAGES = 3;
+  static constexpr int W_STAGES = NT == 256 ? 3 : 6;
+  static constexpr int W_BYTES = TILE_BYTES + TILE * 4 * 5;  // codes, scales, zeros at most
+  static constexpr int X_SCALES = 2 * NT * 4;
+  static constexpr int SMEM = X_STAGES * X_BYTES + A_STAGES * A_BYTES + W_STAGES * W_BYTES +
+                              X_SCALES + 512 + 1024;
+  // registers of the threads that take apart, load and issue, and of those that sum: together
+  // at most the 128 that each of the 512 is launched with
+  static constexpr bool SPLIT_REGS = NT >= 128;
+  static constexpr int REGS_TAKE = NT == 256 ? 64 : 96, REGS_SUM = NT == 256 ? 192 : 216;
+  static_assert((4 - SUM_WGS) * REGS_TAKE + SUM_WGS * REGS_SUM <= 4 * 128, "registers");
+  static_assert(TMEM_COLS <= 512 && SMEM <= 232448, "TMEM, shared memory");
+  static_assert(X_STAGES * X_BYTES >= NT * 512, "a cluster's sums take X's place");
+};
+
+struct Params {
+  int M, C, K, ct, mt, tiles;   // tiles of inputs, of rows, of all
+  int steps;                    // BK inputs each
+  int parts, per, scale_bytes;  // of x; groups in 128 inputs, 0: one per output
+  int box_rows, n;              // rows of a load of X, columns of an MMA
+  int split_log2;               // CTAs of a cluster
+  int q8, x_group, act;
+  const uint8_t *codes, *zeros;
+  const uint8_t* scales;
+  const float* xs;
+  const float* bias;
+  const void* res;
+  long long ldr, ldy;
+  void* y;
+  int* err;
+  unsigned long long wait_ns;
+};
+
+// Output k of rows m, m + step, .. (rows of them); lanes of a warp are 32 consecutive outputs.
+template <typename T>
+__device__ __forceinline__ void finish(const Params& p, float (&v)[8], int m, int step, int rows,
+                                       int k, float scale, float bias) {
+  if (k >= p.K) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float s = scale;
+    if (p.q8 && !p.x_group && i < rows) s *= p.xs[m + i * step];
+    v[i] = fmaf(v[i], s, bias);
+  }
+  if (p.res) {
+    const T* const res = static_cast<const T*>(p.res) + m * p.ldr + k;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < rows) v[i] += gb::fp4::load_f32(res + i * step * p.ldr);
+  }
+  gb::fp4::activate<sizeof(T) == 4>(v, p.act);
+  T* const y = static_cast<T*>(p.y) + m * p.ldy + k;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < rows) gb::fp4::store_f32(y + i * step * p.ldy, v[i]);
+}
+
+__device__ __forceinline__ float scale_at(const uint8_t* scales, size_t i, int bytes) {
+  return bytes == 4
+             ? reinterpret_cast<const float*>(scales)[i]
+             : __uint_as_float((uint32_t) reinterpret_cast<const uint16_t*>(scales)[i] << 16);
+}
+
+// A ring's position.
+struct Turn {
+  int at = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next(int stages) {
+    if (++at == stages) {
+      at = 0;
+      phase ^= 1;
+    }
+  }
+  __device__ __forceinline__ void back(int stages) {
+    if (--at < 0) {
+      at = stages - 1;
+      phase ^= 1;
+    }
+  }
+};
+
+template <int NT, typename T>
+__global__ void __launch_bounds__(THREADS, 1)
+    w4_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const Params p) {
+  using C = Cfg<NT>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* const smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* const sX = smem;
+  uint8_t* const sA = sX + C::X_STAGES * C::X_BYTES;
+  uint8_t* const sW = sA + C::A_STAGES * C::A_BYTES;
+  float* const sXS = reinterpret_cast<float*>(sW + C::W_STAGES * C::W_BYTES);  // [2][NT]
+  uint64_t* const x_full = reinterpret_cast<uint64_t*>(sXS + 2 * NT);
+  uint64_t* const x_empty = x_full + C::X_STAGES;
+  uint64_t* const a_full = x_empty + C::X_STAGES;
+  uint64_t* const a_empty = a_full + C::A_STAGES;
+  uint64_t* const w_full = a_empty + C::A_STAGES;
+  uint64_t* const w_empty = w_full + C::W_STAGES;
+  uint64_t* const d_full = w_empty + C::W_STAGES;
+  uint64_t* const d_empty = d_full + C::NB;
+  uint64_t* const given_up = d_empty + C::NB;
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(given_up + 1);
+
+  const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0);  // uniform
+  const int lane = threadIdx.x & 31, wg = warp >> 2;
+  const int split = 1 << p.split_log2, rank = blockIdx.x & (split - 1);
+  const int first = blockIdx.x >> p.split_log2, step = gridDim.x >> p.split_log2;
+  // this CTA's tiles of inputs
+  const int c0 = (int)((long long)p.ct * rank >> p.split_log2);
+  const int c1 = (int)((long long)p.ct * (rank + 1) >> p.split_log2);
+  // one sum for the whole row: neither the weights nor x change their scale along it
+  const bool whole = p.per == 0 && !p.x_group;
+  const auto halves = [&](int c) { return min(2, p.steps - 2 * c); };  // steps of a tile
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::X_STAGES; ++s) {
+      gb::mbar_init(&x_full[s], 1);
+      gb::mbar_init(&x_empty[s], 1);
+    }
+    for (int s = 0; s < C::A_STAGES; ++s) {
+      gb::mbar_init(&a_full[s], 4 * C::TAKE_WGS);
+      gb::mbar_init(&a_empty[s], 1);
+    }
+    for (int s = 0; s < C::W_STAGES; ++s) {
+      gb::mbar_init(&w_full[s], 1);
+      gb::mbar_init(&w_empty[s], 4 * C::TAKE_WGS + (p.per ? 4 * C::SUM_WGS : 0));
+    }
+    for (int s = 0; s < C::NB; ++s) {
+      gb::mbar_init(&d_full[s], 1);
+      gb::mbar_init(&d_empty[s], 4 * C::SUM_WGS);
+    }
+    gb::mbar_init(given_up, 1);
+    gb::fence_barrier_init();
+    gb::tma_prefetch_desc(&tm_x);
+  }
+  if (warp == 3) {
+    gb::tmem_alloc(tmem_slot, C::TMEM_COLS);
+    gb::tmem_relinquish();
+  }
+  gb::tc_fence_before();
+  __syncthreads();
+  if (split > 1) gb::cluster_sync();
+  gb::tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
+  gb::allow_dependents();
+
+  if (wg == 0) {
+    if constexpr (C::SPLIT_REGS) gb::registers_down_to<C::REGS_TAKE>();
+    if (warp == 0) {
+      // ---------------- X ----------------
+      const bool one = gb::elect_one();
+      const uint32_t tx = (uint32_t)p.box_rows * (BK * 2);
+      Turn x;
+      int issued = 0;
+      bool ok = true;
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      for (int tile = first; tile < p.tiles && ok; tile += step) {
+        const int m0 = tile % p.mt * NT;
+        for (int s = 2 * c0; s < min(2 * c1, p.steps) && ok; ++s)
+          for (int h = 0; h < p.parts; ++h) {
+            ok = gb::mbar_wait_bounded_warp(&x_empty[x.at], x.phase ^ 1, p.wait_ns, p.err);
+            if (!ok) break;
+            if (one) {
+              gb::mbar_arrive_expect_tx(&x_full[x.at], tx);
+              gb::tma_load_3d(sX + x.at * C::X_BYTES, &tm_x, &x_full[x.at], s * BK, m0, h);
+            }
+            __syncwarp();
+            ++issued;
+            x.next(C::X_STAGES);
+          }
+      }
+      // no copy into shared memory may be in flight at exit
+      for (int i = min(issued, C::X_STAGES); i > 0; --i) {
+        x.back(C::X_STAGES);
+        gb::mbar_wait_bounded_warp(&x_full[x.at], x.phase, p.wait_ns, p.err);
+      }
+    } else if (warp == 2) {
+      // ---------------- packed weights ----------------
+      const bool one = gb::elect_one();
+      const uint32_t sb = TILE * p.per * p.scale_bytes, zb = TILE * p.per;
+      Turn w;
+      int issued = 0;
+      bool ok = true;
+      // the first of them on their way to L2 while the kernel before this one ends (whatever
+      // it still writes, L2 holds)
+      if (first < p.tiles && lane < C::W_STAGES && c0 + lane < c1)
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
+                         p.codes + ((size_t)(first / p.mt) * p.ct + c0 + lane) * TILE_BYTES),
+                     "r"(TILE_BYTES)
+                     : "memory");
+      __syncwarp();
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      for (int tile = first; tile < p.tiles && ok; tile += step)
+        for (int c = c0; c < c1; ++c) {
+          ok = gb::mbar_wait_bounded_warp(&w_empty[w.at], w.phase ^ 1, p.wait_ns, p.err);
+          if (!ok) break;
+          if (one) {
+            const size_t t = (size_t)(tile / p.mt) * p.ct + c;
+            uint8_t* const to = sW + w.at * C::W_BYTES;
+            gb::mbar_arrive_expect_tx(&w_full[w.at], TILE_BYTES + sb + zb);
+            gb::bulk_load(to, p.codes + t * TILE_BYTES, &w_full[w.at], TILE_BYTES);
+            if (p.per) {
+              gb::bulk_load(to + TILE_BYTES, p.scales + t * sb, &w_full[w.at], sb);
+              gb::bulk_load(to + TILE_BYTES + sb, p.zeros + t * zb, &w_full[w.at], zb);
+            }
+          }
+          __syncwarp();
+          ++issued;
+          w.next(C::W_STAGES);
+        }
+      for (int i = min(issued, C::W_STAGES); i > 0; --i) {
+        w.back(C::W_STAGES);
+        gb::mbar_wait_bounded_warp(&w_full[w.at], w.phase, p.wait_ns, p.err);
+      }
+    } else if (warp == 1) {
+      // ---------------- MMAs ----------------
+      const bool one = gb::elect_one();
+      const uint32_t id = gb::idesc_f16(128, p.n, 1);
+      const int subs = p.per == 4 ? 2 : 1;  // accumulators of a step
+      Turn x, a, d;
+      int open[2] = {0, 0};
+      bool ok = true;
+      for (int tile = first; tile < p.tiles && ok; tile += step)
+        for (int c = c0; c < c1 && ok; ++c)
+          for (int h = 0; h < halves(c) && ok; ++h) {
+            const bool starts = whole ? c == c0 && h == 0 : p.per >= 2 || h == 0;
+            const bool ends = whole ? c == c1 - 1 && h == halves(c) - 1
+                                    : p.per >= 2 || h == halves(c) - 1;
+            if (starts)
+              for (int u = 0; u < subs && ok; ++u) {
+                ok = gb::mbar_wait_bounded_warp(&d_empty[d.at], d.phase ^ 1, p.wait_ns, p.err);
+                open[u] = d.at;
+                d.next(C::NB);
+              }
+            ok = ok && gb::mbar_wait_bounded_warp(&a_full[a.at], a.phase, p.wait_ns, p.err);
+            const uint64_t ad = gb::sw128_kmajor_desc(gb::smem_u32(sA + a.at * C::A_BYTES));
+            for (int part = 0; part < p.parts && ok; ++part) {
+              ok = gb::mbar_wait_bounded_warp(&x_full[x.at], x.phase, p.wait_ns, p.err);
+              if (!ok) break;
+              gb::tc_fence_after();
+              if (one) {
+                const uint64_t xd = gb::sw128_kmajor_desc(gb::smem_u32(sX + x.at * C::X_BYTES));
+                const bool fresh = starts && part == 0;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const int u = subs == 2 ? k >> 1 : 0;
+                  const bool clear = fresh && (subs == 2 ? (k & 1) == 0 : k == 0);
+                  gb::tc_mma_f16(tmem + (u ? open[1] : open[0]) * NT, ad + k * 2, xd + k * 2, id,
+                                 clear ? 0u : 1u);
+                }
+                gb::tc_commit(&x_empty[x.at]);
+              }
+              __syncwarp();
+              x.next(C::X_STAGES);
+            }
+            if (!ok) break;
+            if (one) {
+              gb::tc_commit(&a_empty[a.at]);
+              if (ends)
+                for (int u = 0; u < subs; ++u) gb::tc_commit(&d_full[u ? open[1] : open[0]]);
+            }
+            __syncwarp();
+            a.next(C::A_STAGES);
+          }
+      if (!ok) {
+        // the MMAs that were issued end before the memory they use is given up
+        if (one) gb::tc_commit(given_up);
+        __syncwarp();
+        gb::mbar_wait_bounded_warp(given_up, 0, p.wait_ns, p.err);
+      }
+    }
+  } else if (wg <= C::TAKE_WGS) {
+    // ---------------- codes to bf16 ----------------
+    if constexpr (C::SPLIT_REGS) gb::registers_down_to<C::REGS_TAKE>();
+    constexpr int PIECES = 4 / C::TAKE_WGS;  // 16 bytes of an output's codes each
+    const int t0 = threadIdx.x - 128;        // piece t0 + 128 TAKE_WGS i
+    const uint32_t zb = TILE_BYTES + TILE * p.per * p.scale_bytes;
+    Turn w, a;
+    bool ok = true;
+    if (p.per == 0) asm volatile("griddepcontrol.wait;" ::: "memory");  // zeros from memory
+    for (int tile = first; tile < p.tiles && ok; tile += step) {
+      uint32_t row_zero[PIECES];
+      if (p.per == 0)
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i)
+          row_zero[i] =
+              p.zeros[tile / p.mt * TILE + ((t0 + 128 * C::TAKE_WGS * i) >> 2)] * 0x01010101u;
+      for (int c = c0; c < c1 && ok; ++c) {
+        ok = gb::mbar_wait_bounded_warp(&w_full[w.at], w.phase, p.wait_ns, p.err);
+        if (!ok) break;
+        const uint8_t* const from = sW + w.at * C::W_BYTES;
+        uint4 code[PIECES];
+        uint32_t zero[PIECES];  // of the words 0 .. 3, one a byte
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i) {
+          const int piece = t0 + 128 * C::TAKE_WGS * i, row = piece >> 2;
+          code[i] = *reinterpret_cast<const uint4*>(from + 16 * piece);
+          const uint8_t* const z = from + zb + row * p.per;
+          zero[i] = p.per == 1   ? *z * 0x01010101u
+                    : p.per == 2 ? *reinterpret_cast<const uint16_t*>(z) * 0x00010001u
+                    : p.per == 4 ? *reinterpret_cast<const uint32_t*>(z)
+                                 : row_zero[i];
+          if (p.per == 2) zero[i] = __byte_perm(zero[i], 0u, 0x1100);
+          // outputs of odd number take the two words of a step the other way round: the
+          // eight lanes that store together then meet no bank twice
+          if (row & 1) {
+            code[i] = make_uint4(code[i].y, code[i].x, code[i].w, code[i].z);
+            zero[i] = __byte_perm(zero[i], 0u, 0x2301);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) gb::mbar_arrive(&w_empty[w.at]);
+        w.next(C::W_STAGES);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (h >= halves(c)) break;
+          ok = gb::mbar_wait_bounded_warp(&a_empty[a.at], a.phase ^ 1, p.wait_ns, p.err);
+          if (!ok) break;
+          uint8_t* const to = sA + a.at * C::A_BYTES;
+#pragma unroll
+          for (int i = 0; i < PIECES; ++i) {
+            const int piece = t0 + 128 * C::TAKE_WGS * i, row = piece >> 2, q = piece & 3;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              const uint32_t word = h ? (t ? code[i].w : code[i].z) : (t ? code[i].y : code[i].x);
+              const uint32_t zz = zero_pair((zero[i] >> (8 * (2 * h + t))) & 15u);
+              const int slot = ((t ^ (row & 1)) * 4 + q) ^ (row & 7);
+              *reinterpret_cast<uint4*>(to + row * 128 + slot * 16) =
+                  make_uint4(weight_pair<0>(word, zz), weight_pair<1>(word, zz),
+                             weight_pair<2>(word, zz), weight_pair<3>(word, zz));
+            }
+          }
+          gb::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) gb::mbar_arrive(&a_full[a.at]);
+          a.next(C::A_STAGES);
+        }
+      }
+    }
+  } else {
+    // ---------------- scales, sums, epilogue ----------------
+    if constexpr (C::SPLIT_REGS) gb::registers_up_to<C::REGS_SUM>();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int part = wg - 1 - C::TAKE_WGS;  // of the columns
+    const int o = (warp & 3) * 32 + lane, col0 = part * C::COLS;
+    const uint32_t t = tmem + ((uint32_t)((warp & 3) * 32) << 16) + col0;
+    float* const xs = sXS + col0;  // [2] of them NT apart
+    Turn w, d;
+    int buffer = 0;  // of x's scales
+    bool ok = true;
+    for (int tile = first; tile < p.tiles && ok; tile += step) {
+      const int m0 = tile % p.mt * NT + col0, k = tile / p.mt * TILE + o;
+      const int live = min(C::COLS, p.M - m0);  // <= 0: none of these columns
+      uint64_t acc[C::COLS / 2];
+#pragma unroll
+      for (int i = 0; i < C::COLS / 2; ++i) acc[i] = 0;
+      const bool scales_x = p.x_group && o < live;
+      const float* const my_xs = scales_x ? p.xs + (long long)(m0 + o) * p.ct : nullptr;
+      float next_xs = scales_x ? my_xs[c0] : 0.0f;
+      uint32_t tc = t;
+      for (int c = c0; c < c1 && ok; ++c) {
+        if (whole && c < c1 - 1) continue;
+        float s[4] = {1.0f, 1.0f, 1.0f, 1.0f};
+        if (p.per) {
+          ok = gb::mbar_wait_bounded_warp(&w_full[w.at], w.phase, p.wait_ns, p.err);
+          if (!ok) break;
+          const uint8_t* const from = sW + w.at * C::W_BYTES + TILE_BYTES;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (i < p.per) s[i] = scale_at(from, o * p.per + i, p.scale_bytes);
+          __syncwarp();
+          if (lane == 0) gb::mbar_arrive(&w_empty[w.at]);
+          w.next(C::W_STAGES);
+        }
+        if (p.x_group) {
+          // the chunk's scales of x, in two buffers used in turn: one barrier is enough
+          buffer ^= NT;
+          if (o < C::COLS) xs[buffer + o] = next_xs;
+          if (scales_x && c + 1 < c1) next_xs = my_xs[c + 1];
+          asm volatile("bar.sync %0, 128;" ::"r"(1 + part) : "memory");
+        }
+        const int sums = p.per <= 1 ? 1 : p.per == 2 ? halves(c) : 2 * halves(c);
+        for (int u = 0; u < sums && ok; ++u) {
+          ok = gb::mbar_wait_bounded_warp(&d_full[d.at], d.phase, p.wait_ns, p.err);
+          if (!ok) break;
+          gb::tc_fence_after();
+          tc = t + d.at * NT;
+          if (whole) break;
+          const float su = u == 0 ? s[0] : u == 1 ? s[1] : u == 2 ? s[2] : s[3];
+          const uint64_t s2 = pack2(su, su);
+#pragma unroll
+          for (int b = 0; b < C::COLS; b += 32) {
+            if (b >= live) break;
+            uint32_t r[32];
+            gb::tmem_ld_x32(tc + b, r);
+            gb::tmem_ld_wait();
+            if (p.x_group) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 4) {
+                const float4 f = *reinterpret_cast<const float4*>(xs + buffer + b + i);
+                acc[(b + i) / 2] =
+                    fma2(pack2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])),
+                         mul2(s2, pack2(f.x, f.y)), acc[(b + i) / 2]);
+                acc[(b + i) / 2 + 1] =
+                    fma2(pack2(__uint_as_float(r[i + 2]), __uint_as_float(r[i + 3])),
+                         mul2(s2, pack2(f.z, f.w)), acc[(b + i) / 2 + 1]);
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; i += 2)
+                acc[(b + i) / 2] = fma2(pack2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])),
+                                        s2, acc[(b + i) / 2]);
+            }
+          }
+          if (c == c1 - 1 && u == sums - 1) break;  // kept for the epilogue
+          gb::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) gb::mbar_arrive(&d_empty[d.at]);
+          d.next(C::NB);
+        }
+      }
+      if (!ok) break;
+      // the sums back to the last accumulator
+      if (!whole) {
+#pragma unroll
+        for (int b = 0; b < C::COLS; b += 32) {
+          if (b >= live) break;
+          uint32_t r[32];
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            float f0, f1;
+            unpack2(acc[(b + i) / 2], f0, f1);
+            r[i] = __float_as_uint(f0);
+            r[i + 1] = __float_as_uint(f1);
+          }
+          gb::tmem_st_x32(tc + b, r);
+        }
+        gb::tmem_st_wait();
+      }
+      if (split == 1) {
+        const float scale = p.per == 0 ? scale_at(p.scales, k, p.scale_bytes) : 1.0f;
+        const float bias = p.bias && k < p.K ? p.bias[k] : 0.0f;
+        for (int b = 0; b < live; b += 8) {
+          uint32_t r[8];
+          gb::tmem_ld_x8(tc + b, r);
+          gb::tmem_ld_wait();
+          float v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+          finish<T>(p, v, m0 + b, 1, min(8, live - b), k, scale, bias);
+        }
+        gb::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) gb::mbar_arrive(&d_empty[d.at]);
+        d.next(C::NB);
+      }
+    }
+    if (split > 1) {
+      // (one tile; all of X has been read once every CTA of the cluster is here)
+      gb::tc_fence_before();
+      __syncwarp();
+      gb::cluster_sync();
+      gb::tc_fence_after();
+      const int m0 = first % p.mt * NT + col0, live = min(C::COLS, p.M - m0);
+      const int rows = min(NT, p.M - first % p.mt * NT);
+      const int places = (rows + split - 1) >> p.split_log2;
+      // row m goes to CTA m % split, place m / split; source rank, place, output
+      const uint32_t mine = gb::smem_u32(sX) + 4 * o + 512 * rank * places;
+      const uint32_t tc = t + d.at * NT;
+      for (int b = 0; b < live; b += 8) {
+        uint32_t r[8];
+        gb::tmem_ld_x8(tc + b, r);
+        gb::tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int m = col0 + b + i;
+          if (b + i < live)
+            gb::store_cluster(gb::mapa_shared(mine + 512 * (m >> p.split_log2),
+                                              (uint32_t)(m & (split - 1))),
+                              r[i]);
+        }
+      }
+      __syncwarp();
+      gb::cluster_sync();
+      const int k = first / p.mt * TILE + o;
+      const float scale = p.per == 0 ? scale_at(p.scales, k, p.scale_bytes) : 1.0f;
+      const float bias = p.bias && k < p.K ? p.bias[k] : 0.0f;
+      const float* const sums = reinterpret_cast<const float*>(sX) + o;
+      for (int i = 8 * part; rank + i * split < rows; i += 8 * C::SUM_WGS) {
+        const int n = min(8, (rows - rank - i * split + split - 1) >> p.split_log2);
+        float v[8] = {};
+        for (int r = 0; r < split; ++r)
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (e < n) v[e] += sums[128 * (r * places + i + e)];
+        finish<T>(p, v, first % p.mt * NT + rank + i * split, split, n, k, scale, bias);
+      }
+    }
+    gb::tc_fence_before();
+  }
+  if (split > 1 && wg <= C::TAKE_WGS) {
+    __syncwarp();
+    gb::cluster_sync();
+    gb::cluster_sync();
+  }
+  __syncthreads();
+  if (warp == 3) {
+    gb::tc_fence_after();
+    gb::tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+// [parts][rows][cols] bf16 in boxes of BK x box_rows
+bool operand_map(CUtensorMap* map, const void* x, int parts, int rows, int cols, long long ld,
+                 int box_rows) {
+  cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)parts};
+  cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)ld * 2 * rows};
+  cuuint32_t box[3] = {BK, (cuuint32_t)box_rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return gb_encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(x), dims,
+                         strides, box, estr, CU_TENSOR_MAP_SWIZZLE_128B) == CUDA_SUCCESS;
+}
+
+// Whether the loads take x where it lies.
+bool in_place(const W4Gemm& g) {
+  return g.x_io == CONV_W4_IO_BF16 && reinterpret_cast<uintptr_t>(g.x) % 16 == 0 &&
+         g.ldx % 8 == 0;
+}
+
+template <int NT, typename T>
+cudaError_t launch_t(const W4Gemm& g, const void* x, int parts, int cols, long long ld,
+                     cudaStream_t st) {
+  using C = Cfg<NT>;
+  const Packed w = packed_layout(g.C, g.K, g.group, g.scale_f32 ? 4 : 2);
+  Params p{};
+  p.M = g.M;
+  p.C = g.C;
+  p.K = g.K;
+  p.ct = w.ct;
+  p.mt = gb_ceil_div(g.M, NT);
+  if ((long long)w.kt * p.mt > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  p.tiles = w.kt * p.mt;
+  p.steps = gb_ceil_div(g.C, BK);
+  p.parts = parts;
+  p.per = w.per;
+  p.scale_bytes = g.scale_f32 ? 4 : 2;
+  p.box_rows = std::min(NT, gb_ceil_div(g.M, 8) * 8);
+  p.n = std::min(NT, gb_ceil_div(g.M, 16) * 16);
+  p.q8 = g.xs != nullptr;
+  p.x_group = g.x_group;
+  p.act = g.act;
+  p.codes = g.packed;
+  p.zeros = g.packed + w.zeros;
+  p.scales = g.packed + w.scales;
+  p.xs = g.xs;
+  p.bias = g.bias;
+  p.res = g.res;
+  p.ldr = g.ldr;
+  p.ldy = g.ldy;
+  p.y = g.y;
+  p.err = gb_device_error_word();
+  p.wait_ns = gb_wait_limit_ns();
+  auto* kern = w4_gemm_kernel<NT, T>;
+  const void* const kp = reinterpret_cast<const void*>(kern);
+  cudaError_t e = gb_set_smem_once(kp, C::SMEM);
+  if (e != cudaSuccess) return e;
+  // split the reduction while the tiles leave SMs idle, each CTA keeps two tiles of inputs and
+  // all clusters find room at once
+  p.split_log2 = 0;
+  while (p.split_log2 < 3 && ((long long)p.tiles << (p.split_log2 + 1)) <= gb_num_sms() &&
+         p.ct >> (p.split_log2 + 2) &&
+         p.tiles <= gb_active_clusters(kp, THREADS, C::SMEM, 2 << p.split_log2))
+    ++p.split_log2;
+  CUtensorMap tx;
+  if (!operand_map(&tx, x, parts, g.M, cols, ld, p.box_rows)) return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.split_log2 ? (unsigned)p.tiles << p.split_log2
+                                  : (unsigned)std::min(p.tiles, gb_num_sms()));
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 1u << p.split_log2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, kern, tx, p);
+  if (e == cudaSuccess) gb_count_launch();
+  return e;
+}
+
+template <typename T>
+cudaError_t launch_y(const W4Gemm& g, const void* x, int parts, int cols, long long ld,
+                     cudaStream_t st) {
+  // The width whose waves of tiles take least: a tile's columns, and about 48 of them for what
+  // a tile takes besides.
+  const auto cost = [&](int nt) {
+    const long long tiles = (long long)gb_ceil_div(g.K, TILE) * gb_ceil_div(g.M, nt);
+    return gb_ceil_div_ll(tiles, gb_num_sms()) * (nt + 48);
+  };
+  if (g.M <= 32) return launch_t<32, T>(g, x, parts, cols, ld, st);
+  if (g.M <= 64 || (cost(64) < cost(128) && cost(64) < cost(256)))
+    return launch_t<64, T>(g, x, parts, cols, ld, st);
+  if (g.M <= 128 || cost(128) < cost(256)) return launch_t<128, T>(g, x, parts, cols, ld, st);
+  return launch_t<256, T>(g, x, parts, cols, ld, st);
+}
+
+}  // namespace
+
+size_t w4_gemm_workspace(const W4Gemm& g) {
+  const size_t parts = g.x_io == CONV_W4_IO_F32 ? 3 : 1;
+  return parts * g.M * (((size_t)g.C + 7) / 8 * 16);
+}
+
+cudaError_t launch_w4_gemm(const W4Gemm& g, cudaStream_t st) {
+  const void* x = g.x;
+  int parts = 1, cols = g.C;
+  long long ld = g.ldx;
+  if (!in_place(g)) {
+    const cudaError_t e = launch_w4_operands(g, g.ws, st);
+    if (e != cudaSuccess) return e;
+    x = g.ws;
+    parts = g.x_io == CONV_W4_IO_F32 ? 3 : 1;
+    cols = gb_ceil_div(g.C, 8) * 8;
+    ld = cols;
+  }
+  return g.y_f32 ? launch_y<float>(g, x, parts, cols, ld, st)
+                 : launch_y<__nv_bfloat16>(g, x, parts, cols, ld, st);
+}

@@ -1,0 +1,125 @@
+// Integer 4-bit weights into the order the products read them (once a layer), and x as bf16
+// operands where it does not lie in memory as such.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "internal.h"
+#include "ptx.cuh"
+#include "w4.cuh"
+#include "walk.cuh"
+
+namespace {
+using namespace gb::w4;
+constexpr int THREADS = gb::walk::THREADS;
+
+// A word of eight codes to a thread.
+__global__ void __launch_bounds__(THREADS)
+    pack_codes_kernel(int C, int K, int group, int kt, int ct, const uint8_t* __restrict__ codes,
+                      const uint8_t* __restrict__ zeros, uint32_t* __restrict__ out) {
+  const long long words = (long long)kt * ct * (TILE_BYTES / 4);
+  const long long pitch = (C + 1LL) / 2;
+  const int groups = group ? (C + group - 1) / group : 1;
+  for (long long i = (long long)blockIdx.x * THREADS + threadIdx.x; i < words;
+       i += (long long)gridDim.x * THREADS) {
+    const int t = (int)(i & 3), q = (int)(i >> 2) & 3;
+    const long long row = i >> 4, tile = row >> 7;  // rows of all tiles
+    const int j = (int)(tile % ct);
+    const long long k = tile / ct * TILE + (row & 127);
+    const int c0 = j * TILE + 32 * t + 8 * q;
+    uint32_t w = 0;
+    if (k < K && c0 < C) {
+      const uint32_t zero =
+          zeros ? zeros[k * groups + (group ? c0 / group : 0)] & 15u : 8u;  // the word's group
+      for (int e = 0; e < 8; ++e) {
+        const int c = c0 + e;
+        uint32_t code = zero;
+        if (c < C) code = (codes[k * pitch + c / 2] >> (4 * (c & 1))) & 15u;
+        w |= code << (4 * (e / 2 + 4 * (e & 1)));
+      }
+    }
+    out[i] = w;
+  }
+}
+
+// Scales (T: of 2 or 4 bytes, copied as they are) and zeros; 0 past the last.
+template <typename T>
+__global__ void __launch_bounds__(THREADS)
+    pack_scales_kernel(int C, int K, int group, int kt, int ct, const T* __restrict__ scales,
+                       const uint8_t* __restrict__ zeros, T* __restrict__ out_s,
+                       uint8_t* __restrict__ out_z) {
+  const int per = group ? TILE / group : 1, groups = group ? (C + group - 1) / group : 1;
+  const int tiles = group ? ct : 1;  // of a row
+  const long long n = (long long)kt * tiles * TILE * per;
+  for (long long i = (long long)blockIdx.x * THREADS + threadIdx.x; i < n;
+       i += (long long)gridDim.x * THREADS) {
+    const long long row = i / per, tile = row / TILE;
+    const long long k = tile / tiles * TILE + row % TILE;
+    const int g = (int)(tile % tiles) * per + (int)(i % per);
+    const bool in = k < K && g < groups;
+    out_s[i] = in ? scales[k * groups + g] : T(0);
+    out_z[i] = in ? (zeros ? zeros[k * groups + g] & 15 : 8) : 0;
+  }
+}
+
+// Eight elements to a thread, into parts of [M][pitch] bf16.
+template <int XIO>
+__global__ void __launch_bounds__(THREADS)
+    operands_kernel(const void* __restrict__ x, long long ldx, int M, int C, int vec, int pieces,
+                    uint4* __restrict__ out) {
+  gb::allow_dependents();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const long long all = (long long)M * pieces;
+  for (long long i = (long long)blockIdx.x * THREADS + threadIdx.x; i < all;
+       i += (long long)gridDim.x * THREADS) {
+    const long long m = i / pieces;
+    const int c = (int)(i - m * pieces) * 8;
+    Raw8<XIO> raw;
+    raw.load(static_cast<const uint8_t*>(x) + m * ldx * kElemBytes<XIO>, c, C, vec);
+#pragma unroll
+    for (int h = 0; h < kParts<XIO>; ++h) out[h * all + i] = raw.part(h);
+  }
+}
+
+unsigned grid_for(long long n) {
+  return (unsigned)std::min<long long>(gb_ceil_div_ll(n, THREADS), (long long)gb_num_sms() * 8);
+}
+
+}  // namespace
+
+cudaError_t launch_w4_pack(int C, int K, int group, int scale_f32, const void* codes,
+                           const void* scales, const void* zeros, void* packed, cudaStream_t st) {
+  const Packed w = packed_layout(C, K, group, scale_f32 ? 4 : 2);
+  uint8_t* const to = static_cast<uint8_t*>(packed);
+  const uint8_t* const z = static_cast<const uint8_t*>(zeros);
+  pack_codes_kernel<<<grid_for((long long)(w.zeros / 4)), THREADS, 0, st>>>(
+      C, K, group, w.kt, w.ct, static_cast<const uint8_t*>(codes), z,
+      reinterpret_cast<uint32_t*>(to));
+  gb_count_launch();
+  const unsigned grid = grid_for((long long)(w.scales - w.zeros));
+  if (scale_f32)
+    pack_scales_kernel<uint32_t><<<grid, THREADS, 0, st>>>(
+        C, K, group, w.kt, w.ct, static_cast<const uint32_t*>(scales), z,
+        reinterpret_cast<uint32_t*>(to + w.scales), to + w.zeros);
+  else
+    pack_scales_kernel<uint16_t><<<grid, THREADS, 0, st>>>(
+        C, K, group, w.kt, w.ct, static_cast<const uint16_t*>(scales), z,
+        reinterpret_cast<uint16_t*>(to + w.scales), to + w.zeros);
+  gb_count_launch();
+  return cudaGetLastError();
+}
+
+cudaError_t launch_w4_operands(const W4Gemm& g, void* out, cudaStream_t st) {
+  const int pieces = gb_ceil_div(g.C, 8), vec = rows_vec8(g.x_io, g.x, g.ldx);
+  const dim3 grid(grid_for((long long)g.M * pieces));
+  uint4* const to = static_cast<uint4*>(out);
+  const auto go = [&](auto* kern) {
+    return gb::walk::launch_walk(kern, grid, st, g.x, g.ldx, g.M, g.C, vec, pieces, to);
+  };
+  switch (g.x_io) {
+    case CONV_W4_IO_BF16: return go(operands_kernel<CONV_W4_IO_BF16>);
+    case CONV_W4_IO_F32: return go(operands_kernel<CONV_W4_IO_F32>);
+    case CONV_W4_IO_E4M3: return go(operands_kernel<CONV_W4_IO_E4M3>);
+    default: return go(operands_kernel<CONV_W4_IO_INT8>);
+  }
+}

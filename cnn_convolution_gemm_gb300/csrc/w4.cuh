@@ -1,0 +1,194 @@
+// Integer 4-bit weights as the products read them, and what the kernels over them share.
+//
+// Packed weights, of [K][C] codes in tiles of 128 outputs x 128 inputs, KT x CT of them:
+//   codes   [KT][CT][128 outputs][64 bytes]: byte 16 q + 4 t .. + 3 of an output holds the
+//           inputs 32 t + 8 q .. + 7 as one word, input i in nibble i / 2 (i even) or
+//           4 + i / 2 (odd).  So a 16-byte piece is what a lane of an m16n8k16 MMA needs for
+//           128 inputs whose order it may choose, four words (w >> 4 j) & 0x000F000F give
+//           the pairs (2 j, 2 j + 1), and a thread of the larger products writes each word
+//           as 16 bytes of bf16.
+//   zeros   [KT][CT][128][G] bytes, G groups in 128 inputs; group 0: [KT][128]
+//   scales  the same of bf16 or fp32
+// Outputs past K and inputs past C have scale 0 and codes that equal their zero.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "fp4.cuh"
+#include "internal.h"
+
+namespace gb {
+namespace w4 {
+
+constexpr int TILE = 128;
+constexpr int TILE_BYTES = TILE * 64;
+
+struct Packed {
+  int kt, ct, per;          // tiles; groups in a tile (0: one per output)
+  size_t zeros, scales, bytes;  // offsets of the parts, and the end
+};
+inline Packed packed_layout(int C, int K, int group, int scale_bytes) {
+  Packed p;
+  p.kt = (int)((K + (long long)TILE - 1) / TILE);
+  p.ct = (int)((C + (long long)TILE - 1) / TILE);
+  p.per = group ? TILE / group : 0;
+  const size_t n = (size_t)p.kt * TILE * (group ? (size_t)p.ct * p.per : 1);
+  p.zeros = (size_t)p.kt * p.ct * TILE_BYTES;
+  p.scales = p.zeros + n;
+  p.bytes = p.scales + n * scale_bytes;
+  return p;
+}
+
+// bf16 pairs (2 j, 2 j + 1) of a word of codes, less zero, all exact; zz: zero_pair(zero).
+__device__ __forceinline__ uint32_t zero_pair(uint32_t zero) {
+  return 0x43004300u | zero * 0x00010001u;  // 128 + zero, twice
+}
+template <int J>
+__device__ __forceinline__ uint32_t weight_pair(uint32_t w, uint32_t zz) {
+  uint32_t q;  // 128 + code
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(q) : "r"(w >> (4 * J)), "r"(0x000F000Fu),
+      "r"(0x43004300u));
+  const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&q),
+                                   *reinterpret_cast<const __nv_bfloat162*>(&zz));
+  return *reinterpret_cast<const uint32_t*>(&d);
+}
+
+// An fp32 value as the sum of three bf16 values, exact: its leading 8 bits, the next 8 and the
+// last 8 (infinities and NaNs in the first alone).
+struct Parts {
+  uint32_t hi, mid, lo;  // in the upper halves
+};
+__device__ __forceinline__ Parts split3(float v) {
+  Parts p;
+  const uint32_t b = __float_as_uint(v);
+  p.hi = b & 0xFFFF0000u;
+  const float r = v - __uint_as_float(p.hi);
+  p.mid = __float_as_uint(r) & 0xFFFF0000u;
+  p.lo = __float_as_uint(r - __uint_as_float(p.mid));
+  if ((b & 0x7F800000u) == 0x7F800000u) {
+    p.hi |= (b & 0x007FFFFFu) ? 0x00400000u : 0u;
+    p.mid = p.lo = 0u;
+  }
+  return p;
+}
+// Two of them side by side: the upper halves of a and b.
+__device__ __forceinline__ uint32_t pair_hi(uint32_t a, uint32_t b) {
+  return __byte_perm(a, b, 0x7632);
+}
+
+// Eight elements of a row of x from column c on as bf16, in PARTS parts (fp32: 3, else 1);
+// zero past the last.
+//   vec: the row allows 16-byte accesses at columns that are multiples of 8 (codes: 8 bytes;
+//   always)
+template <int XIO>
+constexpr int kParts = XIO == CONV_W4_IO_F32 ? 3 : 1;
+
+template <int XIO>
+struct Raw8 {
+  static constexpr int WORDS = XIO == CONV_W4_IO_F32 ? 8 : XIO == CONV_W4_IO_BF16 ? 4 : 2;
+  uint32_t w[WORDS];
+
+  __device__ __forceinline__ void load(const void* row, int c, int C, bool vec) {
+    if constexpr (XIO == CONV_W4_IO_F32) {
+      const float* const p = static_cast<const float*>(row) + c;
+      if (vec && c + 8 <= C) {
+        const uint4 a = *reinterpret_cast<const uint4*>(p), b = *reinterpret_cast<const uint4*>(p + 4);
+        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+        w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = c + i < C ? __float_as_uint(p[i]) : 0u;
+      }
+    } else if constexpr (XIO == CONV_W4_IO_BF16) {
+      const uint16_t* const p = static_cast<const uint16_t*>(row) + c;
+      if (vec && c + 8 <= C) {
+        const uint4 a = *reinterpret_cast<const uint4*>(p);
+        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          w[i] = c + 2 * i < C ? p[2 * i] : 0u;
+          if (c + 2 * i + 1 < C) w[i] |= (uint32_t)p[2 * i + 1] << 16;
+        }
+      }
+    } else {
+      // rows of codes are whole 16-byte pieces, zero past the last column
+      uint2 a = make_uint2(0u, 0u);
+      if (c < C) a = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(row) + c);
+      w[0] = a.x, w[1] = a.y;
+    }
+  }
+  __device__ __forceinline__ uint4 part(int k) const {
+    uint32_t o[4];
+    if constexpr (XIO == CONV_W4_IO_BF16) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = w[i];
+    } else if constexpr (XIO == CONV_W4_IO_F32) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const Parts a = split3(__uint_as_float(w[2 * i])), b = split3(__uint_as_float(w[2 * i + 1]));
+        o[i] = k == 0 ? pair_hi(a.hi, b.hi) : k == 1 ? pair_hi(a.mid, b.mid) : pair_hi(a.lo, b.lo);
+      }
+    } else if constexpr (XIO == CONV_W4_IO_E4M3) {
+      // E4M3 to f16 to fp32, whose upper half is the bf16: 4 significant bits
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t a, b;
+        asm("{\n\t.reg .b16 p, l, h;\n\t.reg .b32 u;\n\t"
+            "cvt.u16.u32 p, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 u, p;\n\tmov.b32 {l, h}, u;\n\t"
+            "cvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
+            : "=r"(a), "=r"(b)
+            : "r"(w[i / 2] >> (16 * (i & 1))));
+        o[i] = pair_hi(a, b);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t u = (w[i / 2] ^ 0x80808080u) >> (16 * (i & 1));
+        const float a = __uint_as_float(0x4B000000u | (u & 255u)) - 8388736.0f;
+        const float b = __uint_as_float(0x4B000000u | ((u >> 8) & 255u)) - 8388736.0f;
+        o[i] = pair_hi(__float_as_uint(a), __float_as_uint(b));
+      }
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+  }
+};
+
+template <int XIO>
+constexpr int kElemBytes = XIO == CONV_W4_IO_F32 ? 4 : XIO == CONV_W4_IO_BF16 ? 2 : 1;
+
+// Whether rows of x allow Raw8's vector loads.
+inline bool rows_vec8(int x_io, const void* x, long long ldx) {
+  const int eb = x_io == CONV_W4_IO_F32 ? 4 : x_io == CONV_W4_IO_BF16 ? 2 : 1;
+  return eb == 1 || (reinterpret_cast<uintptr_t>(x) % 16 == 0 && ldx * eb % 16 == 0);
+}
+
+}  // namespace w4
+}  // namespace gb
+
+// y[m][k] = act(sum_c X[m][c] W[k][c] + bias[k] + res[m][k])
+struct W4Gemm {
+  int M, C, K, group, scale_f32, x_io, x_group, y_f32, act;
+  const uint8_t* packed;
+  const void* x;
+  const float* xs;
+  long long ldx;
+  const float* bias;
+  const void* res;  // of y's type
+  long long ldr, ldy;
+  void* y;
+  void* ws;
+};
+// Up to 16 rows, x in shared memory.
+bool w4_few_applicable(const W4Gemm& g);
+cudaError_t launch_w4_few(const W4Gemm& g, cudaStream_t st);
+// x as bf16 operands: kParts of [M][8 * ceil(C / 8)].
+cudaError_t launch_w4_operands(const W4Gemm& g, void* out, cudaStream_t st);
+// Any number.  Workspace: x as bf16 operands, unless it lies so already.
+size_t w4_gemm_workspace(const W4Gemm& g);
+cudaError_t launch_w4_gemm(const W4Gemm& g, cudaStream_t st);
+cudaError_t launch_w4_pack(int C, int K, int group, int scale_f32, const void* codes,
+                           const void* scales, const void* zeros, void* packed, cudaStream_t st);

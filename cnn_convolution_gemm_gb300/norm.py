@@ -6,7 +6,7 @@ import threading
 import torch
 
 from . import binding as B
-from . import fp4
+from . import fp4, q8
 from .fp4 import CONV_DTYPE, allocating_on, call_stream, rows_of
 
 
@@ -15,18 +15,24 @@ class ResidualNorm:
 
     post, pre: binding.CONV_NORM_*; w_*, b_*: fp32 [C] or None.  gate: binding.CONV_GATE_*,
     one row of gates for gate_rows consecutive rows.  dtype: of x and x'; z_dtype: of z (dtype
-    if None); h_dtype: of gate and h (z_dtype if None, else bf16 with bf16 x and fp32 z).  h_fmt: binding.CONV_FP4_* gives h as an ``Fp4Tensor`` with
-    tensor scale h_scale.  Row strides of 2-D tensors are followed.  Threads may share a
+    if None); h_dtype: of gate and h (z_dtype if None, else bf16 with bf16 x and fp32 z).
+    h_fmt: binding.CONV_FP4_* gives h as an ``Fp4Tensor`` with tensor scale h_scale; h_q8:
+    binding.CONV_Q8_* (or 'e4m3', 'int8') gives it as a ``Q8Tensor`` with a scale for each row
+    (h_group 0) or each 128 columns of it (128).  Row strides of 2-D tensors are followed.  Threads may share a
     layer."""
 
     def __init__(self, C, dtype=torch.bfloat16, z_dtype=None, eps=1e-6, post=B.CONV_NORM_NONE,
                  w_post=None, b_post=None, pre=B.CONV_NORM_NONE, w_pre=None, b_pre=None,
                  gate=B.CONV_GATE_NONE, gate_rows=1, residual_scale=1.0, h_fmt=None, h_scale=1.0,
-                 h_dtype=None):
+                 h_dtype=None, h_q8=None, h_group=0):
         self.C, self.dtype, self.z_dtype = C, dtype, dtype if z_dtype is None else z_dtype
         self.h_dtype = self.z_dtype if h_dtype is None else h_dtype
         self.post, self.pre, self.gate, self.gate_rows = post, pre, gate, gate_rows
         self.h_fmt, self.h_scale = h_fmt, h_scale
+        if h_q8 is not None and h_fmt is not None:
+            raise ValueError("h_fmt, h_q8: expected one of them at most")
+        self.h_q8 = None if h_q8 is None else q8.format_of(h_q8)
+        self.h_group = q8.group_of(h_group)
         self._params = (w_post, b_post, w_pre, b_pre)  # the descriptor holds their addresses
         self.index = None  # the device of the weights; None: there are none
         for p in self._params:
@@ -46,6 +52,8 @@ class ResidualNorm:
         if h_fmt is not None:
             B.conv_norm_set_output(self.desc, B.CONV_NORM_OUT_FP4_MX if h_fmt == B.CONV_FP4_MX
                                    else B.CONV_NORM_OUT_FP4_NV, h_scale)
+        if self.h_q8 is not None:
+            B.conv_norm_set_output_q8(self.desc, self.h_q8, self.h_group)
         # a call gives the descriptor its strides and launches before another call changes them
         self._lock = threading.Lock()
         self._strides = (C,) * 5
@@ -101,6 +109,14 @@ class ResidualNorm:
             elif h_out.index != index:
                 raise ValueError("h_out: on another device than x")
             h_out.tensor_scale = self.h_scale
+            hp, hsp = h_out.codes_ptr, h_out.scales_ptr
+        elif self.h_q8 is not None:
+            if h_out is None:
+                h_out = q8.empty(rows, C, self.h_q8, x.device, self.h_group, stream)
+            elif h_out.shape != (rows, C, self.h_q8, self.h_group):
+                raise ValueError("h_out: an 8-bit matrix of another shape, format or group")
+            elif h_out.index != index:
+                raise ValueError("h_out: on another device than x")
             hp, hsp = h_out.codes_ptr, h_out.scales_ptr
         else:
             if h_out is None:

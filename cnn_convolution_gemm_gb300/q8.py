@@ -1,0 +1,97 @@
+"""8-bit matrices with scales (E4M3 values or whole numbers; conv_q8_* of gbconv.h) as torch
+tensors: what the norms before a layer give and the layers with 4-bit weights take."""
+from __future__ import annotations
+
+import torch
+
+from . import binding as B
+from .fp4 import CONV_DTYPE, allocating_on, call_stream, rows_of
+
+FORMATS = {"e4m3": B.CONV_Q8_E4M3, "int8": B.CONV_Q8_INT8}
+
+
+def format_of(fmt) -> int:
+    """binding.CONV_Q8_*, also by name."""
+    got = FORMATS.get(fmt, fmt)
+    if got not in (B.CONV_Q8_E4M3, B.CONV_Q8_INT8):
+        raise ValueError(f"fmt: {fmt}, expected 'e4m3' or 'int8'")
+    return got
+
+
+def group_of(group) -> int:
+    if group not in (0, 128):
+        raise ValueError(f"group: {group}, expected 0 (one scale a row) or 128")
+    return group
+
+
+class Q8Tensor:
+    """An 8-bit matrix [rows][cols]: codes (contiguous uint8, rows of 16 * ceil(cols / 16) bytes,
+    zero past the last column) and scales (contiguous fp32, one a row, or with group 128 one for
+    each 128 columns), of their sizes or more.  The tensors stay the ones it was made with (their
+    addresses are kept)."""
+
+    __slots__ = ("rows", "cols", "fmt", "group", "codes", "scales", "shape", "codes_ptr",
+                 "scales_ptr", "device", "index")
+
+    def __init__(self, rows, cols, fmt, group, codes, scales):
+        fmt, group = format_of(fmt), group_of(group)
+        if scales.get_device() != codes.get_device():
+            raise ValueError("codes and scales: on different devices")
+        if (codes.dtype is not torch.uint8 or not codes.is_contiguous()
+                or codes.numel() < rows * 16 * -(-cols // 16)):
+            raise ValueError("codes: expected contiguous uint8 of conv_q8_size's bytes")
+        if (scales.dtype is not torch.float32 or not scales.is_contiguous()
+                or scales.numel() < rows * (-(-cols // 128) if group else 1)):
+            raise ValueError("scales: expected contiguous fp32 of conv_q8_size's bytes")
+        self.rows, self.cols, self.fmt, self.group = rows, cols, fmt, group
+        self.codes, self.scales = codes, scales
+        self.shape = (rows, cols, fmt, group)
+        self.codes_ptr, self.scales_ptr = codes.data_ptr(), scales.data_ptr()
+        if (self.codes_ptr | self.scales_ptr) % 16:
+            raise ValueError("codes and scales: must be 16-byte aligned")
+        self.device, self.index = codes.device, codes.get_device()
+
+
+def empty(rows, cols, fmt, device, group=0, stream=None) -> Q8Tensor:
+    """An uninitialised 8-bit matrix."""
+    fmt, group = format_of(fmt), group_of(group)
+    cb, sb = B.conv_q8_size(fmt, group, rows, cols)
+    with allocating_on(stream):
+        return Q8Tensor(rows, cols, fmt, group,
+                        torch.empty(cb, dtype=torch.uint8, device=device),
+                        torch.empty(sb // 4, dtype=torch.float32, device=device))
+
+
+def quantize(x: torch.Tensor, fmt, group=0, out: Q8Tensor | None = None, stream=None) -> Q8Tensor:
+    """x [..., cols] (bf16 or fp32) in 8 bits: fmt 'e4m3' or 'int8' (or binding.CONV_Q8_*), with a
+    scale for each row (group 0) or each 128 columns of it (group 128)."""
+    cols = x.shape[-1]
+    rows, ld = rows_of(x, cols, "x") if cols else (0, 0)
+    fmt, group = format_of(fmt), group_of(group)
+    if out is None:
+        out = empty(rows, cols, fmt, x.device, group, stream)
+    elif out.shape != (rows, cols, fmt, group):
+        raise ValueError("out: an 8-bit matrix of another shape, format or group")
+    index = out.index
+    if x.get_device() != index:
+        raise ValueError("x: on another device than out")
+    B.conv_q8_quantize(fmt, group, CONV_DTYPE[x.dtype], rows, cols, x.data_ptr(), ld,
+                       out.codes_ptr, out.scales_ptr, call_stream(index, stream))
+    return out
+
+
+def dequantize(t: Q8Tensor, dtype=torch.bfloat16, out: torch.Tensor | None = None,
+               stream=None) -> torch.Tensor:
+    """The values that t stands for, [rows][cols] in dtype (or out's)."""
+    if out is None:
+        with allocating_on(stream):
+            out = torch.empty(t.rows, t.cols, dtype=dtype, device=t.device)
+    rows, ld = rows_of(out, t.cols, "out")
+    if rows != t.rows:
+        raise ValueError(f"out: {rows} rows, expected {t.rows}")
+    index = t.index
+    if out.get_device() != index:
+        raise ValueError("out: on another device than t")
+    B.conv_q8_dequantize(t.fmt, t.group, CONV_DTYPE[out.dtype], rows, t.cols, t.codes_ptr,
+                         t.scales_ptr, out.data_ptr(), ld, call_stream(index, stream))
+    return out

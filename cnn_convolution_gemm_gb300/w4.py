@@ -1,0 +1,139 @@
+"""The fully connected layer with integer 4-bit weights (conv_w4_* of gbconv.h): codes 0 .. 15
+with a scale and a zero for each group of inputs, as weight-only quantisation gives them."""
+from __future__ import annotations
+
+import threading
+
+import torch
+
+from . import binding as B
+from . import q8
+from .fp4 import CONV_DTYPE, Types, Workspaces, allocating_on, call_stream, rows_of
+
+IO = Types({torch.bfloat16: B.CONV_W4_IO_BF16, torch.float32: B.CONV_W4_IO_F32})
+IO_Q8 = {B.CONV_Q8_E4M3: B.CONV_W4_IO_E4M3, B.CONV_Q8_INT8: B.CONV_W4_IO_INT8}
+
+
+class W4Linear:
+    """y = act(x W^T + bias (+ residual)), W[k][c] = (code - zero) * scale; equally a 1x1
+    convolution over NHWC pixels (x [..., C]).
+
+    group: inputs that share a scale and a zero, 32, 64, 128 or 0 (all of an output's).
+    scale_dtype: of the scales.  x_dtype: torch.bfloat16 or torch.float32, or None for a
+    ``Q8Tensor`` of format x_q8 and group x_group.  Row strides of the tensors are followed.
+    Threads may share a layer."""
+
+    def __init__(self, C, K, group=128, x_dtype=torch.bfloat16, y_dtype=torch.bfloat16,
+                 act=B.CONV_ACT_NONE, has_residual=False, scale_dtype=torch.bfloat16, x_q8=None,
+                 x_group=0):
+        if (x_dtype is None) != (x_q8 is not None):
+            raise ValueError("x_dtype or x_q8: expected one of them")
+        self.C, self.K, self.group = C, K, group
+        self.x_dtype, self.y_dtype, self.scale_dtype = x_dtype, y_dtype, scale_dtype
+        self.x_q8, self.x_group = None if x_q8 is None else q8.format_of(x_q8), x_group
+        self.desc = B.conv_w4_create(C, K, group, CONV_DTYPE[scale_dtype],
+                                     IO[x_dtype] if x_q8 is None else IO_Q8[self.x_q8],
+                                     CONV_DTYPE[y_dtype])
+        B.conv_w4_set_input_group(self.desc, x_group)
+        B.conv_w4_set_epilogue(self.desc, act, has_residual)
+        self.w = None  # the packed weights
+        # a call gives the descriptor its strides and launches before another call, or other
+        # weights, change them; calls on one stream share its workspace
+        self._lock = threading.Lock()
+        self._strides = (C, K, K)
+        self._sizes = {}  # rows -> workspace bytes
+        self._ws = Workspaces()
+
+    def __del__(self):
+        d = getattr(self, "desc", None)
+        if d is not None:
+            try:
+                B.conv_w4_destroy(d)
+            except Exception:
+                pass
+
+    def load(self, codes: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor | None = None,
+             stream=None):
+        """Lay the weights out, once: codes uint8 [K][ceil(C / 2)], input c in the low (c even)
+        or high half of byte c / 2; scales [K][groups] in scale_dtype; zeros uint8 [K][groups]
+        of 0 .. 15, or None: 8 throughout.  The tensors are not kept."""
+        K, groups = self.K, -(-self.C // self.group) if self.group else 1
+        for t, dtype, cols, what in ((codes, torch.uint8, -(-self.C // 2), "codes"),
+                                     (scales, self.scale_dtype, groups, "scales"),
+                                     (zeros, torch.uint8, groups, "zeros")):
+            if t is None and what == "zeros":
+                continue
+            if t.dtype is not dtype or tuple(t.shape) != (K, cols) or not t.is_contiguous():
+                raise ValueError(f"{what}: expected contiguous {dtype} {[K, cols]}")
+            if t.get_device() != codes.get_device():
+                raise ValueError(f"{what}: on another device than codes")
+        handle = call_stream(codes.get_device(), stream)
+        with allocating_on(stream):
+            packed = torch.empty(B.conv_w4_packed_size(self.desc), dtype=torch.uint8,
+                                 device=codes.device)
+        B.conv_w4_prepack(self.desc, codes.data_ptr(), scales.data_ptr(),
+                          None if zeros is None else zeros.data_ptr(), packed.data_ptr(), handle)
+        with self._lock:
+            self.w = packed
+
+    def forward(self, x, bias=None, residual=None, out=None, stream=None):
+        with self._lock:
+            w = self.w
+            if w is None:
+                raise RuntimeError("load() the weights first")
+            C, K, y_dtype, index = self.C, self.K, self.y_dtype, w.get_device()
+            handle = call_stream(index, stream)
+            bp = rp = xsp = None
+            if self.x_dtype is None:
+                if not isinstance(x, q8.Q8Tensor):
+                    raise ValueError("x: expected a Q8Tensor")
+                if (x.cols, x.fmt, x.group) != (C, self.x_q8, self.x_group):
+                    raise ValueError("x: an 8-bit matrix of another width, format or group")
+                if x.index != index:
+                    raise ValueError("x: on another device than the weights")
+                rows, ldx = x.rows, C
+                xp, xsp = x.codes_ptr, x.scales_ptr
+            else:
+                if x.dtype is not self.x_dtype:
+                    raise ValueError(f"x: {x.dtype}, expected {self.x_dtype}")
+                if x.get_device() != index:
+                    raise ValueError("x: on another device than the weights")
+                rows, ldx = rows_of(x, C, "x")
+                xp = x.data_ptr()
+            if bias is not None:
+                if bias.dtype is not torch.float32 or bias.numel() != K or not bias.is_contiguous():
+                    raise ValueError("bias: expected contiguous fp32 [K]")
+                if bias.get_device() != index:
+                    raise ValueError("bias: on another device than the weights")
+                bp = bias.data_ptr()
+            ldr = K
+            if out is None:
+                lead = (rows,) if self.x_dtype is None else x.shape[:-1]
+                with allocating_on(stream):
+                    out = torch.empty(*lead, K, dtype=y_dtype, device=w.device)
+            elif out.get_device() != index:
+                raise ValueError("out: on another device than the weights")
+            got, ldy = rows_of(out, K, "out")
+            if got != rows or out.dtype is not y_dtype:
+                raise ValueError("out: another number of rows or type")
+            if residual is not None:
+                got, ldr = rows_of(residual, K, "residual")
+                if got != rows or residual.dtype is not y_dtype:
+                    raise ValueError("residual: another number of rows or type than y")
+                if residual.get_device() != index:
+                    raise ValueError("residual: on another device than the weights")
+                rp = residual.data_ptr()
+            strides = (ldx, ldr, ldy)
+            if strides != self._strides:
+                B.conv_w4_set_strides(self.desc, *strides)
+                self._strides = strides
+            need = self._sizes.get(rows)
+            if need is None:
+                need = self._sizes[rows] = B.conv_w4_workspace_size(self.desc, rows)
+            # held until the launches are enqueued
+            ws = self._ws.get(need, w.device, index, stream, handle) if need else None
+            B.conv_w4_fwd(self.desc, rows, xp, xsp, w.data_ptr(), bp, rp, out.data_ptr(),
+                          ws.data_ptr() if need else None, need, handle)
+            return out
+
+    __call__ = forward

@@ -434,6 +434,86 @@ conv_status_t conv_fp4_fwd(conv_fp4_t desc, int M, const void* x, const void* x_
                            const void* residual, void* y, void* y_scales, void* ws,
                            size_t ws_bytes, void* stream);
 
+/* ---- 8-bit matrices with scales ----------------------------------------------- */
+
+/* A matrix [rows][cols] of 8-bit codes, E4M3 values or whole numbers; the codes of a row
+ * (group 0), or of each 128 consecutive columns of it (group 128; the last may be shorter),
+ * share an fp32 scale:
+ *   s = max(max |x| / T rounded to fp32, 2^-100), T = 448 (CONV_Q8_E4M3) or 127 (CONV_Q8_INT8);
+ * a code is the value nearest to x / s (the quotient is not rounded before), ties to the even
+ * one.  Scales of rows or groups that hold an infinity or a NaN are NaN and their codes 0:
+ * their values are NaN, so the fault stays visible in every product it enters.
+ *
+ * In memory:
+ *   codes   [rows][P] bytes, P = 16 * ceil(cols / 16); padding codes are 0.
+ *   scales  fp32 [rows][G], G = 1 (group 0) or ceil(cols / 128). */
+typedef enum { CONV_Q8_E4M3 = 0, CONV_Q8_INT8 = 1 } conv_q8_format_t;
+
+/* Bytes of the codes and of the scales of a [rows][cols] matrix (up to 2^30 each). */
+conv_status_t conv_q8_size(conv_q8_format_t fmt, int group, int rows, int cols,
+                           size_t* code_bytes, size_t* scale_bytes);
+/* Quantise x: device, dtype CONV_BF16 or CONV_F32, row r at x + r * ldx elements
+ * (ldx >= cols, or 0 for contiguous rows), aligned to its element.  codes, scales: device,
+ * 16-byte aligned.  rows may be 0.  Stream-ordered. */
+conv_status_t conv_q8_quantize(conv_q8_format_t fmt, int group, conv_dtype_t dtype, int rows,
+                               int cols, const void* x, long long ldx, void* codes, void* scales,
+                               void* stream);
+/* The values that codes and scales stand for: y = code * s, rounded once to dtype
+ * (CONV_BF16: the fp32 product rounded to bf16); ldy as ldx above.  Stream-ordered. */
+conv_status_t conv_q8_dequantize(conv_q8_format_t fmt, int group, conv_dtype_t dtype, int rows,
+                                 int cols, const void* codes, const void* scales, void* y,
+                                 long long ldy, void* stream);
+
+/* ---- layers with integer 4-bit weights ------------------------------------------ */
+
+/* The fully connected layer (equally the 1x1 convolution over NHWC pixels) whose weights are
+ * held in 4 bits as whole numbers:
+ *   y[m][k] = act(sum_c X[m][c] W[k][c] + bias[k] (+ residual[m][k]))
+ *   W[k][c] = (code[k][c] - zero[k][c / group]) * scale[k][c / group]
+ * with codes and zeros 0 .. 15 and group 32, 64, 128 or 0 (one per output: the whole row).
+ * X is bf16, fp32 (taken as it is: three bf16 parts hold its 24 bits) or a matrix as above.
+ * Products of X and code - zero are exact; they are summed, and the sums scaled, in fp32. */
+typedef enum {
+  CONV_W4_IO_BF16 = 0,
+  CONV_W4_IO_F32 = 1,
+  CONV_W4_IO_E4M3 = 2, /* x alone: codes and scales of conv_q8_quantize */
+  CONV_W4_IO_INT8 = 3
+} conv_w4_io_t;
+typedef struct gbconv_w4_s* conv_w4_t;
+
+/* C inputs, K outputs (1 .. 2^28).  scale_dtype: of the weights' scales, CONV_BF16 or CONV_F32;
+ * x_io: conv_w4_io_t; y_dtype: CONV_BF16 or CONV_F32.  Defaults: no activation, no residual,
+ * scales of an 8-bit x per row, contiguous rows.  Threads and setters: as conv_fp4_create. */
+conv_status_t conv_w4_create(conv_w4_t* out, int C, int K, int group, conv_dtype_t scale_dtype,
+                             int x_io, conv_dtype_t y_dtype);
+conv_status_t conv_w4_destroy(conv_w4_t desc);
+/* The scales of an 8-bit x: one a row (0) or one for each 128 columns of it (128). */
+conv_status_t conv_w4_set_input_group(conv_w4_t desc, int x_group);
+/* act: conv_act_t; has_residual: conv_w4_fwd reads a residual of y's type and adds it before
+ * the activation. */
+conv_status_t conv_w4_set_epilogue(conv_w4_t desc, int act, int has_residual);
+/* Elements between rows of x, residual and y (0: contiguous; an 8-bit x always is). */
+conv_status_t conv_w4_set_strides(conv_w4_t desc, long long ldx, long long ldr, long long ldy);
+/* The weights as conv_w4_fwd reads them, laid out once.  codes: uint8 [K][ceil(C / 2)], input c
+ * in the low (c even) or high (c odd) half of byte c / 2; scales: [K][G] of scale_dtype, G = 1
+ * (group 0) or ceil(C / group); zeros: uint8 [K][G], values 0 .. 15 (of others the low 4 bits
+ * count), or NULL: all 8.  All at any alignment of their elements; packed: 16-byte aligned,
+ * conv_w4_packed_size bytes.  Stream-ordered. */
+conv_status_t conv_w4_packed_size(conv_w4_t desc, size_t* bytes);
+conv_status_t conv_w4_prepack(conv_w4_t desc, const void* codes, const void* scales,
+                              const void* zeros, void* packed, void* stream);
+/* Bytes of device workspace conv_w4_fwd needs for M rows of any stride and alignment on the
+ * current device. */
+conv_status_t conv_w4_workspace_size(conv_w4_t desc, int M, size_t* bytes);
+/* x: device, per x_io and strides, aligned to its element (codes: 16 bytes); x_scales: the fp32
+ * scales of codes, else NULL.  bias: device fp32 [K] or NULL.  residual: NULL unless the
+ * descriptor has one.  y: not overlapping any input (it may equal residual when their row
+ * strides are equal).  ws: 16-byte aligned, conv_w4_workspace_size(M) bytes; calls that can
+ * overlap on the GPU need their own.  M may be 0.  Stream-ordered. */
+conv_status_t conv_w4_fwd(conv_w4_t desc, int M, const void* x, const void* x_scales,
+                          const void* packed, const float* bias, const void* residual, void* y,
+                          void* ws, size_t ws_bytes, void* stream);
+
 /* ---- norms around a residual block ------------------------------------------- */
 
 /* One pass over the rows of a residual stream, between one block and the next:
@@ -474,14 +554,17 @@ conv_status_t conv_norm_set_gate(conv_norm_t desc, int gate, int gate_rows,
                                  float residual_scale);
 /* out: conv_norm_out_t; tensor_scale: of the 4-bit h (1 unless CONV_NORM_OUT_FP4_NV). */
 conv_status_t conv_norm_set_output(conv_norm_t desc, int out, float tensor_scale);
+/* h as 8-bit codes and scales (conv_q8_size, conv_q8_quantize), made from the norm's fp32
+ * values; group 0 or 128. */
+conv_status_t conv_norm_set_output_q8(conv_norm_t desc, conv_q8_format_t fmt, int group);
 /* Elements between rows of x, z, gate, x' and h (0: contiguous). */
 conv_status_t conv_norm_set_strides(conv_norm_t desc, long long ldx, long long ldz, long long ldg,
                                     long long ldxo, long long ldh);
 /* rows may be 0.  z NULL: x' = x (no block before: the first norm of a network).
  * gate: given exactly when the descriptor has a gate and z is given.  x_out: x' or
  * NULL when it is not wanted; it may be x itself.  h: NULL exactly when norm_pre is
- * none; h_scales: the scales of a 4-bit h, else NULL.  Tensors are device memory
- * aligned to their element (4-bit h: 16 bytes) and, but for x_out == x, do not
+ * none; h_scales: the scales of a 4- or 8-bit h, else NULL.  Tensors are device memory
+ * aligned to their element (4- and 8-bit h: 16 bytes) and, but for x_out == x, do not
  * overlap outputs.  Stream-ordered. */
 conv_status_t conv_norm_fwd(conv_norm_t desc, int rows, const void* x, const void* z,
                             const void* gate, void* x_out, void* h, void* h_scales,
