@@ -30,7 +30,8 @@ struct FewParams {
   int pitch;                 // bytes of a row of x in shared memory
   int stages;                // of a warp's ring
   int x_group, vec_x, y_f32, act;
-  const uint8_t *codes, *zeros;
+  const uint8_t* blocks;     // packed
+  const uint8_t* zeros;      // PER 0
   const void* scales;
   const void* x;
   const float* xs;
@@ -55,20 +56,17 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
 // A stage of a warp's ring: 16 outputs' codes, scales and zeros of a tile.
 template <int PER, bool F32>
 struct Stage {
-  static constexpr int CODES = 1024, SCALES = 16 * PER * (F32 ? 4 : 2), ZEROS = 16 * PER;
+  static constexpr int CODES = BLOCK_CODES, SCALES = 16 * PER * (F32 ? 4 : 2), ZEROS = 16 * PER;
   static constexpr int BYTES = CODES + SCALES + ZEROS;
 
   // one thread
+  static __device__ __forceinline__ const uint8_t* block(const FewParams& p, int rg, int j) {
+    return p.blocks + (((size_t)(rg >> 3) * p.ct + j) * 8 + (rg & 7)) * BYTES;
+  }
   static __device__ __forceinline__ void fetch(uint8_t* to, uint64_t* full, const FewParams& p,
                                                int rg, int j) {
-    const size_t row = ((size_t)(rg >> 3) * p.ct + j) * TILE + (rg & 7) * 16;
     gb::mbar_arrive_expect_tx(full, BYTES);
-    gb::bulk_load(to, p.codes + row * 64, full, CODES);
-    if constexpr (PER != 0) {
-      gb::bulk_load(to + CODES, static_cast<const uint8_t*>(p.scales) + row * (SCALES / 16), full,
-                    SCALES);
-      gb::bulk_load(to + CODES + SCALES, p.zeros + row * PER, full, ZEROS);
-    }
+    gb::bulk_load(to, block(p, rg, j), full, BYTES);
   }
   static __device__ __forceinline__ float scale(const uint8_t* stage, int r, int g) {
     const uint8_t* const p = stage + CODES + (r * PER + g) * (F32 ? 4 : 2);
@@ -105,11 +103,11 @@ __global__ void __launch_bounds__(THREADS, 2) w4_few_kernel(const FewParams p) {
   const int rg0 = blockIdx.x * at_once + sub, rg_step = gridDim.x * at_once;
   // the first weights on their way to L2 while the kernel before this one ends (whatever it
   // still writes, L2 holds)
-  if (rg0 < p.row_groups && lane < p.stages && j0 + lane * wc < p.ct) {
-    const uint8_t* const at =
-        p.codes + (((size_t)(rg0 >> 3) * p.ct + j0 + lane * wc) * TILE + (rg0 & 7) * 16) * 64;
-    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(at), "r"(1024) : "memory");
-  }
+  if (rg0 < p.row_groups && lane < p.stages && j0 + lane * wc < p.ct)
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
+                     S::block(p, rg0, j0 + lane * wc)),
+                 "r"(S::BYTES)
+                 : "memory");
   if (lane == 0) {
     for (int i = 0; i < p.stages; ++i) gb::mbar_init(&full[i], 1);
     gb::fence_barrier_init();
@@ -189,8 +187,9 @@ __global__ void __launch_bounds__(THREADS, 2) w4_few_kernel(const FewParams p) {
         ++taken;
         {
           const uint8_t* const w = ring + stage * S::BYTES;
-          const uint4 wa = *reinterpret_cast<const uint4*>(w + r * 64 + 16 * q);
-          const uint4 wb = *reinterpret_cast<const uint4*>(w + (r + 8) * 64 + 16 * q);
+          const uint4 wa = *reinterpret_cast<const uint4*>(w + r * 64 + 16 * piece_slot(r, q));
+          const uint4 wb =
+              *reinterpret_cast<const uint4*>(w + (r + 8) * 64 + 16 * piece_slot(r + 8, q));
           const uint32_t aw[4] = {wa.x, wa.y, wa.z, wa.w}, bw[4] = {wb.x, wb.y, wb.z, wb.w};
           uint32_t zas = za0, zbs = zb0;
           if constexpr (PER != 0) {
@@ -347,7 +346,7 @@ cudaError_t launch_t(const W4Gemm& g, cudaStream_t st) {
   p.vec_x = rows_vec8(g.x_io, g.x, g.ldx);
   p.y_f32 = g.y_f32;
   p.act = g.act;
-  p.codes = g.packed;
+  p.blocks = g.packed;
   p.zeros = g.packed + w.zeros;
   p.scales = g.packed + w.scales;
   p.x = g.x;

@@ -8,8 +8,11 @@
 // threads that keep the tile's sums in registers add scale * sum to them in fp32.
 //
 // Warp 0 loads X (TMA), warp 2 the packed weights, warp 1 issues the MMAs (one elected lane);
-// one or two warpgroups take the codes apart into swizzled bf16 tiles; the others scale and
-// sum, and run the epilogue (through TMEM, so that it is a loop over columns).  Few tiles with
+// two warpgroups take the codes apart, tile by tile in turn, and write them as bf16 into TMEM,
+// an output a lane, where the MMAs read A: through shared memory, whose 128 bytes a cycle are
+// what bounds this kernel, they would pass twice at four times their size (64 x 8192 x 8192
+// 34 us so).  The others scale and sum, and run the epilogue (through TMEM, so that it is a loop
+// over columns).  Few tiles with
 // long reductions are split over the CTAs of a cluster, which add their sums through
 // distributed shared memory in a fixed order.
 #include <cuda.h>
@@ -30,43 +33,48 @@ using gb::fp4::mul2;
 using gb::fp4::pack2;
 using gb::fp4::unpack2;
 
-constexpr int THREADS = 512;
-constexpr int BK = 64;  // inputs of a step: 128 bytes of bf16
+constexpr int BK = 64;  // inputs of a load of X: 128 bytes of bf16
 
 template <int NT>
 struct Cfg {
-  static constexpr int SUM_WGS = NT == 256 ? 2 : 1;   // that scale and sum
-  static constexpr int TAKE_WGS = 3 - SUM_WGS;        // that take codes apart
-  static constexpr int COLS = NT / SUM_WGS;           // columns of a summing thread
-  static constexpr int NB = NT == 256 ? 2 : 4;        // accumulators in TMEM
-  static constexpr int TMEM_COLS = NB * NT;
-  static constexpr int X_BYTES = NT * BK * 2;
-  static constexpr int X_STAGES = NT == 256 ? 4 : NT == 128 ? 5 : 8;
-  static constexpr int A_BYTES = TILE * BK * 2;
-  static constexpr int A_STAGES = 3;
-  static constexpr int W_STAGES = NT == 256 ? 3 : 6;
-  static constexpr int W_BYTES = TILE_BYTES + TILE * 4 * 5;  // codes, scales, zeros at most
+  static constexpr int TAKE_WGS = 2;                   // that take codes apart
+  static constexpr int SUM_WGS = NT > 128 ? 2 : 1;     // that scale and sum
+  static constexpr int THREADS = 128 * (1 + TAKE_WGS + SUM_WGS);
+  static constexpr int COLS = NT / SUM_WGS;            // columns of a summing thread
+  static constexpr int NB = NT >= 128 ? 2 : 4;         // accumulators in TMEM
+  static constexpr int A_STAGES = NT > 128 ? 2 : 4;    // of weights there: 128 inputs
+  static constexpr int A_COLS = TILE / 2;
+  static constexpr int A0 = NB * NT;                   // their first column
+  static constexpr int TMEM_COLS = 512;
+  static constexpr int X_HALF = NT * BK * 2;
+  static constexpr int X_BYTES = 2 * X_HALF;           // a stage: 128 inputs, BK at a time
+  static constexpr int X_STAGES = NT > 128 ? 3 : NT == 128 ? 4 : 6;
+  static constexpr int W_STAGES = NT > 128 ? 5 : 6;
+  static constexpr int W_BYTES = TILE * 64 + TILE * 4 * 5;  // of packed weights, at most
   static constexpr int X_SCALES = 2 * NT * 4;
-  static constexpr int SMEM = X_STAGES * X_BYTES + A_STAGES * A_BYTES + W_STAGES * W_BYTES +
-                              X_SCALES + 512 + 1024;
+  static constexpr int SMEM =
+      X_STAGES * X_BYTES + W_STAGES * W_BYTES + X_SCALES + 512 + 1024;
   // registers of the threads that take apart, load and issue, and of those that sum: together
-  // at most the 128 that each of the 512 is launched with
+  // at most what the block is launched with
   static constexpr bool SPLIT_REGS = NT >= 128;
-  static constexpr int REGS_TAKE = NT == 256 ? 64 : 96, REGS_SUM = NT == 256 ? 192 : 216;
-  static_assert((4 - SUM_WGS) * REGS_TAKE + SUM_WGS * REGS_SUM <= 4 * 128, "registers");
-  static_assert(TMEM_COLS <= 512 && SMEM <= 232448, "TMEM, shared memory");
+  static constexpr int REGS = 65536 / THREADS / 8 * 8;
+  static constexpr int REGS_TAKE = NT > 128 ? 56 : 96, REGS_SUM = NT > 128 ? 152 : 216;
+  static_assert((1 + TAKE_WGS) * REGS_TAKE + SUM_WGS * REGS_SUM <= REGS * THREADS / 128,
+                "registers");
+  static_assert(A0 + A_STAGES * A_COLS <= TMEM_COLS && SMEM <= 232448, "TMEM, shared memory");
   static_assert(X_STAGES * X_BYTES >= NT * 512, "a cluster's sums take X's place");
+  static_assert(COLS % 32 == 0, "columns");
 };
 
 struct Params {
   int M, C, K, ct, mt, tiles;   // tiles of inputs, of rows, of all
-  int steps;                    // BK inputs each
   int parts, per, scale_bytes;  // of x; groups in 128 inputs, 0: one per output
+  int block;                    // bytes of packed weights of 16 outputs
   int box_rows, n;              // rows of a load of X, columns of an MMA
   int split_log2;               // CTAs of a cluster
   int q8, x_group, act;
-  const uint8_t *codes, *zeros;
-  const uint8_t* scales;
+  const uint8_t* blocks;                // packed
+  const uint8_t *zeros, *scales;        // per 0
   const float* xs;
   const float* bias;
   const void* res;
@@ -124,16 +132,99 @@ struct Turn {
   }
 };
 
+// The warp that issues the MMAs.  Its loop is short and knows at compile time how many sums a
+// tile of inputs has: a single warp takes about five cycles an instruction, and with the
+// sums' bounds decided as it went it needed 700 cycles for 64 inputs, whose MMAs take 384.
+template <int NT>
+struct Mmas {
+  using C = Cfg<NT>;
+  uint32_t tmem;
+  const uint8_t* sX;
+  uint64_t *x_full, *x_empty, *a_full, *a_empty, *d_full, *d_empty;
+  uint32_t id;
+
+  // SUMS: of a tile of inputs; 0: one for all of them.  What an MMA is told (addresses,
+  // descriptors) is worked out by the whole warp, before one lane issues it.
+  template <int SUMS, int PARTS>
+  __device__ __forceinline__ bool run(const Params& p, int first, int step, int c0, int c1) const {
+    constexpr int STEPS = SUMS ? 8 / SUMS : 8;  // MMAs of a sum and part of x, 16 inputs each
+    const bool one = gb::elect_one();
+    const uint64_t xd0 = gb::sw128_kmajor_desc(gb::smem_u32(sX));
+    int xs = 0, as = 0, ds = 0;                 // stages
+    uint32_t xp = 0, ap = 0, dp = 0;            // phases
+    bool ok = true;
+    for (int tile = first; tile < p.tiles && ok; tile += step)
+      for (int c = c0; c < c1; ++c) {
+        ok = gb::mbar_wait_bounded_warp(&a_full[as], ap, p.wait_ns, p.err);
+        int at[PARTS];  // stages of x's parts
+#pragma unroll
+        for (int part = 0; part < PARTS; ++part) {
+          ok = ok && gb::mbar_wait_bounded_warp(&x_full[xs], xp, p.wait_ns, p.err);
+          at[part] = xs;
+          if (++xs == C::X_STAGES) {
+            xs = 0;
+            xp ^= 1;
+          }
+        }
+        const uint32_t ad = tmem + C::A0 + as * C::A_COLS;
+#pragma unroll
+        for (int u = 0; u < (SUMS ? SUMS : 1); ++u) {
+          if (SUMS || c == c0)
+            ok = ok && gb::mbar_wait_bounded_warp(&d_empty[ds], dp ^ 1, p.wait_ns, p.err);
+          if (!ok) break;
+          gb::tc_fence_after();
+          const uint32_t dd = tmem + ds * NT;
+          const uint32_t add = SUMS || c == c0 ? 0u : 1u;
+          uint64_t* const done = &d_full[ds];
+#pragma unroll
+          for (int part = 0; part < PARTS; ++part) {
+            const uint64_t xd = xd0 + (uint64_t)(at[part] * (C::X_BYTES >> 4));
+#pragma unroll
+            for (int i = 0; i < STEPS; ++i) {
+              const int k = u * STEPS + i;
+              const uint64_t kd = xd + (k / 4) * (C::X_HALF >> 4) + k % 4 * 2;
+              if (one)
+                gb::tc_mma_f16_ts(dd, ad + 8 * k, kd, id, i == 0 && part == 0 ? add : 1u);
+            }
+          }
+          if (SUMS || c == c1 - 1) {
+            if (one) gb::tc_commit(done);
+            if (++ds == C::NB) {
+              ds = 0;
+              dp ^= 1;
+            }
+          }
+        }
+        if (!ok) break;
+        if (one) gb::tc_commit(&a_empty[as]);
+#pragma unroll
+        for (int part = 0; part < PARTS; ++part)
+          if (one) gb::tc_commit(&x_empty[at[part]]);
+        __syncwarp();
+        if (++as == C::A_STAGES) {
+          as = 0;
+          ap ^= 1;
+        }
+      }
+    return ok;
+  }
+  template <int SUMS>
+  __device__ __forceinline__ bool run(const Params& p, int first, int step, int c0, int c1) const {
+    if constexpr (NT <= 128)  // (fp32 x: its three parts would fill the rings of the widest)
+      if (p.parts == 3) return run<SUMS, 3>(p, first, step, c0, c1);
+    return run<SUMS, 1>(p, first, step, c0, c1);
+  }
+};
+
 template <int NT, typename T>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__(Cfg<NT>::THREADS, 1)
     w4_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const Params p) {
   using C = Cfg<NT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* const sX = smem;
-  uint8_t* const sA = sX + C::X_STAGES * C::X_BYTES;
-  uint8_t* const sW = sA + C::A_STAGES * C::A_BYTES;
+  uint8_t* const sW = sX + C::X_STAGES * C::X_BYTES;
   float* const sXS = reinterpret_cast<float*>(sW + C::W_STAGES * C::W_BYTES);  // [2][NT]
   uint64_t* const x_full = reinterpret_cast<uint64_t*>(sXS + 2 * NT);
   uint64_t* const x_empty = x_full + C::X_STAGES;
@@ -155,7 +246,6 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int c1 = (int)((long long)p.ct * (rank + 1) >> p.split_log2);
   // one sum for the whole row: neither the weights nor x change their scale along it
   const bool whole = p.per == 0 && !p.x_group;
-  const auto halves = [&](int c) { return min(2, p.steps - 2 * c); };  // steps of a tile
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::X_STAGES; ++s) {
@@ -163,12 +253,12 @@ __global__ void __launch_bounds__(THREADS, 1)
       gb::mbar_init(&x_empty[s], 1);
     }
     for (int s = 0; s < C::A_STAGES; ++s) {
-      gb::mbar_init(&a_full[s], 4 * C::TAKE_WGS);
+      gb::mbar_init(&a_full[s], 4);
       gb::mbar_init(&a_empty[s], 1);
     }
     for (int s = 0; s < C::W_STAGES; ++s) {
       gb::mbar_init(&w_full[s], 1);
-      gb::mbar_init(&w_empty[s], 4 * C::TAKE_WGS + (p.per ? 4 * C::SUM_WGS : 0));
+      gb::mbar_init(&w_empty[s], 4 + (p.per ? 4 * C::SUM_WGS : 0));
     }
     for (int s = 0; s < C::NB; ++s) {
       gb::mbar_init(&d_full[s], 1);
@@ -194,20 +284,22 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (warp == 0) {
       // ---------------- X ----------------
       const bool one = gb::elect_one();
-      const uint32_t tx = (uint32_t)p.box_rows * (BK * 2);
+      const uint32_t tx = (uint32_t)p.box_rows * (TILE * 2);
       Turn x;
       int issued = 0;
       bool ok = true;
       asm volatile("griddepcontrol.wait;" ::: "memory");
       for (int tile = first; tile < p.tiles && ok; tile += step) {
         const int m0 = tile % p.mt * NT;
-        for (int s = 2 * c0; s < min(2 * c1, p.steps) && ok; ++s)
+        for (int c = c0; c < c1 && ok; ++c)
           for (int h = 0; h < p.parts; ++h) {
             ok = gb::mbar_wait_bounded_warp(&x_empty[x.at], x.phase ^ 1, p.wait_ns, p.err);
             if (!ok) break;
-            if (one) {
+            if (one) {  // (inputs past the last read as 0)
+              uint8_t* const to = sX + x.at * C::X_BYTES;
               gb::mbar_arrive_expect_tx(&x_full[x.at], tx);
-              gb::tma_load_3d(sX + x.at * C::X_BYTES, &tm_x, &x_full[x.at], s * BK, m0, h);
+              gb::tma_load_3d(to, &tm_x, &x_full[x.at], c * TILE, m0, h);
+              gb::tma_load_3d(to + C::X_HALF, &tm_x, &x_full[x.at], c * TILE + BK, m0, h);
             }
             __syncwarp();
             ++issued;
@@ -222,7 +314,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     } else if (warp == 2) {
       // ---------------- packed weights ----------------
       const bool one = gb::elect_one();
-      const uint32_t sb = TILE * p.per * p.scale_bytes, zb = TILE * p.per;
+      const uint32_t bytes = 8 * p.block;
       Turn w;
       int issued = 0;
       bool ok = true;
@@ -230,8 +322,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       // it still writes, L2 holds)
       if (first < p.tiles && lane < C::W_STAGES && c0 + lane < c1)
         asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
-                         p.codes + ((size_t)(first / p.mt) * p.ct + c0 + lane) * TILE_BYTES),
-                     "r"(TILE_BYTES)
+                         p.blocks + ((size_t)(first / p.mt) * p.ct + c0 + lane) * bytes),
+                     "r"(bytes)
                      : "memory");
       __syncwarp();
       asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -240,14 +332,10 @@ __global__ void __launch_bounds__(THREADS, 1)
           ok = gb::mbar_wait_bounded_warp(&w_empty[w.at], w.phase ^ 1, p.wait_ns, p.err);
           if (!ok) break;
           if (one) {
-            const size_t t = (size_t)(tile / p.mt) * p.ct + c;
-            uint8_t* const to = sW + w.at * C::W_BYTES;
-            gb::mbar_arrive_expect_tx(&w_full[w.at], TILE_BYTES + sb + zb);
-            gb::bulk_load(to, p.codes + t * TILE_BYTES, &w_full[w.at], TILE_BYTES);
-            if (p.per) {
-              gb::bulk_load(to + TILE_BYTES, p.scales + t * sb, &w_full[w.at], sb);
-              gb::bulk_load(to + TILE_BYTES + sb, p.zeros + t * zb, &w_full[w.at], zb);
-            }
+            gb::mbar_arrive_expect_tx(&w_full[w.at], bytes);
+            gb::bulk_load(sW + w.at * C::W_BYTES,
+                          p.blocks + ((size_t)(tile / p.mt) * p.ct + c) * bytes, &w_full[w.at],
+                          bytes);
           }
           __syncwarp();
           ++issued;
@@ -259,57 +347,15 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
     } else if (warp == 1) {
       // ---------------- MMAs ----------------
-      const bool one = gb::elect_one();
-      const uint32_t id = gb::idesc_f16(128, p.n, 1);
-      const int subs = p.per == 4 ? 2 : 1;  // accumulators of a step
-      Turn x, a, d;
-      int open[2] = {0, 0};
-      bool ok = true;
-      for (int tile = first; tile < p.tiles && ok; tile += step)
-        for (int c = c0; c < c1 && ok; ++c)
-          for (int h = 0; h < halves(c) && ok; ++h) {
-            const bool starts = whole ? c == c0 && h == 0 : p.per >= 2 || h == 0;
-            const bool ends = whole ? c == c1 - 1 && h == halves(c) - 1
-                                    : p.per >= 2 || h == halves(c) - 1;
-            if (starts)
-              for (int u = 0; u < subs && ok; ++u) {
-                ok = gb::mbar_wait_bounded_warp(&d_empty[d.at], d.phase ^ 1, p.wait_ns, p.err);
-                open[u] = d.at;
-                d.next(C::NB);
-              }
-            ok = ok && gb::mbar_wait_bounded_warp(&a_full[a.at], a.phase, p.wait_ns, p.err);
-            const uint64_t ad = gb::sw128_kmajor_desc(gb::smem_u32(sA + a.at * C::A_BYTES));
-            for (int part = 0; part < p.parts && ok; ++part) {
-              ok = gb::mbar_wait_bounded_warp(&x_full[x.at], x.phase, p.wait_ns, p.err);
-              if (!ok) break;
-              gb::tc_fence_after();
-              if (one) {
-                const uint64_t xd = gb::sw128_kmajor_desc(gb::smem_u32(sX + x.at * C::X_BYTES));
-                const bool fresh = starts && part == 0;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const int u = subs == 2 ? k >> 1 : 0;
-                  const bool clear = fresh && (subs == 2 ? (k & 1) == 0 : k == 0);
-                  gb::tc_mma_f16(tmem + (u ? open[1] : open[0]) * NT, ad + k * 2, xd + k * 2, id,
-                                 clear ? 0u : 1u);
-                }
-                gb::tc_commit(&x_empty[x.at]);
-              }
-              __syncwarp();
-              x.next(C::X_STAGES);
-            }
-            if (!ok) break;
-            if (one) {
-              gb::tc_commit(&a_empty[a.at]);
-              if (ends)
-                for (int u = 0; u < subs; ++u) gb::tc_commit(&d_full[u ? open[1] : open[0]]);
-            }
-            __syncwarp();
-            a.next(C::A_STAGES);
-          }
+      const Mmas<NT> m{tmem, sX, x_full, x_empty, a_full, a_empty, d_full, d_empty,
+                       gb::idesc_f16(128, p.n, 1)};
+      const bool ok = whole        ? m.template run<0>(p, first, step, c0, c1)
+                      : p.per <= 1 ? m.template run<1>(p, first, step, c0, c1)
+                      : p.per == 2 ? m.template run<2>(p, first, step, c0, c1)
+                                   : m.template run<4>(p, first, step, c0, c1);
       if (!ok) {
         // the MMAs that were issued end before the memory they use is given up
-        if (one) gb::tc_commit(given_up);
+        if (gb::elect_one()) gb::tc_commit(given_up);
         __syncwarp();
         gb::mbar_wait_bounded_warp(given_up, 0, p.wait_ns, p.err);
       }
@@ -317,69 +363,56 @@ __global__ void __launch_bounds__(THREADS, 1)
   } else if (wg <= C::TAKE_WGS) {
     // ---------------- codes to bf16 ----------------
     if constexpr (C::SPLIT_REGS) gb::registers_down_to<C::REGS_TAKE>();
-    constexpr int PIECES = 4 / C::TAKE_WGS;  // 16 bytes of an output's codes each
-    const int t0 = threadIdx.x - 128;        // piece t0 + 128 TAKE_WGS i
-    const uint32_t zb = TILE_BYTES + TILE * p.per * p.scale_bytes;
+    const int row = threadIdx.x & 127;
+    const uint32_t from0 = (row >> 4) * p.block + (row & 15) * 64;
+    const uint32_t z0 = (row >> 4) * p.block + BLOCK_CODES + 16 * p.per * p.scale_bytes +
+                        (row & 15) * p.per;
+    const uint32_t to = tmem + ((uint32_t)((warp & 3) * 32) << 16) + C::A0;
     Turn w, a;
+    int turn = 0;  // the warpgroups take every second tile of inputs
     bool ok = true;
     if (p.per == 0) asm volatile("griddepcontrol.wait;" ::: "memory");  // zeros from memory
     for (int tile = first; tile < p.tiles && ok; tile += step) {
-      uint32_t row_zero[PIECES];
-      if (p.per == 0)
-#pragma unroll
-        for (int i = 0; i < PIECES; ++i)
-          row_zero[i] =
-              p.zeros[tile / p.mt * TILE + ((t0 + 128 * C::TAKE_WGS * i) >> 2)] * 0x01010101u;
-      for (int c = c0; c < c1 && ok; ++c) {
+      const uint32_t row_zero =
+          p.per == 0 ? p.zeros[tile / p.mt * TILE + row] * 0x01010101u : 0u;
+      for (int c = c0; c < c1 && ok; ++c, turn ^= 1, w.next(C::W_STAGES), a.next(C::A_STAGES)) {
+        if (turn != wg - 1) continue;
         ok = gb::mbar_wait_bounded_warp(&w_full[w.at], w.phase, p.wait_ns, p.err);
         if (!ok) break;
         const uint8_t* const from = sW + w.at * C::W_BYTES;
-        uint4 code[PIECES];
-        uint32_t zero[PIECES];  // of the words 0 .. 3, one a byte
+        uint4 code[4];
 #pragma unroll
-        for (int i = 0; i < PIECES; ++i) {
-          const int piece = t0 + 128 * C::TAKE_WGS * i, row = piece >> 2;
-          code[i] = *reinterpret_cast<const uint4*>(from + 16 * piece);
-          const uint8_t* const z = from + zb + row * p.per;
-          zero[i] = p.per == 1   ? *z * 0x01010101u
-                    : p.per == 2 ? *reinterpret_cast<const uint16_t*>(z) * 0x00010001u
-                    : p.per == 4 ? *reinterpret_cast<const uint32_t*>(z)
-                                 : row_zero[i];
-          if (p.per == 2) zero[i] = __byte_perm(zero[i], 0u, 0x1100);
-          // outputs of odd number take the two words of a step the other way round: the
-          // eight lanes that store together then meet no bank twice
-          if (row & 1) {
-            code[i] = make_uint4(code[i].y, code[i].x, code[i].w, code[i].z);
-            zero[i] = __byte_perm(zero[i], 0u, 0x2301);
-          }
-        }
+        for (int q = 0; q < 4; ++q)
+          code[q] = *reinterpret_cast<const uint4*>(from + from0 + 16 * piece_slot(row, q));
+        uint32_t zero = row_zero;  // of the words 0 .. 3 of a piece, one a byte
+        const uint8_t* const z = from + z0;
+        if (p.per == 1) zero = *z * 0x01010101u;
+        if (p.per == 2) zero = __byte_perm(*reinterpret_cast<const uint16_t*>(z), 0u, 0x1100);
+        if (p.per == 4) zero = *reinterpret_cast<const uint32_t*>(z);
         __syncwarp();
         if (lane == 0) gb::mbar_arrive(&w_empty[w.at]);
-        w.next(C::W_STAGES);
+        ok = gb::mbar_wait_bounded_warp(&a_empty[a.at], a.phase ^ 1, p.wait_ns, p.err);
+        if (!ok) break;
+        gb::tc_fence_after();
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (h >= halves(c)) break;
-          ok = gb::mbar_wait_bounded_warp(&a_empty[a.at], a.phase ^ 1, p.wait_ns, p.err);
-          if (!ok) break;
-          uint8_t* const to = sA + a.at * C::A_BYTES;
+        for (int t = 0; t < 4; ++t) {
+          const uint32_t zz = zero_pair((zero >> (8 * t)) & 15u);
+          uint32_t r[16];
 #pragma unroll
-          for (int i = 0; i < PIECES; ++i) {
-            const int piece = t0 + 128 * C::TAKE_WGS * i, row = piece >> 2, q = piece & 3;
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              const uint32_t word = h ? (t ? code[i].w : code[i].z) : (t ? code[i].y : code[i].x);
-              const uint32_t zz = zero_pair((zero[i] >> (8 * (2 * h + t))) & 15u);
-              const int slot = ((t ^ (row & 1)) * 4 + q) ^ (row & 7);
-              *reinterpret_cast<uint4*>(to + row * 128 + slot * 16) =
-                  make_uint4(weight_pair<0>(word, zz), weight_pair<1>(word, zz),
-                             weight_pair<2>(word, zz), weight_pair<3>(word, zz));
-            }
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t word =
+                t == 0 ? code[q].x : t == 1 ? code[q].y : t == 2 ? code[q].z : code[q].w;
+            r[4 * q] = weight_pair<0>(word, zz);
+            r[4 * q + 1] = weight_pair<1>(word, zz);
+            r[4 * q + 2] = weight_pair<2>(word, zz);
+            r[4 * q + 3] = weight_pair<3>(word, zz);
           }
-          gb::fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) gb::mbar_arrive(&a_full[a.at]);
-          a.next(C::A_STAGES);
+          gb::tmem_st_x16(to + a.at * C::A_COLS + 16 * t, r);
         }
+        gb::tmem_st_wait();
+        gb::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) gb::mbar_arrive(&a_full[a.at]);
       }
     }
   } else {
@@ -409,10 +442,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (p.per) {
           ok = gb::mbar_wait_bounded_warp(&w_full[w.at], w.phase, p.wait_ns, p.err);
           if (!ok) break;
-          const uint8_t* const from = sW + w.at * C::W_BYTES + TILE_BYTES;
+          const uint8_t* const from = sW + w.at * C::W_BYTES + (o >> 4) * p.block + BLOCK_CODES;
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (i < p.per) s[i] = scale_at(from, o * p.per + i, p.scale_bytes);
+            if (i < p.per) s[i] = scale_at(from, (o & 15) * p.per + i, p.scale_bytes);
           __syncwarp();
           if (lane == 0) gb::mbar_arrive(&w_empty[w.at]);
           w.next(C::W_STAGES);
@@ -424,7 +457,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (scales_x && c + 1 < c1) next_xs = my_xs[c + 1];
           asm volatile("bar.sync %0, 128;" ::"r"(1 + part) : "memory");
         }
-        const int sums = p.per <= 1 ? 1 : p.per == 2 ? halves(c) : 2 * halves(c);
+        const int sums = p.per <= 1 ? 1 : p.per;
         for (int u = 0; u < sums && ok; ++u) {
           ok = gb::mbar_wait_bounded_warp(&d_full[d.at], d.phase, p.wait_ns, p.err);
           if (!ok) break;
@@ -585,7 +618,7 @@ cudaError_t launch_t(const W4Gemm& g, const void* x, int parts, int cols, long l
   p.mt = gb_ceil_div(g.M, NT);
   if ((long long)w.kt * p.mt > 0x7FFFFFFF) return cudaErrorInvalidValue;
   p.tiles = w.kt * p.mt;
-  p.steps = gb_ceil_div(g.C, BK);
+  p.block = w.block;
   p.parts = parts;
   p.per = w.per;
   p.scale_bytes = g.scale_f32 ? 4 : 2;
@@ -594,7 +627,7 @@ cudaError_t launch_t(const W4Gemm& g, const void* x, int parts, int cols, long l
   p.q8 = g.xs != nullptr;
   p.x_group = g.x_group;
   p.act = g.act;
-  p.codes = g.packed;
+  p.blocks = g.packed;
   p.zeros = g.packed + w.zeros;
   p.scales = g.packed + w.scales;
   p.xs = g.xs;
@@ -614,14 +647,14 @@ cudaError_t launch_t(const W4Gemm& g, const void* x, int parts, int cols, long l
   p.split_log2 = 0;
   while (p.split_log2 < 3 && ((long long)p.tiles << (p.split_log2 + 1)) <= gb_num_sms() &&
          p.ct >> (p.split_log2 + 2) &&
-         p.tiles <= gb_active_clusters(kp, THREADS, C::SMEM, 2 << p.split_log2))
+         p.tiles <= gb_active_clusters(kp, C::THREADS, C::SMEM, 2 << p.split_log2))
     ++p.split_log2;
   CUtensorMap tx;
   if (!operand_map(&tx, x, parts, g.M, cols, ld, p.box_rows)) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.split_log2 ? (unsigned)p.tiles << p.split_log2
                                   : (unsigned)std::min(p.tiles, gb_num_sms()));
-  cfg.blockDim = dim3(THREADS);
+  cfg.blockDim = dim3(C::THREADS);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
@@ -648,10 +681,12 @@ cudaError_t launch_y(const W4Gemm& g, const void* x, int parts, int cols, long l
     return gb_ceil_div_ll(tiles, gb_num_sms()) * (nt + 48);
   };
   if (g.M <= 32) return launch_t<32, T>(g, x, parts, cols, ld, st);
-  if (g.M <= 64 || (cost(64) < cost(128) && cost(64) < cost(256)))
+  if (g.M <= 64 || (cost(64) < cost(128) && cost(64) < cost(192)))
     return launch_t<64, T>(g, x, parts, cols, ld, st);
-  if (g.M <= 128 || cost(128) < cost(256)) return launch_t<128, T>(g, x, parts, cols, ld, st);
-  return launch_t<256, T>(g, x, parts, cols, ld, st);
+  // (fp32 x: its three parts would fill the rings of the widest)
+  if (g.M <= 128 || parts > 1 || cost(128) < cost(192))
+    return launch_t<128, T>(g, x, parts, cols, ld, st);
+  return launch_t<192, T>(g, x, parts, cols, ld, st);
 }
 
 }  // namespace

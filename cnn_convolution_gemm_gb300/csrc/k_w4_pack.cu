@@ -15,22 +15,24 @@ constexpr int THREADS = gb::walk::THREADS;
 
 // A word of eight codes to a thread.
 __global__ void __launch_bounds__(THREADS)
-    pack_codes_kernel(int C, int K, int group, int kt, int ct, const uint8_t* __restrict__ codes,
-                      const uint8_t* __restrict__ zeros, uint32_t* __restrict__ out) {
-  const long long words = (long long)kt * ct * (TILE_BYTES / 4);
+    pack_codes_kernel(int C, int K, int group, const Packed p, const uint8_t* __restrict__ codes,
+                      const uint8_t* __restrict__ zeros, uint8_t* __restrict__ out) {
+  const long long words = (long long)p.kt * p.ct * (TILE * 16);
   const long long pitch = (C + 1LL) / 2;
   const int groups = group ? (C + group - 1) / group : 1;
   for (long long i = (long long)blockIdx.x * THREADS + threadIdx.x; i < words;
        i += (long long)gridDim.x * THREADS) {
-    const int t = (int)(i & 3), q = (int)(i >> 2) & 3;
+    const int t = (int)(i & 3), slot = (int)(i >> 2) & 3;
     const long long row = i >> 4, tile = row >> 7;  // rows of all tiles
-    const int j = (int)(tile % ct);
-    const long long k = tile / ct * TILE + (row & 127);
+    int q = 0;
+    while (piece_slot((int)(row & 15), q) != slot) ++q;
+    const int j = (int)(tile % p.ct);
+    const long long k = tile / p.ct * TILE + (row & 127);
     const int c0 = j * TILE + 32 * t + 8 * q;
+    const int g = group ? c0 / group : 0;  // the word's
     uint32_t w = 0;
-    if (k < K && c0 < C) {
-      const uint32_t zero =
-          zeros ? zeros[k * groups + (group ? c0 / group : 0)] & 15u : 8u;  // the word's group
+    if (k < K && g < groups) {
+      const uint32_t zero = zeros ? zeros[k * groups + g] & 15u : 8u;
       for (int e = 0; e < 8; ++e) {
         const int c = c0 + e;
         uint32_t code = zero;
@@ -38,27 +40,36 @@ __global__ void __launch_bounds__(THREADS)
         w |= code << (4 * (e / 2 + 4 * (e & 1)));
       }
     }
-    out[i] = w;
+    *reinterpret_cast<uint32_t*>(out + (row >> 4) * p.block + (row & 15) * 64 + slot * 16 + t * 4) =
+        w;
   }
 }
 
 // Scales (T: of 2 or 4 bytes, copied as they are) and zeros; 0 past the last.
 template <typename T>
 __global__ void __launch_bounds__(THREADS)
-    pack_scales_kernel(int C, int K, int group, int kt, int ct, const T* __restrict__ scales,
-                       const uint8_t* __restrict__ zeros, T* __restrict__ out_s,
-                       uint8_t* __restrict__ out_z) {
-  const int per = group ? TILE / group : 1, groups = group ? (C + group - 1) / group : 1;
-  const int tiles = group ? ct : 1;  // of a row
-  const long long n = (long long)kt * tiles * TILE * per;
+    pack_scales_kernel(int C, int K, int group, const Packed p, const T* __restrict__ scales,
+                       const uint8_t* __restrict__ zeros, uint8_t* __restrict__ out) {
+  const int per = group ? p.per : 1, groups = group ? (C + group - 1) / group : 1;
+  const int tiles = group ? p.ct : 1;  // of a row
+  const long long n = (long long)p.kt * tiles * TILE * per;
   for (long long i = (long long)blockIdx.x * THREADS + threadIdx.x; i < n;
        i += (long long)gridDim.x * THREADS) {
     const long long row = i / per, tile = row / TILE;
     const long long k = tile / tiles * TILE + row % TILE;
     const int g = (int)(tile % tiles) * per + (int)(i % per);
     const bool in = k < K && g < groups;
-    out_s[i] = in ? scales[k * groups + g] : T(0);
-    out_z[i] = in ? (zeros ? zeros[k * groups + g] & 15 : 8) : 0;
+    const T s = in ? scales[k * groups + g] : T(0);
+    const uint8_t z = in ? (zeros ? zeros[k * groups + g] & 15 : 8) : 0;
+    if (group) {
+      uint8_t* const block = out + (row >> 4) * p.block + BLOCK_CODES;
+      const int at = (int)((row & 15) * per + i % per);
+      reinterpret_cast<T*>(block)[at] = s;
+      block[16 * per * sizeof(T) + at] = z;
+    } else {
+      reinterpret_cast<T*>(out + p.scales)[row] = s;
+      out[p.zeros + row] = z;
+    }
   }
 }
 
@@ -92,19 +103,17 @@ cudaError_t launch_w4_pack(int C, int K, int group, int scale_f32, const void* c
   const Packed w = packed_layout(C, K, group, scale_f32 ? 4 : 2);
   uint8_t* const to = static_cast<uint8_t*>(packed);
   const uint8_t* const z = static_cast<const uint8_t*>(zeros);
-  pack_codes_kernel<<<grid_for((long long)(w.zeros / 4)), THREADS, 0, st>>>(
-      C, K, group, w.kt, w.ct, static_cast<const uint8_t*>(codes), z,
-      reinterpret_cast<uint32_t*>(to));
+  const long long words = (long long)w.kt * w.ct * (TILE * 16);
+  pack_codes_kernel<<<grid_for(words), THREADS, 0, st>>>(C, K, group, w,
+                                                         static_cast<const uint8_t*>(codes), z, to);
   gb_count_launch();
-  const unsigned grid = grid_for((long long)(w.scales - w.zeros));
+  const unsigned grid = grid_for((long long)w.kt * TILE * (group ? (long long)w.ct * w.per : 1));
   if (scale_f32)
     pack_scales_kernel<uint32_t><<<grid, THREADS, 0, st>>>(
-        C, K, group, w.kt, w.ct, static_cast<const uint32_t*>(scales), z,
-        reinterpret_cast<uint32_t*>(to + w.scales), to + w.zeros);
+        C, K, group, w, static_cast<const uint32_t*>(scales), z, to);
   else
     pack_scales_kernel<uint16_t><<<grid, THREADS, 0, st>>>(
-        C, K, group, w.kt, w.ct, static_cast<const uint16_t*>(scales), z,
-        reinterpret_cast<uint16_t*>(to + w.scales), to + w.zeros);
+        C, K, group, w, static_cast<const uint16_t*>(scales), z, to);
   gb_count_launch();
   return cudaGetLastError();
 }

@@ -1,14 +1,19 @@
 // Integer 4-bit weights as the products read them, and what the kernels over them share.
 //
-// Packed weights, of [K][C] codes in tiles of 128 outputs x 128 inputs, KT x CT of them:
-//   codes   [KT][CT][128 outputs][64 bytes]: byte 16 q + 4 t .. + 3 of an output holds the
-//           inputs 32 t + 8 q .. + 7 as one word, input i in nibble i / 2 (i even) or
-//           4 + i / 2 (odd).  So a 16-byte piece is what a lane of an m16n8k16 MMA needs for
-//           128 inputs whose order it may choose, four words (w >> 4 j) & 0x000F000F give
-//           the pairs (2 j, 2 j + 1), and a thread of the larger products writes each word
-//           as 16 bytes of bf16.
-//   zeros   [KT][CT][128][G] bytes, G groups in 128 inputs; group 0: [KT][128]
-//   scales  the same of bf16 or fp32
+// Packed weights, of [K][C] codes in tiles of 128 outputs x 128 inputs: KT x CT tiles, each of
+// eight blocks of 16 outputs, a block whole in one place (a bulk copy costs about 30 cycles of
+// the SM's copy engine however short it is: with codes, scales and zeros apart one token took
+// 45 us through 8192 -> 32768, whose bytes take 21):
+//   codes   [16 outputs][4 pieces of 16 bytes]: word t of an output's piece q, which lies in
+//           place piece_slot(output, q), holds the inputs 32 t + 8 q .. + 7, input i in nibble
+//           i / 2 (i even) or 4 + i / 2 (odd).  So a piece is what a lane of an m16n8k16 MMA
+//           needs of 128 inputs whose order it may choose, (w >> 4 j) & 0x000F000F is the pair
+//           (2 j, 2 j + 1), and threads that each read one output's pieces from shared memory
+//           meet no bank twice.
+//   scales  [16][PER] bf16 or fp32, PER groups in 128 inputs
+//   zeros   [16][PER] bytes
+// Group 0: no scales and zeros there, but behind all tiles zeros [KT * 128] bytes and scales
+// [KT * 128].
 // Outputs past K and inputs past C have scale 0 and codes that equal their zero.
 #pragma once
 
@@ -23,21 +28,24 @@ namespace gb {
 namespace w4 {
 
 constexpr int TILE = 128;
-constexpr int TILE_BYTES = TILE * 64;
+__host__ __device__ constexpr int piece_slot(int output, int q) { return (q + (output >> 1)) & 3; }
+
+constexpr int BLOCK_CODES = 1024;
 
 struct Packed {
-  int kt, ct, per;          // tiles; groups in a tile (0: one per output)
-  size_t zeros, scales, bytes;  // offsets of the parts, and the end
+  int kt, ct, per;  // tiles; groups in a tile (0: one per output)
+  int block;        // bytes of a block
+  size_t zeros, scales, bytes;  // group 0: offsets; the end
 };
 inline Packed packed_layout(int C, int K, int group, int scale_bytes) {
   Packed p;
   p.kt = (int)((K + (long long)TILE - 1) / TILE);
   p.ct = (int)((C + (long long)TILE - 1) / TILE);
   p.per = group ? TILE / group : 0;
-  const size_t n = (size_t)p.kt * TILE * (group ? (size_t)p.ct * p.per : 1);
-  p.zeros = (size_t)p.kt * p.ct * TILE_BYTES;
-  p.scales = p.zeros + n;
-  p.bytes = p.scales + n * scale_bytes;
+  p.block = BLOCK_CODES + 16 * p.per * (scale_bytes + 1);
+  p.zeros = (size_t)p.kt * p.ct * 8 * p.block;
+  p.scales = p.zeros + (group ? 0 : (size_t)p.kt * TILE);
+  p.bytes = p.scales + (group ? 0 : (size_t)p.kt * TILE * scale_bytes);
   return p;
 }
 
