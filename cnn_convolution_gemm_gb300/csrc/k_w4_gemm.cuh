@@ -15,6 +15,9 @@
 // over columns).  Few tiles with
 // long reductions are split over the CTAs of a cluster, which add their sums through
 // distributed shared memory in a fixed order.
+// One translation unit per width includes this file.
+#pragma once
+
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -26,8 +29,9 @@
 #include "ptx.cuh"
 #include "w4.cuh"
 
-namespace {
-using namespace gb::w4;
+namespace gb {
+namespace w4 {
+namespace gemm {
 using gb::fp4::fma2;
 using gb::fp4::mul2;
 using gb::fp4::pack2;
@@ -35,44 +39,53 @@ using gb::fp4::unpack2;
 
 constexpr int BK = 64;  // inputs of a load of X: 128 bytes of bf16
 
-template <int NT>
+// NT: rows of X of a tile; SUMS: accumulators of a tile of inputs (0: one for the whole row).
+template <int NT, int SUMS>
 struct Cfg {
   static constexpr int TAKE_WGS = 2;                   // that take codes apart
-  static constexpr int SUM_WGS = NT > 128 ? 2 : 1;     // that scale and sum
+  static constexpr int SUM_WGS = 2;                    // that scale and sum
   static constexpr int THREADS = 128 * (1 + TAKE_WGS + SUM_WGS);
   static constexpr int COLS = NT / SUM_WGS;            // columns of a summing thread
-  static constexpr int NB = NT >= 128 ? 2 : 4;         // accumulators in TMEM
-  static constexpr int A_STAGES = NT > 128 ? 2 : 4;    // of weights there: 128 inputs
+  // Accumulators in TMEM, and stages of 128 inputs of weights beside them.  A small group's
+  // accumulator takes longer to hand over and to read than its MMAs: three are on their way
+  // then.
+  static constexpr int NB = NT == 128 ? (SUMS >= 2 ? 3 : 2) : NT > 128 ? 2 : 4;
+  static constexpr int A_STAGES = NT > 160 ? 2 : NT > 128 ? 3 : NT == 128 && SUMS >= 2 ? 2 : 4;
   static constexpr int A_COLS = TILE / 2;
   static constexpr int A0 = NB * NT;                   // their first column
   static constexpr int TMEM_COLS = 512;
   static constexpr int X_HALF = NT * BK * 2;
   static constexpr int X_BYTES = 2 * X_HALF;           // a stage: 128 inputs, BK at a time
-  static constexpr int X_STAGES = NT > 128 ? 3 : NT == 128 ? 4 : 6;
-  static constexpr int W_STAGES = NT > 128 ? 5 : 6;
+  static constexpr int X_STAGES = NT > 160 ? 3 : NT >= 128 ? 4 : 6;
+  static constexpr int W_STAGES = NT == 160 ? 4 : NT > 128 ? 5 : 6;
   static constexpr int W_BYTES = TILE * 64 + TILE * 4 * 5;  // of packed weights, at most
-  static constexpr int X_SCALES = 2 * NT * 4;
+  // Scales of a tile of inputs: the weights' [4][128 outputs], x's [NT].  They are written before
+  // the weights are handed to the MMAs and read once the sums are there, and no barrier of
+  // their own says when a place is free: the weights' place in TMEM, A_STAGES tiles earlier,
+  // is free once its MMAs have ended, whose accumulators NB tiles before them had been read.
+  static constexpr int S_STAGES = A_STAGES + NB + 2;
+  static constexpr int S_FLOATS = 4 * TILE + NT;
   static constexpr int SMEM =
-      X_STAGES * X_BYTES + W_STAGES * W_BYTES + X_SCALES + 512 + 1024;
+      X_STAGES * X_BYTES + W_STAGES * W_BYTES + S_STAGES * S_FLOATS * 4 + 512 + 1024;
   // registers of the threads that take apart, load and issue, and of those that sum: together
   // at most what the block is launched with
   static constexpr bool SPLIT_REGS = NT >= 128;
   static constexpr int REGS = 65536 / THREADS / 8 * 8;
-  static constexpr int REGS_TAKE = NT > 128 ? 56 : 96, REGS_SUM = NT > 128 ? 152 : 216;
-  static_assert((1 + TAKE_WGS) * REGS_TAKE + SUM_WGS * REGS_SUM <= REGS * THREADS / 128,
-                "registers");
+  static constexpr int REGS_TAKE = 56, REGS_SUM = 152;
+  static_assert(!SPLIT_REGS || (1 + TAKE_WGS) * REGS_TAKE + SUM_WGS * REGS_SUM <=
+                                   REGS * THREADS / 128, "registers");
   static_assert(A0 + A_STAGES * A_COLS <= TMEM_COLS && SMEM <= 232448, "TMEM, shared memory");
-  static_assert(X_STAGES * X_BYTES >= NT * 512, "a cluster's sums take X's place");
-  static_assert(COLS % 32 == 0, "columns");
+  static_assert(X_STAGES * X_BYTES >= (NT + 32) * 512, "a cluster's sums take X's place");
+  static_assert(COLS % 16 == 0, "columns");
 };
 
 struct Params {
   int M, C, K, ct, mt, tiles;   // tiles of inputs, of rows, of all
-  int parts, per, scale_bytes;  // of x; groups in 128 inputs, 0: one per output
+  int per, scale_bytes;         // groups in 128 inputs, 0: one per output
   int block;                    // bytes of packed weights of 16 outputs
   int box_rows, n;              // rows of a load of X, columns of an MMA
   int split_log2;               // CTAs of a cluster
-  int q8, x_group, act;
+  int q8, x_group, y_f32, act;
   const uint8_t* blocks;                // packed
   const uint8_t *zeros, *scales;        // per 0
   const float* xs;
@@ -84,28 +97,37 @@ struct Params {
   unsigned long long wait_ns;
 };
 
-// Output k of rows m, m + step, .. (rows of them); lanes of a warp are 32 consecutive outputs.
-template <typename T>
-__device__ __forceinline__ void finish(const Params& p, float (&v)[8], int m, int step, int rows,
-                                       int k, float scale, float bias) {
-  if (k >= p.K) return;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float s = scale;
-    if (p.q8 && !p.x_group && i < rows) s *= p.xs[m + i * step];
-    v[i] = fmaf(v[i], s, bias);
-  }
+// Output k of rows m, m + 1, .. (rows of them, up to N); lanes of a warp are 32 consecutive
+// outputs.
+template <typename T, int N>
+__device__ __forceinline__ void finish_as(const Params& p, float (&v)[N], int m, int rows, int k) {
   if (p.res) {
-    const T* const res = static_cast<const T*>(p.res) + m * p.ldr + k;
+    const T* res = static_cast<const T*>(p.res) + m * p.ldr + k;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < rows) v[i] += gb::fp4::load_f32(res + i * step * p.ldr);
+    for (int i = 0; i < N; ++i, res += p.ldr)
+      if (i < rows) v[i] += gb::fp4::load_f32(res);
   }
-  gb::fp4::activate<sizeof(T) == 4>(v, p.act);
-  T* const y = static_cast<T*>(p.y) + m * p.ldy + k;
+  if (p.act != CONV_ACT_NONE) gb::fp4::activate<sizeof(T) == 4>(v, p.act);
+  T* y = static_cast<T*>(p.y) + m * p.ldy + k;
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (i < rows) gb::fp4::store_f32(y + i * step * p.ldy, v[i]);
+  for (int i = 0; i < N; ++i, y += p.ldy)
+    if (i < rows) gb::fp4::store_f32(y, v[i]);
+}
+template <int N>
+__device__ __forceinline__ void finish(const Params& p, float (&v)[N], int m, int rows, int k,
+                                       float scale, float bias) {
+  if (k >= p.K) return;
+  if (p.q8 && !p.x_group) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i < rows) v[i] *= p.xs[m + i];
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = fmaf(v[i], scale, bias);
+  if (p.y_f32)
+    finish_as<float>(p, v, m, rows, k);
+  else
+    finish_as<__nv_bfloat16>(p, v, m, rows, k);
 }
 
 __device__ __forceinline__ float scale_at(const uint8_t* scales, size_t i, int bytes) {
@@ -135,17 +157,17 @@ struct Turn {
 // The warp that issues the MMAs.  Its loop is short and knows at compile time how many sums a
 // tile of inputs has: a single warp takes about five cycles an instruction, and with the
 // sums' bounds decided as it went it needed 700 cycles for 64 inputs, whose MMAs take 384.
-template <int NT>
+template <int NT, int SUMS>
 struct Mmas {
-  using C = Cfg<NT>;
+  using C = Cfg<NT, SUMS>;
   uint32_t tmem;
   const uint8_t* sX;
   uint64_t *x_full, *x_empty, *a_full, *a_empty, *d_full, *d_empty;
   uint32_t id;
 
-  // SUMS: of a tile of inputs; 0: one for all of them.  What an MMA is told (addresses,
+  // What an MMA is told (addresses,
   // descriptors) is worked out by the whole warp, before one lane issues it.
-  template <int SUMS, int PARTS>
+  template <int PARTS>
   __device__ __forceinline__ bool run(const Params& p, int first, int step, int c0, int c1) const {
     constexpr int STEPS = SUMS ? 8 / SUMS : 8;  // MMAs of a sum and part of x, 16 inputs each
     const bool one = gb::elect_one();
@@ -208,25 +230,93 @@ struct Mmas {
       }
     return ok;
   }
-  template <int SUMS>
-  __device__ __forceinline__ bool run(const Params& p, int first, int step, int c0, int c1) const {
-    if constexpr (NT <= 128)  // (fp32 x: its three parts would fill the rings of the widest)
-      if (p.parts == 3) return run<SUMS, 3>(p, first, step, c0, c1);
-    return run<SUMS, 1>(p, first, step, c0, c1);
+};
+
+// The warps that scale the accumulators and sum them up.  As Mmas, with what a tile of inputs
+// brings known at compile time.
+template <int NT, int COUNT>
+struct Sums {
+  using C = Cfg<NT, COUNT>;
+  const float* scales;  // the first place's: of this thread's output
+  const float* xs;      // and of its columns of x
+  uint64_t *d_full, *d_empty;
+  Turn s, d;
+
+  __device__ __forceinline__ void give_back(uint64_t* bar) const {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) gb::mbar_arrive(bar);
+  }
+
+  // One tile; the last accumulator stays this thread's.  t: its first column.  live: whether
+  // any of the columns is a row of X.
+  // XS: x has scales along the row, too.
+  template <bool XS>
+  __device__ __forceinline__ bool run(const Params& p, int c0, int c1, uint32_t t, bool live,
+                                      uint64_t (&acc)[C::COLS / 2]) {
+    for (int c = c0; c < c1; ++c) {
+#pragma unroll
+      for (int u = 0; u < COUNT; ++u) {
+        const float* const at = xs + s.at * C::S_FLOATS;
+        if (!gb::mbar_wait_bounded_warp(&d_full[d.at], d.phase, p.wait_ns, p.err)) return false;
+        gb::tc_fence_after();
+        if (live) {
+          const float su = p.per ? scales[s.at * C::S_FLOATS + u * TILE] : 1.0f;
+          const uint64_t s2 = pack2(su, su);
+          // 16 columns at a time, the next on their way from TMEM meanwhile
+          uint32_t r[2][16];
+          float4 f[2][4];
+          const auto fetch = [&](int b) {
+            gb::tmem_ld_x16(t + d.at * NT + b, r[(b / 16) & 1]);
+            if constexpr (XS)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                f[(b / 16) & 1][i] = *reinterpret_cast<const float4*>(at + b + 4 * i);
+          };
+          fetch(0);
+#pragma unroll
+          for (int b = 0; b < C::COLS; b += 16) {
+            gb::tmem_ld_wait();
+            if (b + 16 < C::COLS) fetch(b + 16);
+            const uint32_t(&v)[16] = r[(b / 16) & 1];
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+              uint64_t f0 = s2, f1 = s2;
+              if constexpr (XS) {
+                const float4 e = f[(b / 16) & 1][i / 4];
+                f0 = mul2(s2, pack2(e.x, e.y));
+                f1 = mul2(s2, pack2(e.z, e.w));
+              }
+              uint64_t& a0 = acc[(b + i) / 2];
+              uint64_t& a1 = acc[(b + i) / 2 + 1];
+              a0 = fma2(pack2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), f0, a0);
+              a1 = fma2(pack2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3])), f1, a1);
+            }
+          }
+        }
+        if (c == c1 - 1 && u == COUNT - 1) break;
+        gb::tc_fence_before();
+        give_back(&d_empty[d.at]);
+        d.next(C::NB);
+      }
+      s.next(C::S_STAGES);
+    }
+    return true;
   }
 };
 
-template <int NT, typename T>
-__global__ void __launch_bounds__(Cfg<NT>::THREADS, 1)
+// SUMS: accumulators of a tile of inputs; 0: one for the whole row (neither the weights nor x
+// change their scale along it).  XS: x has scales along the row.  PARTS: of x.
+template <int NT, int SUMS, bool XS, int PARTS>
+__global__ void __launch_bounds__(Cfg<NT, SUMS>::THREADS, 1)
     w4_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const Params p) {
-  using C = Cfg<NT>;
+  using C = Cfg<NT, SUMS>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* const sX = smem;
   uint8_t* const sW = sX + C::X_STAGES * C::X_BYTES;
-  float* const sXS = reinterpret_cast<float*>(sW + C::W_STAGES * C::W_BYTES);  // [2][NT]
-  uint64_t* const x_full = reinterpret_cast<uint64_t*>(sXS + 2 * NT);
+  float* const sS = reinterpret_cast<float*>(sW + C::W_STAGES * C::W_BYTES);  // scales
+  uint64_t* const x_full = reinterpret_cast<uint64_t*>(sS + C::S_STAGES * C::S_FLOATS);
   uint64_t* const x_empty = x_full + C::X_STAGES;
   uint64_t* const a_full = x_empty + C::X_STAGES;
   uint64_t* const a_empty = a_full + C::A_STAGES;
@@ -244,8 +334,6 @@ __global__ void __launch_bounds__(Cfg<NT>::THREADS, 1)
   // this CTA's tiles of inputs
   const int c0 = (int)((long long)p.ct * rank >> p.split_log2);
   const int c1 = (int)((long long)p.ct * (rank + 1) >> p.split_log2);
-  // one sum for the whole row: neither the weights nor x change their scale along it
-  const bool whole = p.per == 0 && !p.x_group;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::X_STAGES; ++s) {
@@ -253,12 +341,12 @@ __global__ void __launch_bounds__(Cfg<NT>::THREADS, 1)
       gb::mbar_init(&x_empty[s], 1);
     }
     for (int s = 0; s < C::A_STAGES; ++s) {
-      gb::mbar_init(&a_full[s], 4);
+      gb::mbar_init(&a_full[s], XS ? 5 : 4);  // the weights' four warps; x's scales
       gb::mbar_init(&a_empty[s], 1);
     }
     for (int s = 0; s < C::W_STAGES; ++s) {
       gb::mbar_init(&w_full[s], 1);
-      gb::mbar_init(&w_empty[s], 4 + (p.per ? 4 * C::SUM_WGS : 0));
+      gb::mbar_init(&w_empty[s], 4);
     }
     for (int s = 0; s < C::NB; ++s) {
       gb::mbar_init(&d_full[s], 1);
@@ -292,7 +380,7 @@ __global__ void __launch_bounds__(Cfg<NT>::THREADS, 1)
       for (int tile = first; tile < p.tiles && ok; tile += step) {
         const int m0 = tile % p.mt * NT;
         for (int c = c0; c < c1 && ok; ++c)
-          for (int h = 0; h < p.parts; ++h) {
+          for (int h = 0; h < PARTS; ++h) {
             ok = gb::mbar_wait_bounded_warp(&x_empty[x.at], x.phase ^ 1, p.wait_ns, p.err);
             if (!ok) break;
             if (one) {  // (inputs past the last read as 0)
@@ -347,17 +435,50 @@ __global__ void __launch_bounds__(Cfg<NT>::THREADS, 1)
       }
     } else if (warp == 1) {
       // ---------------- MMAs ----------------
-      const Mmas<NT> m{tmem, sX, x_full, x_empty, a_full, a_empty, d_full, d_empty,
+      const Mmas<NT, SUMS> m{tmem, sX, x_full, x_empty, a_full, a_empty, d_full, d_empty,
                        gb::idesc_f16(128, p.n, 1)};
-      const bool ok = whole        ? m.template run<0>(p, first, step, c0, c1)
-                      : p.per <= 1 ? m.template run<1>(p, first, step, c0, c1)
-                      : p.per == 2 ? m.template run<2>(p, first, step, c0, c1)
-                                   : m.template run<4>(p, first, step, c0, c1);
+      const bool ok = m.template run<PARTS>(p, first, step, c0, c1);
       if (!ok) {
         // the MMAs that were issued end before the memory they use is given up
         if (gb::elect_one()) gb::tc_commit(given_up);
         __syncwarp();
         gb::mbar_wait_bounded_warp(given_up, 0, p.wait_ns, p.err);
+      }
+    } else if (XS) {
+      // ---------------- scales of X ----------------
+      Turn s, a;
+      bool ok = true;
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      for (int tile = first; tile < p.tiles && ok; tile += step) {
+        const int m0 = tile % p.mt * NT + lane;
+        const float* const from = p.xs + (long long)m0 * p.ct;
+        // two tiles of inputs ahead: the loads take longer than the MMAs of one
+        constexpr int N = NT / 32;
+        float v[N], next[2][N];
+        const auto fetch = [&](float(&to)[N], int c) {
+#pragma unroll
+          for (int i = 0; i < N; ++i)
+            to[i] = c < c1 && m0 + 32 * i < p.M ? from[(long long)32 * i * p.ct + c] : 0.0f;
+        };
+        fetch(next[0], c0);
+        fetch(next[1], c0 + 1);
+        for (int c = c0; c < c1; ++c) {
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            v[i] = next[0][i];
+            next[0][i] = next[1][i];
+          }
+          fetch(next[1], c + 2);
+          ok = gb::mbar_wait_bounded_warp(&a_empty[a.at], a.phase ^ 1, p.wait_ns, p.err);
+          if (!ok) break;
+          float* const to = sS + s.at * C::S_FLOATS + 4 * TILE + lane;
+#pragma unroll
+          for (int i = 0; i < N; ++i) to[32 * i] = v[i];
+          __syncwarp();
+          if (lane == 0) gb::mbar_arrive(&a_full[a.at]);
+          s.next(C::S_STAGES);
+          a.next(C::A_STAGES);
+        }
       }
     }
   } else if (wg <= C::TAKE_WGS) {
@@ -365,17 +486,18 @@ __global__ void __launch_bounds__(Cfg<NT>::THREADS, 1)
     if constexpr (C::SPLIT_REGS) gb::registers_down_to<C::REGS_TAKE>();
     const int row = threadIdx.x & 127;
     const uint32_t from0 = (row >> 4) * p.block + (row & 15) * 64;
-    const uint32_t z0 = (row >> 4) * p.block + BLOCK_CODES + 16 * p.per * p.scale_bytes +
-                        (row & 15) * p.per;
+    const uint32_t s0 = (row >> 4) * p.block + BLOCK_CODES;
+    const uint32_t z0 = s0 + 16 * p.per * p.scale_bytes + (row & 15) * p.per;
     const uint32_t to = tmem + ((uint32_t)((warp & 3) * 32) << 16) + C::A0;
-    Turn w, a;
+    Turn w, a, s;
     int turn = 0;  // the warpgroups take every second tile of inputs
     bool ok = true;
     if (p.per == 0) asm volatile("griddepcontrol.wait;" ::: "memory");  // zeros from memory
     for (int tile = first; tile < p.tiles && ok; tile += step) {
       const uint32_t row_zero =
           p.per == 0 ? p.zeros[tile / p.mt * TILE + row] * 0x01010101u : 0u;
-      for (int c = c0; c < c1 && ok; ++c, turn ^= 1, w.next(C::W_STAGES), a.next(C::A_STAGES)) {
+      for (int c = c0; c < c1 && ok;
+           ++c, turn ^= 1, w.next(C::W_STAGES), a.next(C::A_STAGES), s.next(C::S_STAGES)) {
         if (turn != wg - 1) continue;
         ok = gb::mbar_wait_bounded_warp(&w_full[w.at], w.phase, p.wait_ns, p.err);
         if (!ok) break;
@@ -389,11 +511,19 @@ __global__ void __launch_bounds__(Cfg<NT>::THREADS, 1)
         if (p.per == 1) zero = *z * 0x01010101u;
         if (p.per == 2) zero = __byte_perm(*reinterpret_cast<const uint16_t*>(z), 0u, 0x1100);
         if (p.per == 4) zero = *reinterpret_cast<const uint32_t*>(z);
+        float scale[SUMS ? SUMS : 1];
+        if (SUMS && p.per)
+#pragma unroll
+          for (int u = 0; u < SUMS; ++u)
+            scale[u] = scale_at(from + s0, (row & 15) * SUMS + u, p.scale_bytes);
         __syncwarp();
         if (lane == 0) gb::mbar_arrive(&w_empty[w.at]);
         ok = gb::mbar_wait_bounded_warp(&a_empty[a.at], a.phase ^ 1, p.wait_ns, p.err);
         if (!ok) break;
         gb::tc_fence_after();
+        if (SUMS && p.per)
+#pragma unroll
+          for (int u = 0; u < SUMS; ++u) sS[s.at * C::S_FLOATS + u * TILE + row] = scale[u];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
           const uint32_t zz = zero_pair((zero >> (8 * t)) & 15u);
@@ -422,102 +552,41 @@ __global__ void __launch_bounds__(Cfg<NT>::THREADS, 1)
     const int part = wg - 1 - C::TAKE_WGS;  // of the columns
     const int o = (warp & 3) * 32 + lane, col0 = part * C::COLS;
     const uint32_t t = tmem + ((uint32_t)((warp & 3) * 32) << 16) + col0;
-    float* const xs = sXS + col0;  // [2] of them NT apart
-    Turn w, d;
-    int buffer = 0;  // of x's scales
+    Sums<NT, SUMS> sums{sS + o, sS + 4 * TILE + col0, d_full, d_empty, {}, {}};
     bool ok = true;
     for (int tile = first; tile < p.tiles && ok; tile += step) {
       const int m0 = tile % p.mt * NT + col0, k = tile / p.mt * TILE + o;
       const int live = min(C::COLS, p.M - m0);  // <= 0: none of these columns
-      uint64_t acc[C::COLS / 2];
+      if constexpr (SUMS == 0) {
+        ok = gb::mbar_wait_bounded_warp(&d_full[sums.d.at], sums.d.phase, p.wait_ns, p.err);
+        if (!ok) break;
+        gb::tc_fence_after();
+      } else {
+        uint64_t acc[C::COLS / 2];
 #pragma unroll
-      for (int i = 0; i < C::COLS / 2; ++i) acc[i] = 0;
-      const bool scales_x = p.x_group && o < live;
-      const float* const my_xs = scales_x ? p.xs + (long long)(m0 + o) * p.ct : nullptr;
-      float next_xs = scales_x ? my_xs[c0] : 0.0f;
-      uint32_t tc = t;
-      for (int c = c0; c < c1 && ok; ++c) {
-        if (whole && c < c1 - 1) continue;
-        float s[4] = {1.0f, 1.0f, 1.0f, 1.0f};
-        if (p.per) {
-          ok = gb::mbar_wait_bounded_warp(&w_full[w.at], w.phase, p.wait_ns, p.err);
-          if (!ok) break;
-          const uint8_t* const from = sW + w.at * C::W_BYTES + (o >> 4) * p.block + BLOCK_CODES;
+        for (int i = 0; i < C::COLS / 2; ++i) acc[i] = 0;
+        ok = sums.template run<XS>(p, c0, c1, t, live > 0, acc);
+        if (!ok) break;
+        // back to the last accumulator
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (i < p.per) s[i] = scale_at(from, (o & 15) * p.per + i, p.scale_bytes);
-          __syncwarp();
-          if (lane == 0) gb::mbar_arrive(&w_empty[w.at]);
-          w.next(C::W_STAGES);
-        }
-        if (p.x_group) {
-          // the chunk's scales of x, in two buffers used in turn: one barrier is enough
-          buffer ^= NT;
-          if (o < C::COLS) xs[buffer + o] = next_xs;
-          if (scales_x && c + 1 < c1) next_xs = my_xs[c + 1];
-          asm volatile("bar.sync %0, 128;" ::"r"(1 + part) : "memory");
-        }
-        const int sums = p.per <= 1 ? 1 : p.per;
-        for (int u = 0; u < sums && ok; ++u) {
-          ok = gb::mbar_wait_bounded_warp(&d_full[d.at], d.phase, p.wait_ns, p.err);
-          if (!ok) break;
-          gb::tc_fence_after();
-          tc = t + d.at * NT;
-          if (whole) break;
-          const float su = u == 0 ? s[0] : u == 1 ? s[1] : u == 2 ? s[2] : s[3];
-          const uint64_t s2 = pack2(su, su);
+        for (int b = 0; b < C::COLS; b += 16) {
+          uint32_t r[16];
 #pragma unroll
-          for (int b = 0; b < C::COLS; b += 32) {
-            if (b >= live) break;
-            uint32_t r[32];
-            gb::tmem_ld_x32(tc + b, r);
-            gb::tmem_ld_wait();
-            if (p.x_group) {
-#pragma unroll
-              for (int i = 0; i < 32; i += 4) {
-                const float4 f = *reinterpret_cast<const float4*>(xs + buffer + b + i);
-                acc[(b + i) / 2] =
-                    fma2(pack2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])),
-                         mul2(s2, pack2(f.x, f.y)), acc[(b + i) / 2]);
-                acc[(b + i) / 2 + 1] =
-                    fma2(pack2(__uint_as_float(r[i + 2]), __uint_as_float(r[i + 3])),
-                         mul2(s2, pack2(f.z, f.w)), acc[(b + i) / 2 + 1]);
-              }
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; i += 2)
-                acc[(b + i) / 2] = fma2(pack2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])),
-                                        s2, acc[(b + i) / 2]);
-            }
-          }
-          if (c == c1 - 1 && u == sums - 1) break;  // kept for the epilogue
-          gb::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) gb::mbar_arrive(&d_empty[d.at]);
-          d.next(C::NB);
-        }
-      }
-      if (!ok) break;
-      // the sums back to the last accumulator
-      if (!whole) {
-#pragma unroll
-        for (int b = 0; b < C::COLS; b += 32) {
-          if (b >= live) break;
-          uint32_t r[32];
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) {
+          for (int i = 0; i < 16; i += 2) {
             float f0, f1;
             unpack2(acc[(b + i) / 2], f0, f1);
             r[i] = __float_as_uint(f0);
             r[i + 1] = __float_as_uint(f1);
           }
-          gb::tmem_st_x32(tc + b, r);
+          gb::tmem_st_x16(t + sums.d.at * NT + b, r);
         }
         gb::tmem_st_wait();
       }
       if (split == 1) {
+        const uint32_t tc = t + sums.d.at * NT;
         const float scale = p.per == 0 ? scale_at(p.scales, k, p.scale_bytes) : 1.0f;
         const float bias = p.bias && k < p.K ? p.bias[k] : 0.0f;
+#pragma unroll 1
         for (int b = 0; b < live; b += 8) {
           uint32_t r[8];
           gb::tmem_ld_x8(tc + b, r);
@@ -525,12 +594,11 @@ __global__ void __launch_bounds__(Cfg<NT>::THREADS, 1)
           float v[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
-          finish<T>(p, v, m0 + b, 1, min(8, live - b), k, scale, bias);
+          finish(p, v, m0 + b, min(8, live - b), k, scale, bias);
         }
         gb::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) gb::mbar_arrive(&d_empty[d.at]);
-        d.next(C::NB);
+        sums.give_back(&d_empty[sums.d.at]);
+        sums.d.next(C::NB);
       }
     }
     if (split > 1) {
@@ -539,39 +607,45 @@ __global__ void __launch_bounds__(Cfg<NT>::THREADS, 1)
       __syncwarp();
       gb::cluster_sync();
       gb::tc_fence_after();
-      const int m0 = first % p.mt * NT + col0, live = min(C::COLS, p.M - m0);
-      const int rows = min(NT, p.M - first % p.mt * NT);
-      const int places = (rows + split - 1) >> p.split_log2;
-      // row m goes to CTA m % split, place m / split; source rank, place, output
-      const uint32_t mine = gb::smem_u32(sX) + 4 * o + 512 * rank * places;
-      const uint32_t tc = t + d.at * NT;
+      const int m0 = first % p.mt * NT, rows = min(NT, p.M - m0);
+      // each CTA of the cluster gets so many rows, four of them side by side:
+      // [source rank][rows / 4][output][4]
+      const int share = ((rows + split - 1) / split + 3) & ~3;
+      const int live = min(C::COLS, rows - col0);
+      const uint32_t mine = gb::smem_u32(sX) + 16 * o;
+      const uint32_t tc = t + sums.d.at * NT;
+#pragma unroll 1
       for (int b = 0; b < live; b += 8) {
         uint32_t r[8];
         gb::tmem_ld_x8(tc + b, r);
         gb::tmem_ld_wait();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int m = col0 + b + i;
+        for (int i = 0; i < 8; i += 4) {
+          const int row = col0 + b + i, to = row / share;
           if (b + i < live)
-            gb::store_cluster(gb::mapa_shared(mine + 512 * (m >> p.split_log2),
-                                              (uint32_t)(m & (split - 1))),
-                              r[i]);
+            gb::store_cluster4(gb::mapa_shared(mine + 512 * (rank * share + row - to * share),
+                                               (uint32_t)to),
+                               r[i], r[i + 1], r[i + 2], r[i + 3]);
         }
       }
       __syncwarp();
       gb::cluster_sync();
-      const int k = first / p.mt * TILE + o;
+      const int k = first / p.mt * TILE + o, row0 = rank * share;
       const float scale = p.per == 0 ? scale_at(p.scales, k, p.scale_bytes) : 1.0f;
       const float bias = p.bias && k < p.K ? p.bias[k] : 0.0f;
-      const float* const sums = reinterpret_cast<const float*>(sX) + o;
-      for (int i = 8 * part; rank + i * split < rows; i += 8 * C::SUM_WGS) {
-        const int n = min(8, (rows - rank - i * split + split - 1) >> p.split_log2);
-        float v[8] = {};
-        for (int r = 0; r < split; ++r)
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (e < n) v[e] += sums[128 * (r * places + i + e)];
-        finish<T>(p, v, first % p.mt * NT + rank + i * split, split, n, k, scale, bias);
+      const float4* const all = reinterpret_cast<const float4*>(sX) + o;
+#pragma unroll 1
+      for (int i = 4 * part; i < share && row0 + i < rows; i += 4 * C::SUM_WGS) {
+        float v[4] = {};
+#pragma unroll 1
+        for (int r = 0; r < split; ++r) {
+          const float4 f = all[32 * (r * share + i)];
+          v[0] += f.x;
+          v[1] += f.y;
+          v[2] += f.z;
+          v[3] += f.w;
+        }
+        finish(p, v, m0 + row0 + i, min(4, rows - row0 - i), k, scale, bias);
       }
     }
     gb::tc_fence_before();
@@ -589,7 +663,7 @@ __global__ void __launch_bounds__(Cfg<NT>::THREADS, 1)
 }
 
 // [parts][rows][cols] bf16 in boxes of BK x box_rows
-bool operand_map(CUtensorMap* map, const void* x, int parts, int rows, int cols, long long ld,
+inline bool operand_map(CUtensorMap* map, const void* x, int parts, int rows, int cols, long long ld,
                  int box_rows) {
   cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)parts};
   cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)ld * 2 * rows};
@@ -599,16 +673,9 @@ bool operand_map(CUtensorMap* map, const void* x, int parts, int rows, int cols,
                          strides, box, estr, CU_TENSOR_MAP_SWIZZLE_128B) == CUDA_SUCCESS;
 }
 
-// Whether the loads take x where it lies.
-bool in_place(const W4Gemm& g) {
-  return g.x_io == CONV_W4_IO_BF16 && reinterpret_cast<uintptr_t>(g.x) % 16 == 0 &&
-         g.ldx % 8 == 0;
-}
-
-template <int NT, typename T>
-cudaError_t launch_t(const W4Gemm& g, const void* x, int parts, int cols, long long ld,
-                     cudaStream_t st) {
-  using C = Cfg<NT>;
+template <int NT, int SUMS, bool XS, int PARTS>
+cudaError_t launch_kernel(const W4Gemm& g, const W4Operand& x, cudaStream_t st) {
+  using C = Cfg<NT, SUMS>;
   const Packed w = packed_layout(g.C, g.K, g.group, g.scale_f32 ? 4 : 2);
   Params p{};
   p.M = g.M;
@@ -619,11 +686,11 @@ cudaError_t launch_t(const W4Gemm& g, const void* x, int parts, int cols, long l
   if ((long long)w.kt * p.mt > 0x7FFFFFFF) return cudaErrorInvalidValue;
   p.tiles = w.kt * p.mt;
   p.block = w.block;
-  p.parts = parts;
   p.per = w.per;
   p.scale_bytes = g.scale_f32 ? 4 : 2;
   p.box_rows = std::min(NT, gb_ceil_div(g.M, 8) * 8);
   p.n = std::min(NT, gb_ceil_div(g.M, 16) * 16);
+  p.y_f32 = g.y_f32;
   p.q8 = g.xs != nullptr;
   p.x_group = g.x_group;
   p.act = g.act;
@@ -638,7 +705,7 @@ cudaError_t launch_t(const W4Gemm& g, const void* x, int parts, int cols, long l
   p.y = g.y;
   p.err = gb_device_error_word();
   p.wait_ns = gb_wait_limit_ns();
-  auto* kern = w4_gemm_kernel<NT, T>;
+  auto* kern = w4_gemm_kernel<NT, SUMS, XS, PARTS>;
   const void* const kp = reinterpret_cast<const void*>(kern);
   cudaError_t e = gb_set_smem_once(kp, C::SMEM);
   if (e != cudaSuccess) return e;
@@ -650,7 +717,7 @@ cudaError_t launch_t(const W4Gemm& g, const void* x, int parts, int cols, long l
          p.tiles <= gb_active_clusters(kp, C::THREADS, C::SMEM, 2 << p.split_log2))
     ++p.split_log2;
   CUtensorMap tx;
-  if (!operand_map(&tx, x, parts, g.M, cols, ld, p.box_rows)) return cudaErrorInvalidValue;
+  if (!operand_map(&tx, x.p, PARTS, g.M, x.cols, x.ld, p.box_rows)) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.split_log2 ? (unsigned)p.tiles << p.split_log2
                                   : (unsigned)std::min(p.tiles, gb_num_sms()));
@@ -671,43 +738,27 @@ cudaError_t launch_t(const W4Gemm& g, const void* x, int parts, int cols, long l
   return e;
 }
 
-template <typename T>
-cudaError_t launch_y(const W4Gemm& g, const void* x, int parts, int cols, long long ld,
-                     cudaStream_t st) {
-  // The width whose waves of tiles take least: a tile's columns, and about 48 of them for what
-  // a tile takes besides.
-  const auto cost = [&](int nt) {
-    const long long tiles = (long long)gb_ceil_div(g.K, TILE) * gb_ceil_div(g.M, nt);
-    return gb_ceil_div_ll(tiles, gb_num_sms()) * (nt + 48);
-  };
-  if (g.M <= 32) return launch_t<32, T>(g, x, parts, cols, ld, st);
-  if (g.M <= 64 || (cost(64) < cost(128) && cost(64) < cost(192)))
-    return launch_t<64, T>(g, x, parts, cols, ld, st);
-  // (fp32 x: its three parts would fill the rings of the widest)
-  if (g.M <= 128 || parts > 1 || cost(128) < cost(192))
-    return launch_t<128, T>(g, x, parts, cols, ld, st);
-  return launch_t<192, T>(g, x, parts, cols, ld, st);
-}
-
-}  // namespace
-
-size_t w4_gemm_workspace(const W4Gemm& g) {
-  const size_t parts = g.x_io == CONV_W4_IO_F32 ? 3 : 1;
-  return parts * g.M * (((size_t)g.C + 7) / 8 * 16);
-}
-
-cudaError_t launch_w4_gemm(const W4Gemm& g, cudaStream_t st) {
-  const void* x = g.x;
-  int parts = 1, cols = g.C;
-  long long ld = g.ldx;
-  if (!in_place(g)) {
-    const cudaError_t e = launch_w4_operands(g, g.ws, st);
-    if (e != cudaSuccess) return e;
-    x = g.ws;
-    parts = g.x_io == CONV_W4_IO_F32 ? 3 : 1;
-    cols = gb_ceil_div(g.C, 8) * 8;
-    ld = cols;
+template <int NT>
+cudaError_t launch(const W4Gemm& g, const W4Operand& x, cudaStream_t st) {
+  const int per = g.group ? TILE / g.group : 0;
+  if constexpr (NT <= 128) {  // (three parts would fill the rings of the widest)
+    if (x.parts == 3)
+      return per == 0   ? launch_kernel<NT, 0, false, 3>(g, x, st)
+             : per == 1 ? launch_kernel<NT, 1, false, 3>(g, x, st)
+             : per == 2 ? launch_kernel<NT, 2, false, 3>(g, x, st)
+                        : launch_kernel<NT, 4, false, 3>(g, x, st);
   }
-  return g.y_f32 ? launch_y<float>(g, x, parts, cols, ld, st)
-                 : launch_y<__nv_bfloat16>(g, x, parts, cols, ld, st);
+  if (x.parts != 1) return cudaErrorInvalidValue;
+  if (g.x_group)
+    return per <= 1   ? launch_kernel<NT, 1, true, 1>(g, x, st)
+           : per == 2 ? launch_kernel<NT, 2, true, 1>(g, x, st)
+                      : launch_kernel<NT, 4, true, 1>(g, x, st);
+  return per == 0   ? launch_kernel<NT, 0, false, 1>(g, x, st)
+         : per == 1 ? launch_kernel<NT, 1, false, 1>(g, x, st)
+         : per == 2 ? launch_kernel<NT, 2, false, 1>(g, x, st)
+                    : launch_kernel<NT, 4, false, 1>(g, x, st);
 }
+
+}  // namespace gemm
+}  // namespace w4
+}  // namespace gb

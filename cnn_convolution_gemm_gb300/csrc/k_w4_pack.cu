@@ -1,8 +1,9 @@
-// Integer 4-bit weights into the order the products read them (once a layer), and x as bf16
-// operands where it does not lie in memory as such.
+// Integer 4-bit weights into the order the products read them (once a layer), x as bf16 operands
+// where it does not lie in memory as such, and the choice of the product's tiles.
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cstdlib>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -131,4 +132,38 @@ cudaError_t launch_w4_operands(const W4Gemm& g, void* out, cudaStream_t st) {
     case CONV_W4_IO_E4M3: return go(operands_kernel<CONV_W4_IO_E4M3>);
     default: return go(operands_kernel<CONV_W4_IO_INT8>);
   }
+}
+
+// Whether the loads take x where it lies.
+static bool in_place(const W4Gemm& g) {
+  return g.x_io == CONV_W4_IO_BF16 && reinterpret_cast<uintptr_t>(g.x) % 16 == 0 &&
+         g.ldx % 8 == 0;
+}
+
+size_t w4_gemm_workspace(const W4Gemm& g) {
+  const size_t parts = g.x_io == CONV_W4_IO_F32 ? 3 : 1;
+  return parts * g.M * (((size_t)g.C + 7) / 8 * 16);
+}
+
+cudaError_t launch_w4_gemm(const W4Gemm& g, cudaStream_t st) {
+  W4Operand x{g.x, 1, g.C, g.ldx};
+  if (!in_place(g)) {
+    const cudaError_t e = launch_w4_operands(g, g.ws, st);
+    if (e != cudaSuccess) return e;
+    x.p = g.ws;
+    x.parts = g.x_io == CONV_W4_IO_F32 ? 3 : 1;
+    x.cols = gb_ceil_div(g.C, 8) * 8;
+    x.ld = x.cols;
+  }
+  if (const char* e = getenv("GB_NT")) { const int n = atoi(e); if (n == 64) return launch_w4_gemm_64(g, x, st); if (n == 128) return launch_w4_gemm_128(g, x, st); if (n == 160) return launch_w4_gemm_160(g, x, st); if (n == 192) return launch_w4_gemm_192(g, x, st); }
+  // The width whose waves of tiles take least: a tile's columns, and about 48 of them for what
+  // a tile takes besides.
+  const auto cost = [&](int nt) {
+    const long long tiles = (long long)gb_ceil_div(g.K, TILE) * gb_ceil_div(g.M, nt);
+    return gb_ceil_div_ll(tiles, gb_num_sms()) * (nt + 48);
+  };
+  const long long c64 = cost(64), c128 = cost(128), c192 = x.parts == 1 ? cost(192) : c128;
+  if (g.M <= 64 || (c64 < c128 && c64 < c192)) return launch_w4_gemm_64(g, x, st);
+  if (g.M <= 128 || x.parts > 1 || c128 < c192) return launch_w4_gemm_128(g, x, st);
+  return launch_w4_gemm_192(g, x, st);
 }

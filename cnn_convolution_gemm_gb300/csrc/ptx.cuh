@@ -266,7 +266,15 @@ __device__ __forceinline__ void store_cluster(uint32_t addr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
-// The same for a barrier that guards tensor memory or operand tiles alone: nothing that
+// Four of them, to a 16-byte aligned address.
+__device__ __forceinline__ void store_cluster4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                               uint32_t d) {
+  asm volatile("st.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
+               "r"(c), "r"(d)
+               : "memory");
+}
+
+// mbar_arrive_cluster for a barrier that guards tensor memory or operand tiles alone: nothing that
 // this thread wrote is read behind it, so the arrival needs no release across the
 // cluster (which waits for the thread's outstanding stores).
 __device__ __forceinline__ void mbar_arrive_cluster_control(uint32_t bar_cluster) {

@@ -195,6 +195,16 @@ bool w4_few_applicable(const W4Gemm& g);
 cudaError_t launch_w4_few(const W4Gemm& g, cudaStream_t st);
 // x as bf16 operands: kParts of [M][8 * ceil(C / 8)].
 cudaError_t launch_w4_operands(const W4Gemm& g, void* out, cudaStream_t st);
+struct W4Operand {
+  const void* p;
+  int parts, cols;  // [parts][M][cols]
+  long long ld;     // elements between rows
+};
+// Tiles of so many rows of X; 192: of one part.
+cudaError_t launch_w4_gemm_64(const W4Gemm& g, const W4Operand& x, cudaStream_t st);
+cudaError_t launch_w4_gemm_128(const W4Gemm& g, const W4Operand& x, cudaStream_t st);
+cudaError_t launch_w4_gemm_160(const W4Gemm& g, const W4Operand& x, cudaStream_t st);
+cudaError_t launch_w4_gemm_192(const W4Gemm& g, const W4Operand& x, cudaStream_t st);
 // Any number.  Workspace: x as bf16 operands, unless it lies so already.
 size_t w4_gemm_workspace(const W4Gemm& g);
 cudaError_t launch_w4_gemm(const W4Gemm& g, cudaStream_t st);
