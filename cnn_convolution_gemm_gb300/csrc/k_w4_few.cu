@@ -20,8 +20,8 @@ namespace {
 using namespace gb::w4;
 
 constexpr int WARPS = 8, THREADS = 32 * WARPS;
-constexpr int MOST_STAGES = 8;
-constexpr int MOST_SMEM = 224 * 1024;
+constexpr int MOST_STAGES = 4;
+constexpr int MOST_SMEM = 227 * 1024 - 1536;
 constexpr int X_PAD = 64;  // bytes between rows of x: two rows' pieces meet no bank twice
 
 struct FewParams {
@@ -44,29 +44,32 @@ struct FewParams {
   unsigned long long wait_ns;
 };
 
+// c = or += the product.
+template <bool ADD>
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                     uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  if constexpr (ADD)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
+        "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
+        "{%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
-// A stage of a warp's ring: 16 outputs' codes, scales and zeros of a tile.
+// 16 outputs' codes, scales and zeros of a tile of inputs; a stage of a warp's ring holds two.
 template <int PER, bool F32>
 struct Stage {
   static constexpr int CODES = BLOCK_CODES, SCALES = 16 * PER * (F32 ? 4 : 2), ZEROS = 16 * PER;
   static constexpr int BYTES = CODES + SCALES + ZEROS;
 
-  // one thread
   static __device__ __forceinline__ const uint8_t* block(const FewParams& p, int rg, int j) {
     return p.blocks + (((size_t)(rg >> 3) * p.ct + j) * 8 + (rg & 7)) * BYTES;
-  }
-  static __device__ __forceinline__ void fetch(uint8_t* to, uint64_t* full, const FewParams& p,
-                                               int rg, int j) {
-    gb::mbar_arrive_expect_tx(full, BYTES);
-    gb::bulk_load(to, block(p, rg, j), full, BYTES);
   }
   static __device__ __forceinline__ float scale(const uint8_t* stage, int r, int g) {
     const uint8_t* const p = stage + CODES + (r * PER + g) * (F32 ? 4 : 2);
@@ -84,15 +87,16 @@ struct Stage {
 
 // PER: groups in 128 inputs (0: one per output).  NT: MMAs of eight rows.
 template <int XIO, int PER, bool F32, int NT>
-__global__ void __launch_bounds__(THREADS, 2) w4_few_kernel(const FewParams p) {
+__global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) w4_few_kernel(const FewParams p) {
   constexpr int PARTS = kParts<XIO>;
   constexpr bool Q8 = XIO == CONV_W4_IO_E4M3 || XIO == CONV_W4_IO_INT8;
   using S = Stage<PER, F32>;
   extern __shared__ uint4 smem4[];
   __shared__ uint64_t full_all[WARPS][MOST_STAGES];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, q = lane & 3;
-  uint8_t* const ring = reinterpret_cast<uint8_t*>(smem4) + warp * p.stages * S::BYTES;
-  uint8_t* const sx = reinterpret_cast<uint8_t*>(smem4) + WARPS * p.stages * S::BYTES;
+  constexpr int STAGE = 2 * S::BYTES;
+  uint8_t* const ring = reinterpret_cast<uint8_t*>(smem4) + warp * p.stages * STAGE;
+  uint8_t* const sx = reinterpret_cast<uint8_t*>(smem4) + WARPS * p.stages * STAGE;
   const int part_bytes = p.M * p.pitch;  // of one of x's parts
   float* const sums = reinterpret_cast<float*>(sx + PARTS * part_bytes);  // [2][WARPS][8 NT][16]
   float* const sxs = sums + 2 * WARPS * NT * 128;                         // [M][ct]: x_group
@@ -103,7 +107,7 @@ __global__ void __launch_bounds__(THREADS, 2) w4_few_kernel(const FewParams p) {
   const int rg0 = blockIdx.x * at_once + sub, rg_step = gridDim.x * at_once;
   // the first weights on their way to L2 while the kernel before this one ends (whatever it
   // still writes, L2 holds)
-  if (rg0 < p.row_groups && lane < p.stages && j0 + lane * wc < p.ct)
+  if (rg0 < p.row_groups && lane < 2 * p.stages && j0 + lane * wc < p.ct)
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
                      S::block(p, rg0, j0 + lane * wc)),
                  "r"(S::BYTES)
@@ -115,14 +119,23 @@ __global__ void __launch_bounds__(THREADS, 2) w4_few_kernel(const FewParams p) {
   __syncwarp();
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  // the (row group, tile) pairs of this warp, in order
+  // the tiles of this warp in order, two to a stage: a wait, a refill and their arithmetic are
+  // as many instructions as half a tile's products
   int frg = rg0, fj = j0, issued = 0;
+  const uint8_t* from = S::block(p, rg0, j0);
+  const int next = wc * 8 * S::BYTES;
   const auto fetch = [&](int stage) {  // lane 0
-    S::fetch(ring + stage * S::BYTES, &full[stage], p, frg, fj);
+    uint8_t* const to = ring + stage * STAGE;
+    const bool two = fj + wc < p.ct;
+    gb::mbar_arrive_expect_tx(&full[stage], two ? STAGE : S::BYTES);
+    gb::bulk_load(to, from, &full[stage], S::BYTES);
+    if (two) gb::bulk_load(to + S::BYTES, from + next, &full[stage], S::BYTES);
     ++issued;
-    if ((fj += wc) >= p.ct) {
+    from += 2 * next;
+    if ((fj += 2 * wc) >= p.ct) {
       fj = j0;
       frg += rg_step;
+      from = S::block(p, frg, j0);
     }
   };
   if (lane == 0)
@@ -174,85 +187,82 @@ __global__ void __launch_bounds__(THREADS, 2) w4_few_kernel(const FewParams p) {
   // all warps go round together
   for (int rgb = blockIdx.x * at_once; rgb < p.row_groups; rgb += rg_step) {
     const int rg = rgb + sub;
-    float acc[NT][4] = {};
+    float acc[NT][4] = {}, acc1[NT][4] = {};
     if (rg < p.row_groups) {
       uint32_t za0 = 0, zb0 = 0;
       if constexpr (PER == 0) {
         za0 = p.zeros[rg * 16 + r];
         zb0 = p.zeros[rg * 16 + r + 8];
       }
-      for (int j = j0; j < p.ct && ok; j += wc) {
-        ok = gb::mbar_wait_bounded_warp(&full[stage], phase, p.wait_ns, p.err);
-        if (!ok) break;
-        ++taken;
-        {
-          const uint8_t* const w = ring + stage * S::BYTES;
-          const uint4 wa = *reinterpret_cast<const uint4*>(w + r * 64 + 16 * piece_slot(r, q));
-          const uint4 wb =
-              *reinterpret_cast<const uint4*>(w + (r + 8) * 64 + 16 * piece_slot(r + 8, q));
-          const uint32_t aw[4] = {wa.x, wa.y, wa.z, wa.w}, bw[4] = {wb.x, wb.y, wb.z, wb.w};
-          uint32_t zas = za0, zbs = zb0;
-          if constexpr (PER != 0) {
-            zas = S::zeros(w, r);
-            zbs = S::zeros(w, r + 8);
-          }
-          float part[NT][4] = {};
+      // w: the tile's block; j: which of the row's tiles
+      const auto product = [&](const uint8_t* w, int j) {
+        const uint4 wa = *reinterpret_cast<const uint4*>(w + r * 64 + 16 * piece_slot(r, q));
+        const uint4 wb =
+            *reinterpret_cast<const uint4*>(w + (r + 8) * 64 + 16 * piece_slot(r + 8, q));
+        const uint32_t aw[4] = {wa.x, wa.y, wa.z, wa.w}, bw[4] = {wb.x, wb.y, wb.z, wb.w};
+        uint32_t zas = za0, zbs = zb0;
+        if constexpr (PER != 0) {
+          zas = S::zeros(w, r);
+          zbs = S::zeros(w, r + 8);
+        }
+        constexpr int SPAN = PER ? 4 / PER : 4;  // words of a group
+        constexpr bool OWN = PER != 0 || Q8;     // sums of the tile's own, scaled afterwards
+        // (two chains: an MMA waits for the one before it on the same sums)
+        float part[2][NT][4];
 #pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            constexpr int SPAN = PER ? 4 / PER : 4;  // words of a group
-            const uint32_t za = (zas >> (8 * (t / SPAN))) & 15u;
-            const uint32_t zb = (zbs >> (8 * (t / SPAN))) & 15u;
-            const uint32_t zza = zero_pair(za), zzb = zero_pair(zb);
-            const uint32_t a0 = weight_pair<0>(aw[t], zza), a1 = weight_pair<1>(aw[t], zza),
-                           a2 = weight_pair<2>(aw[t], zza), a3 = weight_pair<3>(aw[t], zza);
-            const uint32_t b0 = weight_pair<0>(bw[t], zzb), b1 = weight_pair<1>(bw[t], zzb),
-                           b2 = weight_pair<2>(bw[t], zzb), b3 = weight_pair<3>(bw[t], zzb);
+        for (int t = 0; t < 4; ++t) {
+          const uint32_t byte = (t / SPAN) * 0x0101u | 0x4040u;
+          const uint32_t zza = __byte_perm(zas, 0x43434343u, byte);  // 128 + zero, twice
+          const uint32_t zzb = __byte_perm(zbs, 0x43434343u, byte);
+          const uint32_t a0 = weight_pair<0>(aw[t], zza), a1 = weight_pair<1>(aw[t], zza),
+                         a2 = weight_pair<2>(aw[t], zza), a3 = weight_pair<3>(aw[t], zza);
+          const uint32_t b0 = weight_pair<0>(bw[t], zzb), b1 = weight_pair<1>(bw[t], zzb),
+                         b2 = weight_pair<2>(bw[t], zzb), b3 = weight_pair<3>(bw[t], zzb);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              float(&sum)[4] = PER == 0 && !Q8 ? acc[n] : part[n];
+          for (int n = 0; n < NT; ++n) {
 #pragma unroll
-              for (int h = 0; h < PARTS; ++h) {
-                const uint4 xb = *reinterpret_cast<const uint4*>(bx[n] + h * part_bytes +
-                                                                 j * 256 + 64 * t);
-                mma(sum, a0, b0, a1, b1, xb.x, xb.y);
-                mma(sum, a2, b2, a3, b3, xb.z, xb.w);
-              }
-            }
-            if constexpr (PER != 0) {
-              if (t % SPAN == SPAN - 1) {
-                const float sa = S::scale(w, r, t / SPAN), sb = S::scale(w, r + 8, t / SPAN);
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                  float x0 = 1.0f, x1 = 1.0f;
-                  if (Q8 && p.x_group) {
-                    x0 = sxs[bs[n][0] + j];
-                    x1 = sxs[bs[n][1] + j];
-                  }
-                  acc[n][0] = fmaf(part[n][0], sa * x0, acc[n][0]);
-                  acc[n][1] = fmaf(part[n][1], sa * x1, acc[n][1]);
-                  acc[n][2] = fmaf(part[n][2], sb * x0, acc[n][2]);
-                  acc[n][3] = fmaf(part[n][3], sb * x1, acc[n][3]);
-#pragma unroll
-                  for (int i = 0; i < 4; ++i) part[n][i] = 0.0f;
-                }
+            for (int h = 0; h < PARTS; ++h) {
+              const uint4 xb =
+                  *reinterpret_cast<const uint4*>(bx[n] + h * part_bytes + j * 256 + 64 * t);
+              if constexpr (!OWN) {
+                mma<true>(acc[n], a0, b0, a1, b1, xb.x, xb.y);
+                mma<true>(acc1[n], a2, b2, a3, b3, xb.z, xb.w);
+              } else if (t % SPAN == 0 && h == 0) {
+                mma<false>(part[0][n], a0, b0, a1, b1, xb.x, xb.y);
+                mma<false>(part[1][n], a2, b2, a3, b3, xb.z, xb.w);
+              } else {
+                mma<true>(part[0][n], a0, b0, a1, b1, xb.x, xb.y);
+                mma<true>(part[1][n], a2, b2, a3, b3, xb.z, xb.w);
               }
             }
           }
-          if constexpr (PER == 0 && Q8) {
+          if (OWN && t % SPAN == SPAN - 1) {
+            const float sa = PER ? S::scale(w, r, t / SPAN) : 1.0f;
+            const float sb = PER ? S::scale(w, r + 8, t / SPAN) : 1.0f;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-              float x0 = 1.0f, x1 = 1.0f;
-              if (p.x_group) {
-                x0 = sxs[bs[n][0] + j];
-                x1 = sxs[bs[n][1] + j];
+              float s[4] = {sa, sa, sb, sb};
+              if (Q8 && p.x_group) {
+                const float x0 = sxs[bs[n][0] + j], x1 = sxs[bs[n][1] + j];
+                s[0] *= x0;
+                s[1] *= x1;
+                s[2] *= x0;
+                s[3] *= x1;
               }
-              acc[n][0] = fmaf(part[n][0], x0, acc[n][0]);
-              acc[n][1] = fmaf(part[n][1], x1, acc[n][1]);
-              acc[n][2] = fmaf(part[n][2], x0, acc[n][2]);
-              acc[n][3] = fmaf(part[n][3], x1, acc[n][3]);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                acc[n][i] = fmaf(part[0][n][i] + part[1][n][i], s[i], acc[n][i]);
             }
           }
         }
+      };
+      for (int j = j0; j < p.ct && ok; j += 2 * wc) {
+        ok = gb::mbar_wait_bounded_warp(&full[stage], phase, p.wait_ns, p.err);
+        if (!ok) break;
+        ++taken;
+        const uint8_t* const w = ring + stage * STAGE;
+        product(w, j);
+        if (j + wc < p.ct) product(w + S::BYTES, j + wc);
         __syncwarp();  // every lane has read the stage
         if (lane == 0 && frg < p.row_groups) fetch(stage);
         if (++stage == p.stages) {
@@ -267,7 +277,7 @@ __global__ void __launch_bounds__(THREADS, 2) w4_few_kernel(const FewParams p) {
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        to[(8 * n + 2 * q + (i & 1)) * 16 + r + 8 * (i >> 1)] = acc[n][i];
+        to[(8 * n + 2 * q + (i & 1)) * 16 + r + 8 * (i >> 1)] = acc[n][i] + acc1[n][i];
     __syncthreads();
     const int o = threadIdx.x & 15, s = (threadIdx.x >> 4) & (at_once - 1);
     const int k = (rgb + s) * 16 + o;
@@ -284,17 +294,16 @@ __global__ void __launch_bounds__(THREADS, 2) w4_few_kernel(const FewParams p) {
         for (int i = 0; i < wc; ++i) v += from[i * NT * 128];
         if (PER == 0) v *= row_scale;
         if (Q8 && !p.x_group) v *= p.xs[m];
-        float e[2] = {v + bias, 0.0f};
-        if (p.y_f32) {
-          if (p.res) e[0] += static_cast<const float*>(p.res)[m * p.ldr + k];
-          gb::fp4::activate<true>(e, p.act);
+        v += bias;
+        if (p.res)
+          v += p.y_f32 ? static_cast<const float*>(p.res)[m * p.ldr + k]
+                       : __bfloat162float(static_cast<const __nv_bfloat16*>(p.res)[m * p.ldr + k]);
+        float e[2] = {v, 0.0f};
+        if (p.act != CONV_ACT_NONE) gb::fp4::activate<true>(e, p.act);
+        if (p.y_f32)
           static_cast<float*>(p.y)[m * p.ldy + k] = e[0];
-        } else {
-          if (p.res)
-            e[0] += __bfloat162float(static_cast<const __nv_bfloat16*>(p.res)[m * p.ldr + k]);
-          gb::fp4::activate<false>(e, p.act);
+        else
           static_cast<__nv_bfloat16*>(p.y)[m * p.ldy + k] = __float2bfloat16_rn(e[0]);
-        }
       }
     }
     turn ^= 1;
@@ -311,21 +320,32 @@ __global__ void __launch_bounds__(THREADS, 2) w4_few_kernel(const FewParams p) {
   }
 }
 
+int warps_log2(const W4Gemm& g) {  // that share a reduction
+  int n = 0;
+  while (n < 3 && (2 << n) <= gb_ceil_div(g.C, TILE)) ++n;
+  return n;
+}
+
 // Shared memory: x (and its scales), the warps' sums, and the ring, as deep as there is room
-// for in half an SM's (or, where x is larger, all of it); stages 0: x does not fit.
+// for beside as many blocks as an SM gets, up to three (or, where x is larger, fewer); stages
+// 0: x does not fit.  No more blocks than the grid gives an SM: the ring is the deeper then
+// (4096 x 4096 6.0 us with thirds, so 4.9).
 struct FewSmem {
   int bytes, stages;
 };
 FewSmem few_smem(const W4Gemm& g) {
   const int per = g.group ? TILE / g.group : 0;
-  const long long stage = WARPS * (1024 + 16 * per * (g.scale_f32 ? 5 : 3));
+  const long long stage = 2 * WARPS * (BLOCK_CODES + 16 * per * (g.scale_f32 ? 5 : 3));
   const long long ct = gb_ceil_div(g.C, TILE);
   const long long parts = g.x_io == CONV_W4_IO_F32 ? 3 : 1, nt = g.M > 8 ? 2 : 1;
   const long long fixed = parts * g.M * (ct * 256 + X_PAD) + 2 * WARPS * nt * 512 +
                           (g.x_group ? g.M * ct * 4 : 0);
-  for (const long long most : {112 * 1024LL, (long long)MOST_SMEM}) {
+  const long long need = gb_ceil_div(gb_ceil_div(g.K, 16), WARPS >> warps_log2(g));
+  for (int blocks = (int)std::min<long long>(3, gb_ceil_div_ll(need, gb_num_sms())); blocks;
+       --blocks) {
+    const long long most = 227 * 1024 / blocks - 1024 - 512;  // the system's, the barriers
     const long long stages = std::min<long long>(MOST_STAGES, (most - fixed) / stage);
-    if (fixed < most && stages >= 4) return {(int)(fixed + stages * stage), (int)stages};
+    if (fixed < most && stages >= 2) return {(int)(fixed + stages * stage), (int)stages};
   }
   return {0, 0};
 }
@@ -338,8 +358,7 @@ cudaError_t launch_t(const W4Gemm& g, cudaStream_t st) {
   p.C = g.C;
   p.K = g.K;
   p.ct = w.ct;
-  p.wc_log2 = 0;
-  while (p.wc_log2 < 3 && (2 << p.wc_log2) <= w.ct) ++p.wc_log2;
+  p.wc_log2 = warps_log2(g);
   p.row_groups = gb_ceil_div(g.K, 16);
   p.pitch = w.ct * 256 + X_PAD;
   p.x_group = g.x_group;
@@ -366,7 +385,7 @@ cudaError_t launch_t(const W4Gemm& g, cudaStream_t st) {
   cudaError_t e = gb_set_smem_once(reinterpret_cast<const void*>(kern), MOST_SMEM);
   if (e != cudaSuccess) return e;
   const long long per_sm =
-      std::max(1, std::min(2, gb_blocks_per_sm(reinterpret_cast<const void*>(kern), THREADS, smem)));
+      std::max(1, gb_blocks_per_sm(reinterpret_cast<const void*>(kern), THREADS, smem));
   const long long need = gb_ceil_div(p.row_groups, WARPS >> p.wc_log2);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)std::min(need, per_sm * gb_num_sms()));

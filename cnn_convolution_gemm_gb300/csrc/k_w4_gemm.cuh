@@ -42,7 +42,7 @@ constexpr int BK = 64;  // inputs of a load of X: 128 bytes of bf16
 // NT: rows of X of a tile; SUMS: accumulators of a tile of inputs (0: one for the whole row).
 template <int NT, int SUMS>
 struct Cfg {
-  static constexpr int TAKE_WGS = 2;                   // that take codes apart
+  static constexpr int TAKE_WGS = NT == 64 ? 3 : 2;    // that take codes apart
   static constexpr int SUM_WGS = 2;                    // that scale and sum
   static constexpr int THREADS = 128 * (1 + TAKE_WGS + SUM_WGS);
   static constexpr int COLS = NT / SUM_WGS;            // columns of a summing thread
@@ -50,14 +50,18 @@ struct Cfg {
   // accumulator takes longer to hand over and to read than its MMAs: three are on their way
   // then.
   static constexpr int NB = NT == 128 ? (SUMS >= 2 ? 3 : 2) : NT > 128 ? 2 : 4;
-  static constexpr int A_STAGES = NT > 160 ? 2 : NT > 128 ? 3 : NT == 128 && SUMS >= 2 ? 2 : 4;
+  static constexpr int A_STAGES = NT > 128 ? 3 : NT == 128 && SUMS >= 2 ? 2 : 4;
   static constexpr int A_COLS = TILE / 2;
   static constexpr int A0 = NB * NT;                   // their first column
   static constexpr int TMEM_COLS = 512;
   static constexpr int X_HALF = NT * BK * 2;
   static constexpr int X_BYTES = 2 * X_HALF;           // a stage: 128 inputs, BK at a time
-  static constexpr int X_STAGES = NT > 160 ? 3 : NT >= 128 ? 4 : 6;
-  static constexpr int W_STAGES = NT == 160 ? 4 : NT > 128 ? 5 : 6;
+  static constexpr int X_STAGES = NT >= 128 ? 4 : 6;
+  // A multiple of the warpgroups that read them in turn: one that waits for a place has then
+  // itself read what was there before.  A wait by parity tells a phase only from the next: who
+  // waits two ahead, while another's load is still on its way, would pass at once.
+  static constexpr int W_STAGES = NT > 128 ? 4 : 6;
+  static_assert(W_STAGES % TAKE_WGS == 0 && TAKE_WGS <= A_STAGES, "waits by parity");
   static constexpr int W_BYTES = TILE * 64 + TILE * 4 * 5;  // of packed weights, at most
   // Scales of a tile of inputs: the weights' [4][128 outputs], x's [NT].  They are written before
   // the weights are handed to the MMAs and read once the sums are there, and no barrier of
@@ -168,7 +172,7 @@ struct Mmas {
   // What an MMA is told (addresses,
   // descriptors) is worked out by the whole warp, before one lane issues it.
   template <int PARTS>
-  __device__ __forceinline__ bool run(const Params& p, int first, int step, int c0, int c1) const {
+  __device__ __forceinline__ void run(const Params& p, int first, int step, int c0, int c1) const {
     constexpr int STEPS = SUMS ? 8 / SUMS : 8;  // MMAs of a sum and part of x, 16 inputs each
     const bool one = gb::elect_one();
     const uint64_t xd0 = gb::sw128_kmajor_desc(gb::smem_u32(sX));
@@ -228,7 +232,6 @@ struct Mmas {
           ap ^= 1;
         }
       }
-    return ok;
   }
 };
 
@@ -324,8 +327,8 @@ __global__ void __launch_bounds__(Cfg<NT, SUMS>::THREADS, 1)
   uint64_t* const w_empty = w_full + C::W_STAGES;
   uint64_t* const d_full = w_empty + C::W_STAGES;
   uint64_t* const d_empty = d_full + C::NB;
-  uint64_t* const given_up = d_empty + C::NB;
-  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(given_up + 1);
+  uint64_t* const last = d_empty + C::NB;
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(last + 1);
 
   const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0);  // uniform
   const int lane = threadIdx.x & 31, wg = warp >> 2;
@@ -352,7 +355,7 @@ __global__ void __launch_bounds__(Cfg<NT, SUMS>::THREADS, 1)
       gb::mbar_init(&d_full[s], 1);
       gb::mbar_init(&d_empty[s], 4 * C::SUM_WGS);
     }
-    gb::mbar_init(given_up, 1);
+    gb::mbar_init(last, 1);
     gb::fence_barrier_init();
     gb::tma_prefetch_desc(&tm_x);
   }
@@ -437,13 +440,11 @@ __global__ void __launch_bounds__(Cfg<NT, SUMS>::THREADS, 1)
       // ---------------- MMAs ----------------
       const Mmas<NT, SUMS> m{tmem, sX, x_full, x_empty, a_full, a_empty, d_full, d_empty,
                        gb::idesc_f16(128, p.n, 1)};
-      const bool ok = m.template run<PARTS>(p, first, step, c0, c1);
-      if (!ok) {
-        // the MMAs that were issued end before the memory they use is given up
-        if (gb::elect_one()) gb::tc_commit(given_up);
-        __syncwarp();
-        gb::mbar_wait_bounded_warp(given_up, 0, p.wait_ns, p.err);
-      }
+      m.template run<PARTS>(p, first, step, c0, c1);
+      // what was issued, and every arrival on a barrier, ends before the memory is given up
+      if (gb::elect_one()) gb::tc_commit(last);
+      __syncwarp();
+      gb::mbar_wait_bounded_warp(last, 0, p.wait_ns, p.err);
     } else if (XS) {
       // ---------------- scales of X ----------------
       Turn s, a;
@@ -490,14 +491,15 @@ __global__ void __launch_bounds__(Cfg<NT, SUMS>::THREADS, 1)
     const uint32_t z0 = s0 + 16 * p.per * p.scale_bytes + (row & 15) * p.per;
     const uint32_t to = tmem + ((uint32_t)((warp & 3) * 32) << 16) + C::A0;
     Turn w, a, s;
-    int turn = 0;  // the warpgroups take every second tile of inputs
+    int turn = 0;  // the warpgroups take the tiles of inputs in turn
     bool ok = true;
     if (p.per == 0) asm volatile("griddepcontrol.wait;" ::: "memory");  // zeros from memory
     for (int tile = first; tile < p.tiles && ok; tile += step) {
       const uint32_t row_zero =
           p.per == 0 ? p.zeros[tile / p.mt * TILE + row] * 0x01010101u : 0u;
       for (int c = c0; c < c1 && ok;
-           ++c, turn ^= 1, w.next(C::W_STAGES), a.next(C::A_STAGES), s.next(C::S_STAGES)) {
+           ++c, w.next(C::W_STAGES), a.next(C::A_STAGES), s.next(C::S_STAGES),
+           turn = turn + 1 < C::TAKE_WGS ? turn + 1 : 0) {
         if (turn != wg - 1) continue;
         ok = gb::mbar_wait_bounded_warp(&w_full[w.at], w.phase, p.wait_ns, p.err);
         if (!ok) break;

@@ -3,7 +3,6 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <cstdlib>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -155,15 +154,14 @@ cudaError_t launch_w4_gemm(const W4Gemm& g, cudaStream_t st) {
     x.cols = gb_ceil_div(g.C, 8) * 8;
     x.ld = x.cols;
   }
-  if (const char* e = getenv("GB_NT")) { const int n = atoi(e); if (n == 64) return launch_w4_gemm_64(g, x, st); if (n == 128) return launch_w4_gemm_128(g, x, st); if (n == 160) return launch_w4_gemm_160(g, x, st); if (n == 192) return launch_w4_gemm_192(g, x, st); }
   // The width whose waves of tiles take least: a tile's columns, and about 48 of them for what
   // a tile takes besides.
   const auto cost = [&](int nt) {
     const long long tiles = (long long)gb_ceil_div(g.K, TILE) * gb_ceil_div(g.M, nt);
     return gb_ceil_div_ll(tiles, gb_num_sms()) * (nt + 48);
   };
-  const long long c64 = cost(64), c128 = cost(128), c192 = x.parts == 1 ? cost(192) : c128;
-  if (g.M <= 64 || (c64 < c128 && c64 < c192)) return launch_w4_gemm_64(g, x, st);
-  if (g.M <= 128 || x.parts > 1 || c128 < c192) return launch_w4_gemm_128(g, x, st);
-  return launch_w4_gemm_192(g, x, st);
+  const long long c64 = cost(64), c128 = cost(128), c160 = x.parts == 1 ? cost(160) : c128;
+  if (g.M <= 64 || (c64 < c128 && c64 < c160)) return launch_w4_gemm_64(g, x, st);
+  if (g.M <= 128 || x.parts > 1 || c128 < c160) return launch_w4_gemm_128(g, x, st);
+  return launch_w4_gemm_160(g, x, st);
 }

@@ -200,11 +200,10 @@ struct W4Operand {
   int parts, cols;  // [parts][M][cols]
   long long ld;     // elements between rows
 };
-// Tiles of so many rows of X; 192: of one part.
+// Tiles of so many rows of X; 160: of one part.
 cudaError_t launch_w4_gemm_64(const W4Gemm& g, const W4Operand& x, cudaStream_t st);
 cudaError_t launch_w4_gemm_128(const W4Gemm& g, const W4Operand& x, cudaStream_t st);
 cudaError_t launch_w4_gemm_160(const W4Gemm& g, const W4Operand& x, cudaStream_t st);
-cudaError_t launch_w4_gemm_192(const W4Gemm& g, const W4Operand& x, cudaStream_t st);
 // Any number.  Workspace: x as bf16 operands, unless it lies so already.
 size_t w4_gemm_workspace(const W4Gemm& g);
 cudaError_t launch_w4_gemm(const W4Gemm& g, cudaStream_t st);
