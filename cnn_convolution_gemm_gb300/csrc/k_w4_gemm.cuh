@@ -79,7 +79,8 @@ struct Cfg {
   static_assert(!SPLIT_REGS || (1 + TAKE_WGS) * REGS_TAKE + SUM_WGS * REGS_SUM <=
                                    REGS * THREADS / 128, "registers");
   static_assert(A0 + A_STAGES * A_COLS <= TMEM_COLS && SMEM <= 232448, "TMEM, shared memory");
-  static_assert(X_STAGES * X_BYTES >= (NT + 32) * 512, "a cluster's sums take X's place");
+  // a cluster's sums take X's place: at most twice the rows, rounded up to a power of two a CTA
+  static_assert(X_STAGES * X_BYTES >= (NT > 128 ? 256 : 2 * NT) * 512, "sums of a cluster");
   static_assert(COLS % 16 == 0, "columns");
 };
 
@@ -89,6 +90,8 @@ struct Params {
   int block;                    // bytes of packed weights of 16 outputs
   int box_rows, n;              // rows of a load of X, columns of an MMA
   int split_log2;               // CTAs of a cluster
+  int share_log2;               // rows of a tile that each of them finishes (of the last fewer):
+                                // they lie [source rank][rows / 4][output][4] in X's place
   int q8, x_group, y_f32, act;
   const uint8_t* blocks;                // packed
   const uint8_t *zeros, *scales;        // per 0
@@ -181,21 +184,34 @@ struct Mmas {
     bool ok = true;
     for (int tile = first; tile < p.tiles && ok; tile += step)
       for (int c = c0; c < c1; ++c) {
-        ok = gb::mbar_wait_bounded_warp(&a_full[as], ap, p.wait_ns, p.err);
+        // one look at all barriers: most often everything is there, and a look takes about 75
+        // cycles by itself
         int at[PARTS];  // stages of x's parts
+        uint32_t parity[PARTS];
+        bool there = gb::mbar_try_wait(&a_full[as], ap);
 #pragma unroll
         for (int part = 0; part < PARTS; ++part) {
-          ok = ok && gb::mbar_wait_bounded_warp(&x_full[xs], xp, p.wait_ns, p.err);
           at[part] = xs;
+          parity[part] = xp;
+          there &= gb::mbar_try_wait(&x_full[xs], xp);
           if (++xs == C::X_STAGES) {
             xs = 0;
             xp ^= 1;
           }
         }
+        if (SUMS || c == c0) there &= gb::mbar_try_wait(&d_empty[ds], dp ^ 1);
+        there = __all_sync(0xFFFFFFFFu, there);
+        if (!there) {
+          ok = gb::mbar_wait_bounded_warp(&a_full[as], ap, p.wait_ns, p.err);
+#pragma unroll
+          for (int part = 0; part < PARTS; ++part)
+            ok = ok &&
+                 gb::mbar_wait_bounded_warp(&x_full[at[part]], parity[part], p.wait_ns, p.err);
+        }
         const uint32_t ad = tmem + C::A0 + as * C::A_COLS;
 #pragma unroll
         for (int u = 0; u < (SUMS ? SUMS : 1); ++u) {
-          if (SUMS || c == c0)
+          if ((SUMS || c == c0) && !(there && u == 0))
             ok = ok && gb::mbar_wait_bounded_warp(&d_empty[ds], dp ^ 1, p.wait_ns, p.err);
           if (!ok) break;
           gb::tc_fence_after();
@@ -609,11 +625,7 @@ __global__ void __launch_bounds__(Cfg<NT, SUMS>::THREADS, 1)
       __syncwarp();
       gb::cluster_sync();
       gb::tc_fence_after();
-      const int m0 = first % p.mt * NT, rows = min(NT, p.M - m0);
-      // each CTA of the cluster gets so many rows, four of them side by side:
-      // [source rank][rows / 4][output][4]
-      const int share = ((rows + split - 1) / split + 3) & ~3;
-      const int live = min(C::COLS, rows - col0);
+      const int live = min(C::COLS, p.M - first % p.mt * NT - col0);
       const uint32_t mine = gb::smem_u32(sX) + 16 * o;
       const uint32_t tc = t + sums.d.at * NT;
 #pragma unroll 1
@@ -623,39 +635,47 @@ __global__ void __launch_bounds__(Cfg<NT, SUMS>::THREADS, 1)
         gb::tmem_ld_wait();
 #pragma unroll
         for (int i = 0; i < 8; i += 4) {
-          const int row = col0 + b + i, to = row / share;
+          const int row = col0 + b + i;
           if (b + i < live)
-            gb::store_cluster4(gb::mapa_shared(mine + 512 * (rank * share + row - to * share),
-                                               (uint32_t)to),
-                               r[i], r[i + 1], r[i + 2], r[i + 3]);
+            gb::store_cluster4(
+                gb::mapa_shared(mine + 512 * ((rank << p.share_log2) +
+                                              (row & ((1 << p.share_log2) - 1))),
+                                (uint32_t)(row >> p.share_log2)),
+                r[i], r[i + 1], r[i + 2], r[i + 3]);
         }
-      }
-      __syncwarp();
-      gb::cluster_sync();
-      const int k = first / p.mt * TILE + o, row0 = rank * share;
-      const float scale = p.per == 0 ? scale_at(p.scales, k, p.scale_bytes) : 1.0f;
-      const float bias = p.bias && k < p.K ? p.bias[k] : 0.0f;
-      const float4* const all = reinterpret_cast<const float4*>(sX) + o;
-#pragma unroll 1
-      for (int i = 4 * part; i < share && row0 + i < rows; i += 4 * C::SUM_WGS) {
-        float v[4] = {};
-#pragma unroll 1
-        for (int r = 0; r < split; ++r) {
-          const float4 f = all[32 * (r * share + i)];
-          v[0] += f.x;
-          v[1] += f.y;
-          v[2] += f.z;
-          v[3] += f.w;
-        }
-        finish(p, v, m0 + row0 + i, min(4, rows - row0 - i), k, scale, bias);
       }
     }
     gb::tc_fence_before();
   }
-  if (split > 1 && wg <= C::TAKE_WGS) {
+  if (split > 1) {
     __syncwarp();
+    if (wg <= C::TAKE_WGS) gb::cluster_sync();  // the first of the two
     gb::cluster_sync();
-    gb::cluster_sync();
+  }
+  // The warps sum what the CTAs sent and finish it, four rows at a time: all of them, or, where
+  // the others have given registers away, those that hold them.
+  if (split > 1 && (!C::SPLIT_REGS || wg > C::TAKE_WGS)) {
+    constexpr int GROUPS = C::SPLIT_REGS ? C::SUM_WGS : C::THREADS / 128;
+    const int o = (warp & 3) * 32 + lane, k = first / p.mt * TILE + o;
+    const int m0 = first % p.mt * NT + (rank << p.share_log2);
+    const int rows = min(min(1 << p.share_log2, NT - (rank << p.share_log2)), p.M - m0);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const float scale = p.per == 0 ? scale_at(p.scales, k, p.scale_bytes) : 1.0f;
+    const float bias = p.bias && k < p.K ? p.bias[k] : 0.0f;
+    const float4* const all = reinterpret_cast<const float4*>(sX) + o;
+#pragma unroll 1
+    for (int i = 4 * (C::SPLIT_REGS ? wg - 1 - C::TAKE_WGS : wg); i < rows; i += 4 * GROUPS) {
+      float v[4] = {};
+#pragma unroll 1
+      for (int r = 0; r < split; ++r) {
+        const float4 f = all[32 * ((r << p.share_log2) + i)];
+        v[0] += f.x;
+        v[1] += f.y;
+        v[2] += f.z;
+        v[3] += f.w;
+      }
+      finish(p, v, m0 + i, min(4, rows - i), k, scale, bias);
+    }
   }
   __syncthreads();
   if (warp == 3) {
@@ -718,6 +738,8 @@ cudaError_t launch_kernel(const W4Gemm& g, const W4Operand& x, cudaStream_t st) 
          p.ct >> (p.split_log2 + 2) &&
          p.tiles <= gb_active_clusters(kp, C::THREADS, C::SMEM, 2 << p.split_log2))
     ++p.split_log2;
+  p.share_log2 = 2;
+  while ((1 << p.share_log2 << p.split_log2) < std::min(NT, g.M)) ++p.share_log2;
   CUtensorMap tx;
   if (!operand_map(&tx, x.p, PARTS, g.M, x.cols, x.ld, p.box_rows)) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
