@@ -40,7 +40,9 @@ using gb::fp4::unpack2;
 constexpr int BK = 64;  // inputs of a load of X: 128 bytes of bf16
 
 // NT: rows of X of a tile; SUMS: accumulators of a tile of inputs (0: one for the whole row).
-template <int NT, int SUMS>
+// PAIR: two CTAs with the same rows of X and neighbouring outputs share each MMA, and hold
+// half of X each.
+template <int NT, int SUMS, bool PAIR>
 struct Cfg {
   static constexpr int TAKE_WGS = NT == 64 ? 3 : 2;    // that take codes apart
   static constexpr int SUM_WGS = 2;                    // that scale and sum
@@ -54,13 +56,14 @@ struct Cfg {
   static constexpr int A_COLS = TILE / 2;
   static constexpr int A0 = NB * NT;                   // their first column
   static constexpr int TMEM_COLS = 512;
-  static constexpr int X_HALF = NT * BK * 2;
+  static constexpr int X_ROWS = PAIR ? NT / 2 : NT;    // that this CTA holds
+  static constexpr int X_HALF = X_ROWS * BK * 2;
   static constexpr int X_BYTES = 2 * X_HALF;           // a stage: 128 inputs, BK at a time
-  static constexpr int X_STAGES = NT >= 128 ? 4 : 6;
+  static constexpr int X_STAGES = NT >= 128 && !PAIR ? 4 : 6;
   // A multiple of the warpgroups that read them in turn: one that waits for a place has then
   // itself read what was there before.  A wait by parity tells a phase only from the next: who
   // waits two ahead, while another's load is still on its way, would pass at once.
-  static constexpr int W_STAGES = NT > 128 ? 4 : 6;
+  static constexpr int W_STAGES = NT > 128 && !PAIR ? 4 : 6;
   static_assert(W_STAGES % TAKE_WGS == 0 && TAKE_WGS <= A_STAGES, "waits by parity");
   static constexpr int W_BYTES = TILE * 64 + TILE * 4 * 5;  // of packed weights, at most
   // Scales of a tile of inputs: the weights' [4][128 outputs], x's [NT].  They are written before
@@ -80,12 +83,12 @@ struct Cfg {
                                    REGS * THREADS / 128, "registers");
   static_assert(A0 + A_STAGES * A_COLS <= TMEM_COLS && SMEM <= 232448, "TMEM, shared memory");
   // a cluster's sums take X's place: at most twice the rows, rounded up to a power of two a CTA
-  static_assert(X_STAGES * X_BYTES >= (NT > 128 ? 256 : 2 * NT) * 512, "sums of a cluster");
+  static_assert(PAIR || X_STAGES * X_BYTES >= (NT > 128 ? 256 : 2 * NT) * 512, "sums of a cluster");
   static_assert(COLS % 16 == 0, "columns");
 };
 
 struct Params {
-  int M, C, K, ct, mt, tiles;   // tiles of inputs, of rows, of all
+  int M, C, K, kt, ct, mt, tiles;  // tiles of outputs, of inputs, of rows, of all
   int per, scale_bytes;         // groups in 128 inputs, 0: one per output
   int block;                    // bytes of packed weights of 16 outputs
   int box_rows, n;              // rows of a load of X, columns of an MMA
@@ -164,16 +167,24 @@ struct Turn {
 // The warp that issues the MMAs.  Its loop is short and knows at compile time how many sums a
 // tile of inputs has: a single warp takes about five cycles an instruction, and with the
 // sums' bounds decided as it went it needed 700 cycles for 64 inputs, whose MMAs take 384.
-template <int NT, int SUMS>
+template <int NT, int SUMS, bool PAIR>
 struct Mmas {
-  using C = Cfg<NT, SUMS>;
+  using C = Cfg<NT, SUMS, PAIR>;
   uint32_t tmem;
   const uint8_t* sX;
   uint64_t *x_full, *x_empty, *a_full, *a_empty, *d_full, *d_empty;
   uint32_t id;
 
-  // What an MMA is told (addresses,
-  // descriptors) is worked out by the whole warp, before one lane issues it.
+  // one lane: bar is told, in both CTAs of a pair, when what was issued has ended
+  static __device__ __forceinline__ void commit(uint64_t* bar) {
+    if constexpr (PAIR)
+      gb::tc_commit_pair_multicast(bar, 3);
+    else
+      gb::tc_commit(bar);
+  }
+
+  // What an MMA is told (addresses, descriptors) is worked out by the whole warp, before one
+  // lane issues it.
   template <int PARTS>
   __device__ __forceinline__ void run(const Params& p, int first, int step, int c0, int c1) const {
     constexpr int STEPS = SUMS ? 8 / SUMS : 8;  // MMAs of a sum and part of x, 16 inputs each
@@ -225,12 +236,16 @@ struct Mmas {
             for (int i = 0; i < STEPS; ++i) {
               const int k = u * STEPS + i;
               const uint64_t kd = xd + (k / 4) * (C::X_HALF >> 4) + k % 4 * 2;
-              if (one)
-                gb::tc_mma_f16_ts(dd, ad + 8 * k, kd, id, i == 0 && part == 0 ? add : 1u);
+              const uint32_t more = i == 0 && part == 0 ? add : 1u;
+              if constexpr (PAIR) {
+                if (one) gb::tc_mma_f16_ts_pair(dd, ad + 8 * k, kd, id, more);
+              } else {
+                if (one) gb::tc_mma_f16_ts(dd, ad + 8 * k, kd, id, more);
+              }
             }
           }
           if (SUMS || c == c1 - 1) {
-            if (one) gb::tc_commit(done);
+            if (one) commit(done);
             if (++ds == C::NB) {
               ds = 0;
               dp ^= 1;
@@ -238,10 +253,10 @@ struct Mmas {
           }
         }
         if (!ok) break;
-        if (one) gb::tc_commit(&a_empty[as]);
+        if (one) commit(&a_empty[as]);
 #pragma unroll
         for (int part = 0; part < PARTS; ++part)
-          if (one) gb::tc_commit(&x_empty[at[part]]);
+          if (one) commit(&x_empty[at[part]]);
         __syncwarp();
         if (++as == C::A_STAGES) {
           as = 0;
@@ -253,17 +268,23 @@ struct Mmas {
 
 // The warps that scale the accumulators and sum them up.  As Mmas, with what a tile of inputs
 // brings known at compile time.
-template <int NT, int COUNT>
+template <int NT, int COUNT, bool PAIR>
 struct Sums {
-  using C = Cfg<NT, COUNT>;
+  using C = Cfg<NT, COUNT, PAIR>;
   const float* scales;  // the first place's: of this thread's output
   const float* xs;      // and of its columns of x
   uint64_t *d_full, *d_empty;
+  uint32_t d_empty0;    // d_empty of the CTA that issues the MMAs (cluster address)
   Turn s, d;
 
-  __device__ __forceinline__ void give_back(uint64_t* bar) const {
+  __device__ __forceinline__ void give_back() const {
     __syncwarp();
-    if ((threadIdx.x & 31) == 0) gb::mbar_arrive(bar);
+    if ((threadIdx.x & 31) == 0) {
+      if constexpr (PAIR)
+        gb::mbar_arrive_cluster_control(d_empty0 + 8 * d.at);
+      else
+        gb::mbar_arrive(&d_empty[d.at]);
+    }
   }
 
   // One tile; the last accumulator stays this thread's.  t: its first column.  live: whether
@@ -314,7 +335,7 @@ struct Sums {
         }
         if (c == c1 - 1 && u == COUNT - 1) break;
         gb::tc_fence_before();
-        give_back(&d_empty[d.at]);
+        give_back();
         d.next(C::NB);
       }
       s.next(C::S_STAGES);
@@ -325,10 +346,10 @@ struct Sums {
 
 // SUMS: accumulators of a tile of inputs; 0: one for the whole row (neither the weights nor x
 // change their scale along it).  XS: x has scales along the row.  PARTS: of x.
-template <int NT, int SUMS, bool XS, int PARTS>
-__global__ void __launch_bounds__(Cfg<NT, SUMS>::THREADS, 1)
+template <int NT, int SUMS, bool XS, int PARTS, bool PAIR>
+__global__ void __launch_bounds__(Cfg<NT, SUMS, PAIR>::THREADS, 1)
     w4_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const Params p) {
-  using C = Cfg<NT, SUMS>;
+  using C = Cfg<NT, SUMS, PAIR>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -349,7 +370,13 @@ __global__ void __launch_bounds__(Cfg<NT, SUMS>::THREADS, 1)
   const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0);  // uniform
   const int lane = threadIdx.x & 31, wg = warp >> 2;
   const int split = 1 << p.split_log2, rank = blockIdx.x & (split - 1);
-  const int first = blockIdx.x >> p.split_log2, step = gridDim.x >> p.split_log2;
+  // (a pair is not split; its CTAs take the same tiles, the second the next 128 outputs)
+  const int half = PAIR ? (int)(blockIdx.x & 1) : 0;
+  const int first = blockIdx.x >> (PAIR ? 1 : p.split_log2);
+  const int step = gridDim.x >> (PAIR ? 1 : p.split_log2);
+  const auto out_tile = [&](int tile) { return PAIR ? tile / p.mt * 2 + half : tile / p.mt; };
+  // of weights: a pair's second CTA may have none left, and takes the last ones along
+  const auto w_tile = [&](int tile) { return PAIR ? min(out_tile(tile), p.kt - 1) : out_tile(tile); };
   // this CTA's tiles of inputs
   const int c0 = (int)((long long)p.ct * rank >> p.split_log2);
   const int c1 = (int)((long long)p.ct * (rank + 1) >> p.split_log2);
@@ -360,7 +387,8 @@ __global__ void __launch_bounds__(Cfg<NT, SUMS>::THREADS, 1)
       gb::mbar_init(&x_empty[s], 1);
     }
     for (int s = 0; s < C::A_STAGES; ++s) {
-      gb::mbar_init(&a_full[s], XS ? 5 : 4);  // the weights' four warps; x's scales
+      // the weights' four warps and x's scales, of each CTA
+      gb::mbar_init(&a_full[s], (XS ? 5 : 4) * (PAIR ? 2 : 1));
       gb::mbar_init(&a_empty[s], 1);
     }
     for (int s = 0; s < C::W_STAGES; ++s) {
@@ -369,52 +397,75 @@ __global__ void __launch_bounds__(Cfg<NT, SUMS>::THREADS, 1)
     }
     for (int s = 0; s < C::NB; ++s) {
       gb::mbar_init(&d_full[s], 1);
-      gb::mbar_init(&d_empty[s], 4 * C::SUM_WGS);
+      gb::mbar_init(&d_empty[s], 4 * C::SUM_WGS * (PAIR ? 2 : 1));
     }
     gb::mbar_init(last, 1);
     gb::fence_barrier_init();
     gb::tma_prefetch_desc(&tm_x);
   }
   if (warp == 3) {
-    gb::tmem_alloc(tmem_slot, C::TMEM_COLS);
-    gb::tmem_relinquish();
+    if constexpr (PAIR) {
+      gb::tmem_alloc_pair(tmem_slot, C::TMEM_COLS);
+      gb::tmem_relinquish_pair();
+    } else {
+      gb::tmem_alloc(tmem_slot, C::TMEM_COLS);
+      gb::tmem_relinquish();
+    }
   }
   gb::tc_fence_before();
   __syncthreads();
-  if (split > 1) gb::cluster_sync();
+  if (PAIR || split > 1) gb::cluster_sync();
   gb::tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
   gb::allow_dependents();
+  // barriers of the CTA that issues a pair's MMAs
+  const uint32_t x_full0 = PAIR ? gb::mapa_shared(gb::smem_u32(x_full), 0) : 0;
+  const uint32_t a_full0 = PAIR ? gb::mapa_shared(gb::smem_u32(a_full), 0) : 0;
+  // one lane, once its warp's stores into tensor memory have ended; the scales beside them are
+  // read in this CTA (a release across the cluster took 1200 cycles)
+  const auto a_ready = [&](int stage) {
+    if constexpr (PAIR)
+      gb::mbar_arrive_cluster_control(a_full0 + 8 * stage);
+    else
+      gb::mbar_arrive(&a_full[stage]);
+  };
 
   if (wg == 0) {
     if constexpr (C::SPLIT_REGS) gb::registers_down_to<C::REGS_TAKE>();
     if (warp == 0) {
       // ---------------- X ----------------
       const bool one = gb::elect_one();
-      const uint32_t tx = (uint32_t)p.box_rows * (TILE * 2);
+      const uint32_t tx = (uint32_t)p.box_rows * (TILE * 2) * (PAIR ? 2 : 1);
       Turn x;
       int issued = 0;
       bool ok = true;
       asm volatile("griddepcontrol.wait;" ::: "memory");
       for (int tile = first; tile < p.tiles && ok; tile += step) {
-        const int m0 = tile % p.mt * NT;
+        const int m0 = tile % p.mt * NT + half * C::X_ROWS;
         for (int c = c0; c < c1 && ok; ++c)
           for (int h = 0; h < PARTS; ++h) {
             ok = gb::mbar_wait_bounded_warp(&x_empty[x.at], x.phase ^ 1, p.wait_ns, p.err);
             if (!ok) break;
             if (one) {  // (inputs past the last read as 0)
               uint8_t* const to = sX + x.at * C::X_BYTES;
-              gb::mbar_arrive_expect_tx(&x_full[x.at], tx);
-              gb::tma_load_3d(to, &tm_x, &x_full[x.at], c * TILE, m0, h);
-              gb::tma_load_3d(to + C::X_HALF, &tm_x, &x_full[x.at], c * TILE + BK, m0, h);
+              if (half == 0) gb::mbar_arrive_expect_tx(&x_full[x.at], tx);
+              if constexpr (PAIR) {
+                gb::tma_load_3d_pair(to, &tm_x, x_full0 + 8 * x.at, c * TILE, m0, h);
+                gb::tma_load_3d_pair(to + C::X_HALF, &tm_x, x_full0 + 8 * x.at, c * TILE + BK, m0,
+                                     h);
+              } else {
+                gb::tma_load_3d(to, &tm_x, &x_full[x.at], c * TILE, m0, h);
+                gb::tma_load_3d(to + C::X_HALF, &tm_x, &x_full[x.at], c * TILE + BK, m0, h);
+              }
             }
             __syncwarp();
             ++issued;
             x.next(C::X_STAGES);
           }
       }
-      // no copy into shared memory may be in flight at exit
-      for (int i = min(issued, C::X_STAGES); i > 0; --i) {
+      // no copy into shared memory may be in flight at exit (of a pair's second CTA: the first
+      // one's barriers tell; they leave together)
+      for (int i = half == 0 ? min(issued, C::X_STAGES) : 0; i > 0; --i) {
         x.back(C::X_STAGES);
         gb::mbar_wait_bounded_warp(&x_full[x.at], x.phase, p.wait_ns, p.err);
       }
@@ -429,7 +480,7 @@ __global__ void __launch_bounds__(Cfg<NT, SUMS>::THREADS, 1)
       // it still writes, L2 holds)
       if (first < p.tiles && lane < C::W_STAGES && c0 + lane < c1)
         asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
-                         p.blocks + ((size_t)(first / p.mt) * p.ct + c0 + lane) * bytes),
+                         p.blocks + ((size_t)w_tile(first) * p.ct + c0 + lane) * bytes),
                      "r"(bytes)
                      : "memory");
       __syncwarp();
@@ -441,7 +492,7 @@ __global__ void __launch_bounds__(Cfg<NT, SUMS>::THREADS, 1)
           if (one) {
             gb::mbar_arrive_expect_tx(&w_full[w.at], bytes);
             gb::bulk_load(sW + w.at * C::W_BYTES,
-                          p.blocks + ((size_t)(tile / p.mt) * p.ct + c) * bytes, &w_full[w.at],
+                          p.blocks + ((size_t)w_tile(tile) * p.ct + c) * bytes, &w_full[w.at],
                           bytes);
           }
           __syncwarp();
@@ -454,13 +505,17 @@ __global__ void __launch_bounds__(Cfg<NT, SUMS>::THREADS, 1)
       }
     } else if (warp == 1) {
       // ---------------- MMAs ----------------
-      const Mmas<NT, SUMS> m{tmem, sX, x_full, x_empty, a_full, a_empty, d_full, d_empty,
-                       gb::idesc_f16(128, p.n, 1)};
-      m.template run<PARTS>(p, first, step, c0, c1);
-      // what was issued, and every arrival on a barrier, ends before the memory is given up
-      if (gb::elect_one()) gb::tc_commit(last);
-      __syncwarp();
-      gb::mbar_wait_bounded_warp(last, 0, p.wait_ns, p.err);
+      using M = Mmas<NT, SUMS, PAIR>;
+      if (half == 0) {
+        const M m{tmem, sX, x_full, x_empty, a_full, a_empty, d_full, d_empty,
+                  gb::idesc_f16(PAIR ? 256 : 128, p.n, 1)};
+        m.template run<PARTS>(p, first, step, c0, c1);
+        // what was issued, and every arrival on a barrier, ends before the memory is given up
+        if (gb::elect_one()) M::commit(last);
+        __syncwarp();
+      }
+      // (a pair's second CTA waits for its arrival below, when the first one has had its own)
+      if (half == 0) gb::mbar_wait_bounded_warp(last, 0, p.wait_ns, p.err);
     } else if (XS) {
       // ---------------- scales of X ----------------
       Turn s, a;
@@ -492,7 +547,7 @@ __global__ void __launch_bounds__(Cfg<NT, SUMS>::THREADS, 1)
 #pragma unroll
           for (int i = 0; i < N; ++i) to[32 * i] = v[i];
           __syncwarp();
-          if (lane == 0) gb::mbar_arrive(&a_full[a.at]);
+          if (lane == 0) a_ready(a.at);
           s.next(C::S_STAGES);
           a.next(C::A_STAGES);
         }
@@ -512,7 +567,7 @@ __global__ void __launch_bounds__(Cfg<NT, SUMS>::THREADS, 1)
     if (p.per == 0) asm volatile("griddepcontrol.wait;" ::: "memory");  // zeros from memory
     for (int tile = first; tile < p.tiles && ok; tile += step) {
       const uint32_t row_zero =
-          p.per == 0 ? p.zeros[tile / p.mt * TILE + row] * 0x01010101u : 0u;
+          p.per == 0 ? p.zeros[w_tile(tile) * TILE + row] * 0x01010101u : 0u;
       for (int c = c0; c < c1 && ok;
            ++c, w.next(C::W_STAGES), a.next(C::A_STAGES), s.next(C::S_STAGES),
            turn = turn + 1 < C::TAKE_WGS ? turn + 1 : 0) {
@@ -560,7 +615,7 @@ __global__ void __launch_bounds__(Cfg<NT, SUMS>::THREADS, 1)
         gb::tmem_st_wait();
         gb::tc_fence_before();
         __syncwarp();
-        if (lane == 0) gb::mbar_arrive(&a_full[a.at]);
+        if (lane == 0) a_ready(a.at);
       }
     }
   } else {
@@ -570,10 +625,12 @@ __global__ void __launch_bounds__(Cfg<NT, SUMS>::THREADS, 1)
     const int part = wg - 1 - C::TAKE_WGS;  // of the columns
     const int o = (warp & 3) * 32 + lane, col0 = part * C::COLS;
     const uint32_t t = tmem + ((uint32_t)((warp & 3) * 32) << 16) + col0;
-    Sums<NT, SUMS> sums{sS + o, sS + 4 * TILE + col0, d_full, d_empty, {}, {}};
+    Sums<NT, SUMS, PAIR> sums{
+        sS + o, sS + 4 * TILE + col0, d_full, d_empty,
+        PAIR ? gb::mapa_shared(gb::smem_u32(d_empty), 0) : 0, {}, {}};
     bool ok = true;
     for (int tile = first; tile < p.tiles && ok; tile += step) {
-      const int m0 = tile % p.mt * NT + col0, k = tile / p.mt * TILE + o;
+      const int m0 = tile % p.mt * NT + col0, k = out_tile(tile) * TILE + o;
       const int live = min(C::COLS, p.M - m0);  // <= 0: none of these columns
       if constexpr (SUMS == 0) {
         ok = gb::mbar_wait_bounded_warp(&d_full[sums.d.at], sums.d.phase, p.wait_ns, p.err);
@@ -602,7 +659,8 @@ __global__ void __launch_bounds__(Cfg<NT, SUMS>::THREADS, 1)
       }
       if (split == 1) {
         const uint32_t tc = t + sums.d.at * NT;
-        const float scale = p.per == 0 ? scale_at(p.scales, k, p.scale_bytes) : 1.0f;
+        const float scale =
+            p.per == 0 ? scale_at(p.scales, w_tile(tile) * TILE + o, p.scale_bytes) : 1.0f;
         const float bias = p.bias && k < p.K ? p.bias[k] : 0.0f;
 #pragma unroll 1
         for (int b = 0; b < live; b += 8) {
@@ -615,7 +673,7 @@ __global__ void __launch_bounds__(Cfg<NT, SUMS>::THREADS, 1)
           finish(p, v, m0 + b, min(8, live - b), k, scale, bias);
         }
         gb::tc_fence_before();
-        sums.give_back(&d_empty[sums.d.at]);
+        sums.give_back();
         sums.d.next(C::NB);
       }
     }
@@ -652,9 +710,14 @@ __global__ void __launch_bounds__(Cfg<NT, SUMS>::THREADS, 1)
     if (wg <= C::TAKE_WGS) gb::cluster_sync();  // the first of the two
     gb::cluster_sync();
   }
+  if constexpr (PAIR) {  // neither CTA leaves while the other's MMAs or arrivals need it
+    __syncwarp();
+    gb::cluster_sync();
+    if (half && warp == 1) gb::mbar_wait_bounded_warp(last, 0, p.wait_ns, p.err);
+  }
   // The warps sum what the CTAs sent and finish it, four rows at a time: all of them, or, where
   // the others have given registers away, those that hold them.
-  if (split > 1 && (!C::SPLIT_REGS || wg > C::TAKE_WGS)) {
+  if (!PAIR && split > 1 && (!C::SPLIT_REGS || wg > C::TAKE_WGS)) {
     constexpr int GROUPS = C::SPLIT_REGS ? C::SUM_WGS : C::THREADS / 128;
     const int o = (warp & 3) * 32 + lane, k = first / p.mt * TILE + o;
     const int m0 = first % p.mt * NT + (rank << p.share_log2);
@@ -680,7 +743,10 @@ __global__ void __launch_bounds__(Cfg<NT, SUMS>::THREADS, 1)
   __syncthreads();
   if (warp == 3) {
     gb::tc_fence_after();
-    gb::tmem_dealloc(tmem, C::TMEM_COLS);
+    if constexpr (PAIR)
+      gb::tmem_dealloc_pair(tmem, C::TMEM_COLS);
+    else
+      gb::tmem_dealloc(tmem, C::TMEM_COLS);
   }
 }
 
@@ -695,9 +761,9 @@ inline bool operand_map(CUtensorMap* map, const void* x, int parts, int rows, in
                          strides, box, estr, CU_TENSOR_MAP_SWIZZLE_128B) == CUDA_SUCCESS;
 }
 
-template <int NT, int SUMS, bool XS, int PARTS>
-cudaError_t launch_kernel(const W4Gemm& g, const W4Operand& x, cudaStream_t st) {
-  using C = Cfg<NT, SUMS>;
+template <int NT, int SUMS, bool XS, int PARTS, bool PAIR>
+cudaError_t launch_as(const W4Gemm& g, const W4Operand& x, cudaStream_t st) {
+  using C = Cfg<NT, SUMS, PAIR>;
   const Packed w = packed_layout(g.C, g.K, g.group, g.scale_f32 ? 4 : 2);
   Params p{};
   p.M = g.M;
@@ -705,13 +771,14 @@ cudaError_t launch_kernel(const W4Gemm& g, const W4Operand& x, cudaStream_t st) 
   p.K = g.K;
   p.ct = w.ct;
   p.mt = gb_ceil_div(g.M, NT);
+  p.kt = w.kt;
   if ((long long)w.kt * p.mt > 0x7FFFFFFF) return cudaErrorInvalidValue;
-  p.tiles = w.kt * p.mt;
+  p.tiles = (PAIR ? (w.kt + 1) / 2 : w.kt) * p.mt;
   p.block = w.block;
   p.per = w.per;
   p.scale_bytes = g.scale_f32 ? 4 : 2;
-  p.box_rows = std::min(NT, gb_ceil_div(g.M, 8) * 8);
-  p.n = std::min(NT, gb_ceil_div(g.M, 16) * 16);
+  p.box_rows = PAIR ? C::X_ROWS : std::min(NT, gb_ceil_div(g.M, 8) * 8);
+  p.n = PAIR ? NT : std::min(NT, gb_ceil_div(g.M, 16) * 16);
   p.y_f32 = g.y_f32;
   p.q8 = g.xs != nullptr;
   p.x_group = g.x_group;
@@ -727,14 +794,14 @@ cudaError_t launch_kernel(const W4Gemm& g, const W4Operand& x, cudaStream_t st) 
   p.y = g.y;
   p.err = gb_device_error_word();
   p.wait_ns = gb_wait_limit_ns();
-  auto* kern = w4_gemm_kernel<NT, SUMS, XS, PARTS>;
+  auto* kern = w4_gemm_kernel<NT, SUMS, XS, PARTS, PAIR>;
   const void* const kp = reinterpret_cast<const void*>(kern);
   cudaError_t e = gb_set_smem_once(kp, C::SMEM);
   if (e != cudaSuccess) return e;
   // split the reduction while the tiles leave SMs idle, each CTA keeps two tiles of inputs and
   // all clusters find room at once
   p.split_log2 = 0;
-  while (p.split_log2 < 3 && ((long long)p.tiles << (p.split_log2 + 1)) <= gb_num_sms() &&
+  while (!PAIR && p.split_log2 < 3 && ((long long)p.tiles << (p.split_log2 + 1)) <= gb_num_sms() &&
          p.ct >> (p.split_log2 + 2) &&
          p.tiles <= gb_active_clusters(kp, C::THREADS, C::SMEM, 2 << p.split_log2))
     ++p.split_log2;
@@ -743,8 +810,9 @@ cudaError_t launch_kernel(const W4Gemm& g, const W4Operand& x, cudaStream_t st) 
   CUtensorMap tx;
   if (!operand_map(&tx, x.p, PARTS, g.M, x.cols, x.ld, p.box_rows)) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.split_log2 ? (unsigned)p.tiles << p.split_log2
-                                  : (unsigned)std::min(p.tiles, gb_num_sms()));
+  cfg.gridDim = dim3(PAIR           ? 2u * (unsigned)std::min(p.tiles, gb_num_sms() / 2)
+                     : p.split_log2 ? (unsigned)p.tiles << p.split_log2
+                                    : (unsigned)std::min(p.tiles, gb_num_sms()));
   cfg.blockDim = dim3(C::THREADS);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = st;
@@ -752,7 +820,7 @@ cudaError_t launch_kernel(const W4Gemm& g, const W4Operand& x, cudaStream_t st) 
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 1u << p.split_log2;
+  attr[1].val.clusterDim.x = PAIR ? 2u : 1u << p.split_log2;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
@@ -760,6 +828,17 @@ cudaError_t launch_kernel(const W4Gemm& g, const W4Operand& x, cudaStream_t st) 
   e = cudaLaunchKernelEx(&cfg, kern, tx, p);
   if (e == cudaSuccess) gb_count_launch();
   return e;
+}
+
+// Pairs where the tiles fill the GPU: there shared memory's 128 bytes a cycle, which X passes
+// twice, slow everything that goes through it.
+template <int NT, int SUMS, bool XS, int PARTS>
+cudaError_t launch_kernel(const W4Gemm& g, const W4Operand& x, cudaStream_t st) {
+  if constexpr (NT >= 128)
+    if (g.M >= NT && (long long)gb_ceil_div(g.K, 2 * TILE) * gb_ceil_div(g.M, NT) >=
+                         gb_num_sms() / 2)
+      return launch_as<NT, SUMS, XS, PARTS, true>(g, x, st);
+  return launch_as<NT, SUMS, XS, PARTS, false>(g, x, st);
 }
 
 template <int NT>
