@@ -41,11 +41,15 @@ constexpr int BK = 64;  // inputs of a load of X: 128 bytes of bf16
 
 // NT: rows of X of a tile; SUMS: accumulators of a tile of inputs (0: one for the whole row).
 // PAIR: two CTAs with the same rows of X and neighbouring outputs share each MMA, and hold
-// half of X each.
-template <int NT, int SUMS, bool PAIR>
+// half of X each.  XS: x has scales along the row.
+template <int NT, int SUMS, bool XS, bool PAIR>
 struct Cfg {
   static constexpr int TAKE_WGS = NT == 64 ? 3 : 2;    // that take codes apart
-  static constexpr int SUM_WGS = 2;                    // that scale and sum
+  // That scale and sum: their work is a chain of short waits, so there are many; or, where
+  // each column has a scale of its own, few, with registers for the next columns and scales to
+  // be on their way.
+  static constexpr int SUM_WGS = NT >= 128 && !XS ? 4 : 2;
+  static constexpr bool AHEAD = SUM_WGS == 2;
   static constexpr int THREADS = 128 * (1 + TAKE_WGS + SUM_WGS);
   static constexpr int COLS = NT / SUM_WGS;            // columns of a summing thread
   // Accumulators in TMEM, and stages of 128 inputs of weights beside them.  A small group's
@@ -78,13 +82,13 @@ struct Cfg {
   // at most what the block is launched with
   static constexpr bool SPLIT_REGS = NT >= 128;
   static constexpr int REGS = 65536 / THREADS / 8 * 8;
-  static constexpr int REGS_TAKE = 56, REGS_SUM = 152;
+  static constexpr int REGS_TAKE = 56, REGS_SUM = AHEAD ? 152 : 80;
   static_assert(!SPLIT_REGS || (1 + TAKE_WGS) * REGS_TAKE + SUM_WGS * REGS_SUM <=
                                    REGS * THREADS / 128, "registers");
   static_assert(A0 + A_STAGES * A_COLS <= TMEM_COLS && SMEM <= 232448, "TMEM, shared memory");
   // a cluster's sums take X's place: at most twice the rows, rounded up to a power of two a CTA
   static_assert(PAIR || X_STAGES * X_BYTES >= (NT > 128 ? 256 : 2 * NT) * 512, "sums of a cluster");
-  static_assert(COLS % 16 == 0, "columns");
+  static_assert(COLS % 8 == 0, "columns");
 };
 
 struct Params {
@@ -98,7 +102,7 @@ struct Params {
   int q8, x_group, y_f32, act;
   const uint8_t* blocks;                // packed
   const uint8_t *zeros, *scales;        // per 0
-  const float* xs;
+  const float* xs;                      // [M], or, along the row, [ct][M]
   const float* bias;
   const void* res;
   long long ldr, ldy;
@@ -167,9 +171,9 @@ struct Turn {
 // The warp that issues the MMAs.  Its loop is short and knows at compile time how many sums a
 // tile of inputs has: a single warp takes about five cycles an instruction, and with the
 // sums' bounds decided as it went it needed 700 cycles for 64 inputs, whose MMAs take 384.
-template <int NT, int SUMS, bool PAIR>
+template <int NT, int SUMS, bool XS, bool PAIR>
 struct Mmas {
-  using C = Cfg<NT, SUMS, PAIR>;
+  using C = Cfg<NT, SUMS, XS, PAIR>;
   uint32_t tmem;
   const uint8_t* sX;
   uint64_t *x_full, *x_empty, *a_full, *a_empty, *d_full, *d_empty;
@@ -268,9 +272,9 @@ struct Mmas {
 
 // The warps that scale the accumulators and sum them up.  As Mmas, with what a tile of inputs
 // brings known at compile time.
-template <int NT, int COUNT, bool PAIR>
+template <int NT, int COUNT, bool XS, bool PAIR>
 struct Sums {
-  using C = Cfg<NT, COUNT, PAIR>;
+  using C = Cfg<NT, COUNT, XS, PAIR>;
   const float* scales;  // the first place's: of this thread's output
   const float* xs;      // and of its columns of x
   uint64_t *d_full, *d_empty;
@@ -289,8 +293,6 @@ struct Sums {
 
   // One tile; the last accumulator stays this thread's.  t: its first column.  live: whether
   // any of the columns is a row of X.
-  // XS: x has scales along the row, too.
-  template <bool XS>
   __device__ __forceinline__ bool run(const Params& p, int c0, int c1, uint32_t t, bool live,
                                       uint64_t (&acc)[C::COLS / 2]) {
     for (int c = c0; c < c1; ++c) {
@@ -302,30 +304,39 @@ struct Sums {
         if (live) {
           const float su = p.per ? scales[s.at * C::S_FLOATS + u * TILE] : 1.0f;
           const uint64_t s2 = pack2(su, su);
-          // 16 columns at a time, the next on their way from TMEM meanwhile
-          uint32_t r[2][16];
-          float4 f[2][4];
+          // 16 columns at a time (the last 8), AHEAD: the next on their way from TMEM meanwhile
+          constexpr int N = C::AHEAD ? 2 : 1;
+          uint32_t r[N][16];
+          float4 f[N][4];
           const auto fetch = [&](int b) {
-            gb::tmem_ld_x16(t + d.at * NT + b, r[(b / 16) & 1]);
+            const int to = (b / 16) % N;
+            if (b + 16 <= C::COLS)
+              gb::tmem_ld_x16(t + d.at * NT + b, r[to]);
+            else
+              gb::tmem_ld_x8(t + d.at * NT + b, *reinterpret_cast<uint32_t(*)[8]>(r[to]));
             if constexpr (XS)
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                f[(b / 16) & 1][i] = *reinterpret_cast<const float4*>(at + b + 4 * i);
+                if (b + 4 * i < C::COLS)
+                  f[to][i] = *reinterpret_cast<const float4*>(at + b + 4 * i);
           };
-          fetch(0);
+          if (C::AHEAD) fetch(0);
 #pragma unroll
           for (int b = 0; b < C::COLS; b += 16) {
+            if (!C::AHEAD) fetch(b);
             gb::tmem_ld_wait();
-            if (b + 16 < C::COLS) fetch(b + 16);
-            const uint32_t(&v)[16] = r[(b / 16) & 1];
+            if (C::AHEAD && b + 16 < C::COLS) fetch(b + 16);
+            const int in = (b / 16) % N;
 #pragma unroll
             for (int i = 0; i < 16; i += 4) {
+              if (b + i >= C::COLS) break;
               uint64_t f0 = s2, f1 = s2;
               if constexpr (XS) {
-                const float4 e = f[(b / 16) & 1][i / 4];
+                const float4 e = f[in][i / 4];
                 f0 = mul2(s2, pack2(e.x, e.y));
                 f1 = mul2(s2, pack2(e.z, e.w));
               }
+              const uint32_t(&v)[16] = r[in];
               uint64_t& a0 = acc[(b + i) / 2];
               uint64_t& a1 = acc[(b + i) / 2 + 1];
               a0 = fma2(pack2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), f0, a0);
@@ -347,9 +358,9 @@ struct Sums {
 // SUMS: accumulators of a tile of inputs; 0: one for the whole row (neither the weights nor x
 // change their scale along it).  XS: x has scales along the row.  PARTS: of x.
 template <int NT, int SUMS, bool XS, int PARTS, bool PAIR>
-__global__ void __launch_bounds__(Cfg<NT, SUMS, PAIR>::THREADS, 1)
+__global__ void __launch_bounds__(Cfg<NT, SUMS, XS, PAIR>::THREADS, 1)
     w4_gemm_kernel(const __grid_constant__ CUtensorMap tm_x, const Params p) {
-  using C = Cfg<NT, SUMS, PAIR>;
+  using C = Cfg<NT, SUMS, XS, PAIR>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -505,7 +516,7 @@ __global__ void __launch_bounds__(Cfg<NT, SUMS, PAIR>::THREADS, 1)
       }
     } else if (warp == 1) {
       // ---------------- MMAs ----------------
-      using M = Mmas<NT, SUMS, PAIR>;
+      using M = Mmas<NT, SUMS, XS, PAIR>;
       if (half == 0) {
         const M m{tmem, sX, x_full, x_empty, a_full, a_empty, d_full, d_empty,
                   gb::idesc_f16(PAIR ? 256 : 128, p.n, 1)};
@@ -523,14 +534,14 @@ __global__ void __launch_bounds__(Cfg<NT, SUMS, PAIR>::THREADS, 1)
       asm volatile("griddepcontrol.wait;" ::: "memory");
       for (int tile = first; tile < p.tiles && ok; tile += step) {
         const int m0 = tile % p.mt * NT + lane;
-        const float* const from = p.xs + (long long)m0 * p.ct;
         // two tiles of inputs ahead: the loads take longer than the MMAs of one
         constexpr int N = NT / 32;
         float v[N], next[2][N];
         const auto fetch = [&](float(&to)[N], int c) {
+          const float* const from = p.xs + (long long)c * p.M + m0;
 #pragma unroll
           for (int i = 0; i < N; ++i)
-            to[i] = c < c1 && m0 + 32 * i < p.M ? from[(long long)32 * i * p.ct + c] : 0.0f;
+            to[i] = c < c1 && m0 + 32 * i < p.M ? from[32 * i] : 0.0f;
         };
         fetch(next[0], c0);
         fetch(next[1], c0 + 1);
@@ -625,7 +636,7 @@ __global__ void __launch_bounds__(Cfg<NT, SUMS, PAIR>::THREADS, 1)
     const int part = wg - 1 - C::TAKE_WGS;  // of the columns
     const int o = (warp & 3) * 32 + lane, col0 = part * C::COLS;
     const uint32_t t = tmem + ((uint32_t)((warp & 3) * 32) << 16) + col0;
-    Sums<NT, SUMS, PAIR> sums{
+    Sums<NT, SUMS, XS, PAIR> sums{
         sS + o, sS + 4 * TILE + col0, d_full, d_empty,
         PAIR ? gb::mapa_shared(gb::smem_u32(d_empty), 0) : 0, {}, {}};
     bool ok = true;
@@ -640,20 +651,20 @@ __global__ void __launch_bounds__(Cfg<NT, SUMS, PAIR>::THREADS, 1)
         uint64_t acc[C::COLS / 2];
 #pragma unroll
         for (int i = 0; i < C::COLS / 2; ++i) acc[i] = 0;
-        ok = sums.template run<XS>(p, c0, c1, t, live > 0, acc);
+        ok = sums.run(p, c0, c1, t, live > 0, acc);
         if (!ok) break;
         // back to the last accumulator
 #pragma unroll
-        for (int b = 0; b < C::COLS; b += 16) {
-          uint32_t r[16];
+        for (int b = 0; b < C::COLS; b += 8) {
+          uint32_t r[8];
 #pragma unroll
-          for (int i = 0; i < 16; i += 2) {
+          for (int i = 0; i < 8; i += 2) {
             float f0, f1;
             unpack2(acc[(b + i) / 2], f0, f1);
             r[i] = __float_as_uint(f0);
             r[i + 1] = __float_as_uint(f1);
           }
-          gb::tmem_st_x16(t + sums.d.at * NT + b, r);
+          gb::tmem_st_x8(t + sums.d.at * NT + b, r);
         }
         gb::tmem_st_wait();
       }
@@ -763,7 +774,7 @@ inline bool operand_map(CUtensorMap* map, const void* x, int parts, int rows, in
 
 template <int NT, int SUMS, bool XS, int PARTS, bool PAIR>
 cudaError_t launch_as(const W4Gemm& g, const W4Operand& x, cudaStream_t st) {
-  using C = Cfg<NT, SUMS, PAIR>;
+  using C = Cfg<NT, SUMS, XS, PAIR>;
   const Packed w = packed_layout(g.C, g.K, g.group, g.scale_f32 ? 4 : 2);
   Params p{};
   p.M = g.M;
@@ -786,7 +797,7 @@ cudaError_t launch_as(const W4Gemm& g, const W4Operand& x, cudaStream_t st) {
   p.blocks = g.packed;
   p.zeros = g.packed + w.zeros;
   p.scales = g.packed + w.scales;
-  p.xs = g.xs;
+  p.xs = x.xs;
   p.bias = g.bias;
   p.res = g.res;
   p.ldr = g.ldr;

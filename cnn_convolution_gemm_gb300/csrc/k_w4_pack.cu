@@ -77,7 +77,8 @@ __global__ void __launch_bounds__(THREADS)
 template <int XIO>
 __global__ void __launch_bounds__(THREADS)
     operands_kernel(const void* __restrict__ x, long long ldx, int M, int C, int vec, int pieces,
-                    uint4* __restrict__ out) {
+                    uint4* __restrict__ out, const float* __restrict__ xs,
+                    float* __restrict__ xs_out) {
   gb::allow_dependents();
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const long long all = (long long)M * pieces;
@@ -89,6 +90,9 @@ __global__ void __launch_bounds__(THREADS)
     raw.load(static_cast<const uint8_t*>(x) + m * ldx * kElemBytes<XIO>, c, C, vec);
 #pragma unroll
     for (int h = 0; h < kParts<XIO>; ++h) out[h * all + i] = raw.part(h);
+    // the products read the scales of many rows at a time
+    if (xs && c % TILE == 0)
+      xs_out[(long long)(c / TILE) * M + m] = xs[m * ((C + TILE - 1) / TILE) + c / TILE];
   }
 }
 
@@ -118,12 +122,14 @@ cudaError_t launch_w4_pack(int C, int K, int group, int scale_f32, const void* c
   return cudaGetLastError();
 }
 
-cudaError_t launch_w4_operands(const W4Gemm& g, void* out, cudaStream_t st) {
+cudaError_t launch_w4_operands(const W4Gemm& g, void* out, float* xs_out, cudaStream_t st) {
   const int pieces = gb_ceil_div(g.C, 8), vec = rows_vec8(g.x_io, g.x, g.ldx);
   const dim3 grid(grid_for((long long)g.M * pieces));
   uint4* const to = static_cast<uint4*>(out);
+  const float* const xs = g.x_group ? g.xs : nullptr;
   const auto go = [&](auto* kern) {
-    return gb::walk::launch_walk(kern, grid, st, g.x, g.ldx, g.M, g.C, vec, pieces, to);
+    return gb::walk::launch_walk(kern, grid, st, g.x, g.ldx, g.M, g.C, vec, pieces, to, xs,
+                                 xs_out);
   };
   switch (g.x_io) {
     case CONV_W4_IO_BF16: return go(operands_kernel<CONV_W4_IO_BF16>);
@@ -139,17 +145,22 @@ static bool in_place(const W4Gemm& g) {
          g.ldx % 8 == 0;
 }
 
-size_t w4_gemm_workspace(const W4Gemm& g) {
+static size_t operand_bytes(const W4Gemm& g) {
   const size_t parts = g.x_io == CONV_W4_IO_F32 ? 3 : 1;
   return parts * g.M * (((size_t)g.C + 7) / 8 * 16);
 }
+size_t w4_gemm_workspace(const W4Gemm& g) {
+  return operand_bytes(g) + (g.x_group ? (size_t)g.M * gb_ceil_div(g.C, TILE) * 4 : 0);
+}
 
 cudaError_t launch_w4_gemm(const W4Gemm& g, cudaStream_t st) {
-  W4Operand x{g.x, 1, g.C, g.ldx};
+  W4Operand x{g.x, 1, g.C, g.ldx, g.xs};
   if (!in_place(g)) {
-    const cudaError_t e = launch_w4_operands(g, g.ws, st);
+    float* const xs = reinterpret_cast<float*>(static_cast<char*>(g.ws) + operand_bytes(g));
+    const cudaError_t e = launch_w4_operands(g, g.ws, xs, st);
     if (e != cudaSuccess) return e;
     x.p = g.ws;
+    if (g.x_group) x.xs = xs;
     x.parts = g.x_io == CONV_W4_IO_F32 ? 3 : 1;
     x.cols = gb_ceil_div(g.C, 8) * 8;
     x.ld = x.cols;

@@ -193,18 +193,19 @@ struct W4Gemm {
 // Up to 16 rows, x in shared memory.
 bool w4_few_applicable(const W4Gemm& g);
 cudaError_t launch_w4_few(const W4Gemm& g, cudaStream_t st);
-// x as bf16 operands: kParts of [M][8 * ceil(C / 8)].
-cudaError_t launch_w4_operands(const W4Gemm& g, void* out, cudaStream_t st);
+// x as bf16 operands, kParts of [M][8 * ceil(C / 8)]; scales along the row to xs_out, [group][M].
+cudaError_t launch_w4_operands(const W4Gemm& g, void* out, float* xs_out, cudaStream_t st);
 struct W4Operand {
   const void* p;
   int parts, cols;  // [parts][M][cols]
   long long ld;     // elements between rows
+  const float* xs;  // scales: [M], or, with x_group, [ceil(C / 128)][M]
 };
 // Tiles of so many rows of X; 160: of one part.
 cudaError_t launch_w4_gemm_64(const W4Gemm& g, const W4Operand& x, cudaStream_t st);
 cudaError_t launch_w4_gemm_128(const W4Gemm& g, const W4Operand& x, cudaStream_t st);
 cudaError_t launch_w4_gemm_160(const W4Gemm& g, const W4Operand& x, cudaStream_t st);
-// Any number.  Workspace: x as bf16 operands, unless it lies so already.
+// Any number.  Workspace: x as bf16 operands, unless it lies so already, and its scales.
 size_t w4_gemm_workspace(const W4Gemm& g);
 cudaError_t launch_w4_gemm(const W4Gemm& g, cudaStream_t st);
 cudaError_t launch_w4_pack(int C, int K, int group, int scale_f32, const void* codes,
