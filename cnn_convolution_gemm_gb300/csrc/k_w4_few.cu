@@ -85,9 +85,19 @@ struct Stage {
   }
 };
 
+// A grid's y is which rows of X, 8 NT at a time.
 // PER: groups in 128 inputs (0: one per output).  NT: MMAs of eight rows.
 template <int XIO, int PER, bool F32, int NT>
-__global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) w4_few_kernel(const FewParams p) {
+__global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) w4_few_kernel(const FewParams all_rows) {
+  FewParams p = all_rows;
+  if (gridDim.y > 1) {
+    const int m0 = blockIdx.y * 8 * NT, yb = p.y_f32 ? 4 : 2;
+    p.M = min(8 * NT, p.M - m0);
+    p.x = static_cast<const uint8_t*>(p.x) + m0 * p.ldx * kElemBytes<XIO>;
+    if (p.xs) p.xs += (long long)m0 * (p.x_group ? p.ct : 1);
+    if (p.res) p.res = static_cast<const uint8_t*>(p.res) + m0 * p.ldr * yb;
+    p.y = static_cast<uint8_t*>(p.y) + m0 * p.ldy * yb;
+  }
   constexpr int PARTS = kParts<XIO>;
   constexpr bool Q8 = XIO == CONV_W4_IO_E4M3 || XIO == CONV_W4_IO_INT8;
   using S = Stage<PER, F32>;
@@ -338,9 +348,11 @@ FewSmem few_smem(const W4Gemm& g) {
   const long long stage = 2 * WARPS * (BLOCK_CODES + 16 * per * (g.scale_f32 ? 5 : 3));
   const long long ct = gb_ceil_div(g.C, TILE);
   const long long parts = g.x_io == CONV_W4_IO_F32 ? 3 : 1, nt = g.M > 8 ? 2 : 1;
-  const long long fixed = parts * g.M * (ct * 256 + X_PAD) + 2 * WARPS * nt * 512 +
-                          (g.x_group ? g.M * ct * 4 : 0);
-  const long long need = gb_ceil_div(gb_ceil_div(g.K, 16), WARPS >> warps_log2(g));
+  const long long rows = std::min(g.M, 16);  // of a block
+  const long long fixed = parts * rows * (ct * 256 + X_PAD) + 2 * WARPS * nt * 512 +
+                          (g.x_group ? rows * ct * 4 : 0);
+  const long long need = (long long)gb_ceil_div(gb_ceil_div(g.K, 16), WARPS >> warps_log2(g)) *
+                         gb_ceil_div(g.M, 16);
   for (int blocks = (int)std::min<long long>(3, gb_ceil_div_ll(need, gb_num_sms())); blocks;
        --blocks) {
     const long long most = 227 * 1024 / blocks - 1024 - 512;  // the system's, the barriers
@@ -386,9 +398,10 @@ cudaError_t launch_t(const W4Gemm& g, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const long long per_sm =
       std::max(1, gb_blocks_per_sm(reinterpret_cast<const void*>(kern), THREADS, smem));
-  const long long need = gb_ceil_div(p.row_groups, WARPS >> p.wc_log2);
+  const int need = gb_ceil_div(p.row_groups, WARPS >> p.wc_log2), blocks = gb_ceil_div(g.M, 16);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)std::min(need, per_sm * gb_num_sms()));
+  cfg.gridDim = dim3((unsigned)std::min<long long>(need, gb_ceil_div_ll(per_sm * gb_num_sms(), blocks)),
+                     (unsigned)blocks);
   cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
@@ -420,7 +433,15 @@ cudaError_t launch_group(const W4Gemm& g, cudaStream_t st) {
 
 }  // namespace
 
-bool w4_few_applicable(const W4Gemm& g) { return g.M <= 16 && few_smem(g).stages > 0; }
+// Up to eight rows always; more, 16 to a block, where the layer is so small that a call is mostly
+// latency (64 x 512 x 512 3.0 us, on tcgen05 5.3; 16 x 2048 x 2048 4.9 and 5.4, 32 rows 6.2 and
+// 5.8; 16 x 4096 x 1024, where each block converts as much x as it reads weights, 8.0 and 5.8).
+bool w4_few_applicable(const W4Gemm& g) {
+  if (g.M > 8 &&
+      (g.C > 2048 || (long long)gb_ceil_div(g.M, 16) * g.C * g.K > 4500000))
+    return false;
+  return few_smem(g).stages > 0;
+}
 
 cudaError_t launch_w4_few(const W4Gemm& g, cudaStream_t st) {
   switch (g.x_io) {

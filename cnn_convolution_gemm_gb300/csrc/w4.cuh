@@ -190,7 +190,7 @@ struct W4Gemm {
   void* y;
   void* ws;
 };
-// Up to 16 rows, x in shared memory.
+// Few rows or small layers, x in shared memory.
 bool w4_few_applicable(const W4Gemm& g);
 cudaError_t launch_w4_few(const W4Gemm& g, cudaStream_t st);
 // x as bf16 operands, kParts of [M][8 * ceil(C / 8)]; scales along the row to xs_out, [group][M].
