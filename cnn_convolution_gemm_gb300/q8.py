@@ -66,10 +66,13 @@ def quantize(x: torch.Tensor, fmt, group=0, out: Q8Tensor | None = None, stream=
     """x [..., cols] (bf16 or fp32) in 8 bits: fmt 'e4m3' or 'int8' (or binding.CONV_Q8_*), with a
     scale for each row (group 0) or each 128 columns of it (group 128)."""
     cols = x.shape[-1]
-    rows, ld = rows_of(x, cols, "x") if cols else (0, 0)
-    fmt, group = format_of(fmt), group_of(group)
+    if x.is_contiguous() and cols:
+        rows, ld = x.numel() // cols, cols
+    else:
+        rows, ld = rows_of(x, cols, "x") if cols else (0, 0)
+    fmt = FORMATS.get(fmt, fmt)
     if out is None:
-        out = empty(rows, cols, fmt, x.device, group, stream)
+        out = empty(rows, cols, fmt, x.device, group, stream)  # checks fmt and group
     elif out.shape != (rows, cols, fmt, group):
         raise ValueError("out: an 8-bit matrix of another shape, format or group")
     index = out.index
@@ -86,12 +89,16 @@ def dequantize(t: Q8Tensor, dtype=torch.bfloat16, out: torch.Tensor | None = Non
     if out is None:
         with allocating_on(stream):
             out = torch.empty(t.rows, t.cols, dtype=dtype, device=t.device)
-    rows, ld = rows_of(out, t.cols, "out")
-    if rows != t.rows:
-        raise ValueError(f"out: {rows} rows, expected {t.rows}")
+    rows, cols = t.rows, t.cols
+    if out.shape == (rows, cols) and out.is_contiguous():
+        ld = cols
+    else:
+        got, ld = rows_of(out, cols, "out")
+        if got != rows:
+            raise ValueError(f"out: {got} rows, expected {rows}")
     index = t.index
     if out.get_device() != index:
         raise ValueError("out: on another device than t")
-    B.conv_q8_dequantize(t.fmt, t.group, CONV_DTYPE[out.dtype], rows, t.cols, t.codes_ptr,
+    B.conv_q8_dequantize(t.fmt, t.group, CONV_DTYPE[out.dtype], rows, cols, t.codes_ptr,
                          t.scales_ptr, out.data_ptr(), ld, call_stream(index, stream))
     return out

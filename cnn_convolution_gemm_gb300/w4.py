@@ -9,6 +9,7 @@ import torch
 from . import binding as B
 from . import q8
 from .fp4 import CONV_DTYPE, Types, Workspaces, allocating_on, call_stream, rows_of
+from .q8 import Q8Tensor
 
 IO = Types({torch.bfloat16: B.CONV_W4_IO_BF16, torch.float32: B.CONV_W4_IO_F32})
 IO_Q8 = {B.CONV_Q8_E4M3: B.CONV_W4_IO_E4M3, B.CONV_Q8_INT8: B.CONV_W4_IO_INT8}
@@ -31,12 +32,13 @@ class W4Linear:
         self.C, self.K, self.group = C, K, group
         self.x_dtype, self.y_dtype, self.scale_dtype = x_dtype, y_dtype, scale_dtype
         self.x_q8, self.x_group = None if x_q8 is None else q8.format_of(x_q8), x_group
+        self._x_shape = (C, self.x_q8, x_group)
         self.desc = B.conv_w4_create(C, K, group, CONV_DTYPE[scale_dtype],
                                      IO[x_dtype] if x_q8 is None else IO_Q8[self.x_q8],
                                      CONV_DTYPE[y_dtype])
         B.conv_w4_set_input_group(self.desc, x_group)
         B.conv_w4_set_epilogue(self.desc, act, has_residual)
-        self.w = None  # the packed weights
+        self.w = None  # the packed weights, their address and device
         # a call gives the descriptor its strides and launches before another call, or other
         # weights, change them; calls on one stream share its workspace
         self._lock = threading.Lock()
@@ -74,20 +76,21 @@ class W4Linear:
         B.conv_w4_prepack(self.desc, codes.data_ptr(), scales.data_ptr(),
                           None if zeros is None else zeros.data_ptr(), packed.data_ptr(), handle)
         with self._lock:
-            self.w = packed
+            self.w = (packed, packed.data_ptr(), packed.get_device())
 
     def forward(self, x, bias=None, residual=None, out=None, stream=None):
         with self._lock:
             w = self.w
             if w is None:
                 raise RuntimeError("load() the weights first")
-            C, K, y_dtype, index = self.C, self.K, self.y_dtype, w.get_device()
+            w, wp, index = w
+            C, K, y_dtype = self.C, self.K, self.y_dtype
             handle = call_stream(index, stream)
             bp = rp = xsp = None
             if self.x_dtype is None:
-                if not isinstance(x, q8.Q8Tensor):
+                if type(x) is not Q8Tensor:
                     raise ValueError("x: expected a Q8Tensor")
-                if (x.cols, x.fmt, x.group) != (C, self.x_q8, self.x_group):
+                if x.shape[1:] != self._x_shape:
                     raise ValueError("x: an 8-bit matrix of another width, format or group")
                 if x.index != index:
                     raise ValueError("x: on another device than the weights")
@@ -98,7 +101,10 @@ class W4Linear:
                     raise ValueError(f"x: {x.dtype}, expected {self.x_dtype}")
                 if x.get_device() != index:
                     raise ValueError("x: on another device than the weights")
-                rows, ldx = rows_of(x, C, "x")
+                if x.is_contiguous() and x.shape[-1] == C:
+                    rows, ldx = x.numel() // C, C
+                else:
+                    rows, ldx = rows_of(x, C, "x")
                 xp = x.data_ptr()
             if bias is not None:
                 if bias.dtype is not torch.float32 or bias.numel() != K or not bias.is_contiguous():
@@ -113,7 +119,10 @@ class W4Linear:
                     out = torch.empty(*lead, K, dtype=y_dtype, device=w.device)
             elif out.get_device() != index:
                 raise ValueError("out: on another device than the weights")
-            got, ldy = rows_of(out, K, "out")
+            if out.is_contiguous() and out.shape[-1] == K:
+                got, ldy = out.numel() // K, K
+            else:
+                got, ldy = rows_of(out, K, "out")
             if got != rows or out.dtype is not y_dtype:
                 raise ValueError("out: another number of rows or type")
             if residual is not None:
@@ -132,7 +141,7 @@ class W4Linear:
                 need = self._sizes[rows] = B.conv_w4_workspace_size(self.desc, rows)
             # held until the launches are enqueued
             ws = self._ws.get(need, w.device, index, stream, handle) if need else None
-            B.conv_w4_fwd(self.desc, rows, xp, xsp, w.data_ptr(), bp, rp, out.data_ptr(),
+            B.conv_w4_fwd(self.desc, rows, xp, xsp, wp, bp, rp, out.data_ptr(),
                           ws.data_ptr() if need else None, need, handle)
             return out
 

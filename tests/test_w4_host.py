@@ -64,11 +64,11 @@ def test_w4_refusals(B):
     refused(B, BAD, B.conv_w4_create, 64, 64, 128, B.CONV_INT8)
     refused(B, BAD, B.conv_w4_create, 64, 64, 128, B.CONV_BF16, 4)
     refused(B, BAD, B.conv_w4_create, 64, 64, 128, B.CONV_BF16, 0, B.CONV_INT8)
-    d = B.conv_w4_create(96, 48)
+    d = B.conv_w4_create(2100, 48)
     refused(B, BAD, B.conv_w4_set_input_group, d, 64)
     refused(B, UNSUP, B.conv_w4_set_input_group, d, 128)  # bf16 x has no scales
     refused(B, BAD, B.conv_w4_set_epilogue, d, 5, False)
-    refused(B, BAD, B.conv_w4_set_strides, d, 95, 0, 0)
+    refused(B, BAD, B.conv_w4_set_strides, d, 2099, 0, 0)
     refused(B, BAD, B.conv_w4_set_strides, d, 0, 47, 0)
     refused(B, BAD, B.conv_w4_set_strides, d, 0, 0, 47)
     refused(B, BAD, B.conv_w4_prepack, d, None, P, None, P)
@@ -78,7 +78,7 @@ def test_w4_refusals(B):
     refused(B, ALIGN, B.conv_w4_prepack, d, P, P, None, P + 8)
     refused(B, BAD, B.conv_w4_workspace_size, d, -1)
     f, need = B.conv_w4_fwd, B.conv_w4_workspace_size(d, 200)
-    assert need == 200 * 96 * 2 and B.conv_w4_workspace_size(d, 1) == 0
+    assert need == 200 * 2104 * 2 and B.conv_w4_workspace_size(d, 1) == 0
     refused(B, BAD, f, d, -1, P, None, P, None, None, P)
     refused(B, UNSUP, f, d, (1 << 30) + 1, P, None, P, None, None, P)
     refused(B, BAD, f, d, 4, None, None, P, None, None, P)
