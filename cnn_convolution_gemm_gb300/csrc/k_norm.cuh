@@ -373,6 +373,56 @@ __device__ __forceinline__ void store_q8(const NormArgs& a, long long r, int t,
   }
 }
 
+// The same of one row whose threads hold single columns: through shared memory (buf: C floats,
+// rounded up to 16), so that codes are stored 16 at a time and a group of 128 columns is eight
+// neighbouring lanes' (6592 x 1250 fp32 52 us with 16 columns a thread at any alignment).
+template <int FMT, int T, int N>
+__device__ __forceinline__ void store_q8_single(const NormArgs& a, long long r, int t,
+                                                const float (&v)[1][N], float* buf,
+                                                float (*red)[32], int& turn) {
+  using L = Lay<T, N, SINGLE>;
+  const int C = a.C;
+  const bool valid = r < a.rows;
+  uint8_t* const codes = static_cast<uint8_t*>(a.h);
+  float* const scales = reinterpret_cast<float*>(a.hs);
+  float top[1] = {0.0f};
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    top[0] = max_abs(top[0], top[0], v[0][i]);
+    if (L::has(i, t, C)) buf[L::col(i, t)] = v[0][i];
+  }
+  if (t < (-C & 15)) buf[C + t] = 0.0f;
+  // (row_top's barrier comes after the stores, too)
+  if (!a.h_group) row_top<T, 1>(top, red, turn);
+  if (T > 32) {
+    if (a.h_group) __syncthreads();
+  } else {
+    __syncwarp();
+  }
+  for (int c0 = 16 * (t & ~31); c0 < C; c0 += 16 * T) {
+    const int c = c0 + 16 * (t & 31);
+    float e[16] = {};
+    if (c < C) {
+#pragma unroll
+      for (int j = 0; j < 16; j += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(buf + c + j);
+        e[j] = f.x;
+        e[j + 1] = f.y;
+        e[j + 2] = f.z;
+        e[j + 3] = f.w;
+      }
+    }
+    if (a.h_group) {
+      q8::store_grouped16<FMT>(e, valid, r, c, C, codes, scales);
+    } else if (valid && c < C) {
+      const q8::Scale<FMT> s(top[0]);
+      if (c == 0) scales[r] = s.s;
+      *reinterpret_cast<uint4*>(codes + r * q8::code_pitch(C) + c) = s.codes16(e);
+    }
+  }
+  if (T <= 32) __syncwarp();  // (else the next row's sums have a barrier before buf is written)
+}
+
 // Blocks an SM has to hold, which caps the registers: the compiler otherwise spends more on
 // loads it spreads between the sums (8192 x 4096 with gates 52 us, uncapped 74; 14552 x 2579
 // bf16 145, 223).  Without z more fit: 16384 x 8192 bf16 to MX 106 -> 91 us.
@@ -542,10 +592,18 @@ __global__ void __launch_bounds__(T <= 32 ? 128 : T, least_blocks(T, N, LAY, AHE
     if (a.pre != CONV_NORM_NONE) {
       norm_rows<T, N, LAY, R>(v, a.pre, a.eps_pre, w_pre, b_pre, t, C, vec_w, inv, red, turn);
       if constexpr (Q8) {
-        if (a.out == NORM_OUT_Q8_E4M3)
+        if constexpr (LAY == SINGLE) {
+          float* const buf = reinterpret_cast<float*>(ring) +
+                             (T <= 32 ? (int)threadIdx.x / T : 0) * ((C + 15) & ~15);
+          if (a.out == NORM_OUT_Q8_E4M3)
+            store_q8_single<CONV_Q8_E4M3, T, N>(a, r, t, v, buf, red, turn);
+          else
+            store_q8_single<CONV_Q8_INT8, T, N>(a, r, t, v, buf, red, turn);
+        } else if (a.out == NORM_OUT_Q8_E4M3) {
           store_q8<CONV_Q8_E4M3, T, N, R>(a, r, t, v, red, turn);
-        else
+        } else {
           store_q8<CONV_Q8_INT8, T, N, R>(a, r, t, v, red, turn);
+        }
       } else {
 #pragma unroll
         for (int k = 0; k < R; ++k)
@@ -602,7 +660,14 @@ cudaError_t launch_direct(const NormArgs& a, cudaStream_t st) {
   auto* kern = norm_kernel<TX, TZ, TG, T, N, LAY, false, 1, true, Q8>;
   if constexpr (std::is_same_v<TZ, TG>)  // launch(): without z the types are equal
     if (!a.z) kern = norm_kernel<TX, TZ, TG, T, N, LAY, false, 1, false, Q8>;
-  return launch_rows(kern, a, T <= 32 ? 128 : T, T <= 32 ? 128 / T : 1, 0, 0, st);
+  int smem = 0;
+  if constexpr (Q8 && LAY == SINGLE) {  // store_q8_single's rows
+    smem = (T <= 32 ? 128 / T : 1) * ((a.C + 15) & ~15) * 4;
+    const cudaError_t e = gb_set_smem_once(reinterpret_cast<const void*>(kern),
+                                           std::max(48 * 1024, T * N * 4));
+    if (e != cudaSuccess) return e;
+  }
+  return launch_rows(kern, a, T <= 32 ? 128 : T, T <= 32 ? 128 / T : 1, smem, 0, st);
 }
 
 // 16 consecutive columns a thread up to 8192 channels (152 rows of 4160 bf16 with gates
@@ -623,16 +688,16 @@ cudaError_t launch_groups(const NormArgs& a, cudaStream_t st) {
 // 8 single columns a thread (an access is one element: with more of them registers, not
 // bytes on their way, fill the SM: 12544 x 1001 fp32, 16 columns 52 us), 16 and 32 where a
 // row needs them
-template <typename TX, typename TZ, typename TG>
+template <typename TX, typename TZ, typename TG, bool Q8>
 cudaError_t launch_single(const NormArgs& a, cudaStream_t st) {
-  if (a.C <= 256) return launch_direct<TX, TZ, TG, false, 32, 8, SINGLE>(a, st);
-  if (a.C <= 512) return launch_direct<TX, TZ, TG, false, 64, 8, SINGLE>(a, st);
-  if (a.C <= 1024) return launch_direct<TX, TZ, TG, false, 128, 8, SINGLE>(a, st);
-  if (a.C <= 2048) return launch_direct<TX, TZ, TG, false, 256, 8, SINGLE>(a, st);
-  if (a.C <= 4096) return launch_direct<TX, TZ, TG, false, 512, 8, SINGLE>(a, st);
-  if (a.C <= 8192) return launch_direct<TX, TZ, TG, false, 1024, 8, SINGLE>(a, st);
-  if (a.C <= 16384) return launch_direct<TX, TZ, TG, false, 1024, 16, SINGLE>(a, st);
-  return launch_direct<TX, TZ, TG, false, 1024, 32, SINGLE>(a, st);
+  if (a.C <= 256) return launch_direct<TX, TZ, TG, Q8, 32, 8, SINGLE>(a, st);
+  if (a.C <= 512) return launch_direct<TX, TZ, TG, Q8, 64, 8, SINGLE>(a, st);
+  if (a.C <= 1024) return launch_direct<TX, TZ, TG, Q8, 128, 8, SINGLE>(a, st);
+  if (a.C <= 2048) return launch_direct<TX, TZ, TG, Q8, 256, 8, SINGLE>(a, st);
+  if (a.C <= 4096) return launch_direct<TX, TZ, TG, Q8, 512, 8, SINGLE>(a, st);
+  if (a.C <= 8192) return launch_direct<TX, TZ, TG, Q8, 1024, 8, SINGLE>(a, st);
+  if (a.C <= 16384) return launch_direct<TX, TZ, TG, Q8, 1024, 16, SINGLE>(a, st);
+  return launch_direct<TX, TZ, TG, Q8, 1024, 32, SINGLE>(a, st);
 }
 
 // Shared memory of the ring and the weights beside it; the latter as far as they fit.
@@ -706,10 +771,10 @@ cudaError_t launch(const NormArgs& a, cudaStream_t st) {
   }
   if (vec) return launch_groups<TX, TZ, TG, Q8, GROUPS>(a, st);
   if constexpr (Q8)
-    return launch_groups<TX, TZ, TG, true, ANY>(a, st);
+    return launch_single<TX, TZ, TG, true>(a, st);
   else
     return codes ? launch_groups<TX, TZ, TG, false, ANY>(a, st)
-                 : launch_single<TX, TZ, TG>(a, st);
+                 : launch_single<TX, TZ, TG, false>(a, st);
 }
 
 }  // namespace norm

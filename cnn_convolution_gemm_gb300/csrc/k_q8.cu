@@ -32,8 +32,11 @@ __device__ __forceinline__ void load_raw(Raw<T, ANY>& raw, const T* x, long long
     raw.load(x + r * ldx, c, cols, true);
 }
 
-template <int FMT, typename T, bool NARROW, bool ANY>
-__global__ void __launch_bounds__(THREADS)
+// Registers for four blocks to an SM, as the bytes on their way need; of fp32, twice the bytes,
+// for two.
+// LANES: that share a scale.
+template <int FMT, typename T, int LANES, bool NARROW, bool ANY>
+__global__ void __launch_bounds__(THREADS, sizeof(T) == 2 || ANY ? 4 : 2)
     quantize_groups_kernel(const T* __restrict__ x, long long ldx, int rows, int cols,
                            int wx_log2, uint8_t* __restrict__ codes, float* __restrict__ scales) {
   gb::allow_dependents();
@@ -54,73 +57,69 @@ __global__ void __launch_bounds__(THREADS)
       if (l0 + i * w.step >= rows) break;
       float v[16];
       raw[i].get(v);
-      q8::store_grouped16<FMT>(v, r < rows, r, w.c, cols, codes, scales);
+      q8::store_grouped16<FMT, LANES>(v, r < rows, r, w.c, cols, codes, scales);
     }
   }
 }
 
-// A row to PER threads, 16 columns each at a time, the first HELD of these in registers.
+// A row to the PER threads of a block, 16 columns each at a time, the first HELD of these in
+// registers; the next row's are on their way while this one's codes are made.
 template <int FMT, typename T, int PER, int HELD, bool ANY>
-__global__ void __launch_bounds__(PER < THREADS ? THREADS : PER)
+__global__ void __launch_bounds__(PER, (HELD == 2 ? 768 : 1024) / PER)
     quantize_rows_kernel(const T* __restrict__ x, long long ldx, int rows, int cols,
                          uint8_t* __restrict__ codes, float* __restrict__ scales) {
-  constexpr int BLOCK = PER < THREADS ? THREADS : PER, AT_ONCE = BLOCK / PER;
-  __shared__ float red[2][32];
+  constexpr int W = PER / 32;
+  __shared__ float red[2][W];
   gb::allow_dependents();
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int t = threadIdx.x % PER, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long step = (long long)gridDim.x * AT_ONCE, pitch = q8::code_pitch(cols);
-  const long long first = (long long)blockIdx.x * AT_ONCE;
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  const long long pitch = q8::code_pitch(cols);
   int turn = 0;
-  // the threads of a block go round together
-  for (long long r0 = first; r0 < rows; r0 += step) {
-    const long long r = r0 + threadIdx.x / PER;
-    const bool valid = r < rows;
-    Raw<T, ANY> raw[HELD];
-    float v[16], top = 0.0f;
-    if (valid) {
+  Raw<T, ANY> raw[HELD];
+  const auto fetch = [&](long long r) {
+    if (r >= rows) return;
 #pragma unroll
-      for (int i = 0; i < HELD; ++i)
-        load_raw<T, ANY>(raw[i], x, ldx, r, rows, 16 * (i * PER + t), cols);
+    for (int i = 0; i < HELD; ++i)
+      load_raw<T, ANY>(raw[i], x, ldx, r, rows, 16 * (i * PER + t), cols);
+  };
+  fetch(blockIdx.x);
+  for (long long r = blockIdx.x; r < rows; r += gridDim.x) {
+    float v[HELD][16], top = 0.0f;
 #pragma unroll
-      for (int i = 0; i < HELD; ++i) {
-        raw[i].get(v);
-        top = q8::top16(v, top);
-      }
-      for (int c = 16 * (HELD * PER + t); c < cols; c += 16 * PER) {
-        Raw<T, ANY> more;
-        load_raw<T, ANY>(more, x, ldx, r, rows, c, cols);
-        more.get(v);
-        top = q8::top16(v, top);
-      }
+    for (int i = 0; i < HELD; ++i) {
+      raw[i].get(v[i]);
+      top = q8::top16(v[i], top);
+    }
+    fetch(r + gridDim.x);
+    for (int c = 16 * (HELD * PER + t); c < cols; c += 16 * PER) {
+      Raw<T, ANY> more;
+      float e[16];
+      load_raw<T, ANY>(more, x, ldx, r, rows, c, cols);
+      more.get(e);
+      top = q8::top16(e, top);
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) top = max_abs(top, top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    if constexpr (PER > 32) {  // over the row's warps
-      constexpr int W = PER / 32;
-      if (lane == 0) red[turn][warp] = top;
-      __syncthreads();
-      top = red[turn][warp / W * W + lane % W];
+    if (lane == 0) red[turn][warp] = top;
+    __syncthreads();
+    top = red[turn][lane % W];
 #pragma unroll
-      for (int o = W / 2; o; o >>= 1)
-        top = max_abs(top, top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-      turn ^= 1;
-    }
-    if (!valid) continue;
+    for (int o = W / 2; o; o >>= 1)
+      top = max_abs(top, top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    turn ^= 1;  // two buffers used in turn: one barrier is enough
     const q8::Scale<FMT> s(top);
     if (t == 0) scales[r] = s.s;
 #pragma unroll
     for (int i = 0; i < HELD; ++i) {
       const int c = 16 * (i * PER + t);
-      if (c >= cols) break;
-      raw[i].get(v);
-      *reinterpret_cast<uint4*>(codes + r * pitch + c) = s.codes16(v);
+      if (c < cols) *reinterpret_cast<uint4*>(codes + r * pitch + c) = s.codes16(v[i]);
     }
     for (int c = 16 * (HELD * PER + t); c < cols; c += 16 * PER) {
       Raw<T, ANY> more;
+      float e[16];
       load_raw<T, ANY>(more, x, ldx, r, rows, c, cols);
-      more.get(v);
-      *reinterpret_cast<uint4*>(codes + r * pitch + c) = s.codes16(v);
+      more.get(e);
+      *reinterpret_cast<uint4*>(codes + r * pitch + c) = s.codes16(e);
     }
   }
 }
@@ -177,12 +176,19 @@ cudaError_t quantize_rows(int rows, int cols, const T* x, long long ldx, uint8_t
                           float* scales, cudaStream_t st) {
   auto* kern = rows_vec<T>(x, ldx, 32) ? quantize_rows_kernel<FMT, T, PER, HELD, false>
                                        : quantize_rows_kernel<FMT, T, PER, HELD, true>;
-  constexpr int BLOCK = PER < THREADS ? THREADS : PER;
-  const long long per_sm = gb_blocks_per_sm(reinterpret_cast<const void*>(kern), BLOCK, 0);
+  const long long per_sm = gb_blocks_per_sm(reinterpret_cast<const void*>(kern), PER, 0);
   const long long most = (long long)gb_num_sms() * std::max(1LL, per_sm);
-  const long long need = gb_ceil_div_ll(rows, BLOCK / PER);
-  return launch_walk<BLOCK>(kern, dim3((unsigned)std::min(need, most)), st, x, ldx, rows, cols,
-                            codes, scales);
+  return launch_walk<PER>(kern, dim3((unsigned)std::min<long long>(rows, most)), st, x, ldx, rows,
+                          cols, codes, scales);
+}
+
+template <int FMT, typename T, int LANES, bool NARROW>
+cudaError_t quantize_groups(int rows, int cols, const T* x, long long ldx, uint8_t* codes,
+                            float* scales, cudaStream_t st) {
+  const Shape s = walk_shape(rows, cols);
+  auto* kern = rows_vec<T>(x, ldx, 32) ? quantize_groups_kernel<FMT, T, LANES, NARROW, false>
+                                       : quantize_groups_kernel<FMT, T, LANES, NARROW, true>;
+  return launch_walk(kern, s.grid, st, x, ldx, rows, cols, s.wx_log2, codes, scales);
 }
 
 template <int FMT, typename T>
@@ -191,20 +197,19 @@ cudaError_t quantize_t(int group, int rows, int cols, const void* xv, long long 
   const T* const x = static_cast<const T*>(xv);
   uint8_t* const codes = static_cast<uint8_t*>(codes_v);
   float* const scales = static_cast<float*>(scales_v);
-  if (!group && cols > q8::GROUP) {
-    if (cols <= 512) return quantize_rows<FMT, T, 32, 1>(rows, cols, x, ldx, codes, scales, st);
-    if (cols <= 2048) return quantize_rows<FMT, T, 128, 1>(rows, cols, x, ldx, codes, scales, st);
-    if (cols <= 8192) return quantize_rows<FMT, T, 512, 1>(rows, cols, x, ldx, codes, scales, st);
-    return quantize_rows<FMT, T, 512, 2>(rows, cols, x, ldx, codes, scales, st);
-  }
-  // (a row of up to 128 columns is one group)
-  const Shape s = walk_shape(rows, cols);
-  const bool narrow = s.wx_log2 < 0;
-  auto* kern = rows_vec<T>(x, ldx, 32) ? (narrow ? quantize_groups_kernel<FMT, T, true, false>
-                                                 : quantize_groups_kernel<FMT, T, false, false>)
-                                       : (narrow ? quantize_groups_kernel<FMT, T, true, true>
-                                                 : quantize_groups_kernel<FMT, T, false, true>);
-  return launch_walk(kern, s.grid, st, x, ldx, rows, cols, s.wx_log2, codes, scales);
+  // (walk_shape: up to 128 columns on eight lanes, up to 256 on 16, else whole warps)
+  if (cols <= 128) return quantize_groups<FMT, T, 8, true>(rows, cols, x, ldx, codes, scales, st);
+  if (group)
+    return cols <= 256 ? quantize_groups<FMT, T, 8, true>(rows, cols, x, ldx, codes, scales, st)
+                       : quantize_groups<FMT, T, 8, false>(rows, cols, x, ldx, codes, scales, st);
+  if (cols <= 256) return quantize_groups<FMT, T, 16, true>(rows, cols, x, ldx, codes, scales, st);
+  if (cols <= 512) return quantize_groups<FMT, T, 32, false>(rows, cols, x, ldx, codes, scales, st);
+  if (cols <= 2048) return quantize_rows<FMT, T, 128, 1>(rows, cols, x, ldx, codes, scales, st);
+  if (cols <= 4096) return quantize_rows<FMT, T, 256, 1>(rows, cols, x, ldx, codes, scales, st);
+  if (cols <= 8192 && sizeof(T) == 2)
+    return quantize_rows<FMT, T, 256, 2>(rows, cols, x, ldx, codes, scales, st);
+  if (cols <= 8192) return quantize_rows<FMT, T, 512, 1>(rows, cols, x, ldx, codes, scales, st);
+  return quantize_rows<FMT, T, 1024, 1>(rows, cols, x, ldx, codes, scales, st);
 }
 
 template <int FMT, typename T>

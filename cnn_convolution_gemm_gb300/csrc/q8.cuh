@@ -64,6 +64,22 @@ __device__ __forceinline__ void unpack4(uint32_t w, float* v) {
   }
 }
 
+// Which of two neighbouring codes (bytes of w and up, up the larger magnitude) are the nearest
+// to v / s, ties to the even one: the sign of |v| - m s decides, m between them; one fma, so it
+// is the exact one.  Seldom taken.
+template <int FMT>
+__device__ __forceinline__ uint32_t settle(const float* v, float s, uint32_t w, uint32_t up) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t a = (w >> (8 * i)) & 255u, b = (up >> (8 * i)) & 255u;
+    if (a == b) continue;
+    const float m = 0.5f * (magnitude<FMT>(a) + magnitude<FMT>(b));
+    const float e = fmaf(-m, s, fabsf(v[i]));
+    if (e > 0.0f || (e == 0.0f && (a & 1u))) w ^= (a ^ b) << (8 * i);
+  }
+  return w;
+}
+
 // The scale of a row or group from its largest magnitude, and the codes under it.
 template <int FMT>
 struct Scale {
@@ -81,21 +97,11 @@ struct Scale {
     r_hi = r * (1.0f + 0x1p-21f);
   }
 
-  // Four codes, exact: where both sides of 1 / s give the same code it is x / s's too; else
-  // the sign of x - m s (one fma, so it is the exact one) decides, m between the two codes.
+  // Four codes, exact: where both sides of 1 / s give the same code it is x / s's too.
   __device__ __forceinline__ uint32_t codes4(const float* v) const {
     uint32_t w = pack4<FMT>(v, r_lo);
     const uint32_t up = pack4<FMT>(v, r_hi);
-    if (w != up) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t a = (w >> (8 * i)) & 255u, b = (up >> (8 * i)) & 255u;
-        if (a == b) continue;
-        const float m = 0.5f * (magnitude<FMT>(a) + magnitude<FMT>(b));
-        const float e = fmaf(-m, s, fabsf(v[i]));
-        if (e > 0.0f || (e == 0.0f && (a & 1u))) w ^= (a ^ b) << (8 * i);
-      }
-    }
+    if (w != up) w = settle<FMT>(v, s, w, up);
     return r_hi == 0.0f ? 0u : w;
   }
   __device__ __forceinline__ uint4 codes16(const float (&v)[16]) const {
@@ -109,21 +115,22 @@ __device__ __forceinline__ float top16(const float (&v)[16], float top = 0.0f) {
   return top;
 }
 
-// A lane's 16 consecutive columns of a row from column c on, in a matrix with scales per 128
-// of them: the eight lanes of a group are neighbours.  All lanes call it; valid: whether the
-// row exists.
-template <int FMT>
+// A lane's 16 consecutive columns of a row from column c on; LANES neighbours share a scale:
+// the eight of a group of 128 columns, or all of a row of up to 16 LANES columns.  All lanes
+// call it; valid: whether the row exists.
+template <int FMT, int LANES = GROUP / 16>
 __device__ __forceinline__ void store_grouped16(const float (&v)[16], bool valid, long long r,
                                                 int c, int cols, uint8_t* codes, float* scales) {
   float top = top16(v);
 #pragma unroll
-  for (int o = 1; o < GROUP / 16; o <<= 1)
+  for (int o = 1; o < LANES; o <<= 1)
     top = fp4::max_abs(top, top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
   const Scale<FMT> s(top);
   const uint4 w = s.codes16(v);
   if (!valid || c >= cols) return;
   *reinterpret_cast<uint4*>(codes + r * code_pitch(cols) + c) = w;
-  if (c % GROUP == 0) scales[r * scales_per_row(GROUP, cols) + c / GROUP] = s.s;
+  constexpr int SHARE = 16 * LANES;
+  if (c % SHARE == 0) scales[r * ((cols + SHARE - 1) / SHARE) + c / SHARE] = s.s;
 }
 
 }  // namespace q8
