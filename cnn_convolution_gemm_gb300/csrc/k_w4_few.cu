@@ -88,16 +88,8 @@ struct Stage {
 // A grid's y is which rows of X, 8 NT at a time.
 // PER: groups in 128 inputs (0: one per output).  NT: MMAs of eight rows.
 template <int XIO, int PER, bool F32, int NT>
-__global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) w4_few_kernel(const FewParams all_rows) {
-  FewParams p = all_rows;
-  if (gridDim.y > 1) {
-    const int m0 = blockIdx.y * 8 * NT, yb = p.y_f32 ? 4 : 2;
-    p.M = min(8 * NT, p.M - m0);
-    p.x = static_cast<const uint8_t*>(p.x) + m0 * p.ldx * kElemBytes<XIO>;
-    if (p.xs) p.xs += (long long)m0 * (p.x_group ? p.ct : 1);
-    if (p.res) p.res = static_cast<const uint8_t*>(p.res) + m0 * p.ldr * yb;
-    p.y = static_cast<uint8_t*>(p.y) + m0 * p.ldy * yb;
-  }
+__global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) w4_few_kernel(const FewParams p) {
+  const int m0 = blockIdx.y * 8 * NT, M = min(8 * NT, p.M - m0);  // this block's rows
   constexpr int PARTS = kParts<XIO>;
   constexpr bool Q8 = XIO == CONV_W4_IO_E4M3 || XIO == CONV_W4_IO_INT8;
   using S = Stage<PER, F32>;
@@ -107,7 +99,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) w4_few_kernel(const 
   constexpr int STAGE = 2 * S::BYTES;
   uint8_t* const ring = reinterpret_cast<uint8_t*>(smem4) + warp * p.stages * STAGE;
   uint8_t* const sx = reinterpret_cast<uint8_t*>(smem4) + WARPS * p.stages * STAGE;
-  const int part_bytes = p.M * p.pitch;  // of one of x's parts
+  const int part_bytes = M * p.pitch;  // of one of x's parts
   float* const sums = reinterpret_cast<float*>(sx + PARTS * part_bytes);  // [2][WARPS][8 NT][16]
   float* const sxs = sums + 2 * WARPS * NT * 128;                         // [M][ct]: x_group
   uint64_t* const full = full_all[warp];
@@ -131,19 +123,19 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) w4_few_kernel(const 
 
   // the tiles of this warp in order, two to a stage: a wait, a refill and their arithmetic are
   // as many instructions as half a tile's products
-  int frg = rg0, fj = j0, issued = 0;
+  int frg = rg0, left = p.ct - j0, issued = 0;  // left: tiles of the row from the next one on
   const uint8_t* from = S::block(p, rg0, j0);
   const int next = wc * 8 * S::BYTES;
   const auto fetch = [&](int stage) {  // lane 0
     uint8_t* const to = ring + stage * STAGE;
-    const bool two = fj + wc < p.ct;
+    const bool two = left > wc;
     gb::mbar_arrive_expect_tx(&full[stage], two ? STAGE : S::BYTES);
     gb::bulk_load(to, from, &full[stage], S::BYTES);
     if (two) gb::bulk_load(to + S::BYTES, from + next, &full[stage], S::BYTES);
     ++issued;
     from += 2 * next;
-    if ((fj += 2 * wc) >= p.ct) {
-      fj = j0;
+    if ((left -= 2 * wc) <= 0) {
+      left = p.ct - j0;
       frg += rg_step;
       from = S::block(p, frg, j0);
     }
@@ -152,7 +144,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) w4_few_kernel(const 
     for (int i = 0; i < p.stages && frg < p.row_groups; ++i) fetch(i);
 
   // x into shared memory
-  const int pieces = p.pitch / 16 - X_PAD / 16, all = p.M * pieces;
+  const int pieces = p.pitch / 16 - X_PAD / 16, all = M * pieces;
   for (int i0 = threadIdx.x; i0 < all; i0 += 4 * THREADS) {
     Raw8<XIO> raw[4];
     int m[4], c[4];
@@ -162,7 +154,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) w4_few_kernel(const 
       if (i >= all) break;
       m[k] = i / pieces;
       c[k] = (i - m[k] * pieces) * 8;
-      raw[k].load(static_cast<const uint8_t*>(p.x) + m[k] * p.ldx * kElemBytes<XIO>, c[k], p.C,
+      raw[k].load(static_cast<const uint8_t*>(p.x) + (m0 + m[k]) * p.ldx * kElemBytes<XIO>, c[k], p.C,
                   p.vec_x);
     }
 #pragma unroll
@@ -175,7 +167,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) w4_few_kernel(const 
     }
   }
   if (p.x_group)
-    for (int i = threadIdx.x; i < p.M * p.ct; i += THREADS) sxs[i] = p.xs[i];
+    for (int i = threadIdx.x; i < M * p.ct; i += THREADS) sxs[i] = p.xs[(long long)m0 * p.ct + i];
   __syncthreads();
 
   // B operands: row r of x (rows past M: any; their sums are not stored)
@@ -183,11 +175,11 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) w4_few_kernel(const 
   int bs[NT][2];  // x_group: the scales of this lane's two columns
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    bx[n] = sx + (8 * n + r < p.M ? 8 * n + r : 0) * p.pitch + 16 * q;
+    bx[n] = sx + (8 * n + r < M ? 8 * n + r : 0) * p.pitch + 16 * q;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int m = 8 * n + 2 * q + i;
-      bs[n][i] = (m < p.M ? m : 0) * p.ct;
+      bs[n][i] = (m < M ? m : 0) * p.ct;
     }
   }
   int turn = 0, stage = 0, taken = 0;
@@ -291,29 +283,30 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) w4_few_kernel(const 
     __syncthreads();
     const int o = threadIdx.x & 15, s = (threadIdx.x >> 4) & (at_once - 1);
     const int k = (rgb + s) * 16 + o;
-    if (k < p.K) {
+    const int first = (threadIdx.x >> 4) >> (3 - p.wc_log2);
+    if (first < M && k < p.K) {  // (of one row: half a warp)
       const float row_scale =
           PER == 0 ? (F32 ? static_cast<const float*>(p.scales)[k]
                           : __bfloat162float(static_cast<const __nv_bfloat16*>(p.scales)[k]))
                    : 1.0f;
       const float bias = p.bias ? p.bias[k] : 0.0f;
-      for (int m = (threadIdx.x >> 4) >> (3 - p.wc_log2); m < p.M; m += 2 * wc) {
+      for (int m = first; m < M; m += 2 * wc) {
         const float* const from =
             sums + ((turn * WARPS + (s << p.wc_log2)) * NT * 8 + m) * 16 + o;
         float v = 0.0f;
         for (int i = 0; i < wc; ++i) v += from[i * NT * 128];
         if (PER == 0) v *= row_scale;
-        if (Q8 && !p.x_group) v *= p.xs[m];
+        if (Q8 && !p.x_group) v *= p.xs[m0 + m];
         v += bias;
         if (p.res)
-          v += p.y_f32 ? static_cast<const float*>(p.res)[m * p.ldr + k]
-                       : __bfloat162float(static_cast<const __nv_bfloat16*>(p.res)[m * p.ldr + k]);
+          v += p.y_f32 ? static_cast<const float*>(p.res)[(m0 + m) * p.ldr + k]
+                       : __bfloat162float(static_cast<const __nv_bfloat16*>(p.res)[(m0 + m) * p.ldr + k]);
         float e[2] = {v, 0.0f};
         if (p.act != CONV_ACT_NONE) gb::fp4::activate<true>(e, p.act);
         if (p.y_f32)
-          static_cast<float*>(p.y)[m * p.ldy + k] = e[0];
+          static_cast<float*>(p.y)[(m0 + m) * p.ldy + k] = e[0];
         else
-          static_cast<__nv_bfloat16*>(p.y)[m * p.ldy + k] = __float2bfloat16_rn(e[0]);
+          static_cast<__nv_bfloat16*>(p.y)[(m0 + m) * p.ldy + k] = __float2bfloat16_rn(e[0]);
       }
     }
     turn ^= 1;
