@@ -846,9 +846,7 @@ cudaError_t launch_as(const W4Gemm& g, const W4Operand& x, cudaStream_t st) {
 template <int NT, int SUMS, bool XS, int PARTS>
 cudaError_t launch_kernel(const W4Gemm& g, const W4Operand& x, cudaStream_t st) {
   if constexpr (NT >= 128)
-    if (g.M >= NT && (long long)gb_ceil_div(g.K, 2 * TILE) * gb_ceil_div(g.M, NT) >=
-                         gb_num_sms() / 2)
-      return launch_as<NT, SUMS, XS, PARTS, true>(g, x, st);
+    if (w4_gemm_pairs(g, NT)) return launch_as<NT, SUMS, XS, PARTS, true>(g, x, st);
   return launch_as<NT, SUMS, XS, PARTS, false>(g, x, st);
 }
 
