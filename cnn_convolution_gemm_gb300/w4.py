@@ -75,6 +75,11 @@ class W4Linear:
                                  device=codes.device)
         B.conv_w4_prepack(self.desc, codes.data_ptr(), scales.data_ptr(),
                           None if zeros is None else zeros.data_ptr(), packed.data_ptr(), handle)
+        if stream is not None:  # the tensors may be freed before the stream has read them
+            other = torch.cuda.ExternalStream(stream)
+            for t in (codes, scales, zeros):
+                if t is not None:
+                    t.record_stream(other)
         with self._lock:
             self.w = (packed, packed.data_ptr(), packed.get_device())
 

@@ -160,6 +160,68 @@ def test_many_tiles(M, C, K, x, group, x_group):
     Case(C, K, group, x, BF16, x_group=x_group, act=4).check(M)
 
 
+# (rows, outputs): tiles of 64 rows; of 128, and of 128 in pairs of CTAs; of 160, and in pairs
+WIDTHS = [(100, 600), (192, 4096), (500, 5000), (320, 4000), (639, 4790)]
+
+
+@pytest.mark.parametrize("M,K", WIDTHS)
+@pytest.mark.parametrize("group,x,x_group", [(0, BF16, 0), (128, BF16, 0), (64, BF16, 0),
+                                             (32, F32, 0), (128, F32, 0), (0, INT8, 128),
+                                             (64, INT8, 128), (32, E4M3, 128), (128, E4M3, 0)])
+def test_every_tile_width(M, K, group, x, x_group):
+    Case(1500, K, group, x, BF16, x_group=x_group, residual=True, act=1).check(M)
+
+
+@pytest.mark.parametrize("M,x", [(1, BF16), (3, F32), (1, INT8)])
+def test_rows_that_shared_memory_does_not_hold(M, x):
+    Case(120001, 33, 128, x, F32, x_group=128 if x == INT8 else 0).check(M)
+
+
+def test_tensors_of_a_load_on_another_stream_may_go():
+    torch, B, q8, W4Linear = _mods()
+    case = Case(2048, 512, 64)
+    side = torch.cuda.Stream()
+    x, _ = case.input(5)
+    want = case.layer(x)
+    layer = W4Linear(2048, 512, 64)
+    side.wait_stream(torch.cuda.current_stream())
+    codes, scales, zeros = (t.clone() for t in (case.codes, case.scales, case.zeros))
+    side.wait_stream(torch.cuda.current_stream())
+    layer.load(codes, scales, zeros, stream=side.cuda_stream)
+    del codes, scales, zeros
+    torch.full((1 << 22,), 255, dtype=torch.uint8, device="cuda")
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(layer(x), want)
+
+
+def test_threads_share_a_layer():
+    """Two threads, a stream each, calls of other sizes and strides."""
+    import threading
+    case = Case(700, 300, 64)
+    torch = case.torch
+    inputs = [torch.randn(M, 700 + pad, device="cuda").bfloat16()[:, :700]
+              for M, pad in ((3, 0), (40, 4), (700, 0), (9, 100))]
+    want = [case.layer(x) for x in inputs]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(order):
+        stream = torch.cuda.Stream()
+        for _ in range(20):
+            for i in order:
+                with torch.cuda.stream(stream):
+                    y = case.layer(inputs[i])
+                    if not torch.equal(y, want[i]):
+                        wrong.append(i)
+
+    threads = [threading.Thread(target=work, args=(o,)) for o in ((0, 1, 2, 3), (3, 2, 1, 0))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+
+
 @pytest.mark.parametrize("M", [1, 11, 40, 150])
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_strided_rows_and_offsets(M, dtype):
