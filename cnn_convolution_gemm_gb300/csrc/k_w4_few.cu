@@ -44,23 +44,25 @@ struct FewParams {
   unsigned long long wait_ns;
 };
 
-// c = or += the product.
-template <bool ADD>
+// c = or += the product, of bf16 or (F16) f16.
+#define GB_MMA_M16N8K16(T, C, OUT, ...)                                                      \
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32." T "." T ".f32 {%0, %1, %2, %3}, "    \
+               "{%4, %5, %6, %7}, {%8, %9}, " C ";"                                          \
+               : OUT(c[0]), OUT(c[1]), OUT(c[2]), OUT(c[3])                                  \
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1)__VA_ARGS__)
+template <bool ADD, bool F16>
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                     uint32_t a3, uint32_t b0, uint32_t b1) {
-  if constexpr (ADD)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
-        "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  if constexpr (ADD && F16)
+    GB_MMA_M16N8K16("f16", "{%0, %1, %2, %3}", "+f");
+  else if constexpr (ADD)
+    GB_MMA_M16N8K16("bf16", "{%0, %1, %2, %3}", "+f");
+  else if constexpr (F16)
+    GB_MMA_M16N8K16("f16", "{%10, %10, %10, %10}", "=f", , "f"(0.0f));
   else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
-        "{%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
-        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+    GB_MMA_M16N8K16("bf16", "{%10, %10, %10, %10}", "=f", , "f"(0.0f));
 }
+#undef GB_MMA_M16N8K16
 
 // 16 outputs' codes, scales and zeros of a tile of inputs; a stage of a warp's ring holds two.
 template <int PER, bool F32>
@@ -152,7 +154,7 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) w4_few_kernel(const 
     for (int k = 0; k < 4; ++k) {
       const int i = i0 + k * THREADS;
       if (i >= all) break;
-      m[k] = i / pieces;
+      m[k] = M == 1 ? 0 : i / pieces;
       c[k] = (i - m[k] * pieces) * 8;
       raw[k].load(static_cast<const uint8_t*>(p.x) + (m0 + m[k]) * p.ldx * kElemBytes<XIO>, c[k], p.C,
                   p.vec_x);
@@ -162,8 +164,11 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) w4_few_kernel(const 
       if (i0 + k * THREADS >= all) break;
 #pragma unroll
       for (int h = 0; h < PARTS; ++h)
-        *reinterpret_cast<uint4*>(sx + h * part_bytes + m[k] * p.pitch + c[k] * 2) =
-            raw[k].part(h);
+        if constexpr (Q8)
+          *reinterpret_cast<uint4*>(sx + m[k] * p.pitch + c[k] * 2) = raw[k].f16();
+        else
+          *reinterpret_cast<uint4*>(sx + h * part_bytes + m[k] * p.pitch + c[k] * 2) =
+              raw[k].part(h);
     }
   }
   if (p.x_group)
@@ -214,12 +219,21 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) w4_few_kernel(const 
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
           const uint32_t byte = (t / SPAN) * 0x0101u | 0x4040u;
-          const uint32_t zza = __byte_perm(zas, 0x43434343u, byte);  // 128 + zero, twice
-          const uint32_t zzb = __byte_perm(zbs, 0x43434343u, byte);
-          const uint32_t a0 = weight_pair<0>(aw[t], zza), a1 = weight_pair<1>(aw[t], zza),
-                         a2 = weight_pair<2>(aw[t], zza), a3 = weight_pair<3>(aw[t], zza);
-          const uint32_t b0 = weight_pair<0>(bw[t], zzb), b1 = weight_pair<1>(bw[t], zzb),
-                         b2 = weight_pair<2>(bw[t], zzb), b3 = weight_pair<3>(bw[t], zzb);
+          uint32_t a[4], b[4];  // the weights of two outputs
+          if constexpr (Q8) {
+            ZeroF16 za, zb;
+            za.at0 = as_half2(__byte_perm(zas, 0x64646464u, byte));
+            zb.at0 = as_half2(__byte_perm(zbs, 0x64646464u, byte));
+            za.at4 = __hsub2(as_half2(0x63806380u), za.at0);  // 960 - (1024 + zero)
+            zb.at4 = __hsub2(as_half2(0x63806380u), zb.at0);
+            weights_f16(aw[t], za, a);
+            weights_f16(bw[t], zb, b);
+          } else {
+            const uint32_t zza = __byte_perm(zas, 0x43434343u, byte);  // 128 + zero, twice
+            const uint32_t zzb = __byte_perm(zbs, 0x43434343u, byte);
+            weights_bf16(aw[t], zza, a);
+            weights_bf16(bw[t], zzb, b);
+          }
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -227,14 +241,14 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) w4_few_kernel(const 
               const uint4 xb =
                   *reinterpret_cast<const uint4*>(bx[n] + h * part_bytes + j * 256 + 64 * t);
               if constexpr (!OWN) {
-                mma<true>(acc[n], a0, b0, a1, b1, xb.x, xb.y);
-                mma<true>(acc1[n], a2, b2, a3, b3, xb.z, xb.w);
+                mma<true, Q8>(acc[n], a[0], b[0], a[1], b[1], xb.x, xb.y);
+                mma<true, Q8>(acc1[n], a[2], b[2], a[3], b[3], xb.z, xb.w);
               } else if (t % SPAN == 0 && h == 0) {
-                mma<false>(part[0][n], a0, b0, a1, b1, xb.x, xb.y);
-                mma<false>(part[1][n], a2, b2, a3, b3, xb.z, xb.w);
+                mma<false, Q8>(part[0][n], a[0], b[0], a[1], b[1], xb.x, xb.y);
+                mma<false, Q8>(part[1][n], a[2], b[2], a[3], b[3], xb.z, xb.w);
               } else {
-                mma<true>(part[0][n], a0, b0, a1, b1, xb.x, xb.y);
-                mma<true>(part[1][n], a2, b2, a3, b3, xb.z, xb.w);
+                mma<true, Q8>(part[0][n], a[0], b[0], a[1], b[1], xb.x, xb.y);
+                mma<true, Q8>(part[1][n], a[2], b[2], a[3], b[3], xb.z, xb.w);
               }
             }
           }

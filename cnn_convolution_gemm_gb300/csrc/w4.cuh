@@ -18,6 +18,7 @@
 #pragma once
 
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -61,6 +62,39 @@ __device__ __forceinline__ uint32_t weight_pair(uint32_t w, uint32_t zz) {
   const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&q),
                                    *reinterpret_cast<const __nv_bfloat162*>(&zz));
   return *reinterpret_cast<const uint32_t*>(&d);
+}
+
+__device__ __forceinline__ void weights_bf16(uint32_t w, uint32_t zz, uint32_t (&o)[4]) {
+  o[0] = weight_pair<0>(w, zz);
+  o[1] = weight_pair<1>(w, zz);
+  o[2] = weight_pair<2>(w, zz);
+  o[3] = weight_pair<3>(w, zz);
+}
+
+// The same in f16, a whole word: pairs (0, 1), (2, 3), (4, 5), (6, 7).  f16's ten bits behind the
+// point hold a code 4 places up too (1024 + 16 code), so a shift serves two pairs.
+struct ZeroF16 {
+  __half2 at0, at4;  // 1024 + zero; -(64 + zero)
+};
+__device__ __forceinline__ __half2 as_half2(uint32_t w) {
+  return *reinterpret_cast<const __half2*>(&w);
+}
+__device__ __forceinline__ uint32_t as_word(__half2 h) {
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ void weights_f16(uint32_t w, const ZeroF16& z, uint32_t (&o)[4]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint32_t q, q16;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;"
+        : "=r"(q)
+        : "r"(w >> (8 * i)), "r"(0x000F000Fu), "r"(0x64006400u));
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;"
+        : "=r"(q16)
+        : "r"(w >> (8 * i)), "r"(0x00F000F0u), "r"(0x64006400u));
+    o[2 * i] = as_word(__hsub2(as_half2(q), z.at0));
+    o[2 * i + 1] = as_word(__hfma2(as_half2(q16), as_half2(0x2C002C00u), z.at4));  // 1 / 16
+  }
 }
 
 // An fp32 value as the sum of three bf16 values, exact: its leading 8 bits, the next 8 and the
@@ -159,6 +193,23 @@ struct Raw8 {
         const float a = __uint_as_float(0x4B000000u | (u & 255u)) - 8388736.0f;
         const float b = __uint_as_float(0x4B000000u | ((u >> 8) & 255u)) - 8388736.0f;
         o[i] = pair_hi(__float_as_uint(a), __float_as_uint(b));
+      }
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+  }
+  // 8-bit codes as f16, exact
+  __device__ __forceinline__ uint4 f16() const {
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (XIO == CONV_W4_IO_E4M3) {
+        asm("{\n\t.reg .b16 p;\n\tcvt.u16.u32 p, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, p;\n\t}"
+            : "=r"(o[i])
+            : "r"(w[i / 2] >> (16 * (i & 1))));
+      } else {  // 1024 + (code + 128)
+        const uint32_t u =
+            __byte_perm(w[i / 2] ^ 0x80808080u, 0x64646464u, i & 1 ? 0x4342 : 0x4140);
+        o[i] = as_word(__hsub2(as_half2(u), as_half2(0x64806480u)));  // 1152
       }
     }
     return make_uint4(o[0], o[1], o[2], o[3]);
