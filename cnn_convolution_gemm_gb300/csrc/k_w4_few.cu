@@ -444,9 +444,8 @@ cudaError_t launch_group(const W4Gemm& g, cudaStream_t st) {
 // latency (64 x 512 x 512 3.0 us, on tcgen05 5.3; 16 x 2048 x 2048 4.9 and 5.4, 32 rows 6.2 and
 // 5.8; 16 x 4096 x 1024, where each block converts as much x as it reads weights, 8.0 and 5.8).
 bool w4_few_applicable(const W4Gemm& g) {
-  if (g.M > 8 &&
-      (g.C > 2048 || (long long)gb_ceil_div(g.M, 16) * g.C * g.K > 4500000))
-    return false;
+  const long long blocks = gb_ceil_div(g.M, 16);  // of rows; a grid's y
+  if (g.M > 8 && (g.C > 2048 || blocks * g.C * g.K > 4500000 || blocks > 65535)) return false;
   return few_smem(g).stages > 0;
 }
 

@@ -177,6 +177,40 @@ def test_rows_that_shared_memory_does_not_hold(M, x):
     Case(120001, 33, 128, x, F32, x_group=128 if x == INT8 else 0).check(M)
 
 
+def test_more_rows_than_a_grid_has_blocks():
+    """Of a layer so small that its rows would go to blocks 16 at a time."""
+    Case(5, 7, 0, BF16, F32).check(16 * 65535 + 7)
+
+
+@pytest.mark.parametrize("M", [1, 8, 16, 40])
+@pytest.mark.parametrize("fmt", [E4M3, INT8])
+def test_every_8_bit_code_times_every_weight(fmt, M):
+    """A row holds one code, at a column of its own; the scales are 1, so y is exact."""
+    torch, B, q8, W4Linear = _mods()
+    C, K = 128, 256
+    codes = torch.arange(K, dtype=torch.uint8) % 16  # of output k; its zero is k // 16
+    layer = W4Linear(C, K, 128, x_dtype=None, x_q8=fmt, y_dtype=torch.float32,
+                     scale_dtype=torch.float32)
+    layer.load((codes * 17).reshape(K, 1).expand(K, C // 2).contiguous().cuda(),
+               torch.ones(K, 1, device="cuda"),
+               (torch.arange(K) // 16).to(torch.uint8).reshape(K, 1).cuda())
+    weight = codes.double() - torch.arange(K).div(16, rounding_mode="floor").double()
+    x = torch.arange(256, dtype=torch.uint8)
+    value = x.view(torch.float8_e4m3fn if fmt == E4M3 else torch.int8).double()
+    held = [i for i in range(256) if value[i] == value[i]]  # E4M3 has two NaNs
+    while len(held) % M:
+        held.append(held[-1])
+    for start in range(0, len(held), M):
+        rows = held[start:start + M]
+        matrix = torch.zeros(M, C, dtype=torch.uint8)
+        for m, i in enumerate(rows):
+            matrix[m, (37 * i + i // 64) % C] = i
+        t = q8.Q8Tensor(M, C, fmt, 0, matrix.cuda(), torch.ones(M, device="cuda"))
+        y = layer(t)
+        _sync(torch, B)
+        assert torch.equal(y.double().cpu() + 0, torch.outer(value[rows], weight) + 0), start
+
+
 def test_tensors_of_a_load_on_another_stream_may_go():
     torch, B, q8, W4Linear = _mods()
     case = Case(2048, 512, 64)
