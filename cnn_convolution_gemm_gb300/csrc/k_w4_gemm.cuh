@@ -275,8 +275,8 @@ struct Mmas {
 template <int NT, int COUNT, bool XS, bool PAIR>
 struct Sums {
   using C = Cfg<NT, COUNT, XS, PAIR>;
-  const float* scales;  // the first place's: of this thread's output
-  const float* xs;      // and of its columns of x
+  const float* scales;  // the first place's: of this thread's output (XS: the first of four)
+  const float* xs;      // XS: of its first columns of x
   uint64_t *d_full, *d_empty;
   uint32_t d_empty0;    // d_empty of the CTA that issues the MMAs (cluster address)
   Turn s, d;
@@ -291,6 +291,79 @@ struct Sums {
     }
   }
 
+  // acc += scale * an accumulator, of one output: 16 columns at a time (the last 8), AHEAD: the
+  // next on their way from TMEM meanwhile.
+  static __device__ __forceinline__ void scale_outputs(float scale, uint32_t t,
+                                                       uint64_t (&acc)[C::COLS / 2]) {
+    const uint64_t s2 = pack2(scale, scale);
+    constexpr int N = C::AHEAD ? 2 : 1;
+    uint32_t r[N][16];
+    const auto fetch = [&](int b) {
+      const int to = (b / 16) % N;
+      if (b + 16 <= C::COLS)
+        gb::tmem_ld_x16(t + b, r[to]);
+      else
+        gb::tmem_ld_x8(t + b, *reinterpret_cast<uint32_t(*)[8]>(r[to]));
+    };
+    if (C::AHEAD) fetch(0);
+#pragma unroll
+    for (int b = 0; b < C::COLS; b += 16) {
+      if (!C::AHEAD) fetch(b);
+      gb::tmem_ld_wait();
+      if (C::AHEAD && b + 16 < C::COLS) fetch(b + 16);
+      const uint32_t(&v)[16] = r[(b / 16) % N];
+#pragma unroll
+      for (int i = 0; i < 16 && b + i < C::COLS; i += 2)
+        acc[(b + i) / 2] = fma2(pack2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), s2,
+                                acc[(b + i) / 2]);
+    }
+  }
+
+  // The same of four outputs, 8 apart, and two columns of each eight, with scales of x: four
+  // lanes share a column's scale so, not all 32.  A load that gives all lanes the same 16 bytes
+  // takes as long as any other, and the scales' way from shared memory was what bounded the
+  // sums (4096 x 4096 x 16384 with groups of 128 529 us so).
+  static __device__ __forceinline__ void scale_both(const float* scales, const float* xs,
+                                                    uint32_t t, int per,
+                                                    uint64_t (&acc)[C::COLS / 2]) {
+    static_assert(C::COLS % 16 == 0 || !XS, "columns");
+    uint64_t s2[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float su = per ? scales[8 * k] : 1.0f;
+      s2[k] = pack2(su, su);
+    }
+    uint32_t r[2][16];
+    const auto fetch = [&](int b) {
+      gb::tmem_ld_16x256_x2(t + b, r[(b / 16) % 2]);
+      gb::tmem_ld_16x256_x2(t + (16 << 16) + b, r[(b / 16) % 2] + 8);
+    };
+    fetch(0);
+#pragma unroll
+    for (int b = 0; b < C::COLS; b += 16) {
+      uint64_t f[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float2 e = *reinterpret_cast<const float2*>(xs + b + 8 * i);
+        f[i] = pack2(e.x, e.y);
+      }
+      gb::tmem_ld_wait();
+      if (b + 16 < C::COLS) fetch(b + 16);
+      const uint32_t(&v)[16] = r[(b / 16) % 2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t* const e = v + 8 * h + 4 * i + 2 * k;
+            uint64_t& to = acc[b / 2 + 4 * h + 2 * i + k];
+            to = fma2(pack2(__uint_as_float(e[0]), __uint_as_float(e[1])),
+                      mul2(s2[2 * h + k], f[i]), to);
+          }
+    }
+  }
+
   // One tile; the last accumulator stays this thread's.  t: its first column.  live: whether
   // any of the columns is a row of X.
   __device__ __forceinline__ bool run(const Params& p, int c0, int c1, uint32_t t, bool live,
@@ -298,51 +371,15 @@ struct Sums {
     for (int c = c0; c < c1; ++c) {
 #pragma unroll
       for (int u = 0; u < COUNT; ++u) {
-        const float* const at = xs + s.at * C::S_FLOATS;
         if (!gb::mbar_wait_bounded_warp(&d_full[d.at], d.phase, p.wait_ns, p.err)) return false;
         gb::tc_fence_after();
         if (live) {
-          const float su = p.per ? scales[s.at * C::S_FLOATS + u * TILE] : 1.0f;
-          const uint64_t s2 = pack2(su, su);
-          // 16 columns at a time (the last 8), AHEAD: the next on their way from TMEM meanwhile
-          constexpr int N = C::AHEAD ? 2 : 1;
-          uint32_t r[N][16];
-          float4 f[N][4];
-          const auto fetch = [&](int b) {
-            const int to = (b / 16) % N;
-            if (b + 16 <= C::COLS)
-              gb::tmem_ld_x16(t + d.at * NT + b, r[to]);
-            else
-              gb::tmem_ld_x8(t + d.at * NT + b, *reinterpret_cast<uint32_t(*)[8]>(r[to]));
-            if constexpr (XS)
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (b + 4 * i < C::COLS)
-                  f[to][i] = *reinterpret_cast<const float4*>(at + b + 4 * i);
-          };
-          if (C::AHEAD) fetch(0);
-#pragma unroll
-          for (int b = 0; b < C::COLS; b += 16) {
-            if (!C::AHEAD) fetch(b);
-            gb::tmem_ld_wait();
-            if (C::AHEAD && b + 16 < C::COLS) fetch(b + 16);
-            const int in = (b / 16) % N;
-#pragma unroll
-            for (int i = 0; i < 16; i += 4) {
-              if (b + i >= C::COLS) break;
-              uint64_t f0 = s2, f1 = s2;
-              if constexpr (XS) {
-                const float4 e = f[in][i / 4];
-                f0 = mul2(s2, pack2(e.x, e.y));
-                f1 = mul2(s2, pack2(e.z, e.w));
-              }
-              const uint32_t(&v)[16] = r[in];
-              uint64_t& a0 = acc[(b + i) / 2];
-              uint64_t& a1 = acc[(b + i) / 2 + 1];
-              a0 = fma2(pack2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), f0, a0);
-              a1 = fma2(pack2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3])), f1, a1);
-            }
-          }
+          if constexpr (XS)
+            scale_both(scales + s.at * C::S_FLOATS + u * TILE, xs + s.at * C::S_FLOATS,
+                       t + d.at * NT, p.per, acc);
+          else
+            scale_outputs(p.per ? scales[s.at * C::S_FLOATS + u * TILE] : 1.0f, t + d.at * NT,
+                          acc);
         }
         if (c == c1 - 1 && u == COUNT - 1) break;
         gb::tc_fence_before();
@@ -637,7 +674,8 @@ __global__ void __launch_bounds__(Cfg<NT, SUMS, XS, PAIR>::THREADS, 1)
     const int o = (warp & 3) * 32 + lane, col0 = part * C::COLS;
     const uint32_t t = tmem + ((uint32_t)((warp & 3) * 32) << 16) + col0;
     Sums<NT, SUMS, XS, PAIR> sums{
-        sS + o, sS + 4 * TILE + col0, d_full, d_empty,
+        sS + (XS ? (warp & 3) * 32 + lane / 4 : o),
+        sS + 4 * TILE + col0 + (XS ? 2 * (lane & 3) : 0), d_full, d_empty,
         PAIR ? gb::mapa_shared(gb::smem_u32(d_empty), 0) : 0, {}, {}};
     bool ok = true;
     for (int tile = first; tile < p.tiles && ok; tile += step) {
@@ -655,7 +693,7 @@ __global__ void __launch_bounds__(Cfg<NT, SUMS, XS, PAIR>::THREADS, 1)
         if (!ok) break;
         // back to the last accumulator
 #pragma unroll
-        for (int b = 0; b < C::COLS; b += 8) {
+        for (int b = 0; b < C::COLS; b += 8) {  // XS: 16 columns' half of the lanes
           uint32_t r[8];
 #pragma unroll
           for (int i = 0; i < 8; i += 2) {
@@ -664,7 +702,11 @@ __global__ void __launch_bounds__(Cfg<NT, SUMS, XS, PAIR>::THREADS, 1)
             r[i] = __float_as_uint(f0);
             r[i + 1] = __float_as_uint(f1);
           }
-          gb::tmem_st_x8(t + sums.d.at * NT + b, r);
+          const uint32_t to = t + sums.d.at * NT;
+          if constexpr (XS)
+            gb::tmem_st_16x256_x2(to + b / 16 * 16 + (b % 16 ? 16 << 16 : 0), r);
+          else
+            gb::tmem_st_x8(to + b, r);
         }
         gb::tmem_st_wait();
       }
