@@ -14,6 +14,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <type_traits>
 
 #include "fp4.cuh"
@@ -213,7 +214,10 @@ struct Weights {
 };
 
 // v = norm(v) with weight and bias, for R rows; elements past a row's end come and stay 0.
-template <int T, int N, Layout LAY, int R>
+// EACH: every step rounded to fp32 by itself, v / sqrt(sum / C + eps) * w + b.  Codes of fp32 rows
+// are made from that: which of two a value next to the border between them gets, its last bit
+// says, and it should be the formula's as far as can be.
+template <int T, int N, Layout LAY, int R, bool EACH = false>
 __device__ __forceinline__ void norm_rows(float (&v)[R][N], int kind, float eps,
                                           const Weights<T, N, LAY>& w,
                                           const Weights<T, N, LAY>& b, int t, int C, bool vec_w,
@@ -255,7 +259,20 @@ __device__ __forceinline__ void norm_rows(float (&v)[R][N], int kind, float eps,
   row_sum<T, R>(sum, red, turn);
   float f[R];
 #pragma unroll
-  for (int k = 0; k < R; ++k) f[k] = rsqrtf(fmaf(sum[k], inv, eps));
+  for (int k = 0; k < R; ++k) {
+    if constexpr (EACH) {
+      const float root = sqrtf(__fadd_rn(__fdiv_rn(sum[k], (float)C), eps));
+      const float r = __frcp_rn(root), back = root <= FLT_MAX ? -root : 0.0f;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {  // a quotient and its remainder's: rounded as a division
+        const float q = v[k][i] * r;
+        v[k][i] = fmaf(fmaf(back, q, v[k][i]), r, q);
+      }
+      f[k] = 1.0f;
+    } else {
+      f[k] = rsqrtf(fmaf(sum[k], inv, eps));
+    }
+  }
   if (w.w) {
 #pragma unroll
     for (int i = 0; i < N; i += 4) {
@@ -590,7 +607,7 @@ __global__ void __launch_bounds__(T <= 32 ? 128 : T, least_blocks(T, N, LAY, AHE
                                    T >= 32 || r < a.rows, t, C, v[k]);
     }
     if (a.pre != CONV_NORM_NONE) {
-      norm_rows<T, N, LAY, R>(v, a.pre, a.eps_pre, w_pre, b_pre, t, C, vec_w, inv, red, turn);
+      norm_rows<T, N, LAY, R, Q8 && sizeof(TX) == 4>(v, a.pre, a.eps_pre, w_pre, b_pre, t, C, vec_w, inv, red, turn);
       if constexpr (Q8) {
         if constexpr (LAY == SINGLE) {
           float* const buf = reinterpret_cast<float*>(ring) +

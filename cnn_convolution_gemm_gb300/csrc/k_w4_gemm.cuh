@@ -7,14 +7,20 @@
 // group of inputs at a time in TMEM (or all of them, where a row has one scale), and the
 // threads that keep the tile's sums in registers add scale * sum to them in fp32.
 //
-// Warp 0 loads X (TMA), warp 2 the packed weights, warp 1 issues the MMAs (one elected lane);
-// two warpgroups take the codes apart, tile by tile in turn, and write them as bf16 into TMEM,
-// an output a lane, where the MMAs read A: through shared memory, whose 128 bytes a cycle are
-// what bounds this kernel, they would pass twice at four times their size (64 x 8192 x 8192
-// 34 us so).  The others scale and sum, and run the epilogue (through TMEM, so that it is a loop
-// over columns).  Few tiles with
-// long reductions are split over the CTAs of a cluster, which add their sums through
-// distributed shared memory in a fixed order.
+// Warp 0 loads X (TMA), warp 2 the packed weights, warp 3 scales along the rows of X, warp 1
+// issues the MMAs (one elected lane); two or three warpgroups take the codes apart, tile by tile
+// in turn, and write them as bf16 into TMEM, an output a lane, where the MMAs read A: through
+// shared memory, of 128 bytes a cycle, they would pass twice at four times their size (64 x 8192
+// x 8192 34 us so, 20.5 now).  The others scale and sum, and run the epilogue (through TMEM, so
+// that it is a loop over columns).  Few tiles with long reductions are split over the CTAs of a
+// cluster, which add their sums through distributed shared memory in a fixed order.
+//
+// What bounds it: with one scale an output the MMAs (4096 x 4096 x 16384 273 us, 2.0 PFLOP/s).
+// With groups the sums, which read every accumulator beside the MMAs' own use of TMEM: 389 us
+// with groups of 128 (without those reads 314), 541 of 64, 820 of 32; with scales of x per 128
+// inputs 478.  With 64 rows a chain of waits from the bytes to the sums (64 x 8192 x 8192 15.7 us
+// with one scale an output, 17.7 with groups of 128, 20.5 of 64; the bytes take 5.9): neither
+// more places in the rings nor a second warp that issues made it shorter.
 // One translation unit per width includes this file.
 #pragma once
 
@@ -46,8 +52,8 @@ template <int NT, int SUMS, bool XS, bool PAIR>
 struct Cfg {
   static constexpr int TAKE_WGS = NT == 64 ? 3 : 2;    // that take codes apart
   // That scale and sum: their work is a chain of short waits, so there are many; or, where
-  // each column has a scale of its own, few, with registers for the next columns and scales to
-  // be on their way.
+  // each column has a scale of its own, few, with registers for the next columns to be on their
+  // way (4096 x 4096 x 16384 with groups of 128 478 us, with four warpgroups 515).
   static constexpr int SUM_WGS = NT >= 128 && !XS ? 4 : 2;
   static constexpr bool AHEAD = SUM_WGS == 2;
   static constexpr int THREADS = 128 * (1 + TAKE_WGS + SUM_WGS);
