@@ -214,7 +214,7 @@ struct Weights {
 };
 
 // v = norm(v) with weight and bias, for R rows; elements past a row's end come and stay 0.
-// EACH: every step rounded to fp32 by itself, v / sqrt(sum / C + eps) * w + b.  Codes of fp32 rows
+// EACH: every step rounded to fp32 by itself, v / sqrt(sum * (1 / C) + eps) * w + b.  Codes of fp32 rows
 // are made from that: which of two a value next to the border between them gets, its last bit
 // says, and it should be the formula's as far as can be.
 template <int T, int N, Layout LAY, int R, bool EACH = false>
@@ -261,7 +261,7 @@ __device__ __forceinline__ void norm_rows(float (&v)[R][N], int kind, float eps,
 #pragma unroll
   for (int k = 0; k < R; ++k) {
     if constexpr (EACH) {
-      const float root = sqrtf(__fadd_rn(__fdiv_rn(sum[k], (float)C), eps));
+      const float root = sqrtf(__fadd_rn(__fmul_rn(sum[k], inv), eps));
       const float r = __frcp_rn(root), back = root <= FLT_MAX ? -root : 0.0f;
 #pragma unroll
       for (int i = 0; i < N; ++i) {  // a quotient and its remainder's: rounded as a division
