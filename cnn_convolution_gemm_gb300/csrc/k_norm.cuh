@@ -7,7 +7,8 @@
 // memory (bulk copies); otherwise a row's loads are issued together, past L1, so that the
 // weights stay there.  Measured: 32768 x 8192 bf16 325 us (6.6 TB/s), 12544 x 1001 fp32
 // with gates 40 us (5.0 TB/s; single elements), 26400 x 256 bf16 with gates 10, 8192 x 4096 bf16
-// with fp32 z 66 (5.1 TB/s), one row of 4096 3.1 us.
+// with fp32 z 66 (5.1 TB/s), one row of 4096 3.1 us; into 8 bits 16384 x 8192 bf16 167 us (5.6
+// TB/s), fp32 302, 6592 x 1250 fp32 (single elements) 29.
 // One translation unit per set of types includes this file.
 #pragma once
 
@@ -214,9 +215,10 @@ struct Weights {
 };
 
 // v = norm(v) with weight and bias, for R rows; elements past a row's end come and stay 0.
-// EACH: every step rounded to fp32 by itself, v / sqrt(sum * (1 / C) + eps) * w + b.  Codes of fp32 rows
-// are made from that: which of two a value next to the border between them gets, its last bit
-// says, and it should be the formula's as far as can be.
+// EACH: every step rounded to fp32 by itself, v / sqrt(sum * (1 / C) + eps) * w + b.  Codes of
+// fp32 rows are made from that: which of two a value next to the border between them gets, its
+// last bit says, and it should be the formula's as far as can be (of 777 x 1001 values 0.8 were
+// others' with v * (rsqrt * w), 0.05 now; 16384 x 8192 298 -> 302 us).
 template <int T, int N, Layout LAY, int R, bool EACH = false>
 __device__ __forceinline__ void norm_rows(float (&v)[R][N], int kind, float eps,
                                           const Weights<T, N, LAY>& w,
@@ -607,7 +609,8 @@ __global__ void __launch_bounds__(T <= 32 ? 128 : T, least_blocks(T, N, LAY, AHE
                                    T >= 32 || r < a.rows, t, C, v[k]);
     }
     if (a.pre != CONV_NORM_NONE) {
-      norm_rows<T, N, LAY, R, Q8 && sizeof(TX) == 4>(v, a.pre, a.eps_pre, w_pre, b_pre, t, C, vec_w, inv, red, turn);
+      norm_rows<T, N, LAY, R, Q8 && sizeof(TX) == 4>(v, a.pre, a.eps_pre, w_pre, b_pre, t, C,
+                                                     vec_w, inv, red, turn);
       if constexpr (Q8) {
         if constexpr (LAY == SINGLE) {
           float* const buf = reinterpret_cast<float*>(ring) +

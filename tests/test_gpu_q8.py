@@ -245,6 +245,50 @@ def test_norm(fmt, group, rows, C):
 
 @pytest.mark.parametrize("fmt", FMTS, ids=R.NAMES.get)
 @pytest.mark.parametrize("group", [0, 128])
+@pytest.mark.parametrize("rows,C", [(9, 100), (33, 1001), (40, 1024), (1300, 768), (300, 4096),
+                                    (5, 8200), (3, 20000)])
+def test_fp32_norms_round_step_by_step(fmt, group, rows, C):
+    """x and z are whole numbers, so the sum of squares (below 2^24) is exact in any order, and
+    every other step is one fp32 operation: codes and scales follow to the bit."""
+    torch, q8 = _q8()
+    from cnn_convolution_gemm_gb300 import binding as B
+    from cnn_convolution_gemm_gb300.norm import ResidualNorm
+    rng = np.random.default_rng(rows + C)
+    x, z = (rng.integers(-10, 11, (rows, C)).astype(np.float32) for _ in range(2))
+    w = (1 + 0.2 * rng.standard_normal(C)).astype(np.float32)
+    norm = ResidualNorm(C, torch.float32, eps=1e-6, pre=B.CONV_NORM_RMS,
+                        w_pre=torch.from_numpy(w).cuda(), h_q8=fmt, h_group=group)
+    _, h = norm(torch.from_numpy(x).cuda(), torch.from_numpy(z).cuda())
+    _sync(torch)
+    v = x + z
+    mean = (v * v).sum(axis=1, keepdims=True, dtype=np.float64).astype(np.float32) * \
+        (np.float32(1) / np.float32(C))
+    v = v / np.sqrt(mean + np.float32(1e-6)) * w
+    assert v.dtype == np.float32
+    code, s = R.quantize(v, fmt, group)
+    got, pad, got_s = unpack(h)
+    np.testing.assert_array_equal(got_s, s)
+    np.testing.assert_array_equal(got, code)
+    assert not pad.any()
+
+
+def test_fp32_norms_of_rows_whose_squares_overflow():
+    """The root is infinite, the quotients 0; a row with an infinity is NaN, as everywhere."""
+    torch, q8 = _q8()
+    from cnn_convolution_gemm_gb300 import binding as B
+    from cnn_convolution_gemm_gb300.norm import ResidualNorm
+    for C in (100, 1001, 4096):
+        x = torch.ones(3, C, device="cuda")
+        x[0] = 3e19
+        x[1, 5] = float("inf")
+        _, h = ResidualNorm(C, torch.float32, pre=B.CONV_NORM_RMS, h_q8="int8")(x)
+        y = q8.dequantize(h, torch.float32)
+        _sync(torch)
+        assert not y[0].any() and y[1].isnan().all() and (y[2] - 1).abs().max() < 1e-5
+
+
+@pytest.mark.parametrize("fmt", FMTS, ids=R.NAMES.get)
+@pytest.mark.parametrize("group", [0, 128])
 def test_layer_norms_and_no_weights(fmt, group):
     _norm_case(70, 640, "bfloat16", True, fmt, group, pre="layer")
     _norm_case(70, 641, "float32", False, fmt, group, pre="layer", w=False)
