@@ -211,6 +211,31 @@ def test_every_8_bit_code_times_every_weight(fmt, M):
         assert torch.equal(y.double().cpu() + 0, torch.outer(value[rows], weight) + 0), start
 
 
+def test_weights_past_32_bits():
+    """More than 4 GB of packed weights: the first and the last outputs."""
+    torch, B, q8, W4Linear = _mods()
+    C, K, some = 16384, 540100, 100
+    layer = W4Linear(C, K, 128, y_dtype=torch.float32)
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    codes = torch.randint(0, 256, (K, C // 2), generator=gen, device="cuda", dtype=torch.uint8)
+    scales = (torch.rand(K, C // 128, generator=gen, device="cuda") / 128).bfloat16()
+    zeros = torch.randint(0, 16, (K, C // 128), generator=gen, device="cuda", dtype=torch.uint8)
+    layer.load(codes, scales, zeros)
+    assert layer.w[0].numel() > 2 ** 32
+    x = torch.randn(70, C, generator=gen, device="cuda").bfloat16()
+    for M in (1, 70):
+        y = layer(x[:M])
+        _sync(torch, B)
+        for at in (slice(0, some), slice(K - some, K)):
+            q = torch.stack([codes[at] & 15, codes[at] >> 4], dim=2).reshape(some, C).double()
+            w = (q - zeros[at].double().repeat_interleave(128, 1)) * \
+                scales[at].double().repeat_interleave(128, 1)
+            want, size = x[:M].double() @ w.t(), x[:M].double().abs() @ w.abs().t()
+            # as Case.expect: sums, and y's rounding
+            tol = (C / 8 + 32) * 2.0 ** -23 * size + want.abs() * 2.0 ** -24
+            assert ((y[:, at].double() - want).abs() <= tol).all()
+
+
 def test_tensors_of_a_load_on_another_stream_may_go():
     torch, B, q8, W4Linear = _mods()
     case = Case(2048, 512, 64)
