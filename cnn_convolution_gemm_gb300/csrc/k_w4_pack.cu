@@ -84,7 +84,8 @@ __global__ void __launch_bounds__(THREADS)
   const long long all = (long long)M * pieces;
   for (long long i = (long long)blockIdx.x * THREADS + threadIdx.x; i < all;
        i += (long long)gridDim.x * THREADS) {
-    const long long m = i / pieces;
+    // (a 64-bit division is as many instructions as the rest several times)
+    const long long m = all <= 0xFFFFFFFFLL ? (unsigned)i / (unsigned)pieces : i / pieces;
     const int c = (int)(i - m * pieces) * 8;
     Raw8<XIO> raw;
     raw.load(static_cast<const uint8_t*>(x) + m * ldx * kElemBytes<XIO>, c, C, vec);
