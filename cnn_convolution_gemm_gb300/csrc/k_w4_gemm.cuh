@@ -339,34 +339,46 @@ struct Sums {
       const float su = per ? scales[8 * k] : 1.0f;
       s2[k] = pack2(su, su);
     }
-    uint32_t r[2][16];
+    // As many columns at a time as registers hold: a wait for TMEM beside the MMAs is some 150
+    // cycles (1024 x 16384 x 4096 160 us with 16 and the next 16 on their way, 151 with 64 at
+    // once; 4096 x 4096 x 16384, groups of 64, 746 and with 32 700).  Tiles of 64 rows have
+    // registers for 16 and the next.
+    constexpr int CH = NT == 64 ? 16 : NT == 128 ? 64 : 32, N = NT == 64 ? 2 : 1;
+    uint32_t r[N][CH];
     const auto fetch = [&](int b) {
-      gb::tmem_ld_16x256_x2(t + b, r[(b / 16) % 2]);
-      gb::tmem_ld_16x256_x2(t + (16 << 16) + b, r[(b / 16) % 2] + 8);
-    };
-    fetch(0);
 #pragma unroll
-    for (int b = 0; b < C::COLS; b += 16) {
-      uint64_t f[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float2 e = *reinterpret_cast<const float2*>(xs + b + 8 * i);
-        f[i] = pack2(e.x, e.y);
+      for (int i = 0; i < CH && b + i < C::COLS; i += 16) {
+        gb::tmem_ld_16x256_x2(t + b + i, r[(b / CH) % N] + i);
+        gb::tmem_ld_16x256_x2(t + (16 << 16) + b + i, r[(b / CH) % N] + i + 8);
       }
+    };
+    if (N == 2) fetch(0);
+#pragma unroll
+    for (int b0 = 0; b0 < C::COLS; b0 += CH) {
+      if (N == 1) fetch(b0);
       gb::tmem_ld_wait();
-      if (b + 16 < C::COLS) fetch(b + 16);
-      const uint32_t(&v)[16] = r[(b / 16) % 2];
+      if (N == 2 && b0 + CH < C::COLS) fetch(b0 + CH);
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int b = b0; b < b0 + CH && b < C::COLS; b += 16) {
+        const uint32_t* const v = r[(b0 / CH) % N] + b - b0;
+        uint64_t f[2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 2; ++i) {
+          const float2 e = *reinterpret_cast<const float2*>(xs + b + 8 * i);
+          f[i] = pack2(e.x, e.y);
+        }
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const uint32_t* const e = v + 8 * h + 4 * i + 2 * k;
-            uint64_t& to = acc[b / 2 + 4 * h + 2 * i + k];
-            to = fma2(pack2(__uint_as_float(e[0]), __uint_as_float(e[1])),
-                      mul2(s2[2 * h + k], f[i]), to);
-          }
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t* const e = v + 8 * h + 4 * i + 2 * k;
+              uint64_t& to = acc[b / 2 + 4 * h + 2 * i + k];
+              to = fma2(pack2(__uint_as_float(e[0]), __uint_as_float(e[1])),
+                        mul2(s2[2 * h + k], f[i]), to);
+            }
+      }
     }
   }
 
