@@ -16,9 +16,9 @@
 // cluster, which add their sums through distributed shared memory in a fixed order.
 //
 // What bounds it: with one scale an output the MMAs (4096 x 4096 x 16384 273 us, 2.0 PFLOP/s).
-// With groups the sums, which read every accumulator beside the MMAs' own use of TMEM: 389 us
-// with groups of 128 (without those reads 314), 541 of 64, 820 of 32; with scales of x per 128
-// inputs 478.  With 64 rows a chain of waits from the bytes to the sums (64 x 8192 x 8192 15.7 us
+// With groups the sums, which read every accumulator beside the MMAs' own use of TMEM: 384 us
+// with groups of 128 (a variant without those reads 314), 541 of 64, 825 of 32; with scales of
+// x per 128 inputs 472.  With 64 rows a chain of waits from the bytes to the sums (64 x 8192 x 8192 15.7 us
 // with one scale an output, 17.7 with groups of 128, 20.5 of 64; the bytes take 5.9): neither
 // more places in the rings nor a second warp that issues made it shorter.
 // One translation unit per width includes this file.
@@ -51,11 +51,18 @@ constexpr int BK = 64;  // inputs of a load of X: 128 bytes of bf16
 template <int NT, int SUMS, bool XS, bool PAIR>
 struct Cfg {
   static constexpr int TAKE_WGS = NT == 64 ? 3 : 2;    // that take codes apart
-  // That scale and sum: their work is a chain of short waits, so there are many; or, where
-  // each column has a scale of its own, few, with registers for the next columns to be on their
-  // way (4096 x 4096 x 16384 with groups of 128 478 us, with four warpgroups 515).
-  static constexpr int SUM_WGS = NT >= 128 && !XS ? 4 : 2;
-  static constexpr bool AHEAD = SUM_WGS == 2;
+  // That scale and sum.  Their work is a chain of short waits, so there are many (4096 x 4096 x
+  // 16384, groups of 64: 541 us, with two 640); or few, with registers for more columns a wait:
+  // in pairs that sum 128 inputs at a time (1024 x 16384 x 4096 125 -> 112 us; tiles that pairs
+  // do not fill the GPU with 17.2 -> 18.8), and where each column has a scale of its own (4096 x
+  // 4096 x 16384, groups of 128: 478 us, with four 515).
+  static constexpr int SUM_WGS = NT >= 128 && !XS && !(SUMS == 1 && PAIR) ? 4 : 2;
+  // Columns that a thread reads from TMEM at a time, as many as its registers hold: a wait for
+  // them beside the MMAs is some 150 cycles (1024 x 16384 x 4096 with scales of x 160 us with 16
+  // and the next 16 on their way, 151 with 64 at once).  Tiles of 64 rows have registers for 16
+  // and the next.
+  static constexpr int CHUNK = SUM_WGS == 4 || NT == 64 ? 16 : NT == 128 ? 64 : 32;
+  static constexpr int CHUNKS = NT == 64 ? 2 : 1;
   static constexpr int THREADS = 128 * (1 + TAKE_WGS + SUM_WGS);
   static constexpr int COLS = NT / SUM_WGS;            // columns of a summing thread
   // Accumulators in TMEM, and stages of 128 inputs of weights beside them.  A small group's
@@ -88,7 +95,7 @@ struct Cfg {
   // at most what the block is launched with
   static constexpr bool SPLIT_REGS = NT >= 128;
   static constexpr int REGS = 65536 / THREADS / 8 * 8;
-  static constexpr int REGS_TAKE = 56, REGS_SUM = AHEAD ? 152 : 80;
+  static constexpr int REGS_TAKE = 56, REGS_SUM = SUM_WGS == 2 ? 152 : 80;
   static_assert(!SPLIT_REGS || (1 + TAKE_WGS) * REGS_TAKE + SUM_WGS * REGS_SUM <=
                                    REGS * THREADS / 128, "registers");
   static_assert(A0 + A_STAGES * A_COLS <= TMEM_COLS && SMEM <= 232448, "TMEM, shared memory");
@@ -297,31 +304,31 @@ struct Sums {
     }
   }
 
-  // acc += scale * an accumulator, of one output: 16 columns at a time (the last 8), AHEAD: the
-  // next on their way from TMEM meanwhile.
+  // acc += scale * an accumulator, of one output.
   static __device__ __forceinline__ void scale_outputs(float scale, uint32_t t,
                                                        uint64_t (&acc)[C::COLS / 2]) {
     const uint64_t s2 = pack2(scale, scale);
-    constexpr int N = C::AHEAD ? 2 : 1;
-    uint32_t r[N][16];
+    constexpr int CH = C::CHUNK, N = C::CHUNKS;
+    uint32_t r[N][CH];
     const auto fetch = [&](int b) {
-      const int to = (b / 16) % N;
-      if (b + 16 <= C::COLS)
-        gb::tmem_ld_x16(t + b, r[to]);
-      else
-        gb::tmem_ld_x8(t + b, *reinterpret_cast<uint32_t(*)[8]>(r[to]));
+#pragma unroll
+      for (int i = 0; i < CH && b + i < C::COLS; i += 16)
+        if (b + i + 16 <= C::COLS)
+          gb::tmem_ld_x16(t + b + i, *reinterpret_cast<uint32_t(*)[16]>(r[(b / CH) % N] + i));
+        else
+          gb::tmem_ld_x8(t + b + i, *reinterpret_cast<uint32_t(*)[8]>(r[(b / CH) % N] + i));
     };
-    if (C::AHEAD) fetch(0);
+    if (N == 2) fetch(0);
 #pragma unroll
-    for (int b = 0; b < C::COLS; b += 16) {
-      if (!C::AHEAD) fetch(b);
+    for (int b0 = 0; b0 < C::COLS; b0 += CH) {
+      if (N == 1) fetch(b0);
       gb::tmem_ld_wait();
-      if (C::AHEAD && b + 16 < C::COLS) fetch(b + 16);
-      const uint32_t(&v)[16] = r[(b / 16) % N];
+      if (N == 2 && b0 + CH < C::COLS) fetch(b0 + CH);
+      const uint32_t* const v = r[(b0 / CH) % N];
 #pragma unroll
-      for (int i = 0; i < 16 && b + i < C::COLS; i += 2)
-        acc[(b + i) / 2] = fma2(pack2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), s2,
-                                acc[(b + i) / 2]);
+      for (int i = 0; i < CH && b0 + i < C::COLS; i += 2)
+        acc[(b0 + i) / 2] = fma2(pack2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), s2,
+                                 acc[(b0 + i) / 2]);
     }
   }
 
@@ -339,11 +346,7 @@ struct Sums {
       const float su = per ? scales[8 * k] : 1.0f;
       s2[k] = pack2(su, su);
     }
-    // As many columns at a time as registers hold: a wait for TMEM beside the MMAs is some 150
-    // cycles (1024 x 16384 x 4096 160 us with 16 and the next 16 on their way, 151 with 64 at
-    // once; 4096 x 4096 x 16384, groups of 64, 746 and with 32 700).  Tiles of 64 rows have
-    // registers for 16 and the next.
-    constexpr int CH = NT == 64 ? 16 : NT == 128 ? 64 : 32, N = NT == 64 ? 2 : 1;
+    constexpr int CH = C::CHUNK, N = C::CHUNKS;
     uint32_t r[N][CH];
     const auto fetch = [&](int b) {
 #pragma unroll
