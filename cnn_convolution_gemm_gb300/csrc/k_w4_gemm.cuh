@@ -332,10 +332,10 @@ struct Sums {
     }
   }
 
-  // The same of four outputs, 8 apart, and two columns of each eight, with scales of x: four
-  // lanes share a column's scale so, not all 32.  A load that gives all lanes the same 16 bytes
-  // takes as long as any other, and the scales' way from shared memory was what bounded the
-  // sums (4096 x 4096 x 16384 with groups of 128 529 us so).
+  // The same of four outputs, 8 apart, and two columns of each eight, with scales of x: a
+  // column's scale goes to eight lanes so, not to all 32.  A load that gives all lanes the same
+  // 16 bytes takes as long as any other, and the scales' way from shared memory was what bounded
+  // the sums (4096 x 4096 x 16384 with groups of 128 529 us so, 478 with this).
   static __device__ __forceinline__ void scale_both(const float* scales, const float* xs,
                                                     uint32_t t, int per,
                                                     uint64_t (&acc)[C::COLS / 2]) {
