@@ -160,8 +160,8 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) w4_few_kernel(const 
       if (i >= all) break;
       m[k] = M == 1 ? 0 : i / pieces;
       c[k] = (i - m[k] * pieces) * 8;
-      raw[k].load(static_cast<const uint8_t*>(p.x) + (m0 + m[k]) * p.ldx * kElemBytes<XIO>, c[k], p.C,
-                  p.vec_x);
+      raw[k].load(static_cast<const uint8_t*>(p.x) + (m0 + m[k]) * p.ldx * kElemBytes<XIO>, c[k],
+                  p.C, p.vec_x);
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -317,8 +317,9 @@ __global__ void __launch_bounds__(THREADS, NT == 1 ? 3 : 2) w4_few_kernel(const 
         if (Q8 && !p.x_group) v *= p.xs[m0 + m];
         v += bias;
         if (p.res)
-          v += p.y_f32 ? static_cast<const float*>(p.res)[(m0 + m) * p.ldr + k]
-                       : __bfloat162float(static_cast<const __nv_bfloat16*>(p.res)[(m0 + m) * p.ldr + k]);
+          v += p.y_f32 ? gb::fp4::load_f32(static_cast<const float*>(p.res) + (m0 + m) * p.ldr + k)
+                       : gb::fp4::load_f32(static_cast<const __nv_bfloat16*>(p.res) +
+                                           (m0 + m) * p.ldr + k);
         float e[2] = {v, 0.0f};
         if (p.act != CONV_ACT_NONE) gb::fp4::activate<true>(e, p.act);
         if (p.y_f32)
@@ -411,8 +412,8 @@ cudaError_t launch_t(const W4Gemm& g, cudaStream_t st) {
       std::max(1, gb_blocks_per_sm(reinterpret_cast<const void*>(kern), THREADS, smem));
   const int need = gb_ceil_div(p.row_groups, WARPS >> p.wc_log2), blocks = gb_ceil_div(g.M, 16);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)std::min<long long>(need, gb_ceil_div_ll(per_sm * gb_num_sms(), blocks)),
-                     (unsigned)blocks);
+  const long long fit = gb_ceil_div_ll(per_sm * gb_num_sms(), blocks);
+  cfg.gridDim = dim3((unsigned)std::min<long long>(need, fit), (unsigned)blocks);
   cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;

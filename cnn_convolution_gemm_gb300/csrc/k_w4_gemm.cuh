@@ -18,9 +18,9 @@
 // What bounds it: with one scale an output the MMAs (4096 x 4096 x 16384 273 us, 2.0 PFLOP/s).
 // With groups the sums, which read every accumulator beside the MMAs' own use of TMEM: 384 us
 // with groups of 128 (a variant without those reads 314), 541 of 64, 825 of 32; with scales of
-// x per 128 inputs 472.  With 64 rows a chain of waits from the bytes to the sums (64 x 8192 x 8192 15.7 us
-// with one scale an output, 17.7 with groups of 128, 20.5 of 64; the bytes take 5.9): neither
-// more places in the rings nor a second warp that issues made it shorter.
+// x per 128 inputs 472.  With 64 rows a chain of waits from the bytes to the sums (64 x 8192 x
+// 8192 15.7 us with one scale an output, 17.7 with groups of 128, 20.5 of 64; the bytes take
+// 5.9): neither more places in the rings nor a second warp that issues made it shorter.
 // One translation unit per width includes this file.
 #pragma once
 
@@ -445,7 +445,9 @@ __global__ void __launch_bounds__(Cfg<NT, SUMS, XS, PAIR>::THREADS, 1)
   const int step = gridDim.x >> (PAIR ? 1 : p.split_log2);
   const auto out_tile = [&](int tile) { return PAIR ? tile / p.mt * 2 + half : tile / p.mt; };
   // of weights: a pair's second CTA may have none left, and takes the last ones along
-  const auto w_tile = [&](int tile) { return PAIR ? min(out_tile(tile), p.kt - 1) : out_tile(tile); };
+  const auto w_tile = [&](int tile) {
+    return PAIR ? min(out_tile(tile), p.kt - 1) : out_tile(tile);
+  };
   // this CTA's tiles of inputs
   const int c0 = (int)((long long)p.ct * rank >> p.split_log2);
   const int c1 = (int)((long long)p.ct * (rank + 1) >> p.split_log2);
@@ -825,8 +827,8 @@ __global__ void __launch_bounds__(Cfg<NT, SUMS, XS, PAIR>::THREADS, 1)
 }
 
 // [parts][rows][cols] bf16 in boxes of BK x box_rows
-inline bool operand_map(CUtensorMap* map, const void* x, int parts, int rows, int cols, long long ld,
-                 int box_rows) {
+inline bool operand_map(CUtensorMap* map, const void* x, int parts, int rows, int cols,
+                        long long ld, int box_rows) {
   cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)parts};
   cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)ld * 2 * rows};
   cuuint32_t box[3] = {BK, (cuuint32_t)box_rows, 1};

@@ -136,7 +136,8 @@ struct Raw8 {
     if constexpr (XIO == CONV_W4_IO_F32) {
       const float* const p = static_cast<const float*>(row) + c;
       if (vec && c + 8 <= C) {
-        const uint4 a = *reinterpret_cast<const uint4*>(p), b = *reinterpret_cast<const uint4*>(p + 4);
+        const uint4 a = *reinterpret_cast<const uint4*>(p);
+        const uint4 b = *reinterpret_cast<const uint4*>(p + 4);
         w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
         w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
       } else {
@@ -170,7 +171,8 @@ struct Raw8 {
     } else if constexpr (XIO == CONV_W4_IO_F32) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const Parts a = split3(__uint_as_float(w[2 * i])), b = split3(__uint_as_float(w[2 * i + 1]));
+        const Parts a = split3(__uint_as_float(w[2 * i]));
+        const Parts b = split3(__uint_as_float(w[2 * i + 1]));
         o[i] = k == 0 ? pair_hi(a.hi, b.hi) : k == 1 ? pair_hi(a.mid, b.mid) : pair_hi(a.lo, b.lo);
       }
     } else if constexpr (XIO == CONV_W4_IO_E4M3) {
